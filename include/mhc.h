@@ -36,7 +36,9 @@ typedef enum mhc_status {
     MHC_ERR_INVALID_ARGUMENT = 1, /* NULL, misaligned or aliasing pointer, bad count   */
     MHC_ERR_UNSUPPORTED = 2,      /* valid but outside the shapes this library handles */
     MHC_ERR_CUDA = 3,             /* a CUDA runtime call or launch failed               */
-    MHC_ERR_TIMEOUT = 4           /* a bounded device-side wait gave up (see below)      */
+    MHC_ERR_TIMEOUT = 4,          /* a bounded device-side wait gave up (see below)      */
+    MHC_ERR_INDEX = 5             /* bad length, page or offset in device data (mhc_kv.h);
+                                     returned by mhc_device_status only                 */
 } mhc_status;
 
 /*
@@ -349,7 +351,9 @@ const char *mhc_status_string(mhc_status status);
  * cluster peers push into it, then frees its tensor memory and returns.
  * Should one of those drain waits also give up, the kernel returns anyway
  * (a copy still in flight is then not waited for).  No test provokes a
- * timeout.  MHC_ERR_CUDA if the synchronisation or the read failed.
+ * timeout.  MHC_ERR_INDEX (no timeout, but mhc_kv_append or mhc_kv_attend met
+ * an index that mhc_kv.h calls bad since the last call).  MHC_ERR_CUDA if the
+ * synchronisation or the read failed.
  */
 mhc_status mhc_device_status(void);
 

@@ -9,6 +9,13 @@ cannot be loaded, every call raises.
 
     pre_delayed(x, pre_in, fn, bias, alpha, norm_weight=None, ...) -> dict
     post(x, y, comb, post_gate, out=None) -> Tensor
+
+and, for the attention sublayer between them, a paged 8-bit key/value cache
+(``kv.py``, C ABI in ``include/mhc_kv.h``):
+
+    kv_cache(num_pages, heads, page_tokens, head_dim) -> dict
+    kv_append(cache, k, v, block_table, seq_lens, cu_q=None, ...) -> Tensor | None
+    kv_attend(q, cache, block_table, seq_lens, cu_q=None, ...) -> dict
 """
 from __future__ import annotations
 
@@ -19,13 +26,14 @@ import threading
 import torch
 
 __all__ = ["pre_delayed", "pre_delayed_noalloc", "post", "pre_plan", "device_status", "workspace_for",
-           "library_path", "load_library", "MhcError", "SINKHORN_ITERS"]
+           "library_path", "load_library", "MhcError", "SINKHORN_ITERS", "kv_cache", "kv_append", "kv_attend",
+           "kv_workspace_for"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "_build", "libmhc.so")
 SINKHORN_ITERS = 20
 _STATUS = {0: "MHC_OK", 1: "MHC_ERR_INVALID_ARGUMENT", 2: "MHC_ERR_UNSUPPORTED",
-           3: "MHC_ERR_CUDA", 4: "MHC_ERR_TIMEOUT"}
+           3: "MHC_ERR_CUDA", 4: "MHC_ERR_TIMEOUT", 5: "MHC_ERR_INDEX"}
 
 _lock = threading.Lock()
 _lib = None
@@ -96,6 +104,8 @@ def load_library():
         lib.mhc_device_status.restype = I
         lib.mhc_set_launch_overlap.argtypes = [I]
         lib.mhc_set_launch_overlap.restype = I
+        from . import kv
+        kv.declare(lib)
         _lib = lib
         return lib
 
@@ -515,7 +525,7 @@ def seam_host(x: torch.Tensor, y: torch.Tensor, pre_in: torch.Tensor, fn: torch.
 def device_status() -> int:
     """Synchronise the current device and read-and-clear the library's device
     status word (``mhc_device_status``): 0 = OK, 4 = a bounded in-kernel wait
-    timed out since the last check."""
+    timed out since the last check, 5 = a kv call met a bad index."""
     return load_library().mhc_device_status()
 
 
@@ -535,3 +545,6 @@ def pre_plan(T: int, n: int = 4, C: int = 5120) -> dict:
                                   ctypes.byref(tt))
     _check("mhc_pre_delayed_plan", st)
     return {"kernel": k.value, "grid": g.value, "cluster": c.value, "tokens_per_tile": tt.value}
+
+
+from .kv import kv_append, kv_attend, kv_cache, kv_workspace_for  # noqa: E402  (kv.py uses the helpers above)

@@ -1,0 +1,382 @@
+// kv_append.cu -- rotation of the new tokens' queries and keys, and the write
+// of keys and values into the paged e4m3 cache (mhc_kv_append).
+//
+// What bounds it: each input number is read once and each output written
+// once, a few operations a number, so memory for long prompts and the launch
+// with its chain of dependent loads (sequence, length, page, scale) for a
+// decode step.  The work of one page, head and tensor (k or v) belongs to one
+// group of threads, because the scale needs the largest magnitude of all of
+// the page's new numbers before the first of them can be rounded.
+#include <cuda_runtime.h>
+
+#include "kv_common.cuh"
+
+namespace mhc {
+namespace kv {
+
+static __device__ unsigned int g_append_status = 0;
+
+struct AppendArgs {
+    Seqs seqs;
+    uint8_t* code[2];                 // k, v
+    float* scale[2];
+    const uint16_t* x[2];
+    int64_t x_stride[2];
+    int heads;
+    const uint16_t* q;
+    uint16_t* q_out;
+    int64_t q_stride, q_out_stride;
+    int q_heads;
+    const float* cos;
+    const float* sin;
+    int rope_rows, R;                 // R == 0: no rotation
+    int interleaved;
+    int window;                       // tokens whose runs one group takes
+    int windows;                      // ceil(T / window)
+    int kv_blocks;                    // blocks [0, kv_blocks) append, the rest rotate q
+    int q_steps;                      // head steps of one warp in the q part
+};
+
+// cos and sin of one thread's 8 elements (chunk c of a head): four pairs when
+// interleaved, one side of eight pairs otherwise.
+struct Turn {
+    float c[8], s[8];
+};
+
+__device__ __forceinline__ void load_turn(const AppendArgs& a, int pos, int c, Turn& w) {
+    if (c * 8 >= a.R) return;
+    const int half = a.R / 2;
+    const size_t row = (size_t)pos * half;
+    if (a.interleaved) {
+        const float4 u = __ldg(reinterpret_cast<const float4*>(a.cos + row + c * 4));
+        const float4 v = __ldg(reinterpret_cast<const float4*>(a.sin + row + c * 4));
+        w.c[0] = u.x; w.c[1] = u.y; w.c[2] = u.z; w.c[3] = u.w;
+        w.s[0] = v.x; w.s[1] = v.y; w.s[2] = v.z; w.s[3] = v.w;
+    } else {
+        const int i = (c * 8) % half;
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+            const float4 u = __ldg(reinterpret_cast<const float4*>(a.cos + row + i + j));
+            const float4 v = __ldg(reinterpret_cast<const float4*>(a.sin + row + i + j));
+            w.c[j] = u.x; w.c[j + 1] = u.y; w.c[j + 2] = u.z; w.c[j + 3] = u.w;
+            w.s[j] = v.x; w.s[j + 1] = v.y; w.s[j + 2] = v.z; w.s[j + 3] = v.w;
+        }
+    }
+}
+
+// Rotates chunk c of a head whose chunks lie in consecutive lanes.  Every
+// product and sum is rounded to fp32 (no fused multiply-add), as the header
+// states it: the result does not depend on who computes it.  Called by whole
+// warps (the shuffle); `w` is read only where the chunk is rotated.
+__device__ __forceinline__ void rotate(const AppendArgs& a, const uint4& raw, int c, int lane, const Turn& w,
+                                       float (&x)[8]) {
+    unpack8(raw, x);
+    if (a.R == 0) return;
+    if (a.interleaved) {
+        if (c * 8 >= a.R) return;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float u = x[2 * j], v = x[2 * j + 1];
+            x[2 * j] = __fsub_rn(__fmul_rn(u, w.c[j]), __fmul_rn(v, w.s[j]));
+            x[2 * j + 1] = __fadd_rn(__fmul_rn(v, w.c[j]), __fmul_rn(u, w.s[j]));
+        }
+    } else {
+        const int hc = a.R / 16;      // chunks of one side
+        const bool first = c < hc, in = c < 2 * hc;
+        const int other = in ? (first ? lane + hc : lane - hc) : lane;
+        uint4 o;
+        o.x = __shfl_sync(0xffffffffu, raw.x, other);
+        o.y = __shfl_sync(0xffffffffu, raw.y, other);
+        o.z = __shfl_sync(0xffffffffu, raw.z, other);
+        o.w = __shfl_sync(0xffffffffu, raw.w, other);
+        if (!in) return;
+        float y[8];
+        unpack8(o, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float p = __fmul_rn(x[j], w.c[j]), r = __fmul_rn(y[j], w.s[j]);
+            x[j] = first ? __fsub_rn(p, r) : __fadd_rn(p, r);
+        }
+    }
+}
+
+// The smallest power of two 2^e with a <= 448 * 2^e = 1.75 * 2^(8+e), e at
+// least -116 (so that the smallest step, 2^-9 * 2^e, is a normal fp32
+// number).  a is finite.
+__device__ __forceinline__ float scale_for(float a) {
+    const uint32_t u = __float_as_uint(a);
+    int e = (int)(u >> 23) - 135 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    e = e < -116 ? -116 : e;
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+// x / scale; exact as a product where scale is a power of two, which every
+// scale written here is.
+__device__ __forceinline__ void divide(float (&x)[8], float scale) {
+    if ((__float_as_uint(scale) & 0x7fffffu) == 0) {
+        const float r = 1.0f / scale;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] *= r;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] /= scale;
+    }
+}
+
+template <int GT>
+__device__ __forceinline__ void group_sync(int group) {
+    if constexpr (GT > 32) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(GT) : "memory");
+    else __syncwarp();
+}
+
+// Largest of the group's values, for all of its threads; a barrier of the group.
+template <int GT>
+__device__ __forceinline__ float group_max(float v, int group, float* red) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if constexpr (GT > 32) {
+        constexpr int W = GT / 32;
+        const int w = (threadIdx.x % GT) / 32;
+        group_sync<GT>(group);        // the last call's readers are done
+        if (threadIdx.x % 32 == 0) red[group * W + w] = v;
+        group_sync<GT>(group);
+        v = red[group * W];
+#pragma unroll
+        for (int i = 1; i < W; ++i) v = fmaxf(v, red[group * W + i]);
+    } else {
+        __syncwarp();
+    }
+    return v;
+}
+
+// GT threads take one (window, head, k or v); 8 numbers of a token a thread.
+template <int D, int GT>
+__global__ void __launch_bounds__(GT > 256 ? GT : 256) kv_append_kernel(const AppendArgs a) {
+    constexpr int kBlock = GT > 256 ? GT : 256, kGroups = kBlock / GT;
+    constexpr int kChunks = D / 8, kRows = GT / kChunks, kHold = 4;   // rows of one step; steps held in registers
+    __shared__ float red[kBlock / 32];
+    const int lane = threadIdx.x % 32;
+
+    if ((int)blockIdx.x >= a.kv_blocks) {             // queries: a warp takes one token and some of its heads
+        constexpr int kHeads = 32 / kChunks;          // heads of one step
+        constexpr int kAhead = 4;
+        const int steps = (a.q_heads + kHeads - 1) / kHeads;
+        const int parts = (steps + a.q_steps - 1) / a.q_steps;
+        const int64_t w = (int64_t)((int)blockIdx.x - a.kv_blocks) * (kBlock / 32) + threadIdx.x / 32;
+        const int t = (int)(w / parts), part = (int)(w % parts);
+        if (w / parts >= a.seqs.T) return;
+        const int c = lane % kChunks, first = part * a.q_steps * kHeads;
+        const int end = a.q_heads < first + a.q_steps * kHeads ? a.q_heads : first + a.q_steps * kHeads;
+        const int h0 = first + lane / kChunks;
+        const uint16_t* src = a.q + t * a.q_stride + c * 8;
+        uint16_t* dst = a.q_out + t * a.q_out_stride + c * 8;
+        uint4 raw[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)              // the loads do not wait for the position
+            if (h0 + i * kHeads < end) raw[i] = *reinterpret_cast<const uint4*>(src + (h0 + i * kHeads) * D);
+        const int b = seq_of(a.seqs, t, lane);
+        const Span sp = span_of(a.seqs, b);
+        int pos = t >= sp.begin && t < sp.end ? sp.before + (t - sp.begin) : -1;
+        if (pos >= a.rope_rows && a.R) pos = -1;      // reported by the append part
+        Turn turn;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) turn.c[j] = 1.0f, turn.s[j] = 0.0f;
+        if (a.R && pos >= 0) load_turn(a, pos, c, turn);
+        for (int base = first; base < end; base += kHeads * kAhead) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (base + i * kHeads >= end) break;
+                const int h = base + lane / kChunks + i * kHeads;
+                float x[8];
+                uint4 now = raw[i];
+                if (h + kAhead * kHeads < end)
+                    raw[i] = *reinterpret_cast<const uint4*>(src + (h + kAhead * kHeads) * D);
+                rotate(a, now, c, lane, turn, x);
+                if (pos >= 0) now = pack8(x);
+                if (h < end) *reinterpret_cast<uint4*>(dst + h * D) = now;
+            }
+        }
+        return;
+    }
+
+    const int group = threadIdx.x / GT, id = threadIdx.x % GT;
+    const int64_t item = (int64_t)blockIdx.x * kGroups + group;
+    const int head = (int)(item % a.heads), kv = (int)(item / a.heads % 2);
+    const int64_t win = item / (2 * a.heads);
+    if (win >= a.windows) return;
+    const int t1 = (int)((win + 1) * a.window < a.seqs.T ? (win + 1) * a.window : a.seqs.T);
+    const int c = id % kChunks, r0 = id / kChunks;
+    const uint16_t* src = a.x[kv] + head * D + c * 8;
+    const bool turned = kv == 0 && a.R > 0;
+
+    for (int t = (int)(win * a.window); t < t1;) {
+        const int b = seq_of(a.seqs, t, lane);
+        const Span sp = span_of(a.seqs, b);
+        if (sp.bad && id == 0) atomicOr(&g_append_status, kIndexError);
+        if (t < sp.begin || t >= sp.end) {            // cu_q out of order
+            if (id == 0) atomicOr(&g_append_status, kIndexError);
+            ++t;
+            continue;
+        }
+        const Run run = run_at(a.seqs, sp, t);
+        const int t0 = t;
+        t = run.next;
+        if (!starts_run(sp, run, t0)) continue;
+        const int page = page_of(a.seqs, b, run.pos);
+        int n = run.n;
+        if (a.R > 0) {                                // positions beyond the tables: k and v are left out alike
+            const int rows = a.rope_rows - run.pos;
+            if (rows < n) n = rows < 0 ? 0 : rows;
+        }
+        if ((page < 0 || n < run.n) && id == 0) atomicOr(&g_append_status, kIndexError);
+        if (page < 0 || n == 0) continue;
+
+        float* scale_at = a.scale[kv] + (int64_t)page * a.heads + head;
+        uint8_t* code = a.code[kv] + ((int64_t)page * a.heads + head) * a.seqs.page_tokens * D;
+        const float old = run.slot ? *scale_at : 0.0f;
+
+        auto load = [&](int r, float (&x)[8]) {       // r may be past the run: zeros
+            uint4 raw = make_uint4(0, 0, 0, 0);
+            Turn turn;
+            if (r < n) {
+                raw = *reinterpret_cast<const uint4*>(src + (int64_t)(t0 + r) * a.x_stride[kv]);
+                if (turned) load_turn(a, run.pos + r, c, turn);
+            }
+            if (turned) rotate(a, raw, c, lane, turn, x);
+            else unpack8(raw, x);
+            if (r >= n) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+            }
+        };
+        auto largest = [](const float (&x)[8], float m) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = finite(x[j]) ? fmaxf(m, fabsf(x[j])) : m;
+            return m;
+        };
+        float x[kHold][8], top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kHold; ++i)
+            if (i * kRows < n) {                      // the same for the whole group
+                load(i * kRows + r0, x[i]);
+                top = largest(x[i], top);
+            }
+        for (int base = kHold * kRows; base < n; base += kRows) {
+            float y[8];
+            load(base + r0, y);
+            top = largest(y, top);
+        }
+        top = group_max<GT>(top, group, red);
+        const float need = scale_for(top), scale = run.slot ? fmaxf(old, need) : need;
+        if (id == 0) *scale_at = scale;               // every thread has read it: group_max was a barrier
+
+        auto store = [&](int r, float (&y)[8]) {
+            if (r >= n) return;
+            divide(y, scale);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = finite(y[j]) ? y[j] : __int_as_float(0x7fc00000);
+            uint2 v;
+            v.x = e4m3x4(y, 0);
+            v.y = e4m3x4(y, 4);
+            *reinterpret_cast<uint2*>(code + (int64_t)(run.slot + r) * D + c * 8) = v;
+        };
+#pragma unroll
+        for (int i = 0; i < kHold; ++i)
+            if (i * kRows < n) store(i * kRows + r0, x[i]);
+        for (int base = kHold * kRows; base < n; base += kRows) {
+            float y[8];
+            load(base + r0, y);
+            store(base + r0, y);
+        }
+        if (run.slot && scale != old) {               // the scale grew: round the page's earlier slots once more
+            const float by = old / scale;
+            for (int i = id; i < run.slot * kChunks; i += GT) {
+                uint2* at = reinterpret_cast<uint2*>(code) + i;
+                const uint2 v = *at;
+                float y[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t h = f16x2_of_e4m3x2((uint16_t)((j < 2 ? v.x : v.y) >> (16 * (j & 1))));
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                    y[2 * j] = f.x * by;
+                    y[2 * j + 1] = f.y * by;
+                }
+                *at = make_uint2(e4m3x4(y, 0), e4m3x4(y, 4));
+            }
+        }
+    }
+}
+
+template <int D, int GT>
+static cudaError_t launch_append(AppendArgs& a, cudaStream_t stream) {
+    constexpr int kBlock = GT > 256 ? GT : 256;
+    const int64_t items = (int64_t)a.windows * a.heads * 2;
+    const int64_t kv_blocks = (items + kBlock / GT - 1) / (kBlock / GT);
+    int64_t q_blocks = 0;
+    if (a.q) {
+        const int heads = 32 / (D / 8), steps = (a.q_heads + heads - 1) / heads;
+        const int64_t warps = (int64_t)a.seqs.T * ((steps + a.q_steps - 1) / a.q_steps);
+        q_blocks = (warps + kBlock / 32 - 1) / (kBlock / 32);
+    }
+    if (kv_blocks + q_blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    a.kv_blocks = (int)kv_blocks;
+    kv_append_kernel<D, GT><<<(unsigned)(kv_blocks + q_blocks), kBlock, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code, float* k_scale, float* v_scale,
+                             int heads, int head_dim, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                             int64_t v_stride, const uint16_t* q, int64_t q_stride, int q_heads, uint16_t* q_out,
+                             int64_t q_out_stride, const float* cos, const float* sin, int rope_rows, int R,
+                             int interleaved, cudaStream_t stream) {
+    AppendArgs a;
+    a.seqs = seqs;
+    a.code[0] = k_code; a.code[1] = v_code;
+    a.scale[0] = k_scale; a.scale[1] = v_scale;
+    a.x[0] = k; a.x[1] = v;
+    a.x_stride[0] = k_stride; a.x_stride[1] = v_stride;
+    a.heads = heads;
+    a.q = q; a.q_out = q_out;
+    a.q_stride = q_stride; a.q_out_stride = q_out_stride;
+    a.q_heads = q_heads;
+    a.cos = cos; a.sin = sin;
+    a.rope_rows = rope_rows; a.R = R;
+    a.interleaved = interleaved;
+    // Few new tokens a sequence: a warp for each token that may start a run.
+    // Many: as many threads as hold a whole page, for each window of a page.
+    const bool few = seqs.T < 8 * (int64_t)seqs.B;
+    a.window = few ? 1 : seqs.page_tokens;
+    a.windows = (seqs.T + a.window - 1) / a.window;
+    a.q_steps = seqs.T < 2048 ? 1 : 1 << 20;
+    const int gt = few ? 32 : seqs.page_tokens * head_dim / 32;
+    if (head_dim == 64) {
+        switch (gt) {
+            case 32: return launch_append<64, 32>(a, stream);
+            case 64: return launch_append<64, 64>(a, stream);
+            case 128: return launch_append<64, 128>(a, stream);
+            case 256: return launch_append<64, 256>(a, stream);
+        }
+    } else if (head_dim == 128) {
+        switch (gt) {
+            case 32: return launch_append<128, 32>(a, stream);
+            case 64: return launch_append<128, 64>(a, stream);
+            case 128: return launch_append<128, 128>(a, stream);
+            case 256: return launch_append<128, 256>(a, stream);
+            case 512: return launch_append<128, 512>(a, stream);
+        }
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t read_append_status(unsigned int* status) {
+    unsigned int v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_append_status, sizeof v);
+    if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_append_status, &zero, sizeof zero);
+    *status = v;
+    return e;
+}
+
+}  // namespace kv
+}  // namespace mhc

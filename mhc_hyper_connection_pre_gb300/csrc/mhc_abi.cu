@@ -39,6 +39,11 @@ cudaError_t launch_pre_tc_pack(const float* fn, int C, void* out, cudaStream_t s
 cudaError_t read_device_status(unsigned int* status);
 cudaError_t read_decode_status(unsigned int* status);
 cudaError_t read_collapse_status(unsigned int* status);
+namespace kv {
+cudaError_t read_append_status(unsigned int* status);
+cudaError_t read_attend_status(unsigned int* status);
+constexpr unsigned int kIndexError = 2u;   // as in kv_common.cuh
+}  // namespace kv
 }  // namespace mhc
 
 namespace {
@@ -107,6 +112,17 @@ int tc_clusters(int dev) {
     return g_dev[dev].tc_clusters;
 }
 
+}  // namespace
+
+namespace mhc {
+int kv_num_sms() {
+    const int dev = current_device();
+    return dev < 0 ? 0 : num_sms(dev);
+}
+}  // namespace mhc
+
+namespace {
+
 bool use_tc(int64_t T, int C) { return T >= kTcMinTokens && mhc::pre_tc_supports(C); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -138,6 +154,7 @@ const char* mhc_status_string(mhc_status s) {
         case MHC_ERR_UNSUPPORTED: return "MHC_ERR_UNSUPPORTED: shape this library does not handle (n must be 4, C a multiple of 8 up to 6144)";
         case MHC_ERR_CUDA: return "MHC_ERR_CUDA: a CUDA runtime call or kernel launch failed";
         case MHC_ERR_TIMEOUT: return "MHC_ERR_TIMEOUT: a bounded device-side wait gave up";
+        case MHC_ERR_INDEX: return "MHC_ERR_INDEX: a length, page number or token offset read on the device is out of range";
     }
     return "unknown mhc_status";
 }
@@ -152,7 +169,11 @@ mhc_status mhc_device_status(void) {
     if (mhc::read_device_status(&v) != cudaSuccess) return MHC_ERR_CUDA;
     if (mhc::read_decode_status(&w) != cudaSuccess) return MHC_ERR_CUDA;
     if (mhc::read_collapse_status(&c) != cudaSuccess) return MHC_ERR_CUDA;
-    return (v | w | c) ? MHC_ERR_TIMEOUT : MHC_OK;
+    unsigned int ka = 0, kt = 0;
+    if (mhc::kv::read_append_status(&ka) != cudaSuccess) return MHC_ERR_CUDA;
+    if (mhc::kv::read_attend_status(&kt) != cudaSuccess) return MHC_ERR_CUDA;
+    if (v | w | c | ((ka | kt) & ~mhc::kv::kIndexError)) return MHC_ERR_TIMEOUT;
+    return (ka | kt) ? MHC_ERR_INDEX : MHC_OK;
 }
 
 mhc_status mhc_pre_delayed_plan(int64_t T, int n, int C, int* kernel, int* grid, int* cluster,

@@ -1,0 +1,240 @@
+"""Host-only checks of the paged key/value cache: argument checks of the C
+entry points (no call here gets as far as a launch), the binding's refusals,
+and the kernels' index arithmetic compiled for the host."""
+import ctypes
+import os
+import random
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import mhc_hyper_connection_pre_gb300 as mhc
+from mhc_hyper_connection_pre_gb300 import build as mbuild
+from mhc_hyper_connection_pre_gb300 import kv as kvmod
+
+OK, INVALID, UNSUPPORTED, CUDA_ERR = 0, 1, 2, 3
+HERE = os.path.dirname(os.path.abspath(__file__))
+FAKE = 0x10000000000     # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    mbuild.build()
+    return mhc.load_library()
+
+
+def _cache(**kw):
+    a = dict(k=FAKE, v=FAKE + (1 << 32), k_scale=FAKE + (2 << 32), v_scale=FAKE + (3 << 32), num_pages=100, heads=8,
+             page_tokens=64, head_dim=128)
+    a.update(kw)
+    return kvmod._Cache(*a.values())
+
+
+ROW = (40 + 16) * 128
+QKV = FAKE + (4 << 32)
+
+
+def _append(lib, cache=None, **kw):
+    a = dict(k=QKV + 40 * 256, k_stride=ROW, v=QKV + 48 * 256, v_stride=ROW, q=QKV, q_stride=ROW, q_heads=40,
+             q_out=FAKE + (5 << 32), q_out_stride=40 * 128, cos=FAKE + (6 << 32), sin=FAKE + (7 << 32), rope_rows=1000,
+             rotary_dim=128, interleaved=0, table=FAKE + (8 << 32), width=10, lens=FAKE + (9 << 32), cu=None, B=16,
+             T=16, stream=None)
+    a.update(kw)
+    return lib.mhc_kv_append(cache if cache is not None else _cache(), *a.values())
+
+
+def _attend(lib, cache=None, **kw):
+    a = dict(q=QKV, q_stride=ROW, q_heads=40, table=FAKE + (8 << 32), width=10, lens=FAKE + (9 << 32), cu=None, B=16,
+             T=16, scale=0.1, out=FAKE + (5 << 32), lse=FAKE + (6 << 32), ws=FAKE + (10 << 32), ws_bytes=1 << 30,
+             stream=None)
+    a.update(kw)
+    return lib.mhc_kv_attend(cache if cache is not None else _cache(), *a.values())
+
+
+COMMON = [
+    (dict(T=-1), {}, INVALID), (dict(B=-1), {}, INVALID), (dict(width=0), {}, INVALID),
+    (dict(T=17), {}, INVALID),                                      # no cu_q: one token each
+    (dict(B=0, cu=FAKE + (11 << 32)), {}, INVALID),
+    ({}, dict(heads=0), INVALID), ({}, dict(num_pages=0), INVALID), ({}, dict(head_dim=96), UNSUPPORTED),
+    ({}, dict(head_dim=256), UNSUPPORTED), ({}, dict(page_tokens=48), UNSUPPORTED),
+    ({}, dict(page_tokens=8), UNSUPPORTED), ({}, dict(num_pages=1 << 30), UNSUPPORTED),
+    (dict(width=1 << 26), {}, UNSUPPORTED), (dict(T=1 << 31, B=1 << 31), {}, UNSUPPORTED),
+    ({}, dict(k=None), INVALID), ({}, dict(v=FAKE + (1 << 32) + 8), INVALID), ({}, dict(k_scale=None), INVALID),
+    ({}, dict(v_scale=FAKE + (3 << 32) + 2), INVALID), (dict(table=None), {}, INVALID), (dict(lens=None), {}, INVALID),
+    (dict(cu=FAKE + (11 << 32) + 2), {}, INVALID), (dict(q=QKV + 2), {}, INVALID), (dict(q_stride=ROW + 4), {}, INVALID),
+    (dict(q_stride=40 * 128 - 8), {}, INVALID),
+]
+
+
+@pytest.mark.parametrize("call", [_append, _attend])
+@pytest.mark.parametrize("case", range(len(COMMON)))
+def test_both_calls_refuse(lib, call, case):
+    kw, c, status = COMMON[case]
+    assert call(lib, _cache(**c), **kw) == status
+
+
+def test_append_refuses(lib):
+    assert _append(lib, k=None) == INVALID
+    assert _append(lib, v=QKV + 48 * 256 + 4) == INVALID
+    assert _append(lib, k_stride=8) == INVALID
+    assert _append(lib, q=None) == INVALID                         # q_out without q
+    assert _append(lib, q_out=None) == INVALID
+    assert _append(lib, q_heads=0) == INVALID
+    assert _append(lib, cos=None) == INVALID
+    assert _append(lib, sin=FAKE + (7 << 32) + 4) == INVALID
+    assert _append(lib, rotary_dim=-16) == INVALID
+    assert _append(lib, rotary_dim=24) == UNSUPPORTED
+    assert _append(lib, rotary_dim=144) == UNSUPPORTED
+    assert _append(lib, q_out=QKV + 40 * 256, q_out_stride=ROW) == INVALID       # onto k's columns
+    assert _append(lib, q_out=QKV + 256, q_out_stride=ROW) == INVALID            # q shifted by a head
+    assert _append(lib, q_out=QKV, q_out_stride=40 * 128) == INVALID             # q's place, another stride
+    assert _append(lib, q_out=FAKE + 256) == INVALID                             # inside the cache
+    assert _append(lib, _cache(v=FAKE + 64)) == INVALID                          # k and v overlap
+    assert _append(lib, _cache(k_scale=FAKE + 64)) == INVALID
+    assert _append(lib, k=FAKE + 128) == INVALID                                 # reads the cache it writes
+    assert _append(lib, T=0, B=0, k=None, q=None, q_out=None, cu=FAKE) == OK
+
+
+def test_attend_refuses(lib):
+    assert _attend(lib, q_heads=41) == INVALID
+    assert _attend(lib, q_heads=0) == INVALID
+    assert _attend(lib, _cache(heads=1), q_heads=129, q_stride=129 * 128) == UNSUPPORTED
+    assert _attend(lib, scale=-1.0) == INVALID
+    assert _attend(lib, scale=float("nan")) == INVALID
+    assert _attend(lib, scale=float("inf")) == INVALID
+    assert _attend(lib, out=None) == INVALID
+    assert _attend(lib, out=QKV + 256) == INVALID
+    assert _attend(lib, out=FAKE + 256) == INVALID
+    assert _attend(lib, lse=FAKE + (5 << 32) + 64) == INVALID
+    assert _attend(lib, lse=FAKE + (6 << 32) + 4) == INVALID
+    assert _attend(lib, ws=FAKE + (5 << 32)) == INVALID
+    assert _attend(lib, T=0, B=0, q=None, out=None, cu=FAKE) == OK
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a well-formed call would be launched")
+def test_well_formed_calls_pass_the_checks(lib):
+    """With no device in the process they end as MHC_ERR_CUDA."""
+    assert _append(lib) == CUDA_ERR
+    assert _append(lib, q=None, q_out=None, cos=None, sin=None) == CUDA_ERR
+    assert _append(lib, q_out=QKV, q_out_stride=ROW) == CUDA_ERR                  # in place
+    assert _append(lib, q_out=QKV + ROW * 2 * 16, q_out_stride=ROW) == CUDA_ERR   # just behind
+    assert _append(lib, T=40, cu=FAKE + (11 << 32)) == CUDA_ERR
+    assert _attend(lib) == CUDA_ERR
+    assert _attend(lib, lse=None) == CUDA_ERR
+    c = _cache()
+    assert lib.mhc_kv_attend_workspace_bytes(c, 40, 16, 16) == 0                  # sized on a device
+    assert lib.mhc_kv_attend_workspace_bytes(c, 41, 16, 16) == 0
+
+
+def test_status_string_of_a_bad_index(lib):
+    assert lib.mhc_status_string(5).decode().startswith("MHC_ERR_INDEX")
+
+
+def _cpu_cache(H=2, P=16, D=64, pages=3):
+    return mhc.kv_cache(pages, H, P, D, device="cpu")
+
+
+def test_binding_refuses(lib):
+    c = _cpu_cache()
+    x = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    table, lens = torch.zeros(1, 1, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    with pytest.raises(ValueError):                                # not on a CUDA device
+        mhc.kv_append(c, x, x, table, lens)
+    with pytest.raises(ValueError):
+        mhc.kv_attend(x, c, table, lens)
+    with pytest.raises(ValueError):
+        mhc.kv_attend(x, dict(c, v=c["v"][:2]), table, lens)
+    with pytest.raises(ValueError):
+        mhc.kv_attend(x, dict(c, k_scale=c["k_scale"][:2]), table, lens)
+    with pytest.raises(ValueError):
+        kvmod._rows_arg(x[0], "k", 64, x.device)
+    with pytest.raises(ValueError):
+        kvmod._rows_arg(torch.zeros(4, 64, 2, dtype=torch.bfloat16).transpose(1, 2), "k", 64, x.device)
+    with pytest.raises(TypeError):
+        kvmod._rows_arg(x.half(), "k", 64, x.device)
+    with pytest.raises(TypeError):
+        kvmod._rows_arg(None, "k", 64, x.device)
+    with pytest.raises(ValueError):
+        kvmod._seqs_arg(table, lens[0], None, 1, x.device)
+    with pytest.raises(ValueError):
+        kvmod._seqs_arg(table, lens, None, 2, x.device)
+
+
+# ---------------------------------------------------------- index arithmetic ---
+
+@pytest.fixture(scope="module")
+def shim(tmp_path_factory):
+    so = str(tmp_path_factory.mktemp("kv") / "libkvshim.so")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover=undefined", "-shared",
+                    "-fPIC", "-x", "c++", os.path.join(HERE, "kv_index_shim.cpp"), "-o", so], check=True)
+    return ctypes.CDLL(so)
+
+
+def _i32(x):
+    return np.ascontiguousarray(np.array(x, dtype=np.int32))
+
+
+def _ptr(x):
+    return None if x is None else x.ctypes.data_as(ctypes.c_void_p)
+
+
+def _seq_of(cu, T, B):
+    """The kernels' search: the last b with cu[b] <= t, for ascending cu."""
+    return _i32([t if cu is None else max(b for b in range(B) if cu[b] <= t) for t in range(T)])
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_runs_cover_every_new_token_once(shim, seed):
+    r = random.Random(seed)
+    P, B = r.choice([16, 32, 64, 128]), r.randint(1, 9)
+    counts = [r.choice([0, 1, 1, 2, r.randint(0, 300)]) for _ in range(B)]
+    lens = [max(0, n + r.choice([0, r.randint(0, 200), -1])) for n in counts]
+    width = max(1, -(-max(lens) // P))
+    table = _i32([[100 * b + i for i in range(width)] for b in range(B)])
+    cu = [0]
+    for n in counts:
+        cu.append(cu[-1] + n)
+    T = cu[-1]
+    if T == 0:
+        return
+    seq = _seq_of(cu, T, B)
+    out = np.zeros((T, 7), dtype=np.int32)
+    lens_a, cu_a = _i32(lens), _i32(cu)
+    shim.kv_runs(_ptr(table), _ptr(lens_a), _ptr(cu_a), width, B, T, P, 100 * B, _ptr(seq), _ptr(out))
+    for window in (1, P):
+        writer = [0] * T
+        for w in range(0, T, window):
+            t, end = w, min(T, w + window)
+            while t < end:
+                starts, pos, slot, n, nxt, page, bad = out[t]
+                assert not bad and t < nxt <= T
+                if starts:
+                    b = seq[t]
+                    assert page == 100 * b + pos // P and slot == pos % P and slot + n <= P
+                    for i in range(n):
+                        writer[t + i] += 1
+                        assert lens[b] - (cu[b + 1] - (t + i)) == pos + i
+                t = nxt
+        for t in range(T):
+            b = seq[t]
+            assert writer[t] == (1 if lens[b] - (cu[b + 1] - t) >= 0 else 0)
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_runs_stay_inside_whatever_the_arrays_hold(shim, seed):
+    r = random.Random(1000 + seed)
+    wild = lambda: r.choice([0, 1, -1, 5, 17, 2147483647, -2147483648, r.randint(-300, 300)])  # noqa: E731
+    P, B, T, width, pages = r.choice([16, 128]), r.randint(1, 6), r.randint(1, 50), r.randint(1, 4), 7
+    table = _i32([[wild() for _ in range(width)] for _ in range(B)])
+    lens, cu = _i32([wild() for _ in range(B)]), _i32([wild() for _ in range(B + 1)])
+    seq = _i32([r.randrange(B) for _ in range(T)])
+    out = np.zeros((T, 7), dtype=np.int32)
+    shim.kv_runs(_ptr(table), _ptr(lens), _ptr(cu), width, B, T, P, pages, _ptr(seq), _ptr(out))
+    for t in range(T):
+        starts, pos, slot, n, nxt, page, bad = out[t]
+        assert nxt > t and nxt <= T
+        if starts:
+            assert 0 <= slot and n >= 1 and slot + n <= P and t + n <= T and pos + n <= width * P
+            assert -1 <= page < pages

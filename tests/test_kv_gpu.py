@@ -1,0 +1,445 @@
+"""GPU checks of the paged 8-bit key/value cache: mhc_kv_append and
+mhc_kv_attend, through the binding, against plain 64-bit forms."""
+import math
+
+import pytest
+import torch
+
+import mhc_hyper_connection_pre_gb300 as mhc
+from mhc_hyper_connection_pre_gb300.graphs import SeamGraph
+from kv_reference import check_append, check_attend, e4m3_round
+
+pytestmark = pytest.mark.gpu
+
+INDEX_ERROR = 5
+
+
+@pytest.fixture(autouse=True)
+def _status():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    mhc.load_library()
+    assert mhc.device_status() == 0
+    yield
+    assert mhc.device_status() == 0
+
+
+def _cpu(d):
+    return {k: v.cpu() for k, v in d.items()}
+
+
+def _tables(lens, P, seed, extra=2, width=None):
+    """A table of distinct pages in random order, unused entries out of range."""
+    g = torch.Generator().manual_seed(seed)
+    used = [-(-n // P) for n in lens]
+    pages = sum(used) + extra
+    order = torch.randperm(pages, generator=g).tolist()
+    width = width or max(1, max(used))
+    rows, at = [], 0
+    for n in used:
+        rows.append(order[at:at + n] + [-7] * (width - n))
+        at += n
+    return rows, pages
+
+
+def _random_cache(pages, H, P, D, seed, powers=True):
+    """A cache as appended normal values leave it; every slot filled."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    cache = mhc.kv_cache(pages, H, P, D)
+    for n in ("k", "v"):
+        x = torch.randn(pages, H, P, D, generator=g, device="cuda").clamp(-6, 6) * 64
+        cache[n].copy_(x.to(torch.float8_e4m3fn))
+        s = torch.randint(-8, -4, (pages, H), generator=g, device="cuda").float().exp2()
+        if not powers:
+            s = s * (1 + torch.rand(pages, H, generator=g, device="cuda"))
+        cache[n + "_scale"].copy_(s)
+    return cache
+
+
+def _spoil_unused(cache, rows, lens, P):
+    """NaN codes in every slot past a sequence's end."""
+    for r, n in zip(rows, lens):
+        if n % P:
+            for c in ("k", "v"):
+                cache[c].view(torch.uint8)[r[n // P], :, n % P:] = 0x7F
+
+
+def _cu(counts):
+    cu = [0]
+    for n in counts:
+        cu.append(cu[-1] + n)
+    return cu
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ append ---
+
+APPENDS = [
+    # D, P, H, Hq, new tokens of each sequence (None: one each), lengths, R, interleaved, fused
+    (128, 64, 8, 40, None, [1], 128, False, True),
+    (128, 64, 8, 40, None, [64, 65, 1, 130, 0, 63], 128, False, True),
+    (128, 16, 2, 2, [3, 0, 17, 1], [3, 5, 40, 33], 64, True, False),
+    (64, 16, 3, 9, [16, 1, 15], [16, 17, 47], 64, False, True),
+    (64, 32, 1, 5, [100], [101], 32, True, True),
+    (64, 128, 2, 16, [300, 5], [301, 6], 16, False, False),
+    (128, 128, 4, 4, [257, 128, 1], [300, 128, 129], 128, True, True),
+    (128, 32, 2, 8, [5, 4], [3, 4], 128, False, True),        # more new tokens than the sequence has places for
+    (64, 64, 4, 8, [70], [200], 0, False, False),
+    (128, 16, 1, 1, [1] * 45 + [2], [20] * 46, 128, False, True),
+    (64, 16, 1, 1, [2] * 70, list(range(2, 72)), 64, True, False),
+]
+
+
+def _append_inputs(T, H, Hq, D, R, fused, seed, width):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    if fused:
+        rows = torch.randn(T, (Hq + 2 * H) * D, generator=g, device="cuda").bfloat16()
+        q = rows[:, :Hq * D].unflatten(1, (Hq, D))
+        k = rows[:, Hq * D:(Hq + H) * D].unflatten(1, (H, D))
+        v = rows[:, (Hq + H) * D:].unflatten(1, (H, D))
+    else:
+        q, k, v = (torch.randn(T, n, D, generator=g, device="cuda").bfloat16() for n in (Hq, H, H))
+    cos = sin = None
+    if R:
+        angle = torch.rand(width, R // 2, generator=g, device="cuda") * 6.3
+        cos, sin = angle.cos(), angle.sin()
+    return q, k, v, cos, sin
+
+
+@pytest.mark.parametrize("case", range(len(APPENDS)))
+def test_append_is_its_definition(case):
+    D, P, H, Hq, counts, lens, R, inter, fused = APPENDS[case]
+    rows, pages = _tables(lens, P, case)
+    cu = None if counts is None else _cu(counts)
+    T = len(lens) if counts is None else cu[-1]
+    cache = _random_cache(pages, H, P, D, case)
+    for n in ("k", "v"):
+        cache[n + "_scale"] *= 2.0 ** -3                       # old scales that some appends outgrow
+    q, k, v, cos, sin = _append_inputs(T, H, Hq, D, R, fused, case, max(lens) + 1)
+    before = _cpu({n: t.clone() for n, t in cache.items()})
+    q_out = mhc.kv_append(cache, k, v, _i32(rows), _i32(lens), None if cu is None else _i32(cu), q=q, cos=cos,
+                          sin=sin, interleaved=inter)
+    table = _cpu({"k": k, "v": v, "q": q, "o": q_out})
+    check_append(before, _cpu(cache), table["k"], table["v"], rows, lens, cu, None if cos is None else cos.cpu(),
+                 None if sin is None else sin.cpu(), inter, table["q"], table["o"])
+
+
+def test_append_without_queries_and_in_place():
+    D, P, H, lens = 128, 16, 2, [5, 40, 17]
+    rows, pages = _tables(lens, P, 3)
+    q, k, v, cos, sin = _append_inputs(3, H, 4, D, D, True, 3, 64)
+    a, b = _random_cache(pages, H, P, D, 3), _random_cache(pages, H, P, D, 3)
+    expect = mhc.kv_append(a, k, v, _i32(rows), _i32(lens), q=q, cos=cos, sin=sin).clone()
+    assert mhc.kv_append(b, k, v, _i32(rows), _i32(lens), cos=cos, sin=sin) is None
+    for n in a:
+        assert torch.equal(a[n].view(torch.uint8), b[n].view(torch.uint8))
+    got = mhc.kv_append(a, k, v, _i32(rows), _i32(lens), q=q, cos=cos, sin=sin, q_out=q)
+    assert got is q and torch.equal(q, expect)
+    for n in a:                                                # appending the same tokens again changes nothing
+        assert torch.equal(a[n].view(torch.uint8), b[n].view(torch.uint8))
+
+
+def test_append_token_by_token_and_at_once():
+    """A prompt appended at once and token by token: the same scales, and the
+    same numbers where growing scales did not push them into e4m3's subnormals."""
+    D, P, H, n = 64, 16, 2, 50
+    rows, pages = _tables([n], P, 5)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    k, v = (torch.randn(n, H, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    k *= torch.logspace(-2, 2, n, base=2, device="cuda")[:, None, None].bfloat16()
+    whole, steps = mhc.kv_cache(pages, H, P, D), mhc.kv_cache(pages, H, P, D)
+    mhc.kv_append(whole, k, v, _i32(rows), _i32([n]), _i32([0, n]))
+    for t in range(n):
+        mhc.kv_append(steps, k[t:t + 1], v[t:t + 1], _i32(rows), _i32([t + 1]))
+    for c in ("k", "v"):
+        assert torch.equal(whole[c + "_scale"], steps[c + "_scale"])
+        x, y = whole[c].float(), steps[c].float()
+        assert torch.equal(x[x.abs() >= 2.0 ** -6], y[x.abs() >= 2.0 ** -6])
+        assert ((x - y).abs() <= 2.0 ** -9).all()
+
+
+def test_append_special_numbers():
+    """Infinities and NaN are stored as NaN and do not move the scale; zeros
+    and the smallest numbers take the smallest scale."""
+    D, P, H = 64, 16, 1
+    k = torch.zeros(6, H, D, device="cuda", dtype=torch.bfloat16)
+    v = torch.zeros_like(k)
+    k[0, 0, :4] = torch.tensor([math.inf, -math.inf, math.nan, 3.0])
+    k[1, 0, :3] = torch.tensor([448.0, 450.0, -1e-3])
+    k[2, 0, 0] = 2.0 ** -130
+    k[4, 0, 0] = 3.3e38
+    v[3, 0, 0] = -448.0 * 2 ** 5
+    lens = [1] * 6
+    rows, pages = _tables(lens, P, 1)
+    cache = _random_cache(pages, H, P, D, 1)
+    before = _cpu({n: t.clone() for n, t in cache.items()})
+    mhc.kv_append(cache, k, v, _i32(rows), _i32(lens))
+    after = _cpu(cache)
+    check_append(before, after, k.cpu(), v.cpu(), rows, lens, None)
+    p = [r[0] for r in rows]
+    assert after["k"][p[0], 0, 0, :3].double().isnan().all() and after["k_scale"][p[0], 0] == 2.0 ** -7
+    assert after["k_scale"][p[1], 0] == 2.0 and after["k_scale"][p[3], 0] == 2.0 ** -116
+    assert after["v_scale"][p[3], 0] == 2.0 ** 5
+
+
+def test_append_bad_indices_touch_nothing():
+    """Pages out of range, lengths past the table and positions past the
+    rotation's tables: the tokens concerned are left out, the others are not."""
+    D, P, H = 128, 16, 2
+    lens = [5, 20, 33, 4, 10]
+    rows, pages = _tables(lens, P, 9)
+    bad = [list(r) for r in rows]
+    bad[1][1], bad[2][2] = pages, -1
+    q, k, v, cos, sin = _append_inputs(5, H, 2, D, D, True, 9, 40)
+    cache, expect = _random_cache(pages, H, P, D, 9), _random_cache(pages, H, P, D, 9)
+    mhc.kv_append(cache, k, v, _i32(bad), _i32(lens), q=q, cos=cos, sin=sin)
+    assert mhc.device_status() == INDEX_ERROR
+    keep = [0, 3, 4]
+    mhc.kv_append(expect, k[keep], v[keep], _i32([rows[i] for i in keep]), _i32([lens[i] for i in keep]), cos=cos,
+                  sin=sin)
+    for n in cache:
+        assert torch.equal(cache[n].view(torch.uint8), expect[n].view(torch.uint8))
+    cache = _random_cache(pages, H, P, D, 9)
+    before = {n: t.clone() for n, t in cache.items()}
+    mhc.kv_append(cache, k, v, _i32(rows), _i32(lens), cos=cos[:2], sin=sin[:2])          # no row for any position
+    assert mhc.device_status() == INDEX_ERROR
+    for n in cache:
+        assert torch.equal(cache[n].view(torch.uint8), before[n].view(torch.uint8))
+    mhc.kv_append(cache, k, v, _i32(rows), _i32([0] * 5), _i32([0, 9, -4, 900, 2, 5]))    # offsets out of order
+    assert mhc.device_status() == INDEX_ERROR
+
+
+# ------------------------------------------------------------------ attend ---
+
+ATTENDS = [
+    # D, P, H, Hq, new tokens (None: one each), lengths
+    (128, 64, 8, 40, None, [1]),
+    (128, 64, 8, 40, None, [1000]),
+    (128, 64, 2, 2, None, [1, 63, 64, 65, 0, 127, 128, 129, 500]),
+    (64, 16, 4, 16, None, [15, 16, 17, 31, 32, 33, 0, 0, 257]),
+    (64, 32, 1, 7, None, [2049, 3, 900]),
+    (128, 128, 1, 16, None, [4097, 1]),
+    (128, 16, 3, 9, [4, 1, 3, 0, 2], [40, 1, 3, 17, 300]),
+    (128, 32, 2, 32, [4, 4, 4], [100, 4, 2]),                # rows without keys
+    (64, 64, 2, 2, [70, 1], [70, 900]),
+    (64, 16, 2, 10, [33], [50]),
+    (128, 64, 1, 5, [150, 40], [150, 300]),
+    (128, 128, 2, 6, [129, 64], [200, 64]),
+    (64, 128, 1, 1, [260], [260]),
+    (128, 16, 1, 128, [3], [90]),
+    (64, 32, 1, 64, None, [77, 5]),
+    (128, 64, 1, 40, [65, 0, 200], [65, 10, 190]),
+]
+
+
+def _attend(case, seed, scale=None, powers=True, fill=None, **kw):
+    D, P, H, Hq, counts, lens = case
+    rows, pages = _tables(lens, P, seed)
+    cu = None if counts is None else _cu(counts)
+    T = len(lens) if counts is None else cu[-1]
+    cache = _random_cache(pages, H, P, D, seed, powers)
+    _spoil_unused(cache, rows, lens, P)
+    g = torch.Generator(device="cuda").manual_seed(seed + 1)
+    q = torch.randn(T, Hq + 2, D, generator=g, device="cuda").bfloat16()[:, 1:-1]         # rows with a stride
+    if fill:
+        fill(q, cache, rows)
+    got = mhc.kv_attend(q, cache, _i32(rows), _i32(lens), None if cu is None else _i32(cu), softmax_scale=scale,
+                        return_lse=True, **kw)
+    return got, (q, cache, rows, lens, cu, D ** -0.5 if scale is None else scale)
+
+
+@pytest.mark.parametrize("case", range(len(ATTENDS)))
+def test_attend_is_its_definition(case):
+    got, of = _attend(ATTENDS[case], case)
+    check_attend(got, *of)
+
+
+@pytest.mark.parametrize("case", [1, 3, 6, 10, 15])
+@pytest.mark.parametrize("scale", [0.0, 1.5])
+def test_attend_flat_and_sharp(case, scale):
+    """A scale of zero (the mean of the values) and one that leaves one key;
+    page scales that are no powers of two."""
+    got, of = _attend(ATTENDS[case], 100 + case, scale, powers=False)
+    check_attend(got, *of)
+
+
+@pytest.mark.parametrize("case", [6, 7, 8, 10, 15])
+def test_attend_later_keys_stay_out(case):
+    """NaN and the largest numbers in keys and values after a token's position
+    (later tokens of its own sequence) do not reach its row."""
+    D, P, H, Hq, counts, lens = ATTENDS[case]
+
+    def fill(q, cache, rows):
+        for b, (n, m) in enumerate(zip(lens, counts)):
+            if m >= 2 and n >= 2:
+                for c in ("k", "v"):
+                    cache[c].view(torch.uint8)[rows[b][(n - 1) // P], :, (n - 1) % P] = 0x7F
+                    cache[c].view(torch.uint8)[rows[b][(n - 2) // P], :, (n - 2) % P, ::3] = 0x7E
+    got, (q, cache, rows, _, cu, scale) = _attend(ATTENDS[case], 200 + case, fill=fill)
+    clean = {n: t.clone() for n, t in cache.items()}
+    for b, (n, m) in enumerate(zip(lens, counts)):
+        if m >= 2 and n >= 2:
+            for c in ("k", "v"):
+                clean[c].view(torch.uint8)[rows[b][(n - 1) // P], :, (n - 1) % P] = 0x38
+    last = [cu[b + 1] - 1 for b, (n, m) in enumerate(zip(lens, counts)) if m >= 2 and n >= 2]
+    keep = [t for t in range(cu[-1]) if t not in last]
+    ref = mhc.kv_attend(q, clean, _i32(rows), _i32(lens), _i32(cu), return_lse=True)
+    check_attend(ref, q, clean, rows, lens, cu, scale)
+    for n in ("out", "lse"):
+        assert torch.equal(got[n][keep], ref[n][keep])
+        assert got[n][last].isnan().all()
+
+
+def test_attend_nan_query_stays_in_its_row():
+    got, of = _attend(ATTENDS[6], 300, fill=lambda q, c, r: q[2, 1, :2].fill_(math.nan))
+    assert got["out"][2, 1].isnan().all() and got["lse"][2, 1].isnan()
+    got["out"][2, 1], of[0][2, 1] = 0, 0
+    assert not got["out"].isnan().any()
+
+
+def test_attend_large_and_small_queries():
+    def fill(q, cache, rows):
+        q[0] *= 2.0 ** 40
+        q[1] *= 2.0 ** -60
+        q[2, :, ::2] *= 2.0 ** -20
+        q[3] = 0
+    got, of = _attend((128, 32, 2, 8, None, [70, 70, 70, 70]), 400, fill=fill)
+    check_attend(got, *of)
+
+
+@pytest.mark.parametrize("case", [1, 2, 4, 6, 8, 11])
+def test_attend_is_deterministic(case):
+    a, of = _attend(ATTENDS[case], case)
+    b, _ = _attend(ATTENDS[case], case)
+    assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
+
+
+def test_attend_long_context():
+    got, of = _attend((128, 64, 1, 5, None, [40000, 3]), 1)
+    check_attend(got, *of)
+
+
+def test_attend_many_sequences():
+    lens = [(i * 37) % 200 for i in range(700)]
+    got, of = _attend((64, 16, 1, 2, None, lens), 2)
+    check_attend(got, *of)
+
+
+def test_attend_and_append_far_pages():
+    """A cache whose last pages start beyond 2^32 bytes."""
+    D, P, H = 128, 128, 8
+    pages = (1 << 32) // (D * P * H) + 40
+    cache = mhc.kv_cache(pages, H, P, D)
+    small = _random_cache(3, H, P, D, 7)
+    far = [pages - 1, pages - 20, pages - 7]
+    for n in cache:
+        for i, p in enumerate(far):
+            cache[n][p].copy_(small[n][i])
+    g = torch.Generator(device="cuda").manual_seed(8)
+    q, k, v = (torch.randn(2, h, D, generator=g, device="cuda").bfloat16() for h in (16, H, H))
+    lens = [130, 100]
+    near_rows, far_rows = [[0, 1], [2, 0]], [[far[0], far[1]], [far[2], far[0]]]
+    for c, r in ((cache, far_rows), (small, near_rows)):
+        mhc.kv_append(c, k, v, _i32(r), _i32(lens))
+    for n in cache:
+        for i, p in enumerate(far):
+            assert torch.equal(cache[n][p].view(torch.uint8), small[n][i].view(torch.uint8))
+    a = mhc.kv_attend(q, cache, _i32(far_rows), _i32(lens), return_lse=True)
+    b = mhc.kv_attend(q, small, _i32(near_rows), _i32(lens), return_lse=True)
+    assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
+    del cache
+    torch.cuda.empty_cache()
+
+
+def test_attend_bad_pages_are_left_out():
+    """Page numbers out of range hide their keys, and a length past the table
+    is cut to it; the other sequences are as ever."""
+    D, P, H, Hq = 128, 16, 2, 8
+    lens = [40, 50, 20]
+    rows, pages = _tables(lens, P, 11, width=4)
+    cache = _random_cache(pages, H, P, D, 11)
+    q = torch.randn(3, Hq, D, device="cuda").bfloat16()
+    good = mhc.kv_attend(q, cache, _i32(rows), _i32(lens), return_lse=True)
+    bad = [list(r) for r in rows]
+    bad[1][1] = pages + 5
+    got = mhc.kv_attend(q, cache, _i32(bad), _i32(lens), return_lse=True)
+    assert mhc.device_status() == INDEX_ERROR
+    for n in got:
+        assert torch.equal(got[n][[0, 2]], good[n][[0, 2]])
+    assert got["out"][1].isfinite().all() and (got["lse"][1] < good["lse"][1]).all()
+    bad = [list(r) for r in rows]
+    bad[0] = [-1, pages, 1 << 30, -(1 << 31)]
+    got = mhc.kv_attend(q, cache, _i32(bad), _i32(lens), return_lse=True)
+    assert mhc.device_status() == INDEX_ERROR
+    assert (got["out"][0] == 0).all() and (got["lse"][0] == -math.inf).all()
+    got = mhc.kv_attend(q, cache, _i32(rows), _i32([40, 50, -3]), return_lse=True)
+    assert mhc.device_status() == INDEX_ERROR
+    assert (got["out"][2] == 0).all() and torch.equal(got["out"][:2], good["out"][:2])
+    full = [r if i != 2 else r[:2] + rows[0][:2] for i, r in enumerate(rows)]
+    cut = mhc.kv_attend(q, cache, _i32(full), _i32([40, 50, 64]))
+    got = mhc.kv_attend(q, cache, _i32(full), _i32([40, 50, 2000000000]))
+    assert mhc.device_status() == INDEX_ERROR
+    assert torch.equal(got["out"], cut["out"])
+    mhc.kv_attend(q, cache, _i32(rows), _i32(lens), _i32([0, 5, 1, 3]))                     # offsets out of order
+    assert mhc.device_status() == INDEX_ERROR
+
+
+# ------------------------------------------------- streams, graphs, chain ---
+
+def test_other_stream_and_graph_replay():
+    """Both calls on a stream of their own, captured and replayed: the same
+    bits as on the current stream."""
+    D, P, H, Hq = 128, 64, 2, 10
+    lens = [100, 64, 1]
+    rows, pages = _tables(lens, P, 21)
+    q, k, v, cos, sin = _append_inputs(3, H, Hq, D, D, True, 21, 128)
+    table, n = _i32(rows), _i32(lens)
+    a, b = _random_cache(pages, H, P, D, 21), _random_cache(pages, H, P, D, 21)
+    qa = mhc.kv_append(a, k, v, table, n, q=q, cos=cos, sin=sin)
+    oa = mhc.kv_attend(qa, a, table, n, return_lse=True)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    qb = mhc.kv_append(b, k, v, table, n, q=q, cos=cos, sin=sin, stream=st)
+    ob = mhc.kv_attend(qb, b, table, n, return_lse=True, stream=st)
+    st.synchronize()
+    for x in ("out", "lse"):
+        assert torch.equal(oa[x], ob[x])
+    out, lse, qo = torch.zeros_like(oa["out"]), torch.zeros_like(oa["lse"]), torch.empty_like(qa)
+    ws = mhc.kv_workspace_for(b, Hq, 3, 3, st)
+
+    def step(s):
+        mhc.kv_append(b, k, v, table, n, q=q, cos=cos, sin=sin, q_out=qo, stream=s)
+        mhc.kv_attend(qo, b, table, n, out=out, lse=lse, workspace=ws, stream=s)
+    graph = SeamGraph(step, st)
+    for _ in range(3):
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, oa["out"]) and torch.equal(lse, oa["lse"])
+
+
+def test_workspace_contents_do_not_matter():
+    case = (128, 64, 1, 5, None, [5000, 10])
+    a, (q, cache, rows, lens, _, _) = _attend(case, 31)
+    ws = mhc.kv_workspace_for(cache, 5, 2, 2)
+    if ws is not None:
+        for fill in (0xFF, 0x7F, 0):
+            ws.fill_(fill)
+            b = mhc.kv_attend(q, cache, _i32(rows), _i32(lens), return_lse=True, workspace=ws)
+            assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
+
+
+def test_no_tokens():
+    cache = mhc.kv_cache(2, 2, 16, 64)
+    none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    assert mhc.kv_append(cache, none, none, _i32([[0]]), _i32([5]), _i32([0, 0])) is None
+    assert mhc.kv_attend(none, cache, _i32([[0]]), _i32([5]), _i32([0, 0]))["out"].shape == (0, 2, 64)
+
+
+def test_e4m3_rounding_of_the_reference_is_the_format():
+    x = torch.linspace(-448, 448, 40001)
+    x = torch.cat([x, x * 2.0 ** -14])
+    assert torch.equal(e4m3_round(x.double()), x.to(torch.float8_e4m3fn).double())
