@@ -1,129 +1,807 @@
 // kv_attend.cu -- causal attention of the new tokens over the paged e4m3
-// cache (mhc_kv_attend).
+// cache (mhc_kv_attend), for few rows a sequence: decoding.
 //
-// One warp takes one new token and query head and walks over the keys it
-// sees, 32 at a time: each lane forms one key's product with the query, the
-// running maximum and sum of the softmax are kept in fp32, and each lane
-// collects its share of the head's dimensions over the 32 values.
+// Mathematics.  The rows of a tile are the new tokens and query heads that
+// share a key/value head (8 or 16 of them).  A warp takes 32 keys at a time
+// and forms S^T = K Q^T (keys x rows) and O^T += V^T P^T (dims x rows) with
+// m16n8k16 matrix instructions in f16 with fp32 sums, so that the few rows
+// fill the 8-wide side and none of the 16-wide side is padding.  e4m3 becomes
+// f16 exactly; a query row becomes f16 after a division by a power of two that
+// puts its largest element into [2^7, 2^8), which loses nothing of bf16's 8
+// bits down to 2^-21 of the largest.  The softmax keeps a running maximum and
+// sum for each row in fp32, in powers of two.  The weights are rounded to f16
+// for the second product (2^-11 of each, well below the output's own bf16
+// rounding) after a factor of 2^10 that keeps small weights out of f16's
+// subnormal range.  A page's value scale multiplies the weights, relative to
+// the largest scale met so far, so that they stay below 2^10.
+//
+// What bounds it: the cache is read once, 2 * head_dim bytes a key and head
+// for 4 * head_dim * group operations, far below the matrix rate for groups up
+// to 16: HBM.  So every warp runs on its own, with its own ring of TMA loads
+// (24 KB, 192 KB in flight on an SM) and its own part of the keys, and the
+// warps of a block meet only when a segment ends.  All blocks take equally
+// many units of 64 keys whatever the lengths are (kv_index.cuh); what a border
+// cuts is left as partial sums in the workspace and joined by a second, small
+// kernel.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "kv_common.cuh"
+#include "sm100.cuh"
 
 namespace mhc {
 namespace kv {
 
-static __device__ unsigned int g_attend_status = 0;
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kSub = 32;                      // keys of one load of one warp
+constexpr int kTable = 256;                   // sequences of the walk's table
+constexpr int kRing = 24576;                  // bytes of one warp's ring
+constexpr int kPass = 64;                     // dims that warps exchange at a time
+constexpr int kPitch = kPass + 8;             // floats; conflict-free for the fragments' order
+constexpr float kLift = 10.0f;                // weights are 2^10 times the softmax's numerators
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttendArgs {
     Seqs seqs;
-    const uint8_t* k;
-    const uint8_t* v;
+    Cut cut;
     const float* k_scale;
     const float* v_scale;
-    int heads, group;                 // key/value heads; query heads of each
     const uint16_t* q;
     int64_t q_stride;
-    float softmax_scale;
+    float scale_log2;                         // softmax_scale * log2(e)
     uint16_t* out;
     float* lse;
+    float* part;                              // [blocks][2][tile_rows][D + 2]
+    struct PartDesc* desc;                    // [blocks][2]
+};
+
+// What a block left unfinished: slot 1 a tile that it began, slot 0 one that
+// it went on with.
+struct PartDesc {
+    int valid, last;                          // last: the tile ends here
+    int begin, first_row, rows, head;         // rows of the tile
+    int pad[2];
 };
 
 template <int D>
-__global__ void __launch_bounds__(128) kv_attend_rows_kernel(const AttendArgs a) {
-    constexpr int kDims = D / 32;
-    __shared__ float qs[4][D];
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int q_heads = a.heads * a.group;
-    const int64_t row = (int64_t)blockIdx.x * 4 + warp;
-    if (row >= (int64_t)a.seqs.T * q_heads) return;
-    const int t = (int)(row / q_heads), hq = (int)(row % q_heads), h = hq / a.group;
-    const int b = seq_of(a.seqs, t, lane);
-    const Span sp = span_of(a.seqs, b);
-    const bool in = t >= sp.begin && t < sp.end;
-    if ((sp.bad || !in) && lane == 0) atomicOr(&g_attend_status, kIndexError);
-    const int keys = in ? sp.before + (t - sp.begin) + 1 : 0;
+struct Shape {
+    static constexpr int kStage = kSub * D * 2;               // K and V of one load
+    static constexpr int kStages = kRing / kStage;
+};
 
-    for (int i = lane; i < D; i += 32) {
-        const uint32_t w = a.q[t * a.q_stride + hq * D + i];
-        qs[warp][i] = bf16lo(w);
+struct __align__(16) Meta {                   // of one load
+    float scale[4];                           // k of keys 0-15, k of 16-31, v, v; read only where there is a page
+    int page[2];                              // -1: no such page
+    int pad[2];
+};
+
+template <int D>
+struct __align__(1024) Smem {
+    uint8_t ring[kWarps][kRing];
+    float pass[kWarps][8][kPitch];
+    float ml[kWarps][8][2];
+    Meta meta[kWarps][Shape<D>::kStages];
+    SeqInfo info[kTable];
+    int64_t prefix[kTable];
+    int64_t warp_sum[kWarps];
+    uint64_t full[kWarps][Shape<D>::kStages];
+    int abort;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint32_t cvt_lo(uint32_t w) { return f16x2_of_e4m3x2((uint16_t)(w & 0xffffu)); }
+__device__ __forceinline__ uint32_t cvt_hi(uint32_t w) { return f16x2_of_e4m3x2((uint16_t)(w >> 16)); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+
+// Bytes of w that are e4m3's NaN, as 0x80 in each.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// Fills the table with sequences base .. base + kTable - 1 and the running sum
+// of their units; returns the units of them all.  Whole block.
+template <int D>
+__device__ int64_t fill_table(const AttendArgs& a, Smem<D>& sm, int base) {
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    int64_t mine = 0;
+    SeqInfo info{0, 0, 0, 0};
+    if (base + tid < a.seqs.B) {
+        const Span sp = span_of(a.seqs, base + tid);
+        if (sp.bad) atomicOr(&g_device_status, kIndexError);
+        info = info_of(sp, a.cut.group);
+        mine = units_of_seq(info, a.cut);
     }
-    __syncwarp();
-    float m = -INFINITY, l = 0.0f, o[kDims] = {};
-    for (int base = 0; base < keys; base += 32) {
-        const int key = base + lane;
-        const int page = key < keys ? page_of(a.seqs, b, key) : -1;
-        if (key < keys && page < 0) atomicOr(&g_attend_status, kIndexError);
-        const int64_t block = (int64_t)page * a.heads + h;
-        const int64_t at = (block * a.seqs.page_tokens + key % a.seqs.page_tokens) * D;
-        float s = -INFINITY, vs = 0.0f;
-        if (page >= 0) {
-            float dot = 0.0f;
-            for (int i = 0; i < D; i += 16) {
-                const uint4 w = *reinterpret_cast<const uint4*>(a.k + at + i);
-                const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+    sm.info[tid] = info;
+    int64_t run = mine;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t f = f16x2_of_e4m3x2((uint16_t)(word[j / 2] >> (16 * (j & 1))));
-                    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&f));
-                    dot = fmaf(qs[warp][i + 2 * j], x.x, dot);
-                    dot = fmaf(qs[warp][i + 2 * j + 1], x.y, dot);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += up;
+    }
+    if (lane == 31) sm.warp_sum[warp] = run;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const int64_t s = sm.warp_sum[w];
+        if (w < warp) before += s;
+        total += s;
+    }
+    sm.prefix[tid] = before + run - mine;
+    __syncthreads();
+    return total;
+}
+
+// The loads of one warp, in order: the 32-key pieces of each segment that are
+// this warp's (piece w, w + 8, ... of the segment).
+struct Loads {
+    Walk w;
+    int piece, pieces;                        // of the current segment
+    int keys;                                 // the segment's last key + 1
+};
+
+__device__ __forceinline__ void segment_keys(const Walk& w, const SeqInfo* info, const Cut& cut, int& key0, int& keys) {
+    const int all = keys_of_tile(info[w.b], cut, w.tile);
+    key0 = w.first * kUnit;
+    keys = (w.first + w.count) * kUnit < all ? (w.first + w.count) * kUnit : all;
+}
+
+__device__ __forceinline__ void loads_settle(Loads& l, const SeqInfo* info, const Cut& cut, int warp) {
+    while (l.w.left > 0) {                    // on to a segment that has a piece for this warp
+        int key0;
+        segment_keys(l.w, info, cut, key0, l.keys);
+        l.pieces = (l.keys - key0 + kSub - 1) / kSub;
+        if (l.piece < l.pieces) return;
+        l.piece = warp;
+        walk_next(l.w, info, cut);
+    }
+}
+
+// The 32 keys of one piece against the tile's rows.
+template <int D, int NB>
+struct Acc {
+    float o[D / 16][NB][4];
+    float m[NB][2], l[NB][2];                 // of rows 2t, 2t + 1 of each block of 8; l: this thread's share
+    float ref;                                // the value scale that o is in units of
+};
+
+template <int D, int NB, bool kFull>
+__device__ __forceinline__ void piece(uint32_t ks, uint32_t vs, const Meta& meta, const uint32_t (&q)[NB][D / 8],
+                                      const float (&f)[NB][2], const int (&lim)[NB][2], int key0, int keys, int lane,
+                                      Acc<D, NB>& acc) {
+    const int g = lane / 4, t = lane % 4;
+    float s[2][NB][4];
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[mb][nb][i] = 0.0f;
+        const int r = mb * 16 + g;
+        if constexpr (D == 128) {             // 128-byte swizzle: 16-byte chunk c of row r lies at c ^ (r & 7)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t at = ks + r * 128 + (((2 * t + j) ^ g) << 4);
+                const uint4 u = lds128(at), v = lds128(at + 8 * 128);
+                const uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t a0 = cvt_lo(a[i]), a1 = cvt_lo(b[i]), a2 = cvt_hi(a[i]), a3 = cvt_hi(b[i]);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+                        mma_f16(s[mb][nb], a0, a1, a2, a3, q[nb][8 * j + 2 * i], q[nb][8 * j + 2 * i + 1]);
                 }
             }
-            s = dot * a.k_scale[block] * a.softmax_scale;
-            vs = a.v_scale[block];
-        }
-        float top = s;
+        } else {                              // 64-byte swizzle: chunk c of row r lies at c ^ ((r >> 1) & 3)
+            const uint32_t at = ks + r * 64 + ((t ^ ((g >> 1) & 3)) << 4);
+            const uint4 u = lds128(at), v = lds128(at + 8 * 64);
+            const uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-        top = fmaxf(top, m);
-        const float zero = top == -INFINITY ? 0.0f : top;
-        const float p = expf(s - zero), keep = expf(m - zero);
-        float sum = p;
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t a0 = cvt_lo(a[i]), a1 = cvt_lo(b[i]), a2 = cvt_hi(a[i]), a3 = cvt_hi(b[i]);
 #pragma unroll
-        for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-        l = l * keep + sum;
-        m = top;
-#pragma unroll
-        for (int d = 0; d < kDims; ++d) o[d] *= keep;
-        for (int j = 0; j < 32 && base + j < keys; ++j) {
-            const int64_t from = __shfl_sync(0xffffffffu, at, j);
-            const float w = __shfl_sync(0xffffffffu, p * vs, j);
-            if (__shfl_sync(0xffffffffu, page, j) < 0) continue;
-            const uint8_t* v = a.v + from + lane * kDims;
-#pragma unroll
-            for (int d = 0; d < kDims; d += 2) {
-                const uint32_t f = f16x2_of_e4m3x2(*reinterpret_cast<const uint16_t*>(v + d));
-                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&f));
-                o[d] = fmaf(w, x.x, o[d]);
-                o[d + 1] = fmaf(w, x.y, o[d + 1]);
+                for (int nb = 0; nb < NB; ++nb) mma_f16(s[mb][nb], a0, a1, a2, a3, q[nb][2 * i], q[nb][2 * i + 1]);
             }
         }
     }
-    const float r = l == 0.0f ? 0.0f : 1.0f / l;
+
+    // logits in powers of two, masks, the running maximum
+    const float k0 = meta.scale[0], k1 = meta.scale[1];
+    const bool has0 = kFull || meta.page[0] >= 0, has1 = kFull || meta.page[1] >= 0;
+    float keep[NB][2];
+    bool same = true;
 #pragma unroll
-    for (int d = 0; d < kDims; d += 2)
-        *reinterpret_cast<uint32_t*>(a.out + row * D + lane * kDims + d) = pack_bf16x2(o[d] * r, o[d + 1] * r);
-    if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : m + logf(l);
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float f0 = f[nb][e] * k0, f1 = f[nb][e] * k1;
+            float x[4] = {s[0][nb][e] * f0, s[0][nb][e + 2] * f0, s[1][nb][e] * f1, s[1][nb][e + 2] * f1};
+            if (!kFull) {
+                const int n = lim[nb][e] - key0;      // keys of this piece that the row sees
+                x[0] = has0 && g < n ? x[0] : -INFINITY;
+                x[1] = has0 && g + 8 < n ? x[1] : -INFINITY;
+                x[2] = has1 && g + 16 < n ? x[2] : -INFINITY;
+                x[3] = has1 && g + 24 < n ? x[3] : -INFINITY;
+            }
+            float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const float old = acc.m[nb][e], now = fmaxf(old, top);
+            const float zero = now == -INFINITY ? 0.0f : now - kLift;
+            keep[nb][e] = old == now ? 1.0f : ex2(old - now);
+            same = same && old == now;
+            acc.m[nb][e] = now;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = ex2(x[i] - zero);
+                sum += x[i];
+            }
+            acc.l[nb][e] = acc.l[nb][e] * keep[nb][e] + sum;
+            s[0][nb][e] = x[0]; s[0][nb][e + 2] = x[1]; s[1][nb][e] = x[2]; s[1][nb][e + 2] = x[3];
+        }
+    }
+
+    // value scales relative to the largest so far
+    const float v0 = has0 ? meta.scale[2] : 0.0f, v1 = has1 ? meta.scale[3] : 0.0f;   // no page: no weight either
+    const float most = fmaxf(v0, v1);
+    float shrink = 1.0f;
+    if (most > acc.ref) {                     // the same for the whole warp
+        shrink = acc.ref / most;
+        acc.ref = most;
+        same = false;
+    }
+    if (!__all_sync(0xffffffffu, same)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const float x = keep[nb][0] * shrink, y = keep[nb][1] * shrink;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                acc.o[j][nb][0] *= x;
+                acc.o[j][nb][1] *= y;
+                acc.o[j][nb][2] *= x;
+                acc.o[j][nb][3] *= y;
+            }
+        }
+    }
+    const float inv = acc.ref > 0.0f ? 1.0f / acc.ref : 0.0f;
+    const float w0 = v0 * inv, w1 = v1 * inv;
+
+    constexpr int kVW = D / 32;               // words of a key's values that a thread holds (4 dims each)
+    uint32_t nan_at[kVW * 4];                 // first key with NaN in each of the thread's dims
+    bool nans = false;
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb) {
+        const float w = mb ? w1 : w0;
+        uint32_t b[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            b[nb][0] = transpose8x8(pack_f16x2(s[mb][nb][0] * w, s[mb][nb][1] * w));
+            b[nb][1] = transpose8x8(pack_f16x2(s[mb][nb][2] * w, s[mb][nb][3] * w));
+        }
+        uint32_t v[4][kVW];                   // keys 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = mb * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
+            if constexpr (D == 128) {
+                const uint4 u = lds128(vs + r * 128 + ((g ^ (r & 7)) << 4));
+                v[i][0] = u.x; v[i][1] = u.y; v[i][2] = u.z; v[i][3] = u.w;
+            } else {
+                const uint2 u = lds64(vs + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
+                v[i][0] = u.x; v[i][1] = u.y;
+            }
+        }
+        if (!kFull) {
+            // Keys that no row of the tile sees count as zeros, whatever their
+            // bytes are.  NaN among the others must reach only the rows that
+            // see its key, but 0 * NaN is NaN: it is taken out here and put
+            // back into those rows below.
+            uint32_t found = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = mb * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
+                const uint32_t use = (mb ? has1 : has0) && key0 + r < keys ? 0xffffffffu : 0u;
+#pragma unroll
+                for (int x = 0; x < kVW; ++x) {
+                    v[i][x] &= use;
+                    found |= nan_bytes(v[i][x]);
+                }
+            }
+            if (__any_sync(0xffffffffu, found != 0)) {
+                if (!nans) {
+#pragma unroll
+                    for (int x = 0; x < kVW * 4; ++x) nan_at[x] = 0x7fffffffu;
+                    nans = true;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = mb * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
+#pragma unroll
+                    for (int x = 0; x < kVW; ++x) {
+                        const uint32_t n = nan_bytes(v[i][x]);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            if ((n >> (8 * y)) & 0x80u) {
+                                nan_at[4 * x + y] = min(nan_at[4 * x + y], (uint32_t)(key0 + r));
+                                v[i][x] &= ~(0xffu << (8 * y));
+                            }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kVW; ++x) {
+            const uint32_t lo = __byte_perm(v[0][x], v[1][x], 0x5140), hi = __byte_perm(v[0][x], v[1][x], 0x7362);
+            const uint32_t lo8 = __byte_perm(v[2][x], v[3][x], 0x5140), hi8 = __byte_perm(v[2][x], v[3][x], 0x7362);
+            const uint32_t a[2][4] = {{cvt_lo(lo), cvt_hi(lo), cvt_lo(lo8), cvt_hi(lo8)},
+                                      {cvt_lo(hi), cvt_hi(hi), cvt_lo(hi8), cvt_hi(hi8)}};
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                    mma_f16(acc.o[2 * x + y][nb], a[y][0], a[y][1], a[y][2], a[y][3], b[nb][0], b[nb][1]);
+        }
+    }
+    if (!kFull && nans) {
+#pragma unroll
+        for (int x = 0; x < kVW * 4; ++x) {
+            uint32_t n = nan_at[x];
+            n = min(n, __shfl_xor_sync(0xffffffffu, n, 1));
+            n = min(n, __shfl_xor_sync(0xffffffffu, n, 2));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if ((int)n < lim[nb][e]) acc.o[x / 2][nb][2 * (x & 1) + e] = __int_as_float(0x7fc00000);
+        }
+    }
+}
+
+// Dim of position p of the order in which the fragments hold a head's dims:
+// block j = p / 16 of O^T, its row group g = p / 2 % 8, first or second.
+template <int D>
+__device__ __forceinline__ int dim_of(int p) {
+    return (D / 8) * ((p / 2) % 8) + 2 * (p / 16) + (p & 1);
+}
+
+// One tile's row r goes out: o[0..3] are positions p .. p + 3 (unnormalised),
+// m and l the row's maximum and sum.
+template <int D>
+__device__ __forceinline__ void write_row(const AttendArgs& a, int begin, int row, int head, int p, const float4& o,
+                                          float m, float l) {
+    const int token = begin + row / a.cut.group;
+    const int64_t at = (int64_t)token * (a.cut.heads * a.cut.group) + head * a.cut.group + row % a.cut.group;
+    const float r = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t* out = a.out + at * D;
+    *reinterpret_cast<uint32_t*>(out + dim_of<D>(p)) = pack_bf16x2(o.x * r, o.y * r);
+    *reinterpret_cast<uint32_t*>(out + dim_of<D>(p + 2)) = pack_bf16x2(o.z * r, o.w * r);
+    if (p == 0 && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : kLn2 * (m - kLift + __log2f(l));
+}
+
+template <int D, int NB>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                     const AttendArgs a) {
+    constexpr int kStages = Shape<D>::kStages, kStage = Shape<D>::kStage;
+    constexpr int kRows = 8 * NB;
+    extern __shared__ uint8_t raw[];
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, t = lane % 4;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel waits for this one's end
+    if (tid == 0) sm.abort = 0;
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(&sm.full[warp][i], 1 + 4);   // lane 0 and the four scales
+        fence_mbar_init_cluster();
+    }
+    if (tid < 2) a.desc[blockIdx.x * 2 + tid].valid = 0;
+    if (blockIdx.x == 0 && tid == 0 && a.seqs.cu && (a.seqs.cu[0] != 0 || a.seqs.cu[a.seqs.B] != a.seqs.T))
+        atomicOr(&g_device_status, kIndexError);
+
+    // this block's part of the line
+    int64_t total = 0;
+    const bool one_table = a.seqs.B <= kTable;
+    if (!one_table)
+        for (int base = 0; base < a.seqs.B; base += kTable) total += fill_table<D>(a, sm, base);
+    int64_t seen = 0;
+    uint32_t issued = 0, waited = 0;          // loads of this warp, over all tables
+    for (int base = 0; base < a.seqs.B; base += kTable) {
+        const int64_t here = fill_table<D>(a, sm, base);
+        if (one_table) total = here;
+        int64_t from, to;
+        share_of(total, blockIdx.x, gridDim.x, from, to);
+        const int64_t lo = (from > seen ? from : seen) - seen, hi = (to < seen + here ? to : seen + here) - seen;
+        seen += here;
+        if (hi <= lo) continue;               // the same for the whole block
+
+        Loads ld;
+        walk_start(ld.w, sm.info, sm.prefix, kTable, a.cut, lo, hi - lo);
+        Walk seg = ld.w;
+        ld.piece = warp;
+        loads_settle(ld, sm.info, a.cut, warp);
+        int page[2] = {-1, -1};
+        auto find_pages = [&] {               // of the next load; used only when it is issued
+            if (ld.w.left <= 0) return;
+            const int key = ld.w.first * kUnit + ld.piece * kSub;
+            const int32_t* row = a.seqs.table + (int64_t)(base + ld.w.b) * a.seqs.width;
+            page[0] = __ldg(row + key / a.seqs.page_tokens);
+            page[1] = key + 16 < ld.keys ? __ldg(row + (key + 16) / a.seqs.page_tokens) : -1;
+        };
+        auto issue = [&] {
+            if (ld.w.left <= 0 || *(volatile int*)&sm.abort) return;
+            const int st = issued % kStages;
+            const int key = ld.w.first * kUnit + ld.piece * kSub, P = a.seqs.page_tokens;
+            const bool ok0 = page[0] >= 0 && page[0] < a.seqs.num_pages;
+            const bool ok1 = page[1] >= 0 && page[1] < a.seqs.num_pages;
+            const bool two = key + 16 < ld.keys;
+            if ((!ok0 || (two && !ok1)) && lane == 0) atomicOr(&g_device_status, kIndexError);
+            uint64_t* bar = &sm.full[warp][st];
+            Meta& meta = sm.meta[warp][st];
+            if (lane < 4) {
+                const int mb = lane & 1;
+                if (mb ? ok1 : ok0) {
+                    const float* src = (lane < 2 ? a.k_scale : a.v_scale) + (int64_t)page[mb] * a.cut.heads + ld.w.head;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&meta.scale[lane])), "l"(src)
+                                 : "memory");
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+            }
+            if (lane == 0) {
+                uint8_t* dst = sm.ring[warp] + st * kStage;
+                meta.page[0] = ok0 ? page[0] : -1;
+                meta.page[1] = ok1 ? page[1] : -1;
+                if (P >= kSub) {              // both halves lie in one page
+                    mbar_arrive_expect_tx(bar, ok0 ? kStage : 0);
+                    if (ok0) {
+                        const int block = page[0] * a.cut.heads + ld.w.head;
+                        tma_load_3d(dst, &k_map, 0, key % P, block, bar);
+                        tma_load_3d(dst + kStage / 2, &v_map, 0, key % P, block, bar);
+                    }
+                } else {
+                    mbar_arrive_expect_tx(bar, (ok0 ? kStage / 2 : 0) + (ok1 ? kStage / 2 : 0));
+                    if (ok0) {
+                        const int block = page[0] * a.cut.heads + ld.w.head;
+                        tma_load_3d(dst, &k_map, 0, 0, block, bar);
+                        tma_load_3d(dst + kStage / 2, &v_map, 0, 0, block, bar);
+                    }
+                    if (ok1) {
+                        const int block = page[1] * a.cut.heads + ld.w.head;
+                        tma_load_3d(dst + kStage / 4, &k_map, 0, 0, block, bar);
+                        tma_load_3d(dst + kStage / 2 + kStage / 4, &v_map, 0, 0, block, bar);
+                    }
+                }
+            }
+            ++issued;
+            ld.piece += kWarps;
+            loads_settle(ld, sm.info, a.cut, warp);
+            find_pages();
+        };
+        find_pages();
+#pragma unroll 1
+        for (int i = 0; i < kStages; ++i) issue();
+
+        for (; seg.left > 0; walk_next(seg, sm.info, a.cut)) {
+            const SeqInfo info = sm.info[seg.b];
+            int key0, keys;
+            segment_keys(seg, sm.info, a.cut, key0, keys);
+            const int first_row = seg.tile * kRows;
+            const int rows = info.rows - first_row < kRows ? info.rows - first_row : kRows;
+
+            // queries: thread (g, t) holds row g's dims [t D/4, (t + 1) D/4) of each block of 8 rows
+            uint32_t q[NB][D / 8];
+            float f[NB][2];
+            int lim[NB][2];
+            Acc<D, NB> acc;
+            acc.ref = 0.0f;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const int row = nb * 8 + g;
+                uint4 u[D / 32];
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) u[i] = make_uint4(0, 0, 0, 0);
+                if (row < rows) {
+                    const int r = first_row + row, token = info.begin + r / a.cut.group;
+                    const int head = seg.head * a.cut.group + r % a.cut.group;
+                    const uint4* src =
+                        reinterpret_cast<const uint4*>(a.q + token * a.q_stride + head * D + t * (D / 4));
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) u[i] = __ldg(src + i);
+                }
+                float x[D / 4], top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    float y[8];
+                    unpack8(u[i], y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        x[8 * i + j] = y[j];
+                        top = fmaxf(top, fabsf(y[j]));
+                    }
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                int e = 134 - (int)(__float_as_uint(top) >> 23);      // 7 - floor(log2(top))
+                e = e < -120 ? -120 : (e > 120 ? 120 : e);
+                const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+                const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) q[nb][i] = pack_f16x2(x[2 * i] * up, x[2 * i + 1] * up);
+                const float back = down * a.scale_log2;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int c = nb * 8 + 2 * t + i;
+                    f[nb][i] = __shfl_sync(0xffffffffu, back, (2 * t + i) * 4);
+                    lim[nb][i] = c < rows ? keys_of_row(info, a.cut, first_row + c) : 0;
+                    acc.m[nb][i] = -INFINITY;
+                    acc.l[nb][i] = 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc.o[j][nb][i] = 0.0f;
+            }
+            const int all_see = keys_of_row(info, a.cut, first_row);  // keys that every row sees
+
+            for (int key = key0 + warp * kSub; key < keys; key += kWarps * kSub) {
+                const int st = waited % kStages;
+                if (waited == issued) break;  // after a wait that gave up
+                const bool ok = mbar_wait(&sm.full[warp][st], (waited / kStages) & 1, &sm.abort);
+                ++waited;
+                if (!ok) break;
+                const uint32_t base_addr = smem_u32(sm.ring[warp] + st * kStage);
+                const Meta& meta = sm.meta[warp][st];
+                const bool full = key + kSub <= all_see && meta.page[0] >= 0 && meta.page[1] >= 0;
+                if (full)
+                    piece<D, NB, true>(base_addr, base_addr + kStage / 2, meta, q, f, lim, key, keys, lane, acc);
+                else
+                    piece<D, NB, false>(base_addr, base_addr + kStage / 2, meta, q, f, lim, key, keys, lane, acc);
+                __syncwarp();                 // every lane has read the stage
+                issue();
+            }
+
+            // the warps' sums of this segment, joined
+            const bool whole = seg.first == 0 && seg.count == seg.units;
+            const int slot = seg.first == 0 ? 1 : 0;
+            float* part = a.part + ((int64_t)blockIdx.x * 2 + slot) * kRows * (D + 2);
+            if (!whole && tid == 0) {
+                PartDesc d;
+                d.valid = 1;
+                d.last = seg.first + seg.count == seg.units;
+                d.begin = info.begin;
+                d.first_row = first_row;
+                d.rows = rows;
+                d.head = seg.head;
+                a.desc[blockIdx.x * 2 + slot] = d;
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float l = acc.l[nb][e];
+                    l += __shfl_xor_sync(0xffffffffu, l, 4);
+                    l += __shfl_xor_sync(0xffffffffu, l, 8);
+                    l += __shfl_xor_sync(0xffffffffu, l, 16);
+                    if (g == 0) {
+                        sm.ml[warp][2 * t + e][0] = acc.m[nb][e];
+                        sm.ml[warp][2 * t + e][1] = l;
+                    }
+                }
+#pragma unroll
+                for (int pass = 0; pass < D / kPass; ++pass) {
+#pragma unroll
+                    for (int j = 0; j < kPass / 16; ++j) {
+                        const float(&o)[4] = acc.o[pass * (kPass / 16) + j][nb];
+                        float* at = &sm.pass[warp][2 * t][j * 16 + 2 * g];
+                        *reinterpret_cast<float2*>(at) = make_float2(o[0] * acc.ref, o[2] * acc.ref);
+                        *reinterpret_cast<float2*>(at + kPitch) = make_float2(o[1] * acc.ref, o[3] * acc.ref);
+                    }
+                    __syncthreads();
+                    const int row = tid / 16, p = (tid % 16) * 4;     // 8 rows x 16 threads: half of the block
+                    if (tid < 128) {
+                        float m = -INFINITY;
+#pragma unroll
+                        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.ml[w][row][0]);
+                        const float zero = m == -INFINITY ? 0.0f : m;
+                        float l = 0.0f;
+                        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                        for (int w = 0; w < kWarps; ++w) {
+                            const float x = ex2(sm.ml[w][row][0] - zero);
+                            const float4 y = *reinterpret_cast<const float4*>(&sm.pass[w][row][p]);
+                            l = fmaf(x, sm.ml[w][row][1], l);
+                            o.x = fmaf(x, y.x, o.x);
+                            o.y = fmaf(x, y.y, o.y);
+                            o.z = fmaf(x, y.z, o.z);
+                            o.w = fmaf(x, y.w, o.w);
+                        }
+                        const int r = nb * 8 + row, at = pass * kPass + p;
+                        if (r < rows) {
+                            if (whole) {
+                                write_row<D>(a, info.begin, first_row + r, seg.head, at, o, m, l);
+                            } else {
+                                float* dst = part + r * (D + 2);
+                                *reinterpret_cast<float2*>(dst + 2 + at) = make_float2(o.x, o.y);
+                                *reinterpret_cast<float2*>(dst + 2 + at + 2) = make_float2(o.z, o.w);
+                                if (at == 0) *reinterpret_cast<float2*>(dst) = make_float2(m, l);
+                            }
+                        }
+                    }
+                    __syncthreads();
+                }
+            }
+        }
+        __syncthreads();                      // before the table is filled anew
+    }
+    // after a wait that gave up: the loads still under way
+    for (; waited != issued; ++waited) mbar_wait_drain(&sm.full[warp][waited % kStages], (waited / kStages) & 1);
+}
+
+// Joins the parts of the tile that block blockIdx.x of the attention began
+// and did not finish: slot 1 of that block, then slot 0 of the following ones.
+template <int D>
+__global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a, int blocks) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c = blockIdx.x, R = a.cut.tile_rows;
+    const PartDesc d = a.desc[c * 2 + 1];
+    if (!d.valid) return;
+    int n = 1;                                // parts
+    while (c + n < blocks && a.desc[(c + n) * 2].valid) {
+        ++n;
+        if (a.desc[(c + n - 1) * 2].last) break;
+    }
+    const int64_t one = (int64_t)R * (D + 2);
+    const float* first = a.part + ((int64_t)c * 2 + 1) * one;
+    const float* rest = a.part + ((int64_t)c + 1) * 2 * one;
+    for (int i = threadIdx.x; i < d.rows * (D / 4); i += blockDim.x) {
+        const int r = i / (D / 4), p = i % (D / 4) * 4;
+        const int64_t at = (int64_t)r * (D + 2);
+        float m = first[at];
+        for (int k = 0; k + 1 < n; ++k) m = fmaxf(m, rest[k * 2 * one + at]);
+        const float zero = m == -INFINITY ? 0.0f : m;
+        float l = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k = 0; k < n; ++k) {
+            const float* src = (k ? rest + (k - 1) * 2 * one : first) + at;
+            const float2 ml = *reinterpret_cast<const float2*>(src);
+            const float2 y = *reinterpret_cast<const float2*>(src + 2 + p), z = *reinterpret_cast<const float2*>(src + 4 + p);
+            const float x = ex2(ml.x - zero);
+            l = fmaf(x, ml.y, l);
+            o.x = fmaf(x, y.x, o.x);
+            o.y = fmaf(x, y.y, o.y);
+            o.z = fmaf(x, z.x, o.z);
+            o.w = fmaf(x, z.y, o.w);
+        }
+        write_row<D>(a, d.begin, d.first_row + r, d.head, p, o, m, l);
+    }
+}
+
+using PFN_encodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+PFN_encodeTiled encode_fn() {
+    static const PFN_encodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+        return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_encodeTiled>(p) : nullptr;
+    }();
+    return fn;
+}
+
+// Codes as [num_pages * heads][page_tokens][D] bytes, in boxes of up to 32 tokens.
+bool encode_codes(CUtensorMap* map, const uint8_t* codes, int64_t blocks, int page_tokens, int D) {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)page_tokens, (cuuint64_t)blocks};
+    const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * page_tokens};
+    const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)(page_tokens < kSub ? page_tokens : kSub), 1};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return encode_fn() &&
+           encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), dims, strides, box, step,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of a tile: 16 when a sequence has more than 8 on average, else 8.
+int tile_rows(int group, int64_t B, int64_t T) { return T * group > 8 * B ? 16 : 8; }
+
+size_t part_bytes(int rows, int D, int blocks) { return ((size_t)blocks * 2 * rows * (D + 2) * 4 + 255) / 256 * 256; }
+
+template <int D, int NB>
+cudaError_t launch(const CUtensorMap& k_map, const CUtensorMap& v_map, const AttendArgs& a, int blocks,
+                   cudaStream_t stream) {
+    const int bytes = (int)sizeof(Smem<D>) + 1024;
+    // an attribute of the function on the current device: set on every call, which keeps no state here
+    cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kv_attend_kernel<D, NB><<<blocks, kThreads, bytes, stream>>>(k_map, v_map, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(blocks - 1, 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = stream;
+    return blocks > 1 ? cudaLaunchKernelEx(&cfg, kv_join_kernel<D>, a, blocks) : cudaSuccess;
+}
+
+}  // namespace
+
+size_t kv_attend_workspace(int heads, int head_dim, int q_heads, int64_t B, int64_t T, int num_sms) {
+    return part_bytes(tile_rows(q_heads / heads, B, T), head_dim, num_sms) + (size_t)num_sms * 2 * sizeof(PartDesc);
 }
 
 cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* v, const float* k_scale,
                              const float* v_scale, int heads, int head_dim, const uint16_t* q, int64_t q_stride,
                              int q_heads, float softmax_scale, uint16_t* out, float* lse, void* workspace,
                              int num_sms, cudaStream_t stream) {
-    const AttendArgs a{seqs, k, v, k_scale, v_scale, heads, q_heads / heads, q, q_stride, softmax_scale, out, lse};
-    const int64_t blocks = ((int64_t)seqs.T * q_heads + 3) / 4;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    if (head_dim == 64) kv_attend_rows_kernel<64><<<(unsigned)blocks, 128, 0, stream>>>(a);
-    else kv_attend_rows_kernel<128><<<(unsigned)blocks, 128, 0, stream>>>(a);
-    return cudaGetLastError();
+    CUtensorMap k_map, v_map;
+    const int64_t pages = (int64_t)seqs.num_pages * heads;
+    if (!encode_codes(&k_map, k, pages, seqs.page_tokens, head_dim) ||
+        !encode_codes(&v_map, v, pages, seqs.page_tokens, head_dim))
+        return cudaErrorInvalidValue;
+    AttendArgs a;
+    a.seqs = seqs;
+    a.cut = Cut{heads, q_heads / heads, tile_rows(q_heads / heads, seqs.B, seqs.T)};
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.scale_log2 = softmax_scale * kLog2e;
+    a.out = out;
+    a.lse = lse;
+    a.part = static_cast<float*>(workspace);
+    a.desc = reinterpret_cast<PartDesc*>(static_cast<uint8_t*>(workspace) +
+                                         part_bytes(a.cut.tile_rows, head_dim, num_sms));
+    if (a.cut.tile_rows == 8)
+        return head_dim == 64 ? launch<64, 1>(k_map, v_map, a, num_sms, stream)
+                              : launch<128, 1>(k_map, v_map, a, num_sms, stream);
+    return head_dim == 64 ? launch<64, 2>(k_map, v_map, a, num_sms, stream)
+                          : launch<128, 2>(k_map, v_map, a, num_sms, stream);
 }
-
-size_t kv_attend_workspace(int heads, int head_dim, int q_heads, int64_t B, int64_t T, int num_sms) { return 0; }
 
 cudaError_t read_attend_status(unsigned int* status) {
     unsigned int v = 0, zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_attend_status, sizeof v);
-    if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_attend_status, &zero, sizeof zero);
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_device_status, sizeof v);
+    if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof zero);
     *status = v;
     return e;
 }

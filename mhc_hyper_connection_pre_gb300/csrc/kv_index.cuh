@@ -93,5 +93,129 @@ MHC_HD bool starts_run(const Span& sp, const Run& r, int t) {
     return r.n > 0 && (t == sp.begin || r.slot == 0);
 }
 
+// ---------------------------------------------------------------------------
+// How mhc_kv_attend's work is cut.  The rows of one sequence and key/value head
+// are its new tokens times the `group` query heads that share the head, row r
+// being token r / group, query head r % group of it; a tile is `tile_rows` of
+// them.  A tile's keys are cut in units of kUnit; a tile without keys still is
+// one unit (its rows have to be written).  All units of all tiles, ordered by
+// sequence, tile, head and key, form one line that the blocks share evenly
+// whatever the lengths are (share_of), and a tile cut by a border is joined
+// afterwards.
+
+constexpr int kUnit = 64;
+
+// One sequence as the walk needs it.
+struct SeqInfo {
+    int begin;              // first new token
+    int rows;               // new tokens * group
+    int len, before;
+};
+
+struct Cut {
+    int heads, group, tile_rows;
+};
+
+MHC_HD SeqInfo info_of(const Span& sp, int group) {
+    SeqInfo r;
+    r.begin = sp.begin;
+    r.rows = (sp.end - sp.begin) * group;
+    r.len = sp.len;
+    r.before = sp.before;
+    return r;
+}
+
+MHC_HD int tiles_of(const SeqInfo& s, const Cut& c) { return (s.rows + c.tile_rows - 1) / c.tile_rows; }
+
+// How many keys row r sees.
+MHC_HD int keys_of_row(const SeqInfo& s, const Cut& c, int r) {
+    const int n = s.before + r / c.group + 1;
+    return n < 0 ? 0 : n;
+}
+
+// How many keys the last row of tile i sees: the most of any of its rows.
+MHC_HD int keys_of_tile(const SeqInfo& s, const Cut& c, int i) {
+    const int end = (i + 1) * c.tile_rows < s.rows ? (i + 1) * c.tile_rows : s.rows;
+    return keys_of_row(s, c, end - 1);
+}
+
+MHC_HD int units_of_tile(const SeqInfo& s, const Cut& c, int i) {
+    const int n = (keys_of_tile(s, c, i) + kUnit - 1) / kUnit;
+    return n < 1 ? 1 : n;
+}
+
+// Units of all tiles and heads of a sequence.
+MHC_HD int64_t units_of_seq(const SeqInfo& s, const Cut& c) {
+    int64_t n = 0;
+    const int tiles = tiles_of(s, c);
+    for (int i = 0; i < tiles; ++i) n += units_of_tile(s, c, i);
+    return n * c.heads;
+}
+
+// The units [from, to) of the line that block c takes.  With fewer units than
+// blocks the first `total` blocks take one each, so that the blocks that share
+// a tile always follow one another.
+MHC_HD void share_of(int64_t total, int c, int blocks, int64_t& from, int64_t& to) {
+    const int64_t n = total < blocks ? total : blocks;
+    from = c < n ? total * c / n : total;
+    to = c < n ? total * (c + 1) / n : total;
+}
+
+// A walk over the segments (one tile's units that one block takes) of a range
+// of the line, inside a table of sequences.
+struct Walk {
+    int b, tile, head;      // the current segment: index in the table, tile and head
+    int first, count;       // its units
+    int units;              // of its whole tile
+    int64_t left;           // units of the range from this segment on; 0: the walk is over
+};
+
+MHC_HD void walk_cut(Walk& w) {
+    const int rest = w.units - w.first;
+    w.count = w.left < rest ? (int)w.left : rest;
+}
+
+// Starts at unit `from` of the table's line (prefix[b]: units before sequence
+// b), for `count` units that all lie in the table.
+MHC_HD void walk_start(Walk& w, const SeqInfo* seqs, const int64_t* prefix, int n, const Cut& c, int64_t from,
+                       int64_t count) {
+    w.left = count;
+    if (count <= 0) return;
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (prefix[mid] <= from) lo = mid;
+        else hi = mid;
+    }
+    int64_t r = from - prefix[lo];
+    w.b = lo;
+    w.tile = 0;
+    w.units = units_of_tile(seqs[lo], c, 0);
+    while (r >= (int64_t)w.units * c.heads) {
+        r -= (int64_t)w.units * c.heads;
+        ++w.tile;
+        w.units = units_of_tile(seqs[lo], c, w.tile);
+    }
+    w.head = (int)(r / w.units);
+    w.first = (int)(r % w.units);
+    walk_cut(w);
+}
+
+MHC_HD void walk_next(Walk& w, const SeqInfo* seqs, const Cut& c) {
+    w.left -= w.count;
+    if (w.left <= 0) return;
+    w.first = 0;
+    if (++w.head == c.heads) {
+        w.head = 0;
+        if (++w.tile == tiles_of(seqs[w.b], c)) {
+            w.tile = 0;
+            do ++w.b;
+            while (seqs[w.b].rows == 0);
+        }
+        w.units = units_of_tile(seqs[w.b], c, w.tile);
+    }
+    walk_cut(w);
+}
+
 }  // namespace kv
 }  // namespace mhc
