@@ -23,11 +23,7 @@
 // many units of 64 keys whatever the lengths are (kv_index.cuh); what a border
 // cuts is left as partial sums in the workspace and joined by a second, small
 // kernel.
-#include <cuda.h>
-#include <cuda_runtime.h>
-
-#include "kv_common.cuh"
-#include "sm100.cuh"
+#include "kv_attend.cuh"
 
 namespace mhc {
 namespace kv {
@@ -37,34 +33,10 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kSub = 32;                      // keys of one load of one warp
-constexpr int kTable = 256;                   // sequences of the walk's table
 constexpr int kRing = 24576;                  // bytes of one warp's ring
 constexpr int kPass = 64;                     // dims that warps exchange at a time
 constexpr int kPitch = kPass + 8;             // floats; conflict-free for the fragments' order
-constexpr float kLift = 10.0f;                // weights are 2^10 times the softmax's numerators
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-struct AttendArgs {
-    Seqs seqs;
-    Cut cut;
-    const float* k_scale;
-    const float* v_scale;
-    const uint16_t* q;
-    int64_t q_stride;
-    float scale_log2;                         // softmax_scale * log2(e)
-    uint16_t* out;
-    float* lse;
-    float* part;                              // [blocks][2][tile_rows][D + 2]
-    struct PartDesc* desc;                    // [blocks][2]
-};
-
-// What a block left unfinished: slot 1 a tile that it began, slot 0 one that
-// it went on with.
-struct PartDesc {
-    int valid, last;                          // last: the tile ends here
-    int begin, first_row, rows, head;         // rows of the tile
-    int pad[2];
-};
+constexpr int kUnit = 64;                     // keys of a unit of work
 
 template <int D>
 struct Shape {
@@ -84,18 +56,10 @@ struct __align__(1024) Smem {
     float pass[kWarps][8][kPitch];
     float ml[kWarps][8][2];
     Meta meta[kWarps][Shape<D>::kStages];
-    SeqInfo info[kTable];
-    int64_t prefix[kTable];
-    int64_t warp_sum[kWarps];
+    Table tab;
     uint64_t full[kWarps][Shape<D>::kStages];
     int abort;
 };
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -111,62 +75,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ uint32_t cvt_lo(uint32_t w) { return f16x2_of_e4m3x2((uint16_t)(w & 0xffffu)); }
-__device__ __forceinline__ uint32_t cvt_hi(uint32_t w) { return f16x2_of_e4m3x2((uint16_t)(w >> 16)); }
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-    return v;
-}
-
-// Bytes of w that are e4m3's NaN, as 0x80 in each.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-
-// Fills the table with sequences base .. base + kTable - 1 and the running sum
-// of their units; returns the units of them all.  Whole block.
-template <int D>
-__device__ int64_t fill_table(const AttendArgs& a, Smem<D>& sm, int base) {
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    int64_t mine = 0;
-    SeqInfo info{0, 0, 0, 0};
-    if (base + tid < a.seqs.B) {
-        const Span sp = span_of(a.seqs, base + tid);
-        if (sp.bad) atomicOr(&g_device_status, kIndexError);
-        info = info_of(sp, a.cut.group);
-        mine = units_of_seq(info, a.cut);
-    }
-    sm.info[tid] = info;
-    int64_t run = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += up;
-    }
-    if (lane == 31) sm.warp_sum[warp] = run;
-    __syncthreads();
-    int64_t before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const int64_t s = sm.warp_sum[w];
-        if (w < warp) before += s;
-        total += s;
-    }
-    sm.prefix[tid] = before + run - mine;
-    __syncthreads();
-    return total;
-}
-
 // The loads of one warp, in order: the 32-key pieces of each segment that are
 // this warp's (piece w, w + 8, ... of the segment).
 struct Loads {
@@ -174,12 +82,6 @@ struct Loads {
     int piece, pieces;                        // of the current segment
     int keys;                                 // the segment's last key + 1
 };
-
-__device__ __forceinline__ void segment_keys(const Walk& w, const SeqInfo* info, const Cut& cut, int& key0, int& keys) {
-    const int all = keys_of_tile(info[w.b], cut, w.tile);
-    key0 = w.first * kUnit;
-    keys = (w.first + w.count) * kUnit < all ? (w.first + w.count) * kUnit : all;
-}
 
 __device__ __forceinline__ void loads_settle(Loads& l, const SeqInfo* info, const Cut& cut, int warp) {
     while (l.w.left > 0) {                    // on to a segment that has a piece for this warp
@@ -405,13 +307,12 @@ __device__ __forceinline__ int dim_of(int p) {
 template <int D>
 __device__ __forceinline__ void write_row(const AttendArgs& a, int begin, int row, int head, int p, const float4& o,
                                           float m, float l) {
-    const int token = begin + row / a.cut.group;
-    const int64_t at = (int64_t)token * (a.cut.heads * a.cut.group) + head * a.cut.group + row % a.cut.group;
+    const int64_t at = place_of(a, begin, row, head);
     const float r = l == 0.0f ? 0.0f : 1.0f / l;
     uint16_t* out = a.out + at * D;
     *reinterpret_cast<uint32_t*>(out + dim_of<D>(p)) = pack_bf16x2(o.x * r, o.y * r);
     *reinterpret_cast<uint32_t*>(out + dim_of<D>(p + 2)) = pack_bf16x2(o.z * r, o.w * r);
-    if (p == 0 && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : kLn2 * (m - kLift + __log2f(l));
+    if (p == 0 && a.lse) a.lse[at] = lse_of(m, l);
 }
 
 template <int D, int NB>
@@ -430,18 +331,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init_cluster();
     }
     if (tid < 2) a.desc[blockIdx.x * 2 + tid].valid = 0;
-    if (blockIdx.x == 0 && tid == 0 && a.seqs.cu && (a.seqs.cu[0] != 0 || a.seqs.cu[a.seqs.B] != a.seqs.T))
-        atomicOr(&g_device_status, kIndexError);
+    check_offsets(a);
 
     // this block's part of the line
     int64_t total = 0;
     const bool one_table = a.seqs.B <= kTable;
     if (!one_table)
-        for (int base = 0; base < a.seqs.B; base += kTable) total += fill_table<D>(a, sm, base);
+        for (int base = 0; base < a.seqs.B; base += kTable) total += fill_table(a, sm.tab, base);
     int64_t seen = 0;
     uint32_t issued = 0, waited = 0;          // loads of this warp, over all tables
     for (int base = 0; base < a.seqs.B; base += kTable) {
-        const int64_t here = fill_table<D>(a, sm, base);
+        const int64_t here = fill_table(a, sm.tab, base);
         if (one_table) total = here;
         int64_t from, to;
         share_of(total, blockIdx.x, gridDim.x, from, to);
@@ -450,10 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (hi <= lo) continue;               // the same for the whole block
 
         Loads ld;
-        walk_start(ld.w, sm.info, sm.prefix, kTable, a.cut, lo, hi - lo);
+        walk_start(ld.w, sm.tab.info, sm.tab.prefix, kTable, a.cut, lo, hi - lo);
         Walk seg = ld.w;
         ld.piece = warp;
-        loads_settle(ld, sm.info, a.cut, warp);
+        loads_settle(ld, sm.tab.info, a.cut, warp);
         int page[2] = {-1, -1};
         auto find_pages = [&] {               // of the next load; used only when it is issued
             if (ld.w.left <= 0) return;
@@ -476,10 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int mb = lane & 1;
                 if (mb ? ok1 : ok0) {
                     const float* src = (lane < 2 ? a.k_scale : a.v_scale) + (int64_t)page[mb] * a.cut.heads + ld.w.head;
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&meta.scale[lane])), "l"(src)
-                                 : "memory");
+                    copy_async4(&meta.scale[lane], src);
                 }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+                arrive_after_copies(bar);
             }
             if (lane == 0) {
                 uint8_t* dst = sm.ring[warp] + st * kStage;
@@ -508,17 +407,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++issued;
             ld.piece += kWarps;
-            loads_settle(ld, sm.info, a.cut, warp);
+            loads_settle(ld, sm.tab.info, a.cut, warp);
             find_pages();
         };
         find_pages();
 #pragma unroll 1
         for (int i = 0; i < kStages; ++i) issue();
 
-        for (; seg.left > 0; walk_next(seg, sm.info, a.cut)) {
-            const SeqInfo info = sm.info[seg.b];
+        for (; seg.left > 0; walk_next(seg, sm.tab.info, a.cut)) {
+            const SeqInfo info = sm.tab.info[seg.b];
             int key0, keys;
-            segment_keys(seg, sm.info, a.cut, key0, keys);
+            segment_keys(seg, sm.tab.info, a.cut, key0, keys);
             const int first_row = seg.tile * kRows;
             const int rows = info.rows - first_row < kRows ? info.rows - first_row : kRows;
 
@@ -655,8 +554,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 write_row<D>(a, info.begin, first_row + r, seg.head, at, o, m, l);
                             } else {
                                 float* dst = part + r * (D + 2);
-                                *reinterpret_cast<float2*>(dst + 2 + at) = make_float2(o.x, o.y);
-                                *reinterpret_cast<float2*>(dst + 2 + at + 2) = make_float2(o.z, o.w);
+                                *reinterpret_cast<float2*>(dst + 2 + dim_of<D>(at)) = make_float2(o.x, o.y);
+                                *reinterpret_cast<float2*>(dst + 2 + dim_of<D>(at + 2)) = make_float2(o.z, o.w);
                                 if (at == 0) *reinterpret_cast<float2*>(dst) = make_float2(m, l);
                             }
                         }
@@ -706,38 +605,17 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a, int bl
             o.z = fmaf(x, z.x, o.z);
             o.w = fmaf(x, z.y, o.w);
         }
-        write_row<D>(a, d.begin, d.first_row + r, d.head, p, o, m, l);
+        const int64_t to = place_of(a, d.begin, d.first_row + r, d.head);
+        const float y = l == 0.0f ? 0.0f : 1.0f / l;
+        *reinterpret_cast<uint2*>(a.out + to * D + p) =
+            make_uint2(pack_bf16x2(o.x * y, o.y * y), pack_bf16x2(o.z * y, o.w * y));
+        if (p == 0 && a.lse) a.lse[to] = lse_of(m, l);
     }
 }
 
-using PFN_encodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-PFN_encodeTiled encode_fn() {
-    static const PFN_encodeTiled fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
-        return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_encodeTiled>(p) : nullptr;
-    }();
-    return fn;
-}
-
-// Codes as [num_pages * heads][page_tokens][D] bytes, in boxes of up to 32 tokens.
-bool encode_codes(CUtensorMap* map, const uint8_t* codes, int64_t blocks, int page_tokens, int D) {
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)page_tokens, (cuuint64_t)blocks};
-    const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * page_tokens};
-    const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)(page_tokens < kSub ? page_tokens : kSub), 1};
-    const cuuint32_t step[3] = {1, 1, 1};
-    return encode_fn() &&
-           encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), dims, strides, box, step,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Rows of a tile: 16 when a sequence has more than 8 on average, else 8.
-int tile_rows(int group, int64_t B, int64_t T) { return T * group > 8 * B ? 16 : 8; }
+// Rows of a tile.  Up to 16 rows a sequence: one tile of 8 or 16 for the warps
+// of this file; more: the tensor-memory kernel's 256.
+int tile_rows(int group, int64_t B, int64_t T) { return T * group > 16 * B ? 256 : (T * group > 8 * B ? 16 : 8); }
 
 size_t part_bytes(int rows, int D, int blocks) { return ((size_t)blocks * 2 * rows * (D + 2) * 4 + 255) / 256 * 256; }
 
@@ -746,11 +624,14 @@ cudaError_t launch(const CUtensorMap& k_map, const CUtensorMap& v_map, const Att
                    cudaStream_t stream) {
     const int bytes = (int)sizeof(Smem<D>) + 1024;
     // an attribute of the function on the current device: set on every call, which keeps no state here
-    cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     kv_attend_kernel<D, NB><<<blocks, kThreads, bytes, stream>>>(k_map, v_map, a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+cudaError_t launch_join(const AttendArgs& a, int head_dim, int blocks, cudaStream_t stream) {
+    if (blocks < 2) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -760,10 +641,13 @@ cudaError_t launch(const CUtensorMap& k_map, const CUtensorMap& v_map, const Att
     cfg.gridDim = dim3(blocks - 1, 1, 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = stream;
-    return blocks > 1 ? cudaLaunchKernelEx(&cfg, kv_join_kernel<D>, a, blocks) : cudaSuccess;
+    return cudaLaunchKernelEx(&cfg, head_dim == 64 ? kv_join_kernel<64> : kv_join_kernel<128>, a, blocks);
 }
 
 }  // namespace
+
+cudaError_t launch_kv_attend_tc(const AttendArgs& a, const uint8_t* k, const uint8_t* v, int head_dim, int blocks,
+                                cudaStream_t stream);
 
 size_t kv_attend_workspace(int heads, int head_dim, int q_heads, int64_t B, int64_t T, int num_sms) {
     return part_bytes(tile_rows(q_heads / heads, B, T), head_dim, num_sms) + (size_t)num_sms * 2 * sizeof(PartDesc);
@@ -773,14 +657,10 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
                              const float* v_scale, int heads, int head_dim, const uint16_t* q, int64_t q_stride,
                              int q_heads, float softmax_scale, uint16_t* out, float* lse, void* workspace,
                              int num_sms, cudaStream_t stream) {
-    CUtensorMap k_map, v_map;
-    const int64_t pages = (int64_t)seqs.num_pages * heads;
-    if (!encode_codes(&k_map, k, pages, seqs.page_tokens, head_dim) ||
-        !encode_codes(&v_map, v, pages, seqs.page_tokens, head_dim))
-        return cudaErrorInvalidValue;
     AttendArgs a;
+    const int rows = tile_rows(q_heads / heads, seqs.B, seqs.T);
     a.seqs = seqs;
-    a.cut = Cut{heads, q_heads / heads, tile_rows(q_heads / heads, seqs.B, seqs.T)};
+    a.cut = Cut{heads, q_heads / heads, rows, rows == 256 ? 2 * kUnit : kUnit};
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     a.q = q;
@@ -789,13 +669,24 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
     a.out = out;
     a.lse = lse;
     a.part = static_cast<float*>(workspace);
-    a.desc = reinterpret_cast<PartDesc*>(static_cast<uint8_t*>(workspace) +
-                                         part_bytes(a.cut.tile_rows, head_dim, num_sms));
-    if (a.cut.tile_rows == 8)
-        return head_dim == 64 ? launch<64, 1>(k_map, v_map, a, num_sms, stream)
-                              : launch<128, 1>(k_map, v_map, a, num_sms, stream);
-    return head_dim == 64 ? launch<64, 2>(k_map, v_map, a, num_sms, stream)
-                          : launch<128, 2>(k_map, v_map, a, num_sms, stream);
+    a.desc = reinterpret_cast<PartDesc*>(static_cast<uint8_t*>(workspace) + part_bytes(rows, head_dim, num_sms));
+    cudaError_t e;
+    if (rows == 256) {
+        e = launch_kv_attend_tc(a, k, v, head_dim, num_sms, stream);
+    } else {
+        CUtensorMap k_map, v_map;
+        const int64_t pages = (int64_t)seqs.num_pages * heads;
+        if (!encode_codes(&k_map, k, pages, seqs.page_tokens, head_dim, kSub) ||
+            !encode_codes(&v_map, v, pages, seqs.page_tokens, head_dim, kSub))
+            return cudaErrorInvalidValue;
+        if (rows == 8)
+            e = head_dim == 64 ? launch<64, 1>(k_map, v_map, a, num_sms, stream)
+                               : launch<128, 1>(k_map, v_map, a, num_sms, stream);
+        else
+            e = head_dim == 64 ? launch<64, 2>(k_map, v_map, a, num_sms, stream)
+                               : launch<128, 2>(k_map, v_map, a, num_sms, stream);
+    }
+    return e == cudaSuccess ? launch_join(a, head_dim, num_sms, stream) : e;
 }
 
 cudaError_t read_attend_status(unsigned int* status) {

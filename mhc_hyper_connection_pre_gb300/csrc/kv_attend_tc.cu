@@ -1,0 +1,732 @@
+// kv_attend_tc.cu -- causal attention over the paged e4m3 cache
+// (mhc_kv_attend) for many rows a sequence: prompts, chunks of prompts, and
+// drafted tokens with many query heads to a key head.
+//
+// Mathematics.  A block takes 256 rows (new tokens x query heads of one
+// key/value head) as two tiles of 128 and walks over the keys 128 at a time:
+// S = Q K^T and O += P V on the tensor cores (tcgen05), the softmax between
+// them with one thread a row.
+//   * K is used as it is stored: S is an e4m3 product.  A query row, divided
+//     by a power of two so that its largest element lies in [128, 256), is the
+//     sum of two e4m3 numbers an element, hi + lo.  bf16's 8 bits split into
+//     4 + 4 without a remainder down to 2^-10 of the row's largest element;
+//     below that the remainder is at most 2^-19 of it.  S = hi K + lo K costs
+//     as much tensor time as one f16 product and needs no conversion of K.
+//   * V becomes f16 on the way (exactly, times its page's scale over the
+//     largest scale of the segment, times 2^7), because the weights need
+//     more than e4m3's 4 bits: they are f16, 2^10 times the softmax's
+//     numerators, so that small weights stay out of f16's subnormals.
+//   * The running maximum follows only when it has grown by more than 2^5
+//     (weights then reach 2^15, within f16), so that O, in tensor memory, is
+//     rescaled rarely; sums are fp32 and of the unrounded weights.
+//
+// What bounds it: 4 * 128 * 128 * head_dim operations for 128 keys and 128
+// rows on the tensor cores against 128 * 128 exponentials and the conversion
+// of V; the two tiles alternate, so that the softmax of one runs while the
+// other's products do.  The conversion is shared by the two tiles.
+//
+// Warps 0-3 and 4-7: softmax of the two tiles; 8-9: V to f16; 10: TMA loads;
+// 11: the tensor instructions.  (Twelve warps leave the softmax 168 registers.)
+#include "kv_attend.cuh"
+
+namespace mhc {
+namespace kv {
+
+namespace {
+
+constexpr int kThreads = 12 * 32;
+constexpr int kTile = 128;                    // rows of one tile, and keys of one step
+constexpr int kPair = 2 * kTile;              // rows of a block's work
+constexpr int kKStages = 3, kVStages = 2;
+constexpr int kMetas = 2 * kKStages;          // the softmax reads a step's key scales after its keys' stage is free
+constexpr float kGrow = 5.0f;                 // the maximum follows when it has grown by more (in powers of two)
+constexpr float kVLift = 128.0f;              // V in f16 is 2^7 times code * scale / largest scale
+constexpr int kSegs = 4;                      // segments whose value scale and NaNs are kept: the converter runs two ahead
+
+struct __align__(16) Meta {                   // of one step: the scales of each 16 keys, which of them have a page
+    float scale[8];
+    uint32_t valid;
+    int pad[3];
+};
+
+template <int D>
+struct __align__(1024) Smem {
+    uint8_t q[2][2][kTile * D];               // tile, hi / lo
+    uint8_t k[kKStages][kTile * D];
+    uint8_t v[kVStages][kTile * D];           // as stored
+    uint8_t v16[2][kTile * D * 2];            // f16: 64 dims of every key, then the next 64
+    Table tab;
+    Meta k_meta[kMetas];
+    Meta v_meta[kVStages];
+    int nan_key[kSegs][D];                    // first key with NaN in each dim, among those that not every row sees
+    int has_nan[kSegs];
+    float ref[kSegs];                         // largest value scale of the segment
+    float red[2];
+    uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+    uint64_t v16_full[2], v16_empty[2], q_full[2], s_full[2], p_full[2], o_full[2], done;
+    uint32_t tmem;
+    int abort;
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// e4m3 x e4m3, both from shared memory; f16 x f16 with A in tensor memory.
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Byte offset of 16-byte chunk c of row r in a swizzled tile of rows of D bytes
+// (D = 128: 128-byte swizzle, 64: 64-byte), as TMA writes it.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+}
+
+// Columns of tensor memory: S of the two tiles (P in its first half), then O.
+__device__ __forceinline__ uint32_t col_s(int x) { return x * kTile; }
+template <int D>
+__device__ __forceinline__ uint32_t col_o(int x) {
+    return 2 * kTile + x * D;
+}
+
+// Ring position of the n-th use of a ring of N stages.
+template <int N>
+struct Ring {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++stage == N) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+template <bool kMask>
+__device__ __forceinline__ float row_max(const uint32_t (&s)[32], int at, const Meta& meta, float f, int n,
+                                         uint32_t valid) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float x = f * meta.scale[at / 16 + h];
+        float m = -INFINITY;
+        if (kMask) {
+            const bool has = (valid >> (at / 16 + h)) & 1;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                m = fmaxf(m, has && at + 16 * h + i < n ? __uint_as_float(s[16 * h + i]) * x : -INFINITY);
+            top = fmaxf(top, m);
+        } else {                              // scales are not negative: the largest product is the largest times x
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m = fmaxf(m, __uint_as_float(s[16 * h + i]));
+            top = fmaxf(top, m * x);
+        }
+    }
+    return top;
+}
+
+// 32 weights of a row, as 16 pairs of f16, and their sum.
+template <bool kMask>
+__device__ __forceinline__ float weights(const uint32_t (&s)[32], uint32_t (&p)[16], int at, const Meta& meta, float f,
+                                         float zero, int n, uint32_t valid) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float x = f * meta.scale[at / 16 + h];
+        const bool has = !kMask || ((valid >> (at / 16 + h)) & 1);
+        float part = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            float a = ex2(fmaf(__uint_as_float(s[16 * h + i]), x, -zero));
+            float b = ex2(fmaf(__uint_as_float(s[16 * h + i + 1]), x, -zero));
+            if (kMask) {
+                a = has && at + 16 * h + i < n ? a : 0.0f;
+                b = has && at + 16 * h + i + 1 < n ? b : 0.0f;
+            }
+            part += a + b;
+            p[8 * h + i / 2] = pack_f16x2(a, b);
+        }
+        sum += part;
+    }
+    return sum;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_attend_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                        const AttendArgs a) {
+    extern __shared__ uint8_t raw[];
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+    constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel waits for this one's end
+    if (tid == 0) {
+        sm.abort = 0;
+        for (int i = 0; i < kKStages; ++i) mbar_init(&sm.k_full[i], 1 + 8), mbar_init(&sm.k_empty[i], 1);
+        for (int i = 0; i < kVStages; ++i) mbar_init(&sm.v_full[i], 1 + 8), mbar_init(&sm.v_empty[i], 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.v16_full[i], 2);
+            mbar_init(&sm.v16_empty[i], 1);
+            mbar_init(&sm.q_full[i], 4);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.o_full[i], 1);
+        }
+        mbar_init(&sm.done, 1);
+        fence_mbar_init_cluster();
+    }
+    if (warp == 11) tmem_alloc(&sm.tmem, 512);
+    if (tid < 2) a.desc[blockIdx.x * 2 + tid].valid = 0;
+    check_offsets(a);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+
+    int64_t total = 0, seen = 0;
+    const bool one_table = a.seqs.B <= kTable;
+    if (!one_table)
+        for (int base = 0; base < a.seqs.B; base += kTable) total += fill_table(a, sm.tab, base);
+
+    // counters of each role, over all tables
+    Ring<kKStages> kr;
+    Ring<kMetas> mr;
+    Ring<kVStages> vr;
+    Ring<2> v16r;
+    uint32_t segs = 0, pairs = 0;             // segments with keys; of two tiles
+    uint32_t steps = 0, steps1 = 0;           // of a softmax warp's tile; of the first and second tile
+    uint32_t outs = 0, k_loads = 0, v_loads = 0;
+
+    for (int base = 0; base < a.seqs.B; base += kTable) {
+        const int64_t here = fill_table(a, sm.tab, base);
+        if (one_table) total = here;
+        int64_t from, to;
+        share_of(total, blockIdx.x, gridDim.x, from, to);
+        const int64_t lo = (from > seen ? from : seen) - seen, hi = (to < seen + here ? to : seen + here) - seen;
+        seen += here;
+        if (hi <= lo) continue;               // the same for the whole block
+        Walk seg;
+        walk_start(seg, sm.tab.info, sm.tab.prefix, kTable, a.cut, lo, hi - lo);
+
+        if (warp < 8) {
+            // ------------------------------------------------------- softmax
+            const int x = warp / 4, in_tile = (warp % 4) * 32 + lane;
+            const uint32_t lanes = tmem + ((uint32_t)(warp % 4) << 21);
+            bool ok = true;
+            for (; ok && seg.left > 0; walk_next(seg, sm.tab.info, a.cut)) {
+                const SeqInfo info = sm.tab.info[seg.b];
+                const int first_row = seg.tile * kPair, rows = min(info.rows - first_row, kPair);
+                const int mine = x * kTile + in_tile;                // of the block's rows
+                const bool active = x == 0 || rows > kTile;
+                int key0, keys;
+                segment_keys(seg, sm.tab.info, a.cut, key0, keys);
+                const int count = (keys - key0 + kTile - 1) / kTile;  // 0: a tile without keys
+                float f = 0.0f;
+                int lim = 0;
+                if (active && count > 0) {
+                    // this thread's query row as hi + lo
+                    uint4 u[D / 8];
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) u[i] = make_uint4(0, 0, 0, 0);
+                    if (mine < rows) {
+                        const int r = first_row + mine;
+                        lim = keys_of_row(info, a.cut, r);
+                        const uint4* src = reinterpret_cast<const uint4*>(
+                            a.q + (info.begin + r / a.cut.group) * a.q_stride +
+                            (int64_t)(seg.head * a.cut.group + r % a.cut.group) * D);
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i) u[i] = __ldg(src + i);
+                    }
+                    float top = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        float y[8];
+                        unpack8(u[i], y);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[j]));
+                    }
+                    int e = 134 - (int)(__float_as_uint(top) >> 23);  // 7 - floor(log2(top))
+                    e = e < -120 ? -120 : (e > 120 ? 120 : e);
+                    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+                    f = __uint_as_float((uint32_t)(127 - e) << 23) * a.scale_log2;
+                    if (top == INFINITY) f = __int_as_float(0x7fc00000);   // e4m3 has no infinity: such a row is NaN
+                    const uint32_t hi_at = smem_u32(sm.q[x][0]), lo_at = smem_u32(sm.q[x][1]);
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t h[4], l[4];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float y[8], z[8];
+                            unpack8(u[2 * c + i], y);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) y[j] *= up;
+                            h[2 * i] = e4m3x4(y, 0);
+                            h[2 * i + 1] = e4m3x4(y, 4);
+#pragma unroll
+                            for (int j = 0; j < 8; j += 2) {
+                                const uint32_t w = h[2 * i + j / 4];
+                                const uint32_t b = j % 4 ? cvt_hi(w) : cvt_lo(w);
+                                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&b));
+                                z[j] = y[j] - back.x;
+                                z[j + 1] = y[j + 1] - back.y;
+                            }
+                            l[2 * i] = e4m3x4(z, 0);
+                            l[2 * i + 1] = e4m3x4(z, 4);
+                        }
+                        sts128(hi_at + chunk_at<D>(in_tile, c), make_uint4(h[0], h[1], h[2], h[3]));
+                        sts128(lo_at + chunk_at<D>(in_tile, c), make_uint4(l[0], l[1], l[2], l[3]));
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (active && count > 0) {
+                    tc_fence_before();        // the last segment's reads of O come before this one's products
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.q_full[x]);
+                }
+
+                float m = -INFINITY, l = 0.0f;
+                const int all_see = keys_of_row(info, a.cut, first_row + x * kTile);
+                for (int j = 0; j < count; ++j, mr.next()) {
+                    if (!active) continue;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[x], steps & 1, &sm.abort));
+                    if (!ok) break;
+                    ++steps;
+                    tc_fence_after();
+                    const Meta& meta = sm.k_meta[mr.stage];
+                    const uint32_t valid = meta.valid;
+                    const int n = lim - (key0 + j * kTile);   // keys of this step that the row sees
+                    const bool mask = key0 + (j + 1) * kTile > all_see || valid != 0xffu;
+                    float top = -INFINITY;
+                    uint32_t s2[2][32];       // 32 columns at hand, the next 32 on their way
+                    tmem_ld32(lanes + col_s(x), s2[0]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_wait_ld();
+                        tmem_regs_ready(s2[c & 1]);
+                        if (c < 3) tmem_ld32(lanes + col_s(x) + (c + 1) * 32, s2[(c + 1) & 1]);
+                        if (mask) top = fmaxf(top, row_max<true>(s2[c & 1], c * 32, meta, f, n, valid));
+                        else top = fmaxf(top, row_max<false>(s2[c & 1], c * 32, meta, f, n, valid));
+                    }
+                    const bool grow = top > m + kGrow;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float now = grow ? top : m;
+                        const float keep = grow ? ex2(m - now) : 1.0f;
+                        m = now;
+                        l *= keep;
+                        if (j > 0) {          // this tile's products up to now are done: S came after them
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32(lanes + col_o<D>(x) + c * 32, o);
+                                tmem_wait_ld();
+                                tmem_regs_ready(o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                                tmem_st32(lanes + col_o<D>(x) + c * 32, o);
+                            }
+                        }
+                    }
+                    const float zero = m == -INFINITY ? 0.0f : m - kLift;
+                    tmem_ld32(lanes + col_s(x), s2[0]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {             // P takes the first half of S's columns, behind the reads
+                        uint32_t p[16];
+                        tmem_wait_ld();
+                        tmem_regs_ready(s2[c & 1]);
+                        if (c < 3) tmem_ld32(lanes + col_s(x) + (c + 1) * 32, s2[(c + 1) & 1]);
+                        if (mask) l += weights<true>(s2[c & 1], p, c * 32, meta, f, zero, n, valid);
+                        else l += weights<false>(s2[c & 1], p, c * 32, meta, f, zero, n, valid);
+                        tmem_st16(lanes + col_s(x) + c * 16, p);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.p_full[x]);
+                }
+                if (!ok) break;
+                if (!active) {
+                    segs += count > 0;
+                    continue;
+                }
+
+                // the rows go out
+                const bool whole = seg.first == 0 && seg.count == seg.units;
+                const int slot = seg.first == 0 ? 1 : 0;
+                if (!whole && tid == 0) {
+                    PartDesc d;
+                    d.valid = 1;
+                    d.last = seg.first + seg.count == seg.units;
+                    d.begin = info.begin;
+                    d.first_row = first_row;
+                    d.rows = rows;
+                    d.head = seg.head;
+                    a.desc[blockIdx.x * 2 + slot] = d;
+                }
+                if (count > 0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_full[x], outs & 1, &sm.abort));
+                    if (!ok) break;
+                    ++outs;
+                    tc_fence_after();
+                }
+                const int64_t at = mine < rows ? place_of(a, info.begin, first_row + mine, seg.head) : 0;
+                float* part = a.part + (((int64_t)blockIdx.x * 2 + slot) * kPair + mine) * (D + 2);
+                const int kept = segs % kSegs;
+                const float unit = count > 0 ? sm.ref[kept] * (1.0f / kVLift) : 0.0f;
+                const float by = whole ? (l == 0.0f ? 0.0f : unit / l) : unit;
+                const bool nans = count > 0 && sm.has_nan[kept];
+                if (mine < rows) {
+                    if (whole && a.lse) a.lse[at] = lse_of(m, l);
+                    if (!whole) *reinterpret_cast<float2*>(part) = make_float2(m, l);
+                }
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    if (count > 0) {
+                        tmem_ld32(lanes + col_o<D>(x) + c * 32, o);
+                        tmem_wait_ld();
+                        tmem_regs_ready(o);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float y = count > 0 ? __uint_as_float(o[i]) * by : 0.0f;
+                        if (nans && sm.nan_key[kept][c * 32 + i] < lim) y = __int_as_float(0x7fc00000);
+                        o[i] = __float_as_uint(y);
+                    }
+                    if (mine >= rows) continue;
+                    if (whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + c * 32);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float y[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(o[8 * i + k]);
+                            dst[i] = pack8(y);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2)
+                            *reinterpret_cast<uint2*>(part + 2 + c * 32 + i) = make_uint2(o[i], o[i + 1]);
+                    }
+                }
+                segs += count > 0;
+            }
+        } else if (warp < 10) {
+            // ------------------------------------------------- values to f16
+            const int id = tid - 256;         // this thread takes keys id and id + 64 of a step
+            bool ok = true;                   // after a wait that gave up both warps go on to the barriers, without work
+            for (; seg.left > 0; walk_next(seg, sm.tab.info, a.cut)) {
+                const SeqInfo info = sm.tab.info[seg.b];
+                int key0, keys;
+                segment_keys(seg, sm.tab.info, a.cut, key0, keys);
+                if (keys <= key0) continue;
+                const int slot = segs++ % kSegs, P = a.seqs.page_tokens;
+                const int32_t* row = a.seqs.table + (int64_t)(base + seg.b) * a.seqs.width;
+                float most = 0.0f;
+                for (int i = key0 / P + id; i * P < keys; i += 64) {
+                    const int page = __ldg(row + i);
+                    if (page >= 0 && page < a.seqs.num_pages)
+                        most = fmaxf(most, __ldg(a.v_scale + (int64_t)page * a.cut.heads + seg.head));
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                if (lane == 0) sm.red[warp - 8] = most;
+                for (int i = id; i < D; i += 64) sm.nan_key[slot][i] = 0x7fffffff;
+                if (id == 0) sm.has_nan[slot] = 0;
+                named_bar_sync(1, 64);
+                most = fmaxf(sm.red[0], sm.red[1]);
+                if (id == 0) sm.ref[slot] = most;
+                named_bar_sync(1, 64);
+                const float per = most > 0.0f ? kVLift / most : 0.0f;
+                const int all_see = keys_of_row(info, a.cut, seg.tile * kPair);
+                for (int key = key0; ok && key < keys; key += kTile) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.v_full[vr.stage], vr.phase, &sm.abort)) &&
+                         __all_sync(0xffffffffu, mbar_wait(&sm.v16_empty[v16r.stage], v16r.phase ^ 1, &sm.abort));
+                    if (!ok) break;
+                    const Meta& meta = sm.v_meta[vr.stage];
+                    const uint32_t src = smem_u32(sm.v[vr.stage]), dst = smem_u32(sm.v16[v16r.stage]);
+                    const bool some = key + kTile > all_see;          // not every row sees every key of this step
+#pragma unroll 1
+                    for (int key_in = id; key_in < kTile; key_in += 64) {
+                        const bool use = ((meta.valid >> (key_in / 16)) & 1) && key + key_in < keys;
+                        const float ratio = use ? meta.scale[key_in / 16] * per : 0.0f;
+                        const bool exact = (__float_as_uint(ratio) & 0x7fffffu) == 0 && ratio >= 5.9604645e-8f;
+                        const uint32_t times = pack_f16x2(ratio, ratio);
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) {
+                            const uint4 u = lds128(src + chunk_at<D>(key_in, c));
+                            uint32_t w[4] = {u.x, u.y, u.z, u.w}, h[8];
+                            if (!use) w[0] = w[1] = w[2] = w[3] = 0;
+                            if (some) {
+                                // NaN must reach only the rows that see this key, but 0 * NaN is
+                                // NaN: it is taken out here and put back as the rows go out
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint32_t n = nan_bytes(w[i]);
+                                    if (n) {
+                                        sm.has_nan[slot] = 1;
+                                        for (int b = 0; b < 4; ++b)
+                                            if ((n >> (8 * b)) & 0x80u) {
+                                                atomicMin(&sm.nan_key[slot][16 * c + 4 * i + b], key + key_in);
+                                                w[i] &= ~(0xffu << (8 * b));
+                                            }
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                h[2 * i] = cvt_lo(w[i]);
+                                h[2 * i + 1] = cvt_hi(w[i]);
+                            }
+                            if (exact) {          // a power of two: one rounding at most, in f16's subnormals
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) h[i] = mul_f16x2(h[i], times);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+                                    h[i] = pack_f16x2(y.x * ratio, y.y * ratio);
+                                }
+                            }
+                            // 64 dims of a key are one 128-byte row, swizzled; the next 64 dims follow all keys
+                            const uint32_t to_row = dst + (c / 4) * (kTile * 128) + key_in * 128;
+                            const int c16 = (2 * c) % 8;
+                            sts128(to_row + ((c16 ^ (key_in & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+                            sts128(to_row + (((c16 + 1) ^ (key_in & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sm.v16_full[v16r.stage]);
+                        mbar_arrive(&sm.v_empty[vr.stage]);
+                    }
+                    vr.next();
+                    v16r.next();
+                }
+            }
+        } else if (warp == 10) {
+            // ----------------------------------------------------------- TMA
+            const int P = a.seqs.page_tokens, per_box = P / 16;
+            bool ok = true;
+            for (; ok && seg.left > 0; walk_next(seg, sm.tab.info, a.cut)) {
+                int key0, keys;
+                segment_keys(seg, sm.tab.info, a.cut, key0, keys);
+                const int32_t* row = a.seqs.table + (int64_t)(base + seg.b) * a.seqs.width;
+                auto page_at = [&](int key) { return lane < 8 && key + 16 * lane < keys ? __ldg(row + (key + 16 * lane) / P) : -1; };
+                int page = page_at(key0);
+                for (int key = key0; key < keys; key += kTile) {
+                    const int ahead = page_at(key + kTile);
+                    const bool has = page >= 0 && page < a.seqs.num_pages;
+                    if (lane < 8 && key + 16 * lane < keys && !has) atomicOr(&g_device_status, kIndexError);
+                    const uint32_t valid = __ballot_sync(0xffffffffu, lane < 8 && has);
+                    const bool box = lane < 8 && has && lane % per_box == 0;
+                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box)) * P * D;
+                    const int block = has ? page * a.cut.heads + seg.head : 0;
+
+                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.k_empty[kr.stage], kr.phase ^ 1, &sm.abort));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        sm.k_meta[mr.stage].valid = valid;
+                        mbar_arrive_expect_tx(&sm.k_full[kr.stage], bytes);
+                    }
+                    __syncwarp();
+                    if (lane < 8) {
+                        if (has) copy_async4(&sm.k_meta[mr.stage].scale[lane], a.k_scale + block);
+                        arrive_after_copies(&sm.k_full[kr.stage]);
+                    }
+                    if (box) tma_load_3d(sm.k[kr.stage] + lane * 16 * D, &k_map, 0, 0, block, &sm.k_full[kr.stage]);
+                    ++k_loads;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.v_empty[vr.stage], vr.phase ^ 1, &sm.abort));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        sm.v_meta[vr.stage].valid = valid;
+                        mbar_arrive_expect_tx(&sm.v_full[vr.stage], bytes);
+                    }
+                    __syncwarp();
+                    if (lane < 8) {
+                        if (has) copy_async4(&sm.v_meta[vr.stage].scale[lane], a.v_scale + block);
+                        arrive_after_copies(&sm.v_full[vr.stage]);
+                    }
+                    if (box) tma_load_3d(sm.v[vr.stage] + lane * 16 * D, &v_map, 0, 0, block, &sm.v_full[vr.stage]);
+                    ++v_loads;
+                    kr.next();
+                    mr.next();
+                    vr.next();
+                    page = ahead;
+                }
+            }
+        } else if (lane == 0) {
+            // ------------------------------------------- tensor instructions
+            auto product_s = [&](int x, int stage) {
+                const uint64_t kd = smem_desc(smem_u32(sm.k[stage]), 16, D * 8, D == 128 ? 2 : 4);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint64_t qd = smem_desc(smem_u32(sm.q[x][h]), 16, D * 8, D == 128 ? 2 : 4);
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i)
+                        mma_e4m3(tmem + col_s(x), qd + 2 * i, kd + 2 * i, kIdescS, h + i > 0);
+                }
+            };
+            auto product_o = [&](int x, int stage, bool more) {
+                // values: dims contiguous ("MN-major"); 64 dims a 128-byte row, 8 keys an atom, 64 further dims 16 KB on
+                const uint64_t vd = smem_desc(smem_u32(sm.v16[stage]), kTile * 128, 1024, 2);
+#pragma unroll
+                for (int i = 0; i < kTile / 16; ++i)
+                    mma_f16_ts(tmem + col_o<D>(x), tmem + col_s(x) + 8 * i, vd + 128 * i, kIdescO, more || i > 0);
+            };
+            bool ok = true;
+            for (; ok && seg.left > 0; walk_next(seg, sm.tab.info, a.cut)) {
+                int key0, keys;
+                segment_keys(seg, sm.tab.info, a.cut, key0, keys);
+                const bool two = sm.tab.info[seg.b].rows - seg.tile * kPair > kTile;
+                const int count = (keys - key0 + kTile - 1) / kTile;
+                if (count == 0) continue;
+                ok = mbar_wait(&sm.q_full[0], segs & 1, &sm.abort) &&
+                     mbar_wait(&sm.k_full[kr.stage], kr.phase, &sm.abort);
+                if (!ok) break;
+                ++segs;
+                tc_fence_after();
+                product_s(0, kr.stage);
+                mma_commit(&sm.s_full[0]);
+                if (two) {
+                    ok = mbar_wait(&sm.q_full[1], pairs & 1, &sm.abort);
+                    if (!ok) break;
+                    ++pairs;
+                    tc_fence_after();
+                    product_s(1, kr.stage);
+                    mma_commit(&sm.s_full[1]);
+                }
+                mma_commit(&sm.k_empty[kr.stage]);
+                kr.next();
+                for (int j = 0; j < count; ++j) {
+                    const bool more = j + 1 < count;
+                    ok = mbar_wait(&sm.v16_full[v16r.stage], v16r.phase, &sm.abort) &&
+                         mbar_wait(&sm.p_full[0], steps & 1, &sm.abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    product_o(0, v16r.stage, j > 0);
+                    if (!more) mma_commit(&sm.o_full[0]);
+                    if (more) {
+                        ok = mbar_wait(&sm.k_full[kr.stage], kr.phase, &sm.abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        product_s(0, kr.stage);
+                        mma_commit(&sm.s_full[0]);
+                    }
+                    if (two) {
+                        ok = mbar_wait(&sm.p_full[1], steps1 & 1, &sm.abort);
+                        if (!ok) break;
+                        ++steps1;
+                        tc_fence_after();
+                        product_o(1, v16r.stage, j > 0);
+                        if (!more) mma_commit(&sm.o_full[1]);
+                        mma_commit(&sm.v16_empty[v16r.stage]);
+                        if (more) {
+                            product_s(1, kr.stage);
+                            mma_commit(&sm.s_full[1]);
+                        }
+                    } else {
+                        mma_commit(&sm.v16_empty[v16r.stage]);
+                    }
+                    if (more) {
+                        mma_commit(&sm.k_empty[kr.stage]);
+                        kr.next();
+                    }
+                    v16r.next();
+                    ++steps;
+                }
+            }
+        }
+        __syncwarp();
+        __syncthreads();                      // before the table is filled anew
+    }
+
+    // Everything asynchronous has ended before the block does: the products by
+    // their last commit, and, after a wait that gave up, the loads under way.
+    if (warp == 11 && lane == 0) {
+        mma_commit(&sm.done);
+        mbar_wait_drain(&sm.done, 0);
+    }
+    if (warp == 10 && lane == 0 && sm.abort) {
+        for (uint32_t i = k_loads > kKStages ? k_loads - kKStages : 0; i < k_loads; ++i)
+            mbar_wait_drain(&sm.k_full[i % kKStages], (i / kKStages) & 1);
+        for (uint32_t i = v_loads > kVStages ? v_loads - kVStages : 0; i < v_loads; ++i)
+            mbar_wait_drain(&sm.v_full[i % kVStages], (i / kVStages) & 1);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 11) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const AttendArgs& a, const uint8_t* k, const uint8_t* v, int blocks, cudaStream_t stream) {
+    CUtensorMap k_map, v_map;
+    const int64_t pages = (int64_t)a.seqs.num_pages * a.cut.heads;
+    if (!encode_codes(&k_map, k, pages, a.seqs.page_tokens, D, kTile) ||
+        !encode_codes(&v_map, v, pages, a.seqs.page_tokens, D, kTile))
+        return cudaErrorInvalidValue;
+    const int bytes = (int)sizeof(Smem<D>) + 1024;
+    const cudaError_t e = cudaFuncSetAttribute(kv_attend_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kv_attend_tc_kernel<D><<<blocks, kThreads, bytes, stream>>>(k_map, v_map, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_attend_tc(const AttendArgs& a, const uint8_t* k, const uint8_t* v, int head_dim, int blocks,
+                                cudaStream_t stream) {
+    return head_dim == 64 ? launch<64>(a, k, v, blocks, stream) : launch<128>(a, k, v, blocks, stream);
+}
+
+cudaError_t read_attend_tc_status(unsigned int* status) {
+    unsigned int v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_device_status, sizeof v);
+    if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof zero);
+    *status = v;
+    return e;
+}
+
+}  // namespace kv
+}  // namespace mhc

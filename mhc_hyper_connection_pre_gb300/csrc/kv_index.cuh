@@ -97,13 +97,11 @@ MHC_HD bool starts_run(const Span& sp, const Run& r, int t) {
 // How mhc_kv_attend's work is cut.  The rows of one sequence and key/value head
 // are its new tokens times the `group` query heads that share the head, row r
 // being token r / group, query head r % group of it; a tile is `tile_rows` of
-// them.  A tile's keys are cut in units of kUnit; a tile without keys still is
+// them.  A tile's keys are cut in units of `unit`; a tile without keys still is
 // one unit (its rows have to be written).  All units of all tiles, ordered by
 // sequence, tile, head and key, form one line that the blocks share evenly
 // whatever the lengths are (share_of), and a tile cut by a border is joined
 // afterwards.
-
-constexpr int kUnit = 64;
 
 // One sequence as the walk needs it.
 struct SeqInfo {
@@ -113,7 +111,7 @@ struct SeqInfo {
 };
 
 struct Cut {
-    int heads, group, tile_rows;
+    int heads, group, tile_rows, unit;
 };
 
 MHC_HD SeqInfo info_of(const Span& sp, int group) {
@@ -140,7 +138,7 @@ MHC_HD int keys_of_tile(const SeqInfo& s, const Cut& c, int i) {
 }
 
 MHC_HD int units_of_tile(const SeqInfo& s, const Cut& c, int i) {
-    const int n = (keys_of_tile(s, c, i) + kUnit - 1) / kUnit;
+    const int n = (keys_of_tile(s, c, i) + c.unit - 1) / c.unit;
     return n < 1 ? 1 : n;
 }
 

@@ -42,6 +42,7 @@ cudaError_t read_collapse_status(unsigned int* status);
 namespace kv {
 cudaError_t read_append_status(unsigned int* status);
 cudaError_t read_attend_status(unsigned int* status);
+cudaError_t read_attend_tc_status(unsigned int* status);
 constexpr unsigned int kIndexError = 2u;   // as in kv_common.cuh
 }  // namespace kv
 }  // namespace mhc
@@ -169,9 +170,11 @@ mhc_status mhc_device_status(void) {
     if (mhc::read_device_status(&v) != cudaSuccess) return MHC_ERR_CUDA;
     if (mhc::read_decode_status(&w) != cudaSuccess) return MHC_ERR_CUDA;
     if (mhc::read_collapse_status(&c) != cudaSuccess) return MHC_ERR_CUDA;
-    unsigned int ka = 0, kt = 0;
+    unsigned int ka = 0, kt = 0, kc = 0;
     if (mhc::kv::read_append_status(&ka) != cudaSuccess) return MHC_ERR_CUDA;
     if (mhc::kv::read_attend_status(&kt) != cudaSuccess) return MHC_ERR_CUDA;
+    if (mhc::kv::read_attend_tc_status(&kc) != cudaSuccess) return MHC_ERR_CUDA;
+    kt |= kc;
     if (v | w | c | ((ka | kt) & ~mhc::kv::kIndexError)) return MHC_ERR_TIMEOUT;
     return (ka | kt) ? MHC_ERR_INDEX : MHC_OK;
 }

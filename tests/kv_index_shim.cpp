@@ -39,10 +39,10 @@ void kv_runs(const int32_t* table, const int32_t* lens, const int32_t* cu, int w
 // tile}.  Returns how many, or -1 if there are more than `most`; total: units
 // of the whole line.
 int kv_segments(const int32_t* table, const int32_t* lens, const int32_t* cu, int width, int B, int T, int P,
-                int pages, int heads, int group, int tile_rows, int table_size, int block, int blocks, int32_t* out,
+                int pages, int heads, int group, int tile_rows, int unit, int table_size, int block, int blocks, int32_t* out,
                 int most, int64_t* total) {
     const Seqs s = make(table, lens, cu, width, B, T, P, pages);
-    const Cut c{heads, group, tile_rows};
+    const Cut c{heads, group, tile_rows, unit};
     *total = 0;
     for (int b = 0; b < B; ++b) *total += units_of_seq(info_of(span_of(s, b), group), c);
     int64_t from, to;

@@ -240,13 +240,13 @@ def test_runs_stay_inside_whatever_the_arrays_hold(shim, seed):
             assert -1 <= page < pages
 
 
-def _segments(shim, lens, cu, T, B, width, heads, group, rows, table, blocks, P=16):
+def _segments(shim, lens, cu, T, B, width, heads, group, rows, table, blocks, unit=64):
     """Every block's segments, in order, and the number of units."""
     pages = _i32(np.zeros((B, width)))
     out, total, got = np.zeros((20000, 6), dtype=np.int32), ctypes.c_int64(0), []
     for c in range(blocks):
-        n = shim.kv_segments(_ptr(pages), _ptr(lens), _ptr(cu), width, B, T, P, 1, heads, group, rows, table, c, blocks,
-                             _ptr(out), 20000, ctypes.byref(total))
+        n = shim.kv_segments(_ptr(pages), _ptr(lens), _ptr(cu), width, B, T, 16, 1, heads, group, rows, unit, table, c,
+                             blocks, _ptr(out), 20000, ctypes.byref(total))
         assert n >= 0
         got.append(out[:n].tolist())
     return got, total.value
@@ -258,7 +258,7 @@ def test_blocks_share_every_unit_once(shim, seed):
     order; every tile has a unit, no block takes much more than another, and
     of a block's segments only the first and the last may be parts of tiles."""
     r = random.Random(50 + seed)
-    B, blocks, P = r.choice([1, 3, 17, 40]), r.choice([1, 7, 152]), 16
+    B, blocks, P, unit = r.choice([1, 3, 17, 40]), r.choice([1, 7, 152]), 16, r.choice([64, 128])
     heads, group, rows, table = r.choice([1, 2, 8]), r.choice([1, 5, 16]), r.choice([8, 16, 128]), r.choice([4, 16, 256])
     counts = [r.choice([0, 1, 1, r.randint(0, 40)]) for _ in range(B)]
     lens = [r.choice([0, n, n + r.randint(0, 3000)]) for n in counts]
@@ -268,12 +268,13 @@ def test_blocks_share_every_unit_once(shim, seed):
     cu = [0]
     for n in counts:
         cu.append(cu[-1] + n)
-    got, total = _segments(shim, _i32(lens), _i32(cu), cu[-1], B, width, heads, group, rows, table, blocks)
+    got, total = _segments(shim, _i32(lens), _i32(cu), cu[-1], B, width, heads, group, rows, table, blocks,
+                           unit)
     expect = []
     for b, (n, m) in enumerate(zip(lens, counts)):
         for i in range(-(-m * group // rows)):
             last = min((i + 1) * rows, m * group) - 1
-            units = max(1, -(-max(0, n - m + last // group + 1) // 64))
+            units = max(1, -(-max(0, n - m + last // group + 1) // unit))
             for h in range(heads):
                 expect += [(b, i, h, u, units) for u in range(units)]
     flat = [(b, i, h, u, units) for c in got for b, i, h, first, count, units in c for u in range(first, first + count)]
