@@ -336,15 +336,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int n = lim - (key0 + j * kTile);   // keys of this step that the row sees
                     const bool mask = key0 + (j + 1) * kTile > all_see || valid != 0xffu;
                     float top = -INFINITY;
-                    uint32_t s2[2][32];       // 32 columns at hand, the next 32 on their way
-                    tmem_ld32(lanes + col_s(x), s2[0]);
-#pragma unroll
+#pragma unroll 1                                  // rolled, here and below: the roles' code has to fit the instruction cache
                     for (int c = 0; c < 4; ++c) {
+                        uint32_t s[32];
+                        tmem_ld32(lanes + col_s(x) + c * 32, s);
                         tmem_wait_ld();
-                        tmem_regs_ready(s2[c & 1]);
-                        if (c < 3) tmem_ld32(lanes + col_s(x) + (c + 1) * 32, s2[(c + 1) & 1]);
-                        if (mask) top = fmaxf(top, row_max<true>(s2[c & 1], c * 32, meta, f, n, valid));
-                        else top = fmaxf(top, row_max<false>(s2[c & 1], c * 32, meta, f, n, valid));
+                        tmem_regs_ready(s);
+                        if (mask) top = fmaxf(top, row_max<true>(s, c * 32, meta, f, n, valid));
+                        else top = fmaxf(top, row_max<false>(s, c * 32, meta, f, n, valid));
                     }
                     const bool grow = top > m + kGrow;
                     if (__any_sync(0xffffffffu, grow)) {
@@ -353,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m = now;
                         l *= keep;
                         if (j > 0) {          // this tile's products up to now are done: S came after them
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < D / 32; ++c) {
                                 uint32_t o[32];
                                 tmem_ld32(lanes + col_o<D>(x) + c * 32, o);
@@ -366,15 +365,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const float zero = m == -INFINITY ? 0.0f : m - kLift;
-                    tmem_ld32(lanes + col_s(x), s2[0]);
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {             // P takes the first half of S's columns, behind the reads
-                        uint32_t p[16];
+                        uint32_t s[32], p[16];
+                        tmem_ld32(lanes + col_s(x) + c * 32, s);
                         tmem_wait_ld();
-                        tmem_regs_ready(s2[c & 1]);
-                        if (c < 3) tmem_ld32(lanes + col_s(x) + (c + 1) * 32, s2[(c + 1) & 1]);
-                        if (mask) l += weights<true>(s2[c & 1], p, c * 32, meta, f, zero, n, valid);
-                        else l += weights<false>(s2[c & 1], p, c * 32, meta, f, zero, n, valid);
+                        tmem_regs_ready(s);
+                        if (mask) l += weights<true>(s, p, c * 32, meta, f, zero, n, valid);
+                        else l += weights<false>(s, p, c * 32, meta, f, zero, n, valid);
                         tmem_st16(lanes + col_s(x) + c * 16, p);
                     }
                     tmem_wait_st();
@@ -417,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (whole && a.lse) a.lse[at] = lse_of(m, l);
                     if (!whole) *reinterpret_cast<float2*>(part) = make_float2(m, l);
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
                     if (count > 0) {
@@ -490,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float ratio = use ? meta.scale[key_in / 16] * per : 0.0f;
                         const bool exact = (__float_as_uint(ratio) & 0x7fffffu) == 0 && ratio >= 5.9604645e-8f;
                         const uint32_t times = pack_f16x2(ratio, ratio);
-#pragma unroll
+#pragma unroll 2
                         for (int c = 0; c < D / 16; ++c) {
                             const uint4 u = lds128(src + chunk_at<D>(key_in, c));
                             uint32_t w[4] = {u.x, u.y, u.z, u.w}, h[8];
