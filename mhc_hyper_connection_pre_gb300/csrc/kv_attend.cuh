@@ -87,6 +87,10 @@ __device__ __forceinline__ void check_offsets(const AttendArgs& a) {
         atomicOr(&g_device_status, kIndexError);
 }
 
+// The barrier of the whole block; unlike __syncthreads, it may be met in
+// different places of the code.
+__device__ __forceinline__ void block_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
+
 // Fills the table with sequences base .. base + kTable - 1 and the running sum
 // of their units; returns the units of them all.  Whole block, of at least
 // kTable threads.
@@ -110,7 +114,7 @@ __device__ inline int64_t fill_table(const AttendArgs& a, Table& tab, int base) 
         }
         if (lane == 31) tab.warp_sum[warp] = run;
     }
-    __syncthreads();
+    block_sync();
     int64_t before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < kTable / 32; ++w) {
@@ -119,7 +123,7 @@ __device__ inline int64_t fill_table(const AttendArgs& a, Table& tab, int base) 
         total += s;
     }
     if (tid < kTable) tab.prefix[tid] = before + run - mine;
-    __syncthreads();
+    block_sync();
     return total;
 }
 

@@ -25,8 +25,9 @@
 // of V; the two tiles alternate, so that the softmax of one runs while the
 // other's products do.  The conversion is shared by the two tiles.
 //
-// Warps 0-3 and 4-7: softmax of the two tiles; 8-9: V to f16; 10: TMA loads;
-// 11: the tensor instructions.  (Twelve warps leave the softmax 168 registers.)
+// Warps 0-3 and 4-7: softmax of the two tiles; 8-11: V to f16; 12: TMA loads;
+// 13: the tensor instructions.  The softmax gets 176 registers a thread and the
+// others 80 of the 128 that 16 warps start with.
 #include "kv_attend.cuh"
 
 namespace mhc {
@@ -34,7 +35,7 @@ namespace kv {
 
 namespace {
 
-constexpr int kThreads = 12 * 32;
+constexpr int kThreads = 16 * 32;
 constexpr int kTile = 128;                    // rows of one tile, and keys of one step
 constexpr int kPair = 2 * kTile;              // rows of a block's work
 constexpr int kKStages = 3, kVStages = 2;
@@ -61,7 +62,7 @@ struct __align__(1024) Smem {
     int nan_key[kSegs][D];                    // first key with NaN in each dim, among those that not every row sees
     int has_nan[kSegs];
     float ref[kSegs];                         // largest value scale of the segment
-    float red[2];
+    float red[4];
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t v16_full[2], v16_empty[2], q_full[2], s_full[2], p_full[2], o_full[2], done;
     uint32_t tmem;
@@ -202,9 +203,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         sm.abort = 0;
         for (int i = 0; i < kKStages; ++i) mbar_init(&sm.k_full[i], 1 + 8), mbar_init(&sm.k_empty[i], 1);
-        for (int i = 0; i < kVStages; ++i) mbar_init(&sm.v_full[i], 1 + 8), mbar_init(&sm.v_empty[i], 2);
+        for (int i = 0; i < kVStages; ++i) mbar_init(&sm.v_full[i], 1 + 8), mbar_init(&sm.v_empty[i], 4);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.v16_full[i], 2);
+            mbar_init(&sm.v16_full[i], 4);
             mbar_init(&sm.v16_empty[i], 1);
             mbar_init(&sm.q_full[i], 4);
             mbar_init(&sm.s_full[i], 1);
@@ -214,18 +215,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.done, 1);
         fence_mbar_init_cluster();
     }
-    if (warp == 11) tmem_alloc(&sm.tmem, 512);
+    if (warp == 13) tmem_alloc(&sm.tmem, 512);
     if (tid < 2) a.desc[blockIdx.x * 2 + tid].valid = 0;
     check_offsets(a);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-
-    int64_t total = 0, seen = 0;
-    const bool one_table = a.seqs.B <= kTable;
-    if (!one_table)
-        for (int base = 0; base < a.seqs.B; base += kTable) total += fill_table(a, sm.tab, base);
+    // Runs a role over this block's segments, table by table.  Each role has its
+    // own copy of this loop, inside its own register budget.
+    auto each_table = [&](auto&& role) {
+        int64_t total = 0, seen = 0;
+        const bool one_table = a.seqs.B <= kTable;
+        if (!one_table)
+#pragma unroll 1
+            for (int base = 0; base < a.seqs.B; base += kTable) total += fill_table(a, sm.tab, base);
+#pragma unroll 1
+        for (int base = 0; base < a.seqs.B; base += kTable) {
+            const int64_t here = fill_table(a, sm.tab, base);
+            if (one_table) total = here;
+            int64_t from, to;
+            share_of(total, blockIdx.x, gridDim.x, from, to);
+            const int64_t lo = (from > seen ? from : seen) - seen, hi = (to < seen + here ? to : seen + here) - seen;
+            seen += here;
+            if (hi <= lo) continue;           // the same for the whole block
+            Walk seg;
+            walk_start(seg, sm.tab.info, sm.tab.prefix, kTable, a.cut, lo, hi - lo);
+            role(seg, base);
+            __syncwarp();
+            block_sync();                     // before the table is filled anew
+        }
+    };
 
     // counters of each role, over all tables
     Ring<kKStages> kr;
@@ -236,19 +256,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t steps = 0, steps1 = 0;           // of a softmax warp's tile; of the first and second tile
     uint32_t outs = 0, k_loads = 0, v_loads = 0;
 
-    for (int base = 0; base < a.seqs.B; base += kTable) {
-        const int64_t here = fill_table(a, sm.tab, base);
-        if (one_table) total = here;
-        int64_t from, to;
-        share_of(total, blockIdx.x, gridDim.x, from, to);
-        const int64_t lo = (from > seen ? from : seen) - seen, hi = (to < seen + here ? to : seen + here) - seen;
-        seen += here;
-        if (hi <= lo) continue;               // the same for the whole block
-        Walk seg;
-        walk_start(seg, sm.tab.info, sm.tab.prefix, kTable, a.cut, lo, hi - lo);
-
-        if (warp < 8) {
-            // ------------------------------------------------------- softmax
+    if (warp < 8) {
+        // ------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        each_table([&](Walk seg, int) {
             const int x = warp / 4, in_tile = (warp % 4) * 32 + lane;
             const uint32_t lanes = tmem + ((uint32_t)(warp % 4) << 21);
             bool ok = true;
@@ -447,10 +458,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 segs += count > 0;
             }
-        } else if (warp < 10) {
-            // ------------------------------------------------- values to f16
-            const int id = tid - 256;         // this thread takes keys id and id + 64 of a step
-            bool ok = true;                   // after a wait that gave up both warps go on to the barriers, without work
+        });
+    } else if (warp < 12) {
+        // ------------------------------------------------- values to f16
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        each_table([&](Walk seg, int base) {
+            const int id = tid - 256;         // this thread's key of a step
+            bool ok = true;                   // after a wait that gave up all go on to the barriers, without work
             for (; seg.left > 0; walk_next(seg, sm.tab.info, a.cut)) {
                 const SeqInfo info = sm.tab.info[seg.b];
                 int key0, keys;
@@ -459,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int slot = segs++ % kSegs, P = a.seqs.page_tokens;
                 const int32_t* row = a.seqs.table + (int64_t)(base + seg.b) * a.seqs.width;
                 float most = 0.0f;
-                for (int i = key0 / P + id; i * P < keys; i += 64) {
+                for (int i = key0 / P + id; i * P < keys; i += 128) {
                     const int page = __ldg(row + i);
                     if (page >= 0 && page < a.seqs.num_pages)
                         most = fmaxf(most, __ldg(a.v_scale + (int64_t)page * a.cut.heads + seg.head));
@@ -467,12 +481,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
                 if (lane == 0) sm.red[warp - 8] = most;
-                for (int i = id; i < D; i += 64) sm.nan_key[slot][i] = 0x7fffffff;
+                for (int i = id; i < D; i += 128) sm.nan_key[slot][i] = 0x7fffffff;
                 if (id == 0) sm.has_nan[slot] = 0;
-                named_bar_sync(1, 64);
-                most = fmaxf(sm.red[0], sm.red[1]);
+                named_bar_sync(1, 128);
+                most = fmaxf(fmaxf(sm.red[0], sm.red[1]), fmaxf(sm.red[2], sm.red[3]));
                 if (id == 0) sm.ref[slot] = most;
-                named_bar_sync(1, 64);
+                named_bar_sync(1, 128);
                 const float per = most > 0.0f ? kVLift / most : 0.0f;
                 const int all_see = keys_of_row(info, a.cut, seg.tile * kPair);
                 for (int key = key0; ok && key < keys; key += kTile) {
@@ -482,53 +496,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const Meta& meta = sm.v_meta[vr.stage];
                     const uint32_t src = smem_u32(sm.v[vr.stage]), dst = smem_u32(sm.v16[v16r.stage]);
                     const bool some = key + kTile > all_see;          // not every row sees every key of this step
+                    const bool use = ((meta.valid >> (id / 16)) & 1) && key + id < keys;
+                    const float ratio = use ? meta.scale[id / 16] * per : 0.0f;
+                    const bool exact = (__float_as_uint(ratio) & 0x7fffffu) == 0 && ratio >= 5.9604645e-8f;
+                    const uint32_t times = pack_f16x2(ratio, ratio);
 #pragma unroll 1
-                    for (int key_in = id; key_in < kTile; key_in += 64) {
-                        const bool use = ((meta.valid >> (key_in / 16)) & 1) && key + key_in < keys;
-                        const float ratio = use ? meta.scale[key_in / 16] * per : 0.0f;
-                        const bool exact = (__float_as_uint(ratio) & 0x7fffffu) == 0 && ratio >= 5.9604645e-8f;
-                        const uint32_t times = pack_f16x2(ratio, ratio);
-#pragma unroll 2
-                        for (int c = 0; c < D / 16; ++c) {
-                            const uint4 u = lds128(src + chunk_at<D>(key_in, c));
-                            uint32_t w[4] = {u.x, u.y, u.z, u.w}, h[8];
+                    for (int c0 = 0; c0 < D / 16; c0 += 4) {
+                        uint4 u[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) u[i] = lds128(src + chunk_at<D>(id, c0 + i));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int c = c0 + i;
+                            uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, h[8];
                             if (!use) w[0] = w[1] = w[2] = w[3] = 0;
                             if (some) {
                                 // NaN must reach only the rows that see this key, but 0 * NaN is
                                 // NaN: it is taken out here and put back as the rows go out
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const uint32_t n = nan_bytes(w[i]);
+                                for (int k = 0; k < 4; ++k) {
+                                    const uint32_t n = nan_bytes(w[k]);
                                     if (n) {
                                         sm.has_nan[slot] = 1;
                                         for (int b = 0; b < 4; ++b)
                                             if ((n >> (8 * b)) & 0x80u) {
-                                                atomicMin(&sm.nan_key[slot][16 * c + 4 * i + b], key + key_in);
-                                                w[i] &= ~(0xffu << (8 * b));
+                                                atomicMin(&sm.nan_key[slot][16 * c + 4 * k + b], key + id);
+                                                w[k] &= ~(0xffu << (8 * b));
                                             }
                                     }
                                 }
                             }
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                h[2 * i] = cvt_lo(w[i]);
-                                h[2 * i + 1] = cvt_hi(w[i]);
+                            for (int k = 0; k < 4; ++k) {
+                                h[2 * k] = cvt_lo(w[k]);
+                                h[2 * k + 1] = cvt_hi(w[k]);
                             }
                             if (exact) {          // a power of two: one rounding at most, in f16's subnormals
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) h[i] = mul_f16x2(h[i], times);
+                                for (int k = 0; k < 8; ++k) h[k] = mul_f16x2(h[k], times);
                             } else {
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-                                    h[i] = pack_f16x2(y.x * ratio, y.y * ratio);
+                                for (int k = 0; k < 8; ++k) {
+                                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+                                    h[k] = pack_f16x2(y.x * ratio, y.y * ratio);
                                 }
                             }
                             // 64 dims of a key are one 128-byte row, swizzled; the next 64 dims follow all keys
-                            const uint32_t to_row = dst + (c / 4) * (kTile * 128) + key_in * 128;
+                            const uint32_t to_row = dst + (c / 4) * (kTile * 128) + id * 128;
                             const int c16 = (2 * c) % 8;
-                            sts128(to_row + ((c16 ^ (key_in & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
-                            sts128(to_row + (((c16 + 1) ^ (key_in & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
+                            sts128(to_row + ((c16 ^ (id & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+                            sts128(to_row + (((c16 + 1) ^ (id & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
                         }
                     }
                     fence_proxy_async_smem();
@@ -541,150 +558,160 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v16r.next();
                 }
             }
-        } else if (warp == 10) {
+        });
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == 12) {
             // ----------------------------------------------------------- TMA
-            const int P = a.seqs.page_tokens, per_box = P / 16;
-            bool ok = true;
-            for (; ok && seg.left > 0; walk_next(seg, sm.tab.info, a.cut)) {
-                int key0, keys;
-                segment_keys(seg, sm.tab.info, a.cut, key0, keys);
-                const int32_t* row = a.seqs.table + (int64_t)(base + seg.b) * a.seqs.width;
-                auto page_at = [&](int key) { return lane < 8 && key + 16 * lane < keys ? __ldg(row + (key + 16 * lane) / P) : -1; };
-                int page = page_at(key0);
-                for (int key = key0; key < keys; key += kTile) {
-                    const int ahead = page_at(key + kTile);
-                    const bool has = page >= 0 && page < a.seqs.num_pages;
-                    if (lane < 8 && key + 16 * lane < keys && !has) atomicOr(&g_device_status, kIndexError);
-                    const uint32_t valid = __ballot_sync(0xffffffffu, lane < 8 && has);
-                    const bool box = lane < 8 && has && lane % per_box == 0;
-                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box)) * P * D;
-                    const int block = has ? page * a.cut.heads + seg.head : 0;
+            each_table([&](Walk seg, int base) {
+                const int P = a.seqs.page_tokens, per_box = P / 16;
+                bool ok = true;
+                for (; ok && seg.left > 0; walk_next(seg, sm.tab.info, a.cut)) {
+                    int key0, keys;
+                    segment_keys(seg, sm.tab.info, a.cut, key0, keys);
+                    const int32_t* row = a.seqs.table + (int64_t)(base + seg.b) * a.seqs.width;
+                    auto page_at = [&](int key) {   // of this lane's 16 keys of a step
+                        return lane < 8 && key + 16 * lane < keys ? __ldg(row + (key + 16 * lane) / P) : -1;
+                    };
+                    int page = page_at(key0);
+                    for (int key = key0; key < keys; key += kTile) {
+                        const int ahead = page_at(key + kTile);
+                        const bool has = page >= 0 && page < a.seqs.num_pages;
+                        if (lane < 8 && key + 16 * lane < keys && !has) atomicOr(&g_device_status, kIndexError);
+                        const uint32_t valid = __ballot_sync(0xffffffffu, lane < 8 && has);
+                        const bool box = lane < 8 && has && lane % per_box == 0;
+                        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box)) * P * D;
+                        const int block = has ? page * a.cut.heads + seg.head : 0;
 
-                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.k_empty[kr.stage], kr.phase ^ 1, &sm.abort));
-                    if (!ok) break;
-                    if (lane == 0) {
-                        sm.k_meta[mr.stage].valid = valid;
-                        mbar_arrive_expect_tx(&sm.k_full[kr.stage], bytes);
-                    }
-                    __syncwarp();
-                    if (lane < 8) {
-                        if (has) copy_async4(&sm.k_meta[mr.stage].scale[lane], a.k_scale + block);
-                        arrive_after_copies(&sm.k_full[kr.stage]);
-                    }
-                    if (box) tma_load_3d(sm.k[kr.stage] + lane * 16 * D, &k_map, 0, 0, block, &sm.k_full[kr.stage]);
-                    ++k_loads;
-                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.v_empty[vr.stage], vr.phase ^ 1, &sm.abort));
-                    if (!ok) break;
-                    if (lane == 0) {
-                        sm.v_meta[vr.stage].valid = valid;
-                        mbar_arrive_expect_tx(&sm.v_full[vr.stage], bytes);
-                    }
-                    __syncwarp();
-                    if (lane < 8) {
-                        if (has) copy_async4(&sm.v_meta[vr.stage].scale[lane], a.v_scale + block);
-                        arrive_after_copies(&sm.v_full[vr.stage]);
-                    }
-                    if (box) tma_load_3d(sm.v[vr.stage] + lane * 16 * D, &v_map, 0, 0, block, &sm.v_full[vr.stage]);
-                    ++v_loads;
-                    kr.next();
-                    mr.next();
-                    vr.next();
-                    page = ahead;
-                }
-            }
-        } else if (lane == 0) {
-            // ------------------------------------------- tensor instructions
-            auto product_s = [&](int x, int stage) {
-                const uint64_t kd = smem_desc(smem_u32(sm.k[stage]), 16, D * 8, D == 128 ? 2 : 4);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint64_t qd = smem_desc(smem_u32(sm.q[x][h]), 16, D * 8, D == 128 ? 2 : 4);
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i)
-                        mma_e4m3(tmem + col_s(x), qd + 2 * i, kd + 2 * i, kIdescS, h + i > 0);
-                }
-            };
-            auto product_o = [&](int x, int stage, bool more) {
-                // values: dims contiguous ("MN-major"); 64 dims a 128-byte row, 8 keys an atom, 64 further dims 16 KB on
-                const uint64_t vd = smem_desc(smem_u32(sm.v16[stage]), kTile * 128, 1024, 2);
-#pragma unroll
-                for (int i = 0; i < kTile / 16; ++i)
-                    mma_f16_ts(tmem + col_o<D>(x), tmem + col_s(x) + 8 * i, vd + 128 * i, kIdescO, more || i > 0);
-            };
-            bool ok = true;
-            for (; ok && seg.left > 0; walk_next(seg, sm.tab.info, a.cut)) {
-                int key0, keys;
-                segment_keys(seg, sm.tab.info, a.cut, key0, keys);
-                const bool two = sm.tab.info[seg.b].rows - seg.tile * kPair > kTile;
-                const int count = (keys - key0 + kTile - 1) / kTile;
-                if (count == 0) continue;
-                ok = mbar_wait(&sm.q_full[0], segs & 1, &sm.abort) &&
-                     mbar_wait(&sm.k_full[kr.stage], kr.phase, &sm.abort);
-                if (!ok) break;
-                ++segs;
-                tc_fence_after();
-                product_s(0, kr.stage);
-                mma_commit(&sm.s_full[0]);
-                if (two) {
-                    ok = mbar_wait(&sm.q_full[1], pairs & 1, &sm.abort);
-                    if (!ok) break;
-                    ++pairs;
-                    tc_fence_after();
-                    product_s(1, kr.stage);
-                    mma_commit(&sm.s_full[1]);
-                }
-                mma_commit(&sm.k_empty[kr.stage]);
-                kr.next();
-                for (int j = 0; j < count; ++j) {
-                    const bool more = j + 1 < count;
-                    ok = mbar_wait(&sm.v16_full[v16r.stage], v16r.phase, &sm.abort) &&
-                         mbar_wait(&sm.p_full[0], steps & 1, &sm.abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                    product_o(0, v16r.stage, j > 0);
-                    if (!more) mma_commit(&sm.o_full[0]);
-                    if (more) {
-                        ok = mbar_wait(&sm.k_full[kr.stage], kr.phase, &sm.abort);
+                        ok = __all_sync(0xffffffffu, mbar_wait(&sm.k_empty[kr.stage], kr.phase ^ 1, &sm.abort));
                         if (!ok) break;
-                        tc_fence_after();
-                        product_s(0, kr.stage);
-                        mma_commit(&sm.s_full[0]);
-                    }
-                    if (two) {
-                        ok = mbar_wait(&sm.p_full[1], steps1 & 1, &sm.abort);
-                        if (!ok) break;
-                        ++steps1;
-                        tc_fence_after();
-                        product_o(1, v16r.stage, j > 0);
-                        if (!more) mma_commit(&sm.o_full[1]);
-                        mma_commit(&sm.v16_empty[v16r.stage]);
-                        if (more) {
-                            product_s(1, kr.stage);
-                            mma_commit(&sm.s_full[1]);
+                        if (lane == 0) {
+                            sm.k_meta[mr.stage].valid = valid;
+                            mbar_arrive_expect_tx(&sm.k_full[kr.stage], bytes);
                         }
-                    } else {
-                        mma_commit(&sm.v16_empty[v16r.stage]);
-                    }
-                    if (more) {
-                        mma_commit(&sm.k_empty[kr.stage]);
+                        __syncwarp();
+                        if (lane < 8) {
+                            if (has) copy_async4(&sm.k_meta[mr.stage].scale[lane], a.k_scale + block);
+                            arrive_after_copies(&sm.k_full[kr.stage]);
+                        }
+                        if (box) tma_load_3d(sm.k[kr.stage] + lane * 16 * D, &k_map, 0, 0, block, &sm.k_full[kr.stage]);
+                        ++k_loads;
+                        ok = __all_sync(0xffffffffu, mbar_wait(&sm.v_empty[vr.stage], vr.phase ^ 1, &sm.abort));
+                        if (!ok) break;
+                        if (lane == 0) {
+                            sm.v_meta[vr.stage].valid = valid;
+                            mbar_arrive_expect_tx(&sm.v_full[vr.stage], bytes);
+                        }
+                        __syncwarp();
+                        if (lane < 8) {
+                            if (has) copy_async4(&sm.v_meta[vr.stage].scale[lane], a.v_scale + block);
+                            arrive_after_copies(&sm.v_full[vr.stage]);
+                        }
+                        if (box) tma_load_3d(sm.v[vr.stage] + lane * 16 * D, &v_map, 0, 0, block, &sm.v_full[vr.stage]);
+                        ++v_loads;
                         kr.next();
+                        mr.next();
+                        vr.next();
+                        page = ahead;
                     }
-                    v16r.next();
-                    ++steps;
                 }
-            }
+            });
+        } else if (warp == 13) {
+            // ------------------------------------------- tensor instructions
+            each_table([&](Walk seg, int) {
+                if (lane > 0) return;
+                auto product_s = [&](int x, int stage) {
+                    const uint64_t kd = smem_desc(smem_u32(sm.k[stage]), 16, D * 8, D == 128 ? 2 : 4);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint64_t qd = smem_desc(smem_u32(sm.q[x][h]), 16, D * 8, D == 128 ? 2 : 4);
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i)
+                            mma_e4m3(tmem + col_s(x), qd + 2 * i, kd + 2 * i, kIdescS, h + i > 0);
+                    }
+                };
+                auto product_o = [&](int x, int stage, bool more) {
+                    // values: dims contiguous ("MN-major"); 64 dims a 128-byte row, 8 keys an atom, 64 further dims 16 KB on
+                    const uint64_t vd = smem_desc(smem_u32(sm.v16[stage]), kTile * 128, 1024, 2);
+#pragma unroll
+                    for (int i = 0; i < kTile / 16; ++i)
+                        mma_f16_ts(tmem + col_o<D>(x), tmem + col_s(x) + 8 * i, vd + 128 * i, kIdescO, more || i > 0);
+                };
+                bool ok = true;
+                for (; ok && seg.left > 0; walk_next(seg, sm.tab.info, a.cut)) {
+                    int key0, keys;
+                    segment_keys(seg, sm.tab.info, a.cut, key0, keys);
+                    const bool two = sm.tab.info[seg.b].rows - seg.tile * kPair > kTile;
+                    const int count = (keys - key0 + kTile - 1) / kTile;
+                    if (count == 0) continue;
+                    ok = mbar_wait(&sm.q_full[0], segs & 1, &sm.abort) &&
+                         mbar_wait(&sm.k_full[kr.stage], kr.phase, &sm.abort);
+                    if (!ok) break;
+                    ++segs;
+                    tc_fence_after();
+                    product_s(0, kr.stage);
+                    mma_commit(&sm.s_full[0]);
+                    if (two) {
+                        ok = mbar_wait(&sm.q_full[1], pairs & 1, &sm.abort);
+                        if (!ok) break;
+                        ++pairs;
+                        tc_fence_after();
+                        product_s(1, kr.stage);
+                        mma_commit(&sm.s_full[1]);
+                    }
+                    mma_commit(&sm.k_empty[kr.stage]);
+                    kr.next();
+                    for (int j = 0; j < count; ++j) {
+                        const bool more = j + 1 < count;
+                        ok = mbar_wait(&sm.v16_full[v16r.stage], v16r.phase, &sm.abort) &&
+                             mbar_wait(&sm.p_full[0], steps & 1, &sm.abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        product_o(0, v16r.stage, j > 0);
+                        if (!more) mma_commit(&sm.o_full[0]);
+                        if (more) {
+                            ok = mbar_wait(&sm.k_full[kr.stage], kr.phase, &sm.abort);
+                            if (!ok) break;
+                            tc_fence_after();
+                            product_s(0, kr.stage);
+                            mma_commit(&sm.s_full[0]);
+                        }
+                        if (two) {
+                            ok = mbar_wait(&sm.p_full[1], steps1 & 1, &sm.abort);
+                            if (!ok) break;
+                            ++steps1;
+                            tc_fence_after();
+                            product_o(1, v16r.stage, j > 0);
+                            if (!more) mma_commit(&sm.o_full[1]);
+                            mma_commit(&sm.v16_empty[v16r.stage]);
+                            if (more) {
+                                product_s(1, kr.stage);
+                                mma_commit(&sm.s_full[1]);
+                            }
+                        } else {
+                            mma_commit(&sm.v16_empty[v16r.stage]);
+                        }
+                        if (more) {
+                            mma_commit(&sm.k_empty[kr.stage]);
+                            kr.next();
+                        }
+                        v16r.next();
+                        ++steps;
+                    }
+                }
+            });
+        } else {
+            each_table([](Walk, int) {});
         }
-        __syncwarp();
-        __syncthreads();                      // before the table is filled anew
     }
 
     // Everything asynchronous has ended before the block does: the products by
     // their last commit, and, after a wait that gave up, the loads under way.
-    if (warp == 11 && lane == 0) {
+    if (warp == 13 && lane == 0) {
         mma_commit(&sm.done);
         mbar_wait_drain(&sm.done, 0);
     }
-    if (warp == 10 && lane == 0 && sm.abort) {
+    if (warp == 12 && lane == 0 && sm.abort) {
         for (uint32_t i = k_loads > kKStages ? k_loads - kKStages : 0; i < k_loads; ++i)
             mbar_wait_drain(&sm.k_full[i % kKStages], (i / kKStages) & 1);
         for (uint32_t i = v_loads > kVStages ? v_loads - kVStages : 0; i < v_loads; ++i)
@@ -694,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 11) tmem_dealloc(tmem, 512);
+    if (warp == 13) tmem_dealloc(tmem, 512);
 }
 
 template <int D>
