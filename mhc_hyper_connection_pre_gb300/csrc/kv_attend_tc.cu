@@ -26,8 +26,8 @@
 // other's products do.  The conversion is shared by the two tiles.
 //
 // Warps 0-3 and 4-7: softmax of the two tiles; 8-11: V to f16; 12: TMA loads;
-// 13: the tensor instructions.  The softmax gets 176 registers a thread and the
-// others 80 of the 128 that 16 warps start with.
+// 13: the tensor instructions.  The softmax gets 152 registers a thread and the
+// others 104 of the 128 that 16 warps start with.
 #include "kv_attend.cuh"
 
 namespace mhc {
@@ -141,53 +141,65 @@ struct Ring {
     }
 };
 
-template <bool kMask>
-__device__ __forceinline__ float row_max(const uint32_t (&s)[32], int at, const Meta& meta, float f, int n,
-                                         uint32_t valid) {
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+// The bits of keys at .. at + 31 of a step that the row sees: those before the
+// n-th, in blocks of 16 that have a page.
+__device__ __forceinline__ uint32_t seen_bits(int at, int n, uint32_t valid) {
+    const int k = n - at;
+    const uint32_t v = valid >> (at / 16);
+    const uint32_t pages = ((v & 1) ? 0xffffu : 0u) | ((v & 2) ? 0xffff0000u : 0u);
+    return k <= 0 ? 0u : (k >= 32 ? pages : pages & ((1u << k) - 1));
+}
+
+// The factor that makes a row's products with 16 keys logits in powers of two.
+// Above zero, so that what is hidden stays minus infinity (a scale of zero
+// makes logits of 1e-30 instead).
+__device__ __forceinline__ float factor(const Meta& meta, int block, float f) {
+    return fmaxf(f * meta.scale[block], 1e-37f);
+}
+
+// The largest of 32 logits: scales are not negative, so the largest product
+// times the factor.
+__device__ __forceinline__ float row_max(const uint32_t (&s)[32], int at, const Meta& meta, float f) {
     float top = -INFINITY;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const float x = f * meta.scale[at / 16 + h];
-        float m = -INFINITY;
-        if (kMask) {
-            const bool has = (valid >> (at / 16 + h)) & 1;
+        float m = __uint_as_float(s[16 * h]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                m = fmaxf(m, has && at + 16 * h + i < n ? __uint_as_float(s[16 * h + i]) * x : -INFINITY);
-            top = fmaxf(top, m);
-        } else {                              // scales are not negative: the largest product is the largest times x
-#pragma unroll
-            for (int i = 0; i < 16; ++i) m = fmaxf(m, __uint_as_float(s[16 * h + i]));
-            top = fmaxf(top, m * x);
-        }
+        for (int i = 1; i < 16; ++i) m = fmaxf(m, __uint_as_float(s[16 * h + i]));
+        top = fmaxf(top, m * factor(meta, at / 16 + h, f));
     }
     return top;
 }
 
-// 32 weights of a row, as 16 pairs of f16, and their sum.
-template <bool kMask>
-__device__ __forceinline__ float weights(const uint32_t (&s)[32], uint32_t (&p)[16], int at, const Meta& meta, float f,
-                                         float zero, int n, uint32_t valid) {
-    float sum = 0.0f;
+// 32 weights of a row, as 16 pairs of f16, added to the row's two sums.
+__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t (&p)[16], int at, const Meta& meta, float f,
+                                        float zero, f32x2& sum) {
+    const f32x2 z = make_f32x2(-zero, -zero);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const float x = f * meta.scale[at / 16 + h];
-        const bool has = !kMask || ((valid >> (at / 16 + h)) & 1);
-        float part = 0.0f;
+        const float x = factor(meta, at / 16 + h, f);
+        const f32x2 xx = make_f32x2(x, x);
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-            float a = ex2(fmaf(__uint_as_float(s[16 * h + i]), x, -zero));
-            float b = ex2(fmaf(__uint_as_float(s[16 * h + i + 1]), x, -zero));
-            if (kMask) {
-                a = has && at + 16 * h + i < n ? a : 0.0f;
-                b = has && at + 16 * h + i + 1 < n ? b : 0.0f;
-            }
-            part += a + b;
+            float a, b;
+            split_f32x2(fma2(make_f32x2(__uint_as_float(s[16 * h + i]), __uint_as_float(s[16 * h + i + 1])), xx, z), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            sum = add2(sum, make_f32x2(a, b));
             p[8 * h + i / 2] = pack_f16x2(a, b);
         }
-        sum += part;
     }
-    return sum;
 }
 
 template <int D>
@@ -258,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 8) {
         // ------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         each_table([&](Walk seg, int) {
             const int x = warp / 4, in_tile = (warp % 4) * 32 + lane;
             const uint32_t lanes = tmem + ((uint32_t)(warp % 4) << 21);
@@ -271,60 +283,67 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int key0, keys;
                 segment_keys(seg, sm.tab.info, a.cut, key0, keys);
                 const int count = (keys - key0 + kTile - 1) / kTile;  // 0: a tile without keys
-                float f = 0.0f;
+                float f = 0.0f, m = -INFINITY, l = 0.0f;
                 int lim = 0;
                 if (active && count > 0) {
-                    // this thread's query row as hi + lo
-                    uint4 u[D / 8];
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) u[i] = make_uint4(0, 0, 0, 0);
+                    // this thread's query row as hi + lo: once over it for its largest
+                    // element, once more (from the cache) to split it, as the whole row
+                    // would not fit the registers
+                    const uint4* src = nullptr;
                     if (mine < rows) {
                         const int r = first_row + mine;
                         lim = keys_of_row(info, a.cut, r);
-                        const uint4* src = reinterpret_cast<const uint4*>(
-                            a.q + (info.begin + r / a.cut.group) * a.q_stride +
-                            (int64_t)(seg.head * a.cut.group + r % a.cut.group) * D);
-#pragma unroll
-                        for (int i = 0; i < D / 8; ++i) u[i] = __ldg(src + i);
+                        src = reinterpret_cast<const uint4*>(a.q + (info.begin + r / a.cut.group) * a.q_stride +
+                                                             (int64_t)(seg.head * a.cut.group + r % a.cut.group) * D);
                     }
+                    auto load = [&](int i) { return src ? __ldg(src + i) : make_uint4(0, 0, 0, 0); };
                     float top = 0.0f;
+#pragma unroll 1
+                    for (int i = 0; i < D / 8; i += 8) {
+                        uint4 u[8];
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        float y[8];
-                        unpack8(u[i], y);
+                        for (int j = 0; j < 8; ++j) u[j] = load(i + j);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[j]));
+                        for (int j = 0; j < 8; ++j) {
+                            float y[8];
+                            unpack8(u[j], y);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(y[k]));
+                        }
                     }
                     int e = 134 - (int)(__float_as_uint(top) >> 23);  // 7 - floor(log2(top))
                     e = e < -120 ? -120 : (e > 120 ? 120 : e);
                     const float up = __uint_as_float((uint32_t)(127 + e) << 23);
                     f = __uint_as_float((uint32_t)(127 - e) << 23) * a.scale_log2;
-                    if (top == INFINITY) f = __int_as_float(0x7fc00000);   // e4m3 has no infinity: such a row is NaN
+                    if (top == INFINITY) l = __int_as_float(0x7fc00000);   // e4m3 has no infinity: such a row is NaN
                     const uint32_t hi_at = smem_u32(sm.q[x][0]), lo_at = smem_u32(sm.q[x][1]);
-#pragma unroll
+                    uint4 u[2] = {load(0), load(1)};
+#pragma unroll 1
                     for (int c = 0; c < D / 16; ++c) {
-                        uint32_t h[4], l[4];
+                        uint32_t hi[4], rest[4];
+                        const uint4 now[2] = {u[0], u[1]};
+                        if (c + 1 < D / 16) u[0] = load(2 * c + 2), u[1] = load(2 * c + 3);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             float y[8], z[8];
-                            unpack8(u[2 * c + i], y);
+                            unpack8(now[i], y);
 #pragma unroll
                             for (int j = 0; j < 8; ++j) y[j] *= up;
-                            h[2 * i] = e4m3x4(y, 0);
-                            h[2 * i + 1] = e4m3x4(y, 4);
+                            hi[2 * i] = e4m3x4(y, 0);
+                            hi[2 * i + 1] = e4m3x4(y, 4);
 #pragma unroll
                             for (int j = 0; j < 8; j += 2) {
-                                const uint32_t w = h[2 * i + j / 4];
+                                const uint32_t w = hi[2 * i + j / 4];
                                 const uint32_t b = j % 4 ? cvt_hi(w) : cvt_lo(w);
                                 const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&b));
                                 z[j] = y[j] - back.x;
                                 z[j + 1] = y[j + 1] - back.y;
                             }
-                            l[2 * i] = e4m3x4(z, 0);
-                            l[2 * i + 1] = e4m3x4(z, 4);
+                            rest[2 * i] = e4m3x4(z, 0);
+                            rest[2 * i + 1] = e4m3x4(z, 4);
                         }
-                        sts128(hi_at + chunk_at<D>(in_tile, c), make_uint4(h[0], h[1], h[2], h[3]));
-                        sts128(lo_at + chunk_at<D>(in_tile, c), make_uint4(l[0], l[1], l[2], l[3]));
+                        sts128(hi_at + chunk_at<D>(in_tile, c), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                        sts128(lo_at + chunk_at<D>(in_tile, c), make_uint4(rest[0], rest[1], rest[2], rest[3]));
                     }
                     fence_proxy_async_smem();
                 }
@@ -334,7 +353,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(&sm.q_full[x]);
                 }
 
-                float m = -INFINITY, l = 0.0f;
                 const int all_see = keys_of_row(info, a.cut, first_row + x * kTile);
                 for (int j = 0; j < count; ++j, mr.next()) {
                     if (!active) continue;
@@ -346,46 +364,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t valid = meta.valid;
                     const int n = lim - (key0 + j * kTile);   // keys of this step that the row sees
                     const bool mask = key0 + (j + 1) * kTile > all_see || valid != 0xffu;
-                    float top = -INFINITY;
-#pragma unroll 1                                  // rolled, here and below: the roles' code has to fit the instruction cache
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t s[32];
-                        tmem_ld32(lanes + col_s(x) + c * 32, s);
-                        tmem_wait_ld();
-                        tmem_regs_ready(s);
-                        if (mask) top = fmaxf(top, row_max<true>(s, c * 32, meta, f, n, valid));
-                        else top = fmaxf(top, row_max<false>(s, c * 32, meta, f, n, valid));
-                    }
-                    const bool grow = top > m + kGrow;
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float now = grow ? top : m;
-                        const float keep = grow ? ex2(m - now) : 1.0f;
-                        m = now;
-                        l *= keep;
-                        if (j > 0) {          // this tile's products up to now are done: S came after them
+                    // The row's 128 products, 64 at a time: their largest, the weights and
+                    // their sum.  P takes the first half of S's columns, behind the reads.
+                    f32x2 sum = make_f32x2(0.0f, 0.0f);
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tmem_ld32(lanes + col_o<D>(x) + c * 32, o);
-                                tmem_wait_ld();
-                                tmem_regs_ready(o);
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t s[2][32];
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                                tmem_st32(lanes + col_o<D>(x) + c * 32, o);
+                        for (int c = 0; c < 2; ++c) tmem_ld32(lanes + col_s(x) + half * 64 + c * 32, s[c]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) tmem_regs_ready(s[c]);
+                        if (mask) {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const uint32_t bits = seen_bits(half * 64 + c * 32, n, valid);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) s[c][i] = (bits >> i) & 1 ? s[c][i] : 0xff800000u;
                             }
                         }
-                    }
-                    const float zero = m == -INFINITY ? 0.0f : m - kLift;
+                        const float top = fmaxf(row_max(s[0], half * 64, meta, f), row_max(s[1], half * 64 + 32, meta, f));
+                        const bool grow = top > m + kGrow;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            const float keep = grow ? ex2(m - top) : 1.0f;
+                            m = grow ? top : m;
+                            l *= keep;
+                            sum = mul_rn2(sum, make_f32x2(keep, keep));
+                            if (half) {       // the weights of the first half
+                                const uint32_t k2 = pack_f16x2(keep, keep);
+                                uint32_t p[32];
+                                tmem_ld32(lanes + col_s(x), p);
+                                tmem_wait_ld();
+                                tmem_regs_ready(p);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) p[i] = mul_f16x2(p[i], k2);
+                                tmem_st32(lanes + col_s(x), p);
+                            }
+                            if (j > 0) {      // this tile's products up to now are done: S came after them
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {             // P takes the first half of S's columns, behind the reads
-                        uint32_t s[32], p[16];
-                        tmem_ld32(lanes + col_s(x) + c * 32, s);
-                        tmem_wait_ld();
-                        tmem_regs_ready(s);
-                        if (mask) l += weights<true>(s, p, c * 32, meta, f, zero, n, valid);
-                        else l += weights<false>(s, p, c * 32, meta, f, zero, n, valid);
-                        tmem_st16(lanes + col_s(x) + c * 16, p);
+                                for (int c = 0; c < D / 32; ++c) {
+                                    uint32_t o[32];
+                                    tmem_ld32(lanes + col_o<D>(x) + c * 32, o);
+                                    tmem_wait_ld();
+                                    tmem_regs_ready(o);
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                                    tmem_st32(lanes + col_o<D>(x) + c * 32, o);
+                                }
+                            }
+                        }
+                        const float zero = m == -INFINITY ? 0.0f : m - kLift;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t p[16];
+                            weights(s[c], p, half * 64 + c * 32, meta, f, zero, sum);
+                            tmem_st16(lanes + col_s(x) + half * 32 + c * 16, p);
+                        }
                     }
+                    float sum0, sum1;
+                    split_f32x2(sum, sum0, sum1);
+                    l += sum0 + sum1;
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -461,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         });
     } else if (warp < 12) {
         // ------------------------------------------------- values to f16
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         each_table([&](Walk seg, int base) {
             const int id = tid - 256;         // this thread's key of a step
             bool ok = true;                   // after a wait that gave up all go on to the barriers, without work
@@ -560,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         });
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp == 12) {
             // ----------------------------------------------------------- TMA
             each_table([&](Walk seg, int base) {
