@@ -112,19 +112,6 @@ __device__ __forceinline__ float scale_for(float a) {
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
-// x / scale; exact as a product where scale is a power of two, which every
-// scale written here is.
-__device__ __forceinline__ void divide(float (&x)[8], float scale) {
-    if ((__float_as_uint(scale) & 0x7fffffu) == 0) {
-        const float r = 1.0f / scale;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= r;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] /= scale;
-    }
-}
-
 template <int GT>
 __device__ __forceinline__ void group_sync(int group) {
     if constexpr (GT > 32) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(GT) : "memory");
@@ -270,13 +257,13 @@ __global__ void __launch_bounds__(GT > 256 ? GT : 256) kv_append_kernel(const Ap
         }
         top = group_max<GT>(top, group, red);
         const float need = scale_for(top), scale = run.slot ? fmaxf(old, need) : need;
+        const float per = 1.0f / scale;               // scales are powers of two: x * per is x / scale
         if (id == 0) *scale_at = scale;               // every thread has read it: group_max was a barrier
 
         auto store = [&](int r, float (&y)[8]) {
             if (r >= n) return;
-            divide(y, scale);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = finite(y[j]) ? y[j] : __int_as_float(0x7fc00000);
+            for (int j = 0; j < 8; ++j) y[j] = finite(y[j]) ? y[j] * per : __int_as_float(0x7fc00000);
             uint2 v;
             v.x = e4m3x4(y, 0);
             v.y = e4m3x4(y, 4);

@@ -36,7 +36,7 @@ constexpr int kSub = 32;                      // keys of one load of one warp
 constexpr int kRing = 24576;                  // bytes of one warp's ring
 constexpr int kPass = 64;                     // dims that warps exchange at a time
 constexpr int kPitch = kPass + 8;             // floats; conflict-free for the fragments' order
-constexpr int kUnit = 64;                     // keys of a unit of work
+constexpr int kUnitLog2 = 6;                  // units of 64 keys
 
 template <int D>
 struct Shape {
@@ -56,7 +56,8 @@ struct __align__(1024) Smem {
     float pass[kWarps][8][kPitch];
     float ml[kWarps][8][2];
     Meta meta[kWarps][Shape<D>::kStages];
-    Table tab;
+    Segment segs[kSegments];
+    int count;                                // of segs
     uint64_t full[kWarps][Shape<D>::kStages];
     int abort;
 };
@@ -78,20 +79,25 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // The loads of one warp, in order: the 32-key pieces of each segment that are
 // this warp's (piece w, w + 8, ... of the segment).
 struct Loads {
-    Walk w;
-    int piece, pieces;                        // of the current segment
-    int keys;                                 // the segment's last key + 1
+    int seg;                                  // index of the segment
+    int key, keys;                            // the piece's first key, the segment's last key + 1
 };
 
-__device__ __forceinline__ void loads_settle(Loads& l, const SeqInfo* info, const Cut& cut, int warp) {
-    while (l.w.left > 0) {                    // on to a segment that has a piece for this warp
-        int key0;
-        segment_keys(l.w, info, cut, key0, l.keys);
-        l.pieces = (l.keys - key0 + kSub - 1) / kSub;
-        if (l.piece < l.pieces) return;
-        l.piece = warp;
-        walk_next(l.w, info, cut);
+__device__ __forceinline__ void loads_settle(Loads& l, const Segment* segs, int count, const Cut& cut, int warp) {
+    while (l.key >= l.keys) {                 // on to a segment that has a piece for this warp
+        if (++l.seg >= count) return;
+        keys_of(segs[l.seg], cut, l.key, l.keys);
+        l.key += warp * kSub;
     }
+}
+
+// Word x of the dims that row group g holds of key r's values.
+template <int D>
+__device__ __forceinline__ uint32_t value_word(uint32_t vs, int r, int g, int x) {
+    const uint32_t at = D == 128 ? r * 128 + ((g ^ (r & 7)) << 4) : r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8;
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(vs + at + 4 * x));
+    return v;
 }
 
 // The 32 keys of one piece against the tile's rows.
@@ -206,8 +212,7 @@ __device__ __forceinline__ void piece(uint32_t ks, uint32_t vs, const Meta& meta
     const float w0 = v0 * inv, w1 = v1 * inv;
 
     constexpr int kVW = D / 32;               // words of a key's values that a thread holds (4 dims each)
-    uint32_t nan_at[kVW * 4];                 // first key with NaN in each of the thread's dims
-    bool nans = false;
+    uint32_t nans = 0;
 #pragma unroll
     for (int mb = 0; mb < 2; ++mb) {
         const float w = mb ? w1 : w0;
@@ -234,36 +239,15 @@ __device__ __forceinline__ void piece(uint32_t ks, uint32_t vs, const Meta& meta
             // bytes are.  NaN among the others must reach only the rows that
             // see its key, but 0 * NaN is NaN: it is taken out here and put
             // back into those rows below.
-            uint32_t found = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = mb * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
                 const uint32_t use = (mb ? has1 : has0) && key0 + r < keys ? 0xffffffffu : 0u;
 #pragma unroll
                 for (int x = 0; x < kVW; ++x) {
-                    v[i][x] &= use;
-                    found |= nan_bytes(v[i][x]);
-                }
-            }
-            if (__any_sync(0xffffffffu, found != 0)) {
-                if (!nans) {
-#pragma unroll
-                    for (int x = 0; x < kVW * 4; ++x) nan_at[x] = 0x7fffffffu;
-                    nans = true;
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = mb * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
-#pragma unroll
-                    for (int x = 0; x < kVW; ++x) {
-                        const uint32_t n = nan_bytes(v[i][x]);
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            if ((n >> (8 * y)) & 0x80u) {
-                                nan_at[4 * x + y] = min(nan_at[4 * x + y], (uint32_t)(key0 + r));
-                                v[i][x] &= ~(0xffu << (8 * y));
-                            }
-                    }
+                    const uint32_t n = nan_bytes(v[i][x]) & use;
+                    nans |= n;
+                    v[i][x] &= use & ~((n >> 7) * 0xffu);
                 }
             }
         }
@@ -280,17 +264,21 @@ __device__ __forceinline__ void piece(uint32_t ks, uint32_t vs, const Meta& meta
                     mma_f16(acc.o[2 * x + y][nb], a[y][0], a[y][1], a[y][2], a[y][3], b[nb][0], b[nb][1]);
         }
     }
-    if (!kFull && nans) {
+    if (!kFull && __any_sync(0xffffffffu, nans != 0)) {
+#pragma unroll 1
+        for (int r = 0; r < kSub && key0 + r < keys; ++r) {
+            if (!(r < 16 ? has0 : has1)) continue;
+            uint32_t v[kVW];                  // this thread's dims of key r
 #pragma unroll
-        for (int x = 0; x < kVW * 4; ++x) {
-            uint32_t n = nan_at[x];
-            n = min(n, __shfl_xor_sync(0xffffffffu, n, 1));
-            n = min(n, __shfl_xor_sync(0xffffffffu, n, 2));
+            for (int x = 0; x < kVW; ++x) v[x] = nan_bytes(value_word<D>(vs, r, g, x));
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int x = 0; x < kVW * 4; ++x)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if ((int)n < lim[nb][e]) acc.o[x / 2][nb][2 * (x & 1) + e] = __int_as_float(0x7fc00000);
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if ((v[x / 4] >> (8 * (x % 4))) & 0x80u && key0 + r < lim[nb][e])
+                            acc.o[x / 2][nb][2 * (x & 1) + e] = __int_as_float(0x7fc00000);
         }
     }
 }
@@ -331,41 +319,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init_cluster();
     }
     if (tid < 2) a.desc[blockIdx.x * 2 + tid].valid = 0;
-    check_offsets(a);
 
-    // this block's part of the line
-    int64_t total = 0;
-    const bool one_table = a.seqs.B <= kTable;
-    if (!one_table)
-        for (int base = 0; base < a.seqs.B; base += kTable) total += fill_table(a, sm.tab, base);
-    int64_t seen = 0;
-    uint32_t issued = 0, waited = 0;          // loads of this warp, over all tables
-    for (int base = 0; base < a.seqs.B; base += kTable) {
-        const int64_t here = fill_table(a, sm.tab, base);
-        if (one_table) total = here;
-        int64_t from, to;
-        share_of(total, blockIdx.x, gridDim.x, from, to);
-        const int64_t lo = (from > seen ? from : seen) - seen, hi = (to < seen + here ? to : seen + here) - seen;
-        seen += here;
-        if (hi <= lo) continue;               // the same for the whole block
+    Planner plan;                             // of the first warp
+    uint32_t issued = 0, waited = 0;          // loads of this warp
+    for (bool begun = false;; begun = true) {
+        if (warp == 0) {
+            if (!begun) plan.begin(a, lane);
+            const int n = plan.next(a, sm.segs, lane);
+            if (lane == 0) sm.count = n;
+        }
+        __syncthreads();
+        const int count = sm.count;
+        if (count == 0) break;
 
-        Loads ld;
-        walk_start(ld.w, sm.tab.info, sm.tab.prefix, kTable, a.cut, lo, hi - lo);
-        Walk seg = ld.w;
-        ld.piece = warp;
-        loads_settle(ld, sm.tab.info, a.cut, warp);
+        Loads ld{-1, 0, 0};
+        loads_settle(ld, sm.segs, count, a.cut, warp);
         int page[2] = {-1, -1};
         auto find_pages = [&] {               // of the next load; used only when it is issued
-            if (ld.w.left <= 0) return;
-            const int key = ld.w.first * kUnit + ld.piece * kSub;
-            const int32_t* row = a.seqs.table + (int64_t)(base + ld.w.b) * a.seqs.width;
-            page[0] = __ldg(row + key / a.seqs.page_tokens);
-            page[1] = key + 16 < ld.keys ? __ldg(row + (key + 16) / a.seqs.page_tokens) : -1;
+            if (ld.seg >= count) return;
+            const int32_t* row = a.seqs.table + (int64_t)sm.segs[ld.seg].b * a.seqs.width;
+            page[0] = __ldg(row + ld.key / a.seqs.page_tokens);
+            page[1] = ld.key + 16 < ld.keys ? __ldg(row + (ld.key + 16) / a.seqs.page_tokens) : -1;
         };
         auto issue = [&] {
-            if (ld.w.left <= 0 || *(volatile int*)&sm.abort) return;
+            if (ld.seg >= count || *(volatile int*)&sm.abort) return;
             const int st = issued % kStages;
-            const int key = ld.w.first * kUnit + ld.piece * kSub, P = a.seqs.page_tokens;
+            const int key = ld.key, P = a.seqs.page_tokens, head = sm.segs[ld.seg].head;
             const bool ok0 = page[0] >= 0 && page[0] < a.seqs.num_pages;
             const bool ok1 = page[1] >= 0 && page[1] < a.seqs.num_pages;
             const bool two = key + 16 < ld.keys;
@@ -375,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane < 4) {
                 const int mb = lane & 1;
                 if (mb ? ok1 : ok0) {
-                    const float* src = (lane < 2 ? a.k_scale : a.v_scale) + (int64_t)page[mb] * a.cut.heads + ld.w.head;
+                    const float* src = (lane < 2 ? a.k_scale : a.v_scale) + (int64_t)page[mb] * a.cut.heads + head;
                     copy_async4(&meta.scale[lane], src);
                 }
                 arrive_after_copies(bar);
@@ -387,37 +366,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (P >= kSub) {              // both halves lie in one page
                     mbar_arrive_expect_tx(bar, ok0 ? kStage : 0);
                     if (ok0) {
-                        const int block = page[0] * a.cut.heads + ld.w.head;
+                        const int block = page[0] * a.cut.heads + head;
                         tma_load_3d(dst, &k_map, 0, key % P, block, bar);
                         tma_load_3d(dst + kStage / 2, &v_map, 0, key % P, block, bar);
                     }
                 } else {
                     mbar_arrive_expect_tx(bar, (ok0 ? kStage / 2 : 0) + (ok1 ? kStage / 2 : 0));
                     if (ok0) {
-                        const int block = page[0] * a.cut.heads + ld.w.head;
+                        const int block = page[0] * a.cut.heads + head;
                         tma_load_3d(dst, &k_map, 0, 0, block, bar);
                         tma_load_3d(dst + kStage / 2, &v_map, 0, 0, block, bar);
                     }
                     if (ok1) {
-                        const int block = page[1] * a.cut.heads + ld.w.head;
+                        const int block = page[1] * a.cut.heads + head;
                         tma_load_3d(dst + kStage / 4, &k_map, 0, 0, block, bar);
                         tma_load_3d(dst + kStage / 2 + kStage / 4, &v_map, 0, 0, block, bar);
                     }
                 }
             }
             ++issued;
-            ld.piece += kWarps;
-            loads_settle(ld, sm.tab.info, a.cut, warp);
+            ld.key += kWarps * kSub;
+            loads_settle(ld, sm.segs, count, a.cut, warp);
             find_pages();
         };
         find_pages();
 #pragma unroll 1
         for (int i = 0; i < kStages; ++i) issue();
 
-        for (; seg.left > 0; walk_next(seg, sm.tab.info, a.cut)) {
-            const SeqInfo info = sm.tab.info[seg.b];
+        for (int index = 0; index < count; ++index) {
+            const Segment seg = sm.segs[index];
+            const SeqInfo info = seg.info;
             int key0, keys;
-            segment_keys(seg, sm.tab.info, a.cut, key0, keys);
+            keys_of(seg, a.cut, key0, keys);
             const int first_row = seg.tile * kRows;
             const int rows = info.rows - first_row < kRows ? info.rows - first_row : kRows;
 
@@ -479,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int key = key0 + warp * kSub; key < keys; key += kWarps * kSub) {
                 const int st = waited % kStages;
                 if (waited == issued) break;  // after a wait that gave up
-                const bool ok = mbar_wait(&sm.full[warp][st], (waited / kStages) & 1, &sm.abort);
+                const bool ok = wait_for(&sm.full[warp][st], (waited / kStages) & 1, &sm.abort);
                 ++waited;
                 if (!ok) break;
                 const uint32_t base_addr = smem_u32(sm.ring[warp] + st * kStage);
@@ -564,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        __syncthreads();                      // before the table is filled anew
+        __syncthreads();                      // before the next segments are planned
     }
     // after a wait that gave up: the loads still under way
     for (; waited != issued; ++waited) mbar_wait_drain(&sm.full[warp][waited % kStages], (waited / kStages) & 1);
@@ -660,7 +640,7 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
     AttendArgs a;
     const int rows = tile_rows(q_heads / heads, seqs.B, seqs.T);
     a.seqs = seqs;
-    a.cut = Cut{heads, q_heads / heads, rows, rows == 256 ? 2 * kUnit : kUnit};
+    a.cut = Cut{heads, q_heads / heads, rows, rows == 256 ? kUnitLog2 + 1 : kUnitLog2};
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     a.q = q;

@@ -1,5 +1,5 @@
 // kv_attend.cuh -- what the kernels of mhc_kv_attend share: their arguments,
-// the table of sequences from which blocks find their part of the work, the
+// how a block finds its part of the work, the
 // parts that cut tiles leave behind, and the tensor maps of the cache.
 #pragma once
 
@@ -12,7 +12,6 @@
 namespace mhc {
 namespace kv {
 
-constexpr int kTable = 256;                   // sequences of a block's table
 constexpr float kLift = 10.0f;                // weights are 2^10 times the softmax's numerators
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -38,11 +37,7 @@ struct AttendArgs {
     PartDesc* desc;                           // [blocks][2]
 };
 
-struct Table {
-    SeqInfo info[kTable];
-    int64_t prefix[kTable];
-    int64_t warp_sum[kTable / 32];
-};
+constexpr int kSegments = 32;                 // of a block that are planned at a time
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -87,51 +82,109 @@ __device__ __forceinline__ void check_offsets(const AttendArgs& a) {
         atomicOr(&g_device_status, kIndexError);
 }
 
+// Finds a block's segments.  Run by one warp, every lane alike but for the
+// sequences it looks up, and kept out of the other warps' code: the kernels'
+// loops have to fit the instruction cache.
+struct Planner {
+    Walk w;
+    int b;                                    // the walk's sequence
+    SeqInfo info;
+    int base;                                 // sequences base .. base + 31 are at hand, one a lane
+    SeqInfo at_hand;
+
+    __device__ __forceinline__ SeqInfo look_up(const AttendArgs& a, int seq) const {
+        return seq < a.seqs.B ? info_of(span_of(a.seqs, seq), a.cut.group) : SeqInfo{0, 0, 0, 0};
+    }
+
+    __device__ __forceinline__ void fetch(const AttendArgs& a, int seq, int lane) {
+        if (seq - base >= 32) {
+            base = seq;
+            at_hand = look_up(a, seq + lane);
+        }
+        const int from = seq - base;
+        info.begin = __shfl_sync(0xffffffffu, at_hand.begin, from);
+        info.rows = __shfl_sync(0xffffffffu, at_hand.rows, from);
+        info.len = __shfl_sync(0xffffffffu, at_hand.len, from);
+        info.before = __shfl_sync(0xffffffffu, at_hand.before, from);
+        b = seq;
+    }
+
+    // Counts the units of all sequences (lane i those of the i-th of 32 equal
+    // parts) and enters the block's share.
+    __device__ void begin(const AttendArgs& a, int lane) {
+        const int each = (a.seqs.B + 31) / 32, first = lane * each;
+        const int end = first + each < a.seqs.B ? first + each : a.seqs.B;
+        int64_t mine = 0;
+        bool bad = false;
+#pragma unroll 1
+        for (int i = first; i < end; ++i) {
+            const Span sp = span_of(a.seqs, i);
+            bad = bad || sp.bad;
+            mine += units_of_seq(info_of(sp, a.cut.group), a.cut);
+        }
+        if (blockIdx.x == 0) {
+            if (lane == 0 && a.seqs.cu) bad = bad || a.seqs.cu[0] != 0 || a.seqs.cu[a.seqs.B] != a.seqs.T;
+            if (bad) atomicOr(&g_device_status, kIndexError);
+        }
+        int64_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += up;
+        }
+        int64_t from, to;
+        share_of(__shfl_sync(0xffffffffu, upto, 31), blockIdx.x, gridDim.x, from, to);
+        w.left = to - from;
+        if (w.left <= 0) return;
+        const int part = __ffs(__ballot_sync(0xffffffffu, upto > from)) - 1;
+        int64_t r = from - __shfl_sync(0xffffffffu, upto - mine, part);
+        base = part * each;
+        at_hand = look_up(a, base + lane);
+#pragma unroll 1
+        for (int i = part * each;; ++i) {
+            fetch(a, i, lane);
+            const int64_t u = units_of_seq(info, a.cut);
+            if (r < u) break;
+            r -= u;
+        }
+        walk_enter(w, info, a.cut, r, w.left);
+    }
+
+    // Up to kSegments further segments; returns how many.
+    __device__ int next(const AttendArgs& a, Segment* out, int lane) {
+        int n = 0;
+#pragma unroll 1
+        while (w.left > 0 && n < kSegments) {
+            if (lane == 0) out[n] = Segment{b, info, w.t.tile, w.head, w.first, w.count, w.t.units};
+            ++n;
+            if (!walk_next(w, info, a.cut) && w.left > 0) {
+                do fetch(a, b + 1, lane);
+                while (info.rows == 0);
+                walk_enter(w, info, a.cut, 0, w.left);
+            }
+        }
+        return n;
+    }
+};
+
+// mbar_wait, with the polling kept to a few instructions: the kernels here
+// have many waits, and their loops have to fit the instruction cache.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    const uint32_t at = smem_u32(bar);
+#pragma unroll 1
+    for (int i = 0; i < kSpinLimit; ++i) {
+        if (mbar_try_wait(at, parity)) return true;
+        if (*abort) return false;
+        if (i > 256) __nanosleep(64);
+    }
+    atomicOr(&g_device_status, kDeviceTimeout);
+    *abort = 1;
+    return false;
+}
+
 // The barrier of the whole block; unlike __syncthreads, it may be met in
 // different places of the code.
 __device__ __forceinline__ void block_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
-
-// Fills the table with sequences base .. base + kTable - 1 and the running sum
-// of their units; returns the units of them all.  Whole block, of at least
-// kTable threads.
-__device__ inline int64_t fill_table(const AttendArgs& a, Table& tab, int base) {
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    int64_t mine = 0, run = 0;
-    if (tid < kTable) {
-        SeqInfo info{0, 0, 0, 0};
-        if (base + tid < a.seqs.B) {
-            const Span sp = span_of(a.seqs, base + tid);
-            if (sp.bad) atomicOr(&g_device_status, kIndexError);
-            info = info_of(sp, a.cut.group);
-            mine = units_of_seq(info, a.cut);
-        }
-        tab.info[tid] = info;
-        run = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, run, o);
-            if (lane >= o) run += up;
-        }
-        if (lane == 31) tab.warp_sum[warp] = run;
-    }
-    block_sync();
-    int64_t before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kTable / 32; ++w) {
-        const int64_t s = tab.warp_sum[w];
-        if (w < warp) before += s;
-        total += s;
-    }
-    if (tid < kTable) tab.prefix[tid] = before + run - mine;
-    block_sync();
-    return total;
-}
-
-__device__ __forceinline__ void segment_keys(const Walk& w, const SeqInfo* info, const Cut& cut, int& key0, int& keys) {
-    const int all = keys_of_tile(info[w.b], cut, w.tile), end = (w.first + w.count) * cut.unit;
-    key0 = w.first * cut.unit;
-    keys = end < all ? end : all;
-}
 
 // Row `row` of a sequence (new token row / group, query head row % group of
 // the key/value head): its place in out and lse.

@@ -26,7 +26,7 @@
 // other's products do.  The conversion is shared by the two tiles.
 //
 // Warps 0-3 and 4-7: softmax of the two tiles; 8-11: V to f16; 12: TMA loads;
-// 13: the tensor instructions.  The softmax gets 152 registers a thread and the
+// 13: the tensor instructions; 14: planning.  The softmax gets 152 registers a thread and the
 // others 104 of the 128 that 16 warps start with.
 #include "kv_attend.cuh"
 
@@ -56,7 +56,8 @@ struct __align__(1024) Smem {
     uint8_t k[kKStages][kTile * D];
     uint8_t v[kVStages][kTile * D];           // as stored
     uint8_t v16[2][kTile * D * 2];            // f16: 64 dims of every key, then the next 64
-    Table tab;
+    Segment segs[kSegments];
+    int count;                                // of segs
     Meta k_meta[kMetas];
     Meta v_meta[kVStages];
     int nan_key[kSegs][D];                    // first key with NaN in each dim, among those that not every row sees
@@ -229,37 +230,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 13) tmem_alloc(&sm.tmem, 512);
     if (tid < 2) a.desc[blockIdx.x * 2 + tid].valid = 0;
-    check_offsets(a);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    // Runs a role over this block's segments, table by table.  Each role has its
-    // own copy of this loop, inside its own register budget.
-    auto each_table = [&](auto&& role) {
-        int64_t total = 0, seen = 0;
-        const bool one_table = a.seqs.B <= kTable;
-        if (!one_table)
+    // Runs a role over this block's segments, kSegments at a time; `plan` finds
+    // them (warp 14).
+    auto each_segments = [&](auto&& plan, auto&& role) {
 #pragma unroll 1
-            for (int base = 0; base < a.seqs.B; base += kTable) total += fill_table(a, sm.tab, base);
-#pragma unroll 1
-        for (int base = 0; base < a.seqs.B; base += kTable) {
-            const int64_t here = fill_table(a, sm.tab, base);
-            if (one_table) total = here;
-            int64_t from, to;
-            share_of(total, blockIdx.x, gridDim.x, from, to);
-            const int64_t lo = (from > seen ? from : seen) - seen, hi = (to < seen + here ? to : seen + here) - seen;
-            seen += here;
-            if (hi <= lo) continue;           // the same for the whole block
-            Walk seg;
-            walk_start(seg, sm.tab.info, sm.tab.prefix, kTable, a.cut, lo, hi - lo);
-            role(seg, base);
+        for (;;) {
+            plan();
+            block_sync();
+            if (sm.count == 0) break;
+            role();
             __syncwarp();
-            block_sync();                     // before the table is filled anew
+            block_sync();                     // before the next segments are planned
         }
     };
+    const auto others = [] {};
 
-    // counters of each role, over all tables
+    // counters of each role, over all segments
     Ring<kKStages> kr;
     Ring<kMetas> mr;
     Ring<kVStages> vr;
@@ -271,17 +261,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 8) {
         // ------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-        each_table([&](Walk seg, int) {
+        each_segments(others, [&] {
             const int x = warp / 4, in_tile = (warp % 4) * 32 + lane;
             const uint32_t lanes = tmem + ((uint32_t)(warp % 4) << 21);
             bool ok = true;
-            for (; ok && seg.left > 0; walk_next(seg, sm.tab.info, a.cut)) {
-                const SeqInfo info = sm.tab.info[seg.b];
+            for (int index = 0; ok && index < sm.count; ++index) {
+                const Segment seg = sm.segs[index];
+                const SeqInfo info = seg.info;
                 const int first_row = seg.tile * kPair, rows = min(info.rows - first_row, kPair);
                 const int mine = x * kTile + in_tile;                // of the block's rows
                 const bool active = x == 0 || rows > kTile;
                 int key0, keys;
-                segment_keys(seg, sm.tab.info, a.cut, key0, keys);
+                keys_of(seg, a.cut, key0, keys);
                 const int count = (keys - key0 + kTile - 1) / kTile;  // 0: a tile without keys
                 float f = 0.0f, m = -INFINITY, l = 0.0f;
                 int lim = 0;
@@ -356,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int all_see = keys_of_row(info, a.cut, first_row + x * kTile);
                 for (int j = 0; j < count; ++j, mr.next()) {
                     if (!active) continue;
-                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[x], steps & 1, &sm.abort));
+                    ok = __all_sync(0xffffffffu, wait_for(&sm.s_full[x], steps & 1, &sm.abort));
                     if (!ok) break;
                     ++steps;
                     tc_fence_after();
@@ -449,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     a.desc[blockIdx.x * 2 + slot] = d;
                 }
                 if (count > 0) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_full[x], outs & 1, &sm.abort));
+                    ok = __all_sync(0xffffffffu, wait_for(&sm.o_full[x], outs & 1, &sm.abort));
                     if (!ok) break;
                     ++outs;
                     tc_fence_after();
@@ -500,16 +491,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < 12) {
         // ------------------------------------------------- values to f16
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-        each_table([&](Walk seg, int base) {
+        each_segments(others, [&] {
             const int id = tid - 256;         // this thread's key of a step
             bool ok = true;                   // after a wait that gave up all go on to the barriers, without work
-            for (; seg.left > 0; walk_next(seg, sm.tab.info, a.cut)) {
-                const SeqInfo info = sm.tab.info[seg.b];
+            for (int index = 0; index < sm.count; ++index) {
+                const Segment seg = sm.segs[index];
+                const SeqInfo info = seg.info;
                 int key0, keys;
-                segment_keys(seg, sm.tab.info, a.cut, key0, keys);
+                keys_of(seg, a.cut, key0, keys);
                 if (keys <= key0) continue;
                 const int slot = segs++ % kSegs, P = a.seqs.page_tokens;
-                const int32_t* row = a.seqs.table + (int64_t)(base + seg.b) * a.seqs.width;
+                const int32_t* row = a.seqs.table + (int64_t)seg.b * a.seqs.width;
                 float most = 0.0f;
                 for (int i = key0 / P + id; i * P < keys; i += 128) {
                     const int page = __ldg(row + i);
@@ -528,8 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float per = most > 0.0f ? kVLift / most : 0.0f;
                 const int all_see = keys_of_row(info, a.cut, seg.tile * kPair);
                 for (int key = key0; ok && key < keys; key += kTile) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.v_full[vr.stage], vr.phase, &sm.abort)) &&
-                         __all_sync(0xffffffffu, mbar_wait(&sm.v16_empty[v16r.stage], v16r.phase ^ 1, &sm.abort));
+                    ok = __all_sync(0xffffffffu, wait_for(&sm.v_full[vr.stage], vr.phase, &sm.abort)) &&
+                         __all_sync(0xffffffffu, wait_for(&sm.v16_empty[v16r.stage], v16r.phase ^ 1, &sm.abort));
                     if (!ok) break;
                     const Meta& meta = sm.v_meta[vr.stage];
                     const uint32_t src = smem_u32(sm.v[vr.stage]), dst = smem_u32(sm.v16[v16r.stage]);
@@ -551,17 +543,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (some) {
                                 // NaN must reach only the rows that see this key, but 0 * NaN is
                                 // NaN: it is taken out here and put back as the rows go out
+                                uint32_t any = 0;
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
                                     const uint32_t n = nan_bytes(w[k]);
-                                    if (n) {
-                                        sm.has_nan[slot] = 1;
-                                        for (int b = 0; b < 4; ++b)
-                                            if ((n >> (8 * b)) & 0x80u) {
-                                                atomicMin(&sm.nan_key[slot][16 * c + 4 * k + b], key + id);
-                                                w[k] &= ~(0xffu << (8 * b));
-                                            }
-                                    }
+                                    any |= n;
+                                    w[k] &= ~((n >> 7) * 0xffu);
+                                }
+                                if (any) {
+                                    sm.has_nan[slot] = 1;
+#pragma unroll 1
+                                    for (int b = 0; b < 16; ++b)
+                                        if ((sm.v[vr.stage][chunk_at<D>(id, c) + b] & 0x7f) == 0x7f)
+                                            atomicMin(&sm.nan_key[slot][16 * c + b], key + id);
                                 }
                             }
 #pragma unroll
@@ -601,13 +595,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp == 12) {
             // ----------------------------------------------------------- TMA
-            each_table([&](Walk seg, int base) {
+            each_segments(others, [&] {
                 const int P = a.seqs.page_tokens, per_box = P / 16;
                 bool ok = true;
-                for (; ok && seg.left > 0; walk_next(seg, sm.tab.info, a.cut)) {
+                for (int index = 0; ok && index < sm.count; ++index) {
+                    const Segment seg = sm.segs[index];
                     int key0, keys;
-                    segment_keys(seg, sm.tab.info, a.cut, key0, keys);
-                    const int32_t* row = a.seqs.table + (int64_t)(base + seg.b) * a.seqs.width;
+                    keys_of(seg, a.cut, key0, keys);
+                    const int32_t* row = a.seqs.table + (int64_t)seg.b * a.seqs.width;
                     auto page_at = [&](int key) {   // of this lane's 16 keys of a step
                         return lane < 8 && key + 16 * lane < keys ? __ldg(row + (key + 16 * lane) / P) : -1;
                     };
@@ -621,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box)) * P * D;
                         const int block = has ? page * a.cut.heads + seg.head : 0;
 
-                        ok = __all_sync(0xffffffffu, mbar_wait(&sm.k_empty[kr.stage], kr.phase ^ 1, &sm.abort));
+                        ok = __all_sync(0xffffffffu, wait_for(&sm.k_empty[kr.stage], kr.phase ^ 1, &sm.abort));
                         if (!ok) break;
                         if (lane == 0) {
                             sm.k_meta[mr.stage].valid = valid;
@@ -634,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (box) tma_load_3d(sm.k[kr.stage] + lane * 16 * D, &k_map, 0, 0, block, &sm.k_full[kr.stage]);
                         ++k_loads;
-                        ok = __all_sync(0xffffffffu, mbar_wait(&sm.v_empty[vr.stage], vr.phase ^ 1, &sm.abort));
+                        ok = __all_sync(0xffffffffu, wait_for(&sm.v_empty[vr.stage], vr.phase ^ 1, &sm.abort));
                         if (!ok) break;
                         if (lane == 0) {
                             sm.v_meta[vr.stage].valid = valid;
@@ -656,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             });
         } else if (warp == 13) {
             // ------------------------------------------- tensor instructions
-            each_table([&](Walk seg, int) {
+            each_segments(others, [&] {
                 if (lane > 0) return;
                 auto product_s = [&](int x, int stage) {
                     const uint64_t kd = smem_desc(smem_u32(sm.k[stage]), 16, D * 8, D == 128 ? 2 : 4);
@@ -676,70 +671,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_f16_ts(tmem + col_o<D>(x), tmem + col_s(x) + 8 * i, vd + 128 * i, kIdescO, more || i > 0);
                 };
                 bool ok = true;
-                for (; ok && seg.left > 0; walk_next(seg, sm.tab.info, a.cut)) {
+                for (int index = 0; ok && index < sm.count; ++index) {
+                    const Segment seg = sm.segs[index];
                     int key0, keys;
-                    segment_keys(seg, sm.tab.info, a.cut, key0, keys);
-                    const bool two = sm.tab.info[seg.b].rows - seg.tile * kPair > kTile;
+                    keys_of(seg, a.cut, key0, keys);
+                    const bool two = seg.info.rows - seg.tile * kPair > kTile;
                     const int count = (keys - key0 + kTile - 1) / kTile;
                     if (count == 0) continue;
-                    ok = mbar_wait(&sm.q_full[0], segs & 1, &sm.abort) &&
-                         mbar_wait(&sm.k_full[kr.stage], kr.phase, &sm.abort);
-                    if (!ok) break;
-                    ++segs;
-                    tc_fence_after();
-                    product_s(0, kr.stage);
-                    mma_commit(&sm.s_full[0]);
-                    if (two) {
-                        ok = mbar_wait(&sm.q_full[1], pairs & 1, &sm.abort);
-                        if (!ok) break;
-                        ++pairs;
-                        tc_fence_after();
-                        product_s(1, kr.stage);
-                        mma_commit(&sm.s_full[1]);
-                    }
-                    mma_commit(&sm.k_empty[kr.stage]);
-                    kr.next();
-                    for (int j = 0; j < count; ++j) {
-                        const bool more = j + 1 < count;
-                        ok = mbar_wait(&sm.v16_full[v16r.stage], v16r.phase, &sm.abort) &&
-                             mbar_wait(&sm.p_full[0], steps & 1, &sm.abort);
-                        if (!ok) break;
-                        tc_fence_after();
-                        product_o(0, v16r.stage, j > 0);
-                        if (!more) mma_commit(&sm.o_full[0]);
-                        if (more) {
-                            ok = mbar_wait(&sm.k_full[kr.stage], kr.phase, &sm.abort);
-                            if (!ok) break;
-                            tc_fence_after();
-                            product_s(0, kr.stage);
-                            mma_commit(&sm.s_full[0]);
-                        }
-                        if (two) {
-                            ok = mbar_wait(&sm.p_full[1], steps1 & 1, &sm.abort);
-                            if (!ok) break;
-                            ++steps1;
-                            tc_fence_after();
-                            product_o(1, v16r.stage, j > 0);
-                            if (!more) mma_commit(&sm.o_full[1]);
-                            mma_commit(&sm.v16_empty[v16r.stage]);
-                            if (more) {
-                                product_s(1, kr.stage);
-                                mma_commit(&sm.s_full[1]);
+                    // step j: for each tile O with the weights of step j - 1, then S of step j
+#pragma unroll 1
+                    for (int j = 0; ok && j <= count; ++j) {
+#pragma unroll 1
+                        for (int x = 0; x <= (int)two; ++x) {
+                            if (j > 0) {
+                                if (x == 0) ok = wait_for(&sm.v16_full[v16r.stage], v16r.phase, &sm.abort);
+                                ok = ok && wait_for(&sm.p_full[x], (x ? steps1 : steps) & 1, &sm.abort);
+                                if (!ok) break;
+                                if (x) ++steps1;
+                                else ++steps;
+                                tc_fence_after();
+                                product_o(x, v16r.stage, j > 1);
+                                if (j == count) mma_commit(&sm.o_full[x]);
                             }
-                        } else {
-                            mma_commit(&sm.v16_empty[v16r.stage]);
+                            if (j < count) {
+                                if (x == 0) ok = wait_for(&sm.k_full[kr.stage], kr.phase, &sm.abort);
+                                if (j == 0) ok = ok && wait_for(&sm.q_full[x], (x ? pairs : segs) & 1, &sm.abort);
+                                if (!ok) break;
+                                tc_fence_after();
+                                product_s(x, kr.stage);
+                                mma_commit(&sm.s_full[x]);
+                            }
                         }
-                        if (more) {
+                        if (!ok) break;
+                        if (j > 0) {
+                            mma_commit(&sm.v16_empty[v16r.stage]);
+                            v16r.next();
+                        }
+                        if (j < count) {
                             mma_commit(&sm.k_empty[kr.stage]);
                             kr.next();
                         }
-                        v16r.next();
-                        ++steps;
                     }
+                    ++segs;
+                    pairs += two;
                 }
             });
+        } else if (warp == 14) {
+            // ------------------------------------------------------ planning
+            Planner plan;
+            bool begun = false;
+            each_segments(
+                [&] {
+                    if (!begun) plan.begin(a, lane);
+                    begun = true;
+                    const int n = plan.next(a, sm.segs, lane);
+                    if (lane == 0) sm.count = n;
+                },
+                others);
         } else {
-            each_table([](Walk, int) {});
+            each_segments(others, others);
         }
     }
 

@@ -97,7 +97,7 @@ MHC_HD bool starts_run(const Span& sp, const Run& r, int t) {
 // How mhc_kv_attend's work is cut.  The rows of one sequence and key/value head
 // are its new tokens times the `group` query heads that share the head, row r
 // being token r / group, query head r % group of it; a tile is `tile_rows` of
-// them.  A tile's keys are cut in units of `unit`; a tile without keys still is
+// them.  A tile's keys are cut in units of 2^unit_log2; a tile without keys still is
 // one unit (its rows have to be written).  All units of all tiles, ordered by
 // sequence, tile, head and key, form one line that the blocks share evenly
 // whatever the lengths are (share_of), and a tile cut by a border is joined
@@ -111,7 +111,7 @@ struct SeqInfo {
 };
 
 struct Cut {
-    int heads, group, tile_rows, unit;
+    int heads, group, tile_rows, unit_log2;
 };
 
 MHC_HD SeqInfo info_of(const Span& sp, int group) {
@@ -137,16 +137,53 @@ MHC_HD int keys_of_tile(const SeqInfo& s, const Cut& c, int i) {
     return keys_of_row(s, c, end - 1);
 }
 
-MHC_HD int units_of_tile(const SeqInfo& s, const Cut& c, int i) {
-    const int n = (keys_of_tile(s, c, i) + c.unit - 1) / c.unit;
+MHC_HD int units_of(int keys, const Cut& c) {
+    const int n = (keys + (1 << c.unit_log2) - 1) >> c.unit_log2;
     return n < 1 ? 1 : n;
+}
+
+// The tiles of a sequence one after the other, with the units of each; the
+// last row's token (row / group) is kept without a division a tile.
+struct Tiles {
+    int tile, units;
+    int token, left;        // of the tile's last row, were the tile full: token * group + left
+};
+
+MHC_HD void tiles_units(Tiles& t, const SeqInfo& s, const Cut& c) {
+    const int last = (s.rows - 1) / c.group;
+    const int keys = s.before + (t.token < last ? t.token : last) + 1;
+    t.units = units_of(keys < 0 ? 0 : keys, c);
+}
+
+MHC_HD void tiles_start(Tiles& t, const SeqInfo& s, const Cut& c) {
+    t.tile = 0;
+    t.token = (c.tile_rows - 1) / c.group;
+    t.left = (c.tile_rows - 1) % c.group;
+    tiles_units(t, s, c);
+}
+
+MHC_HD void tiles_next(Tiles& t, const SeqInfo& s, const Cut& c) {
+    ++t.tile;
+    t.token += c.tile_rows / c.group;
+    t.left += c.tile_rows % c.group;
+    if (t.left >= c.group) {
+        t.left -= c.group;
+        ++t.token;
+    }
+    tiles_units(t, s, c);
 }
 
 // Units of all tiles and heads of a sequence.
 MHC_HD int64_t units_of_seq(const SeqInfo& s, const Cut& c) {
-    int64_t n = 0;
     const int tiles = tiles_of(s, c);
-    for (int i = 0; i < tiles; ++i) n += units_of_tile(s, c, i);
+    if (tiles == 0) return 0;
+    int64_t n = 0;
+    Tiles t;
+    tiles_start(t, s, c);
+    for (int i = 0; i < tiles; ++i) {
+        n += t.units;
+        tiles_next(t, s, c);
+    }
     return n * c.heads;
 }
 
@@ -154,65 +191,69 @@ MHC_HD int64_t units_of_seq(const SeqInfo& s, const Cut& c) {
 // blocks the first `total` blocks take one each, so that the blocks that share
 // a tile always follow one another.
 MHC_HD void share_of(int64_t total, int c, int blocks, int64_t& from, int64_t& to) {
-    const int64_t n = total < blocks ? total : blocks;
-    from = c < n ? total * c / n : total;
-    to = c < n ? total * (c + 1) / n : total;
+    // one division, in 32 bits where they hold: equal parts, the first `extra` of them one longer
+    const int64_t each = total >> 31 ? total / blocks : (int64_t)((uint32_t)total / (uint32_t)blocks);
+    const int64_t extra = total - each * blocks;
+    from = each * c + (c < extra ? c : extra);
+    to = from + each + (c < extra ? 1 : 0);
 }
 
-// A walk over the segments (one tile's units that one block takes) of a range
-// of the line, inside a table of sequences.
+// A segment: the units of one tile and head that one block takes.
+struct Segment {
+    int b;                  // sequence
+    SeqInfo info;
+    int tile, head;
+    int first, count;       // units
+    int units;              // of the whole tile
+};
+
+// The keys [key0, keys) of a segment.
+MHC_HD void keys_of(const Segment& s, const Cut& c, int& key0, int& keys) {
+    const int all = keys_of_tile(s.info, c, s.tile), end = (s.first + s.count) << c.unit_log2;
+    key0 = s.first << c.unit_log2;
+    keys = end < all ? end : all;
+}
+
+// A walk over a block's segments inside one sequence.
 struct Walk {
-    int b, tile, head;      // the current segment: index in the table, tile and head
-    int first, count;       // its units
-    int units;              // of its whole tile
-    int64_t left;           // units of the range from this segment on; 0: the walk is over
+    Tiles t;
+    int head, first, count;
+    int64_t left;           // units of the block's share from this segment on; 0: the walk is over
 };
 
 MHC_HD void walk_cut(Walk& w) {
-    const int rest = w.units - w.first;
+    const int rest = w.t.units - w.first;
     w.count = w.left < rest ? (int)w.left : rest;
 }
 
-// Starts at unit `from` of the table's line (prefix[b]: units before sequence
-// b), for `count` units that all lie in the table.
-MHC_HD void walk_start(Walk& w, const SeqInfo* seqs, const int64_t* prefix, int n, const Cut& c, int64_t from,
-                       int64_t count) {
-    w.left = count;
-    if (count <= 0) return;
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (prefix[mid] <= from) lo = mid;
-        else hi = mid;
+// Enters a sequence (with new tokens) at unit r of its part of the line, with
+// `left` units of the block's share to go.
+MHC_HD void walk_enter(Walk& w, const SeqInfo& s, const Cut& c, int64_t r, int64_t left) {
+    w.left = left;
+    tiles_start(w.t, s, c);
+    while (r >= (int64_t)w.t.units * c.heads) {
+        r -= (int64_t)w.t.units * c.heads;
+        tiles_next(w.t, s, c);
     }
-    int64_t r = from - prefix[lo];
-    w.b = lo;
-    w.tile = 0;
-    w.units = units_of_tile(seqs[lo], c, 0);
-    while (r >= (int64_t)w.units * c.heads) {
-        r -= (int64_t)w.units * c.heads;
-        ++w.tile;
-        w.units = units_of_tile(seqs[lo], c, w.tile);
-    }
-    w.head = (int)(r / w.units);
-    w.first = (int)(r % w.units);
+    const int at = (int)r;  // less than units * heads, which fits: both are bounded by what memory holds
+    w.head = at / w.t.units;
+    w.first = at % w.t.units;
     walk_cut(w);
 }
 
-MHC_HD void walk_next(Walk& w, const SeqInfo* seqs, const Cut& c) {
+// The next segment; false where the sequence is done (then the caller enters
+// the next one with new tokens, if w.left > 0).
+MHC_HD bool walk_next(Walk& w, const SeqInfo& s, const Cut& c) {
     w.left -= w.count;
-    if (w.left <= 0) return;
+    if (w.left <= 0) return false;
     w.first = 0;
     if (++w.head == c.heads) {
         w.head = 0;
-        if (++w.tile == tiles_of(seqs[w.b], c)) {
-            w.tile = 0;
-            do ++w.b;
-            while (seqs[w.b].rows == 0);
-        }
-        w.units = units_of_tile(seqs[w.b], c, w.tile);
+        if (w.t.tile + 1 == tiles_of(s, c)) return false;
+        tiles_next(w.t, s, c);
     }
     walk_cut(w);
+    return true;
 }
 
 }  // namespace kv

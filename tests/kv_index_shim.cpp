@@ -34,48 +34,45 @@ void kv_runs(const int32_t* table, const int32_t* lens, const int32_t* cu, int w
     }
 }
 
-// The segments of block `block` of `blocks`, table by table as the kernel
-// walks them: out[i] = {sequence, tile, head, first unit, units, units of the
-// tile}.  Returns how many, or -1 if there are more than `most`; total: units
-// of the whole line.
+// The segments of block `block` of `blocks`: out[i] = {sequence, tile, head,
+// first unit, units, units of the tile, first key, last key + 1}.  Returns how
+// many, or -1 if there are more than `most`; total: units of the whole line.
 int kv_segments(const int32_t* table, const int32_t* lens, const int32_t* cu, int width, int B, int T, int P,
-                int pages, int heads, int group, int tile_rows, int unit, int table_size, int block, int blocks, int32_t* out,
+                int pages, int heads, int group, int tile_rows, int unit_log2, int block, int blocks, int32_t* out,
                 int most, int64_t* total) {
     const Seqs s = make(table, lens, cu, width, B, T, P, pages);
-    const Cut c{heads, group, tile_rows, unit};
+    const Cut c{heads, group, tile_rows, unit_log2};
     *total = 0;
     for (int b = 0; b < B; ++b) *total += units_of_seq(info_of(span_of(s, b), group), c);
-    int64_t from, to;
+    int64_t from, to, seen = 0;
     share_of(*total, block, blocks, from, to);
-    int64_t seen = 0;
-    int n = 0;
-    SeqInfo* info = new SeqInfo[table_size];
-    int64_t* prefix = new int64_t[table_size];
-    for (int base = 0; base < B; base += table_size) {
-        int64_t here = 0;
-        for (int i = 0; i < table_size; ++i) {
-            info[i] = base + i < B ? info_of(span_of(s, base + i), group) : SeqInfo{0, 0, 0, 0};
-            prefix[i] = here;
-            here += units_of_seq(info[i], c);
-        }
-        const int64_t lo = (from > seen ? from : seen) - seen, hi = (to < seen + here ? to : seen + here) - seen;
-        seen += here;
-        if (hi <= lo) continue;
-        Walk w;
-        for (walk_start(w, info, prefix, table_size, c, lo, hi - lo); w.left > 0; walk_next(w, info, c)) {
-            if (n == most) { n = -1; break; }
-            int32_t* o = out + 6 * n++;
-            o[0] = base + w.b;
-            o[1] = w.tile;
-            o[2] = w.head;
-            o[3] = w.first;
-            o[4] = w.count;
-            o[5] = w.units;
-        }
-        if (n < 0) break;
+    int n = 0, b = 0;
+    for (; b < B; ++b) {
+        const int64_t u = units_of_seq(info_of(span_of(s, b), group), c);
+        if (from < seen + u) break;
+        seen += u;
     }
-    delete[] info;
-    delete[] prefix;
+    int64_t left = to - from, r = from - seen;
+    for (; left > 0; ++b) {
+        const SeqInfo info = info_of(span_of(s, b), group);
+        if (info.rows == 0) continue;
+        Walk w;
+        walk_enter(w, info, c, r, left);
+        r = 0;
+        do {
+            if (n == most) return -1;
+            const Segment g{b, info, w.t.tile, w.head, w.first, w.count, w.t.units};
+            int32_t* o = out + 8 * n++;
+            o[0] = b;
+            o[1] = g.tile;
+            o[2] = g.head;
+            o[3] = g.first;
+            o[4] = g.count;
+            o[5] = g.units;
+            keys_of(g, c, o[6], o[7]);
+        } while (walk_next(w, info, c));
+        left = w.left;
+    }
     return n;
 }
 
