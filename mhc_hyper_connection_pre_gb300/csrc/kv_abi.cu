@@ -85,7 +85,9 @@ bool rows_ok(const void* p, int64_t stride, int64_t width) {
 
 Seqs seqs_of(const mhc_kv_cache* c, const int32_t* block_table, int64_t table_width, const int32_t* seq_lens,
              const int32_t* cu_q, int64_t B, int64_t T) {
-    return Seqs{block_table, seq_lens, cu_q, (int)table_width, (int)B, (int)T, c->page_tokens, (int)c->num_pages};
+    int log2 = 4;                                        // page_tokens is a power of two from 16 on (check_common)
+    while ((1 << log2) < c->page_tokens) ++log2;
+    return Seqs{block_table, seq_lens, cu_q, (int)table_width, (int)B, (int)T, log2, (int)c->num_pages};
 }
 
 }  // namespace

@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(GT > 256 ? GT : 256) kv_append_kernel(const Ap
         if (page < 0 || n == 0) continue;
 
         float* scale_at = a.scale[kv] + (int64_t)page * a.heads + head;
-        uint8_t* code = a.code[kv] + ((int64_t)page * a.heads + head) * a.seqs.page_tokens * D;
+        uint8_t* code = a.code[kv] + (((int64_t)page * a.heads + head) * D << a.seqs.page_log2);
         const float old = run.slot ? *scale_at : 0.0f;
 
         auto load = [&](int r, float (&x)[8]) {       // r may be past the run: zeros
@@ -334,10 +334,10 @@ cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code,
     // Few new tokens a sequence: a warp for each token that may start a run.
     // Many: as many threads as hold a whole page, for each window of a page.
     const bool few = seqs.T < 8 * (int64_t)seqs.B;
-    a.window = few ? 1 : seqs.page_tokens;
+    a.window = few ? 1 : 1 << seqs.page_log2;
     a.windows = (seqs.T + a.window - 1) / a.window;
     a.q_steps = seqs.T < 2048 ? 1 : 1 << 20;
-    const int gt = few ? 32 : seqs.page_tokens * head_dim / 32;
+    const int gt = few ? 32 : (head_dim << seqs.page_log2) / 32;
     if (head_dim == 64) {
         switch (gt) {
             case 32: return launch_append<64, 32>(a, stream);

@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kStages; ++i) mbar_init(&sm.full[warp][i], 1 + 4);   // lane 0 and the four scales
         fence_mbar_init_cluster();
     }
-    if (tid < 2) a.desc[blockIdx.x * 2 + tid].valid = 0;
+    if (tid == 0) a.desc[blockIdx.x].parts = 0;
 
     Planner plan;                             // of the first warp
     uint32_t issued = 0, waited = 0;          // loads of this warp
@@ -338,16 +338,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto find_pages = [&] {               // of the next load; used only when it is issued
             if (ld.seg >= count) return;
             const int32_t* row = a.seqs.table + (int64_t)sm.segs[ld.seg].b * a.seqs.width;
-            page[0] = __ldg(row + ld.key / a.seqs.page_tokens);
-            page[1] = ld.key + 16 < ld.keys ? __ldg(row + (ld.key + 16) / a.seqs.page_tokens) : -1;
+            page[0] = __ldg(row + (ld.key >> a.seqs.page_log2));
+            page[1] = ld.key + 16 < ld.keys ? __ldg(row + ((ld.key + 16) >> a.seqs.page_log2)) : -1;
         };
         auto issue = [&] {
             if (ld.seg >= count || *(volatile int*)&sm.abort) return;
             const int st = issued % kStages;
-            const int key = ld.key, P = a.seqs.page_tokens, head = sm.segs[ld.seg].head;
+            const int slot = ld.key & ((1 << a.seqs.page_log2) - 1), head = sm.segs[ld.seg].head;
             const bool ok0 = page[0] >= 0 && page[0] < a.seqs.num_pages;
             const bool ok1 = page[1] >= 0 && page[1] < a.seqs.num_pages;
-            const bool two = key + 16 < ld.keys;
+            const bool two = ld.key + 16 < ld.keys;
             if ((!ok0 || (two && !ok1)) && lane == 0) atomicOr(&g_device_status, kIndexError);
             uint64_t* bar = &sm.full[warp][st];
             Meta& meta = sm.meta[warp][st];
@@ -363,12 +363,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t* dst = sm.ring[warp] + st * kStage;
                 meta.page[0] = ok0 ? page[0] : -1;
                 meta.page[1] = ok1 ? page[1] : -1;
-                if (P >= kSub) {              // both halves lie in one page
+                if (a.seqs.page_log2 >= 5) {            // both halves lie in one page
                     mbar_arrive_expect_tx(bar, ok0 ? kStage : 0);
                     if (ok0) {
                         const int block = page[0] * a.cut.heads + head;
-                        tma_load_3d(dst, &k_map, 0, key % P, block, bar);
-                        tma_load_3d(dst + kStage / 2, &v_map, 0, key % P, block, bar);
+                        tma_load_3d(dst, &k_map, 0, slot, block, bar);
+                        tma_load_3d(dst + kStage / 2, &v_map, 0, slot, block, bar);
                     }
                 } else {
                     mbar_arrive_expect_tx(bar, (ok0 ? kStage / 2 : 0) + (ok1 ? kStage / 2 : 0));
@@ -476,17 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the warps' sums of this segment, joined
             const bool whole = seg.first == 0 && seg.count == seg.units;
             const int slot = seg.first == 0 ? 1 : 0;
-            float* part = a.part + ((int64_t)blockIdx.x * 2 + slot) * kRows * (D + 2);
-            if (!whole && tid == 0) {
-                PartDesc d;
-                d.valid = 1;
-                d.last = seg.first + seg.count == seg.units;
-                d.begin = info.begin;
-                d.first_row = first_row;
-                d.rows = rows;
-                d.head = seg.head;
-                a.desc[blockIdx.x * 2 + slot] = d;
-            }
+            float* part = part_of(a, blockIdx.x, slot, D);
+            if (!whole && slot && tid == 0)
+                a.desc[blockIdx.x] = PartDesc{seg.parts, info.begin, first_row, rows, seg.head, {}};
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -533,10 +525,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (whole) {
                                 write_row<D>(a, info.begin, first_row + r, seg.head, at, o, m, l);
                             } else {
-                                float* dst = part + r * (D + 2);
-                                *reinterpret_cast<float2*>(dst + 2 + dim_of<D>(at)) = make_float2(o.x, o.y);
-                                *reinterpret_cast<float2*>(dst + 2 + dim_of<D>(at + 2)) = make_float2(o.z, o.w);
-                                if (at == 0) *reinterpret_cast<float2*>(dst) = make_float2(m, l);
+                                float* dst = part + r * D;
+                                *reinterpret_cast<float2*>(dst + dim_of<D>(at)) = make_float2(o.x, o.y);
+                                *reinterpret_cast<float2*>(dst + dim_of<D>(at + 2)) = make_float2(o.z, o.w);
+                                if (at == 0)
+                                    *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(m, l);
                             }
                         }
                     }
@@ -551,45 +544,59 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the tile that block blockIdx.x of the attention began
-// and did not finish: slot 1 of that block, then slot 0 of the following ones.
+// and did not finish: its slot 1, then slot 0 of the blocks after it.  A row is
+// D / 4 lanes' work: first a lane for each part finds the parts' weights, then
+// each lane adds up its four dims.  Every load but the first depends on nothing
+// that came before it.
 template <int D>
-__global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a, int blocks) {
+__global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a) {
+    constexpr int kLanes = D / 4, kRows = 256 / kLanes;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x, R = a.cut.tile_rows;
-    const PartDesc d = a.desc[c * 2 + 1];
-    if (!d.valid) return;
-    int n = 1;                                // parts
-    while (c + n < blocks && a.desc[(c + n) * 2].valid) {
-        ++n;
-        if (a.desc[(c + n - 1) * 2].last) break;
-    }
-    const int64_t one = (int64_t)R * (D + 2);
-    const float* first = a.part + ((int64_t)c * 2 + 1) * one;
-    const float* rest = a.part + ((int64_t)c + 1) * 2 * one;
-    for (int i = threadIdx.x; i < d.rows * (D / 4); i += blockDim.x) {
-        const int r = i / (D / 4), p = i % (D / 4) * 4;
-        const int64_t at = (int64_t)r * (D + 2);
-        float m = first[at];
-        for (int k = 0; k + 1 < n; ++k) m = fmaxf(m, rest[k * 2 * one + at]);
-        const float zero = m == -INFINITY ? 0.0f : m;
-        float l = 0.0f;
+    const int c = blockIdx.x;
+    const PartDesc d = a.desc[c];
+    if (d.parts == 0) return;
+    const int lane = threadIdx.x % kLanes;
+    const int64_t next = 2 * (int64_t)a.cut.tile_rows * (D + 2);      // from a block's part to the next block's
+    const float* first = part_of(a, c, 1, D);
+    const float* rest = part_of(a, c + 1, 0, D) - next;               // part k, k > 0, at rest + k * next
+    const int ml = a.cut.tile_rows * D;
+    for (int r0 = blockIdx.y * kRows; r0 < d.rows; r0 += gridDim.y * kRows) {
+        const int row = r0 + threadIdx.x / kLanes, r = row < d.rows ? row : d.rows - 1;   // whole warps shuffle
+        float m = -INFINITY, l = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int k = 0; k < n; ++k) {
-            const float* src = (k ? rest + (k - 1) * 2 * one : first) + at;
-            const float2 ml = *reinterpret_cast<const float2*>(src);
-            const float2 y = *reinterpret_cast<const float2*>(src + 2 + p), z = *reinterpret_cast<const float2*>(src + 4 + p);
-            const float x = ex2(ml.x - zero);
-            l = fmaf(x, ml.y, l);
-            o.x = fmaf(x, y.x, o.x);
-            o.y = fmaf(x, y.y, o.y);
-            o.z = fmaf(x, z.x, o.z);
-            o.w = fmaf(x, z.y, o.w);
+        for (int base = 0; base < d.parts; base += kLanes) {
+            const int n = d.parts - base < kLanes ? d.parts - base : kLanes, k = base + lane;
+            float2 mine = make_float2(-INFINITY, 0.0f);
+            if (lane < n) mine = *reinterpret_cast<const float2*>((k ? rest + k * next : first) + ml + 2 * r);
+            float now = mine.x;
+#pragma unroll
+            for (int i = kLanes / 2; i; i >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, i));
+            now = fmaxf(now, m);
+            const float zero = now == -INFINITY ? 0.0f : now, keep = ex2(m - zero);
+            const float w = ex2(mine.x - zero);
+            float sum = w * mine.y;
+#pragma unroll
+            for (int i = kLanes / 2; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+            l = fmaf(l, keep, sum);
+            o.x *= keep; o.y *= keep; o.z *= keep; o.w *= keep;
+            m = now;
+#pragma unroll 8
+            for (int i = 0; i < n; ++i) {
+                const float x = __shfl_sync(0xffffffffu, w, i, kLanes);
+                const float4 y =
+                    reinterpret_cast<const float4*>((base + i ? rest + (base + i) * next : first) + r * D)[lane];
+                o.x = fmaf(x, y.x, o.x);
+                o.y = fmaf(x, y.y, o.y);
+                o.z = fmaf(x, y.z, o.z);
+                o.w = fmaf(x, y.w, o.w);
+            }
         }
+        if (row >= d.rows) continue;
         const int64_t to = place_of(a, d.begin, d.first_row + r, d.head);
         const float y = l == 0.0f ? 0.0f : 1.0f / l;
-        *reinterpret_cast<uint2*>(a.out + to * D + p) =
+        *reinterpret_cast<uint2*>(a.out + to * D + 4 * lane) =
             make_uint2(pack_bf16x2(o.x * y, o.y * y), pack_bf16x2(o.z * y, o.w * y));
-        if (p == 0 && a.lse) a.lse[to] = lse_of(m, l);
+        if (lane == 0 && a.lse) a.lse[to] = lse_of(m, l);
     }
 }
 
@@ -618,10 +625,10 @@ cudaError_t launch_join(const AttendArgs& a, int head_dim, int blocks, cudaStrea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(blocks - 1, 1, 1);
+    cfg.gridDim = dim3(blocks - 1, a.cut.tile_rows > 16 ? 8 : 1, 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = stream;
-    return cudaLaunchKernelEx(&cfg, head_dim == 64 ? kv_join_kernel<64> : kv_join_kernel<128>, a, blocks);
+    return cudaLaunchKernelEx(&cfg, head_dim == 64 ? kv_join_kernel<64> : kv_join_kernel<128>, a);
 }
 
 }  // namespace
@@ -630,7 +637,7 @@ cudaError_t launch_kv_attend_tc(const AttendArgs& a, const uint8_t* k, const uin
                                 cudaStream_t stream);
 
 size_t kv_attend_workspace(int heads, int head_dim, int q_heads, int64_t B, int64_t T, int num_sms) {
-    return part_bytes(tile_rows(q_heads / heads, B, T), head_dim, num_sms) + (size_t)num_sms * 2 * sizeof(PartDesc);
+    return part_bytes(tile_rows(q_heads / heads, B, T), head_dim, num_sms) + (size_t)num_sms * sizeof(PartDesc);
 }
 
 cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* v, const float* k_scale,
@@ -656,8 +663,8 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
     } else {
         CUtensorMap k_map, v_map;
         const int64_t pages = (int64_t)seqs.num_pages * heads;
-        if (!encode_codes(&k_map, k, pages, seqs.page_tokens, head_dim, kSub) ||
-            !encode_codes(&v_map, v, pages, seqs.page_tokens, head_dim, kSub))
+        if (!encode_codes(&k_map, k, pages, 1 << seqs.page_log2, head_dim, kSub) ||
+            !encode_codes(&v_map, v, pages, 1 << seqs.page_log2, head_dim, kSub))
             return cudaErrorInvalidValue;
         if (rows == 8)
             e = head_dim == 64 ? launch<64, 1>(k_map, v_map, a, num_sms, stream)

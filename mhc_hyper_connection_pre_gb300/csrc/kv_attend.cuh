@@ -15,12 +15,11 @@ namespace kv {
 constexpr float kLift = 10.0f;                // weights are 2^10 times the softmax's numerators
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// What a block left unfinished: slot 1 a tile that it began, slot 0 one that
-// it went on with.
+// The tile that a block began and did not finish.
 struct PartDesc {
-    int valid, last;                          // last: the tile ends here
+    int parts;                                // blocks that share it, 0: no such tile
     int begin, first_row, rows, head;         // rows of the tile
-    int pad[2];
+    int pad[3];
 };
 
 struct AttendArgs {
@@ -33,9 +32,14 @@ struct AttendArgs {
     float scale_log2;                         // softmax_scale * log2(e)
     uint16_t* out;
     float* lse;
-    float* part;                              // [blocks][2][tile_rows][D + 2]: maximum, sum, the weighted values
-    PartDesc* desc;                           // [blocks][2]
+    float* part;                              // [blocks][2]: weighted values [tile_rows][D], maximum and sum [tile_rows][2]
+    PartDesc* desc;                           // [blocks]: the tile that a block began and did not finish
 };
+
+// Part `slot` of a block: 1 a tile that the block began, 0 one that it went on with.
+__device__ __forceinline__ float* part_of(const AttendArgs& a, int block, int slot, int D) {
+    return a.part + ((int64_t)block * 2 + slot) * a.cut.tile_rows * (D + 2);
+}
 
 constexpr int kSegments = 32;                 // of a block that are planned at a time
 
@@ -89,6 +93,7 @@ struct Planner {
     Walk w;
     int b;                                    // the walk's sequence
     SeqInfo info;
+    int64_t total;                            // units of the line
     int base;                                 // sequences base .. base + 31 are at hand, one a lane
     SeqInfo at_hand;
 
@@ -133,7 +138,8 @@ struct Planner {
             if (lane >= o) upto += up;
         }
         int64_t from, to;
-        share_of(__shfl_sync(0xffffffffu, upto, 31), blockIdx.x, gridDim.x, from, to);
+        total = __shfl_sync(0xffffffffu, upto, 31);
+        share_of(total, blockIdx.x, gridDim.x, from, to);
         w.left = to - from;
         if (w.left <= 0) return;
         const int part = __ffs(__ballot_sync(0xffffffffu, upto > from)) - 1;
@@ -155,7 +161,9 @@ struct Planner {
         int n = 0;
 #pragma unroll 1
         while (w.left > 0 && n < kSegments) {
-            if (lane == 0) out[n] = Segment{b, info, w.t.tile, w.head, w.first, w.count, w.t.units};
+            if (lane == 0)
+                out[n] = Segment{b, info, w.t.tile, w.head, w.first, w.count, w.t.units,
+                                 blocks_beyond(total, blockIdx.x, gridDim.x, w.t.units - w.first - w.count) + 1};
             ++n;
             if (!walk_next(w, info, a.cut) && w.left > 0) {
                 do fetch(a, b + 1, lane);

@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init_cluster();
     }
     if (warp == 13) tmem_alloc(&sm.tmem, 512);
-    if (tid < 2) a.desc[blockIdx.x * 2 + tid].valid = 0;
+    if (tid == 0) a.desc[blockIdx.x].parts = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -429,16 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the rows go out
                 const bool whole = seg.first == 0 && seg.count == seg.units;
                 const int slot = seg.first == 0 ? 1 : 0;
-                if (!whole && tid == 0) {
-                    PartDesc d;
-                    d.valid = 1;
-                    d.last = seg.first + seg.count == seg.units;
-                    d.begin = info.begin;
-                    d.first_row = first_row;
-                    d.rows = rows;
-                    d.head = seg.head;
-                    a.desc[blockIdx.x * 2 + slot] = d;
-                }
+                if (!whole && slot && tid == 0)
+                    a.desc[blockIdx.x] = PartDesc{seg.parts, info.begin, first_row, rows, seg.head, {}};
                 if (count > 0) {
                     ok = __all_sync(0xffffffffu, wait_for(&sm.o_full[x], outs & 1, &sm.abort));
                     if (!ok) break;
@@ -446,14 +438,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                 }
                 const int64_t at = mine < rows ? place_of(a, info.begin, first_row + mine, seg.head) : 0;
-                float* part = a.part + (((int64_t)blockIdx.x * 2 + slot) * kPair + mine) * (D + 2);
+                float* part = part_of(a, blockIdx.x, slot, D);
                 const int kept = segs % kSegs;
                 const float unit = count > 0 ? sm.ref[kept] * (1.0f / kVLift) : 0.0f;
                 const float by = whole ? (l == 0.0f ? 0.0f : unit / l) : unit;
                 const bool nans = count > 0 && sm.has_nan[kept];
                 if (mine < rows) {
                     if (whole && a.lse) a.lse[at] = lse_of(m, l);
-                    if (!whole) *reinterpret_cast<float2*>(part) = make_float2(m, l);
+                    if (!whole) *reinterpret_cast<float2*>(part + kPair * D + 2 * mine) = make_float2(m, l);
                 }
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
@@ -480,9 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             dst[i] = pack8(y);
                         }
                     } else {
+                        uint4* dst = reinterpret_cast<uint4*>(part + mine * D + c * 32);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2)
-                            *reinterpret_cast<uint2*>(part + 2 + c * 32 + i) = make_uint2(o[i], o[i + 1]);
+                        for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                 }
                 segs += count > 0;
@@ -500,10 +492,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int key0, keys;
                 keys_of(seg, a.cut, key0, keys);
                 if (keys <= key0) continue;
-                const int slot = segs++ % kSegs, P = a.seqs.page_tokens;
+                const int slot = segs++ % kSegs, log2 = a.seqs.page_log2;
                 const int32_t* row = a.seqs.table + (int64_t)seg.b * a.seqs.width;
                 float most = 0.0f;
-                for (int i = key0 / P + id; i * P < keys; i += 128) {
+                for (int i = (key0 >> log2) + id; i << log2 < keys; i += 128) {
                     const int page = __ldg(row + i);
                     if (page >= 0 && page < a.seqs.num_pages)
                         most = fmaxf(most, __ldg(a.v_scale + (int64_t)page * a.cut.heads + seg.head));
@@ -596,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 12) {
             // ----------------------------------------------------------- TMA
             each_segments(others, [&] {
-                const int P = a.seqs.page_tokens, per_box = P / 16;
+                const int log2 = a.seqs.page_log2, per_box = 1 << (log2 - 4);
                 bool ok = true;
                 for (int index = 0; ok && index < sm.count; ++index) {
                     const Segment seg = sm.segs[index];
@@ -604,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     keys_of(seg, a.cut, key0, keys);
                     const int32_t* row = a.seqs.table + (int64_t)seg.b * a.seqs.width;
                     auto page_at = [&](int key) {   // of this lane's 16 keys of a step
-                        return lane < 8 && key + 16 * lane < keys ? __ldg(row + (key + 16 * lane) / P) : -1;
+                        return lane < 8 && key + 16 * lane < keys ? __ldg(row + ((key + 16 * lane) >> log2)) : -1;
                     };
                     int page = page_at(key0);
                     for (int key = key0; key < keys; key += kTile) {
@@ -612,8 +604,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const bool has = page >= 0 && page < a.seqs.num_pages;
                         if (lane < 8 && key + 16 * lane < keys && !has) atomicOr(&g_device_status, kIndexError);
                         const uint32_t valid = __ballot_sync(0xffffffffu, lane < 8 && has);
-                        const bool box = lane < 8 && has && lane % per_box == 0;
-                        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box)) * P * D;
+                        const bool box = lane < 8 && has && (lane & (per_box - 1)) == 0;
+                        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box)) * D << log2;
                         const int block = has ? page * a.cut.heads + seg.head : 0;
 
                         ok = __all_sync(0xffffffffu, wait_for(&sm.k_empty[kr.stage], kr.phase ^ 1, &sm.abort));
@@ -756,8 +748,8 @@ template <int D>
 cudaError_t launch(const AttendArgs& a, const uint8_t* k, const uint8_t* v, int blocks, cudaStream_t stream) {
     CUtensorMap k_map, v_map;
     const int64_t pages = (int64_t)a.seqs.num_pages * a.cut.heads;
-    if (!encode_codes(&k_map, k, pages, a.seqs.page_tokens, D, kTile) ||
-        !encode_codes(&v_map, v, pages, a.seqs.page_tokens, D, kTile))
+    if (!encode_codes(&k_map, k, pages, 1 << a.seqs.page_log2, D, kTile) ||
+        !encode_codes(&v_map, v, pages, 1 << a.seqs.page_log2, D, kTile))
         return cudaErrorInvalidValue;
     const int bytes = (int)sizeof(Smem<D>) + 1024;
     const cudaError_t e = cudaFuncSetAttribute(kv_attend_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);

@@ -21,7 +21,7 @@ struct Seqs {
     const int32_t* cu;      // [B + 1] or null: one token each
     int width;              // pages of a table row
     int B, T;
-    int page_tokens;
+    int page_log2;          // tokens of a page: 2^page_log2
     int num_pages;
 };
 
@@ -38,7 +38,7 @@ MHC_HD int clampi(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x
 
 MHC_HD Span span_of(const Seqs& s, int b) {
     Span r;
-    const int cap = s.width * s.page_tokens;      // at most 2^30 (checked on the host)
+    const int cap = s.width << s.page_log2;       // at most 2^30 (checked on the host)
     int begin, end;
     if (s.cu) {
         const int c0 = s.cu[b], c1 = s.cu[b + 1];
@@ -59,9 +59,9 @@ MHC_HD Span span_of(const Seqs& s, int b) {
     return r;
 }
 
-// Page holding position pos of sequence b (pos < width * page_tokens), or -1.
+// Page holding position pos of sequence b (pos < width * tokens of a page), or -1.
 MHC_HD int page_of(const Seqs& s, int b, int pos) {
-    const int p = s.table[(int64_t)b * s.width + pos / s.page_tokens];
+    const int p = s.table[(int64_t)b * s.width + (pos >> s.page_log2)];
     return p >= 0 && p < s.num_pages ? p : -1;
 }
 
@@ -81,8 +81,8 @@ MHC_HD Run run_at(const Seqs& s, const Span& sp, int t) {
         r.next = first < sp.end ? first : sp.end;
         return r;
     }
-    r.slot = r.pos % s.page_tokens;
-    const int room = s.page_tokens - r.slot, left = sp.end - t;
+    r.slot = r.pos & ((1 << s.page_log2) - 1);
+    const int room = (1 << s.page_log2) - r.slot, left = sp.end - t;
     r.n = room < left ? room : left;
     r.next = t + r.n;
     return r;
@@ -198,6 +198,16 @@ MHC_HD void share_of(int64_t total, int c, int blocks, int64_t& from, int64_t& t
     to = from + each + (c < extra ? 1 : 0);
 }
 
+// How many blocks after block c it takes for `units` more units of the line.
+MHC_HD int blocks_beyond(int64_t total, int c, int blocks, int units) {
+    if (units <= 0) return 0;
+    const int64_t each = total >> 31 ? total / blocks : (int64_t)((uint32_t)total / (uint32_t)blocks);
+    const int64_t longer = total - each * blocks - (c + 1);      // following blocks that take one unit more
+    if (longer > 0 && units <= longer * (each + 1)) return (int)((units + each) / (each + 1));
+    const int64_t more = longer > 0 ? longer : 0, rest = units - more * (each + 1);
+    return (int)(more + (rest + each - 1) / each);
+}
+
 // A segment: the units of one tile and head that one block takes.
 struct Segment {
     int b;                  // sequence
@@ -205,6 +215,7 @@ struct Segment {
     int tile, head;
     int first, count;       // units
     int units;              // of the whole tile
+    int parts;              // blocks that share the tile's units from this segment on
 };
 
 // The keys [key0, keys) of a segment.

@@ -4,7 +4,9 @@
 using namespace mhc::kv;
 
 static Seqs make(const int32_t* table, const int32_t* lens, const int32_t* cu, int width, int B, int T, int P, int pages) {
-    return Seqs{table, lens, cu, width, B, T, P, pages};
+    int log2 = 0;
+    while ((1 << log2) < P) ++log2;
+    return Seqs{table, lens, cu, width, B, T, log2, pages};
 }
 
 extern "C" {
@@ -35,7 +37,7 @@ void kv_runs(const int32_t* table, const int32_t* lens, const int32_t* cu, int w
 }
 
 // The segments of block `block` of `blocks`: out[i] = {sequence, tile, head,
-// first unit, units, units of the tile, first key, last key + 1}.  Returns how
+// first unit, units, units of the tile, first key, last key + 1, blocks from here on}.  Returns how
 // many, or -1 if there are more than `most`; total: units of the whole line.
 int kv_segments(const int32_t* table, const int32_t* lens, const int32_t* cu, int width, int B, int T, int P,
                 int pages, int heads, int group, int tile_rows, int unit_log2, int block, int blocks, int32_t* out,
@@ -61,8 +63,9 @@ int kv_segments(const int32_t* table, const int32_t* lens, const int32_t* cu, in
         r = 0;
         do {
             if (n == most) return -1;
-            const Segment g{b, info, w.t.tile, w.head, w.first, w.count, w.t.units};
-            int32_t* o = out + 8 * n++;
+            const Segment g{b, info, w.t.tile, w.head, w.first, w.count, w.t.units,
+                            blocks_beyond(*total, block, blocks, w.t.units - w.first - w.count) + 1};
+            int32_t* o = out + 9 * n++;
             o[0] = b;
             o[1] = g.tile;
             o[2] = g.head;
@@ -70,6 +73,7 @@ int kv_segments(const int32_t* table, const int32_t* lens, const int32_t* cu, in
             o[4] = g.count;
             o[5] = g.units;
             keys_of(g, c, o[6], o[7]);
+            o[8] = g.parts;
         } while (walk_next(w, info, c));
         left = w.left;
     }

@@ -243,7 +243,7 @@ def test_runs_stay_inside_whatever_the_arrays_hold(shim, seed):
 def _segments(shim, lens, cu, T, B, width, heads, group, rows, blocks, unit=64):
     """Every block's segments, in order, and the number of units."""
     pages = _i32(np.zeros((B, width)))
-    out, total, got = np.zeros((20000, 8), dtype=np.int32), ctypes.c_int64(0), []
+    out, total, got = np.zeros((20000, 9), dtype=np.int32), ctypes.c_int64(0), []
     for c in range(blocks):
         n = shim.kv_segments(_ptr(pages), _ptr(lens), _ptr(cu), width, B, T, 16, 1, heads, group, rows, unit.bit_length() - 1, c,
                              blocks, _ptr(out), 20000, ctypes.byref(total))
@@ -277,14 +277,21 @@ def test_blocks_share_every_unit_once(shim, seed):
             units = max(1, -(-keys // unit))
             for h in range(heads):
                 expect += [(b, i, h, u, units, u * unit, min((u + 1) * unit, keys)) for u in range(units)]
-    flat = [(b, i, h, u, units, u * unit, min((u + 1) * unit, k1)) for c in got for b, i, h, first, count, units, k0, k1
+    flat = [(b, i, h, u, units, u * unit, min((u + 1) * unit, k1)) for c in got for b, i, h, first, count, units, k0, k1, _
             in c for u in range(first, first + count)]
     assert flat == expect and total == len(expect)
     sizes = [sum(s[4] for s in c) for c in got]
     assert max(sizes) - min(sizes) <= 1
     assert not any(sizes[total:])                      # the blocks of a tile follow one another
+    owners = {}
+    for c, segs in enumerate(got):
+        for s in segs:
+            owners.setdefault(tuple(s[:3]), []).append((c, s[8]))
+    for of in owners.values():                         # a tile's blocks are consecutive, and each knows how many follow
+        assert [c for c, _ in of] == list(range(of[0][0], of[0][0] + len(of)))
+        assert [parts for _, parts in of] == list(range(len(of), 0, -1))
     for c in got:
-        for k, (b, i, h, first, count, units, k0, k1) in enumerate(c):
+        for k, (b, i, h, first, count, units, k0, k1, _) in enumerate(c):
             assert count >= 1 and first + count <= units and k0 == first * unit
             assert first == 0 or k == 0
             assert first + count == units or k == len(c) - 1
@@ -299,7 +306,7 @@ def test_segments_stay_inside_whatever_the_arrays_hold(shim, seed):
     got, total = _segments(shim, lens, cu, T, B, width, heads, group, rows, 5)
     assert sum(s[4] for c in got for s in c) == total
     for c in got:
-        for b, i, h, first, count, units, k0, k1 in c:
+        for b, i, h, first, count, units, k0, k1, _ in c:
             assert 0 <= b < B and 0 <= h < heads and 0 <= i and (i * rows) // group < T
             assert 0 <= first and count >= 1 and first + count <= units <= max(1, -(-width * 16 // 64))
             assert k1 <= width * 16
