@@ -30,18 +30,17 @@ namespace kv {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kSub = 32;                      // keys of one load of one warp
-constexpr int kRing = 24576;                  // bytes of one warp's ring
 constexpr int kPass = 64;                     // dims that warps exchange at a time
 constexpr int kPitch = kPass + 8;             // floats; conflict-free for the fragments' order
 constexpr int kUnitLog2 = 6;                  // units of 64 keys
 
-template <int D>
+template <int D, int NB>
 struct Shape {
+    static constexpr int kWarps = NB == 1 ? (D == 128 ? 12 : 16) : (D == 128 ? 8 : 12);   // as the registers allow
+    static constexpr int kThreads = 32 * kWarps;
     static constexpr int kStage = kSub * D * 2;               // K and V of one load
-    static constexpr int kStages = kRing / kStage;
+    static constexpr int kStages = (D == 128 ? 192 : 160) * 1024 / (kWarps * kStage);     // of one warp's ring
 };
 
 struct __align__(16) Meta {                   // of one load
@@ -50,15 +49,16 @@ struct __align__(16) Meta {                   // of one load
     int pad[2];
 };
 
-template <int D>
+template <int D, int NB>
 struct __align__(1024) Smem {
-    uint8_t ring[kWarps][kRing];
+    static constexpr int kWarps = Shape<D, NB>::kWarps, kStages = Shape<D, NB>::kStages;
+    uint8_t ring[kWarps][kStages * Shape<D, NB>::kStage];
     float pass[kWarps][8][kPitch];
     float ml[kWarps][8][2];
-    Meta meta[kWarps][Shape<D>::kStages];
+    Meta meta[kWarps][kStages];
     Segment segs[kSegments];
     int count;                                // of segs
-    uint64_t full[kWarps][Shape<D>::kStages];
+    uint64_t full[kWarps][kStages];
     int abort;
 };
 
@@ -77,7 +77,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 
 // The loads of one warp, in order: the 32-key pieces of each segment that are
-// this warp's (piece w, w + 8, ... of the segment).
+// this warp's (every kWarps-th from the warp-th on).
 struct Loads {
     int seg;                                  // index of the segment
     int key, keys;                            // the piece's first key, the segment's last key + 1
@@ -304,13 +304,13 @@ __device__ __forceinline__ void write_row(const AttendArgs& a, int begin, int ro
 }
 
 template <int D, int NB>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     kv_attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                      const AttendArgs a) {
-    constexpr int kStages = Shape<D>::kStages, kStage = Shape<D>::kStage;
+    constexpr int kWarps = Shape<D, NB>::kWarps, kStages = Shape<D, NB>::kStages, kStage = Shape<D, NB>::kStage;
     constexpr int kRows = 8 * NB;
     extern __shared__ uint8_t raw[];
-    Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    Smem<D, NB>& sm = *reinterpret_cast<Smem<D, NB>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, t = lane % 4;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel waits for this one's end
     if (tid == 0) sm.abort = 0;
@@ -609,11 +609,11 @@ size_t part_bytes(int rows, int D, int blocks) { return ((size_t)blocks * 2 * ro
 template <int D, int NB>
 cudaError_t launch(const CUtensorMap& k_map, const CUtensorMap& v_map, const AttendArgs& a, int blocks,
                    cudaStream_t stream) {
-    const int bytes = (int)sizeof(Smem<D>) + 1024;
+    const int bytes = (int)sizeof(Smem<D, NB>) + 1024;
     // an attribute of the function on the current device: set on every call, which keeps no state here
     const cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kv_attend_kernel<D, NB><<<blocks, kThreads, bytes, stream>>>(k_map, v_map, a);
+    kv_attend_kernel<D, NB><<<blocks, Shape<D, NB>::kThreads, bytes, stream>>>(k_map, v_map, a);
     return cudaGetLastError();
 }
 
