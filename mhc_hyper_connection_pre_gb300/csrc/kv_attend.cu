@@ -17,12 +17,13 @@
 //
 // What bounds it: the cache is read once, 2 * head_dim bytes a key and head
 // for 4 * head_dim * group operations, far below the matrix rate for groups up
-// to 16: HBM.  So every warp runs on its own, with its own ring of TMA loads
-// (24 KB, 192 KB in flight on an SM) and its own part of the keys, and the
-// warps of a block meet only when a segment ends.  All blocks take equally
-// many units of 64 keys whatever the lengths are (kv_index.cuh); what a border
-// cuts is left as partial sums in the workspace and joined by a second, small
-// kernel.
+// to 16: HBM, as long as the conversion keeps up.  Every warp runs on its own:
+// it has its own equal share of all units of 32 keys, whatever the lengths are
+// (kv_index.cuh), its own ring of TMA loads, 192 KB in flight on an SM together,
+// and it meets no other warp.  A block-wide join of the warps at each tile's
+// end cost 10 us a tile and more in barriers and idle warps.  Tiles that a
+// border between shares cuts are left as partial sums in the workspace and
+// joined by a second kernel.
 #include "kv_attend.cuh"
 
 namespace mhc {
@@ -31,16 +32,15 @@ namespace kv {
 namespace {
 
 constexpr int kSub = 32;                      // keys of one load of one warp
-constexpr int kPass = 64;                     // dims that warps exchange at a time
-constexpr int kPitch = kPass + 8;             // floats; conflict-free for the fragments' order
-constexpr int kUnitLog2 = 6;                  // units of 64 keys
+constexpr int kQueue = 8;                     // segments that a warp's loads may be ahead of its products
+constexpr int kUnitLog2 = 5;                  // units of 32 keys, one load
 
 template <int D, int NB>
 struct Shape {
     static constexpr int kWarps = NB == 1 ? (D == 128 ? 12 : 16) : (D == 128 ? 8 : 12);   // as the registers allow
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kStage = kSub * D * 2;               // K and V of one load
-    static constexpr int kStages = (D == 128 ? 192 : 160) * 1024 / (kWarps * kStage);     // of one warp's ring
+    static constexpr int kStages = 192 * 1024 / (kWarps * kStage);     // of one warp's ring
 };
 
 struct __align__(16) Meta {                   // of one load
@@ -53,11 +53,10 @@ template <int D, int NB>
 struct __align__(1024) Smem {
     static constexpr int kWarps = Shape<D, NB>::kWarps, kStages = Shape<D, NB>::kStages;
     uint8_t ring[kWarps][kStages * Shape<D, NB>::kStage];
-    float pass[kWarps][8][kPitch];
-    float ml[kWarps][8][2];
     Meta meta[kWarps][kStages];
-    Segment segs[kSegments];
-    int count;                                // of segs
+    Segment queue[kWarps][kQueue];
+    Plan plan[kWarps];
+    Census census;
     uint64_t full[kWarps][kStages];
     int abort;
 };
@@ -76,21 +75,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
-// The loads of one warp, in order: the 32-key pieces of each segment that are
-// this warp's (every kWarps-th from the warp-th on).
-struct Loads {
-    int seg;                                  // index of the segment
-    int key, keys;                            // the piece's first key, the segment's last key + 1
-};
-
-__device__ __forceinline__ void loads_settle(Loads& l, const Segment* segs, int count, const Cut& cut, int warp) {
-    while (l.key >= l.keys) {                 // on to a segment that has a piece for this warp
-        if (++l.seg >= count) return;
-        keys_of(segs[l.seg], cut, l.key, l.keys);
-        l.key += warp * kSub;
-    }
-}
-
 // Word x of the dims that row group g holds of key r's values.
 template <int D>
 __device__ __forceinline__ uint32_t value_word(uint32_t vs, int r, int g, int x) {
@@ -105,11 +89,13 @@ template <int D, int NB>
 struct Acc {
     float o[D / 16][NB][4];
     float m[NB][2], l[NB][2];                 // of rows 2t, 2t + 1 of each block of 8; l: this thread's share
-    float ref;                                // the value scale that o is in units of
+    float ref, inv;                           // the value scale that o is in units of, and one over it
 };
 
-template <int D, int NB, bool kFull>
-__device__ __forceinline__ void piece(uint32_t ks, uint32_t vs, const Meta& meta, const uint32_t (&q)[NB][D / 8],
+// `full`: every row sees all of them.  One copy of the code for both cases, as a
+// second one would fall out of the instruction cache between its rare uses.
+template <int D, int NB>
+__device__ __forceinline__ void piece(bool full, uint32_t ks, uint32_t vs, const Meta& meta, const uint32_t (&q)[NB][D / 8],
                                       const float (&f)[NB][2], const int (&lim)[NB][2], int key0, int keys, int lane,
                                       Acc<D, NB>& acc) {
     const int g = lane / 4, t = lane % 4;
@@ -150,7 +136,7 @@ __device__ __forceinline__ void piece(uint32_t ks, uint32_t vs, const Meta& meta
 
     // logits in powers of two, masks, the running maximum
     const float k0 = meta.scale[0], k1 = meta.scale[1];
-    const bool has0 = kFull || meta.page[0] >= 0, has1 = kFull || meta.page[1] >= 0;
+    const bool has0 = meta.page[0] >= 0, has1 = meta.page[1] >= 0;
     float keep[NB][2];
     bool same = true;
 #pragma unroll
@@ -159,13 +145,12 @@ __device__ __forceinline__ void piece(uint32_t ks, uint32_t vs, const Meta& meta
         for (int e = 0; e < 2; ++e) {
             const float f0 = f[nb][e] * k0, f1 = f[nb][e] * k1;
             float x[4] = {s[0][nb][e] * f0, s[0][nb][e + 2] * f0, s[1][nb][e] * f1, s[1][nb][e + 2] * f1};
-            if (!kFull) {
-                const int n = lim[nb][e] - key0;      // keys of this piece that the row sees
-                x[0] = has0 && g < n ? x[0] : -INFINITY;
-                x[1] = has0 && g + 8 < n ? x[1] : -INFINITY;
-                x[2] = has1 && g + 16 < n ? x[2] : -INFINITY;
-                x[3] = has1 && g + 24 < n ? x[3] : -INFINITY;
-            }
+            const int n = lim[nb][e] - key0 - g;      // of this thread's keys g, g + 8, .. the row sees those below n
+            const int n0 = has0 ? n : 0, n1 = has1 ? n : 0;
+            x[0] = n0 > 0 ? x[0] : -INFINITY;
+            x[1] = n0 > 8 ? x[1] : -INFINITY;
+            x[2] = n1 > 16 ? x[2] : -INFINITY;
+            x[3] = n1 > 24 ? x[3] : -INFINITY;
             float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
@@ -191,7 +176,8 @@ __device__ __forceinline__ void piece(uint32_t ks, uint32_t vs, const Meta& meta
     const float most = fmaxf(v0, v1);
     float shrink = 1.0f;
     if (most > acc.ref) {                     // the same for the whole warp
-        shrink = acc.ref / most;
+        acc.inv = 1.0f / most;
+        shrink = acc.ref * acc.inv;
         acc.ref = most;
         same = false;
     }
@@ -208,8 +194,7 @@ __device__ __forceinline__ void piece(uint32_t ks, uint32_t vs, const Meta& meta
             }
         }
     }
-    const float inv = acc.ref > 0.0f ? 1.0f / acc.ref : 0.0f;
-    const float w0 = v0 * inv, w1 = v1 * inv;
+    const float w0 = v0 * acc.inv, w1 = v1 * acc.inv;
 
     constexpr int kVW = D / 32;               // words of a key's values that a thread holds (4 dims each)
     uint32_t nans = 0;
@@ -234,7 +219,7 @@ __device__ __forceinline__ void piece(uint32_t ks, uint32_t vs, const Meta& meta
                 v[i][0] = u.x; v[i][1] = u.y;
             }
         }
-        if (!kFull) {
+        if (!full) {
             // Keys that no row of the tile sees count as zeros, whatever their
             // bytes are.  NaN among the others must reach only the rows that
             // see its key, but 0 * NaN is NaN: it is taken out here and put
@@ -264,7 +249,7 @@ __device__ __forceinline__ void piece(uint32_t ks, uint32_t vs, const Meta& meta
                     mma_f16(acc.o[2 * x + y][nb], a[y][0], a[y][1], a[y][2], a[y][3], b[nb][0], b[nb][1]);
         }
     }
-    if (!kFull && __any_sync(0xffffffffu, nans != 0)) {
+    if (!full && __any_sync(0xffffffffu, nans != 0)) {
 #pragma unroll 1
         for (int r = 0; r < kSub && key0 + r < keys; ++r) {
             if (!(r < 16 ? has0 : has1)) continue;
@@ -283,31 +268,17 @@ __device__ __forceinline__ void piece(uint32_t ks, uint32_t vs, const Meta& meta
     }
 }
 
-// Dim of position p of the order in which the fragments hold a head's dims:
-// block j = p / 16 of O^T, its row group g = p / 2 % 8, first or second.
-template <int D>
-__device__ __forceinline__ int dim_of(int p) {
-    return (D / 8) * ((p / 2) % 8) + 2 * (p / 16) + (p & 1);
-}
-
-// One tile's row r goes out: o[0..3] are positions p .. p + 3 (unnormalised),
-// m and l the row's maximum and sum.
-template <int D>
-__device__ __forceinline__ void write_row(const AttendArgs& a, int begin, int row, int head, int p, const float4& o,
-                                          float m, float l) {
-    const int64_t at = place_of(a, begin, row, head);
-    const float r = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t* out = a.out + at * D;
-    *reinterpret_cast<uint32_t*>(out + dim_of<D>(p)) = pack_bf16x2(o.x * r, o.y * r);
-    *reinterpret_cast<uint32_t*>(out + dim_of<D>(p + 2)) = pack_bf16x2(o.z * r, o.w * r);
-    if (p == 0 && a.lse) a.lse[at] = lse_of(m, l);
+// The plan's segment into the queue.  A call of its own: it is rare, and its
+// code does not belong between the loads'.
+__device__ __noinline__ void push_segment(const AttendArgs& a, Plan& plan, const Shares& shares, Segment& to) {
+    plan_next(plan, Lookup{a}, a.cut, shares, to);
 }
 
 template <int D, int NB>
 __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     kv_attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                     const AttendArgs a) {
-    constexpr int kWarps = Shape<D, NB>::kWarps, kStages = Shape<D, NB>::kStages, kStage = Shape<D, NB>::kStage;
+                     const __grid_constant__ AttendArgs a) {
+    constexpr int kStages = Shape<D, NB>::kStages, kStage = Shape<D, NB>::kStage;
     constexpr int kRows = 8 * NB;
     extern __shared__ uint8_t raw[];
     Smem<D, NB>& sm = *reinterpret_cast<Smem<D, NB>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -318,285 +289,308 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
         for (int i = 0; i < kStages; ++i) mbar_init(&sm.full[warp][i], 1 + 4);   // lane 0 and the four scales
         fence_mbar_init_cluster();
     }
-    if (tid == 0) a.desc[blockIdx.x].parts = 0;
+    if (warp == 0) take_census(a, sm.census, lane);
+    __syncthreads();
 
-    Planner plan;                             // of the first warp
-    uint32_t issued = 0, waited = 0;          // loads of this warp
-    for (bool begun = false;; begun = true) {
-        if (warp == 0) {
-            if (!begun) plan.begin(a, lane);
-            const int n = plan.next(a, sm.segs, lane);
-            if (lane == 0) sm.count = n;
+    // neighbouring shares go to different SMs, so that few units still spread over all of them
+    const int share = warp * gridDim.x + blockIdx.x;
+    if (lane < 2) a.desc[2 * share + lane].parts = 0;
+    Plan& plan = sm.plan[warp];
+    enter_share(a, sm.census, share, plan, lane);
+
+    uint32_t issued = 0, waited = 0;          // loads
+    uint32_t pushed = 0, popped = 0;          // segments
+    int key = 0, keys = 0, head = 0;          // of the next load: its first key, its segment's last key + 1 and head
+    const int32_t* row = nullptr;
+    int page[2];
+
+    // On to the next load; false: there is none, or none before a segment of the queue is done.
+    auto settle = [&] {
+        while (key >= keys) {
+            if (plan.w.left <= 0 || pushed - popped == kQueue) return false;
+            Segment& s = sm.queue[warp][pushed % kQueue];
+            if (lane == 0) push_segment(a, plan, sm.census.shares, s);
+            __syncwarp();
+            ++pushed;
+            key = s.key0;
+            keys = s.keys;
+            head = s.head;
+            row = a.seqs.table + (int64_t)s.b * a.seqs.width;
         }
-        __syncthreads();
-        const int count = sm.count;
-        if (count == 0) break;
+        page[0] = __ldg(row + (key >> a.seqs.page_log2));             // used only when the load is issued
+        page[1] = key + 16 < keys ? __ldg(row + ((key + 16) >> a.seqs.page_log2)) : -1;
+        return true;
+    };
+    bool more = settle();
+    auto issue = [&] {
+        const int st = issued % kStages;
+        const bool ok0 = page[0] >= 0 && page[0] < a.seqs.num_pages;
+        const bool ok1 = page[1] >= 0 && page[1] < a.seqs.num_pages;
+        if ((!ok0 || (key + 16 < keys && !ok1)) && lane == 0) atomicOr(&g_device_status, kIndexError);
+        uint64_t* bar = &sm.full[warp][st];
+        Meta& meta = sm.meta[warp][st];
+        if (lane < 4) {
+            const int mb = lane & 1;
+            if (mb ? ok1 : ok0)
+                copy_async4(&meta.scale[lane],
+                            (lane < 2 ? a.k_scale : a.v_scale) + (int64_t)page[mb] * a.cut.heads + head);
+            arrive_after_copies(bar);
+        }
+        if (lane == 0) {
+            uint8_t* dst = sm.ring[warp] + st * kStage;
+            meta.page[0] = ok0 ? page[0] : -1;
+            meta.page[1] = ok1 ? page[1] : -1;
+            const int block0 = page[0] * a.cut.heads + head, block1 = page[1] * a.cut.heads + head;
+            if (a.seqs.page_log2 >= 5) {      // both halves lie in one page
+                const int slot = key & ((1 << a.seqs.page_log2) - 1);
+                mbar_arrive_expect_tx(bar, ok0 ? kStage : 0);
+                if (ok0) {
+                    tma_load_3d(dst, &k_map, 0, slot, block0, bar);
+                    tma_load_3d(dst + kStage / 2, &v_map, 0, slot, block0, bar);
+                }
+            } else {
+                mbar_arrive_expect_tx(bar, (ok0 ? kStage / 2 : 0) + (ok1 ? kStage / 2 : 0));
+                if (ok0) {
+                    tma_load_3d(dst, &k_map, 0, 0, block0, bar);
+                    tma_load_3d(dst + kStage / 2, &v_map, 0, 0, block0, bar);
+                }
+                if (ok1) {
+                    tma_load_3d(dst + kStage / 4, &k_map, 0, 0, block1, bar);
+                    tma_load_3d(dst + kStage / 2 + kStage / 4, &v_map, 0, 0, block1, bar);
+                }
+            }
+        }
+        ++issued;
+        key += kSub;
+        more = settle();
+    };
 
-        Loads ld{-1, 0, 0};
-        loads_settle(ld, sm.segs, count, a.cut, warp);
-        int page[2] = {-1, -1};
-        auto find_pages = [&] {               // of the next load; used only when it is issued
-            if (ld.seg >= count) return;
-            const int32_t* row = a.seqs.table + (int64_t)sm.segs[ld.seg].b * a.seqs.width;
-            page[0] = __ldg(row + (ld.key >> a.seqs.page_log2));
-            page[1] = ld.key + 16 < ld.keys ? __ldg(row + ((ld.key + 16) >> a.seqs.page_log2)) : -1;
-        };
-        auto issue = [&] {
-            if (ld.seg >= count || *(volatile int*)&sm.abort) return;
-            const int st = issued % kStages;
-            const int slot = ld.key & ((1 << a.seqs.page_log2) - 1), head = sm.segs[ld.seg].head;
-            const bool ok0 = page[0] >= 0 && page[0] < a.seqs.num_pages;
-            const bool ok1 = page[1] >= 0 && page[1] < a.seqs.num_pages;
-            const bool two = ld.key + 16 < ld.keys;
-            if ((!ok0 || (two && !ok1)) && lane == 0) atomicOr(&g_device_status, kIndexError);
-            uint64_t* bar = &sm.full[warp][st];
-            Meta& meta = sm.meta[warp][st];
-            if (lane < 4) {
-                const int mb = lane & 1;
-                if (mb ? ok1 : ok0) {
-                    const float* src = (lane < 2 ? a.k_scale : a.v_scale) + (int64_t)page[mb] * a.cut.heads + head;
-                    copy_async4(&meta.scale[lane], src);
-                }
-                arrive_after_copies(bar);
+    for (;;) {
+        if (!more) more = settle();
+        while (more && issued - waited < kStages && !*(volatile int*)&sm.abort) issue();
+        if (popped == pushed) break;
+        const Segment seg = sm.queue[warp][popped % kQueue];
+
+        // queries: thread (g, t) holds row g's dims [t D/4, (t + 1) D/4) of each block of 8 rows
+        uint32_t q[NB][D / 8];
+        float f[NB][2];
+        int lim[NB][2];
+        Acc<D, NB> acc;
+        acc.ref = acc.inv = 0.0f;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int r = nb * 8 + g;
+            uint4 u[D / 32];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) u[i] = make_uint4(0, 0, 0, 0);
+            if (r < seg.rows) {
+                int token, in_group;
+                row_of(seg, a.cut, r, token, in_group);
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    a.q + token * a.q_stride + (seg.head * a.cut.group + in_group) * D + t * (D / 4));
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) u[i] = __ldg(src + i);
             }
-            if (lane == 0) {
-                uint8_t* dst = sm.ring[warp] + st * kStage;
-                meta.page[0] = ok0 ? page[0] : -1;
-                meta.page[1] = ok1 ? page[1] : -1;
-                if (a.seqs.page_log2 >= 5) {            // both halves lie in one page
-                    mbar_arrive_expect_tx(bar, ok0 ? kStage : 0);
-                    if (ok0) {
-                        const int block = page[0] * a.cut.heads + head;
-                        tma_load_3d(dst, &k_map, 0, slot, block, bar);
-                        tma_load_3d(dst + kStage / 2, &v_map, 0, slot, block, bar);
-                    }
-                } else {
-                    mbar_arrive_expect_tx(bar, (ok0 ? kStage / 2 : 0) + (ok1 ? kStage / 2 : 0));
-                    if (ok0) {
-                        const int block = page[0] * a.cut.heads + head;
-                        tma_load_3d(dst, &k_map, 0, 0, block, bar);
-                        tma_load_3d(dst + kStage / 2, &v_map, 0, 0, block, bar);
-                    }
-                    if (ok1) {
-                        const int block = page[1] * a.cut.heads + head;
-                        tma_load_3d(dst + kStage / 4, &k_map, 0, 0, block, bar);
-                        tma_load_3d(dst + kStage / 2 + kStage / 4, &v_map, 0, 0, block, bar);
-                    }
+            float x[D / 4], top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                float y[8];
+                unpack8(u[i], y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    x[8 * i + j] = y[j];
+                    top = fmaxf(top, fabsf(y[j]));
                 }
             }
-            ++issued;
-            ld.key += kWarps * kSub;
-            loads_settle(ld, sm.segs, count, a.cut, warp);
-            find_pages();
-        };
-        find_pages();
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            int e = 134 - (int)(__float_as_uint(top) >> 23);      // 7 - floor(log2(top))
+            e = e < -120 ? -120 : (e > 120 ? 120 : e);
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) q[nb][i] = pack_f16x2(x[2 * i] * up, x[2 * i + 1] * up);
+            const float back = down * a.scale_log2;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int c = nb * 8 + 2 * t + i;
+                f[nb][i] = __shfl_sync(0xffffffffu, back, (2 * t + i) * 4);
+                lim[nb][i] = c < seg.rows ? keys_of_row(seg, a.cut, c) : 0;
+                acc.m[nb][i] = -INFINITY;
+                acc.l[nb][i] = 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc.o[j][nb][i] = 0.0f;
+        }
+        const int all_see = keys_of_row(seg, a.cut, 0);           // keys that every row sees
+
+        bool ok = true;
 #pragma unroll 1
-        for (int i = 0; i < kStages; ++i) issue();
+        for (int at = seg.key0; at < seg.keys; at += kSub) {
+            const int st = waited % kStages;
+            ok = waited != issued &&          // so after a wait that gave up
+                 __all_sync(0xffffffffu, wait_for(&sm.full[warp][st], (waited / kStages) & 1, &sm.abort));
+            if (!ok) break;
+            ++waited;
+            const uint32_t base_addr = smem_u32(sm.ring[warp] + st * kStage);
+            const Meta& meta = sm.meta[warp][st];
+            const bool full = at + kSub <= all_see && meta.page[0] >= 0 && meta.page[1] >= 0;
+            piece<D, NB>(full, base_addr, base_addr + kStage / 2, meta, q, f, lim, at, seg.keys, lane, acc);
+            __syncwarp();                     // every lane has read the stage
+            if (more && !*(volatile int*)&sm.abort) issue();
+        }
+        if (!ok) break;
 
-        for (int index = 0; index < count; ++index) {
-            const Segment seg = sm.segs[index];
-            const SeqInfo info = seg.info;
-            int key0, keys;
-            keys_of(seg, a.cut, key0, keys);
-            const int first_row = seg.tile * kRows;
-            const int rows = info.rows - first_row < kRows ? info.rows - first_row : kRows;
-
-            // queries: thread (g, t) holds row g's dims [t D/4, (t + 1) D/4) of each block of 8 rows
-            uint32_t q[NB][D / 8];
-            float f[NB][2];
-            int lim[NB][2];
-            Acc<D, NB> acc;
-            acc.ref = 0.0f;
+        // the rows go out, or to the workspace: thread (g, t) has D/8 dims of rows 2t and 2t + 1
+        const bool whole = seg.parts == 1;
+        const int slot = seg.owner == share ? 1 : 0;
+        float* part = part_of(a, share, slot, D);
+        if (!whole && lane == 0) a.desc[2 * share + slot] = PartDesc{seg.parts, seg.owner, seg};
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                const int row = nb * 8 + g;
-                uint4 u[D / 32];
+        for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) u[i] = make_uint4(0, 0, 0, 0);
-                if (row < rows) {
-                    const int r = first_row + row, token = info.begin + r / a.cut.group;
-                    const int head = seg.head * a.cut.group + r % a.cut.group;
-                    const uint4* src =
-                        reinterpret_cast<const uint4*>(a.q + token * a.q_stride + head * D + t * (D / 4));
+            for (int e = 0; e < 2; ++e) {
+                float l = acc.l[nb][e];
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                const float m = acc.m[nb][e];
+                const int r = nb * 8 + 2 * t + e;
+                if (r >= seg.rows) continue;
+                const float by = whole ? (l == 0.0f ? 0.0f : acc.ref / l) : acc.ref;
+                if (whole) {
+                    const int64_t to = place_of(a, seg, r);
+                    uint4* out = reinterpret_cast<uint4*>(a.out + to * D + g * (D / 8));
 #pragma unroll
-                    for (int i = 0; i < D / 32; ++i) u[i] = __ldg(src + i);
-                }
-                float x[D / 4], top = 0.0f;
+                    for (int j = 0; j < D / 16; j += 4) {
+                        float y[8];
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    float y[8];
-                    unpack8(u[i], y);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        x[8 * i + j] = y[j];
-                        top = fmaxf(top, fabsf(y[j]));
-                    }
-                }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                int e = 134 - (int)(__float_as_uint(top) >> 23);      // 7 - floor(log2(top))
-                e = e < -120 ? -120 : (e > 120 ? 120 : e);
-                const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-                const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) q[nb][i] = pack_f16x2(x[2 * i] * up, x[2 * i + 1] * up);
-                const float back = down * a.scale_log2;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int c = nb * 8 + 2 * t + i;
-                    f[nb][i] = __shfl_sync(0xffffffffu, back, (2 * t + i) * 4);
-                    lim[nb][i] = c < rows ? keys_of_row(info, a.cut, first_row + c) : 0;
-                    acc.m[nb][i] = -INFINITY;
-                    acc.l[nb][i] = 0.0f;
-                }
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc.o[j][nb][i] = 0.0f;
-            }
-            const int all_see = keys_of_row(info, a.cut, first_row);  // keys that every row sees
-
-            for (int key = key0 + warp * kSub; key < keys; key += kWarps * kSub) {
-                const int st = waited % kStages;
-                if (waited == issued) break;  // after a wait that gave up
-                const bool ok = wait_for(&sm.full[warp][st], (waited / kStages) & 1, &sm.abort);
-                ++waited;
-                if (!ok) break;
-                const uint32_t base_addr = smem_u32(sm.ring[warp] + st * kStage);
-                const Meta& meta = sm.meta[warp][st];
-                const bool full = key + kSub <= all_see && meta.page[0] >= 0 && meta.page[1] >= 0;
-                if (full)
-                    piece<D, NB, true>(base_addr, base_addr + kStage / 2, meta, q, f, lim, key, keys, lane, acc);
-                else
-                    piece<D, NB, false>(base_addr, base_addr + kStage / 2, meta, q, f, lim, key, keys, lane, acc);
-                __syncwarp();                 // every lane has read the stage
-                issue();
-            }
-
-            // the warps' sums of this segment, joined
-            const bool whole = seg.first == 0 && seg.count == seg.units;
-            const int slot = seg.first == 0 ? 1 : 0;
-            float* part = part_of(a, blockIdx.x, slot, D);
-            if (!whole && slot && tid == 0)
-                a.desc[blockIdx.x] = PartDesc{seg.parts, info.begin, first_row, rows, seg.head, {}};
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float l = acc.l[nb][e];
-                    l += __shfl_xor_sync(0xffffffffu, l, 4);
-                    l += __shfl_xor_sync(0xffffffffu, l, 8);
-                    l += __shfl_xor_sync(0xffffffffu, l, 16);
-                    if (g == 0) {
-                        sm.ml[warp][2 * t + e][0] = acc.m[nb][e];
-                        sm.ml[warp][2 * t + e][1] = l;
-                    }
-                }
-#pragma unroll
-                for (int pass = 0; pass < D / kPass; ++pass) {
-#pragma unroll
-                    for (int j = 0; j < kPass / 16; ++j) {
-                        const float(&o)[4] = acc.o[pass * (kPass / 16) + j][nb];
-                        float* at = &sm.pass[warp][2 * t][j * 16 + 2 * g];
-                        *reinterpret_cast<float2*>(at) = make_float2(o[0] * acc.ref, o[2] * acc.ref);
-                        *reinterpret_cast<float2*>(at + kPitch) = make_float2(o[1] * acc.ref, o[3] * acc.ref);
-                    }
-                    __syncthreads();
-                    const int row = tid / 16, p = (tid % 16) * 4;     // 8 rows x 16 threads: half of the block
-                    if (tid < 128) {
-                        float m = -INFINITY;
-#pragma unroll
-                        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.ml[w][row][0]);
-                        const float zero = m == -INFINITY ? 0.0f : m;
-                        float l = 0.0f;
-                        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                        for (int w = 0; w < kWarps; ++w) {
-                            const float x = ex2(sm.ml[w][row][0] - zero);
-                            const float4 y = *reinterpret_cast<const float4*>(&sm.pass[w][row][p]);
-                            l = fmaf(x, sm.ml[w][row][1], l);
-                            o.x = fmaf(x, y.x, o.x);
-                            o.y = fmaf(x, y.y, o.y);
-                            o.z = fmaf(x, y.z, o.z);
-                            o.w = fmaf(x, y.w, o.w);
+                        for (int i = 0; i < 4; ++i) {
+                            y[2 * i] = acc.o[j + i][nb][e] * by;
+                            y[2 * i + 1] = acc.o[j + i][nb][e + 2] * by;
                         }
-                        const int r = nb * 8 + row, at = pass * kPass + p;
-                        if (r < rows) {
-                            if (whole) {
-                                write_row<D>(a, info.begin, first_row + r, seg.head, at, o, m, l);
-                            } else {
-                                float* dst = part + r * D;
-                                *reinterpret_cast<float2*>(dst + dim_of<D>(at)) = make_float2(o.x, o.y);
-                                *reinterpret_cast<float2*>(dst + dim_of<D>(at + 2)) = make_float2(o.z, o.w);
-                                if (at == 0)
-                                    *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(m, l);
-                            }
-                        }
+                        out[j / 4] = pack8(y);
                     }
-                    __syncthreads();
+                    if (g == 0 && a.lse) a.lse[to] = lse_of(m, l);
+                } else {
+                    float4* out = reinterpret_cast<float4*>(part + r * D + g * (D / 8));
+#pragma unroll
+                    for (int j = 0; j < D / 16; j += 2)
+                        out[j / 2] = make_float4(acc.o[j][nb][e] * by, acc.o[j][nb][e + 2] * by,
+                                                 acc.o[j + 1][nb][e] * by, acc.o[j + 1][nb][e + 2] * by);
+                    if (g == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(m, l);
                 }
             }
         }
-        __syncthreads();                      // before the next segments are planned
+        ++popped;
     }
     // after a wait that gave up: the loads still under way
     for (; waited != issued; ++waited) mbar_wait_drain(&sm.full[warp][waited % kStages], (waited / kStages) & 1);
 }
 
-// Joins the parts of the tile that block blockIdx.x of the attention began
-// and did not finish: its slot 1, then slot 0 of the blocks after it.  A row is
-// D / 4 lanes' work: first a lane for each part finds the parts' weights, then
-// each lane adds up its four dims.  Every load but the first depends on nothing
-// that came before it.
+// Joins the tiles that borders between shares have cut.  A tile's parts are
+// slot 1 of the share that began it (its owner) and slot 0 of the shares after
+// it; the blocks of these shares divide the tile's rows among them.  With few
+// parts a warp takes a row; with many a block does, its warps dividing the
+// parts.  Every load but the first depends on nothing that came before it.
 template <int D>
 __global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a) {
-    constexpr int kLanes = D / 4, kRows = 256 / kLanes;
+    constexpr int kDims = D / 32, kMany = 32;
+    __shared__ float acc[8][D + 2];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x;
-    const PartDesc d = a.desc[c];
-    if (d.parts == 0) return;
-    const int lane = threadIdx.x % kLanes;
-    const int64_t next = 2 * (int64_t)a.cut.tile_rows * (D + 2);      // from a block's part to the next block's
-    const float* first = part_of(a, c, 1, D);
-    const float* rest = part_of(a, c + 1, 0, D) - next;               // part k, k > 0, at rest + k * next
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t next = 2 * (int64_t)a.cut.tile_rows * (D + 2);      // from a share's part to the next share's
     const int ml = a.cut.tile_rows * D;
-    for (int r0 = blockIdx.y * kRows; r0 < d.rows; r0 += gridDim.y * kRows) {
-        const int row = r0 + threadIdx.x / kLanes, r = row < d.rows ? row : d.rows - 1;   // whole warps shuffle
-        float m = -INFINITY, l = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int base = 0; base < d.parts; base += kLanes) {
-            const int n = d.parts - base < kLanes ? d.parts - base : kLanes, k = base + lane;
-            float2 mine = make_float2(-INFINITY, 0.0f);
-            if (lane < n) mine = *reinterpret_cast<const float2*>((k ? rest + k * next : first) + ml + 2 * r);
-            float now = mine.x;
+    for (int slot = 0; slot < 2; ++slot) {
+        const PartDesc& d = a.desc[2 * blockIdx.x + slot];
+        const int parts = d.parts;
+        if (parts == 0) continue;
+        const int owner = d.owner, mine = blockIdx.x - owner, rows = d.seg.rows;
+        const float* first = part_of(a, owner, 1, D);
+        const float* rest = part_of(a, owner + 1, 0, D) - next;       // part k, k > 0, at rest + k * next
+
+        // the weighted sum of row r over parts k0, k0 + step, ..
+        auto sum = [&](int r, int k0, int step, float& m, float& l, float (&o)[kDims]) {
+            m = -INFINITY;
+            l = 0.0f;
 #pragma unroll
-            for (int i = kLanes / 2; i; i >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, i));
-            now = fmaxf(now, m);
-            const float zero = now == -INFINITY ? 0.0f : now, keep = ex2(m - zero);
-            const float w = ex2(mine.x - zero);
-            float sum = w * mine.y;
+            for (int i = 0; i < kDims; ++i) o[i] = 0.0f;
+            for (int base = k0; base < parts; base += 32 * step) {
+                const int k = base + lane * step, left = (parts - base + step - 1) / step, n = left < 32 ? left : 32;
+                float2 own = make_float2(-INFINITY, 0.0f);
+                if (lane < n) own = *reinterpret_cast<const float2*>((k ? rest + k * next : first) + ml + 2 * r);
+                float now = own.x;
 #pragma unroll
-            for (int i = kLanes / 2; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-            l = fmaf(l, keep, sum);
-            o.x *= keep; o.y *= keep; o.z *= keep; o.w *= keep;
-            m = now;
+                for (int i = 16; i; i >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, i));
+                now = fmaxf(now, m);
+                const float zero = now == -INFINITY ? 0.0f : now, keep = ex2(m - zero), w = ex2(own.x - zero);
+                float all = w * own.y;
+#pragma unroll
+                for (int i = 16; i; i >>= 1) all += __shfl_xor_sync(0xffffffffu, all, i);
+                l = fmaf(l, keep, all);
+                m = now;
+#pragma unroll
+                for (int i = 0; i < kDims; ++i) o[i] *= keep;
 #pragma unroll 8
-            for (int i = 0; i < n; ++i) {
-                const float x = __shfl_sync(0xffffffffu, w, i, kLanes);
-                const float4 y =
-                    reinterpret_cast<const float4*>((base + i ? rest + (base + i) * next : first) + r * D)[lane];
-                o.x = fmaf(x, y.x, o.x);
-                o.y = fmaf(x, y.y, o.y);
-                o.z = fmaf(x, y.z, o.z);
-                o.w = fmaf(x, y.w, o.w);
+                for (int j = 0; j < n; ++j) {
+                    const float x = __shfl_sync(0xffffffffu, w, j);
+                    const int kk = base + j * step;
+                    const float* src = (kk ? rest + kk * next : first) + r * D + lane * kDims;
+                    if constexpr (D == 128) {
+                        const float4 y = *reinterpret_cast<const float4*>(src);
+                        o[0] = fmaf(x, y.x, o[0]);
+                        o[1] = fmaf(x, y.y, o[1]);
+                        o[2] = fmaf(x, y.z, o[2]);
+                        o[3] = fmaf(x, y.w, o[3]);
+                    } else {
+                        const float2 y = *reinterpret_cast<const float2*>(src);
+                        o[0] = fmaf(x, y.x, o[0]);
+                        o[1] = fmaf(x, y.y, o[1]);
+                    }
+                }
+            }
+        };
+        auto write = [&](int r, float m, float l, const float (&o)[kDims]) {
+            const int64_t to = place_of(a, d.seg, r);
+            const float y = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+            for (int i = 0; i < kDims; i += 2)
+                *reinterpret_cast<uint32_t*>(a.out + to * D + lane * kDims + i) = pack_bf16x2(o[i] * y, o[i + 1] * y);
+            if (lane == 0 && a.lse) a.lse[to] = lse_of(m, l);
+        };
+        float m, l, o[kDims];
+        if (parts <= kMany) {
+            for (int r = mine + parts * (warp + 8 * blockIdx.y); r < rows; r += parts * 8 * gridDim.y) {
+                sum(r, 0, 1, m, l, o);
+                write(r, m, l, o);
+            }
+        } else {
+            for (int r = mine + parts * blockIdx.y; r < rows; r += parts * gridDim.y) {   // the same for the block
+                sum(r, warp, 8, m, l, o);
+#pragma unroll
+                for (int i = 0; i < kDims; ++i) acc[warp][lane * kDims + i] = o[i];
+                if (lane == 0) acc[warp][D] = m, acc[warp][D + 1] = l;
+                __syncthreads();
+                if (warp == 0) {
+                    m = -INFINITY;
+                    for (int w = 0; w < 8; ++w) m = fmaxf(m, acc[w][D]);
+                    const float zero = m == -INFINITY ? 0.0f : m;
+                    l = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kDims; ++i) o[i] = 0.0f;
+                    for (int w = 0; w < 8; ++w) {
+                        const float x = ex2(acc[w][D] - zero);
+                        l = fmaf(x, acc[w][D + 1], l);
+#pragma unroll
+                        for (int i = 0; i < kDims; ++i) o[i] = fmaf(x, acc[w][lane * kDims + i], o[i]);
+                    }
+                    write(r, m, l, o);
+                }
+                __syncthreads();
             }
         }
-        if (row >= d.rows) continue;
-        const int64_t to = place_of(a, d.begin, d.first_row + r, d.head);
-        const float y = l == 0.0f ? 0.0f : 1.0f / l;
-        *reinterpret_cast<uint2*>(a.out + to * D + 4 * lane) =
-            make_uint2(pack_bf16x2(o.x * y, o.y * y), pack_bf16x2(o.z * y, o.w * y));
-        if (lane == 0 && a.lse) a.lse[to] = lse_of(m, l);
     }
 }
 
@@ -604,7 +598,14 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a) {
 // of this file; more: the tensor-memory kernel's 256.
 int tile_rows(int group, int64_t B, int64_t T) { return T * group > 16 * B ? 256 : (T * group > 8 * B ? 16 : 8); }
 
-size_t part_bytes(int rows, int D, int blocks) { return ((size_t)blocks * 2 * rows * (D + 2) * 4 + 255) / 256 * 256; }
+// Shares of the work: warps, or the tensor-memory kernel's blocks.
+int shares_of(int rows, int D, int num_sms) {
+    if (rows == 256) return num_sms;
+    if (D == 64) return num_sms * (rows == 8 ? Shape<64, 1>::kWarps : Shape<64, 2>::kWarps);
+    return num_sms * (rows == 8 ? Shape<128, 1>::kWarps : Shape<128, 2>::kWarps);
+}
+
+size_t part_bytes(int rows, int D, int shares) { return ((size_t)shares * 2 * rows * (D + 2) * 4 + 255) / 256 * 256; }
 
 template <int D, int NB>
 cudaError_t launch(const CUtensorMap& k_map, const CUtensorMap& v_map, const AttendArgs& a, int blocks,
@@ -617,15 +618,15 @@ cudaError_t launch(const CUtensorMap& k_map, const CUtensorMap& v_map, const Att
     return cudaGetLastError();
 }
 
-cudaError_t launch_join(const AttendArgs& a, int head_dim, int blocks, cudaStream_t stream) {
-    if (blocks < 2) return cudaSuccess;
+cudaError_t launch_join(const AttendArgs& a, int head_dim, cudaStream_t stream) {
+    if (a.shares < 2) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(blocks - 1, a.cut.tile_rows > 16 ? 8 : 1, 1);
+    cfg.gridDim = dim3(a.shares, a.cut.tile_rows > 16 ? 8 : 1, 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = stream;
     return cudaLaunchKernelEx(&cfg, head_dim == 64 ? kv_join_kernel<64> : kv_join_kernel<128>, a);
@@ -637,7 +638,8 @@ cudaError_t launch_kv_attend_tc(const AttendArgs& a, const uint8_t* k, const uin
                                 cudaStream_t stream);
 
 size_t kv_attend_workspace(int heads, int head_dim, int q_heads, int64_t B, int64_t T, int num_sms) {
-    return part_bytes(tile_rows(q_heads / heads, B, T), head_dim, num_sms) + (size_t)num_sms * sizeof(PartDesc);
+    const int rows = tile_rows(q_heads / heads, B, T), shares = shares_of(rows, head_dim, num_sms);
+    return part_bytes(rows, head_dim, shares) + (size_t)shares * 2 * sizeof(PartDesc);
 }
 
 cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* v, const float* k_scale,
@@ -645,9 +647,10 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
                              int q_heads, float softmax_scale, uint16_t* out, float* lse, void* workspace,
                              int num_sms, cudaStream_t stream) {
     AttendArgs a;
-    const int rows = tile_rows(q_heads / heads, seqs.B, seqs.T);
+    const int group = q_heads / heads, rows = tile_rows(group, seqs.B, seqs.T);
     a.seqs = seqs;
-    a.cut = Cut{heads, q_heads / heads, rows, rows == 256 ? kUnitLog2 + 1 : kUnitLog2};
+    a.cut = Cut{heads, group, rows, rows == 256 ? 7 : kUnitLog2, 65536 / group + 1};
+    a.shares = shares_of(rows, head_dim, num_sms);
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     a.q = q;
@@ -656,7 +659,7 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
     a.out = out;
     a.lse = lse;
     a.part = static_cast<float*>(workspace);
-    a.desc = reinterpret_cast<PartDesc*>(static_cast<uint8_t*>(workspace) + part_bytes(rows, head_dim, num_sms));
+    a.desc = reinterpret_cast<PartDesc*>(static_cast<uint8_t*>(workspace) + part_bytes(rows, head_dim, a.shares));
     cudaError_t e;
     if (rows == 256) {
         e = launch_kv_attend_tc(a, k, v, head_dim, num_sms, stream);
@@ -673,7 +676,7 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
             e = head_dim == 64 ? launch<64, 2>(k_map, v_map, a, num_sms, stream)
                                : launch<128, 2>(k_map, v_map, a, num_sms, stream);
     }
-    return e == cudaSuccess ? launch_join(a, head_dim, num_sms, stream) : e;
+    return e == cudaSuccess ? launch_join(a, head_dim, stream) : e;
 }
 
 cudaError_t read_attend_status(unsigned int* status) {

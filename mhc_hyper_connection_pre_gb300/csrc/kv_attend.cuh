@@ -15,16 +15,16 @@ namespace kv {
 constexpr float kLift = 10.0f;                // weights are 2^10 times the softmax's numerators
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// The tile that a block began and did not finish.
+// A part of a tile that a share has left in the workspace.
 struct PartDesc {
-    int parts;                                // blocks that share it, 0: no such tile
-    int begin, first_row, rows, head;         // rows of the tile
-    int pad[3];
+    int parts, owner;                         // as the segment's; parts 0: nothing here
+    Segment seg;
 };
 
 struct AttendArgs {
     Seqs seqs;
     Cut cut;
+    int shares;
     const float* k_scale;
     const float* v_scale;
     const uint16_t* q;
@@ -32,16 +32,16 @@ struct AttendArgs {
     float scale_log2;                         // softmax_scale * log2(e)
     uint16_t* out;
     float* lse;
-    float* part;                              // [blocks][2]: weighted values [tile_rows][D], maximum and sum [tile_rows][2]
-    PartDesc* desc;                           // [blocks]: the tile that a block began and did not finish
+    float* part;                              // [shares][2]: weighted values [tile_rows][D], maximum and sum [tile_rows][2]
+    PartDesc* desc;                           // [shares][2]
 };
 
-// Part `slot` of a block: 1 a tile that the block began, 0 one that it went on with.
-__device__ __forceinline__ float* part_of(const AttendArgs& a, int block, int slot, int D) {
-    return a.part + ((int64_t)block * 2 + slot) * a.cut.tile_rows * (D + 2);
+// Part `slot` of a share: 1 of the tile that it began (it is the owner), 0 of one that it went on with.
+__device__ __forceinline__ float* part_of(const AttendArgs& a, int share, int slot, int D) {
+    return a.part + ((int64_t)share * 2 + slot) * a.cut.tile_rows * (D + 2);
 }
 
-constexpr int kSegments = 32;                 // of a block that are planned at a time
+constexpr int kSegments = 32;                 // that the tensor-memory kernel plans at a time
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -86,94 +86,76 @@ __device__ __forceinline__ void check_offsets(const AttendArgs& a) {
         atomicOr(&g_device_status, kIndexError);
 }
 
-// Finds a block's segments.  Run by one warp, every lane alike but for the
-// sequences it looks up, and kept out of the other warps' code: the kernels'
-// loops have to fit the instruction cache.
-struct Planner {
-    Walk w;
-    int b;                                    // the walk's sequence
-    SeqInfo info;
-    int64_t total;                            // units of the line
-    int base;                                 // sequences base .. base + 31 are at hand, one a lane
-    SeqInfo at_hand;
+// Finds sequence b for a plan.
+struct Lookup {
+    const AttendArgs& a;
+    __device__ __forceinline__ SeqInfo operator()(int b) const { return info_of(span_of(a.seqs, b), a.cut.group); }
+};
 
-    __device__ __forceinline__ SeqInfo look_up(const AttendArgs& a, int seq) const {
-        return seq < a.seqs.B ? info_of(span_of(a.seqs, seq), a.cut.group) : SeqInfo{0, 0, 0, 0};
-    }
+// The line's shares, and how many units precede the end of each 32nd of the
+// sequences.
+struct Census {
+    Shares shares;
+    int each;                                 // sequences of a 32nd
+    int64_t upto[32];
+};
 
-    __device__ __forceinline__ void fetch(const AttendArgs& a, int seq, int lane) {
-        if (seq - base >= 32) {
-            base = seq;
-            at_hand = look_up(a, seq + lane);
-        }
-        const int from = seq - base;
-        info.begin = __shfl_sync(0xffffffffu, at_hand.begin, from);
-        info.rows = __shfl_sync(0xffffffffu, at_hand.rows, from);
-        info.len = __shfl_sync(0xffffffffu, at_hand.len, from);
-        info.before = __shfl_sync(0xffffffffu, at_hand.before, from);
-        b = seq;
-    }
-
-    // Counts the units of all sequences (lane i those of the i-th of 32 equal
-    // parts) and enters the block's share.
-    __device__ void begin(const AttendArgs& a, int lane) {
-        const int each = (a.seqs.B + 31) / 32, first = lane * each;
-        const int end = first + each < a.seqs.B ? first + each : a.seqs.B;
-        int64_t mine = 0;
-        bool bad = false;
+// Counts the units of all sequences, lane i those of the i-th 32nd.  One warp.
+__device__ inline void take_census(const AttendArgs& a, Census& c, int lane) {
+    const int each = (a.seqs.B + 31) / 32, first = lane * each;
+    const int end = first + each < a.seqs.B ? first + each : a.seqs.B;
+    int64_t mine = 0;
+    bool bad = false;
 #pragma unroll 1
-        for (int i = first; i < end; ++i) {
-            const Span sp = span_of(a.seqs, i);
-            bad = bad || sp.bad;
-            mine += units_of_seq(info_of(sp, a.cut.group), a.cut);
-        }
-        if (blockIdx.x == 0) {
-            if (lane == 0 && a.seqs.cu) bad = bad || a.seqs.cu[0] != 0 || a.seqs.cu[a.seqs.B] != a.seqs.T;
-            if (bad) atomicOr(&g_device_status, kIndexError);
-        }
-        int64_t upto = mine;
+    for (int i = first; i < end; ++i) {
+        const Span sp = span_of(a.seqs, i);
+        bad = bad || sp.bad;
+        mine += units_of_seq(info_of(sp, a.cut.group), a.cut);
+    }
+    if (blockIdx.x == 0) {
+        if (lane == 0 && a.seqs.cu) bad = bad || a.seqs.cu[0] != 0 || a.seqs.cu[a.seqs.B] != a.seqs.T;
+        if (bad) atomicOr(&g_device_status, kIndexError);
+    }
+    int64_t upto = mine;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += up;
-        }
-        int64_t from, to;
-        total = __shfl_sync(0xffffffffu, upto, 31);
-        share_of(total, blockIdx.x, gridDim.x, from, to);
-        w.left = to - from;
-        if (w.left <= 0) return;
-        const int part = __ffs(__ballot_sync(0xffffffffu, upto > from)) - 1;
-        int64_t r = from - __shfl_sync(0xffffffffu, upto - mine, part);
-        base = part * each;
-        at_hand = look_up(a, base + lane);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += up;
+    }
+    c.upto[lane] = upto;
+    if (lane == 31) {
+        c.shares = shares_of(upto, a.shares);
+        c.each = each;
+    }
+}
+
+// Starts the plan of a share.  One warp.
+__device__ inline void enter_share(const AttendArgs& a, const Census& c, int share, Plan& p, int lane) {
+    const int64_t from = share_start(c.shares, share), left = share_start(c.shares, share + 1) - from;
+    const int64_t upto = c.upto[lane];
+    const int part = __ffs(__ballot_sync(0xffffffffu, upto > from)) - 1;
+    if (left > 0) {                           // then some part reaches beyond `from`
+        int64_t r = from - (part ? c.upto[part - 1] : 0);
+        int b = part * c.each;
+        SeqInfo info;
 #pragma unroll 1
-        for (int i = part * each;; ++i) {
-            fetch(a, i, lane);
+        for (;; ++b) {
+            info = Lookup{a}(b);
             const int64_t u = units_of_seq(info, a.cut);
             if (r < u) break;
             r -= u;
         }
-        walk_enter(w, info, a.cut, r, w.left);
-    }
-
-    // Up to kSegments further segments; returns how many.
-    __device__ int next(const AttendArgs& a, Segment* out, int lane) {
-        int n = 0;
-#pragma unroll 1
-        while (w.left > 0 && n < kSegments) {
-            if (lane == 0)
-                out[n] = Segment{b, info, w.t.tile, w.head, w.first, w.count, w.t.units,
-                                 blocks_beyond(total, blockIdx.x, gridDim.x, w.t.units - w.first - w.count) + 1};
-            ++n;
-            if (!walk_next(w, info, a.cut) && w.left > 0) {
-                do fetch(a, b + 1, lane);
-                while (info.rows == 0);
-                walk_enter(w, info, a.cut, 0, w.left);
-            }
+        if (lane == 0) {
+            p.b = b;
+            p.info = info;
+            p.at = from;
+            walk_enter(p.w, info, a.cut, r, left);
         }
-        return n;
+    } else if (lane == 0) {
+        p.w.left = 0;
     }
-};
+    __syncwarp();
+}
 
 // mbar_wait, with the polling kept to a few instructions: the kernels here
 // have many waits, and their loops have to fit the instruction cache.
@@ -194,10 +176,11 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
 // different places of the code.
 __device__ __forceinline__ void block_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
 
-// Row `row` of a sequence (new token row / group, query head row % group of
-// the key/value head): its place in out and lse.
-__device__ __forceinline__ int64_t place_of(const AttendArgs& a, int begin, int row, int head) {
-    return (int64_t)(begin + row / a.cut.group) * (a.cut.heads * a.cut.group) + head * a.cut.group + row % a.cut.group;
+// Row r of a segment's tile: its place in out and lse.
+__device__ __forceinline__ int64_t place_of(const AttendArgs& a, const Segment& s, int r) {
+    int token, in_group;
+    row_of(s, a.cut, r, token, in_group);
+    return (int64_t)token * (a.cut.heads * a.cut.group) + s.head * a.cut.group + in_group;
 }
 
 __device__ __forceinline__ float lse_of(float m, float l) {

@@ -57,6 +57,8 @@ struct __align__(1024) Smem {
     uint8_t v[kVStages][kTile * D];           // as stored
     uint8_t v16[2][kTile * D * 2];            // f16: 64 dims of every key, then the next 64
     Segment segs[kSegments];
+    Plan plan;
+    Census census;
     int count;                                // of segs
     Meta k_meta[kMetas];
     Meta v_meta[kVStages];
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init_cluster();
     }
     if (warp == 13) tmem_alloc(&sm.tmem, 512);
-    if (tid == 0) a.desc[blockIdx.x].parts = 0;
+    if (tid < 2) a.desc[2 * blockIdx.x + tid].parts = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -267,12 +269,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int index = 0; ok && index < sm.count; ++index) {
                 const Segment seg = sm.segs[index];
-                const SeqInfo info = seg.info;
-                const int first_row = seg.tile * kPair, rows = min(info.rows - first_row, kPair);
+                                const int rows = seg.rows;
                 const int mine = x * kTile + in_tile;                // of the block's rows
                 const bool active = x == 0 || rows > kTile;
-                int key0, keys;
-                keys_of(seg, a.cut, key0, keys);
+                const int key0 = seg.key0, keys = seg.keys;
                 const int count = (keys - key0 + kTile - 1) / kTile;  // 0: a tile without keys
                 float f = 0.0f, m = -INFINITY, l = 0.0f;
                 int lim = 0;
@@ -282,10 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // would not fit the registers
                     const uint4* src = nullptr;
                     if (mine < rows) {
-                        const int r = first_row + mine;
-                        lim = keys_of_row(info, a.cut, r);
-                        src = reinterpret_cast<const uint4*>(a.q + (info.begin + r / a.cut.group) * a.q_stride +
-                                                             (int64_t)(seg.head * a.cut.group + r % a.cut.group) * D);
+                        int token, in_group;
+                        row_of(seg, a.cut, mine, token, in_group);
+                        lim = keys_of_row(seg, a.cut, mine);
+                        src = reinterpret_cast<const uint4*>(a.q + token * a.q_stride +
+                                                             (seg.head * a.cut.group + in_group) * D);
                     }
                     auto load = [&](int i) { return src ? __ldg(src + i) : make_uint4(0, 0, 0, 0); };
                     float top = 0.0f;
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(&sm.q_full[x]);
                 }
 
-                const int all_see = keys_of_row(info, a.cut, first_row + x * kTile);
+                const int all_see = keys_of_row(seg, a.cut, x * kTile);
                 for (int j = 0; j < count; ++j, mr.next()) {
                     if (!active) continue;
                     ok = __all_sync(0xffffffffu, wait_for(&sm.s_full[x], steps & 1, &sm.abort));
@@ -427,17 +428,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 
                 // the rows go out
-                const bool whole = seg.first == 0 && seg.count == seg.units;
-                const int slot = seg.first == 0 ? 1 : 0;
-                if (!whole && slot && tid == 0)
-                    a.desc[blockIdx.x] = PartDesc{seg.parts, info.begin, first_row, rows, seg.head, {}};
+                const bool whole = seg.parts == 1;
+                const int slot = seg.owner == blockIdx.x ? 1 : 0;
+                if (!whole && tid == 0) a.desc[2 * blockIdx.x + slot] = PartDesc{seg.parts, seg.owner, seg};
                 if (count > 0) {
                     ok = __all_sync(0xffffffffu, wait_for(&sm.o_full[x], outs & 1, &sm.abort));
                     if (!ok) break;
                     ++outs;
                     tc_fence_after();
                 }
-                const int64_t at = mine < rows ? place_of(a, info.begin, first_row + mine, seg.head) : 0;
+                const int64_t at = mine < rows ? place_of(a, seg, mine) : 0;
                 float* part = part_of(a, blockIdx.x, slot, D);
                 const int kept = segs % kSegs;
                 const float unit = count > 0 ? sm.ref[kept] * (1.0f / kVLift) : 0.0f;
@@ -488,9 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;                   // after a wait that gave up all go on to the barriers, without work
             for (int index = 0; index < sm.count; ++index) {
                 const Segment seg = sm.segs[index];
-                const SeqInfo info = seg.info;
-                int key0, keys;
-                keys_of(seg, a.cut, key0, keys);
+                                const int key0 = seg.key0, keys = seg.keys;
                 if (keys <= key0) continue;
                 const int slot = segs++ % kSegs, log2 = a.seqs.page_log2;
                 const int32_t* row = a.seqs.table + (int64_t)seg.b * a.seqs.width;
@@ -510,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (id == 0) sm.ref[slot] = most;
                 named_bar_sync(1, 128);
                 const float per = most > 0.0f ? kVLift / most : 0.0f;
-                const int all_see = keys_of_row(info, a.cut, seg.tile * kPair);
+                const int all_see = keys_of_row(seg, a.cut, 0);
                 for (int key = key0; ok && key < keys; key += kTile) {
                     ok = __all_sync(0xffffffffu, wait_for(&sm.v_full[vr.stage], vr.phase, &sm.abort)) &&
                          __all_sync(0xffffffffu, wait_for(&sm.v16_empty[v16r.stage], v16r.phase ^ 1, &sm.abort));
@@ -592,8 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool ok = true;
                 for (int index = 0; ok && index < sm.count; ++index) {
                     const Segment seg = sm.segs[index];
-                    int key0, keys;
-                    keys_of(seg, a.cut, key0, keys);
+                    const int key0 = seg.key0, keys = seg.keys;
                     const int32_t* row = a.seqs.table + (int64_t)seg.b * a.seqs.width;
                     auto page_at = [&](int key) {   // of this lane's 16 keys of a step
                         return lane < 8 && key + 16 * lane < keys ? __ldg(row + ((key + 16 * lane) >> log2)) : -1;
@@ -665,9 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool ok = true;
                 for (int index = 0; ok && index < sm.count; ++index) {
                     const Segment seg = sm.segs[index];
-                    int key0, keys;
-                    keys_of(seg, a.cut, key0, keys);
-                    const bool two = seg.info.rows - seg.tile * kPair > kTile;
+                    const int key0 = seg.key0, keys = seg.keys;
+                    const bool two = seg.rows > kTile;
                     const int count = (keys - key0 + kTile - 1) / kTile;
                     if (count == 0) continue;
                     // step j: for each tile O with the weights of step j - 1, then S of step j
@@ -710,14 +706,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             });
         } else if (warp == 14) {
             // ------------------------------------------------------ planning
-            Planner plan;
-            bool begun = false;
+            take_census(a, sm.census, lane);
+            __syncwarp();
+            enter_share(a, sm.census, blockIdx.x, sm.plan, lane);
             each_segments(
                 [&] {
-                    if (!begun) plan.begin(a, lane);
-                    begun = true;
-                    const int n = plan.next(a, sm.segs, lane);
-                    if (lane == 0) sm.count = n;
+                    if (lane == 0) {
+                        int n = 0;
+#pragma unroll 1
+                        while (sm.plan.w.left > 0 && n < kSegments)
+                            plan_next(sm.plan, Lookup{a}, a.cut, sm.census.shares, sm.segs[n++]);
+                        sm.count = n;
+                    }
                 },
                 others);
         } else {

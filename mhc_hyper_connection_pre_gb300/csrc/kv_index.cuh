@@ -99,8 +99,8 @@ MHC_HD bool starts_run(const Span& sp, const Run& r, int t) {
 // being token r / group, query head r % group of it; a tile is `tile_rows` of
 // them.  A tile's keys are cut in units of 2^unit_log2; a tile without keys still is
 // one unit (its rows have to be written).  All units of all tiles, ordered by
-// sequence, tile, head and key, form one line that the blocks share evenly
-// whatever the lengths are (share_of), and a tile cut by a border is joined
+// sequence, tile, head and key, form one line that the takers (warps or blocks)
+// share evenly whatever the lengths are, and a tile cut by a border is joined
 // afterwards.
 
 // One sequence as the walk needs it.
@@ -112,6 +112,7 @@ struct SeqInfo {
 
 struct Cut {
     int heads, group, tile_rows, unit_log2;
+    int group_inv;          // 65536 / group + 1: x / group is x * group_inv >> 16 for x up to 384
 };
 
 MHC_HD SeqInfo info_of(const Span& sp, int group) {
@@ -124,18 +125,6 @@ MHC_HD SeqInfo info_of(const Span& sp, int group) {
 }
 
 MHC_HD int tiles_of(const SeqInfo& s, const Cut& c) { return (s.rows + c.tile_rows - 1) / c.tile_rows; }
-
-// How many keys row r sees.
-MHC_HD int keys_of_row(const SeqInfo& s, const Cut& c, int r) {
-    const int n = s.before + r / c.group + 1;
-    return n < 0 ? 0 : n;
-}
-
-// How many keys the last row of tile i sees: the most of any of its rows.
-MHC_HD int keys_of_tile(const SeqInfo& s, const Cut& c, int i) {
-    const int end = (i + 1) * c.tile_rows < s.rows ? (i + 1) * c.tile_rows : s.rows;
-    return keys_of_row(s, c, end - 1);
-}
 
 MHC_HD int units_of(int keys, const Cut& c) {
     const int n = (keys + (1 << c.unit_log2) - 1) >> c.unit_log2;
@@ -187,49 +176,61 @@ MHC_HD int64_t units_of_seq(const SeqInfo& s, const Cut& c) {
     return n * c.heads;
 }
 
-// The units [from, to) of the line that block c takes.  With fewer units than
-// blocks the first `total` blocks take one each, so that the blocks that share
-// a tile always follow one another.
-MHC_HD void share_of(int64_t total, int c, int blocks, int64_t& from, int64_t& to) {
-    // one division, in 32 bits where they hold: equal parts, the first `extra` of them one longer
-    const int64_t each = total >> 31 ? total / blocks : (int64_t)((uint32_t)total / (uint32_t)blocks);
-    const int64_t extra = total - each * blocks;
-    from = each * c + (c < extra ? c : extra);
-    to = from + each + (c < extra ? 1 : 0);
-}
-
-// How many blocks after block c it takes for `units` more units of the line.
-MHC_HD int blocks_beyond(int64_t total, int c, int blocks, int units) {
-    if (units <= 0) return 0;
-    const int64_t each = total >> 31 ? total / blocks : (int64_t)((uint32_t)total / (uint32_t)blocks);
-    const int64_t longer = total - each * blocks - (c + 1);      // following blocks that take one unit more
-    if (longer > 0 && units <= longer * (each + 1)) return (int)((units + each) / (each + 1));
-    const int64_t more = longer > 0 ? longer : 0, rest = units - more * (each + 1);
-    return (int)(more + (rest + each - 1) / each);
-}
-
-// A segment: the units of one tile and head that one block takes.
-struct Segment {
-    int b;                  // sequence
-    SeqInfo info;
-    int tile, head;
-    int first, count;       // units
-    int units;              // of the whole tile
-    int parts;              // blocks that share the tile's units from this segment on
+// The line's equal shares; with fewer units than takers the first `total` take
+// one each, so that the takers of a tile always follow one another.
+struct Shares {
+    int64_t total, each, extra;      // units of the line; of a share; how many first shares take one more
 };
 
-// The keys [key0, keys) of a segment.
-MHC_HD void keys_of(const Segment& s, const Cut& c, int& key0, int& keys) {
-    const int all = keys_of_tile(s.info, c, s.tile), end = (s.first + s.count) << c.unit_log2;
-    key0 = s.first << c.unit_log2;
-    keys = end < all ? end : all;
+MHC_HD int64_t divide(int64_t a, int64_t b) {      // in 32 bits where they hold
+    return (a | b) >> 31 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
-// A walk over a block's segments inside one sequence.
+MHC_HD Shares shares_of(int64_t total, int n) {
+    Shares s;
+    s.total = total;
+    s.each = divide(total, n);
+    s.extra = total - s.each * n;
+    return s;
+}
+
+// The first unit of share c.
+MHC_HD int64_t share_start(const Shares& s, int c) { return s.each * c + (c < s.extra ? c : s.extra); }
+
+// The share that unit u of the line is in.
+MHC_HD int share_at(const Shares& s, int64_t u) {
+    const int64_t longer = s.extra * (s.each + 1);
+    return (int)(u < longer ? divide(u, s.each + 1) : s.extra + divide(u - longer, s.each));
+}
+
+// A segment: the units of one tile and head that one share has.
+struct Segment {
+    int b, head;            // sequence, key/value head
+    int token, rem;         // row 0 of the tile: new token, query head of the group
+    int rows;               // of the tile
+    int see;                // keys before that token
+    int key0, keys;         // the segment's keys [key0, keys); none where the tile sees none
+    int parts, owner;       // shares that the tile's units lie in, the first of them
+};
+
+// Row r of a segment's tile.
+MHC_HD void row_of(const Segment& s, const Cut& c, int r, int& token, int& in_group) {
+    const int x = s.rem + r, n = x * c.group_inv >> 16;
+    token = s.token + n;
+    in_group = x - n * c.group;
+}
+
+// How many keys that row sees.
+MHC_HD int keys_of_row(const Segment& s, const Cut& c, int r) {
+    const int n = s.see + ((s.rem + r) * c.group_inv >> 16) + 1;
+    return n < 0 ? 0 : n;
+}
+
+// A walk over a share's segments.
 struct Walk {
     Tiles t;
     int head, first, count;
-    int64_t left;           // units of the block's share from this segment on; 0: the walk is over
+    int64_t left;           // units of the share from this segment on; 0: the walk is over
 };
 
 MHC_HD void walk_cut(Walk& w) {
@@ -238,7 +239,7 @@ MHC_HD void walk_cut(Walk& w) {
 }
 
 // Enters a sequence (with new tokens) at unit r of its part of the line, with
-// `left` units of the block's share to go.
+// `left` units of the share to go.
 MHC_HD void walk_enter(Walk& w, const SeqInfo& s, const Cut& c, int64_t r, int64_t left) {
     w.left = left;
     tiles_start(w.t, s, c);
@@ -246,9 +247,8 @@ MHC_HD void walk_enter(Walk& w, const SeqInfo& s, const Cut& c, int64_t r, int64
         r -= (int64_t)w.t.units * c.heads;
         tiles_next(w.t, s, c);
     }
-    const int at = (int)r;  // less than units * heads, which fits: both are bounded by what memory holds
-    w.head = at / w.t.units;
-    w.first = at % w.t.units;
+    w.head = (int)divide(r, w.t.units);
+    w.first = (int)(r - (int64_t)w.head * w.t.units);
     walk_cut(w);
 }
 
@@ -265,6 +265,44 @@ MHC_HD bool walk_next(Walk& w, const SeqInfo& s, const Cut& c) {
     }
     walk_cut(w);
     return true;
+}
+
+// A share's plan: the walk, the sequence it is in and the line's unit that its
+// segment starts at.
+struct Plan {
+    Walk w;
+    SeqInfo info;
+    int b;
+    int64_t at;
+};
+
+// The plan's segment; then steps on.  look(b) finds sequence b.
+template <class Look>
+MHC_HD void plan_next(Plan& p, const Look& look, const Cut& c, const Shares& shares, Segment& s) {
+    const int row0 = p.w.t.tile * c.tile_rows, tokens = row0 / c.group;
+    s.b = p.b;
+    s.head = p.w.head;
+    s.token = p.info.begin + tokens;
+    s.rem = row0 - tokens * c.group;
+    s.rows = p.info.rows - row0 < c.tile_rows ? p.info.rows - row0 : c.tile_rows;
+    s.see = p.info.before + tokens;
+    const int all = keys_of_row(s, c, s.rows - 1), end = (p.w.first + p.w.count) << c.unit_log2;
+    s.key0 = p.w.first << c.unit_log2;
+    s.keys = end < all ? end : all;
+    if (p.w.count == p.w.t.units) {
+        s.parts = 1;
+        s.owner = 0;
+    } else {
+        const int64_t begin = p.at - p.w.first;
+        s.owner = share_at(shares, begin);
+        s.parts = share_at(shares, begin + p.w.t.units - 1) - s.owner + 1;
+    }
+    p.at += p.w.count;
+    if (!walk_next(p.w, p.info, c) && p.w.left > 0) {
+        do p.info = look(++p.b);
+        while (p.info.rows == 0);
+        walk_enter(p.w, p.info, c, 0, p.w.left);
+    }
 }
 
 }  // namespace kv

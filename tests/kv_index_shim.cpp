@@ -36,48 +36,48 @@ void kv_runs(const int32_t* table, const int32_t* lens, const int32_t* cu, int w
     }
 }
 
-// The segments of block `block` of `blocks`: out[i] = {sequence, tile, head,
-// first unit, units, units of the tile, first key, last key + 1, blocks from here on}.  Returns how
-// many, or -1 if there are more than `most`; total: units of the whole line.
+// The segments of share `share` of `n`: out[i] = {sequence, first token, query
+// head of its first row, rows, head, first key, last key + 1, shares of the
+// tile, the first of them, keys that the first and the last row see}.  Returns
+// how many, or -1 if there are more than `most`; total: units of the line.
 int kv_segments(const int32_t* table, const int32_t* lens, const int32_t* cu, int width, int B, int T, int P,
-                int pages, int heads, int group, int tile_rows, int unit_log2, int block, int blocks, int32_t* out,
+                int pages, int heads, int group, int tile_rows, int unit_log2, int share, int n, int32_t* out,
                 int most, int64_t* total) {
     const Seqs s = make(table, lens, cu, width, B, T, P, pages);
-    const Cut c{heads, group, tile_rows, unit_log2};
+    const Cut c{heads, group, tile_rows, unit_log2, 65536 / group + 1};
     *total = 0;
     for (int b = 0; b < B; ++b) *total += units_of_seq(info_of(span_of(s, b), group), c);
-    int64_t from, to, seen = 0;
-    share_of(*total, block, blocks, from, to);
-    int n = 0, b = 0;
-    for (; b < B; ++b) {
-        const int64_t u = units_of_seq(info_of(span_of(s, b), group), c);
+    const Shares shares = shares_of(*total, n);
+    const int64_t from = share_start(shares, share), left = share_start(shares, share + 1) - from;
+    if (left <= 0) return 0;
+    int64_t seen = 0;
+    Plan p;
+    for (p.b = 0;; ++p.b) {
+        p.info = info_of(span_of(s, p.b), group);
+        const int64_t u = units_of_seq(p.info, c);
         if (from < seen + u) break;
         seen += u;
     }
-    int64_t left = to - from, r = from - seen;
-    for (; left > 0; ++b) {
-        const SeqInfo info = info_of(span_of(s, b), group);
-        if (info.rows == 0) continue;
-        Walk w;
-        walk_enter(w, info, c, r, left);
-        r = 0;
-        do {
-            if (n == most) return -1;
-            const Segment g{b, info, w.t.tile, w.head, w.first, w.count, w.t.units,
-                            blocks_beyond(*total, block, blocks, w.t.units - w.first - w.count) + 1};
-            int32_t* o = out + 9 * n++;
-            o[0] = b;
-            o[1] = g.tile;
-            o[2] = g.head;
-            o[3] = g.first;
-            o[4] = g.count;
-            o[5] = g.units;
-            keys_of(g, c, o[6], o[7]);
-            o[8] = g.parts;
-        } while (walk_next(w, info, c));
-        left = w.left;
+    p.at = from;
+    walk_enter(p.w, p.info, c, from - seen, left);
+    int found = 0;
+    while (p.w.left > 0) {
+        if (found == most) return -1;
+        Segment g;
+        plan_next(p, [&](int b) { return info_of(span_of(s, b), group); }, c, shares, g);
+        const int32_t o[] = {g.b, g.token, g.rem, g.rows, g.head, g.key0, g.keys, g.parts, g.owner,
+                             keys_of_row(g, c, 0), keys_of_row(g, c, g.rows - 1)};
+        for (int i = 0; i < 11; ++i) out[11 * found + i] = o[i];
+        ++found;
     }
-    return n;
+    return found;
+}
+
+// Token and query head of every row of a segment's tile.
+void kv_rows(int token, int rem, int rows, int group, int32_t* out) {
+    const Cut c{1, group, 256, 5, 65536 / group + 1};
+    const Segment g{0, 0, token, rem, rows, 0, 0, 0, 1, 0};
+    for (int r = 0; r < rows; ++r) row_of(g, c, r, out[2 * r], out[2 * r + 1]);
 }
 
 }

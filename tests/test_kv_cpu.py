@@ -240,27 +240,27 @@ def test_runs_stay_inside_whatever_the_arrays_hold(shim, seed):
             assert -1 <= page < pages
 
 
-def _segments(shim, lens, cu, T, B, width, heads, group, rows, blocks, unit=64):
-    """Every block's segments, in order, and the number of units."""
+def _segments(shim, lens, cu, T, B, width, heads, group, rows, shares, unit=32):
+    """Every share's segments, in order, and the number of units."""
     pages = _i32(np.zeros((B, width)))
-    out, total, got = np.zeros((20000, 9), dtype=np.int32), ctypes.c_int64(0), []
-    for c in range(blocks):
-        n = shim.kv_segments(_ptr(pages), _ptr(lens), _ptr(cu), width, B, T, 16, 1, heads, group, rows, unit.bit_length() - 1, c,
-                             blocks, _ptr(out), 20000, ctypes.byref(total))
+    out, total, got = np.zeros((20000, 11), dtype=np.int32), ctypes.c_int64(0), []
+    for c in range(shares):
+        n = shim.kv_segments(_ptr(pages), _ptr(lens), _ptr(cu), width, B, T, 16, 1, heads, group, rows,
+                             unit.bit_length() - 1, c, shares, _ptr(out), 20000, ctypes.byref(total))
         assert n >= 0
         got.append(out[:n].tolist())
     return got, total.value
 
 
 @pytest.mark.parametrize("seed", range(25))
-def test_blocks_share_every_unit_once(shim, seed):
-    """The blocks' segments are all units of all tiles, each once and in
-    order; every tile has a unit, no block takes much more than another, and
-    of a block's segments only the first and the last may be parts of tiles."""
+def test_shares_have_every_unit_once(shim, seed):
+    """The shares' segments are all units of all tiles, each once and in
+    order; every tile has a unit, no share is more than a unit longer than
+    another, and the parts of a tile know of one another."""
     r = random.Random(50 + seed)
-    B, blocks, P, unit = r.choice([1, 3, 17, 40]), r.choice([1, 7, 152]), 16, r.choice([64, 128])
-    heads, group, rows = r.choice([1, 2, 8]), r.choice([1, 5, 16]), r.choice([8, 16, 256])
-    counts = [r.choice([0, 1, 1, r.randint(0, 40), r.randint(0, 300)]) for _ in range(B)]
+    B, shares, P, unit = r.choice([1, 3, 17, 40]), r.choice([1, 7, 152, 1000]), 16, r.choice([32, 128])
+    heads, group, rows = r.choice([1, 2, 8]), r.choice([1, 3, 5, 16, 128]), r.choice([8, 16, 256])
+    counts = [r.choice([0, 1, 1, r.randint(0, 40), r.randint(0, 300 // group + 1)]) for _ in range(B)]
     lens = [r.choice([0, n, n + r.randint(0, 3000)]) for n in counts]
     if not any(counts):
         counts[0] = 1
@@ -268,33 +268,41 @@ def test_blocks_share_every_unit_once(shim, seed):
     cu = [0]
     for n in counts:
         cu.append(cu[-1] + n)
-    got, total = _segments(shim, _i32(lens), _i32(cu), cu[-1], B, width, heads, group, rows, blocks, unit)
+    got, total = _segments(shim, _i32(lens), _i32(cu), cu[-1], B, width, heads, group, rows, shares, unit)
     expect = []
     for b, (n, m) in enumerate(zip(lens, counts)):
         for i in range(-(-m * group // rows)):
-            last = min((i + 1) * rows, m * group) - 1
-            keys = max(0, n - m + last // group + 1)
-            units = max(1, -(-keys // unit))
+            end = min((i + 1) * rows, m * group)
+            sees = [max(0, n - m + x // group + 1) for x in (i * rows, end - 1)]
+            tile = (b, cu[b] + i * rows // group, i * rows % group, end - i * rows)
+            units = max(1, -(-sees[1] // unit))
             for h in range(heads):
-                expect += [(b, i, h, u, units, u * unit, min((u + 1) * unit, keys)) for u in range(units)]
-    flat = [(b, i, h, u, units, u * unit, min((u + 1) * unit, k1)) for c in got for b, i, h, first, count, units, k0, k1, _
-            in c for u in range(first, first + count)]
-    assert flat == expect and total == len(expect)
-    sizes = [sum(s[4] for s in c) for c in got]
-    assert max(sizes) - min(sizes) <= 1
-    assert not any(sizes[total:])                      # the blocks of a tile follow one another
-    owners = {}
+                expect += [(*tile, h, *sees, u * unit, min((u + 1) * unit, sees[1])) for u in range(units)]
+    flat, sizes, owners = [], [], {}
     for c, segs in enumerate(got):
-        for s in segs:
-            owners.setdefault(tuple(s[:3]), []).append((c, s[8]))
-    for of in owners.values():                         # a tile's blocks are consecutive, and each knows how many follow
-        assert [c for c, _ in of] == list(range(of[0][0], of[0][0] + len(of)))
-        assert [parts for _, parts in of] == list(range(len(of), 0, -1))
-    for c in got:
-        for k, (b, i, h, first, count, units, k0, k1, _) in enumerate(c):
-            assert count >= 1 and first + count <= units and k0 == first * unit
-            assert first == 0 or k == 0
-            assert first + count == units or k == len(c) - 1
+        sizes.append(0)
+        for b, t, rem, n, h, k0, k1, parts, owner, see0, see1 in segs:
+            units = max(1, -(-(k1 - k0) // unit))
+            sizes[-1] += units
+            flat += [(b, t, rem, n, h, see0, see1, k0 + u * unit, min(k0 + (u + 1) * unit, k1)) for u in range(units)]
+            owners.setdefault((b, t, rem, h), []).append((c, parts, owner))
+    assert flat == expect and total == len(expect)
+    assert max(sizes) - min(sizes) <= 1 and not any(sizes[total:])
+    for of in owners.values():
+        assert [c for c, _, _ in of] == list(range(of[0][0], of[0][0] + len(of)))
+        for _, parts, owner in of:
+            assert parts == len(of) and (parts == 1 or owner == of[0][0])
+    for c, segs in enumerate(got):                     # at most one tile begun and left, one gone on with
+        cut = [(owner == c) for *_, parts, owner, _, _ in segs if parts > 1]
+        assert cut.count(True) <= 1 and cut.count(False) <= 1
+
+
+@pytest.mark.parametrize("group", range(1, 129))
+def test_rows_of_a_tile(shim, group):
+    out = np.zeros((256, 2), dtype=np.int32)
+    for rem in {0, 1 % group, group // 2, group - 1}:
+        shim.kv_rows(7, rem, 256, group, _ptr(out))
+        assert out.tolist() == [[7 + (rem + r) // group, (rem + r) % group] for r in range(256)]
 
 
 @pytest.mark.parametrize("seed", range(25))
@@ -304,9 +312,8 @@ def test_segments_stay_inside_whatever_the_arrays_hold(shim, seed):
     B, T, width, heads, group, rows = r.randint(1, 9), r.randint(1, 30), r.randint(1, 40), 2, 3, 16
     lens, cu = _i32([wild() for _ in range(B)]), _i32([wild() for _ in range(B + 1)])
     got, total = _segments(shim, lens, cu, T, B, width, heads, group, rows, 5)
-    assert sum(s[4] for c in got for s in c) == total
+    assert sum(max(1, -(-(s[6] - s[5]) // 32)) for c in got for s in c) == total
     for c in got:
-        for b, i, h, first, count, units, k0, k1, _ in c:
-            assert 0 <= b < B and 0 <= h < heads and 0 <= i and (i * rows) // group < T
-            assert 0 <= first and count >= 1 and first + count <= units <= max(1, -(-width * 16 // 64))
-            assert k1 <= width * 16
+        for b, t, rem, n, h, k0, k1, parts, owner, see0, see1 in c:
+            assert 0 <= b < B and 0 <= h < heads and 0 <= t and 1 <= n <= rows and t + (rem + n - 1) // group < T
+            assert 0 <= k0 and k1 <= width * 16 and see1 <= width * 16 and 1 <= parts <= 5 and 0 <= owner < 5
