@@ -492,105 +492,153 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
 
 // Joins the tiles that borders between shares have cut.  A tile's parts are
 // slot 1 of the share that began it (its owner) and slot 0 of the shares after
-// it; the blocks of these shares divide the tile's rows among them.  With few
-// parts a warp takes a row; with many a block does, its warps dividing the
-// parts.  Every load but the first depends on nothing that came before it.
+// it.  Each share has a warp for either slot (or gridDim.y of them), and a
+// tile's warps divide its rows.  What bounds it is the number of instructions
+// a row where there are few parts, and the loads' latency where there are many.
 template <int D>
 __global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a) {
-    constexpr int kDims = D / 32, kMany = 32;
-    __shared__ float acc[8][D + 2];
+    constexpr int kMany = 16, kAhead = 8, kDims = D / 32;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32, share = blockIdx.x * 8 + threadIdx.x / 32;
+    if (share >= a.shares) return;
     const int64_t next = 2 * (int64_t)a.cut.tile_rows * (D + 2);      // from a share's part to the next share's
-    const int ml = a.cut.tile_rows * D;
-    for (int slot = 0; slot < 2; ++slot) {
-        const PartDesc& d = a.desc[2 * blockIdx.x + slot];
-        const int parts = d.parts;
-        if (parts == 0) continue;
-        const int owner = d.owner, mine = blockIdx.x - owner, rows = d.seg.rows;
-        const float* first = part_of(a, owner, 1, D);
-        const float* rest = part_of(a, owner + 1, 0, D) - next;       // part k, k > 0, at rest + k * next
+    const PartDesc& d = a.desc[2 * share + blockIdx.z];
+    const int parts = d.parts;
+    if (parts == 0) return;
+    const Segment seg = d.seg;
+    const float* first = part_of(a, d.owner, 1, D);
+    const float* rest = part_of(a, d.owner + 1, 0, D) - next;     // part k, k > 0, at rest + k * next
+    const float* sums = a.cut.tile_rows * D + first;              // maxima and sums of the first part
+    const int64_t to_rest = rest - first;
+    const int mine = share - d.owner + parts * blockIdx.y, step = parts * gridDim.y;
 
-        // the weighted sum of row r over parts k0, k0 + step, ..
-        auto sum = [&](int r, int k0, int step, float& m, float& l, float (&o)[kDims]) {
-            m = -INFINITY;
-            l = 0.0f;
+    if (parts < kMany) {                      // a warp takes a row; four parts at a time, all their loads at once
+#pragma unroll 1
+        for (int r = mine; r < seg.rows; r += step) {
+            float m = -INFINITY, l = 0.0f, o[kDims] = {};
+#pragma unroll 1
+            for (int base = 0; base < parts; base += 4) {
+                float2 ml[4];
+                float y[4][kDims];
 #pragma unroll
-            for (int i = 0; i < kDims; ++i) o[i] = 0.0f;
-            for (int base = k0; base < parts; base += 32 * step) {
-                const int k = base + lane * step, left = (parts - base + step - 1) / step, n = left < 32 ? left : 32;
-                float2 own = make_float2(-INFINITY, 0.0f);
-                if (lane < n) own = *reinterpret_cast<const float2*>((k ? rest + k * next : first) + ml + 2 * r);
-                float now = own.x;
+                for (int i = 0; i < 4; ++i) {
+                    const int k = base + i;
+                    const int64_t off = k ? to_rest + k * next : 0;
+                    ml[i] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
-                for (int i = 16; i; i >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, i));
-                now = fmaxf(now, m);
-                const float zero = now == -INFINITY ? 0.0f : now, keep = ex2(m - zero), w = ex2(own.x - zero);
-                float all = w * own.y;
-#pragma unroll
-                for (int i = 16; i; i >>= 1) all += __shfl_xor_sync(0xffffffffu, all, i);
-                l = fmaf(l, keep, all);
+                    for (int c = 0; c < kDims; ++c) y[i][c] = 0.0f;
+                    if (k < parts) {
+                        ml[i] = *reinterpret_cast<const float2*>(sums + off + 2 * r);
+                        const float* src = first + off + r * D + lane * kDims;
+                        if constexpr (D == 128) {
+                            const float4 v = *reinterpret_cast<const float4*>(src);
+                            y[i][0] = v.x; y[i][1] = v.y; y[i][2] = v.z; y[i][3] = v.w;
+                        } else {
+                            const float2 v = *reinterpret_cast<const float2*>(src);
+                            y[i][0] = v.x; y[i][1] = v.y;
+                        }
+                    }
+                }
+                const float now = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+                const float zero = now == -INFINITY ? 0.0f : now, keep = ex2(m - zero);
                 m = now;
+                l *= keep;
 #pragma unroll
-                for (int i = 0; i < kDims; ++i) o[i] *= keep;
-#pragma unroll 8
-                for (int j = 0; j < n; ++j) {
-                    const float x = __shfl_sync(0xffffffffu, w, j);
-                    const int kk = base + j * step;
-                    const float* src = (kk ? rest + kk * next : first) + r * D + lane * kDims;
-                    if constexpr (D == 128) {
-                        const float4 y = *reinterpret_cast<const float4*>(src);
-                        o[0] = fmaf(x, y.x, o[0]);
-                        o[1] = fmaf(x, y.y, o[1]);
-                        o[2] = fmaf(x, y.z, o[2]);
-                        o[3] = fmaf(x, y.w, o[3]);
-                    } else {
-                        const float2 y = *reinterpret_cast<const float2*>(src);
-                        o[0] = fmaf(x, y.x, o[0]);
-                        o[1] = fmaf(x, y.y, o[1]);
-                    }
+                for (int c = 0; c < kDims; ++c) o[c] *= keep;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = ex2(ml[i].x - zero);
+                    l = fmaf(x, ml[i].y, l);
+#pragma unroll
+                    for (int c = 0; c < kDims; ++c) o[c] = fmaf(x, y[i][c], o[c]);
                 }
             }
-        };
-        auto write = [&](int r, float m, float l, const float (&o)[kDims]) {
-            const int64_t to = place_of(a, d.seg, r);
-            const float y = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-            for (int i = 0; i < kDims; i += 2)
-                *reinterpret_cast<uint32_t*>(a.out + to * D + lane * kDims + i) = pack_bf16x2(o[i] * y, o[i + 1] * y);
+            const int64_t to = place_of(a, seg, r);
+            const float by = l == 0.0f ? 0.0f : 1.0f / l;
+            uint32_t* out = reinterpret_cast<uint32_t*>(a.out + to * D + lane * kDims);
+            if constexpr (D == 128)
+                *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o[0] * by, o[1] * by), pack_bf16x2(o[2] * by, o[3] * by));
+            else
+                *out = pack_bf16x2(o[0] * by, o[1] * by);
             if (lane == 0 && a.lse) a.lse[to] = lse_of(m, l);
-        };
-        float m, l, o[kDims];
-        if (parts <= kMany) {
-            for (int r = mine + parts * (warp + 8 * blockIdx.y); r < rows; r += parts * 8 * gridDim.y) {
-                sum(r, 0, 1, m, l, o);
-                write(r, m, l, o);
+        }
+        return;
+    }
+
+    // a warp takes a quarter of a row: first the weights of up to 256 parts, kAhead to
+    // a lane, then their values, D / 16 lanes to a part
+    constexpr int lanes = D / 16, at_once = 32 / lanes;
+    const int sub = lane / lanes, x4 = lane % lanes;
+#pragma unroll 1
+    for (int item = mine; item < seg.rows * 4; item += step) {
+        const int r = item / 4, at = r * D + (item % 4 * lanes + x4) * 4;
+        float m = -INFINITY, l = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+        for (int base = 0; base < parts; base += 32 * kAhead) {
+            // the maxima and sums of up to 32 * kAhead parts, kAhead to a lane, become their weights
+            float2 own[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int k = base + 32 * i + lane;
+                own[i] = make_float2(-INFINITY, 0.0f);
+                if (k < parts)
+                    own[i] = *reinterpret_cast<const float2*>(sums + (k ? to_rest + k * next : 0) + 2 * r);
             }
-        } else {
-            for (int r = mine + parts * blockIdx.y; r < rows; r += parts * gridDim.y) {   // the same for the block
-                sum(r, warp, 8, m, l, o);
+            float now = own[0].x;
 #pragma unroll
-                for (int i = 0; i < kDims; ++i) acc[warp][lane * kDims + i] = o[i];
-                if (lane == 0) acc[warp][D] = m, acc[warp][D + 1] = l;
-                __syncthreads();
-                if (warp == 0) {
-                    m = -INFINITY;
-                    for (int w = 0; w < 8; ++w) m = fmaxf(m, acc[w][D]);
-                    const float zero = m == -INFINITY ? 0.0f : m;
-                    l = 0.0f;
+            for (int i = 1; i < kAhead; ++i) now = fmaxf(now, own[i].x);
 #pragma unroll
-                    for (int i = 0; i < kDims; ++i) o[i] = 0.0f;
-                    for (int w = 0; w < 8; ++w) {
-                        const float x = ex2(acc[w][D] - zero);
-                        l = fmaf(x, acc[w][D + 1], l);
+            for (int i = 16; i; i >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, i));
+            now = fmaxf(now, m);
+            const float zero = now == -INFINITY ? 0.0f : now, keep = ex2(m - zero);
+            float all = 0.0f;
 #pragma unroll
-                        for (int i = 0; i < kDims; ++i) o[i] = fmaf(x, acc[w][lane * kDims + i], o[i]);
+            for (int i = 0; i < kAhead; ++i) {
+                own[i].x = ex2(own[i].x - zero);
+                all = fmaf(own[i].x, own[i].y, all);
+            }
+#pragma unroll
+            for (int i = 16; i; i >>= 1) all += __shfl_xor_sync(0xffffffffu, all, i);
+            l = fmaf(l, keep, all);
+            m = now;
+            o.x *= keep; o.y *= keep; o.z *= keep; o.w *= keep;
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const int from = base + 32 * q, n = parts - from < 32 ? parts - from : 32;
+#pragma unroll 1
+                for (int k0 = 0; k0 < n; k0 += 8 * at_once) {
+                    float4 y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int k = k0 + i * at_once + sub;
+                        y[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (k < n)
+                            y[i] = *reinterpret_cast<const float4*>((from + k ? rest + (from + k) * next : first) + at);
                     }
-                    write(r, m, l, o);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float x = __shfl_sync(0xffffffffu, own[q].x, (k0 + i * at_once + sub) & 31);
+                        o.x = fmaf(x, y[i].x, o.x);
+                        o.y = fmaf(x, y[i].y, o.y);
+                        o.z = fmaf(x, y[i].z, o.z);
+                        o.w = fmaf(x, y[i].w, o.w);
+                    }
                 }
-                __syncthreads();
             }
         }
+        for (int i = lanes; i < 32; i <<= 1) {                    // over the parts taken at a time
+            o.x += __shfl_xor_sync(0xffffffffu, o.x, i);
+            o.y += __shfl_xor_sync(0xffffffffu, o.y, i);
+            o.z += __shfl_xor_sync(0xffffffffu, o.z, i);
+            o.w += __shfl_xor_sync(0xffffffffu, o.w, i);
+        }
+        if (sub) continue;
+        const int64_t to = place_of(a, seg, r);
+        const float y = l == 0.0f ? 0.0f : 1.0f / l;
+        *reinterpret_cast<uint2*>(a.out + to * D + (at - r * D)) =
+            make_uint2(pack_bf16x2(o.x * y, o.y * y), pack_bf16x2(o.z * y, o.w * y));
+        if (at == r * D && a.lse) a.lse[to] = lse_of(m, l);
     }
 }
 
@@ -626,7 +674,7 @@ cudaError_t launch_join(const AttendArgs& a, int head_dim, cudaStream_t stream) 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(a.shares, a.cut.tile_rows > 16 ? 8 : 1, 1);
+    cfg.gridDim = dim3((a.shares + 7) / 8, a.cut.tile_rows > 16 ? 64 : 1, 2);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = stream;
     return cudaLaunchKernelEx(&cfg, head_dim == 64 ? kv_join_kernel<64> : kv_join_kernel<128>, a);
