@@ -2,8 +2,9 @@
 
 Each CUDA translation unit under ``csrc/`` is compiled in parallel to an
 object file, then linked into ``_build/libmhc.so`` (CUDA runtime linked
-statically, so loading the library needs no GPU).  Rebuilds only what
-changed.  Usage: ``python -m mhc_hyper_connection_pre_gb300.build [--ptxas-v]``.
+statically, so loading the library needs no GPU).  ``csrc/kv_binding.cpp``, a
+CPython extension over PyTorch's headers, becomes ``_build/_mhc_kv.so``, linked
+to libmhc.so beside it.  Rebuilds only what changed.  Usage: ``python -m mhc_hyper_connection_pre_gb300.build [--ptxas-v]``.
 """
 from __future__ import annotations
 
@@ -13,12 +14,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmhc.so")
+BINDING = os.path.join(BUILD, "_mhc_kv.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -53,14 +56,50 @@ def _compile(src: str, ptxas_v: bool) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def _run(cmd: list, what: str) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding() -> str:
+    """The object of the kv binding, for the running interpreter and PyTorch."""
+    import torch
+    src, obj = os.path.join(CSRC, "kv_binding.cpp"), os.path.join(BUILD, "kv_binding.cpp.o")
+    if os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(src), _newest_dep_mtime()):
+        return obj
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    dirs = [INCLUDE, inc, os.path.join(inc, "torch", "csrc", "api", "include"), cuda, sysconfig.get_paths()["include"]]
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *[f"-I{d}" for d in dirs], "-c", src,
+          "-o", obj + ".tmp"], "g++ for kv_binding.cpp")
+    os.replace(obj + ".tmp", obj)
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= os.path.getmtime(obj):
+        return
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "lib64")
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    _run(["g++", "-shared", "-o", tmp, obj, f"-L{BUILD}", "-l:libmhc.so", "-Wl,-rpath,$ORIGIN", f"-L{libs}",
+          "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-L{cuda}", "-lcudart_static", "-ldl",
+          "-lrt", "-lpthread"], "link of _mhc_kv.so")
+    os.replace(tmp, BINDING)
+
+
 def build(ptxas_v: bool = False, force: bool = False) -> str:
-    """Compile every ``csrc/*.cu`` and link ``_build/libmhc.so``; returns its path."""
+    """Compile ``csrc/``, link ``_build/libmhc.so`` and ``_build/_mhc_kv.so``; returns the former's path."""
     os.makedirs(BUILD, exist_ok=True)
     if force:
         for o in glob.glob(os.path.join(BUILD, "*.o")):
             os.remove(o)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, ptxas_v), srcs))
     if ptxas_v:
         for _, log in results:
@@ -74,6 +113,7 @@ def build(ptxas_v: bool = False, force: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link of libmhc.so failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _link_binding(binding.result())
     return LIB
 
 

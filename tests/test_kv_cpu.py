@@ -148,18 +148,10 @@ def test_binding_refuses(lib):
         mhc.kv_attend(x, dict(c, v=c["v"][:2]), table, lens)
     with pytest.raises(ValueError):
         mhc.kv_attend(x, dict(c, k_scale=c["k_scale"][:2]), table, lens)
-    with pytest.raises(ValueError):
-        kvmod._rows_arg(x[0], "k", 64, x.device)
-    with pytest.raises(ValueError):
-        kvmod._rows_arg(torch.zeros(4, 64, 2, dtype=torch.bfloat16).transpose(1, 2), "k", 64, x.device)
     with pytest.raises(TypeError):
-        kvmod._rows_arg(x.half(), "k", 64, x.device)
+        mhc.kv_attend(x, dict(c, v_scale=None), table, lens)
     with pytest.raises(TypeError):
-        kvmod._rows_arg(None, "k", 64, x.device)
-    with pytest.raises(ValueError):
-        kvmod._seqs_arg(table, lens[0], None, 1, x.device)
-    with pytest.raises(ValueError):
-        kvmod._seqs_arg(table, lens, None, 2, x.device)
+        mhc.kv_append(dict(c, k=None), x, x, table, lens)
 
 
 # ---------------------------------------------------------- index arithmetic ---

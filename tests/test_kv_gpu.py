@@ -432,6 +432,65 @@ def test_workspace_contents_do_not_matter():
             assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
 
 
+def test_binding_refuses():
+    """Nothing is launched for tensors that are not what the calls take."""
+    D, P, H, Hq, T = 64, 16, 2, 4, 3
+    c = _random_cache(4, H, P, D, 1)
+    before = {n: t.clone() for n, t in c.items()}
+    q, k, v, cos, sin = _append_inputs(T, H, Hq, D, D, False, 1, 64)
+    table, lens = _i32([[0], [1], [2]]), _i32([1, 2, 3])
+
+    def both(error, cache=c, q=q, k=k, v=v, table=table, lens=lens, cu=None, **kw):
+        with pytest.raises(error):
+            mhc.kv_append(cache, k, v, table, lens, cu, q=q, cos=cos, sin=sin)
+        with pytest.raises(error):
+            mhc.kv_attend(q, cache, table, lens, cu)
+
+    for n in c:
+        both(ValueError, dict(c, **{n: c[n].cpu()}))
+        both(TypeError, dict(c, **{n: c[n].view(torch.uint8) if n in "kv" else c[n].double()}))
+        both(TypeError, dict(c, **{n: None}))
+    both(ValueError, dict(c, v=c["v"][:3]))
+    both(ValueError, dict(c, k_scale=c["k_scale"].t().contiguous()))
+    both(ValueError, dict(c, k=c["k"].transpose(1, 2).contiguous().transpose(1, 2)))
+    both(TypeError, q=q.half(), k=k.half())
+    both(ValueError, q=q.cpu(), k=k.cpu())
+    both(ValueError, q=q[0], k=k[0])
+    both(ValueError, q=q[:, :, :32], k=k[:, :, :32])
+    both(ValueError, q=q[:, ::2], k=torch.cat([k, k], 1)[:, ::2])
+    both(ValueError, q=q[:2], k=k[:2], v=v[:2])                    # without cu_q one token for each sequence
+    both(TypeError, table=table.long())
+    both(ValueError, table=table[:2])
+    both(ValueError, lens=lens.cpu())
+    both(ValueError, cu=_i32([0, 3]))
+    both(TypeError, cu=_i32([0, 1, 2, 3]).long())
+    with pytest.raises(ValueError):
+        mhc.kv_append(c, k, v[:, :1], table, lens)
+    with pytest.raises(ValueError):
+        mhc.kv_append(c, k, v, table, lens, cos=cos)
+    with pytest.raises(ValueError):
+        mhc.kv_append(c, k, v, table, lens, cos=cos, sin=sin[:3])
+    with pytest.raises(ValueError):
+        mhc.kv_append(c, k, v, table, lens, q_out=q)
+    with pytest.raises(mhc.MhcError) as e:
+        mhc.kv_append(c, k, v, table, lens, cos=cos[:, :5].contiguous(), sin=sin[:, :5].contiguous())
+    assert e.value.status == 2
+    with pytest.raises(mhc.MhcError):
+        mhc.kv_append(c, k, v, table, lens, q=q, q_out=k.expand(T, H, D).repeat(1, 2, 1)[:, :Hq].as_strided((T, Hq, D), (0, D, 1)))
+    with pytest.raises(mhc.MhcError) as e:
+        mhc.kv_attend(q[:, :3], c, table, lens)                     # three query heads over two key heads
+    assert e.value.status == 1
+    for bad in (dict(out=q[:2]), dict(lse=torch.empty(T, Hq + 1, device="cuda")), dict(out=torch.empty_like(q).cpu())):
+        with pytest.raises(ValueError):
+            mhc.kv_attend(q, c, table, lens, **bad)
+    with pytest.raises(mhc.MhcError):
+        mhc.kv_attend(q, c, table, lens, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(mhc.MhcError):
+        mhc.kv_attend(q, c, table, lens, out=q)
+    for n in c:
+        assert torch.equal(c[n].view(torch.uint8), before[n].view(torch.uint8))
+
+
 def test_no_tokens():
     cache = mhc.kv_cache(2, 2, 16, 64)
     none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
