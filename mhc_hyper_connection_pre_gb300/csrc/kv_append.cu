@@ -6,7 +6,10 @@
 // with its chain of dependent loads (sequence, length, page, scale) for a
 // decode step.  The work of one page, head and tensor (k or v) belongs to one
 // group of threads, because the scale needs the largest magnitude of all of
-// the page's new numbers before the first of them can be rounded.
+// the page's new numbers before the first of them can be rounded.  The group
+// reads its numbers twice, the second time from the L1 cache: held in registers
+// between the passes they left half as many threads on an SM, and the loads of
+// a long prompt took 1.5 times as long.
 #include <cuda_runtime.h>
 
 #include "kv_common.cuh"
@@ -30,7 +33,6 @@ struct AppendArgs {
     const float* cos;
     const float* sin;
     int rope_rows, R;                 // R == 0: no rotation
-    int interleaved;
     int window;                       // tokens whose runs one group takes
     int windows;                      // ceil(T / window)
     int kv_blocks;                    // blocks [0, kv_blocks) append, the rest rotate q
@@ -43,17 +45,20 @@ struct Turn {
     float c[8], s[8];
 };
 
+enum Mode { kPlain, kHalves, kPairs };        // no rotation; pairs (i, i + R/2); pairs (2i, 2i + 1)
+
+template <int kMode>
 __device__ __forceinline__ void load_turn(const AppendArgs& a, int pos, int c, Turn& w) {
-    if (c * 8 >= a.R) return;
+    if (kMode == kPlain || c * 8 >= a.R) return;
     const int half = a.R / 2;
     const size_t row = (size_t)pos * half;
-    if (a.interleaved) {
+    if constexpr (kMode == kPairs) {
         const float4 u = __ldg(reinterpret_cast<const float4*>(a.cos + row + c * 4));
         const float4 v = __ldg(reinterpret_cast<const float4*>(a.sin + row + c * 4));
         w.c[0] = u.x; w.c[1] = u.y; w.c[2] = u.z; w.c[3] = u.w;
         w.s[0] = v.x; w.s[1] = v.y; w.s[2] = v.z; w.s[3] = v.w;
     } else {
-        const int i = (c * 8) % half;
+        const int i = c * 8 < half ? c * 8 : c * 8 - half;
 #pragma unroll
         for (int j = 0; j < 8; j += 4) {
             const float4 u = __ldg(reinterpret_cast<const float4*>(a.cos + row + i + j));
@@ -68,11 +73,11 @@ __device__ __forceinline__ void load_turn(const AppendArgs& a, int pos, int c, T
 // product and sum is rounded to fp32 (no fused multiply-add), as the header
 // states it: the result does not depend on who computes it.  Called by whole
 // warps (the shuffle); `w` is read only where the chunk is rotated.
+template <int kMode>
 __device__ __forceinline__ void rotate(const AppendArgs& a, const uint4& raw, int c, int lane, const Turn& w,
                                        float (&x)[8]) {
     unpack8(raw, x);
-    if (a.R == 0) return;
-    if (a.interleaved) {
+    if constexpr (kMode == kPairs) {
         if (c * 8 >= a.R) return;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -80,7 +85,7 @@ __device__ __forceinline__ void rotate(const AppendArgs& a, const uint4& raw, in
             x[2 * j] = __fsub_rn(__fmul_rn(u, w.c[j]), __fmul_rn(v, w.s[j]));
             x[2 * j + 1] = __fadd_rn(__fmul_rn(v, w.c[j]), __fmul_rn(u, w.s[j]));
         }
-    } else {
+    } else if constexpr (kMode == kHalves) {
         const int hc = a.R / 16;      // chunks of one side
         const bool first = c < hc, in = c < 2 * hc;
         const int other = in ? (first ? lane + hc : lane - hc) : lane;
@@ -139,66 +144,58 @@ __device__ __forceinline__ float group_max(float v, int group, float* red) {
 }
 
 // GT threads take one (window, head, k or v); 8 numbers of a token a thread.
-template <int D, int GT>
-__global__ void __launch_bounds__(GT > 256 ? GT : 256) kv_append_kernel(const AppendArgs a) {
-    constexpr int kBlock = GT > 256 ? GT : 256, kGroups = kBlock / GT;
-    constexpr int kChunks = D / 8, kRows = GT / kChunks, kHold = 4;   // rows of one step; steps held in registers
+template <int D, int GT, int kMode>
+__global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
+    constexpr int kBlock = 256, kGroups = kBlock / GT;
+    constexpr int kChunks = D / 8, kRows = GT / kChunks;              // rows of one step
     __shared__ float red[kBlock / 32];
     const int lane = threadIdx.x % 32;
 
     if ((int)blockIdx.x >= a.kv_blocks) {             // queries: a warp takes one token and some of its heads
         constexpr int kHeads = 32 / kChunks;          // heads of one step
-        constexpr int kAhead = 4;
         const int steps = (a.q_heads + kHeads - 1) / kHeads;
-        const int parts = (steps + a.q_steps - 1) / a.q_steps;
-        const int64_t w = (int64_t)((int)blockIdx.x - a.kv_blocks) * (kBlock / 32) + threadIdx.x / 32;
+        const uint32_t parts = (steps + a.q_steps - 1) / a.q_steps;
+        const uint32_t w = (blockIdx.x - a.kv_blocks) * (kBlock / 32) + threadIdx.x / 32;
         const int t = (int)(w / parts), part = (int)(w % parts);
-        if (w / parts >= a.seqs.T) return;
+        if (t >= a.seqs.T) return;
         const int c = lane % kChunks, first = part * a.q_steps * kHeads;
         const int end = a.q_heads < first + a.q_steps * kHeads ? a.q_heads : first + a.q_steps * kHeads;
-        const int h0 = first + lane / kChunks;
         const uint16_t* src = a.q + t * a.q_stride + c * 8;
         uint16_t* dst = a.q_out + t * a.q_out_stride + c * 8;
-        uint4 raw[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)              // the loads do not wait for the position
-            if (h0 + i * kHeads < end) raw[i] = *reinterpret_cast<const uint4*>(src + (h0 + i * kHeads) * D);
+        auto fetch = [&](int h) {
+            return h < end ? *reinterpret_cast<const uint4*>(src + h * D) : make_uint4(0, 0, 0, 0);
+        };
+        int h = first + lane / kChunks;
+        uint4 a0 = fetch(h), a1 = fetch(h + kHeads);  // these loads do not wait for the position
         const int b = seq_of(a.seqs, t, lane);
         const Span sp = span_of(a.seqs, b);
         int pos = t >= sp.begin && t < sp.end ? sp.before + (t - sp.begin) : -1;
-        if (pos >= a.rope_rows && a.R) pos = -1;      // reported by the append part
+        if (pos >= a.rope_rows && kMode != kPlain) pos = -1;          // reported by the append part
         Turn turn;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) turn.c[j] = 1.0f, turn.s[j] = 0.0f;
-        if (a.R && pos >= 0) load_turn(a, pos, c, turn);
-        for (int base = first; base < end; base += kHeads * kAhead) {
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                if (base + i * kHeads >= end) break;
-                const int h = base + lane / kChunks + i * kHeads;
-                float x[8];
-                uint4 now = raw[i];
-                if (h + kAhead * kHeads < end)
-                    raw[i] = *reinterpret_cast<const uint4*>(src + (h + kAhead * kHeads) * D);
-                rotate(a, now, c, lane, turn, x);
-                if (pos >= 0) now = pack8(x);
-                if (h < end) *reinterpret_cast<uint4*>(dst + h * D) = now;
-            }
+        if (pos >= 0) load_turn<kMode>(a, pos, c, turn);
+#pragma unroll 1
+        for (int base = first; base < end; base += kHeads, h += kHeads) {
+            const uint4 raw = a0;
+            a0 = a1;
+            a1 = fetch(h + 2 * kHeads);
+            float x[8];
+            rotate<kMode>(a, raw, c, lane, turn, x);  // whole warps
+            if (h < end) *reinterpret_cast<uint4*>(dst + h * D) = pos >= 0 ? pack8(x) : raw;
         }
         return;
     }
 
     const int group = threadIdx.x / GT, id = threadIdx.x % GT;
-    const int64_t item = (int64_t)blockIdx.x * kGroups + group;
-    const int head = (int)(item % a.heads), kv = (int)(item / a.heads % 2);
-    const int64_t win = item / (2 * a.heads);
+    const uint32_t item = blockIdx.x * kGroups + group, pair = item / a.heads;
+    const int head = (int)(item % a.heads), kv = (int)(pair & 1), win = (int)(pair >> 1);
     if (win >= a.windows) return;
-    const int t1 = (int)((win + 1) * a.window < a.seqs.T ? (win + 1) * a.window : a.seqs.T);
+    const int64_t next = (int64_t)(win + 1) * a.window;
+    const int t1 = (int)(next < a.seqs.T ? next : a.seqs.T);
     const int c = id % kChunks, r0 = id / kChunks;
     const uint16_t* src = a.x[kv] + head * D + c * 8;
-    const bool turned = kv == 0 && a.R > 0;
 
-    for (int t = (int)(win * a.window); t < t1;) {
+#pragma unroll 1
+    for (int t = win * a.window; t < t1;) {
         const int b = seq_of(a.seqs, t, lane);
         const Span sp = span_of(a.seqs, b);
         if (sp.bad && id == 0) atomicOr(&g_append_status, kIndexError);
@@ -211,74 +208,58 @@ __global__ void __launch_bounds__(GT > 256 ? GT : 256) kv_append_kernel(const Ap
         const int t0 = t;
         t = run.next;
         if (!starts_run(sp, run, t0)) continue;
-        const int page = page_of(a.seqs, b, run.pos);
         int n = run.n;
-        if (a.R > 0) {                                // positions beyond the tables: k and v are left out alike
+        if (kMode != kPlain) {                        // positions beyond the tables: k and v are left out alike
             const int rows = a.rope_rows - run.pos;
             if (rows < n) n = rows < 0 ? 0 : rows;
         }
+        auto fetch = [&](int r) {                     // r may be past the run: zeros
+            return r < n ? *reinterpret_cast<const uint4*>(src + (int64_t)(t0 + r) * a.x_stride[kv])
+                         : make_uint4(0, 0, 0, 0);
+        };
+        // f(r, the 8 numbers of row r): for every step of the run; whole warps
+        auto each = [&](uint4 raw, auto&& f) {
+#pragma unroll 1
+            for (int r = r0; r - r0 < n; r += kRows) {
+                const uint4 now = raw;
+                raw = fetch(r + kRows);
+                float x[8];
+                if (kMode != kPlain && kv == 0) {
+                    Turn turn;
+                    load_turn<kMode>(a, run.pos + (r < n ? r : 0), c, turn);
+                    rotate<kMode>(a, now, c, lane, turn, x);
+                } else {
+                    unpack8(now, x);
+                }
+                f(r, x);
+            }
+        };
+        const uint4 begin = fetch(r0);                // under way before the page, and its scale, are known
+        const int page = page_of(a.seqs, b, run.pos);
         if ((page < 0 || n < run.n) && id == 0) atomicOr(&g_append_status, kIndexError);
         if (page < 0 || n == 0) continue;
 
         float* scale_at = a.scale[kv] + (int64_t)page * a.heads + head;
         uint8_t* code = a.code[kv] + (((int64_t)page * a.heads + head) * D << a.seqs.page_log2);
         const float old = run.slot ? *scale_at : 0.0f;
-
-        auto load = [&](int r, float (&x)[8]) {       // r may be past the run: zeros
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            Turn turn;
-            if (r < n) {
-                raw = *reinterpret_cast<const uint4*>(src + (int64_t)(t0 + r) * a.x_stride[kv]);
-                if (turned) load_turn(a, run.pos + r, c, turn);
-            }
-            if (turned) rotate(a, raw, c, lane, turn, x);
-            else unpack8(raw, x);
-            if (r >= n) {
+        float top = 0.0f;
+        each(begin, [&](int, const float(&x)[8]) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-            }
-        };
-        auto largest = [](const float (&x)[8], float m) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m = finite(x[j]) ? fmaxf(m, fabsf(x[j])) : m;
-            return m;
-        };
-        float x[kHold][8], top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kHold; ++i)
-            if (i * kRows < n) {                      // the same for the whole group
-                load(i * kRows + r0, x[i]);
-                top = largest(x[i], top);
-            }
-        for (int base = kHold * kRows; base < n; base += kRows) {
-            float y[8];
-            load(base + r0, y);
-            top = largest(y, top);
-        }
+            for (int j = 0; j < 8; ++j) top = finite(x[j]) ? fmaxf(top, fabsf(x[j])) : top;
+        });
         top = group_max<GT>(top, group, red);
         const float need = scale_for(top), scale = run.slot ? fmaxf(old, need) : need;
         const float per = 1.0f / scale;               // scales are powers of two: x * per is x / scale
         if (id == 0) *scale_at = scale;               // every thread has read it: group_max was a barrier
-
-        auto store = [&](int r, float (&y)[8]) {
+        each(begin, [&](int r, float(&x)[8]) {
             if (r >= n) return;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = finite(y[j]) ? y[j] * per : __int_as_float(0x7fc00000);
-            uint2 v;
-            v.x = e4m3x4(y, 0);
-            v.y = e4m3x4(y, 4);
-            *reinterpret_cast<uint2*>(code + (int64_t)(run.slot + r) * D + c * 8) = v;
-        };
-#pragma unroll
-        for (int i = 0; i < kHold; ++i)
-            if (i * kRows < n) store(i * kRows + r0, x[i]);
-        for (int base = kHold * kRows; base < n; base += kRows) {
-            float y[8];
-            load(base + r0, y);
-            store(base + r0, y);
-        }
+            for (int j = 0; j < 8; ++j) x[j] = finite(x[j]) ? x[j] * per : __int_as_float(0x7fc00000);
+            *reinterpret_cast<uint2*>(code + (run.slot + r) * D + c * 8) = make_uint2(e4m3x4(x, 0), e4m3x4(x, 4));
+        });
         if (run.slot && scale != old) {               // the scale grew: round the page's earlier slots once more
             const float by = old / scale;
+#pragma unroll 1
             for (int i = id; i < run.slot * kChunks; i += GT) {
                 uint2* at = reinterpret_cast<uint2*>(code) + i;
                 const uint2 v = *at;
@@ -296,21 +277,28 @@ __global__ void __launch_bounds__(GT > 256 ? GT : 256) kv_append_kernel(const Ap
     }
 }
 
-template <int D, int GT>
-static cudaError_t launch_append(AppendArgs& a, cudaStream_t stream) {
-    constexpr int kBlock = GT > 256 ? GT : 256;
+template <int D, int GT, int kMode>
+static cudaError_t launch_mode(AppendArgs& a, cudaStream_t stream) {
+    constexpr int kBlock = 256;
     const int64_t items = (int64_t)a.windows * a.heads * 2;
     const int64_t kv_blocks = (items + kBlock / GT - 1) / (kBlock / GT);
     int64_t q_blocks = 0;
     if (a.q) {
         const int heads = 32 / (D / 8), steps = (a.q_heads + heads - 1) / heads;
         const int64_t warps = (int64_t)a.seqs.T * ((steps + a.q_steps - 1) / a.q_steps);
+        if (warps > 0x7fffffff) return cudaErrorInvalidValue;
         q_blocks = (warps + kBlock / 32 - 1) / (kBlock / 32);
     }
-    if (kv_blocks + q_blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    if (items > 0x7fffffff || kv_blocks + q_blocks > 0x7fffffff) return cudaErrorInvalidValue;
     a.kv_blocks = (int)kv_blocks;
-    kv_append_kernel<D, GT><<<(unsigned)(kv_blocks + q_blocks), kBlock, 0, stream>>>(a);
+    kv_append_kernel<D, GT, kMode><<<(unsigned)(kv_blocks + q_blocks), kBlock, 0, stream>>>(a);
     return cudaGetLastError();
+}
+
+template <int D, int GT>
+static cudaError_t launch_append(AppendArgs& a, int interleaved, cudaStream_t stream) {
+    if (a.R == 0) return launch_mode<D, GT, kPlain>(a, stream);
+    return interleaved ? launch_mode<D, GT, kPairs>(a, stream) : launch_mode<D, GT, kHalves>(a, stream);
 }
 
 cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code, float* k_scale, float* v_scale,
@@ -330,31 +318,16 @@ cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code,
     a.q_heads = q_heads;
     a.cos = cos; a.sin = sin;
     a.rope_rows = rope_rows; a.R = R;
-    a.interleaved = interleaved;
     // Few new tokens a sequence: a warp for each token that may start a run.
-    // Many: as many threads as hold a whole page, for each window of a page.
+    // Many: four warps for each window of as many tokens as a page has.
     const bool few = seqs.T < 8 * (int64_t)seqs.B;
     a.window = few ? 1 : 1 << seqs.page_log2;
     a.windows = (seqs.T + a.window - 1) / a.window;
+    // With few tokens a warp takes one step of a token's heads, else all of
+    // them, so that the position is found and its row of cos and sin read once.
     a.q_steps = seqs.T < 2048 ? 1 : 1 << 20;
-    const int gt = few ? 32 : (head_dim << seqs.page_log2) / 32;
-    if (head_dim == 64) {
-        switch (gt) {
-            case 32: return launch_append<64, 32>(a, stream);
-            case 64: return launch_append<64, 64>(a, stream);
-            case 128: return launch_append<64, 128>(a, stream);
-            case 256: return launch_append<64, 256>(a, stream);
-        }
-    } else if (head_dim == 128) {
-        switch (gt) {
-            case 32: return launch_append<128, 32>(a, stream);
-            case 64: return launch_append<128, 64>(a, stream);
-            case 128: return launch_append<128, 128>(a, stream);
-            case 256: return launch_append<128, 256>(a, stream);
-            case 512: return launch_append<128, 512>(a, stream);
-        }
-    }
-    return cudaErrorInvalidValue;
+    if (few) return head_dim == 64 ? launch_append<64, 32>(a, interleaved, stream) : launch_append<128, 32>(a, interleaved, stream);
+    return head_dim == 64 ? launch_append<64, 128>(a, interleaved, stream) : launch_append<128, 128>(a, interleaved, stream);
 }
 
 cudaError_t read_append_status(unsigned int* status) {
