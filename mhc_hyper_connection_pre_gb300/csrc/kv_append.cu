@@ -143,9 +143,10 @@ __device__ __forceinline__ float group_max(float v, int group, float* red) {
     return v;
 }
 
-// GT threads take one (window, head, k or v); 8 numbers of a token a thread.
-template <int D, int GT, int kMode>
-__global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
+// GT threads take one (window, head, k or v); 8 numbers of a token a thread, the
+// loads of kAhead steps under way together.
+template <int D, int GT, int kMode, int kAhead>
+__global__ void __launch_bounds__(256, kAhead > 1 ? 3 : 4) kv_append_kernel(const AppendArgs a) {
     constexpr int kBlock = 256, kGroups = kBlock / GT;
     constexpr int kChunks = D / 8, kRows = GT / kChunks;              // rows of one step
     __shared__ float red[kBlock / 32];
@@ -166,7 +167,9 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
             return h < end ? *reinterpret_cast<const uint4*>(src + h * D) : make_uint4(0, 0, 0, 0);
         };
         int h = first + lane / kChunks;
-        uint4 a0 = fetch(h), a1 = fetch(h + kHeads);  // these loads do not wait for the position
+        uint4 raw[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) raw[i] = fetch(h + i * kHeads);      // these loads do not wait for the position
         const int b = seq_of(a.seqs, t, lane);
         const Span sp = span_of(a.seqs, b);
         int pos = t >= sp.begin && t < sp.end ? sp.before + (t - sp.begin) : -1;
@@ -174,13 +177,15 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
         Turn turn;
         if (pos >= 0) load_turn<kMode>(a, pos, c, turn);
 #pragma unroll 1
-        for (int base = first; base < end; base += kHeads, h += kHeads) {
-            const uint4 raw = a0;
-            a0 = a1;
-            a1 = fetch(h + 2 * kHeads);
-            float x[8];
-            rotate<kMode>(a, raw, c, lane, turn, x);  // whole warps
-            if (h < end) *reinterpret_cast<uint4*>(dst + h * D) = pos >= 0 ? pack8(x) : raw;
+        for (int base = first; base < end; base += kAhead * kHeads) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                float x[8];
+                rotate<kMode>(a, raw[i], c, lane, turn, x);           // whole warps
+                if (h < end) *reinterpret_cast<uint4*>(dst + h * D) = pos >= 0 ? pack8(x) : raw[i];
+                raw[i] = fetch(h + kAhead * kHeads);
+                h += kHeads;
+            }
         }
         return;
     }
@@ -217,24 +222,33 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
             return r < n ? *reinterpret_cast<const uint4*>(src + (int64_t)(t0 + r) * a.x_stride[kv])
                          : make_uint4(0, 0, 0, 0);
         };
-        // f(r, the 8 numbers of row r): for every step of the run; whole warps
-        auto each = [&](uint4 raw, auto&& f) {
+        uint4 raw[kAhead];
+        auto fetch_all = [&](int r) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) raw[i] = fetch(r + i * kRows);
+        };
+        // f(r, the 8 numbers of row r): for every step of the run; whole warps.  The first steps are in `raw`.
+        auto each = [&](auto&& f) {
 #pragma unroll 1
-            for (int r = r0; r - r0 < n; r += kRows) {
-                const uint4 now = raw;
-                raw = fetch(r + kRows);
-                float x[8];
-                if (kMode != kPlain && kv == 0) {
-                    Turn turn;
-                    load_turn<kMode>(a, run.pos + (r < n ? r : 0), c, turn);
-                    rotate<kMode>(a, now, c, lane, turn, x);
-                } else {
-                    unpack8(now, x);
+            for (int base = 0; base < n; base += kAhead * kRows) {
+                if (base) fetch_all(base + r0);
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const int r = base + i * kRows + r0;
+                    if (base + i * kRows >= n) break;                 // the same for the whole group
+                    float x[8];
+                    if (kMode != kPlain && kv == 0) {
+                        Turn turn;
+                        load_turn<kMode>(a, run.pos + (r < n ? r : 0), c, turn);
+                        rotate<kMode>(a, raw[i], c, lane, turn, x);
+                    } else {
+                        unpack8(raw[i], x);
+                    }
+                    f(r, x);
                 }
-                f(r, x);
             }
         };
-        const uint4 begin = fetch(r0);                // under way before the page, and its scale, are known
+        fetch_all(r0);                                // under way before the page, and its scale, are known
         const int page = page_of(a.seqs, b, run.pos);
         if ((page < 0 || n < run.n) && id == 0) atomicOr(&g_append_status, kIndexError);
         if (page < 0 || n == 0) continue;
@@ -243,7 +257,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
         uint8_t* code = a.code[kv] + (((int64_t)page * a.heads + head) * D << a.seqs.page_log2);
         const float old = run.slot ? *scale_at : 0.0f;
         float top = 0.0f;
-        each(begin, [&](int, const float(&x)[8]) {
+        each([&](int, const float(&x)[8]) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) top = finite(x[j]) ? fmaxf(top, fabsf(x[j])) : top;
         });
@@ -251,7 +265,8 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
         const float need = scale_for(top), scale = run.slot ? fmaxf(old, need) : need;
         const float per = 1.0f / scale;               // scales are powers of two: x * per is x / scale
         if (id == 0) *scale_at = scale;               // every thread has read it: group_max was a barrier
-        each(begin, [&](int r, float(&x)[8]) {
+        if (n > kAhead * kRows) fetch_all(r0);
+        each([&](int r, float(&x)[8]) {
             if (r >= n) return;
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = finite(x[j]) ? x[j] * per : __int_as_float(0x7fc00000);
@@ -277,7 +292,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
     }
 }
 
-template <int D, int GT, int kMode>
+template <int D, int GT, int kMode, int kAhead>
 static cudaError_t launch_mode(AppendArgs& a, cudaStream_t stream) {
     constexpr int kBlock = 256;
     const int64_t items = (int64_t)a.windows * a.heads * 2;
@@ -291,14 +306,14 @@ static cudaError_t launch_mode(AppendArgs& a, cudaStream_t stream) {
     }
     if (items > 0x7fffffff || kv_blocks + q_blocks > 0x7fffffff) return cudaErrorInvalidValue;
     a.kv_blocks = (int)kv_blocks;
-    kv_append_kernel<D, GT, kMode><<<(unsigned)(kv_blocks + q_blocks), kBlock, 0, stream>>>(a);
+    kv_append_kernel<D, GT, kMode, kAhead><<<(unsigned)(kv_blocks + q_blocks), kBlock, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
-template <int D, int GT>
+template <int D, int GT, int kAhead>
 static cudaError_t launch_append(AppendArgs& a, int interleaved, cudaStream_t stream) {
-    if (a.R == 0) return launch_mode<D, GT, kPlain>(a, stream);
-    return interleaved ? launch_mode<D, GT, kPairs>(a, stream) : launch_mode<D, GT, kHalves>(a, stream);
+    if (a.R == 0) return launch_mode<D, GT, kPlain, kAhead>(a, stream);
+    return interleaved ? launch_mode<D, GT, kPairs, kAhead>(a, stream) : launch_mode<D, GT, kHalves, kAhead>(a, stream);
 }
 
 cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code, float* k_scale, float* v_scale,
@@ -319,15 +334,23 @@ cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code,
     a.cos = cos; a.sin = sin;
     a.rope_rows = rope_rows; a.R = R;
     // Few new tokens a sequence: a warp for each token that may start a run.
-    // Many: four warps for each window of as many tokens as a page has.
+    // Many: one to four warps for each window of as many tokens as a page has.
     const bool few = seqs.T < 8 * (int64_t)seqs.B;
     a.window = few ? 1 : 1 << seqs.page_log2;
     a.windows = (seqs.T + a.window - 1) / a.window;
     // With few tokens a warp takes one step of a token's heads, else all of
     // them, so that the position is found and its row of cos and sin read once.
     a.q_steps = seqs.T < 2048 ? 1 : 1 << 20;
-    if (few) return head_dim == 64 ? launch_append<64, 32>(a, interleaved, stream) : launch_append<128, 32>(a, interleaved, stream);
-    return head_dim == 64 ? launch_append<64, 128>(a, interleaved, stream) : launch_append<128, 128>(a, interleaved, stream);
+    if (few)
+        return head_dim == 64 ? launch_append<64, 32, 1>(a, interleaved, stream)
+                              : launch_append<128, 32, 1>(a, interleaved, stream);
+    switch ((head_dim << seqs.page_log2) / 128) {     // a page is 16 steps of its group, or fewer
+        case 128: return launch_append<128, 128, 4>(a, interleaved, stream);
+        case 64: return head_dim == 64 ? launch_append<64, 64, 4>(a, interleaved, stream)
+                                       : launch_append<128, 64, 4>(a, interleaved, stream);
+        default: return head_dim == 64 ? launch_append<64, 32, 4>(a, interleaved, stream)
+                                       : launch_append<128, 32, 4>(a, interleaved, stream);
+    }
 }
 
 cudaError_t read_append_status(unsigned int* status) {
