@@ -9,7 +9,8 @@
 // the page's new numbers before the first of them can be rounded.  The group
 // reads its numbers twice, the second time from the L1 cache: held in registers
 // between the passes they left half as many threads on an SM, and the loads of
-// a long prompt took 1.5 times as long.
+// a long prompt took 1.5 times as long.  16384 tokens of 40 query and 8 key
+// heads take 83 us: 445 MB at 5.4 TB/s (the queries alone 6.0 TB/s).
 #include <cuda_runtime.h>
 
 #include "kv_common.cuh"
@@ -39,69 +40,57 @@ struct AppendArgs {
     int q_steps;                      // head steps of one warp in the q part
 };
 
-// cos and sin of one thread's 8 elements (chunk c of a head): four pairs when
-// interleaved, one side of eight pairs otherwise.
-struct Turn {
+enum Mode { kPlain, kHalves, kPairs };        // no rotation; pairs (i, i + R/2); pairs (2i, 2i + 1)
+
+// A thread takes 16 numbers of a head: two chunks of 8 that hold both numbers
+// of its pairs, so that nothing is exchanged between threads and each cos and
+// sin is loaded once.  Thread p of a head's D/16 turns pairs 8p .. 8p + 7 if the
+// rotation has so many.
+struct Chunks {
+    int a, b;                                 // first numbers of the two chunks
+    bool turned;
+};
+
+template <int kMode>
+__device__ __forceinline__ Chunks chunks_of(int R, int p) {
+    const bool turned = kMode != kPlain && 16 * p < R;
+    if (kMode == kHalves && turned) return Chunks{8 * p, 8 * p + R / 2, true};
+    return Chunks{16 * p, 16 * p + 8, turned};        // with halves: what is left after the rotated numbers
+}
+
+struct Raw {                                  // the 16 numbers as stored
+    uint4 a, b;
+};
+
+struct Turn {                                 // cos and sin of the eight pairs
     float c[8], s[8];
 };
 
-enum Mode { kPlain, kHalves, kPairs };        // no rotation; pairs (i, i + R/2); pairs (2i, 2i + 1)
-
-template <int kMode>
-__device__ __forceinline__ void load_turn(const AppendArgs& a, int pos, int c, Turn& w) {
-    if (kMode == kPlain || c * 8 >= a.R) return;
-    const int half = a.R / 2;
-    const size_t row = (size_t)pos * half;
-    if constexpr (kMode == kPairs) {
-        const float4 u = __ldg(reinterpret_cast<const float4*>(a.cos + row + c * 4));
-        const float4 v = __ldg(reinterpret_cast<const float4*>(a.sin + row + c * 4));
-        w.c[0] = u.x; w.c[1] = u.y; w.c[2] = u.z; w.c[3] = u.w;
-        w.s[0] = v.x; w.s[1] = v.y; w.s[2] = v.z; w.s[3] = v.w;
-    } else {
-        const int i = c * 8 < half ? c * 8 : c * 8 - half;
+__device__ __forceinline__ void load_turn(const AppendArgs& a, int pos, int p, Turn& w) {
+    const size_t at = (size_t)pos * (a.R / 2) + 8 * p;
 #pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-            const float4 u = __ldg(reinterpret_cast<const float4*>(a.cos + row + i + j));
-            const float4 v = __ldg(reinterpret_cast<const float4*>(a.sin + row + i + j));
-            w.c[j] = u.x; w.c[j + 1] = u.y; w.c[j + 2] = u.z; w.c[j + 3] = u.w;
-            w.s[j] = v.x; w.s[j + 1] = v.y; w.s[j + 2] = v.z; w.s[j + 3] = v.w;
-        }
+    for (int j = 0; j < 8; j += 4) {
+        const float4 u = __ldg(reinterpret_cast<const float4*>(a.cos + at + j));
+        const float4 v = __ldg(reinterpret_cast<const float4*>(a.sin + at + j));
+        w.c[j] = u.x; w.c[j + 1] = u.y; w.c[j + 2] = u.z; w.c[j + 3] = u.w;
+        w.s[j] = v.x; w.s[j + 1] = v.y; w.s[j + 2] = v.z; w.s[j + 3] = v.w;
     }
 }
 
-// Rotates chunk c of a head whose chunks lie in consecutive lanes.  Every
-// product and sum is rounded to fp32 (no fused multiply-add), as the header
-// states it: the result does not depend on who computes it.  Called by whole
-// warps (the shuffle); `w` is read only where the chunk is rotated.
+// Every product and sum is rounded to fp32 (no fused multiply-add), as the
+// header states it: the result does not depend on who computes it.
 template <int kMode>
-__device__ __forceinline__ void rotate(const AppendArgs& a, const uint4& raw, int c, int lane, const Turn& w,
-                                       float (&x)[8]) {
-    unpack8(raw, x);
-    if constexpr (kMode == kPairs) {
-        if (c * 8 >= a.R) return;
+__device__ __forceinline__ void rotate(const Turn& w, float (&x)[8], float (&y)[8]) {
+    auto turn = [](float& u, float& v, float c, float s) {
+        const float p = u, q = v;
+        u = __fsub_rn(__fmul_rn(p, c), __fmul_rn(q, s));
+        v = __fadd_rn(__fmul_rn(q, c), __fmul_rn(p, s));
+    };
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float u = x[2 * j], v = x[2 * j + 1];
-            x[2 * j] = __fsub_rn(__fmul_rn(u, w.c[j]), __fmul_rn(v, w.s[j]));
-            x[2 * j + 1] = __fadd_rn(__fmul_rn(v, w.c[j]), __fmul_rn(u, w.s[j]));
-        }
-    } else if constexpr (kMode == kHalves) {
-        const int hc = a.R / 16;      // chunks of one side
-        const bool first = c < hc, in = c < 2 * hc;
-        const int other = in ? (first ? lane + hc : lane - hc) : lane;
-        uint4 o;
-        o.x = __shfl_sync(0xffffffffu, raw.x, other);
-        o.y = __shfl_sync(0xffffffffu, raw.y, other);
-        o.z = __shfl_sync(0xffffffffu, raw.z, other);
-        o.w = __shfl_sync(0xffffffffu, raw.w, other);
-        if (!in) return;
-        float y[8];
-        unpack8(o, y);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float p = __fmul_rn(x[j], w.c[j]), r = __fmul_rn(y[j], w.s[j]);
-            x[j] = first ? __fsub_rn(p, r) : __fadd_rn(p, r);
-        }
+    for (int j = 0; j < 8; ++j) {
+        if constexpr (kMode == kHalves) turn(x[j], y[j], w.c[j], w.s[j]);
+        else if (j < 4) turn(x[2 * j], x[2 * j + 1], w.c[j], w.s[j]);
+        else turn(y[2 * j - 8], y[2 * j - 7], w.c[j], w.s[j]);
     }
 }
 
@@ -143,46 +132,57 @@ __device__ __forceinline__ float group_max(float v, int group, float* red) {
     return v;
 }
 
-// GT threads take one (window, head, k or v); 8 numbers of a token a thread, the
-// loads of kAhead steps under way together.
+// GT threads take one (window, head, k or v), the loads of kAhead steps under
+// way together.
 template <int D, int GT, int kMode, int kAhead>
-__global__ void __launch_bounds__(256, kAhead > 1 ? 3 : 4) kv_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
     constexpr int kBlock = 256, kGroups = kBlock / GT;
-    constexpr int kChunks = D / 8, kRows = GT / kChunks;              // rows of one step
+    constexpr int kLanes = D / 16, kRows = GT / kLanes;               // threads of a head; rows of one step
     __shared__ float red[kBlock / 32];
     const int lane = threadIdx.x % 32;
+    const Chunks at = chunks_of<kMode>(a.R, lane % kLanes);
+    auto load = [&](const uint16_t* head) {
+        return Raw{*reinterpret_cast<const uint4*>(head + at.a), *reinterpret_cast<const uint4*>(head + at.b)};
+    };
+    const uint4 none = make_uint4(0, 0, 0, 0);
 
     if ((int)blockIdx.x >= a.kv_blocks) {             // queries: a warp takes one token and some of its heads
-        constexpr int kHeads = 32 / kChunks;          // heads of one step
+        constexpr int kHeads = 32 / kLanes;           // heads of one step
         const int steps = (a.q_heads + kHeads - 1) / kHeads;
         const uint32_t parts = (steps + a.q_steps - 1) / a.q_steps;
         const uint32_t w = (blockIdx.x - a.kv_blocks) * (kBlock / 32) + threadIdx.x / 32;
         const int t = (int)(w / parts), part = (int)(w % parts);
         if (t >= a.seqs.T) return;
-        const int c = lane % kChunks, first = part * a.q_steps * kHeads;
+        const int first = part * a.q_steps * kHeads;
         const int end = a.q_heads < first + a.q_steps * kHeads ? a.q_heads : first + a.q_steps * kHeads;
-        const uint16_t* src = a.q + t * a.q_stride + c * 8;
-        uint16_t* dst = a.q_out + t * a.q_out_stride + c * 8;
-        auto fetch = [&](int h) {
-            return h < end ? *reinterpret_cast<const uint4*>(src + h * D) : make_uint4(0, 0, 0, 0);
-        };
-        int h = first + lane / kChunks;
-        uint4 raw[kAhead];
+        const uint16_t* src = a.q + t * a.q_stride;
+        uint16_t* dst = a.q_out + t * a.q_out_stride;
+        auto fetch = [&](int h) { return h < end ? load(src + h * D) : Raw{none, none}; };
+        int h = first + lane / kLanes;
+        Raw raw[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) raw[i] = fetch(h + i * kHeads);      // these loads do not wait for the position
         const int b = seq_of(a.seqs, t, lane);
         const Span sp = span_of(a.seqs, b);
-        int pos = t >= sp.begin && t < sp.end ? sp.before + (t - sp.begin) : -1;
-        if (pos >= a.rope_rows && kMode != kPlain) pos = -1;          // reported by the append part
+        const int pos = t >= sp.begin && t < sp.end ? sp.before + (t - sp.begin) : -1;
+        const bool turned = at.turned && pos >= 0 && pos < a.rope_rows;       // beyond: reported by the append part
         Turn turn;
-        if (pos >= 0) load_turn<kMode>(a, pos, c, turn);
+        if (turned) load_turn(a, pos, lane % kLanes, turn);
 #pragma unroll 1
         for (int base = first; base < end; base += kAhead * kHeads) {
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                float x[8];
-                rotate<kMode>(a, raw[i], c, lane, turn, x);           // whole warps
-                if (h < end) *reinterpret_cast<uint4*>(dst + h * D) = pos >= 0 ? pack8(x) : raw[i];
+                if (turned) {
+                    float x[8], y[8];
+                    unpack8(raw[i].a, x);
+                    unpack8(raw[i].b, y);
+                    rotate<kMode>(turn, x, y);
+                    raw[i] = Raw{pack8(x), pack8(y)};
+                }
+                if (h < end) {
+                    *reinterpret_cast<uint4*>(dst + h * D + at.a) = raw[i].a;
+                    *reinterpret_cast<uint4*>(dst + h * D + at.b) = raw[i].b;
+                }
                 raw[i] = fetch(h + kAhead * kHeads);
                 h += kHeads;
             }
@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(256, kAhead > 1 ? 3 : 4) kv_append_kernel(cons
     if (win >= a.windows) return;
     const int64_t next = (int64_t)(win + 1) * a.window;
     const int t1 = (int)(next < a.seqs.T ? next : a.seqs.T);
-    const int c = id % kChunks, r0 = id / kChunks;
-    const uint16_t* src = a.x[kv] + head * D + c * 8;
+    const int r0 = id / kLanes;
+    const uint16_t* src = a.x[kv] + head * D;
 
 #pragma unroll 1
     for (int t = win * a.window; t < t1;) {
@@ -218,16 +218,13 @@ __global__ void __launch_bounds__(256, kAhead > 1 ? 3 : 4) kv_append_kernel(cons
             const int rows = a.rope_rows - run.pos;
             if (rows < n) n = rows < 0 ? 0 : rows;
         }
-        auto fetch = [&](int r) {                     // r may be past the run: zeros
-            return r < n ? *reinterpret_cast<const uint4*>(src + (int64_t)(t0 + r) * a.x_stride[kv])
-                         : make_uint4(0, 0, 0, 0);
-        };
-        uint4 raw[kAhead];
-        auto fetch_all = [&](int r) {
+        Raw raw[kAhead];
+        auto fetch_all = [&](int r) {                 // rows past the run: zeros
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) raw[i] = fetch(r + i * kRows);
+            for (int i = 0; i < kAhead; ++i)
+                raw[i] = r + i * kRows < n ? load(src + (int64_t)(t0 + r + i * kRows) * a.x_stride[kv]) : Raw{none, none};
         };
-        // f(r, the 8 numbers of row r): for every step of the run; whole warps.  The first steps are in `raw`.
+        // f(r, the 16 numbers of row r) for every row of this thread.  The first rows are in `raw`.
         auto each = [&](auto&& f) {
 #pragma unroll 1
             for (int base = 0; base < n; base += kAhead * kRows) {
@@ -235,16 +232,16 @@ __global__ void __launch_bounds__(256, kAhead > 1 ? 3 : 4) kv_append_kernel(cons
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
                     const int r = base + i * kRows + r0;
-                    if (base + i * kRows >= n) break;                 // the same for the whole group
-                    float x[8];
-                    if (kMode != kPlain && kv == 0) {
+                    if (r >= n) break;
+                    float x[8], y[8];
+                    unpack8(raw[i].a, x);
+                    unpack8(raw[i].b, y);
+                    if (kMode != kPlain && kv == 0 && at.turned) {
                         Turn turn;
-                        load_turn<kMode>(a, run.pos + (r < n ? r : 0), c, turn);
-                        rotate<kMode>(a, raw[i], c, lane, turn, x);
-                    } else {
-                        unpack8(raw[i], x);
+                        load_turn(a, run.pos + r, lane % kLanes, turn);
+                        rotate<kMode>(turn, x, y);
                     }
-                    f(r, x);
+                    f(r, x, y);
                 }
             }
         };
@@ -257,27 +254,34 @@ __global__ void __launch_bounds__(256, kAhead > 1 ? 3 : 4) kv_append_kernel(cons
         uint8_t* code = a.code[kv] + (((int64_t)page * a.heads + head) * D << a.seqs.page_log2);
         const float old = run.slot ? *scale_at : 0.0f;
         float top = 0.0f;
-        each([&](int, const float(&x)[8]) {
+        each([&](int, const float(&x)[8], const float(&y)[8]) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = finite(x[j]) ? fmaxf(top, fabsf(x[j])) : top;
+            for (int j = 0; j < 8; ++j) {
+                top = finite(x[j]) ? fmaxf(top, fabsf(x[j])) : top;
+                top = finite(y[j]) ? fmaxf(top, fabsf(y[j])) : top;
+            }
         });
         top = group_max<GT>(top, group, red);
         const float need = scale_for(top), scale = run.slot ? fmaxf(old, need) : need;
         const float per = 1.0f / scale;               // scales are powers of two: x * per is x / scale
         if (id == 0) *scale_at = scale;               // every thread has read it: group_max was a barrier
         if (n > kAhead * kRows) fetch_all(r0);
-        each([&](int r, float(&x)[8]) {
-            if (r >= n) return;
+        each([&](int r, float(&x)[8], float(&y)[8]) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = finite(x[j]) ? x[j] * per : __int_as_float(0x7fc00000);
-            *reinterpret_cast<uint2*>(code + (run.slot + r) * D + c * 8) = make_uint2(e4m3x4(x, 0), e4m3x4(x, 4));
+            for (int j = 0; j < 8; ++j) {
+                x[j] = finite(x[j]) ? x[j] * per : __int_as_float(0x7fc00000);
+                y[j] = finite(y[j]) ? y[j] * per : __int_as_float(0x7fc00000);
+            }
+            uint8_t* to = code + (run.slot + r) * D;
+            *reinterpret_cast<uint2*>(to + at.a) = make_uint2(e4m3x4(x, 0), e4m3x4(x, 4));
+            *reinterpret_cast<uint2*>(to + at.b) = make_uint2(e4m3x4(y, 0), e4m3x4(y, 4));
         });
         if (run.slot && scale != old) {               // the scale grew: round the page's earlier slots once more
             const float by = old / scale;
 #pragma unroll 1
-            for (int i = id; i < run.slot * kChunks; i += GT) {
-                uint2* at = reinterpret_cast<uint2*>(code) + i;
-                const uint2 v = *at;
+            for (int i = id; i < run.slot * (D / 8); i += GT) {
+                uint2* old_at = reinterpret_cast<uint2*>(code) + i;
+                const uint2 v = *old_at;
                 float y[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(256, kAhead > 1 ? 3 : 4) kv_append_kernel(cons
                     y[2 * j] = f.x * by;
                     y[2 * j + 1] = f.y * by;
                 }
-                *at = make_uint2(e4m3x4(y, 0), e4m3x4(y, 4));
+                *old_at = make_uint2(e4m3x4(y, 0), e4m3x4(y, 4));
             }
         }
     }
@@ -299,7 +303,7 @@ static cudaError_t launch_mode(AppendArgs& a, cudaStream_t stream) {
     const int64_t kv_blocks = (items + kBlock / GT - 1) / (kBlock / GT);
     int64_t q_blocks = 0;
     if (a.q) {
-        const int heads = 32 / (D / 8), steps = (a.q_heads + heads - 1) / heads;
+        const int heads = 32 / (D / 16), steps = (a.q_heads + heads - 1) / heads;
         const int64_t warps = (int64_t)a.seqs.T * ((steps + a.q_steps - 1) / a.q_steps);
         if (warps > 0x7fffffff) return cudaErrorInvalidValue;
         q_blocks = (warps + kBlock / 32 - 1) / (kBlock / 32);
@@ -344,12 +348,12 @@ cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code,
     if (few)
         return head_dim == 64 ? launch_append<64, 32, 1>(a, interleaved, stream)
                               : launch_append<128, 32, 1>(a, interleaved, stream);
-    switch ((head_dim << seqs.page_log2) / 128) {     // a page is 16 steps of its group, or fewer
-        case 128: return launch_append<128, 128, 4>(a, interleaved, stream);
-        case 64: return head_dim == 64 ? launch_append<64, 64, 4>(a, interleaved, stream)
-                                       : launch_append<128, 64, 4>(a, interleaved, stream);
-        default: return head_dim == 64 ? launch_append<64, 32, 4>(a, interleaved, stream)
-                                       : launch_append<128, 32, 4>(a, interleaved, stream);
+    switch ((head_dim << seqs.page_log2) / 128) {     // a page is 8 steps of its group, or fewer
+        case 128: return launch_append<128, 128, 2>(a, interleaved, stream);
+        case 64: return head_dim == 64 ? launch_append<64, 64, 2>(a, interleaved, stream)
+                                       : launch_append<128, 64, 2>(a, interleaved, stream);
+        default: return head_dim == 64 ? launch_append<64, 32, 2>(a, interleaved, stream)
+                                       : launch_append<128, 32, 2>(a, interleaved, stream);
     }
 }
 
