@@ -3,7 +3,7 @@
 // drafted tokens with many query heads to a key head.
 //
 // Mathematics.  A block takes 256 rows (new tokens x query heads of one
-// key/value head) as two tiles of 128 and walks over the keys 128 at a time:
+// key/value head) as two tiles of 128 and walks over the keys 64 at a time:
 // S = Q K^T and O += P V on the tensor cores (tcgen05), the softmax between
 // them with one thread a row.
 //   * K is used as it is stored: S is an e4m3 product.  A query row, divided
@@ -20,14 +20,16 @@
 //     (weights then reach 2^15, within f16), so that O, in tensor memory, is
 //     rescaled rarely; sums are fp32 and of the unrounded weights.
 //
-// What bounds it: 4 * 128 * 128 * head_dim operations for 128 keys and 128
-// rows on the tensor cores against 128 * 128 exponentials and the conversion
-// of V; the two tiles alternate, so that the softmax of one runs while the
-// other's products do.  The conversion is shared by the two tiles.
+// What bounds it: 4 * 128 * 64 * head_dim operations for 64 keys and 128 rows on
+// the tensor cores against 128 * 64 exponentials and the conversion of V.  Each
+// tile's S has two buffers in tensor memory, so that the next step's products
+// run during the softmax of this one; the two tiles share loads and conversion.
+// With one buffer (128 keys a step) each softmax waited for P V and Q K^T of its
+// own tile: 1272 us for a chunk of 4096 tokens over 16384 keys, 40 heads.
 //
 // Warps 0-3 and 4-7: softmax of the two tiles; 8-11: V to f16; 12: TMA loads;
-// 13: the tensor instructions; 14: planning.  The softmax gets 152 registers a thread and the
-// others 104 of the 128 that 16 warps start with.
+// 13 and 15: the tensor instructions of the two tiles; 14: planning.  The softmax gets 168 registers a thread and the
+// others 88 of the 128 that 16 warps start with.
 #include "kv_attend.cuh"
 
 namespace mhc {
@@ -36,15 +38,16 @@ namespace kv {
 namespace {
 
 constexpr int kThreads = 16 * 32;
-constexpr int kTile = 128;                    // rows of one tile, and keys of one step
+constexpr int kTile = 128;                    // rows of one tile, and keys of one load
+constexpr int kStep = 64;                     // keys of one step
 constexpr int kPair = 2 * kTile;              // rows of a block's work
 constexpr int kKStages = 3, kVStages = 2;
-constexpr int kMetas = 2 * kKStages;          // the softmax reads a step's key scales after its keys' stage is free
+constexpr int kMetas = 2 * kKStages;          // the softmax reads a load's key scales after its stage is free
 constexpr float kGrow = 5.0f;                 // the maximum follows when it has grown by more (in powers of two)
 constexpr float kVLift = 128.0f;              // V in f16 is 2^7 times code * scale / largest scale
 constexpr int kSegs = 4;                      // segments whose value scale and NaNs are kept: the converter runs two ahead
 
-struct __align__(16) Meta {                   // of one step: the scales of each 16 keys, which of them have a page
+struct __align__(16) Meta {                   // of one load: the scales of each 16 keys, which of them have a page
     float scale[8];
     uint32_t valid;
     int pad[3];
@@ -67,7 +70,7 @@ struct __align__(1024) Smem {
     float ref[kSegs];                         // largest value scale of the segment
     float red[4];
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-    uint64_t v16_full[2], v16_empty[2], q_full[2], s_full[2], p_full[2], o_full[2], done;
+    uint64_t v16_full[2], v16_empty[2], q_full[2], s_full[2][2], p_full[2][2], o_done[2], o_full[2], done;
     uint32_t tmem;
     int abort;
 };
@@ -124,11 +127,19 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
 }
 
-// Columns of tensor memory: S of the two tiles (P in its first half), then O.
-__device__ __forceinline__ uint32_t col_s(int x) { return x * kTile; }
+// Columns of tensor memory: S of the two tiles, two buffers each (P takes the
+// first half of its S), then O.
+__device__ __forceinline__ uint32_t col_s(int x, int buffer) { return x * 2 * kStep + buffer * kStep; }
 template <int D>
 __device__ __forceinline__ uint32_t col_o(int x) {
-    return 2 * kTile + x * D;
+    return 4 * kStep + x * D;
+}
+
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
 }
 
 // Ring position of the n-th use of a ring of N stages.
@@ -212,22 +223,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t raw[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+    constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kStep >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
     constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel waits for this one's end
     if (tid == 0) {
         sm.abort = 0;
-        for (int i = 0; i < kKStages; ++i) mbar_init(&sm.k_full[i], 1 + 8), mbar_init(&sm.k_empty[i], 1);
+        for (int i = 0; i < kKStages; ++i) mbar_init(&sm.k_full[i], 1 + 8), mbar_init(&sm.k_empty[i], 2);
         for (int i = 0; i < kVStages; ++i) mbar_init(&sm.v_full[i], 1 + 8), mbar_init(&sm.v_empty[i], 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.v16_full[i], 4);
-            mbar_init(&sm.v16_empty[i], 1);
+            mbar_init(&sm.v16_empty[i], 2);
             mbar_init(&sm.q_full[i], 4);
-            mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 4);
+            for (int b = 0; b < 2; ++b) mbar_init(&sm.s_full[i][b], 1), mbar_init(&sm.p_full[i][b], 4);
+            mbar_init(&sm.o_done[i], 1);
             mbar_init(&sm.o_full[i], 1);
         }
-        mbar_init(&sm.done, 1);
+        mbar_init(&sm.done, 2);
         fence_mbar_init_cluster();
     }
     if (warp == 13) tmem_alloc(&sm.tmem, 512);
@@ -256,13 +267,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<kMetas> mr;
     Ring<kVStages> vr;
     Ring<2> v16r;
-    uint32_t segs = 0, pairs = 0;             // segments with keys; of two tiles
-    uint32_t steps = 0, steps1 = 0;           // of a softmax warp's tile; of the first and second tile
-    uint32_t outs = 0, k_loads = 0, v_loads = 0;
+    uint32_t segs = 0;                        // segments with keys
+    uint32_t phases = 0;                      // of a tile's s_full or p_full: a bit for each buffer
+    uint32_t products = 0, outs = 0;          // P V of a softmax warp's tile so far; segments
+    uint32_t k_loads = 0, v_loads = 0;
 
     if (warp < 8) {
         // ------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         each_segments(others, [&] {
             const int x = warp / 4, in_tile = (warp % 4) * 32 + lane;
             const uint32_t lanes = tmem + ((uint32_t)(warp % 4) << 21);
@@ -273,10 +285,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int mine = x * kTile + in_tile;                // of the block's rows
                 const bool active = x == 0 || rows > kTile;
                 const int key0 = seg.key0, keys = seg.keys;
-                const int count = (keys - key0 + kTile - 1) / kTile;  // 0: a tile without keys
+                const int steps = (keys - key0 + kStep - 1) / kStep;   // 0: a tile without keys
                 float f = 0.0f, m = -INFINITY, l = 0.0f;
                 int lim = 0;
-                if (active && count > 0) {
+                if (active && steps > 0) {
                     // this thread's query row as hi + lo: once over it for its largest
                     // element, once more (from the cache) to split it, as the whole row
                     // would not fit the registers
@@ -339,79 +351,69 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                if (active && count > 0) {
+                if (active && steps > 0) {
                     tc_fence_before();        // the last segment's reads of O come before this one's products
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.q_full[x]);
                 }
 
                 const int all_see = keys_of_row(seg, a.cut, x * kTile);
-                for (int j = 0; j < count; ++j, mr.next()) {
-                    if (!active) continue;
-                    ok = __all_sync(0xffffffffu, wait_for(&sm.s_full[x], steps & 1, &sm.abort));
+                for (int j = 0; active && j < steps; ++j) {
+                    const int buffer = j & 1, half = 64 * buffer;
+                    ok = __all_sync(0xffffffffu, wait_for(&sm.s_full[x][buffer], (phases >> buffer) & 1, &sm.abort));
                     if (!ok) break;
-                    ++steps;
+                    phases ^= 1u << buffer;
                     tc_fence_after();
                     const Meta& meta = sm.k_meta[mr.stage];
-                    const uint32_t valid = meta.valid;
-                    const int n = lim - (key0 + j * kTile);   // keys of this step that the row sees
-                    const bool mask = key0 + (j + 1) * kTile > all_see || valid != 0xffu;
-                    // The row's 128 products, 64 at a time: their largest, the weights and
-                    // their sum.  P takes the first half of S's columns, behind the reads.
-                    f32x2 sum = make_f32x2(0.0f, 0.0f);
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t s[2][32];
+                    const int key = key0 + j * kStep, n = lim - key;      // n: keys of this step that the row sees
+                    const uint32_t valid = meta.valid >> (half / 16);
+                    const uint32_t from = lanes + col_s(x, buffer);
+                    // the row's 64 products: their largest, the weights and their sum
+                    uint32_t s[2][32];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) tmem_ld32(lanes + col_s(x) + half * 64 + c * 32, s[c]);
-                        tmem_wait_ld();
+                    for (int c = 0; c < 2; ++c) tmem_ld32(from + c * 32, s[c]);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) tmem_regs_ready(s[c]);
-                        if (mask) {
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const uint32_t bits = seen_bits(half * 64 + c * 32, n, valid);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) s[c][i] = (bits >> i) & 1 ? s[c][i] : 0xff800000u;
-                            }
-                        }
-                        const float top = fmaxf(row_max(s[0], half * 64, meta, f), row_max(s[1], half * 64 + 32, meta, f));
-                        const bool grow = top > m + kGrow;
-                        if (__any_sync(0xffffffffu, grow)) {
-                            const float keep = grow ? ex2(m - top) : 1.0f;
-                            m = grow ? top : m;
-                            l *= keep;
-                            sum = mul_rn2(sum, make_f32x2(keep, keep));
-                            if (half) {       // the weights of the first half
-                                const uint32_t k2 = pack_f16x2(keep, keep);
-                                uint32_t p[32];
-                                tmem_ld32(lanes + col_s(x), p);
-                                tmem_wait_ld();
-                                tmem_regs_ready(p);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) p[i] = mul_f16x2(p[i], k2);
-                                tmem_st32(lanes + col_s(x), p);
-                            }
-                            if (j > 0) {      // this tile's products up to now are done: S came after them
-#pragma unroll 1
-                                for (int c = 0; c < D / 32; ++c) {
-                                    uint32_t o[32];
-                                    tmem_ld32(lanes + col_o<D>(x) + c * 32, o);
-                                    tmem_wait_ld();
-                                    tmem_regs_ready(o);
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                                    tmem_st32(lanes + col_o<D>(x) + c * 32, o);
-                                }
-                            }
-                        }
-                        const float zero = m == -INFINITY ? 0.0f : m - kLift;
+                    for (int c = 0; c < 2; ++c) tmem_regs_ready(s[c]);
+                    if (key + kStep > all_see || (valid & 0xfu) != 0xfu) {
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            uint32_t p[16];
-                            weights(s[c], p, half * 64 + c * 32, meta, f, zero, sum);
-                            tmem_st16(lanes + col_s(x) + half * 32 + c * 16, p);
+                            const uint32_t bits = seen_bits(c * 32, n, valid);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) s[c][i] = (bits >> i) & 1 ? s[c][i] : 0xff800000u;
                         }
+                    }
+                    const float top = fmaxf(row_max(s[0], half, meta, f), row_max(s[1], half + 32, meta, f));
+                    const bool grow = top > m + kGrow;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float keep = grow ? ex2(m - top) : 1.0f;
+                        m = grow ? top : m;
+                        l *= keep;
+                        // after the last step's P V; the one before it is done, as S of this step came after
+                        // it, so that the phase's parity tells
+                        if (j > 0) {
+                            ok = __all_sync(0xffffffffu, wait_for(&sm.o_done[x], (products + j - 1) & 1, &sm.abort));
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32(lanes + col_o<D>(x) + c * 32, o);
+                                tmem_wait_ld();
+                                tmem_regs_ready(o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                                tmem_st32(lanes + col_o<D>(x) + c * 32, o);
+                            }
+                        }
+                    }
+                    const float zero = m == -INFINITY ? 0.0f : m - kLift;
+                    f32x2 sum = make_f32x2(0.0f, 0.0f);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t p[16];
+                        weights(s[c], p, half + c * 32, meta, f, zero, sum);
+                        tmem_st16(from + c * 16, p);
                     }
                     float sum0, sum1;
                     split_f32x2(sum, sum0, sum1);
@@ -419,11 +421,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.p_full[x]);
+                    if (lane == 0) mbar_arrive(&sm.p_full[x][buffer]);
+                    if (buffer || j + 1 == steps) mr.next();
                 }
+                if (!active)
+                    for (int j = 0; j < steps; j += 2) mr.next();
                 if (!ok) break;
                 if (!active) {
-                    segs += count > 0;
+                    segs += steps > 0;
                     continue;
                 }
 
@@ -431,7 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool whole = seg.parts == 1;
                 const int slot = seg.owner == blockIdx.x ? 1 : 0;
                 if (!whole && tid == 0) a.desc[2 * blockIdx.x + slot] = PartDesc{seg.parts, seg.owner, seg};
-                if (count > 0) {
+                if (steps > 0) {
+                    products += steps - 1;    // the last one completes o_full
                     ok = __all_sync(0xffffffffu, wait_for(&sm.o_full[x], outs & 1, &sm.abort));
                     if (!ok) break;
                     ++outs;
@@ -440,9 +446,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t at = mine < rows ? place_of(a, seg, mine) : 0;
                 float* part = part_of(a, blockIdx.x, slot, D);
                 const int kept = segs % kSegs;
-                const float unit = count > 0 ? sm.ref[kept] * (1.0f / kVLift) : 0.0f;
+                const float unit = steps > 0 ? sm.ref[kept] * (1.0f / kVLift) : 0.0f;
                 const float by = whole ? (l == 0.0f ? 0.0f : unit / l) : unit;
-                const bool nans = count > 0 && sm.has_nan[kept];
+                const bool nans = steps > 0 && sm.has_nan[kept];
                 if (mine < rows) {
                     if (whole && a.lse) a.lse[at] = lse_of(m, l);
                     if (!whole) *reinterpret_cast<float2*>(part + kPair * D + 2 * mine) = make_float2(m, l);
@@ -450,14 +456,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
-                    if (count > 0) {
+                    if (steps > 0) {
                         tmem_ld32(lanes + col_o<D>(x) + c * 32, o);
                         tmem_wait_ld();
                         tmem_regs_ready(o);
                     }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        float y = count > 0 ? __uint_as_float(o[i]) * by : 0.0f;
+                        float y = steps > 0 ? __uint_as_float(o[i]) * by : 0.0f;
                         if (nans && sm.nan_key[kept][c * 32 + i] < lim) y = __int_as_float(0x7fc00000);
                         o[i] = __float_as_uint(y);
                     }
@@ -477,12 +483,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                 }
-                segs += count > 0;
+                segs += steps > 0;
             }
         });
     } else if (warp < 12) {
         // ------------------------------------------------- values to f16
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         each_segments(others, [&] {
             const int id = tid - 256;         // this thread's key of a step
             bool ok = true;                   // after a wait that gave up all go on to the barriers, without work
@@ -582,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         });
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 12) {
             // ----------------------------------------------------------- TMA
             each_segments(others, [&] {
@@ -638,73 +644,85 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             });
-        } else if (warp == 13) {
-            // ------------------------------------------- tensor instructions
+        } else if (warp != 14) {
+            // ------------------------------- tensor instructions of one tile
+            // The whole warp runs the loop, so that the addresses stay in uniform
+            // registers, and one elected lane issues.  A warp for each tile: the
+            // issue of a step's twelve products takes longer than the products.
+            const int x = warp == 13 ? 0 : 1;
+            const uint64_t q_desc[2] = {smem_desc(smem_u32(sm.q[x][0]), 16, D * 8, D == 128 ? 2 : 4),
+                                        smem_desc(smem_u32(sm.q[x][1]), 16, D * 8, D == 128 ? 2 : 4)};
+            const uint64_t k_desc = smem_desc(smem_u32(sm.k[0]), 16, D * 8, D == 128 ? 2 : 4);
+            // values: dims contiguous ("MN-major"); 64 dims a 128-byte row, 8 keys an atom, 64 further dims 16 KB on
+            const uint64_t v_desc = smem_desc(smem_u32(sm.v16[0]), kTile * 128, 1024, 2);
+            const uint32_t s_col = tmem + col_s(x, 0), o_col = tmem + col_o<D>(x);
             each_segments(others, [&] {
-                if (lane > 0) return;
-                auto product_s = [&](int x, int stage) {
-                    const uint64_t kd = smem_desc(smem_u32(sm.k[stage]), 16, D * 8, D == 128 ? 2 : 4);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint64_t qd = smem_desc(smem_u32(sm.q[x][h]), 16, D * 8, D == 128 ? 2 : 4);
-#pragma unroll
-                        for (int i = 0; i < D / 32; ++i)
-                            mma_e4m3(tmem + col_s(x), qd + 2 * i, kd + 2 * i, kIdescS, h + i > 0);
-                    }
-                };
-                auto product_o = [&](int x, int stage, bool more) {
-                    // values: dims contiguous ("MN-major"); 64 dims a 128-byte row, 8 keys an atom, 64 further dims 16 KB on
-                    const uint64_t vd = smem_desc(smem_u32(sm.v16[stage]), kTile * 128, 1024, 2);
-#pragma unroll
-                    for (int i = 0; i < kTile / 16; ++i)
-                        mma_f16_ts(tmem + col_o<D>(x), tmem + col_s(x) + 8 * i, vd + 128 * i, kIdescO, more || i > 0);
-                };
+                const int segments = __shfl_sync(0xffffffffu, sm.count, 0);
                 bool ok = true;
-                for (int index = 0; ok && index < sm.count; ++index) {
-                    const Segment seg = sm.segs[index];
-                    const int key0 = seg.key0, keys = seg.keys;
-                    const bool two = seg.rows > kTile;
-                    const int count = (keys - key0 + kTile - 1) / kTile;
-                    if (count == 0) continue;
-                    // step j: for each tile O with the weights of step j - 1, then S of step j
 #pragma unroll 1
-                    for (int j = 0; ok && j <= count; ++j) {
+                for (int index = 0; ok && index < segments; ++index) {
+                    const bool mine = x == 0 || __shfl_sync(0xffffffffu, sm.segs[index].rows, 0) > kTile;
+                    const int steps =
+                        (__shfl_sync(0xffffffffu, sm.segs[index].keys - sm.segs[index].key0, 0) + kStep - 1) / kStep;
+                    if (steps <= 0) continue;
+                    if (!mine) {              // no second tile: its share of the stages is free as soon as it is full
 #pragma unroll 1
-                        for (int x = 0; x <= (int)two; ++x) {
-                            if (j > 0) {
-                                if (x == 0) ok = wait_for(&sm.v16_full[v16r.stage], v16r.phase, &sm.abort);
-                                ok = ok && wait_for(&sm.p_full[x], (x ? steps1 : steps) & 1, &sm.abort);
-                                if (!ok) break;
-                                if (x) ++steps1;
-                                else ++steps;
-                                tc_fence_after();
-                                product_o(x, v16r.stage, j > 1);
-                                if (j == count) mma_commit(&sm.o_full[x]);
+                        for (int j = 0; ok && j < steps; j += 2) {
+                            ok = __all_sync(0xffffffffu, wait_for(&sm.k_full[kr.stage], kr.phase, &sm.abort) &&
+                                                             wait_for(&sm.v16_full[v16r.stage], v16r.phase, &sm.abort));
+                            if (!ok) break;
+                            if (lane == 0) {
+                                mbar_arrive(&sm.k_empty[kr.stage]);
+                                mbar_arrive(&sm.v16_empty[v16r.stage]);
                             }
-                            if (j < count) {
-                                if (x == 0) ok = wait_for(&sm.k_full[kr.stage], kr.phase, &sm.abort);
-                                if (j == 0) ok = ok && wait_for(&sm.q_full[x], (x ? pairs : segs) & 1, &sm.abort);
-                                if (!ok) break;
-                                tc_fence_after();
-                                product_s(x, kr.stage);
-                                mma_commit(&sm.s_full[x]);
-                            }
-                        }
-                        if (!ok) break;
-                        if (j > 0) {
-                            mma_commit(&sm.v16_empty[v16r.stage]);
+                            kr.next();
                             v16r.next();
                         }
-                        if (j < count) {
-                            mma_commit(&sm.k_empty[kr.stage]);
-                            kr.next();
+                        continue;
+                    }
+                    // O with the weights of step j, then S of step j + 2 into their buffer
+#pragma unroll 1
+                    for (int j = -2; j < steps; ++j) {
+                        const int buffer = j & 1, next = j + 2;
+                        if (j >= 0) {
+                            if (buffer == 0) ok = wait_for(&sm.v16_full[v16r.stage], v16r.phase, &sm.abort);
+                            ok = __all_sync(0xffffffffu, ok && wait_for(&sm.p_full[x][buffer], (phases >> buffer) & 1, &sm.abort));
+                            if (!ok) break;
+                            phases ^= 1u << buffer;
+                            tc_fence_after();
+                            const uint64_t vd = v_desc + v16r.stage * (kTile * D * 2 / 16) + buffer * (kStep * 128 / 16);
+                            if (elect_one()) {
+#pragma unroll
+                                for (int i = 0; i < kStep / 16; ++i)
+                                    mma_f16_ts(o_col, s_col + buffer * kStep + 8 * i, vd + 128 * i, kIdescO, j > 0 || i > 0);
+                                mma_commit(j + 1 < steps ? &sm.o_done[x] : &sm.o_full[x]);
+                                if (buffer || j + 1 == steps) mma_commit(&sm.v16_empty[v16r.stage]);
+                            }
+                            if (buffer || j + 1 == steps) v16r.next();
+                        }
+                        if (next < steps) {   // 64 of the load's keys
+                            if (buffer == 0) ok = wait_for(&sm.k_full[kr.stage], kr.phase, &sm.abort);
+                            if (next == 0) ok = ok && wait_for(&sm.q_full[x], segs & 1, &sm.abort);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t kd = k_desc + kr.stage * (kTile * D / 16) + buffer * (kStep * D / 16);
+                            if (elect_one()) {
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                    for (int i = 0; i < D / 32; ++i)
+                                        mma_e4m3(s_col + buffer * kStep, q_desc[h] + 2 * i, kd + 2 * i, kIdescS, h + i > 0);
+                                mma_commit(&sm.s_full[x][buffer]);
+                                if (buffer || next + 1 == steps) mma_commit(&sm.k_empty[kr.stage]);
+                            }
+                            if (buffer || next + 1 == steps) kr.next();
                         }
                     }
                     ++segs;
-                    pairs += two;
                 }
             });
-        } else if (warp == 14) {
+        } else {
             // ------------------------------------------------------ planning
             take_census(a, sm.census, lane);
             __syncwarp();
@@ -720,15 +738,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 },
                 others);
-        } else {
-            each_segments(others, others);
         }
     }
 
     // Everything asynchronous has ended before the block does: the products by
     // their last commit, and, after a wait that gave up, the loads under way.
-    if (warp == 13 && lane == 0) {
-        mma_commit(&sm.done);
+    if (warp == 13 || warp == 15) {
+        if (elect_one()) mma_commit(&sm.done);
         mbar_wait_drain(&sm.done, 0);
     }
     if (warp == 12 && lane == 0 && sm.abort) {
