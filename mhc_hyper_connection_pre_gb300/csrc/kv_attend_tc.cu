@@ -684,40 +684,42 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int j = -2; j < steps; ++j) {
                         const int buffer = j & 1, next = j + 2;
-                        if (j >= 0) {
-                            if (buffer == 0) ok = wait_for(&sm.v16_full[v16r.stage], v16r.phase, &sm.abort);
-                            ok = __all_sync(0xffffffffu, ok && wait_for(&sm.p_full[x][buffer], (phases >> buffer) & 1, &sm.abort));
-                            if (!ok) break;
-                            phases ^= 1u << buffer;
-                            tc_fence_after();
-                            const uint64_t vd = v_desc + v16r.stage * (kTile * D * 2 / 16) + buffer * (kStep * 128 / 16);
-                            if (elect_one()) {
+                        const bool has_o = j >= 0, has_s = next < steps;
+                        const bool last_o = has_o && (buffer || j + 1 == steps);      // the last use of its load
+                        const bool last_s = has_s && (buffer || next + 1 == steps);
+                        // first what is there already, as a rule, then the weights: nothing else lies between
+                        // them and the products
+                        if (has_s && buffer == 0) ok = wait_for(&sm.k_full[kr.stage], kr.phase, &sm.abort);
+                        if (next == 0) ok = ok && wait_for(&sm.q_full[x], segs & 1, &sm.abort);
+                        if (has_o && buffer == 0) ok = ok && wait_for(&sm.v16_full[v16r.stage], v16r.phase, &sm.abort);
+                        const uint64_t vd = v_desc + v16r.stage * (kTile * D * 2 / 16) + buffer * (kStep * 128 / 16);
+                        const uint64_t kd = k_desc + kr.stage * (kTile * D / 16) + buffer * (kStep * D / 16);
+                        if (has_o) ok = ok && wait_for(&sm.p_full[x][buffer], (phases >> buffer) & 1, &sm.abort);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            if (has_o) {
 #pragma unroll
                                 for (int i = 0; i < kStep / 16; ++i)
                                     mma_f16_ts(o_col, s_col + buffer * kStep + 8 * i, vd + 128 * i, kIdescO, j > 0 || i > 0);
                                 mma_commit(j + 1 < steps ? &sm.o_done[x] : &sm.o_full[x]);
-                                if (buffer || j + 1 == steps) mma_commit(&sm.v16_empty[v16r.stage]);
                             }
-                            if (buffer || j + 1 == steps) v16r.next();
-                        }
-                        if (next < steps) {   // 64 of the load's keys
-                            if (buffer == 0) ok = wait_for(&sm.k_full[kr.stage], kr.phase, &sm.abort);
-                            if (next == 0) ok = ok && wait_for(&sm.q_full[x], segs & 1, &sm.abort);
-                            ok = __all_sync(0xffffffffu, ok);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint64_t kd = k_desc + kr.stage * (kTile * D / 16) + buffer * (kStep * D / 16);
-                            if (elect_one()) {
+                            if (has_s) {      // 64 of the load's keys
 #pragma unroll
                                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                                     for (int i = 0; i < D / 32; ++i)
                                         mma_e4m3(s_col + buffer * kStep, q_desc[h] + 2 * i, kd + 2 * i, kIdescS, h + i > 0);
                                 mma_commit(&sm.s_full[x][buffer]);
-                                if (buffer || next + 1 == steps) mma_commit(&sm.k_empty[kr.stage]);
                             }
-                            if (buffer || next + 1 == steps) kr.next();
+                            if (last_o) mma_commit(&sm.v16_empty[v16r.stage]);
+                            if (last_s) mma_commit(&sm.k_empty[kr.stage]);
                         }
+                        __syncwarp();
+                        if (has_o) phases ^= 1u << buffer;
+                        if (last_o) v16r.next();
+                        if (last_s) kr.next();
                     }
                     ++segs;
                 }
