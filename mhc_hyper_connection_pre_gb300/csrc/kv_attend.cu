@@ -270,8 +270,8 @@ __device__ __forceinline__ void piece(bool full, uint32_t ks, uint32_t vs, const
 
 // The plan's segment into the queue.  A call of its own: it is rare, and its
 // code does not belong between the loads'.
-__device__ __noinline__ void push_segment(const AttendArgs& a, Plan& plan, const Shares& shares, Segment& to) {
-    plan_next(plan, Lookup{a}, a.cut, shares, to);
+__device__ __noinline__ bool push_segment(const AttendArgs& a, Plan& plan, const Shares& shares, Segment& to) {
+    return plan_next(plan, Lookup{a}, a.cut, shares, to);
 }
 
 template <int D, int NB>
@@ -309,8 +309,8 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
         while (key >= keys) {
             if (plan.w.left <= 0 || pushed - popped == kQueue) return false;
             Segment& s = sm.queue[warp][pushed % kQueue];
-            if (lane == 0) push_segment(a, plan, sm.census.shares, s);
-            __syncwarp();
+            const bool found = lane == 0 && push_segment(a, plan, sm.census.shares, s);
+            if (!__any_sync(0xffffffffu, found)) return false;        // the share ends in a tile's extra units
             ++pushed;
             key = s.key0;
             keys = s.keys;
@@ -697,7 +697,7 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
     AttendArgs a;
     const int group = q_heads / heads, rows = tile_rows(group, seqs.B, seqs.T);
     a.seqs = seqs;
-    a.cut = Cut{heads, group, rows, rows == 256 ? 7 : kUnitLog2, 65536 / group + 1};
+    a.cut = Cut{heads, group, rows, rows == 256 ? 7 : kUnitLog2, rows == 256 ? 4 : 3, 65536 / group + 1};
     a.shares = shares_of(rows, head_dim, num_sms);
     a.k_scale = k_scale;
     a.v_scale = v_scale;

@@ -734,8 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) {
                         int n = 0;
 #pragma unroll 1
-                        while (sm.plan.w.left > 0 && n < kSegments)
-                            plan_next(sm.plan, Lookup{a}, a.cut, sm.census.shares, sm.segs[n++]);
+                        while (n < kSegments && plan_next(sm.plan, Lookup{a}, a.cut, sm.census.shares, sm.segs[n])) ++n;
                         sm.count = n;
                     }
                 },

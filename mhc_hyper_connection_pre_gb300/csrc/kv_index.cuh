@@ -97,8 +97,9 @@ MHC_HD bool starts_run(const Span& sp, const Run& r, int t) {
 // How mhc_kv_attend's work is cut.  The rows of one sequence and key/value head
 // are its new tokens times the `group` query heads that share the head, row r
 // being token r / group, query head r % group of it; a tile is `tile_rows` of
-// them.  A tile's keys are cut in units of 2^unit_log2; a tile without keys still is
-// one unit (its rows have to be written).  All units of all tiles, ordered by
+// them.  A tile's keys are cut in units of 2^unit_log2; a tile without keys
+// still is one unit (its rows have to be written), and what a tile costs beside
+// its keys (its queries, its rows' way out) counts as `extra` units.  All units of all tiles, ordered by
 // sequence, tile, head and key, form one line that the takers (warps or blocks)
 // share evenly whatever the lengths are, and a tile cut by a border is joined
 // afterwards.
@@ -112,6 +113,7 @@ struct SeqInfo {
 
 struct Cut {
     int heads, group, tile_rows, unit_log2;
+    int extra;              // units that a tile counts for beside those of its keys
     int group_inv;          // 65536 / group + 1: x / group is x * group_inv >> 16 for x up to 384
 };
 
@@ -126,9 +128,10 @@ MHC_HD SeqInfo info_of(const Span& sp, int group) {
 
 MHC_HD int tiles_of(const SeqInfo& s, const Cut& c) { return (s.rows + c.tile_rows - 1) / c.tile_rows; }
 
+// Units of a tile: those of its keys, at least one, and the extra ones, which come first.
 MHC_HD int units_of(int keys, const Cut& c) {
     const int n = (keys + (1 << c.unit_log2) - 1) >> c.unit_log2;
-    return n < 1 ? 1 : n;
+    return (n < 1 ? 1 : n) + c.extra;
 }
 
 // The tiles of a sequence one after the other, with the units of each; the
@@ -276,33 +279,43 @@ struct Plan {
     int64_t at;
 };
 
-// The plan's segment; then steps on.  look(b) finds sequence b.
+// The plan's next segment, if it has one: a part of a share that has only
+// extra units of a tile is none.  look(b) finds sequence b.
 template <class Look>
-MHC_HD void plan_next(Plan& p, const Look& look, const Cut& c, const Shares& shares, Segment& s) {
-    const int row0 = p.w.t.tile * c.tile_rows, tokens = row0 / c.group;
-    s.b = p.b;
-    s.head = p.w.head;
-    s.token = p.info.begin + tokens;
-    s.rem = row0 - tokens * c.group;
-    s.rows = p.info.rows - row0 < c.tile_rows ? p.info.rows - row0 : c.tile_rows;
-    s.see = p.info.before + tokens;
-    const int all = keys_of_row(s, c, s.rows - 1), end = (p.w.first + p.w.count) << c.unit_log2;
-    s.key0 = p.w.first << c.unit_log2;
-    s.keys = end < all ? end : all;
-    if (p.w.count == p.w.t.units) {
-        s.parts = 1;
-        s.owner = 0;
-    } else {
-        const int64_t begin = p.at - p.w.first;
-        s.owner = share_at(shares, begin);
-        s.parts = share_at(shares, begin + p.w.t.units - 1) - s.owner + 1;
+MHC_HD bool plan_next(Plan& p, const Look& look, const Cut& c, const Shares& shares, Segment& s) {
+    while (p.w.left > 0) {
+        const int end = p.w.first + p.w.count - c.extra;     // of the tile's key units
+        const bool some = end > 0;
+        if (some) {
+            const int first = p.w.first > c.extra ? p.w.first - c.extra : 0;
+            const int row0 = p.w.t.tile * c.tile_rows, tokens = row0 / c.group;
+            s.b = p.b;
+            s.head = p.w.head;
+            s.token = p.info.begin + tokens;
+            s.rem = row0 - tokens * c.group;
+            s.rows = p.info.rows - row0 < c.tile_rows ? p.info.rows - row0 : c.tile_rows;
+            s.see = p.info.before + tokens;
+            const int all = keys_of_row(s, c, s.rows - 1);
+            s.key0 = first << c.unit_log2;
+            s.keys = end << c.unit_log2 < all ? end << c.unit_log2 : all;
+            if (first == 0 && end == p.w.t.units - c.extra) {
+                s.parts = 1;
+                s.owner = 0;
+            } else {
+                const int64_t begin = p.at - p.w.first;      // of the tile
+                s.owner = share_at(shares, begin + c.extra);
+                s.parts = share_at(shares, begin + p.w.t.units - 1) - s.owner + 1;
+            }
+        }
+        p.at += p.w.count;
+        if (!walk_next(p.w, p.info, c) && p.w.left > 0) {
+            do p.info = look(++p.b);
+            while (p.info.rows == 0);
+            walk_enter(p.w, p.info, c, 0, p.w.left);
+        }
+        if (some) return true;
     }
-    p.at += p.w.count;
-    if (!walk_next(p.w, p.info, c) && p.w.left > 0) {
-        do p.info = look(++p.b);
-        while (p.info.rows == 0);
-        walk_enter(p.w, p.info, c, 0, p.w.left);
-    }
+    return false;
 }
 
 }  // namespace kv

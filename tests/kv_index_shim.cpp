@@ -41,10 +41,10 @@ void kv_runs(const int32_t* table, const int32_t* lens, const int32_t* cu, int w
 // tile, the first of them, keys that the first and the last row see}.  Returns
 // how many, or -1 if there are more than `most`; total: units of the line.
 int kv_segments(const int32_t* table, const int32_t* lens, const int32_t* cu, int width, int B, int T, int P,
-                int pages, int heads, int group, int tile_rows, int unit_log2, int share, int n, int32_t* out,
+                int pages, int heads, int group, int tile_rows, int unit_log2, int extra, int share, int n, int32_t* out,
                 int most, int64_t* total) {
     const Seqs s = make(table, lens, cu, width, B, T, P, pages);
-    const Cut c{heads, group, tile_rows, unit_log2, 65536 / group + 1};
+    const Cut c{heads, group, tile_rows, unit_log2, extra, 65536 / group + 1};
     *total = 0;
     for (int b = 0; b < B; ++b) *total += units_of_seq(info_of(span_of(s, b), group), c);
     const Shares shares = shares_of(*total, n);
@@ -61,10 +61,9 @@ int kv_segments(const int32_t* table, const int32_t* lens, const int32_t* cu, in
     p.at = from;
     walk_enter(p.w, p.info, c, from - seen, left);
     int found = 0;
-    while (p.w.left > 0) {
+    Segment g;
+    while (plan_next(p, [&](int b) { return info_of(span_of(s, b), group); }, c, shares, g)) {
         if (found == most) return -1;
-        Segment g;
-        plan_next(p, [&](int b) { return info_of(span_of(s, b), group); }, c, shares, g);
         const int32_t o[] = {g.b, g.token, g.rem, g.rows, g.head, g.key0, g.keys, g.parts, g.owner,
                              keys_of_row(g, c, 0), keys_of_row(g, c, g.rows - 1)};
         for (int i = 0; i < 11; ++i) out[11 * found + i] = o[i];
@@ -75,7 +74,7 @@ int kv_segments(const int32_t* table, const int32_t* lens, const int32_t* cu, in
 
 // Token and query head of every row of a segment's tile.
 void kv_rows(int token, int rem, int rows, int group, int32_t* out) {
-    const Cut c{1, group, 256, 5, 65536 / group + 1};
+    const Cut c{1, group, 256, 5, 0, 65536 / group + 1};
     const Segment g{0, 0, token, rem, rows, 0, 0, 0, 1, 0};
     for (int r = 0; r < rows; ++r) row_of(g, c, r, out[2 * r], out[2 * r + 1]);
 }

@@ -232,13 +232,13 @@ def test_runs_stay_inside_whatever_the_arrays_hold(shim, seed):
             assert -1 <= page < pages
 
 
-def _segments(shim, lens, cu, T, B, width, heads, group, rows, shares, unit=32):
+def _segments(shim, lens, cu, T, B, width, heads, group, rows, shares, unit=32, extra=0):
     """Every share's segments, in order, and the number of units."""
     pages = _i32(np.zeros((B, width)))
     out, total, got = np.zeros((20000, 11), dtype=np.int32), ctypes.c_int64(0), []
     for c in range(shares):
         n = shim.kv_segments(_ptr(pages), _ptr(lens), _ptr(cu), width, B, T, 16, 1, heads, group, rows,
-                             unit.bit_length() - 1, c, shares, _ptr(out), 20000, ctypes.byref(total))
+                             unit.bit_length() - 1, extra, c, shares, _ptr(out), 20000, ctypes.byref(total))
         assert n >= 0
         got.append(out[:n].tolist())
     return got, total.value
@@ -248,10 +248,11 @@ def _segments(shim, lens, cu, T, B, width, heads, group, rows, shares, unit=32):
 def test_shares_have_every_unit_once(shim, seed):
     """The shares' segments are all units of all tiles, each once and in
     order; every tile has a unit, no share is more than a unit longer than
-    another, and the parts of a tile know of one another."""
+    another (a tile's extra units counted), and a tile's parts know of one another."""
     r = random.Random(50 + seed)
     B, shares, P, unit = r.choice([1, 3, 17, 40]), r.choice([1, 7, 152, 1000]), 16, r.choice([32, 128])
     heads, group, rows = r.choice([1, 2, 8]), r.choice([1, 3, 5, 16, 128]), r.choice([8, 16, 256])
+    extra = r.choice([0, 1, 2, 5])
     counts = [r.choice([0, 1, 1, r.randint(0, 40), r.randint(0, 300 // group + 1)]) for _ in range(B)]
     lens = [r.choice([0, n, n + r.randint(0, 3000)]) for n in counts]
     if not any(counts):
@@ -260,14 +261,15 @@ def test_shares_have_every_unit_once(shim, seed):
     cu = [0]
     for n in counts:
         cu.append(cu[-1] + n)
-    got, total = _segments(shim, _i32(lens), _i32(cu), cu[-1], B, width, heads, group, rows, shares, unit)
-    expect = []
+    got, total = _segments(shim, _i32(lens), _i32(cu), cu[-1], B, width, heads, group, rows, shares, unit, extra)
+    expect, tiles = [], 0
     for b, (n, m) in enumerate(zip(lens, counts)):
         for i in range(-(-m * group // rows)):
             end = min((i + 1) * rows, m * group)
             sees = [max(0, n - m + x // group + 1) for x in (i * rows, end - 1)]
             tile = (b, cu[b] + i * rows // group, i * rows % group, end - i * rows)
             units = max(1, -(-sees[1] // unit))
+            tiles += heads
             for h in range(heads):
                 expect += [(*tile, h, *sees, u * unit, min((u + 1) * unit, sees[1])) for u in range(units)]
     flat, sizes, owners = [], [], {}
@@ -278,8 +280,11 @@ def test_shares_have_every_unit_once(shim, seed):
             sizes[-1] += units
             flat += [(b, t, rem, n, h, see0, see1, k0 + u * unit, min(k0 + (u + 1) * unit, k1)) for u in range(units)]
             owners.setdefault((b, t, rem, h), []).append((c, parts, owner))
-    assert flat == expect and total == len(expect)
-    assert max(sizes) - min(sizes) <= 1 and not any(sizes[total:])
+    assert flat == expect and total == len(expect) + extra * tiles
+    each = total // shares
+    assert max(sizes) <= each + 1 and not any(sizes[total:])
+    if extra == 0:
+        assert min(sizes) >= each
     for of in owners.values():
         assert [c for c, _, _ in of] == list(range(of[0][0], of[0][0] + len(of)))
         for _, parts, owner in of:
