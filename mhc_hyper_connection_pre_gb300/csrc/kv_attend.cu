@@ -56,7 +56,7 @@ struct __align__(1024) Smem {
     Meta meta[kWarps][kStages];
     Segment queue[kWarps][kQueue];
     Plan plan[kWarps];
-    Census census;
+    Shares shares[kWarps];
     uint64_t full[kWarps][kStages];
     int abort;
 };
@@ -176,7 +176,7 @@ __device__ __forceinline__ void piece(bool full, uint32_t ks, uint32_t vs, const
     const float most = fmaxf(v0, v1);
     float shrink = 1.0f;
     if (most > acc.ref) {                     // the same for the whole warp
-        acc.inv = 1.0f / most;
+        acc.inv = __frcp_rn(most);
         shrink = acc.ref * acc.inv;
         acc.ref = most;
         same = false;
@@ -289,14 +289,13 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
         for (int i = 0; i < kStages; ++i) mbar_init(&sm.full[warp][i], 1 + 4);   // lane 0 and the four scales
         fence_mbar_init_cluster();
     }
-    if (warp == 0) take_census(a, sm.census, lane);
     __syncthreads();
 
     // neighbouring shares go to different SMs, so that few units still spread over all of them
     const int share = warp * gridDim.x + blockIdx.x;
     if (lane < 2) a.desc[2 * share + lane].parts = 0;
     Plan& plan = sm.plan[warp];
-    enter_share(a, sm.census, share, plan, lane);
+    find_share(a, share, plan, sm.shares[warp], lane);
 
     uint32_t issued = 0, waited = 0;          // loads
     uint32_t pushed = 0, popped = 0;          // segments
@@ -309,7 +308,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
         while (key >= keys) {
             if (plan.w.left <= 0 || pushed - popped == kQueue) return false;
             Segment& s = sm.queue[warp][pushed % kQueue];
-            const bool found = lane == 0 && push_segment(a, plan, sm.census.shares, s);
+            const bool found = lane == 0 && push_segment(a, plan, sm.shares[warp], s);
             if (!__any_sync(0xffffffffu, found)) return false;        // the share ends in a tile's extra units
             ++pushed;
             key = s.key0;
@@ -365,73 +364,83 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
         more = settle();
     };
 
-    for (;;) {
-        if (!more) more = settle();
-        while (more && issued - waited < kStages && !*(volatile int*)&sm.abort) issue();
-        if (popped == pushed) break;
-        const Segment seg = sm.queue[warp][popped % kQueue];
-
-        // queries: thread (g, t) holds row g's dims [t D/4, (t + 1) D/4) of each block of 8 rows
-        uint32_t q[NB][D / 8];
-        float f[NB][2];
-        int lim[NB][2];
-        Acc<D, NB> acc;
-        acc.ref = acc.inv = 0.0f;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const int r = nb * 8 + g;
-            uint4 u[D / 32];
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) u[i] = make_uint4(0, 0, 0, 0);
-            if (r < seg.rows) {
-                int token, in_group;
-                row_of(seg, a.cut, r, token, in_group);
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    a.q + token * a.q_stride + (seg.head * a.cut.group + in_group) * D + t * (D / 4));
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) u[i] = __ldg(src + i);
-            }
-            float x[D / 4], top = 0.0f;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                float y[8];
-                unpack8(u[i], y);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x[8 * i + j] = y[j];
-                    top = fmaxf(top, fabsf(y[j]));
-                }
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            int e = 134 - (int)(__float_as_uint(top) >> 23);      // 7 - floor(log2(top))
-            e = e < -120 ? -120 : (e > 120 ? 120 : e);
-            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) q[nb][i] = pack_f16x2(x[2 * i] * up, x[2 * i + 1] * up);
-            const float back = down * a.scale_log2;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int c = nb * 8 + 2 * t + i;
-                f[nb][i] = __shfl_sync(0xffffffffu, back, (2 * t + i) * 4);
-                lim[nb][i] = c < seg.rows ? keys_of_row(seg, a.cut, c) : 0;
-                acc.m[nb][i] = -INFINITY;
-                acc.l[nb][i] = 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc.o[j][nb][i] = 0.0f;
-        }
-        const int all_see = keys_of_row(seg, a.cut, 0);           // keys that every row sees
-
-        bool ok = true;
+    // One turn: the loads that there is room for, then a piece of the segment
+    // under way, or the beginning or end of one.  So each part of the code is
+    // there once, and the loop stays in the instruction cache.
+    uint32_t q[NB][D / 8];
+    float f[NB][2];
+    int lim[NB][2], all_see = 0;
+    Acc<D, NB> acc;
+    Segment seg;
+    int at = 0;                               // the next piece's first key
+    bool open = false;                        // a segment is under way
 #pragma unroll 1
-        for (int at = seg.key0; at < seg.keys; at += kSub) {
+    for (;;) {
+        while (!*(volatile int*)&sm.abort && issued - waited < kStages) {
+            if (!more) more = settle();
+            if (!more) break;
+            issue();
+        }
+        if (!open) {
+            if (popped == pushed) break;
+            seg = sm.queue[warp][popped % kQueue];
+            at = seg.key0;
+            open = true;
+            // queries: thread (g, t) holds row g's dims [t D/4, (t + 1) D/4) of each block of 8 rows
+            acc.ref = acc.inv = 0.0f;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const int r = nb * 8 + g;
+                uint4 u[D / 32];
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) u[i] = make_uint4(0, 0, 0, 0);
+                if (r < seg.rows) {
+                    int token, in_group;
+                    row_of(seg, a.cut, r, token, in_group);
+                    const uint4* src = reinterpret_cast<const uint4*>(
+                        a.q + token * a.q_stride + (seg.head * a.cut.group + in_group) * D + t * (D / 4));
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) u[i] = __ldg(src + i);
+                }
+                float x[D / 4], top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    float y[8];
+                    unpack8(u[i], y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        x[8 * i + j] = y[j];
+                        top = fmaxf(top, fabsf(y[j]));
+                    }
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                int e = 134 - (int)(__float_as_uint(top) >> 23);      // 7 - floor(log2(top))
+                e = e < -120 ? -120 : (e > 120 ? 120 : e);
+                const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+                const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) q[nb][i] = pack_f16x2(x[2 * i] * up, x[2 * i + 1] * up);
+                const float back = down * a.scale_log2;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int c = nb * 8 + 2 * t + i;
+                    f[nb][i] = __shfl_sync(0xffffffffu, back, (2 * t + i) * 4);
+                    lim[nb][i] = c < seg.rows ? keys_of_row(seg, a.cut, c) : 0;
+                    acc.m[nb][i] = -INFINITY;
+                    acc.l[nb][i] = 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc.o[j][nb][i] = 0.0f;
+            }
+            all_see = keys_of_row(seg, a.cut, 0);           // keys that every row sees
+        }
+        if (at < seg.keys) {
             const int st = waited % kStages;
-            ok = waited != issued &&          // so after a wait that gave up
-                 __all_sync(0xffffffffu, wait_for(&sm.full[warp][st], (waited / kStages) & 1, &sm.abort));
+            const bool ok = waited != issued &&   // so after a wait that gave up
+                            __all_sync(0xffffffffu, wait_for(&sm.full[warp][st], (waited / kStages) & 1, &sm.abort));
             if (!ok) break;
             ++waited;
             const uint32_t base_addr = smem_u32(sm.ring[warp] + st * kStage);
@@ -439,9 +448,10 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
             const bool full = at + kSub <= all_see && meta.page[0] >= 0 && meta.page[1] >= 0;
             piece<D, NB>(full, base_addr, base_addr + kStage / 2, meta, q, f, lim, at, seg.keys, lane, acc);
             __syncwarp();                     // every lane has read the stage
-            if (more && !*(volatile int*)&sm.abort) issue();
+            at += kSub;
+            continue;
         }
-        if (!ok) break;
+        open = false;
 
         // the rows go out, or to the workspace: thread (g, t) has D/8 dims of rows 2t and 2t + 1
         const bool whole = seg.parts == 1;
@@ -459,7 +469,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
                 const float m = acc.m[nb][e];
                 const int r = nb * 8 + 2 * t + e;
                 if (r >= seg.rows) continue;
-                const float by = whole ? (l == 0.0f ? 0.0f : acc.ref / l) : acc.ref;
+                const float by = whole ? (l == 0.0f ? 0.0f : acc.ref * __frcp_rn(l)) : acc.ref;
                 if (whole) {
                     const int64_t to = place_of(a, seg, r);
                     uint4* out = reinterpret_cast<uint4*>(a.out + to * D + g * (D / 8));
@@ -486,6 +496,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
         }
         ++popped;
     }
+    if (share == 0) check_sequences(a, lane);
     // after a wait that gave up: the loads still under way
     for (; waited != issued; ++waited) mbar_wait_drain(&sm.full[warp][waited % kStages], (waited / kStages) & 1);
 }
@@ -501,14 +512,14 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x % 32, share = blockIdx.x * 8 + threadIdx.x / 32;
     if (share >= a.shares) return;
-    const int64_t next = 2 * (int64_t)a.cut.tile_rows * (D + 2);      // from a share's part to the next share's
+    const int64_t next = (int64_t)(2 * (D + 2)) << a.cut.tile_log2;      // from a share's part to the next share's
     const PartDesc& d = a.desc[2 * share + blockIdx.z];
     const int parts = d.parts;
     if (parts == 0) return;
     const Segment seg = d.seg;
     const float* first = part_of(a, d.owner, 1, D);
     const float* rest = part_of(a, d.owner + 1, 0, D) - next;     // part k, k > 0, at rest + k * next
-    const float* sums = a.cut.tile_rows * D + first;              // maxima and sums of the first part
+    const float* sums = (D << a.cut.tile_log2) + first;              // maxima and sums of the first part
     const int64_t to_rest = rest - first;
     const int mine = share - d.owner + parts * blockIdx.y, step = parts * gridDim.y;
 
@@ -554,7 +565,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a) {
                 }
             }
             const int64_t to = place_of(a, seg, r);
-            const float by = l == 0.0f ? 0.0f : 1.0f / l;
+            const float by = l == 0.0f ? 0.0f : __frcp_rn(l);
             uint32_t* out = reinterpret_cast<uint32_t*>(a.out + to * D + lane * kDims);
             if constexpr (D == 128)
                 *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o[0] * by, o[1] * by), pack_bf16x2(o[2] * by, o[3] * by));
@@ -635,7 +646,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a) {
         }
         if (sub) continue;
         const int64_t to = place_of(a, seg, r);
-        const float y = l == 0.0f ? 0.0f : 1.0f / l;
+        const float y = l == 0.0f ? 0.0f : __frcp_rn(l);
         *reinterpret_cast<uint2*>(a.out + to * D + (at - r * D)) =
             make_uint2(pack_bf16x2(o.x * y, o.y * y), pack_bf16x2(o.z * y, o.w * y));
         if (at == r * D && a.lse) a.lse[to] = lse_of(m, l);
@@ -674,7 +685,7 @@ cudaError_t launch_join(const AttendArgs& a, int head_dim, cudaStream_t stream) 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3((a.shares + 7) / 8, a.cut.tile_rows > 16 ? 64 : 1, 2);
+    cfg.gridDim = dim3((a.shares + 7) / 8, a.cut.tile_log2 > 4 ? 64 : 1, 2);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = stream;
     return cudaLaunchKernelEx(&cfg, head_dim == 64 ? kv_join_kernel<64> : kv_join_kernel<128>, a);
@@ -697,7 +708,7 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
     AttendArgs a;
     const int group = q_heads / heads, rows = tile_rows(group, seqs.B, seqs.T);
     a.seqs = seqs;
-    a.cut = Cut{heads, group, rows, rows == 256 ? 7 : kUnitLog2, rows == 256 ? 4 : 3, 65536 / group + 1};
+    a.cut = rows == 256 ? make_cut(heads, group, 8, 7, 4) : make_cut(heads, group, rows == 8 ? 3 : 4, kUnitLog2, 3);
     a.shares = shares_of(rows, head_dim, num_sms);
     a.k_scale = k_scale;
     a.v_scale = v_scale;

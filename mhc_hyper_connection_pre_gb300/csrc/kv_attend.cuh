@@ -32,13 +32,13 @@ struct AttendArgs {
     float scale_log2;                         // softmax_scale * log2(e)
     uint16_t* out;
     float* lse;
-    float* part;                              // [shares][2]: weighted values [tile_rows][D], maximum and sum [tile_rows][2]
+    float* part;                              // [shares][2]: weighted values [rows][D], maximum and sum [rows][2]
     PartDesc* desc;                           // [shares][2]
 };
 
 // Part `slot` of a share: 1 of the tile that it began (it is the owner), 0 of one that it went on with.
 __device__ __forceinline__ float* part_of(const AttendArgs& a, int share, int slot, int D) {
-    return a.part + ((int64_t)share * 2 + slot) * a.cut.tile_rows * (D + 2);
+    return a.part + (((int64_t)share * 2 + slot) * (D + 2) << a.cut.tile_log2);
 }
 
 constexpr int kSegments = 32;                 // that the tensor-memory kernel plans at a time
@@ -80,81 +80,83 @@ __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// What the first threads of the first block check of the call as a whole.
-__device__ __forceinline__ void check_offsets(const AttendArgs& a) {
-    if (blockIdx.x == 0 && threadIdx.x == 0 && a.seqs.cu && (a.seqs.cu[0] != 0 || a.seqs.cu[a.seqs.B] != a.seqs.T))
-        atomicOr(&g_device_status, kIndexError);
-}
-
 // Finds sequence b for a plan.
 struct Lookup {
     const AttendArgs& a;
-    __device__ __forceinline__ SeqInfo operator()(int b) const { return info_of(span_of(a.seqs, b), a.cut.group); }
+    __device__ __forceinline__ SeqInfo operator()(int b) const { return info_of(span_of(a.seqs, b)); }
 };
 
-// The line's shares, and how many units precede the end of each 32nd of the
-// sequences.
-struct Census {
-    Shares shares;
-    int each;                                 // sequences of a 32nd
-    int64_t upto[32];
-};
-
-// Counts the units of all sequences, lane i those of the i-th 32nd.  One warp.
-__device__ inline void take_census(const AttendArgs& a, Census& c, int lane) {
-    const int each = (a.seqs.B + 31) / 32, first = lane * each;
-    const int end = first + each < a.seqs.B ? first + each : a.seqs.B;
-    int64_t mine = 0;
-    bool bad = false;
+__device__ __forceinline__ int64_t sum_upto(int64_t x, int lane) {
 #pragma unroll 1
-    for (int i = first; i < end; ++i) {
-        const Span sp = span_of(a.seqs, i);
-        bad = bad || sp.bad;
-        mine += units_of_seq(info_of(sp, a.cut.group), a.cut);
-    }
-    if (blockIdx.x == 0) {
-        if (lane == 0 && a.seqs.cu) bad = bad || a.seqs.cu[0] != 0 || a.seqs.cu[a.seqs.B] != a.seqs.T;
-        if (bad) atomicOr(&g_device_status, kIndexError);
-    }
-    int64_t upto = mine;
-#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += up;
+        const int64_t up = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += up;
     }
-    c.upto[lane] = upto;
-    if (lane == 31) {
-        c.shares = shares_of(upto, a.shares);
-        c.each = each;
-    }
+    return x;
 }
 
-// Starts the plan of a share.  One warp.
-__device__ inline void enter_share(const AttendArgs& a, const Census& c, int share, Plan& p, int lane) {
-    const int64_t from = share_start(c.shares, share), left = share_start(c.shares, share + 1) - from;
-    const int64_t upto = c.upto[lane];
-    const int part = __ffs(__ballot_sync(0xffffffffu, upto > from)) - 1;
-    if (left > 0) {                           // then some part reaches beyond `from`
-        int64_t r = from - (part ? c.upto[part - 1] : 0);
-        int b = part * c.each;
-        SeqInfo info;
+// Finds a share of the line and starts its plan; the line's shares in `shares`.
+// One warp, which counts the units of all sequences: up to 32 of them a lane
+// each, beyond that a 32nd of them each and then the ones of the 32nd in which
+// the share begins.  No block-wide step, and each length is loaded once or
+// twice: what a decode step's latency consists of is loads that wait for one
+// another.
+__device__ inline void find_share(const AttendArgs& a, int share, Plan& p, Shares& shares, int lane) {
+    const Lookup look{a};
+    const int each = a.seqs.B <= 32 ? 1 : (a.seqs.B + 31) / 32, first = lane * each;
+    const int end = first + each < a.seqs.B ? first + each : a.seqs.B;
+    SeqInfo info{0, 0, 0};
+    int64_t mine = 0;
+#pragma unroll 4
+    for (int i = first; i < end; ++i) {
+        info = look(i);
+        mine += units_of_seq(info, a.cut);
+    }
+    int64_t upto = sum_upto(mine, lane);
+    const Shares sh = shares_of(__shfl_sync(0xffffffffu, upto, 31), a.shares);
+    if (lane == 0) shares = sh;
+    const int64_t from = share_start(sh, share), left = share_start(sh, share + 1) - from;
+    int at = __ffs(__ballot_sync(0xffffffffu, upto > from)) - 1, b = at;
+    int64_t before = __shfl_sync(0xffffffffu, upto - mine, at & 31);
+    if (each > 1 && left > 0) {               // inside the 32nd, 32 sequences at a time
+        const int stop = at * each + each < a.seqs.B ? at * each + each : a.seqs.B;
 #pragma unroll 1
-        for (;; ++b) {
-            info = Lookup{a}(b);
-            const int64_t u = units_of_seq(info, a.cut);
-            if (r < u) break;
-            r -= u;
+        for (b = at * each; b < stop; b += 32) {
+            info = b + lane < stop ? look(b + lane) : SeqInfo{0, 0, 0};
+            mine = units_of_seq(info, a.cut);
+            upto = before + sum_upto(mine, lane);
+            const uint32_t beyond = __ballot_sync(0xffffffffu, upto > from);
+            if (beyond) {
+                at = __ffs(beyond) - 1;
+                before = __shfl_sync(0xffffffffu, upto - mine, at);
+                b += at;
+                break;
+            }
+            before = __shfl_sync(0xffffffffu, upto, 31);
         }
-        if (lane == 0) {
+    }
+    info.begin = __shfl_sync(0xffffffffu, info.begin, at & 31);
+    info.tokens = __shfl_sync(0xffffffffu, info.tokens, at & 31);
+    info.before = __shfl_sync(0xffffffffu, info.before, at & 31);
+    if (lane == 0) {
+        p.w.left = 0;
+        if (left > 0) {
             p.b = b;
             p.info = info;
             p.at = from;
-            walk_enter(p.w, info, a.cut, r, left);
+            walk_enter(p.w, info, a.cut, from - before, left);
         }
-    } else if (lane == 0) {
-        p.w.left = 0;
     }
     __syncwarp();
+}
+
+// Reports lengths and offsets that had to be cut to what the arrays hold.  One
+// warp of the grid, when it has nothing else to do.
+__device__ inline void check_sequences(const AttendArgs& a, int lane) {
+    bool bad = lane == 0 && a.seqs.cu && (a.seqs.cu[0] != 0 || a.seqs.cu[a.seqs.B] != a.seqs.T);
+#pragma unroll 1
+    for (int i = lane; i < a.seqs.B; i += 32) bad = bad || span_of(a.seqs, i).bad;
+    if (bad) atomicOr(&g_device_status, kIndexError);
 }
 
 // mbar_wait, with the polling kept to a few instructions: the kernels here

@@ -61,7 +61,7 @@ struct __align__(1024) Smem {
     uint8_t v16[2][kTile * D * 2];            // f16: 64 dims of every key, then the next 64
     Segment segs[kSegments];
     Plan plan;
-    Census census;
+    Shares shares;
     int count;                                // of segs
     Meta k_meta[kMetas];
     Meta v_meta[kVStages];
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float* part = part_of(a, blockIdx.x, slot, D);
                 const int kept = segs % kSegs;
                 const float unit = steps > 0 ? sm.ref[kept] * (1.0f / kVLift) : 0.0f;
-                const float by = whole ? (l == 0.0f ? 0.0f : unit / l) : unit;
+                const float by = whole ? (l == 0.0f ? 0.0f : unit * __frcp_rn(l)) : unit;
                 const bool nans = steps > 0 && sm.has_nan[kept];
                 if (mine < rows) {
                     if (whole && a.lse) a.lse[at] = lse_of(m, l);
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 most = fmaxf(fmaxf(sm.red[0], sm.red[1]), fmaxf(sm.red[2], sm.red[3]));
                 if (id == 0) sm.ref[slot] = most;
                 named_bar_sync(1, 128);
-                const float per = most > 0.0f ? kVLift / most : 0.0f;
+                const float per = most > 0.0f ? kVLift * __frcp_rn(most) : 0.0f;
                 const int all_see = keys_of_row(seg, a.cut, 0);
                 for (int key = key0; ok && key < keys; key += kTile) {
                     ok = __all_sync(0xffffffffu, wait_for(&sm.v_full[vr.stage], vr.phase, &sm.abort)) &&
@@ -726,19 +726,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             });
         } else {
             // ------------------------------------------------------ planning
-            take_census(a, sm.census, lane);
-            __syncwarp();
-            enter_share(a, sm.census, blockIdx.x, sm.plan, lane);
+            find_share(a, blockIdx.x, sm.plan, sm.shares, lane);
             each_segments(
                 [&] {
                     if (lane == 0) {
                         int n = 0;
 #pragma unroll 1
-                        while (n < kSegments && plan_next(sm.plan, Lookup{a}, a.cut, sm.census.shares, sm.segs[n])) ++n;
+                        while (n < kSegments && plan_next(sm.plan, Lookup{a}, a.cut, sm.shares, sm.segs[n])) ++n;
                         sm.count = n;
                     }
                 },
                 others);
+            if (blockIdx.x == 0) check_sequences(a, lane);
         }
     }
 

@@ -7,8 +7,10 @@
 
 #ifdef __CUDACC__
 #define MHC_HD __host__ __device__ __forceinline__
+#define MHC_ROLLED _Pragma("unroll 1")      // a loop that is rare and must not fill the instruction cache
 #else
 #define MHC_HD inline
+#define MHC_ROLLED
 #endif
 
 namespace mhc {
@@ -96,7 +98,7 @@ MHC_HD bool starts_run(const Span& sp, const Run& r, int t) {
 // ---------------------------------------------------------------------------
 // How mhc_kv_attend's work is cut.  The rows of one sequence and key/value head
 // are its new tokens times the `group` query heads that share the head, row r
-// being token r / group, query head r % group of it; a tile is `tile_rows` of
+// being token r / group, query head r % group of it; a tile is 2^tile_log2 of
 // them.  A tile's keys are cut in units of 2^unit_log2; a tile without keys
 // still is one unit (its rows have to be written), and what a tile costs beside
 // its keys (its queries, its rows' way out) counts as `extra` units.  All units of all tiles, ordered by
@@ -107,26 +109,35 @@ MHC_HD bool starts_run(const Span& sp, const Run& r, int t) {
 // One sequence as the walk needs it.
 struct SeqInfo {
     int begin;              // first new token
-    int rows;               // new tokens * group
-    int len, before;
+    int tokens;             // new tokens
+    int before;             // keys before them
 };
 
+// The cut's sizes; what would be divisions by the group is worked out once.
 struct Cut {
-    int heads, group, tile_rows, unit_log2;
+    int heads, group;
+    int tile_log2, unit_log2;
     int extra;              // units that a tile counts for beside those of its keys
     int group_inv;          // 65536 / group + 1: x / group is x * group_inv >> 16 for x up to 384
+    int step_tokens, step_rem;  // rows of a tile / group and % group
 };
 
-MHC_HD SeqInfo info_of(const Span& sp, int group) {
+MHC_HD Cut make_cut(int heads, int group, int tile_log2, int unit_log2, int extra) {
+    const int rows = 1 << tile_log2;
+    return Cut{heads, group, tile_log2, unit_log2, extra, 65536 / group + 1, rows / group, rows % group};
+}
+
+MHC_HD SeqInfo info_of(const Span& sp) {
     SeqInfo r;
     r.begin = sp.begin;
-    r.rows = (sp.end - sp.begin) * group;
-    r.len = sp.len;
+    r.tokens = sp.end - sp.begin;
     r.before = sp.before;
     return r;
 }
 
-MHC_HD int tiles_of(const SeqInfo& s, const Cut& c) { return (s.rows + c.tile_rows - 1) / c.tile_rows; }
+MHC_HD int tiles_of(const SeqInfo& s, const Cut& c) {
+    return (s.tokens * c.group + (1 << c.tile_log2) - 1) >> c.tile_log2;
+}
 
 // Units of a tile: those of its keys, at least one, and the extra ones, which come first.
 MHC_HD int units_of(int keys, const Cut& c) {
@@ -134,35 +145,35 @@ MHC_HD int units_of(int keys, const Cut& c) {
     return (n < 1 ? 1 : n) + c.extra;
 }
 
-// The tiles of a sequence one after the other, with the units of each; the
-// last row's token (row / group) is kept without a division a tile.
+// The tiles of a sequence one after the other.
 struct Tiles {
     int tile, units;
-    int token, left;        // of the tile's last row, were the tile full: token * group + left
+    int token, rem;         // of its row 0: new token of the sequence, query head of the group
+    int rows, keys;         // keys: the most that any of its rows sees
 };
 
-MHC_HD void tiles_units(Tiles& t, const SeqInfo& s, const Cut& c) {
-    const int last = (s.rows - 1) / c.group;
-    const int keys = s.before + (t.token < last ? t.token : last) + 1;
-    t.units = units_of(keys < 0 ? 0 : keys, c);
+MHC_HD void tiles_measure(Tiles& t, const SeqInfo& s, const Cut& c) {
+    const int left = s.tokens * c.group - (t.tile << c.tile_log2);
+    t.rows = left < 1 << c.tile_log2 ? left : 1 << c.tile_log2;
+    const int n = s.before + t.token + ((t.rem + t.rows - 1) * c.group_inv >> 16) + 1;    // its last row's
+    t.keys = n < 0 ? 0 : n;
+    t.units = units_of(t.keys, c);
 }
 
 MHC_HD void tiles_start(Tiles& t, const SeqInfo& s, const Cut& c) {
-    t.tile = 0;
-    t.token = (c.tile_rows - 1) / c.group;
-    t.left = (c.tile_rows - 1) % c.group;
-    tiles_units(t, s, c);
+    t.tile = t.token = t.rem = 0;
+    tiles_measure(t, s, c);
 }
 
 MHC_HD void tiles_next(Tiles& t, const SeqInfo& s, const Cut& c) {
     ++t.tile;
-    t.token += c.tile_rows / c.group;
-    t.left += c.tile_rows % c.group;
-    if (t.left >= c.group) {
-        t.left -= c.group;
+    t.token += c.step_tokens;
+    t.rem += c.step_rem;
+    if (t.rem >= c.group) {
+        t.rem -= c.group;
         ++t.token;
     }
-    tiles_units(t, s, c);
+    tiles_measure(t, s, c);
 }
 
 // Units of all tiles and heads of a sequence.
@@ -172,9 +183,10 @@ MHC_HD int64_t units_of_seq(const SeqInfo& s, const Cut& c) {
     int64_t n = 0;
     Tiles t;
     tiles_start(t, s, c);
+    MHC_ROLLED
     for (int i = 0; i < tiles; ++i) {
         n += t.units;
-        tiles_next(t, s, c);
+        if (i + 1 < tiles) tiles_next(t, s, c);
     }
     return n * c.heads;
 }
@@ -246,6 +258,7 @@ MHC_HD void walk_cut(Walk& w) {
 MHC_HD void walk_enter(Walk& w, const SeqInfo& s, const Cut& c, int64_t r, int64_t left) {
     w.left = left;
     tiles_start(w.t, s, c);
+    MHC_ROLLED
     while (r >= (int64_t)w.t.units * c.heads) {
         r -= (int64_t)w.t.units * c.heads;
         tiles_next(w.t, s, c);
@@ -283,21 +296,20 @@ struct Plan {
 // extra units of a tile is none.  look(b) finds sequence b.
 template <class Look>
 MHC_HD bool plan_next(Plan& p, const Look& look, const Cut& c, const Shares& shares, Segment& s) {
+    MHC_ROLLED
     while (p.w.left > 0) {
         const int end = p.w.first + p.w.count - c.extra;     // of the tile's key units
         const bool some = end > 0;
         if (some) {
             const int first = p.w.first > c.extra ? p.w.first - c.extra : 0;
-            const int row0 = p.w.t.tile * c.tile_rows, tokens = row0 / c.group;
             s.b = p.b;
             s.head = p.w.head;
-            s.token = p.info.begin + tokens;
-            s.rem = row0 - tokens * c.group;
-            s.rows = p.info.rows - row0 < c.tile_rows ? p.info.rows - row0 : c.tile_rows;
-            s.see = p.info.before + tokens;
-            const int all = keys_of_row(s, c, s.rows - 1);
+            s.token = p.info.begin + p.w.t.token;
+            s.rem = p.w.t.rem;
+            s.rows = p.w.t.rows;
+            s.see = p.info.before + p.w.t.token;
             s.key0 = first << c.unit_log2;
-            s.keys = end << c.unit_log2 < all ? end << c.unit_log2 : all;
+            s.keys = end << c.unit_log2 < p.w.t.keys ? end << c.unit_log2 : p.w.t.keys;
             if (first == 0 && end == p.w.t.units - c.extra) {
                 s.parts = 1;
                 s.owner = 0;
@@ -309,8 +321,9 @@ MHC_HD bool plan_next(Plan& p, const Look& look, const Cut& c, const Shares& sha
         }
         p.at += p.w.count;
         if (!walk_next(p.w, p.info, c) && p.w.left > 0) {
+            MHC_ROLLED
             do p.info = look(++p.b);
-            while (p.info.rows == 0);
+            while (p.info.tokens == 0);
             walk_enter(p.w, p.info, c, 0, p.w.left);
         }
         if (some) return true;

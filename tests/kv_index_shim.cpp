@@ -41,19 +41,19 @@ void kv_runs(const int32_t* table, const int32_t* lens, const int32_t* cu, int w
 // tile, the first of them, keys that the first and the last row see}.  Returns
 // how many, or -1 if there are more than `most`; total: units of the line.
 int kv_segments(const int32_t* table, const int32_t* lens, const int32_t* cu, int width, int B, int T, int P,
-                int pages, int heads, int group, int tile_rows, int unit_log2, int extra, int share, int n, int32_t* out,
+                int pages, int heads, int group, int tile_log2, int unit_log2, int extra, int share, int n, int32_t* out,
                 int most, int64_t* total) {
     const Seqs s = make(table, lens, cu, width, B, T, P, pages);
-    const Cut c{heads, group, tile_rows, unit_log2, extra, 65536 / group + 1};
+    const Cut c = make_cut(heads, group, tile_log2, unit_log2, extra);
     *total = 0;
-    for (int b = 0; b < B; ++b) *total += units_of_seq(info_of(span_of(s, b), group), c);
+    for (int b = 0; b < B; ++b) *total += units_of_seq(info_of(span_of(s, b)), c);
     const Shares shares = shares_of(*total, n);
     const int64_t from = share_start(shares, share), left = share_start(shares, share + 1) - from;
     if (left <= 0) return 0;
     int64_t seen = 0;
     Plan p;
     for (p.b = 0;; ++p.b) {
-        p.info = info_of(span_of(s, p.b), group);
+        p.info = info_of(span_of(s, p.b));
         const int64_t u = units_of_seq(p.info, c);
         if (from < seen + u) break;
         seen += u;
@@ -62,7 +62,7 @@ int kv_segments(const int32_t* table, const int32_t* lens, const int32_t* cu, in
     walk_enter(p.w, p.info, c, from - seen, left);
     int found = 0;
     Segment g;
-    while (plan_next(p, [&](int b) { return info_of(span_of(s, b), group); }, c, shares, g)) {
+    while (plan_next(p, [&](int b) { return info_of(span_of(s, b)); }, c, shares, g)) {
         if (found == most) return -1;
         const int32_t o[] = {g.b, g.token, g.rem, g.rows, g.head, g.key0, g.keys, g.parts, g.owner,
                              keys_of_row(g, c, 0), keys_of_row(g, c, g.rows - 1)};
@@ -74,7 +74,7 @@ int kv_segments(const int32_t* table, const int32_t* lens, const int32_t* cu, in
 
 // Token and query head of every row of a segment's tile.
 void kv_rows(int token, int rem, int rows, int group, int32_t* out) {
-    const Cut c{1, group, 256, 5, 0, 65536 / group + 1};
+    const Cut c = make_cut(1, group, 8, 5, 0);
     const Segment g{0, 0, token, rem, rows, 0, 0, 0, 1, 0};
     for (int r = 0; r < rows; ++r) row_of(g, c, r, out[2 * r], out[2 * r + 1]);
 }

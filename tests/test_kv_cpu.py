@@ -237,7 +237,7 @@ def _segments(shim, lens, cu, T, B, width, heads, group, rows, shares, unit=32, 
     pages = _i32(np.zeros((B, width)))
     out, total, got = np.zeros((20000, 11), dtype=np.int32), ctypes.c_int64(0), []
     for c in range(shares):
-        n = shim.kv_segments(_ptr(pages), _ptr(lens), _ptr(cu), width, B, T, 16, 1, heads, group, rows,
+        n = shim.kv_segments(_ptr(pages), _ptr(lens), _ptr(cu), width, B, T, 16, 1, heads, group, rows.bit_length() - 1,
                              unit.bit_length() - 1, extra, c, shares, _ptr(out), 20000, ctypes.byref(total))
         assert n >= 0
         got.append(out[:n].tolist())
