@@ -26,6 +26,8 @@ extern "C" {
  * mantissa bits, no infinity, NaN = 0x7f / 0xff), dense
  * [num_pages][heads][page_tokens][head_dim]; a stored number stands for
  * code * scale[page][head].  k and v are 16-byte aligned, the scales 4-byte.
+Scales are finite and not negative; those of pages that mhc_kv_append goes on
+with are powers of two, as it writes them (mhc_kv_attend takes any).
  * page_tokens is 16, 32, 64 or 128; head_dim 64 or 128; num_pages * heads
  * at most 2^31 - 1.
  */

@@ -1,5 +1,5 @@
 // kv_attend.cu -- causal attention of the new tokens over the paged e4m3
-// cache (mhc_kv_attend), for few rows a sequence: decoding.
+// cache (mhc_kv_attend), for few rows a sequence (see tile_rows): decoding.
 //
 // Mathematics.  The rows of a tile are the new tokens and query heads that
 // share a key/value head (8 or 16 of them).  A warp takes 32 keys at a time
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     bool open = false;                        // a segment is under way
 #pragma unroll 1
     for (;;) {
-        while (!*(volatile int*)&sm.abort && issued - waited < kStages) {
+        while (issued - waited < kStages && !__any_sync(0xffffffffu, *(volatile int*)&sm.abort)) {
             if (!more) more = settle();
             if (!more) break;
             issue();
@@ -653,9 +653,19 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a) {
     }
 }
 
-// Rows of a tile.  Up to 16 rows a sequence: one tile of 8 or 16 for the warps
-// of this file; more: the tensor-memory kernel's 256.
-int tile_rows(int group, int64_t B, int64_t T) { return T * group > 16 * B ? 256 : (T * group > 8 * B ? 16 : 8); }
+// Rows of a tile: 8 or 16 for the warps of this file, 256 for the
+// tensor-memory kernel.  On average B sequences have T * group / B rows, and a
+// tile reads all their keys.  Measured (us; 8 key heads; 64 sequences of 4096
+// keys | 1 of 32768):
+//    rows   head_dim 128: 8, 16, 256               head_dim 64: 8, 16, 256
+//       8   106, 119, 217 | 30, 31, 40             65,  82, 181 | 30, 31, 35
+//      16     -, 122, 221 |  -, 33, 42              -,  85, 185 |  -, 34, 36
+//      32     -, 224, 227 |  -, 42, 42              -, 150, 188 |  -, 36, 36
+//      48     -, 325, 231 |  -, 56, 44              -, 213, 191 |  -, 42, 36
+int tile_rows(int group, int head_dim, int64_t B, int64_t T) {
+    const int64_t rows = T * group;
+    return rows > (head_dim == 64 ? 32 : 16) * B ? 256 : (rows > 8 * B ? 16 : 8);
+}
 
 // Shares of the work: warps, or the tensor-memory kernel's blocks.
 int shares_of(int rows, int D, int num_sms) {
@@ -697,7 +707,7 @@ cudaError_t launch_kv_attend_tc(const AttendArgs& a, const uint8_t* k, const uin
                                 cudaStream_t stream);
 
 size_t kv_attend_workspace(int heads, int head_dim, int q_heads, int64_t B, int64_t T, int num_sms) {
-    const int rows = tile_rows(q_heads / heads, B, T), shares = shares_of(rows, head_dim, num_sms);
+    const int rows = tile_rows(q_heads / heads, head_dim, B, T), shares = shares_of(rows, head_dim, num_sms);
     return part_bytes(rows, head_dim, shares) + (size_t)shares * 2 * sizeof(PartDesc);
 }
 
@@ -706,7 +716,7 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
                              int q_heads, float softmax_scale, uint16_t* out, float* lse, void* workspace,
                              int num_sms, cudaStream_t stream) {
     AttendArgs a;
-    const int group = q_heads / heads, rows = tile_rows(group, seqs.B, seqs.T);
+    const int group = q_heads / heads, rows = tile_rows(group, head_dim, seqs.B, seqs.T);
     a.seqs = seqs;
     a.cut = rows == 256 ? make_cut(heads, group, 8, 7, 4) : make_cut(heads, group, rows == 8 ? 3 : 4, kUnitLog2, 3);
     a.shares = shares_of(rows, head_dim, num_sms);

@@ -1,6 +1,6 @@
 // kv_attend.cuh -- what the kernels of mhc_kv_attend share: their arguments,
-// how a block finds its part of the work, the
-// parts that cut tiles leave behind, and the tensor maps of the cache.
+// how a warp or block finds its part of the work, the parts that cut tiles
+// leave behind, and the tensor maps of the cache.
 #pragma once
 
 #include <cuda.h>

@@ -28,8 +28,9 @@
 // own tile: 1272 us for a chunk of 4096 tokens over 16384 keys, 40 heads.
 //
 // Warps 0-3 and 4-7: softmax of the two tiles; 8-11: V to f16; 12: TMA loads;
-// 13 and 15: the tensor instructions of the two tiles; 14: planning.  The softmax gets 168 registers a thread and the
-// others 88 of the 128 that 16 warps start with.
+// 13 and 15: the tensor instructions of the two tiles; 14: planning.  The
+// softmax gets 168 registers a thread and the others 88 of the 128 that 16
+// warps start with.
 #include "kv_attend.cuh"
 
 namespace mhc {
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int index = 0; ok && index < sm.count; ++index) {
                 const Segment seg = sm.segs[index];
-                                const int rows = seg.rows;
+                const int rows = seg.rows;
                 const int mine = x * kTile + in_tile;                // of the block's rows
                 const bool active = x == 0 || rows > kTile;
                 const int key0 = seg.key0, keys = seg.keys;
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;                   // after a wait that gave up all go on to the barriers, without work
             for (int index = 0; index < sm.count; ++index) {
                 const Segment seg = sm.segs[index];
-                                const int key0 = seg.key0, keys = seg.keys;
+                const int key0 = seg.key0, keys = seg.keys;
                 if (keys <= key0) continue;
                 const int slot = segs++ % kSegs, log2 = a.seqs.page_log2;
                 const int32_t* row = a.seqs.table + (int64_t)seg.b * a.seqs.width;

@@ -231,6 +231,12 @@ ATTENDS = [
     (128, 16, 1, 128, [3], [90]),
     (64, 32, 1, 64, None, [77, 5]),
     (128, 64, 1, 40, [65, 0, 200], [65, 10, 190]),
+    (64, 32, 2, 32, [2, 2], [300, 2]),                       # 32 and 33 rows, 16 and 17 rows
+    (64, 32, 1, 11, [3, 3], [300, 1000]),
+    (128, 32, 1, 8, [2, 2], [300, 2]),
+    (128, 32, 1, 17, None, [1000, 30, 0]),
+    (128, 16, 2, 64, [4, 3], [5000, 130]),                   # 128 and 129 rows, long
+    (64, 64, 1, 43, [3, 3], [3001, 64]),
 ]
 
 
@@ -502,3 +508,20 @@ def test_e4m3_rounding_of_the_reference_is_the_format():
     x = torch.linspace(-448, 448, 40001)
     x = torch.cat([x, x * 2.0 ** -14])
     assert torch.equal(e4m3_round(x.double()), x.to(torch.float8_e4m3fn).double())
+
+
+def test_example_prompt_then_tokens():
+    """The attention sublayer of examples/: prompts and then single tokens from a replayed graph, against all
+    tokens in one call.  The two write the same keys and values with scales that grew differently, so each side
+    is off by at most e4m3's half step (2^-4 of a value); the streams carry the rest unchanged."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_decode.py")
+    spec = importlib.util.spec_from_file_location("attention_decode", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    stepped, at_once = (t.double() for t in m.run())
+    assert stepped.shape == at_once.shape == (3, 4, 4, 5120)
+    assert (stepped - at_once).norm() <= 2 * 2.0 ** -4 * at_once.norm()
+    for i in range(4):                                   # and no step is another's
+        assert (stepped[:, i] - at_once[:, i]).norm() <= 2 * 2.0 ** -4 * at_once[:, i].norm()
