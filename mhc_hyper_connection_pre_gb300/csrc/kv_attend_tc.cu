@@ -70,8 +70,9 @@ struct __align__(1024) Smem {
     int has_nan[kSegs];
     float ref[kSegs];                         // largest value scale of the segment
     float red[4];
+    float2 half[kTile];                       // maximum and sum of a row's odd halves
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-    uint64_t v16_full[2], v16_empty[2], q_full[2], s_full[2][2], p_full[2][2], o_done[2], o_full[2], done;
+    uint64_t v16_full[2], v16_empty[2], q_full[2], s_full[2][2], p_full[2][2], o_done[2], o_full[2], half_full, half_read, done;
     uint32_t tmem;
     int abort;
 };
@@ -217,6 +218,12 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t (&p)[1
     }
 }
 
+// Steps of a tile for so many keys.  `split`: up to 128 rows, which both tiles
+// take, the first the even and the second the odd 64 keys of each load.
+__device__ __forceinline__ int steps_of(bool split, int keys) {
+    return split ? (keys + kTile - 1) / kTile : (keys + kStep - 1) / kStep;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_attend_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
@@ -239,6 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.o_done[i], 1);
             mbar_init(&sm.o_full[i], 1);
         }
+        mbar_init(&sm.half_full, 4);
+        mbar_init(&sm.half_read, 4);
         mbar_init(&sm.done, 2);
         fence_mbar_init_cluster();
     }
@@ -270,7 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<2> v16r;
     uint32_t segs = 0;                        // segments with keys
     uint32_t phases = 0;                      // of a tile's s_full or p_full: a bit for each buffer
-    uint32_t products = 0, outs = 0;          // P V of a softmax warp's tile so far; segments
+    uint32_t products = 0, halves = 0;        // P V of a softmax warp's tile so far; segments in halves
+    bool unread = false;                      // tile 0 may still read this tile's last O
     uint32_t k_loads = 0, v_loads = 0;
 
     if (warp < 8) {
@@ -283,13 +293,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int index = 0; ok && index < sm.count; ++index) {
                 const Segment seg = sm.segs[index];
                 const int rows = seg.rows;
-                const int mine = x * kTile + in_tile;                // of the block's rows
-                const bool active = x == 0 || rows > kTile;
+                const bool split = rows <= kTile;
+                const int mine = split ? in_tile : x * kTile + in_tile;              // of the block's rows
                 const int key0 = seg.key0, keys = seg.keys;
-                const int steps = (keys - key0 + kStep - 1) / kStep;   // 0: a tile without keys
+                const int steps = steps_of(split, keys - key0);      // 0: a tile without keys
                 float f = 0.0f, m = -INFINITY, l = 0.0f;
                 int lim = 0;
-                if (active && steps > 0) {
+                if (steps > 0) {
                     // this thread's query row as hi + lo: once over it for its largest
                     // element, once more (from the cache) to split it, as the whole row
                     // would not fit the registers
@@ -351,22 +361,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sts128(lo_at + chunk_at<D>(in_tile, c), make_uint4(rest[0], rest[1], rest[2], rest[3]));
                     }
                     fence_proxy_async_smem();
-                }
-                if (active && steps > 0) {
-                    tc_fence_before();        // the last segment's reads of O come before this one's products
+                    if (unread) {             // the last segment's reads of O come before this one's products
+                        ok = __all_sync(0xffffffffu, wait_for(&sm.half_read, (halves - 1) & 1, &sm.abort));
+                        if (!ok) break;
+                        unread = false;
+                        tc_fence_after();
+                    }
+                    tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.q_full[x]);
                 }
 
-                const int all_see = keys_of_row(seg, a.cut, x * kTile);
-                for (int j = 0; active && j < steps; ++j) {
-                    const int buffer = j & 1, half = 64 * buffer;
+                const int all_see = keys_of_row(seg, a.cut, split ? 0 : x * kTile);
+                for (int j = 0; j < steps; ++j) {
+                    const int buffer = j & 1, half = kStep * (split ? x : buffer);   // of the load
                     ok = __all_sync(0xffffffffu, wait_for(&sm.s_full[x][buffer], (phases >> buffer) & 1, &sm.abort));
                     if (!ok) break;
                     phases ^= 1u << buffer;
                     tc_fence_after();
                     const Meta& meta = sm.k_meta[mr.stage];
-                    const int key = key0 + j * kStep, n = lim - key;      // n: keys of this step that the row sees
+                    const int key = key0 + (split ? j * kTile : (j & ~1) * kStep) + half;
+                    const int n = lim - key;  // keys of this step that the row sees
                     const uint32_t valid = meta.valid >> (half / 16);
                     const uint32_t from = lanes + col_s(x, buffer);
                     // the row's 64 products: their largest, the weights and their sum
@@ -423,12 +438,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.p_full[x][buffer]);
-                    if (buffer || j + 1 == steps) mr.next();
+                    if (split || buffer || j + 1 == steps) mr.next();
                 }
-                if (!active)
-                    for (int j = 0; j < steps; j += 2) mr.next();
                 if (!ok) break;
-                if (!active) {
+                if (steps > 0) {
+                    products += steps - 1;    // the last one completes o_full
+                    ok = __all_sync(0xffffffffu, wait_for(&sm.o_full[x], segs & 1, &sm.abort));
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                // tile 0 brings the halves of the keys together
+                const bool join = split && steps > 0;
+                float own = 1.0f, other = 0.0f;       // weights of the two O
+                if (join) {
+                    if (x == 1) {
+                        sm.half[in_tile] = make_float2(m, l);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.half_full);
+                        unread = true;
+                    } else {
+                        ok = __all_sync(0xffffffffu, wait_for(&sm.half_full, halves & 1, &sm.abort));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const float2 ml = sm.half[in_tile];
+                        const float top = fmaxf(m, ml.x), zero = top == -INFINITY ? 0.0f : top;
+                        own = ex2(m - zero);
+                        other = ex2(ml.x - zero);
+                        m = top;
+                        l = l * own + ml.y * other;
+                    }
+                    ++halves;
+                }
+                if (split && x == 1) {
                     segs += steps > 0;
                     continue;
                 }
@@ -437,13 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool whole = seg.parts == 1;
                 const int slot = seg.owner == blockIdx.x ? 1 : 0;
                 if (!whole && tid == 0) a.desc[2 * blockIdx.x + slot] = PartDesc{seg.parts, seg.owner, seg};
-                if (steps > 0) {
-                    products += steps - 1;    // the last one completes o_full
-                    ok = __all_sync(0xffffffffu, wait_for(&sm.o_full[x], outs & 1, &sm.abort));
-                    if (!ok) break;
-                    ++outs;
-                    tc_fence_after();
-                }
                 const int64_t at = mine < rows ? place_of(a, seg, mine) : 0;
                 float* part = part_of(a, blockIdx.x, slot, D);
                 const int kept = segs % kSegs;
@@ -461,6 +496,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld32(lanes + col_o<D>(x) + c * 32, o);
                         tmem_wait_ld();
                         tmem_regs_ready(o);
+                    }
+                    if (join) {
+                        uint32_t o1[32];
+                        tmem_ld32(lanes + col_o<D>(1) + c * 32, o1);
+                        tmem_wait_ld();
+                        tmem_regs_ready(o1);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * own + __uint_as_float(o1[i]) * other);
                     }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
@@ -483,6 +527,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
+                }
+                if (join) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.half_read);
                 }
                 segs += steps > 0;
             }
@@ -662,39 +711,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool ok = true;
 #pragma unroll 1
                 for (int index = 0; ok && index < segments; ++index) {
-                    const bool mine = x == 0 || __shfl_sync(0xffffffffu, sm.segs[index].rows, 0) > kTile;
+                    const bool split = __shfl_sync(0xffffffffu, sm.segs[index].rows, 0) <= kTile;
                     const int steps =
-                        (__shfl_sync(0xffffffffu, sm.segs[index].keys - sm.segs[index].key0, 0) + kStep - 1) / kStep;
+                        steps_of(split, __shfl_sync(0xffffffffu, sm.segs[index].keys - sm.segs[index].key0, 0));
                     if (steps <= 0) continue;
-                    if (!mine) {              // no second tile: its share of the stages is free as soon as it is full
-#pragma unroll 1
-                        for (int j = 0; ok && j < steps; j += 2) {
-                            ok = __all_sync(0xffffffffu, wait_for(&sm.k_full[kr.stage], kr.phase, &sm.abort) &&
-                                                             wait_for(&sm.v16_full[v16r.stage], v16r.phase, &sm.abort));
-                            if (!ok) break;
-                            if (lane == 0) {
-                                mbar_arrive(&sm.k_empty[kr.stage]);
-                                mbar_arrive(&sm.v16_empty[v16r.stage]);
-                            }
-                            kr.next();
-                            v16r.next();
-                        }
-                        continue;
-                    }
                     // O with the weights of step j, then S of step j + 2 into their buffer
 #pragma unroll 1
                     for (int j = -2; j < steps; ++j) {
                         const int buffer = j & 1, next = j + 2;
                         const bool has_o = j >= 0, has_s = next < steps;
-                        const bool last_o = has_o && (buffer || j + 1 == steps);      // the last use of its load
-                        const bool last_s = has_s && (buffer || next + 1 == steps);
+                        const int half = split ? x : buffer;          // of the load
+                        const bool last_o = has_o && (split || buffer || j + 1 == steps);     // the last use of its load
+                        const bool last_s = has_s && (split || buffer || next + 1 == steps);
                         // first what is there already, as a rule, then the weights: nothing else lies between
                         // them and the products
-                        if (has_s && buffer == 0) ok = wait_for(&sm.k_full[kr.stage], kr.phase, &sm.abort);
+                        if (has_s && (split || buffer == 0)) ok = wait_for(&sm.k_full[kr.stage], kr.phase, &sm.abort);
                         if (next == 0) ok = ok && wait_for(&sm.q_full[x], segs & 1, &sm.abort);
-                        if (has_o && buffer == 0) ok = ok && wait_for(&sm.v16_full[v16r.stage], v16r.phase, &sm.abort);
-                        const uint64_t vd = v_desc + v16r.stage * (kTile * D * 2 / 16) + buffer * (kStep * 128 / 16);
-                        const uint64_t kd = k_desc + kr.stage * (kTile * D / 16) + buffer * (kStep * D / 16);
+                        if (has_o && (split || buffer == 0)) ok = ok && wait_for(&sm.v16_full[v16r.stage], v16r.phase, &sm.abort);
+                        const uint64_t vd = v_desc + v16r.stage * (kTile * D * 2 / 16) + half * (kStep * 128 / 16);
+                        const uint64_t kd = k_desc + kr.stage * (kTile * D / 16) + half * (kStep * D / 16);
                         if (has_o) ok = ok && wait_for(&sm.p_full[x][buffer], (phases >> buffer) & 1, &sm.abort);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
