@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
         ++popped;
     }
     if (share == 0) check_sequences(a, lane);
+    if (lane == 0) report_abort(&sm.abort);
     // after a wait that gave up: the loads still under way
     for (; waited != issued; ++waited) mbar_wait_drain(&sm.full[warp][waited % kStages], (waited / kStages) & 1);
 }

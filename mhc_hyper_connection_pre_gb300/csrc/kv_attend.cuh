@@ -159,19 +159,21 @@ __device__ inline void check_sequences(const AttendArgs& a, int lane) {
     if (bad) atomicOr(&g_device_status, kIndexError);
 }
 
-// mbar_wait, with the polling kept to a few instructions: the kernels here
-// have many waits, and their loops have to fit the instruction cache.
+// mbar_wait for loops that have to fit the instruction cache: a few
+// instructions.  A wait that gives up only sets `abort`; report_abort tells the
+// host at the kernel's end.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
     const uint32_t at = smem_u32(bar);
 #pragma unroll 1
     for (int i = 0; i < kSpinLimit; ++i) {
         if (mbar_try_wait(at, parity)) return true;
         if (*abort) return false;
-        if (i > 256) __nanosleep(64);
     }
-    atomicOr(&g_device_status, kDeviceTimeout);
     *abort = 1;
     return false;
+}
+__device__ __forceinline__ void report_abort(volatile int* abort) {
+    if (*abort) atomicOr(&g_device_status, kDeviceTimeout);
 }
 
 // The barrier of the whole block; unlike __syncthreads, it may be met in

@@ -571,22 +571,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     const Meta& meta = sm.v_meta[vr.stage];
                     const uint32_t src = smem_u32(sm.v[vr.stage]), dst = smem_u32(sm.v16[v16r.stage]);
-                    const bool some = key + kTile > all_see;          // not every row sees every key of this step
                     const bool use = ((meta.valid >> (id / 16)) & 1) && key + id < keys;
                     const float ratio = use ? meta.scale[id / 16] * per : 0.0f;
+                    // 64 dims of a key are one 128-byte row, swizzled; the next 64 dims follow all keys
+                    auto put = [&](int c, const uint32_t (&h)[8]) {
+                        const uint32_t to_row = dst + (c / 4) * (kTile * 128) + id * 128;
+                        const int c16 = (2 * c) % 8;
+                        sts128(to_row + ((c16 ^ (id & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+                        sts128(to_row + (((c16 + 1) ^ (id & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
+                    };
+                    // a power of two, as mhc_kv_append writes them: exact, or one rounding in f16's subnormals
                     const bool exact = (__float_as_uint(ratio) & 0x7fffffu) == 0 && ratio >= 5.9604645e-8f;
-                    const uint32_t times = pack_f16x2(ratio, ratio);
+                    if (__all_sync(0xffffffffu, exact && key + kTile <= all_see)) {
+                        const uint32_t times = pack_f16x2(ratio, ratio);
 #pragma unroll 1
-                    for (int c0 = 0; c0 < D / 16; c0 += 4) {
-                        uint4 u[4];
+                        for (int c0 = 0; c0 < D / 16; c0 += 4) {
+                            uint4 u[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) u[i] = lds128(src + chunk_at<D>(id, c0 + i));
+                            for (int i = 0; i < 4; ++i) u[i] = lds128(src + chunk_at<D>(id, c0 + i));
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int c = c0 + i;
-                            uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, h[8];
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                                uint32_t h[8];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    h[2 * k] = mul_f16x2(cvt_lo(w[k]), times);
+                                    h[2 * k + 1] = mul_f16x2(cvt_hi(w[k]), times);
+                                }
+                                put(c0 + i, h);
+                            }
+                        }
+                    } else {                  // any scales, and keys that not every row sees
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            const uint4 u = lds128(src + chunk_at<D>(id, c));
+                            uint32_t w[4] = {u.x, u.y, u.z, u.w}, h[8];
                             if (!use) w[0] = w[1] = w[2] = w[3] = 0;
-                            if (some) {
+                            if (key + id >= all_see) {
                                 // NaN must reach only the rows that see this key, but 0 * NaN is
                                 // NaN: it is taken out here and put back as the rows go out
                                 uint32_t any = 0;
@@ -605,25 +626,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                             }
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                h[2 * k] = cvt_lo(w[k]);
-                                h[2 * k + 1] = cvt_hi(w[k]);
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t x = k % 2 ? cvt_hi(w[k / 2]) : cvt_lo(w[k / 2]);
+                                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x));
+                                h[k] = pack_f16x2(y.x * ratio, y.y * ratio);
                             }
-                            if (exact) {          // a power of two: one rounding at most, in f16's subnormals
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) h[k] = mul_f16x2(h[k], times);
-                            } else {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
-                                    h[k] = pack_f16x2(y.x * ratio, y.y * ratio);
-                                }
-                            }
-                            // 64 dims of a key are one 128-byte row, swizzled; the next 64 dims follow all keys
-                            const uint32_t to_row = dst + (c / 4) * (kTile * 128) + id * 128;
-                            const int c16 = (2 * c) % 8;
-                            sts128(to_row + ((c16 ^ (id & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
-                            sts128(to_row + (((c16 + 1) ^ (id & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
+                            put(c, h);
                         }
                     }
                     fence_proxy_async_smem();
@@ -794,6 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 13) tmem_dealloc(tmem, 512);
+    if (tid == 0) report_abort(&sm.abort);
 }
 
 template <int D>
