@@ -116,6 +116,9 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -218,6 +221,13 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t (&p)[1
     }
 }
 
+// The power of two, within 2^+-120, that brings a row's largest magnitude to [128, 256).
+__device__ __forceinline__ float power_up(float top) {
+    int e = 134 - (int)(__float_as_uint(top) >> 23);              // 7 - floor(log2(top))
+    e = e < -120 ? -120 : (e > 120 ? 120 : e);
+    return __uint_as_float((uint32_t)(127 + e) << 23);
+}
+
 // Steps of a tile for so many keys.  `split`: up to 128 rows, which both tiles
 // take, the first the even and the second the odd 64 keys of each load.
 __device__ __forceinline__ int steps_of(bool split, int keys) {
@@ -300,66 +310,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float f = 0.0f, m = -INFINITY, l = 0.0f;
                 int lim = 0;
                 if (steps > 0) {
-                    // this thread's query row as hi + lo: once over it for its largest
-                    // element, once more (from the cache) to split it, as the whole row
-                    // would not fit the registers
-                    const uint4* src = nullptr;
+                    // the warp's 32 query rows as hi + lo: D / 8 lanes to a row, so that the loads
+                    // are whole lines (a thread to a row took 7400 to 12,600 cycles at head_dim
+                    // 128, this takes 6000 to 7700)
+                    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kAhead = 4;
+                    const int sub = lane / kLanes, part8 = lane % kLanes;
+                    const int in_rows = rows - (mine - lane);     // of the warp's 32, those that there are
+                    int64_t off = 0;
                     if (mine < rows) {
                         int token, in_group;
                         row_of(seg, a.cut, mine, token, in_group);
                         lim = keys_of_row(seg, a.cut, mine);
-                        src = reinterpret_cast<const uint4*>(a.q + token * a.q_stride +
-                                                             (seg.head * a.cut.group + in_group) * D);
+                        off = token * a.q_stride + (seg.head * a.cut.group + in_group) * D;
                     }
-                    auto load = [&](int i) { return src ? __ldg(src + i) : make_uint4(0, 0, 0, 0); };
-                    float top = 0.0f;
-#pragma unroll 1
-                    for (int i = 0; i < D / 8; i += 8) {
-                        uint4 u[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) u[j] = load(i + j);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float y[8];
-                            unpack8(u[j], y);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(y[k]));
-                        }
-                    }
-                    int e = 134 - (int)(__float_as_uint(top) >> 23);  // 7 - floor(log2(top))
-                    e = e < -120 ? -120 : (e > 120 ? 120 : e);
-                    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-                    f = __uint_as_float((uint32_t)(127 - e) << 23) * a.scale_log2;
-                    if (top == INFINITY) l = __int_as_float(0x7fc00000);   // e4m3 has no infinity: such a row is NaN
+                    auto load = [&](int r) {
+                        const int64_t from = __shfl_sync(0xffffffffu, off, r & 31) + part8 * 8;
+                        return r < in_rows && r < 32 ? __ldg(reinterpret_cast<const uint4*>(a.q + from))
+                                                     : make_uint4(0, 0, 0, 0);
+                    };
                     const uint32_t hi_at = smem_u32(sm.q[x][0]), lo_at = smem_u32(sm.q[x][1]);
-                    uint4 u[2] = {load(0), load(1)};
+                    float my_top = 0.0f;
+                    uint4 u[kAhead];
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k) u[k] = load(k * kRows + sub);
 #pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint32_t hi[4], rest[4];
-                        const uint4 now[2] = {u[0], u[1]};
-                        if (c + 1 < D / 16) u[0] = load(2 * c + 2), u[1] = load(2 * c + 3);
+                    for (int r0 = 0; r0 < 32; r0 += kAhead * kRows) {
+                        uint4 now[kAhead];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            float y[8], z[8];
-                            unpack8(now[i], y);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) y[j] *= up;
-                            hi[2 * i] = e4m3x4(y, 0);
-                            hi[2 * i + 1] = e4m3x4(y, 4);
-#pragma unroll
-                            for (int j = 0; j < 8; j += 2) {
-                                const uint32_t w = hi[2 * i + j / 4];
-                                const uint32_t b = j % 4 ? cvt_hi(w) : cvt_lo(w);
-                                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&b));
-                                z[j] = y[j] - back.x;
-                                z[j + 1] = y[j + 1] - back.y;
-                            }
-                            rest[2 * i] = e4m3x4(z, 0);
-                            rest[2 * i + 1] = e4m3x4(z, 4);
+                        for (int k = 0; k < kAhead; ++k) {
+                            now[k] = u[k];
+                            u[k] = load(r0 + (kAhead + k) * kRows + sub);
                         }
-                        sts128(hi_at + chunk_at<D>(in_tile, c), make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                        sts128(lo_at + chunk_at<D>(in_tile, c), make_uint4(rest[0], rest[1], rest[2], rest[3]));
+#pragma unroll
+                        for (int k = 0; k < kAhead; ++k) {
+                            const int r = r0 + k * kRows + sub;
+                            float y[8], z[8], top = 0.0f;
+                            unpack8(now[k], y);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(y[i]));
+#pragma unroll
+                            for (int o = kLanes / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            const float up = power_up(top);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) y[i] *= up;
+                            const uint32_t hi[2] = {e4m3x4(y, 0), e4m3x4(y, 4)};
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) {
+                                const uint32_t b = i % 4 ? cvt_hi(hi[i / 4]) : cvt_lo(hi[i / 4]);
+                                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&b));
+                                z[i] = y[i] - back.x;
+                                z[i + 1] = y[i + 1] - back.y;
+                            }
+                            const uint32_t to = chunk_at<D>(in_tile - lane + r, part8 / 2) + (part8 & 1) * 8;
+                            sts64(hi_at + to, hi[0], hi[1]);
+                            sts64(lo_at + to, e4m3x4(z, 0), e4m3x4(z, 4));
+                            const float t = __shfl_sync(0xffffffffu, top, (lane % kRows) * kLanes);
+                            if (lane - lane % kRows == r - sub) my_top = t;
+                        }
                     }
+                    f = a.scale_log2 * __uint_as_float(0x7f000000u - __float_as_uint(power_up(my_top)));
+                    if (my_top == INFINITY) l = __int_as_float(0x7fc00000);   // e4m3 has no infinity: such a row is NaN
                     fence_proxy_async_smem();
                     if (unread) {             // the last segment's reads of O come before this one's products
                         ok = __all_sync(0xffffffffu, wait_for(&sm.half_read, (halves - 1) & 1, &sm.abort));
@@ -485,10 +495,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float unit = steps > 0 ? sm.ref[kept] * (1.0f / kVLift) : 0.0f;
                 const float by = whole ? (l == 0.0f ? 0.0f : unit * __frcp_rn(l)) : unit;
                 const bool nans = steps > 0 && sm.has_nan[kept];
+                own *= by;
+                other *= by;
+                // Rows go out by way of shared memory, 128 bytes of each of the warp's 32 at a time, so that
+                // the stores are whole lines.  The queries' place is free, and its rows are this warp's.
+                uint64_t to = 0;
                 if (mine < rows) {
+                    to = whole ? reinterpret_cast<uint64_t>(a.out + at * D) : reinterpret_cast<uint64_t>(part + mine * D);
                     if (whole && a.lse) a.lse[at] = lse_of(m, l);
                     if (!whole) *reinterpret_cast<float2*>(part + kPair * D + 2 * mine) = make_float2(m, l);
                 }
+                auto staged = [&](int r, int c) {             // 16-byte chunk c of row r of the warp
+                    const uint32_t row = D == 128 ? smem_u32(sm.q[x][0]) + (warp % 4) * 4096 + r * 128
+                                                  : smem_u32(sm.q[x][r / 16]) + (warp % 4) * 2048 + (r % 16) * 128;
+                    return row + ((c ^ (r & 7)) << 4);
+                };
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
@@ -497,6 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_ld();
                         tmem_regs_ready(o);
                     }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = steps > 0 ? __float_as_uint(__uint_as_float(o[i]) * own) : 0u;
                     if (join) {
                         uint32_t o1[32];
                         tmem_ld32(lanes + col_o<D>(1) + c * 32, o1);
@@ -504,29 +527,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_regs_ready(o1);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) * own + __uint_as_float(o1[i]) * other);
+                            o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), other, __uint_as_float(o[i])));
                     }
+                    if (nans) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float y = steps > 0 ? __uint_as_float(o[i]) * by : 0.0f;
-                        if (nans && sm.nan_key[kept][c * 32 + i] < lim) y = __int_as_float(0x7fc00000);
-                        o[i] = __float_as_uint(y);
+                        for (int i = 0; i < 32; ++i)
+                            if (sm.nan_key[kept][c * 32 + i] < lim) o[i] = 0x7fc00000u;
                     }
-                    if (mine >= rows) continue;
                     if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + c * 32);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             float y[8];
 #pragma unroll
                             for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(o[8 * i + k]);
-                            dst[i] = pack8(y);
+                            sts128(staged(lane, (c & 1) * 4 + i), pack8(y));
                         }
+                        if (!(c & 1)) continue;
                     } else {
-                        uint4* dst = reinterpret_cast<uint4*>(part + mine * D + c * 32);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        for (int i = 0; i < 8; ++i)
+                            sts128(staged(lane, i), make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
                     }
+                    __syncwarp();
+#pragma unroll 4
+                    for (int r = lane / 8; r < 32; r += 4) {
+                        const uint64_t row = __shfl_sync(0xffffffffu, to, r);
+                        const uint4 v = lds128(staged(r, lane % 8));
+                        if (row) *reinterpret_cast<uint4*>(row + lane % 8 * 16) = v;
+                    }
+                    __syncwarp();
+                    if (to) to += 128;
                 }
                 if (join) {
                     tc_fence_before();
