@@ -504,14 +504,21 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
 
 // Joins the tiles that borders between shares have cut.  A tile's parts are
 // slot 1 of the share that began it (its owner) and slot 0 of the shares after
-// it.  Each share has a warp for either slot (or gridDim.y of them), and a
-// tile's warps divide its rows.  What bounds it is the number of instructions
-// a row where there are few parts, and the loads' latency where there are many.
+// it.  Each share has a warp for either slot (or gridDim.y of them).  A tile's
+// warps divide its rows; from kMany parts on, a long sequence, the blocks whose
+// shares are all slot 0 of it do (there are kMany / 8 - 1 at least), and a
+// block's warps divide a row's parts.  What bounds it is the number of
+// instructions a row where there are few parts, so that they are loaded four at
+// a time, and the loads' latency where there are many: 16 at a time, two rounds
+// for the 228 parts of a whole GPU over eight heads.  Measured with blocks from
+// 16 parts on: one sequence of 1001 keys 14.3 us, 12.4 from 64 on.
 template <int D>
 __global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a) {
-    constexpr int kMany = 16, kAhead = 8, kDims = D / 32;
+    constexpr int kSome = 16, kMany = 64, kDims = D / 32;
+    __shared__ float sum_o[8][D];
+    __shared__ float2 sum_ml[8];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x % 32, share = blockIdx.x * 8 + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, share = blockIdx.x * 8 + warp;
     if (share >= a.shares) return;
     const int64_t next = (int64_t)(2 * (D + 2)) << a.cut.tile_log2;      // from a share's part to the next share's
     const PartDesc& d = a.desc[2 * share + blockIdx.z];
@@ -519,14 +526,11 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a) {
     if (parts == 0) return;
     const Segment seg = d.seg;
     const float* first = part_of(a, d.owner, 1, D);
-    const float* rest = part_of(a, d.owner + 1, 0, D) - next;     // part k, k > 0, at rest + k * next
     const float* sums = (D << a.cut.tile_log2) + first;              // maxima and sums of the first part
-    const int64_t to_rest = rest - first;
-    const int mine = share - d.owner + parts * blockIdx.y, step = parts * gridDim.y;
-
-    if (parts < kMany) {                      // a warp takes a row; four parts at a time, all their loads at once
+    const int64_t to_rest = part_of(a, d.owner + 1, 0, D) - next - first;   // part k, k > 0, is k * next further
+    if (parts < kSome) {                      // a warp takes a row; four parts at a time, all their loads at once
 #pragma unroll 1
-        for (int r = mine; r < seg.rows; r += step) {
+        for (int r = share - d.owner + parts * blockIdx.y; r < seg.rows; r += parts * gridDim.y) {
             float m = -INFINITY, l = 0.0f, o[kDims] = {};
 #pragma unroll 1
             for (int base = 0; base < parts; base += 4) {
@@ -577,80 +581,94 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a) {
         return;
     }
 
-    // a warp takes a quarter of a row: first the weights of up to 256 parts, kAhead to
-    // a lane, then their values, D / 16 lanes to a part
-    constexpr int lanes = D / 16, at_once = 32 / lanes;
-    const int sub = lane / lanes, x4 = lane % lanes;
+    int r = share - d.owner + parts * blockIdx.y, step = parts * gridDim.y, k0 = 0, k1 = parts;
+    if (parts >= kMany) {
+        const int begin = blockIdx.x * 8, end = d.owner + parts;     // the block's shares; the tile's
+        if (begin <= d.owner || begin + 8 > end) return;             // the same for the whole block
+        const int at = (d.owner + 8) / 8, blocks = end / 8 - at;     // of this tile
+        r = blockIdx.x - at + blocks * blockIdx.y;
+        step = blocks * gridDim.y;
+        const int per = (parts + 7) / 8;
+        k0 = warp * per;
+        k1 = k0 + per < parts ? k0 + per : parts;
+    }
+    constexpr int kAhead = 16;
 #pragma unroll 1
-    for (int item = mine; item < seg.rows * 4; item += step) {
-        const int r = item / 4, at = r * D + (item % 4 * lanes + x4) * 4;
-        float m = -INFINITY, l = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (; r < seg.rows; r += step) {
+        float m = -INFINITY, l = 0.0f, o[kDims] = {};
 #pragma unroll 1
-        for (int base = 0; base < parts; base += 32 * kAhead) {
-            // the maxima and sums of up to 32 * kAhead parts, kAhead to a lane, become their weights
-            float2 own[kAhead];
+        for (int base = k0; base < k1; base += kAhead) {             // the loads of kAhead parts at once
+            float y[kAhead][kDims];
+            float2 ml = make_float2(-INFINITY, 0.0f);
+            if (lane < kAhead && base + lane < k1)
+                ml = *reinterpret_cast<const float2*>(sums + (base + lane ? to_rest + (base + lane) * next : 0) + 2 * r);
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                const int k = base + 32 * i + lane;
-                own[i] = make_float2(-INFINITY, 0.0f);
-                if (k < parts)
-                    own[i] = *reinterpret_cast<const float2*>(sums + (k ? to_rest + k * next : 0) + 2 * r);
-            }
-            float now = own[0].x;
+                const int k = base + i;
 #pragma unroll
-            for (int i = 1; i < kAhead; ++i) now = fmaxf(now, own[i].x);
-#pragma unroll
-            for (int i = 16; i; i >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, i));
-            now = fmaxf(now, m);
-            const float zero = now == -INFINITY ? 0.0f : now, keep = ex2(m - zero);
-            float all = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                own[i].x = ex2(own[i].x - zero);
-                all = fmaf(own[i].x, own[i].y, all);
-            }
-#pragma unroll
-            for (int i = 16; i; i >>= 1) all += __shfl_xor_sync(0xffffffffu, all, i);
-            l = fmaf(l, keep, all);
-            m = now;
-            o.x *= keep; o.y *= keep; o.z *= keep; o.w *= keep;
-#pragma unroll
-            for (int q = 0; q < kAhead; ++q) {
-                const int from = base + 32 * q, n = parts - from < 32 ? parts - from : 32;
-#pragma unroll 1
-                for (int k0 = 0; k0 < n; k0 += 8 * at_once) {
-                    float4 y[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int k = k0 + i * at_once + sub;
-                        y[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (k < n)
-                            y[i] = *reinterpret_cast<const float4*>((from + k ? rest + (from + k) * next : first) + at);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float x = __shfl_sync(0xffffffffu, own[q].x, (k0 + i * at_once + sub) & 31);
-                        o.x = fmaf(x, y[i].x, o.x);
-                        o.y = fmaf(x, y[i].y, o.y);
-                        o.z = fmaf(x, y[i].z, o.z);
-                        o.w = fmaf(x, y[i].w, o.w);
+                for (int c = 0; c < kDims; ++c) y[i][c] = 0.0f;
+                if (k < k1) {
+                    const float* src = first + (k ? to_rest + k * next : 0) + r * D + lane * kDims;
+                    if constexpr (D == 128) {
+                        const float4 v = *reinterpret_cast<const float4*>(src);
+                        y[i][0] = v.x; y[i][1] = v.y; y[i][2] = v.z; y[i][3] = v.w;
+                    } else {
+                        const float2 v = *reinterpret_cast<const float2*>(src);
+                        y[i][0] = v.x; y[i][1] = v.y;
                     }
                 }
             }
+            float now = ml.x;
+#pragma unroll
+            for (int i = kAhead / 2; i; i >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, i));
+            now = fmaxf(__shfl_sync(0xffffffffu, now, 0), m);
+            const float zero = now == -INFINITY ? 0.0f : now, keep = ex2(m - zero), w = ex2(ml.x - zero);
+            float all = w * ml.y;
+#pragma unroll
+            for (int i = kAhead / 2; i; i >>= 1) all += __shfl_xor_sync(0xffffffffu, all, i);
+            l = fmaf(l, keep, __shfl_sync(0xffffffffu, all, 0));
+            m = now;
+#pragma unroll
+            for (int c = 0; c < kDims; ++c) o[c] *= keep;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const float x = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+                for (int c = 0; c < kDims; ++c) o[c] = fmaf(x, y[i][c], o[c]);
+            }
         }
-        for (int i = lanes; i < 32; i <<= 1) {                    // over the parts taken at a time
-            o.x += __shfl_xor_sync(0xffffffffu, o.x, i);
-            o.y += __shfl_xor_sync(0xffffffffu, o.y, i);
-            o.z += __shfl_xor_sync(0xffffffffu, o.z, i);
-            o.w += __shfl_xor_sync(0xffffffffu, o.w, i);
+        if (parts < kMany) {
+            const int64_t to = place_of(a, seg, r);
+            const float by = l == 0.0f ? 0.0f : __frcp_rn(l);
+            uint32_t* out = reinterpret_cast<uint32_t*>(a.out + to * D + lane * kDims);
+            out[0] = pack_bf16x2(o[0] * by, o[1] * by);
+            if constexpr (D == 128) out[1] = pack_bf16x2(o[2] * by, o[3] * by);
+            if (lane == 0 && a.lse) a.lse[to] = lse_of(m, l);
+            continue;
         }
-        if (sub) continue;
-        const int64_t to = place_of(a, seg, r);
-        const float y = l == 0.0f ? 0.0f : __frcp_rn(l);
-        *reinterpret_cast<uint2*>(a.out + to * D + (at - r * D)) =
-            make_uint2(pack_bf16x2(o.x * y, o.y * y), pack_bf16x2(o.z * y, o.w * y));
-        if (at == r * D && a.lse) a.lse[to] = lse_of(m, l);
+#pragma unroll
+        for (int c = 0; c < kDims; ++c) sum_o[warp][lane * kDims + c] = o[c];
+        if (lane == 0) sum_ml[warp] = make_float2(m, l);
+        __syncthreads();
+        if (threadIdx.x < D / 2) {                                   // two dims a thread
+            float top = -INFINITY, total = 0.0f, x = 0.0f, y = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) top = fmaxf(top, sum_ml[w].x);
+            const float zero = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                const float by = ex2(sum_ml[w].x - zero);
+                const float2 v = *reinterpret_cast<const float2*>(&sum_o[w][2 * threadIdx.x]);
+                total = fmaf(by, sum_ml[w].y, total);
+                x = fmaf(by, v.x, x);
+                y = fmaf(by, v.y, y);
+            }
+            const int64_t to = place_of(a, seg, r);
+            const float by = total == 0.0f ? 0.0f : __frcp_rn(total);
+            reinterpret_cast<uint32_t*>(a.out + to * D)[threadIdx.x] = pack_bf16x2(x * by, y * by);
+            if (threadIdx.x == 0 && a.lse) a.lse[to] = lse_of(top, total);
+        }
+        __syncthreads();
     }
 }
 
@@ -659,14 +677,11 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a) {
 // tile reads all their keys.  Measured (us; 8 key heads; 64 sequences of 4096
 // keys | 1 of 32768):
 //    rows   head_dim 128: 8, 16, 256               head_dim 64: 8, 16, 256
-//       8   106, 119, 217 | 30, 31, 40             65,  82, 181 | 30, 31, 35
-//      16     -, 122, 221 |  -, 33, 42              -,  85, 185 |  -, 34, 36
-//      32     -, 224, 227 |  -, 42, 42              -, 150, 188 |  -, 36, 36
-//      48     -, 325, 231 |  -, 56, 44              -, 213, 191 |  -, 42, 36
-int tile_rows(int group, int head_dim, int64_t B, int64_t T) {
-    const int64_t rows = T * group;
-    return rows > (head_dim == 64 ? 32 : 16) * B ? 256 : (rows > 8 * B ? 16 : 8);
-}
+//       8   106, 119, 169 | 30, 31, 37             64,  82, 126 | 30, 31, 27
+//      16     -, 122, 171 |  -, 33, 38              -,  85, 127 |  -, 34, 28
+//      24     -, 223, 173 |  -, 42, 38              -, 147, 128 |  -, 35, 28
+//      48     -, 323, 175 |  -, 56, 39              -, 211, 129 |  -, 41, 29
+int tile_rows(int group, int64_t B, int64_t T) { return T * group > 16 * B ? 256 : (T * group > 8 * B ? 16 : 8); }
 
 // Shares of the work: warps, or the tensor-memory kernel's blocks.
 int shares_of(int rows, int D, int num_sms) {
@@ -708,7 +723,7 @@ cudaError_t launch_kv_attend_tc(const AttendArgs& a, const uint8_t* k, const uin
                                 cudaStream_t stream);
 
 size_t kv_attend_workspace(int heads, int head_dim, int q_heads, int64_t B, int64_t T, int num_sms) {
-    const int rows = tile_rows(q_heads / heads, head_dim, B, T), shares = shares_of(rows, head_dim, num_sms);
+    const int rows = tile_rows(q_heads / heads, B, T), shares = shares_of(rows, head_dim, num_sms);
     return part_bytes(rows, head_dim, shares) + (size_t)shares * 2 * sizeof(PartDesc);
 }
 
@@ -717,7 +732,7 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
                              int q_heads, float softmax_scale, uint16_t* out, float* lse, void* workspace,
                              int num_sms, cudaStream_t stream) {
     AttendArgs a;
-    const int group = q_heads / heads, rows = tile_rows(group, head_dim, seqs.B, seqs.T);
+    const int group = q_heads / heads, rows = tile_rows(group, seqs.B, seqs.T);
     a.seqs = seqs;
     a.cut = rows == 256 ? make_cut(heads, group, 8, 7, 4) : make_cut(heads, group, rows == 8 ? 3 : 4, kUnitLog2, 3);
     a.shares = shares_of(rows, head_dim, num_sms);

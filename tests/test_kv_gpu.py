@@ -327,6 +327,15 @@ def test_attend_long_context():
     check_attend(got, *of)
 
 
+@pytest.mark.parametrize("case", [(64, 64, 1, 7, None, [40000]), (128, 32, 1, 17, None, [30001, 5]),
+                                  (64, 16, 1, 40, [7], [30000]), (128, 128, 4, 44, None, [20000]),
+                                  (64, 32, 2, 16, [2], [9000])])
+def test_attend_few_long_sequences(case):
+    """Tiles whose parts come from many shares of the work, in each kernel."""
+    got, of = _attend(case, 3)
+    check_attend(got, *of)
+
+
 def test_attend_many_sequences():
     lens = [(i * 37) % 200 for i in range(700)]
     got, of = _attend((64, 16, 1, 2, None, lens), 2)
