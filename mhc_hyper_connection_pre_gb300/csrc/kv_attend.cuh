@@ -83,7 +83,8 @@ __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
 // Finds sequence b for a plan.
 struct Lookup {
     const AttendArgs& a;
-    __device__ __forceinline__ SeqInfo operator()(int b) const { return info_of(span_of(a.seqs, b)); }
+    __device__ __forceinline__ int count() const { return a.seqs.B; }
+    __device__ __forceinline__ SeqInfo operator()(int b) const { return info_of(span_of(a.seqs, b < a.seqs.B ? b : a.seqs.B - 1)); }
 };
 
 __device__ __forceinline__ int64_t sum_upto(int64_t x, int lane) {

@@ -323,8 +323,9 @@ MHC_HD bool plan_next(Plan& p, const Look& look, const Cut& c, const Shares& sha
         if (!walk_next(p.w, p.info, c) && p.w.left > 0) {
             MHC_ROLLED
             do p.info = look(++p.b);
-            while (p.info.tokens == 0);
-            walk_enter(p.w, p.info, c, 0, p.w.left);
+            while (p.info.tokens == 0 && p.b + 1 < look.count());
+            if (p.info.tokens > 0) walk_enter(p.w, p.info, c, 0, p.w.left);
+            else p.w.left = 0;               // lengths that changed since they were counted
         }
         if (some) return true;
     }

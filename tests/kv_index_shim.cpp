@@ -9,6 +9,12 @@ static Seqs make(const int32_t* table, const int32_t* lens, const int32_t* cu, i
     return Seqs{table, lens, cu, width, B, T, log2, pages};
 }
 
+struct Look {
+    const Seqs& s;
+    int count() const { return s.B; }
+    SeqInfo operator()(int b) const { return info_of(span_of(s, b)); }
+};
+
 extern "C" {
 
 // The runs that an append writes: for each token t, what a thread group that
@@ -62,7 +68,7 @@ int kv_segments(const int32_t* table, const int32_t* lens, const int32_t* cu, in
     walk_enter(p.w, p.info, c, from - seen, left);
     int found = 0;
     Segment g;
-    while (plan_next(p, [&](int b) { return info_of(span_of(s, b)); }, c, shares, g)) {
+    while (plan_next(p, Look{s}, c, shares, g)) {
         if (found == most) return -1;
         const int32_t o[] = {g.b, g.token, g.rem, g.rows, g.head, g.key0, g.keys, g.parts, g.owner,
                              keys_of_row(g, c, 0), keys_of_row(g, c, g.rows - 1)};
