@@ -20,12 +20,23 @@
 //     (weights then reach 2^15, within f16), so that O, in tensor memory, is
 //     rescaled rarely; sums are fp32 and of the unrounded weights.
 //
+// Up to 128 rows are one tile; both of a block's tiles then take it, each half
+// of every load's keys, and their results are joined as the rows go out: 48 rows
+// of 64 sequences of 4096 keys, 8 heads: 231 -> 203 us (head_dim 128), 191 ->
+// 146 (64).
+//
 // What bounds it: 4 * 128 * 64 * head_dim operations for 64 keys and 128 rows on
 // the tensor cores against 128 * 64 exponentials and the conversion of V.  Each
 // tile's S has two buffers in tensor memory, so that the next step's products
 // run during the softmax of this one; the two tiles share loads and conversion.
 // With one buffer (128 keys a step) each softmax waited for P V and Q K^T of its
-// own tile: 1272 us for a chunk of 4096 tokens over 16384 keys, 40 heads.
+// own tile: 1272 us for a chunk of 4096 tokens over 16384 keys, 40 heads; now
+// 935.  A step of both tiles takes about 2000 cycles, of which the tensor cores
+// work 1280: their warps' instructions between the products (waits and
+// addresses, 10 cycles each among the softmax's) and the softmax's own chain
+// take the rest, about evenly.  A tile's queries, its first and last steps and
+// its rows' way out take 8000 (head_dim 64) to 14,000 cycles on top, which
+// bounds short prompts.
 //
 // Warps 0-3 and 4-7: softmax of the two tiles; 8-11: V to f16; 12: TMA loads;
 // 13 and 15: the tensor instructions of the two tiles; 14: planning.  The
@@ -843,6 +854,7 @@ cudaError_t launch(const AttendArgs& a, const uint8_t* k, const uint8_t* v, int 
         !encode_codes(&v_map, v, pages, 1 << a.seqs.page_log2, D, kTile))
         return cudaErrorInvalidValue;
     const int bytes = (int)sizeof(Smem<D>) + 1024;
+    static_assert(sizeof(Smem<D>) + 1024 <= 227 * 1024, "shared memory of a block");
     const cudaError_t e = cudaFuncSetAttribute(kv_attend_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     kv_attend_tc_kernel<D><<<blocks, kThreads, bytes, stream>>>(k_map, v_map, a);
