@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     uint32_t pushed = 0, popped = 0;          // segments
     int key = 0, keys = 0, head = 0;          // of the next load: its first key, its segment's last key + 1 and head
     const int32_t* row = nullptr;
-    int page[2];
+    int pages[2], ahead = 32;                 // pages of both halves of 32 loads, one in each lane; the next load's lane
 
     // On to the next load; false: there is none, or none before a segment of the queue is done.
     auto settle = [&] {
@@ -315,14 +315,23 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
             keys = s.keys;
             head = s.head;
             row = a.seqs.table + (int64_t)s.b * a.seqs.width;
+            ahead = 32;
         }
-        page[0] = __ldg(row + (key >> a.seqs.page_log2));             // used only when the load is issued
-        page[1] = key + 16 < keys ? __ldg(row + ((key + 16) >> a.seqs.page_log2)) : -1;
+        if (ahead == 32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int k = key + kSub * lane + 16 * i;
+                pages[i] = k < keys ? __ldg(row + (k >> a.seqs.page_log2)) : -1;
+            }
+            ahead = 0;
+        }
         return true;
     };
     bool more = settle();
     auto issue = [&] {
         const int st = issued % kStages;
+        const int page[2] = {__shfl_sync(0xffffffffu, pages[0], ahead), __shfl_sync(0xffffffffu, pages[1], ahead)};
+        ++ahead;
         const bool ok0 = page[0] >= 0 && page[0] < a.seqs.num_pages;
         const bool ok1 = page[1] >= 0 && page[1] < a.seqs.num_pages;
         if ((!ok0 || (key + 16 < keys && !ok1)) && lane == 0) atomicOr(&g_device_status, kIndexError);
