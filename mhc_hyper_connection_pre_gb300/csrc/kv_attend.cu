@@ -45,7 +45,7 @@ struct Shape {
 
 struct __align__(16) Meta {                   // of one load
     float scale[4];                           // k of keys 0-15, k of 16-31, v, v; read only where there is a page
-    int page[2];                              // -1: no such page
+    int block[2];                             // -1: no such page
     int pad[2];
 };
 
@@ -136,7 +136,7 @@ __device__ __forceinline__ void piece(bool full, uint32_t ks, uint32_t vs, const
 
     // logits in powers of two, masks, the running maximum
     const float k0 = meta.scale[0], k1 = meta.scale[1];
-    const bool has0 = meta.page[0] >= 0, has1 = meta.page[1] >= 0;
+    const bool has0 = meta.block[0] >= 0, has1 = meta.block[1] >= 0;
     float keep[NB][2];
     bool same = true;
 #pragma unroll
@@ -297,11 +297,13 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     Plan& plan = sm.plan[warp];
     find_share(a, share, plan, sm.shares[warp], lane);
 
-    uint32_t issued = 0, waited = 0;          // loads
+    int flight = 0, from = 0;                 // loads under way; the stage of the first
+    uint32_t phase = 0;                       // of that stage
     uint32_t pushed = 0, popped = 0;          // segments
     int key = 0, keys = 0, head = 0;          // of the next load: its first key, its segment's last key + 1 and head
-    const int32_t* row = nullptr;
-    int pages[2], ahead = 32;                 // pages of both halves of 32 loads, one in each lane; the next load's lane
+    int b = 0;
+    int blocks[2], ahead = 32;                // page and head of both halves of 32 loads, one in each lane (-1: no page);
+                                              // the next load's lane
 
     // On to the next load; false: there is none, or none before a segment of the queue is done.
     auto settle = [&] {
@@ -314,14 +316,18 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
             key = s.key0;
             keys = s.keys;
             head = s.head;
-            row = a.seqs.table + (int64_t)s.b * a.seqs.width;
+            b = s.b;
             ahead = 32;
         }
         if (ahead == 32) {
+            const int32_t* row = a.seqs.table + (int64_t)b * a.seqs.width;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int k = key + kSub * lane + 16 * i;
-                pages[i] = k < keys ? __ldg(row + (k >> a.seqs.page_log2)) : -1;
+                const int page = k < keys ? __ldg(row + (k >> a.seqs.page_log2)) : -1;
+                const bool ok = page >= 0 && page < a.seqs.num_pages;
+                if (k < keys && !ok) atomicOr(&g_device_status, kIndexError);
+                blocks[i] = ok ? page * a.cut.heads + head : -1;
             }
             ahead = 0;
         }
@@ -329,26 +335,21 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     };
     bool more = settle();
     auto issue = [&] {
-        const int st = issued % kStages;
-        const int page[2] = {__shfl_sync(0xffffffffu, pages[0], ahead), __shfl_sync(0xffffffffu, pages[1], ahead)};
+        const int st = from + flight < kStages ? from + flight : from + flight - kStages;
+        const int block0 = __shfl_sync(0xffffffffu, blocks[0], ahead), block1 = __shfl_sync(0xffffffffu, blocks[1], ahead);
+        const bool ok0 = block0 >= 0, ok1 = block1 >= 0;
         ++ahead;
-        const bool ok0 = page[0] >= 0 && page[0] < a.seqs.num_pages;
-        const bool ok1 = page[1] >= 0 && page[1] < a.seqs.num_pages;
-        if ((!ok0 || (key + 16 < keys && !ok1)) && lane == 0) atomicOr(&g_device_status, kIndexError);
         uint64_t* bar = &sm.full[warp][st];
         Meta& meta = sm.meta[warp][st];
         if (lane < 4) {
-            const int mb = lane & 1;
-            if (mb ? ok1 : ok0)
-                copy_async4(&meta.scale[lane],
-                            (lane < 2 ? a.k_scale : a.v_scale) + (int64_t)page[mb] * a.cut.heads + head);
+            const int block = lane & 1 ? block1 : block0;
+            if (block >= 0) copy_async4(&meta.scale[lane], (lane < 2 ? a.k_scale : a.v_scale) + block);
             arrive_after_copies(bar);
         }
         if (lane == 0) {
             uint8_t* dst = sm.ring[warp] + st * kStage;
-            meta.page[0] = ok0 ? page[0] : -1;
-            meta.page[1] = ok1 ? page[1] : -1;
-            const int block0 = page[0] * a.cut.heads + head, block1 = page[1] * a.cut.heads + head;
+            meta.block[0] = block0;
+            meta.block[1] = block1;
             if (a.seqs.page_log2 >= 5) {      // both halves lie in one page
                 const int slot = key & ((1 << a.seqs.page_log2) - 1);
                 mbar_arrive_expect_tx(bar, ok0 ? kStage : 0);
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
                 }
             }
         }
-        ++issued;
+        ++flight;
         key += kSub;
         more = settle();
     };
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     bool open = false;                        // a segment is under way
 #pragma unroll 1
     for (;;) {
-        while (issued - waited < kStages && !__any_sync(0xffffffffu, *(volatile int*)&sm.abort)) {
+        while (flight < kStages) {
             if (!more) more = settle();
             if (!more) break;
             issue();
@@ -447,14 +448,15 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
             all_see = keys_of_row(seg, a.cut, 0);           // keys that every row sees
         }
         if (at < seg.keys) {
-            const int st = waited % kStages;
-            const bool ok = waited != issued &&   // so after a wait that gave up
-                            __all_sync(0xffffffffu, wait_for(&sm.full[warp][st], (waited / kStages) & 1, &sm.abort));
+            const int st = from;
+            const bool ok = __all_sync(0xffffffffu, wait_for(&sm.full[warp][st], phase, &sm.abort));
             if (!ok) break;
-            ++waited;
+            --flight;
+            from = from + 1 == kStages ? 0 : from + 1;
+            phase ^= from == 0;
             const uint32_t base_addr = smem_u32(sm.ring[warp] + st * kStage);
             const Meta& meta = sm.meta[warp][st];
-            const bool full = at + kSub <= all_see && meta.page[0] >= 0 && meta.page[1] >= 0;
+            const bool full = at + kSub <= all_see && meta.block[0] >= 0 && meta.block[1] >= 0;
             piece<D, NB>(full, base_addr, base_addr + kStage / 2, meta, q, f, lim, at, seg.keys, lane, acc);
             __syncwarp();                     // every lane has read the stage
             at += kSub;
@@ -508,7 +510,11 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     if (share == 0) check_sequences(a, lane);
     if (lane == 0) report_abort(&sm.abort);
     // after a wait that gave up: the loads still under way
-    for (; waited != issued; ++waited) mbar_wait_drain(&sm.full[warp][waited % kStages], (waited / kStages) & 1);
+    for (; flight; --flight) {
+        mbar_wait_drain(&sm.full[warp][from], phase);
+        from = from + 1 == kStages ? 0 : from + 1;
+        phase ^= from == 0;
+    }
 }
 
 // Joins the tiles that borders between shares have cut.  A tile's parts are
