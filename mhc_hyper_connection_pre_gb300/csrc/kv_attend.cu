@@ -134,39 +134,29 @@ __device__ __forceinline__ void piece(bool full, uint32_t ks, uint32_t vs, const
         }
     }
 
-    // logits in powers of two, masks, the running maximum
+    // Logits in powers of two and masks.  The running maximum follows only when a
+    // logit is more than 2^5 above it (weights reach 2^15 then, within f16), so
+    // that the rows' maxima are seldom brought together across the lanes.
     const float k0 = meta.scale[0], k1 = meta.scale[1];
     const bool has0 = meta.block[0] >= 0, has1 = meta.block[1] >= 0;
-    float keep[NB][2];
-    bool same = true;
+    bool grow = false;
+    float top[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const float f0 = f[nb][e] * k0, f1 = f[nb][e] * k1;
             float x[4] = {s[0][nb][e] * f0, s[0][nb][e + 2] * f0, s[1][nb][e] * f1, s[1][nb][e + 2] * f1};
-            const int n = lim[nb][e] - key0 - g;      // of this thread's keys g, g + 8, .. the row sees those below n
-            const int n0 = has0 ? n : 0, n1 = has1 ? n : 0;
-            x[0] = n0 > 0 ? x[0] : -INFINITY;
-            x[1] = n0 > 8 ? x[1] : -INFINITY;
-            x[2] = n1 > 16 ? x[2] : -INFINITY;
-            x[3] = n1 > 24 ? x[3] : -INFINITY;
-            float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float old = acc.m[nb][e], now = fmaxf(old, top);
-            const float zero = now == -INFINITY ? 0.0f : now - kLift;
-            keep[nb][e] = old == now ? 1.0f : ex2(old - now);
-            same = same && old == now;
-            acc.m[nb][e] = now;
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = ex2(x[i] - zero);
-                sum += x[i];
+            if (!full) {
+                const int n = lim[nb][e] - key0 - g;      // of this thread's keys g, g + 8, .. the row sees those below n
+                const int n0 = has0 ? n : 0, n1 = has1 ? n : 0;
+                x[0] = n0 > 0 ? x[0] : -INFINITY;
+                x[1] = n0 > 8 ? x[1] : -INFINITY;
+                x[2] = n1 > 16 ? x[2] : -INFINITY;
+                x[3] = n1 > 24 ? x[3] : -INFINITY;
             }
-            acc.l[nb][e] = acc.l[nb][e] * keep[nb][e] + sum;
+            top[nb][e] = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+            grow = grow || top[nb][e] > acc.m[nb][e] + kGrow;
             s[0][nb][e] = x[0]; s[0][nb][e + 2] = x[1]; s[1][nb][e] = x[2]; s[1][nb][e + 2] = x[3];
         }
     }
@@ -174,24 +164,49 @@ __device__ __forceinline__ void piece(bool full, uint32_t ks, uint32_t vs, const
     // value scales relative to the largest so far
     const float v0 = has0 ? meta.scale[2] : 0.0f, v1 = has1 ? meta.scale[3] : 0.0f;   // no page: no weight either
     const float most = fmaxf(v0, v1);
-    float shrink = 1.0f;
-    if (most > acc.ref) {                     // the same for the whole warp
-        acc.inv = __frcp_rn(most);
-        shrink = acc.ref * acc.inv;
-        acc.ref = most;
-        same = false;
-    }
-    if (!__all_sync(0xffffffffu, same)) {
+    grow = __any_sync(0xffffffffu, grow);
+    if (grow || most > acc.ref) {             // the same for the whole warp
+        float shrink = 1.0f;
+        if (most > acc.ref) {
+            acc.inv = __frcp_rn(most);
+            shrink = acc.ref * acc.inv;
+            acc.ref = most;
+        }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const float x = keep[nb][0] * shrink, y = keep[nb][1] * shrink;
+            float keep[2];
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-                acc.o[j][nb][0] *= x;
-                acc.o[j][nb][1] *= y;
-                acc.o[j][nb][2] *= x;
-                acc.o[j][nb][3] *= y;
+            for (int e = 0; e < 2; ++e) {
+                float now = top[nb][e];
+                now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 4));
+                now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 8));
+                now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 16));
+                const float old = acc.m[nb][e];
+                now = fmaxf(old, now);
+                keep[e] = old == now ? 1.0f : ex2(old - now);
+                acc.m[nb][e] = now;
+                acc.l[nb][e] *= keep[e];
+                keep[e] *= shrink;
             }
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc.o[j][nb][i] *= keep[i & 1];
+        }
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float m = acc.m[nb][e], zero = m == -INFINITY ? 0.0f : m - kLift;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float& x = s[i / 2][nb][e + 2 * (i & 1)];
+                x = ex2(x - zero);
+                sum += x;
+            }
+            acc.l[nb][e] += sum;
         }
     }
     const float w0 = v0 * acc.inv, w1 = v1 * acc.inv;
@@ -381,8 +396,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     float f[NB][2];
     int lim[NB][2], all_see = 0;
     Acc<D, NB> acc;
-    Segment seg;
-    int at = 0;                               // the next piece's first key
+    int at = 0, end = 0;                      // the next piece's first key, the segment's last + 1
     bool open = false;                        // a segment is under way
 #pragma unroll 1
     for (;;) {
@@ -393,8 +407,9 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
         }
         if (!open) {
             if (popped == pushed) break;
-            seg = sm.queue[warp][popped % kQueue];
+            const Segment& seg = sm.queue[warp][popped % kQueue];
             at = seg.key0;
+            end = seg.keys;
             open = true;
             // queries: thread (g, t) holds row g's dims [t D/4, (t + 1) D/4) of each block of 8 rows
             acc.ref = acc.inv = 0.0f;
@@ -447,7 +462,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
             }
             all_see = keys_of_row(seg, a.cut, 0);           // keys that every row sees
         }
-        if (at < seg.keys) {
+        if (at < end) {
             const int st = from;
             const bool ok = __all_sync(0xffffffffu, wait_for(&sm.full[warp][st], phase, &sm.abort));
             if (!ok) break;
@@ -457,7 +472,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
             const uint32_t base_addr = smem_u32(sm.ring[warp] + st * kStage);
             const Meta& meta = sm.meta[warp][st];
             const bool full = at + kSub <= all_see && meta.block[0] >= 0 && meta.block[1] >= 0;
-            piece<D, NB>(full, base_addr, base_addr + kStage / 2, meta, q, f, lim, at, seg.keys, lane, acc);
+            piece<D, NB>(full, base_addr, base_addr + kStage / 2, meta, q, f, lim, at, end, lane, acc);
             __syncwarp();                     // every lane has read the stage
             at += kSub;
             continue;
@@ -465,6 +480,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
         open = false;
 
         // the rows go out, or to the workspace: thread (g, t) has D/8 dims of rows 2t and 2t + 1
+        const Segment& seg = sm.queue[warp][popped % kQueue];
         const bool whole = seg.parts == 1;
         const int slot = seg.owner == share ? 1 : 0;
         float* part = part_of(a, share, slot, D);
@@ -505,6 +521,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
                 }
             }
         }
+        __syncwarp();                         // every lane has read the segment
         ++popped;
     }
     if (share == 0) check_sequences(a, lane);

@@ -13,6 +13,7 @@ namespace mhc {
 namespace kv {
 
 constexpr float kLift = 10.0f;                // weights are 2^10 times the softmax's numerators
+constexpr float kGrow = 5.0f;                   // the maximum follows when it has grown by more (in powers of two)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // A part of a tile that a share has left in the workspace.

@@ -55,7 +55,6 @@ constexpr int kStep = 64;                     // keys of one step
 constexpr int kPair = 2 * kTile;              // rows of a block's work
 constexpr int kKStages = 3, kVStages = 2;
 constexpr int kMetas = 2 * kKStages;          // the softmax reads a load's key scales after its stage is free
-constexpr float kGrow = 5.0f;                 // the maximum follows when it has grown by more (in powers of two)
 constexpr float kVLift = 128.0f;              // V in f16 is 2^7 times code * scale / largest scale
 constexpr int kSegs = 4;                      // segments whose value scale and NaNs are kept: the converter runs two ahead
 
