@@ -12,8 +12,9 @@
 // sum for each row in fp32, in powers of two.  The weights are rounded to f16
 // for the second product (2^-11 of each, well below the output's own bf16
 // rounding) after a factor of 2^10 that keeps small weights out of f16's
-// subnormal range.  A page's value scale multiplies the weights, relative to
-// the largest scale met so far, so that they stay below 2^10.
+// subnormal range.  The maximum follows only when a logit is more than 2^5 above
+// it, so weights reach 2^15.  A page's value scale multiplies the weights,
+// relative to the largest scale met so far, so that they get no larger.
 //
 // What bounds it: the cache is read once, 2 * head_dim bytes a key and head
 // for 4 * head_dim * group operations, far below the matrix rate for groups up
@@ -544,8 +545,8 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
 // a time, and the loads' latency where there are many: 16 at a time, two rounds
 // for the 228 parts of a whole GPU over eight heads.  Measured with blocks from
 // 16 parts on: one sequence of 1001 keys 14.3 us, 12.4 from 64 on.
-template <int D>
-__global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a) {
+template <int D, int kAhead>
+__global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const AttendArgs a) {
     constexpr int kSome = 16, kMany = 64, kDims = D / 32;
     __shared__ float sum_o[8][D];
     __shared__ float2 sum_ml[8];
@@ -624,7 +625,6 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a) {
         k0 = warp * per;
         k1 = k0 + per < parts ? k0 + per : parts;
     }
-    constexpr int kAhead = 16;
 #pragma unroll 1
     for (; r < seg.rows; r += step) {
         float m = -INFINITY, l = 0.0f, o[kDims] = {};
@@ -709,10 +709,10 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const AttendArgs a) {
 // tile reads all their keys.  Measured (us; 8 key heads; 64 sequences of 4096
 // keys | 1 of 32768):
 //    rows   head_dim 128: 8, 16, 256               head_dim 64: 8, 16, 256
-//       8   106, 119, 169 | 30, 31, 37             64,  82, 126 | 30, 31, 27
-//      16     -, 122, 171 |  -, 33, 38              -,  85, 127 |  -, 34, 28
-//      24     -, 223, 173 |  -, 42, 38              -, 147, 128 |  -, 35, 28
-//      48     -, 323, 175 |  -, 56, 39              -, 211, 129 |  -, 41, 29
+//       8   104, 105, 170 | 25, 26, 36             65,  72, 127 | 21, 23, 27
+//      16     -, 108, 172 |  -, 27, 37              -,  75, 128 |  -, 23, 29
+//      24     -, 196, 173 |  -, 37, 37              -, 129, 128 |  -, 29, 29
+//      48     -, 284, 175 |  -, 52, 38              -, 184, 130 |  -, 35, 29
 int tile_rows(int group, int64_t B, int64_t T) { return T * group > 16 * B ? 256 : (T * group > 8 * B ? 16 : 8); }
 
 // Shares of the work: warps, or the tensor-memory kernel's blocks.
@@ -743,10 +743,13 @@ cudaError_t launch_join(const AttendArgs& a, int head_dim, cudaStream_t stream) 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3((a.shares + 7) / 8, a.cut.tile_log2 > 4 ? 64 : 1, 2);
+    const bool tall = a.cut.tile_log2 > 4;    // many rows: more of them at a time rather than more of a row's parts
+    auto kernel = tall ? (head_dim == 64 ? kv_join_kernel<64, 4> : kv_join_kernel<128, 4>)
+                       : (head_dim == 64 ? kv_join_kernel<64, 16> : kv_join_kernel<128, 16>);
+    cfg.gridDim = dim3((a.shares + 7) / 8, tall ? 64 : 1, 2);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = stream;
-    return cudaLaunchKernelEx(&cfg, head_dim == 64 ? kv_join_kernel<64> : kv_join_kernel<128>, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace
@@ -766,6 +769,10 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
     AttendArgs a;
     const int group = q_heads / heads, rows = tile_rows(group, seqs.B, seqs.T);
     a.seqs = seqs;
+    // What a tile costs beside its keys, in units.  Tensor-memory kernel: 2, 3, 4, 6, 8 took 660, 560, 515, 522, 532 us
+    // for a prompt of 8192 tokens (4 heads of 128, 8 rows each), and 4 was within 3% of the best for others.  Warps: 0, 1,
+    // 2, 3, 4, 6 took 39.5, 33.4, 31.6, 31.6, 31.7, 31.6 us for 256 sequences up to 300 keys, 700 short ones 47.5, 41.2,
+    // 39.7, 39.6, 40.0, 41.7.
     a.cut = rows == 256 ? make_cut(heads, group, 8, 7, 4) : make_cut(heads, group, rows == 8 ? 3 : 4, kUnitLog2, 3);
     a.shares = shares_of(rows, head_dim, num_sms);
     a.k_scale = k_scale;
