@@ -773,10 +773,11 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
     const int group = q_heads / heads, rows = tile_rows(group, seqs.B, seqs.T);
     a.seqs = seqs;
     // What a tile costs beside its keys, in units.  Tensor-memory kernel: 2, 3, 4, 6, 8 took 660, 560, 515, 522, 532 us
-    // for a prompt of 8192 tokens (4 heads of 128, 8 rows each), and 4 was within 3% of the best for others.  Warps: 0, 1,
-    // 2, 3, 4, 6 took 39.5, 33.4, 31.6, 31.6, 31.7, 31.6 us for 256 sequences up to 300 keys, 700 short ones 47.5, 41.2,
+    // for a prompt of 8192 tokens (4 heads of 128, 8 rows each), with heads of 64 458, 425, 430, 438, 446.  Warps: 0, 1, 2,
+    // 3, 4, 6 took 39.5, 33.4, 31.6, 31.6, 31.7, 31.6 us for 256 sequences up to 300 keys, 700 short ones 47.5, 41.2,
     // 39.7, 39.6, 40.0, 41.7.
-    a.cut = rows == 256 ? make_cut(heads, group, 8, 7, 4) : make_cut(heads, group, rows == 8 ? 3 : 4, kUnitLog2, 3);
+    const int extra = rows == 256 && head_dim == 128 ? 4 : 3;
+    a.cut = rows == 256 ? make_cut(heads, group, 8, 7, extra) : make_cut(heads, group, rows == 8 ? 3 : 4, kUnitLog2, extra);
     a.shares = shares_of(rows, head_dim, num_sms);
     a.k_scale = k_scale;
     a.v_scale = v_scale;
