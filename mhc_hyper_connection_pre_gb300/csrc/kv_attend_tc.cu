@@ -22,8 +22,8 @@
 //
 // Up to 128 rows are one tile; both of a block's tiles then take it, each half
 // of every load's keys, and their results are joined as the rows go out: 48 rows
-// of 64 sequences of 4096 keys, 8 heads: 231 -> 203 us (head_dim 128), 191 ->
-// 146 (64).
+// of 64 sequences of 4096 keys, 8 heads, took 231 us with one tile and 203 with
+// both (head_dim 128; now 172), 191 and 146 (64; now 130).
 //
 // What bounds it: 4 * 128 * 64 * head_dim operations for 64 keys and 128 rows on
 // the tensor cores against 128 * 64 exponentials and the conversion of V.  Each
@@ -31,7 +31,7 @@
 // run during the softmax of this one; the two tiles share loads and conversion.
 // With one buffer (128 keys a step) each softmax waited for P V and Q K^T of its
 // own tile: 1272 us for a chunk of 4096 tokens over 16384 keys, 40 heads; now
-// 935.  A step of both tiles takes about 2000 cycles, of which the tensor cores
+// 925.  A step of both tiles takes about 2000 cycles, of which the tensor cores
 // work 1280: their warps' instructions between the products (waits and
 // addresses, 10 cycles each among the softmax's) and the softmax's own chain
 // take the rest, about evenly.  A tile's queries, its first and last steps and

@@ -427,13 +427,14 @@ def test_other_stream_and_graph_replay():
     def step(s):
         mhc.kv_append(b, k, v, table, n, q=q, cos=cos, sin=sin, q_out=qo, stream=s)
         mhc.kv_attend(qo, b, table, n, out=out, lse=lse, workspace=ws, stream=s)
-    graph = SeamGraph(step, st)
-    for _ in range(3):
-        out.zero_()
-        torch.cuda.synchronize()
-        graph.replay()
-        torch.cuda.synchronize()
-        assert torch.equal(out, oa["out"]) and torch.equal(lse, oa["lse"])
+    for early in (False, True):
+        graph = SeamGraph(step, st, early_launch=early)
+        for _ in range(3):
+            out.zero_()
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, oa["out"]) and torch.equal(lse, oa["lse"])
 
 
 def test_workspace_contents_do_not_matter():
