@@ -97,22 +97,42 @@ __device__ __forceinline__ int64_t sum_upto(int64_t x, int lane) {
     return x;
 }
 
+// With more than 32 sequences a 32nd of them is this many.
+__device__ __forceinline__ int each_of(const AttendArgs& a) { return a.seqs.B <= 32 ? 1 : (a.seqs.B + 31) / 32; }
+
+// Units of the sequences of 32nd i, by one warp.
+__device__ inline void count_units(const AttendArgs& a, int i, int lane, int64_t& units) {
+    const Lookup look{a};
+    const int each = each_of(a), end = (i + 1) * each < a.seqs.B ? (i + 1) * each : a.seqs.B;
+    int64_t n = 0;
+#pragma unroll 1
+    for (int b = i * each + lane; b < end; b += 32) n += units_of_seq(look(b), a.cut);
+#pragma unroll 1
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    if (lane == 0) units = n;
+}
+
 // Finds a share of the line and starts its plan; the line's shares in `shares`.
 // One warp, which counts the units of all sequences: up to 32 of them a lane
-// each, beyond that a 32nd of them each and then the ones of the 32nd in which
-// the share begins.  No block-wide step, and each length is loaded once or
-// twice: what a decode step's latency consists of is loads that wait for one
-// another.
-__device__ inline void find_share(const AttendArgs& a, int share, Plan& p, Shares& shares, int lane) {
+// each, beyond that a 32nd of them each (or takes the counts of count_units) and
+// then the ones of the 32nd in which the share begins.  No block-wide step, and
+// each length is loaded once or twice: what a decode step's latency consists of
+// is loads that wait for one another.
+__device__ inline void find_share(const AttendArgs& a, int share, Plan& p, Shares& shares, int lane,
+                                  const int64_t* counted = nullptr) {
     const Lookup look{a};
-    const int each = a.seqs.B <= 32 ? 1 : (a.seqs.B + 31) / 32, first = lane * each;
+    const int each = each_of(a), first = lane * each;
     const int end = first + each < a.seqs.B ? first + each : a.seqs.B;
     SeqInfo info{0, 0, 0};
     int64_t mine = 0;
+    if (counted) {
+        mine = counted[lane];
+    } else {
 #pragma unroll 4
-    for (int i = first; i < end; ++i) {
-        info = look(i);
-        mine += units_of_seq(info, a.cut);
+        for (int i = first; i < end; ++i) {
+            info = look(i);
+            mine += units_of_seq(info, a.cut);
+        }
     }
     int64_t upto = sum_upto(mine, lane);
     const Shares sh = shares_of(__shfl_sync(0xffffffffu, upto, 31), a.shares);
@@ -152,12 +172,12 @@ __device__ inline void find_share(const AttendArgs& a, int share, Plan& p, Share
     __syncwarp();
 }
 
-// Reports lengths and offsets that had to be cut to what the arrays hold.  One
-// warp of the grid, when it has nothing else to do.
-__device__ inline void check_sequences(const AttendArgs& a, int lane) {
-    bool bad = lane == 0 && a.seqs.cu && (a.seqs.cu[0] != 0 || a.seqs.cu[a.seqs.B] != a.seqs.T);
+// Reports lengths and offsets that had to be cut to what the arrays hold: every
+// share's warp looks at some of them when it has nothing else to do.
+__device__ inline void check_sequences(const AttendArgs& a, int share, int lane) {
+    bool bad = share == 0 && lane == 0 && a.seqs.cu && (a.seqs.cu[0] != 0 || a.seqs.cu[a.seqs.B] != a.seqs.T);
 #pragma unroll 1
-    for (int i = lane; i < a.seqs.B; i += 32) bad = bad || span_of(a.seqs, i).bad;
+    for (int i = share * 32 + lane; i < a.seqs.B; i += a.shares * 32) bad = bad || span_of(a.seqs, i).bad;
     if (bad) atomicOr(&g_device_status, kIndexError);
 }
 

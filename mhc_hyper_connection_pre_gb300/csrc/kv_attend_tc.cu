@@ -6,12 +6,15 @@
 // key/value head) as two tiles of 128 and walks over the keys 64 at a time:
 // S = Q K^T and O += P V on the tensor cores (tcgen05), the softmax between
 // them with one thread a row.
-//   * K is used as it is stored: S is an e4m3 product.  A query row, divided
+//   * K is used as it is stored: S is an 8-bit product.  A query row, divided
 //     by a power of two so that its largest element lies in [128, 256), is the
-//     sum of two e4m3 numbers an element, hi + lo.  bf16's 8 bits split into
-//     4 + 4 without a remainder down to 2^-10 of the row's largest element;
-//     below that the remainder is at most 2^-19 of it.  S = hi K + lo K costs
-//     as much tensor time as one f16 product and needs no conversion of K.
+//     sum of two 8-bit numbers an element, hi in e4m3 and lo in e5m2.  What hi
+//     leaves of bf16's 8 bits is 0 to 8 of their last place, which e5m2's 3
+//     bits hold, down to 2^-14 of the row's largest element (hi's smallest
+//     normal number); below that what is lost is at most 2^-13, 2^-20 of the
+//     largest.  (lo in e4m3 lost up to 2^-17 of it, from 2^-10 on.)  S = hi K +
+//     lo K costs as much tensor time as one f16 product and needs no conversion
+//     of K.
 //   * V becomes f16 on the way (exactly, times its page's scale over the
 //     largest scale of the segment, times 2^7), because the weights need
 //     more than e4m3's 4 bits: they are f16, 2^10 times the softmax's
@@ -66,7 +69,7 @@ struct __align__(16) Meta {                   // of one load: the scales of each
 
 template <int D>
 struct __align__(1024) Smem {
-    uint8_t q[2][2][kTile * D];               // tile, hi / lo
+    uint8_t q[2][2][kTile * D];               // tile, hi / lo (e4m3, e5m2)
     uint8_t k[kKStages][kTile * D];
     uint8_t v[kVStages][kTile * D];           // as stored
     uint8_t v16[2][kTile * D * 2];            // f16: 64 dims of every key, then the next 64
@@ -109,8 +112,8 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         : "memory");
 }
 
-// e4m3 x e4m3, both from shared memory; f16 x f16 with A in tensor memory.
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// 8-bit numbers, both from shared memory; f16 x f16 with A in tensor memory.
+__device__ __forceinline__ void mma_8bit(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
@@ -125,6 +128,11 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint32_t e5m2x4(const float (&x)[8], int at) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[at], x[at + 1]), __NV_SATFINITE, __NV_E5M2);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[at + 2], x[at + 3]), __NV_SATFINITE, __NV_E5M2);
+    return lo | (hi << 16);
 }
 __device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y) {
     asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
@@ -373,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             const uint32_t to = chunk_at<D>(in_tile - lane + r, part8 / 2) + (part8 & 1) * 8;
                             sts64(hi_at + to, hi[0], hi[1]);
-                            sts64(lo_at + to, e4m3x4(z, 0), e4m3x4(z, 4));
+                            sts64(lo_at + to, e5m2x4(z, 0), e5m2x4(z, 4));
                             const float t = __shfl_sync(0xffffffffu, top, (lane % kRows) * kLanes);
                             if (lane - lane % kRows == r - sub) my_top = t;
                         }
@@ -794,7 +802,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                                     for (int i = 0; i < D / 32; ++i)
-                                        mma_e4m3(s_col + buffer * kStep, q_desc[h] + 2 * i, kd + 2 * i, kIdescS, h + i > 0);
+                                        mma_8bit(s_col + buffer * kStep, q_desc[h] + 2 * i, kd + 2 * i,
+                                                 kIdescS | (uint32_t)h << 7, h + i > 0);      // A: e4m3, e5m2
                                 mma_commit(&sm.s_full[x][buffer]);
                             }
                             if (last_o) mma_commit(&sm.v16_empty[v16r.stage]);
@@ -821,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 },
                 others);
-            if (blockIdx.x == 0) check_sequences(a, lane);
+            check_sequences(a, blockIdx.x, lane);
         }
     }
 

@@ -342,6 +342,27 @@ def test_attend_many_sequences():
     check_attend(got, *of)
 
 
+@pytest.mark.parametrize("B", [33, 257, 1500])
+@pytest.mark.parametrize("Hq", [2, 16, 48])
+def test_attend_many_short_sequences(B, Hq):
+    """More sequences than a warp has lanes, counted by a warp and by a block; some empty."""
+    lens = [(i * 29) % 40 for i in range(B)]
+    got, of = _attend((64, 16, 1, Hq, None, lens), 5)
+    check_attend(got, *of)
+
+
+def test_attend_bad_length_among_many():
+    """The last of many sequences is looked at as well."""
+    lens = [3] * 900
+    rows, pages = _tables(lens, 16, 6)
+    cache = _random_cache(pages, 1, 16, 64, 6)
+    q = torch.randn(900, 2, 64, device="cuda").bfloat16()
+    mhc.kv_attend(q, cache, _i32(rows), _i32(lens[:-1] + [17]))
+    assert mhc.device_status() == INDEX_ERROR
+    mhc.kv_attend(q.repeat(1, 20, 1), cache, _i32(rows), _i32(lens[:-1] + [-1]))
+    assert mhc.device_status() == INDEX_ERROR
+
+
 def test_attend_and_append_far_pages():
     """A cache whose last pages start beyond 2^32 bytes."""
     D, P, H = 128, 128, 8
