@@ -33,7 +33,6 @@ namespace kv {
 namespace {
 
 constexpr int kSub = 32;                      // keys of one load of one warp
-constexpr int kTogether = 256;
 constexpr int kQueue = 8;                     // segments that a warp's loads may be ahead of its products
 constexpr int kUnitLog2 = 5;                  // units of 32 keys, one load
 
@@ -313,8 +312,6 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     const int share = warp * gridDim.x + blockIdx.x;
     if (lane < 2) a.desc[2 * share + lane].parts = 0;
     Plan& plan = sm.plan[warp];
-    // Many sequences: counted by all warps together (1024 sequences up to 100 keys, 1 head: 21 us, each warp by itself 27;
-    // 200: 17.4 and 17.1, 300: 17.3 and 19.0).
     const bool together = a.seqs.B > kTogether;
     if (together) {
 #pragma unroll 1

@@ -76,6 +76,7 @@ struct __align__(1024) Smem {
     Segment segs[kSegments];
     Plan plan;
     Shares shares;
+    int64_t counted[32];
     int count;                                // of segs
     Meta k_meta[kMetas];
     Meta v_meta[kVStages];
@@ -281,6 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 13) tmem_alloc(&sm.tmem, 512);
     if (tid < 2) a.desc[2 * blockIdx.x + tid].parts = 0;
+    const bool together = a.seqs.B > kTogether;
+    if (together) {
+#pragma unroll 1
+        for (int i = warp; i < 32; i += kThreads / 32) count_units(a, i, lane, sm.counted[i]);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -819,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             });
         } else {
             // ------------------------------------------------------ planning
-            find_share(a, blockIdx.x, sm.plan, sm.shares, lane);
+            find_share(a, blockIdx.x, sm.plan, sm.shares, lane, together ? sm.counted : nullptr);
             each_segments(
                 [&] {
                     if (lane == 0) {

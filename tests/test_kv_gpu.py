@@ -351,6 +351,14 @@ def test_attend_many_short_sequences(B, Hq):
     check_attend(got, *of)
 
 
+def test_attend_many_short_drafts():
+    """More than 256 sequences in the tensor-memory kernel, ragged, some empty."""
+    counts = [(i * 7) % 5 for i in range(400)]
+    lens = [(i * 29) % 40 if n else 0 for i, n in enumerate(counts)]
+    got, of = _attend((128, 16, 1, 12, counts, lens), 8)
+    check_attend(got, *of)
+
+
 def test_attend_bad_length_among_many():
     """The last of many sequences is looked at as well."""
     lens = [3] * 900
