@@ -712,15 +712,18 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
 }
 
 // Rows of a tile: 8 or 16 for the warps of this file, 256 for the
-// tensor-memory kernel.  On average B sequences have T * group / B rows, and a
-// tile reads all their keys.  Measured (us; 8 key heads; 64 sequences of 4096
-// keys | 1 of 32768):
-//    rows   head_dim 128: 8, 16, 256               head_dim 64: 8, 16, 256
-//       8   104, 105, 170 | 25, 26, 36             65,  72, 127 | 21, 23, 27
-//      16     -, 108, 172 |  -, 27, 37              -,  75, 128 |  -, 23, 29
-//      24     -, 196, 173 |  -, 37, 37              -, 129, 128 |  -, 29, 29
-//      48     -, 284, 175 |  -, 52, 38              -, 184, 130 |  -, 35, 29
-int tile_rows(int group, int64_t B, int64_t T) { return T * group > 16 * B ? 256 : (T * group > 8 * B ? 16 : 8); }
+// tensor-memory kernel, whose tiles cost more beside their keys.  On average B
+// sequences have T * group / B rows, and a tile reads all their keys.  Measured
+// (us; 8 key heads; 256 sequences of up to 300 keys | 64 of up to 2000 | 64 of
+// 4096 | 1 of 32768):
+//    rows   head_dim 128: 16, 256                           head_dim 64: 16, 256
+//      16     -    |    -    | 108, 172 | 27, 37               -   |    -   |  75, 128 | 23, 29
+//      24  67, 124 | 59, 73  | 196, 173 | 37, 37            41, 90 | 42, 56 | 129, 128 | 29, 29
+//      32  75, 126 | 72, 79  | 196, 174 | 38, 37            46, 90 | 48, 58 | 130, 129 | 29, 29
+//      44  93, 125 | 85, 78  |                              56, 93 | 58, 56 |
+//      48     -    |    -    | 284, 175 | 52, 38               -   |    -   | 184, 130 | 35, 29
+// Of the tiles of 8 and 16: up to 8 rows 104, 105 | 65, 72 for 64 sequences of 4096.
+int tile_rows(int group, int64_t B, int64_t T) { return T * group > 32 * B ? 256 : (T * group > 8 * B ? 16 : 8); }
 
 // Shares of the work: warps, or the tensor-memory kernel's blocks.
 int shares_of(int rows, int D, int num_sms) {

@@ -34,7 +34,7 @@
 // run during the softmax of this one; the two tiles share loads and conversion.
 // With one buffer (128 keys a step) each softmax waited for P V and Q K^T of its
 // own tile: 1272 us for a chunk of 4096 tokens over 16384 keys, 40 heads; now
-// 925.  A step of both tiles takes about 2000 cycles, of which the tensor cores
+// 930.  A step of both tiles takes about 2000 cycles, of which the tensor cores
 // work 1280: their warps' instructions between the products (waits and
 // addresses, 10 cycles each among the softmax's) and the softmax's own chain
 // take the rest, about evenly.  A tile's queries, its first and last steps and

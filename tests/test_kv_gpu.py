@@ -237,6 +237,8 @@ ATTENDS = [
     (128, 32, 1, 17, None, [1000, 30, 0]),
     (128, 16, 2, 64, [4, 3], [5000, 130]),                   # 128 and 129 rows, long
     (64, 64, 1, 43, [3, 3], [3001, 64]),
+    (128, 32, 1, 33, None, [1000, 30, 0]),                   # one row more than the one-token kernel takes
+    (128, 64, 2, 64, None, [700, 64]),
 ]
 
 
@@ -328,7 +330,8 @@ def test_attend_long_context():
 
 
 @pytest.mark.parametrize("case", [(64, 64, 1, 7, None, [40000]), (128, 32, 1, 17, None, [30001, 5]),
-                                  (64, 16, 1, 40, [7], [30000]), (128, 128, 4, 44, None, [20000]),
+                                  (64, 16, 1, 40, [7], [30000]), (128, 128, 4, 44, None, [20000]), (128, 32, 1, 34, None, [30001, 5]),
+                                 
                                   (64, 32, 2, 16, [2], [9000])])
 def test_attend_few_long_sequences(case):
     """Tiles whose parts come from many shares of the work, in each kernel."""
