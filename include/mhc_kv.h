@@ -54,8 +54,12 @@ typedef struct mhc_kv_cache {
  * Bad indices.  A page number outside [0, num_pages), a length above
  * table_width * page_tokens or below zero, cu_q entries out of order or
  * range, and a position without a row in the rotation's tables touch no
- * memory: the tokens concerned are not written, or not attended to, and
- * mhc_device_status returns MHC_ERR_INDEX once.
+ * memory, and mhc_device_status returns MHC_ERR_INDEX once.
+ *   mhc_kv_append does not write the tokens concerned: those of the page or of
+ *     the positions; with a bad length or offset all of the sequence's new
+ *     tokens, which then have no place.
+ *   mhc_kv_attend does not attend to the keys of a bad page, and takes a bad
+ *     length as the nearest one that the table can hold.
  */
 
 /*

@@ -163,8 +163,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) raw[i] = fetch(h + i * kHeads);      // these loads do not wait for the position
         const int b = seq_of(a.seqs, t, lane);
-        const Span sp = span_of(a.seqs, b);
-        const int pos = t >= sp.begin && t < sp.end ? sp.before + (t - sp.begin) : -1;
+        const int pos = pos_of(span_of(a.seqs, b), t);
         const bool turned = at.turned && pos >= 0 && pos < a.rope_rows;       // beyond: reported by the append part
         Turn turn;
         if (turned) load_turn(a, pos, lane % kLanes, turn);

@@ -67,15 +67,29 @@ MHC_HD int page_of(const Seqs& s, int b, int pos) {
     return p >= 0 && p < s.num_pages ? p : -1;
 }
 
-// The new tokens of one page, from token t on: slot..slot + n - 1 of that
-// page.  n == 0: token t has no place (next: the first that may have one).
+// Position of new token t, or -1: not one of the sequence's, or one without a
+// place.  A span that had to be clamped has no places: its positions would be
+// those of other tokens.
+MHC_HD int pos_of(const Span& sp, int t) {
+    if (sp.bad || t < sp.begin || t >= sp.end) return -1;
+    const int pos = sp.before + (t - sp.begin);
+    return pos < 0 ? -1 : pos;
+}
+
+// The new tokens of one page, from the sequence's token t on: slot..slot + n - 1
+// of that page.  n == 0: token t has no place (next: the first that may have one).
 struct Run {
     int pos, slot, n, next;
 };
 
 MHC_HD Run run_at(const Seqs& s, const Span& sp, int t) {
     Run r;
-    r.pos = sp.before + (t - sp.begin);
+    r.pos = pos_of(sp, t);
+    if (sp.bad) {
+        r.slot = r.n = 0;
+        r.next = sp.end;
+        return r;
+    }
     if (r.pos < 0) {
         const int first = sp.begin - sp.before;   // the token at position 0
         r.n = 0;

@@ -42,6 +42,13 @@ void kv_runs(const int32_t* table, const int32_t* lens, const int32_t* cu, int w
     }
 }
 
+// The position that each token's query is rotated by, -1: none.
+void kv_positions(const int32_t* table, const int32_t* lens, const int32_t* cu, int width, int B, int T, int P, int pages,
+                  const int32_t* seq, int32_t* out) {
+    const Seqs s = make(table, lens, cu, width, B, T, P, pages);
+    for (int t = 0; t < T; ++t) out[t] = pos_of(span_of(s, seq[t]), t);
+}
+
 // The segments of share `share` of `n`: out[i] = {sequence, first token, query
 // head of its first row, rows, head, first key, last key + 1, shares of the
 // tile, the first of them, keys that the first and the last row see}.  Returns

@@ -314,3 +314,22 @@ def test_segments_stay_inside_whatever_the_arrays_hold(shim, seed):
         for b, t, rem, n, h, k0, k1, parts, owner, see0, see1 in c:
             assert 0 <= b < B and 0 <= h < heads and 0 <= t and 1 <= n <= rows and t + (rem + n - 1) // group < T
             assert 0 <= k0 and k1 <= width * 16 and see1 <= width * 16 and 1 <= parts <= 5 and 0 <= owner < 5
+
+
+@pytest.mark.parametrize("length,new", [(49, 1), (60, 20), (49, 48), (2147483647, 3), (-1, 1), (-2147483648, 20)])
+def test_a_bad_length_has_no_places(shim, length, new):
+    """Of a sequence longer than its table, or shorter than empty, nothing is
+    written and no query is rotated; its neighbours have their places."""
+    P, width, B, lens = 16, 3, 3, [20, length, 48]
+    cu = [0, 5, 5 + new, 9 + new]
+    T = cu[-1]
+    seq, out, pos = _seq_of(cu, T, B), np.zeros((T, 7), dtype=np.int32), np.zeros(T, dtype=np.int32)
+    table, lens_a, cu_a = _i32([[10 * b + i for i in range(width)] for b in range(B)]), _i32(lens), _i32(cu)
+    shim.kv_runs(_ptr(table), _ptr(lens_a), _ptr(cu_a), width, B, T, P, 40, _ptr(seq), _ptr(out))
+    shim.kv_positions(_ptr(table), _ptr(lens_a), _ptr(cu_a), width, B, T, P, 40, _ptr(seq), _ptr(pos))
+    for t in range(T):
+        starts, _, _, n, nxt, _, bad = out[t]
+        assert t < nxt <= cu[seq[t] + 1] and bool(bad) == (seq[t] == 1)
+        assert (pos[t] == -1 and not starts and n == 0) if bad else pos[t] == lens[seq[t]] - cu[seq[t] + 1] + t
+    assert [bool(out[t][0]) for t in range(5)] == [True, True, False, False, False]       # positions 15 | 16 .. 19
+    assert out[5 + new][0]

@@ -567,3 +567,27 @@ def test_example_prompt_then_tokens():
     assert (stepped - at_once).norm() <= 2 * 2.0 ** -4 * at_once.norm()
     for i in range(4):                                   # and no step is another's
         assert (stepped[:, i] - at_once[:, i]).norm() <= 2 * 2.0 ** -4 * at_once[:, i].norm()
+
+
+# ------------------------------------------------------- bad device data ---
+
+@pytest.mark.parametrize("counts", [None, [20, 7, 1]])
+@pytest.mark.parametrize("length", [49, 60, 2147483647, -1, -2147483648])
+def test_append_past_the_table_writes_nothing(length, counts):
+    """A sequence longer than its table, or shorter than empty: its tokens
+    are left out, as nothing says where they belong, so its pages keep their
+    bytes and its queries are copied; the other sequences are appended."""
+    D, P, H, Hq, lens = 64, 16, 2, 4, [48, 30, 5]
+    rows, pages = _tables(lens, P, 13)
+    cu = _cu(counts or [1, 1, 1])
+    q, k, v, cos, sin = _append_inputs(cu[-1], H, Hq, D, D, True, 13, 64)
+    got, expect = _random_cache(pages, H, P, D, 13), _random_cache(pages, H, P, D, 13)
+    n, own = cu[1], lambda t: t[cu[1]:]
+    q_out = mhc.kv_append(got, k, v, _i32(rows), _i32([length, 30, 5]), None if counts is None else _i32(cu), q=q,
+                          cos=cos, sin=sin)
+    assert mhc.device_status() == INDEX_ERROR
+    q_own = mhc.kv_append(expect, own(k), own(v), _i32(rows[1:]), _i32([30, 5]), _i32([c - n for c in cu[1:]]),
+                          q=own(q), cos=cos, sin=sin)
+    for x in got:
+        assert torch.equal(got[x].view(torch.uint8), expect[x].view(torch.uint8)), x
+    assert torch.equal(q_out[:n], q[:n]) and torch.equal(q_out[n:], q_own)
