@@ -197,6 +197,9 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
     const int t1 = (int)(next < a.seqs.T ? next : a.seqs.T);
     const int r0 = id / kLanes;
     const uint16_t* src = a.x[kv] + head * D;
+    // the other offsets are looked at by the tokens that they are those of
+    if (item == 0 && id == 0 && a.seqs.cu && (a.seqs.cu[0] != 0 || a.seqs.cu[a.seqs.B] != a.seqs.T))
+        atomicOr(&g_append_status, kIndexError);
 
 #pragma unroll 1
     for (int t = win * a.window; t < t1;) {

@@ -591,3 +591,12 @@ def test_append_past_the_table_writes_nothing(length, counts):
     for x in got:
         assert torch.equal(got[x].view(torch.uint8), expect[x].view(torch.uint8)), x
     assert torch.equal(q_out[:n], q[:n]) and torch.equal(q_out[n:], q_own)
+
+
+@pytest.mark.parametrize("cu", [[0, 2, 4, 5], [0, 2, 4, 3], [1, 2, 4, 4], [-1, 2, 4, 4]])
+def test_append_reports_offsets_that_miss_the_tokens(cu):
+    """Also where the offset is that of a sequence without any of the call's tokens."""
+    rows, pages = _tables([10, 11, 12], 16, 16)
+    x = torch.ones(4, 1, 64, device="cuda").bfloat16()
+    mhc.kv_append(mhc.kv_cache(pages, 1, 16, 64), x, x, _i32(rows), _i32([10, 11, 12]), _i32(cu))
+    assert mhc.device_status() == INDEX_ERROR
