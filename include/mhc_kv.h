@@ -59,7 +59,8 @@ typedef struct mhc_kv_cache {
  *     the positions; with a bad length or offset all of the sequence's new
  *     tokens, which then have no place.
  *   mhc_kv_attend does not attend to the keys of a bad page, and takes a bad
- *     length as the nearest one that the table can hold.
+ *     length as the nearest one that the table can hold; with a bad offset it
+ *     does not write the rows of the sequence's tokens.
  */
 
 /*

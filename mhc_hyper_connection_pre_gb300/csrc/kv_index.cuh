@@ -47,6 +47,7 @@ MHC_HD Span span_of(const Seqs& s, int b) {
         begin = clampi(c0, 0, s.T);
         end = clampi(c1, begin, s.T);
         r.bad = begin != c0 || end != c1;
+        if (r.bad) end = begin;                   // cut short, its tokens would get the positions of others
     } else {
         begin = b;
         end = b + 1;

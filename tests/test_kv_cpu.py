@@ -333,3 +333,15 @@ def test_a_bad_length_has_no_places(shim, length, new):
         assert (pos[t] == -1 and not starts and n == 0) if bad else pos[t] == lens[seq[t]] - cu[seq[t] + 1] + t
     assert [bool(out[t][0]) for t in range(5)] == [True, True, False, False, False]       # positions 15 | 16 .. 19
     assert out[5 + new][0]
+
+
+@pytest.mark.parametrize("cu,good", [([0, 2, 9, 9], [0]), ([-3, 2, 4, 4], [1]), ([0, 2, 4, 5], [0, 1]), ([0, 3, 1, 4], [0, 2])])
+def test_bad_offsets_leave_their_sequence_out(shim, cu, good):
+    T, B, width, heads, group = 4, 3, 3, 2, 5
+    lens, cu_a = _i32([40, 45, 20]), _i32(cu)
+    got, _ = _segments(shim, lens, cu_a, T, B, width, heads, group, 8, 7)
+    rows = {(b, h): 0 for b in good for h in range(heads)}
+    for b, t, rem, n, h, k0, k1, parts, owner, see0, see1 in (s for c in got for s in c):
+        assert b in good and cu[b] <= t and see1 <= lens[b]
+        rows[b, h] += n if k0 == 0 else 0
+    assert all(n == (cu[b + 1] - cu[b]) * group for (b, _), n in rows.items())

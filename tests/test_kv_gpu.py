@@ -600,3 +600,33 @@ def test_append_reports_offsets_that_miss_the_tokens(cu):
     x = torch.ones(4, 1, 64, device="cuda").bfloat16()
     mhc.kv_append(mhc.kv_cache(pages, 1, 16, 64), x, x, _i32(rows), _i32([10, 11, 12]), _i32(cu))
     assert mhc.device_status() == INDEX_ERROR
+
+
+@pytest.mark.parametrize("cu,good", [([0, 2, 9, 9], (0, 0, 2)), ([-3, 2, 4, 4], (1, 2, 4)),
+                                     ([0, 2, 4, 5], (0, 0, 2))])
+@pytest.mark.parametrize("Hq", [2, 80])
+def test_offsets_out_of_range_leave_their_sequences_out(cu, good, Hq):
+    """Offsets beyond the tokens or below zero do not say which positions a
+    sequence's tokens have: they are not written to the cache and
+    not attended to; a sequence with good offsets is."""
+    D, P, H, T, lens = 128, 16, 2, 4, [40, 45, 20]
+    rows, pages = _tables(lens, P, 14)
+    q, k, v, cos, sin = _append_inputs(T, H, Hq, D, D, True, 14, 64)
+    got, expect = _random_cache(pages, H, P, D, 14), _random_cache(pages, H, P, D, 14)
+    b, begin, end = good
+    at = slice(begin, end)
+    q_out = mhc.kv_append(got, k, v, _i32(rows), _i32(lens), _i32(cu), q=q, cos=cos, sin=sin)
+    assert mhc.device_status() == INDEX_ERROR
+    q_good = mhc.kv_append(expect, k[at], v[at], _i32([rows[b]]), _i32([lens[b]]), _i32([0, end - begin]), q=q[at],
+                           cos=cos, sin=sin)
+    whole = {i for c, d in zip(cu, cu[1:]) if 0 <= c <= d <= T for i in range(c, d)}
+    if whole == set(range(begin, end)):
+        for x in got:
+            assert torch.equal(got[x].view(torch.uint8), expect[x].view(torch.uint8)), x
+    assert torch.equal(q_out[at], q_good)
+    out, lse = torch.full((T, Hq, D), 7.0, device="cuda").bfloat16(), torch.full((T, Hq), 7.0, device="cuda")
+    mhc.kv_attend(q_out, expect, _i32(rows), _i32(lens), _i32(cu), out=out, lse=lse)
+    assert mhc.device_status() == INDEX_ERROR
+    check_attend({"out": out[at], "lse": lse[at]}, q_good, expect, [rows[b]], [lens[b]], [0, end - begin], D ** -0.5)
+    rest = [i for i in range(T) if i not in whole]
+    assert (out[rest] == 7).all() and (lse[rest] == 7).all()
