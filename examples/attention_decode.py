@@ -95,7 +95,7 @@ def run(prompts=(130, 5, 77), steps=4):
     load(0)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    with torch.cuda.stream(side):               # the first step as it is: the library's workspaces are made here
+    with torch.cuda.stream(side):               # the first step as it is: what is set up on first use is set up here
         out = [step().clone()]
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):

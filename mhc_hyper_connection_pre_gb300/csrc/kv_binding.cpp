@@ -14,11 +14,13 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <map>
 #include <mutex>
 #include <string>
 #include <utility>
+#include <vector>
 
 #include "mhc_kv.h"
 
@@ -122,21 +124,95 @@ Seqs seqs_of(PyObject* table_o, PyObject* lens_o, PyObject* cu_o, int64_t T, con
     return s;
 }
 
+void check_cuda(cudaError_t e, const char* what) {
+    if (e != cudaSuccess) throw Refused{PyExc_RuntimeError, std::string(what) + ": " + cudaGetErrorString(e)};
+}
+
+// The workspace of captured calls.  Replays write it at any time and on any
+// stream, so it is the graph's alone, for as long as the graph or an
+// instantiation of it lives: the graph holds a CUDA user object whose end hands
+// the memory back.  The calls of one capture on one stream follow one another
+// and share it.  (A buffer of the capturing allocator alone would not do: it is
+// free again once the call has returned, and outside of PyTorch's own captures
+// to anybody.)
+struct Captured {
+    at::Tensor memory;
+    cudaStream_t stream;
+    unsigned long long capture;
+};
+
+std::mutex g_mutex;                                              // of what follows; never held during a CUDA call
+auto* const g_kept = new std::map<std::pair<int, cudaStream_t>, at::Tensor>();    // never destroyed: outlives CUDA
+auto* const g_captured = new std::vector<Captured*>();           // of graphs that live
+auto* const g_gone = new std::vector<Captured*>();               // of graphs that do not
+
+// Called by CUDA, on a thread of its own, where no CUDA function may be called.
+void CUDART_CB graph_is_gone(void* p) {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    g_captured->erase(std::remove(g_captured->begin(), g_captured->end(), p), g_captured->end());
+    g_gone->push_back(static_cast<Captured*>(p));
+}
+
+at::Tensor new_workspace(size_t need, const at::Device& dev) {
+    return at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(dev));
+}
+
+// The workspace for a call on a stream that is being captured; undefined if it is not.
+at::Tensor captured_workspace(size_t need, const at::Device& dev, cudaStream_t stream) {
+    std::vector<Captured*> gone;
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        gone.swap(*g_gone);
+    }
+    for (Captured* c : gone) delete c;
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    check_cuda(cudaStreamIsCapturing(stream, &status), "cudaStreamIsCapturing");
+    if (status == cudaStreamCaptureStatusNone) return at::Tensor();
+    unsigned long long capture = 0;
+    cudaGraph_t graph = nullptr;
+    const cudaGraphNode_t* nodes = nullptr;
+    const cudaGraphEdgeData* edges = nullptr;
+    size_t n = 0;
+    check_cuda(cudaStreamGetCaptureInfo(stream, &status, &capture, &graph, &nodes, &edges, &n), "cudaStreamGetCaptureInfo");
+    if (status != cudaStreamCaptureStatusActive) check_cuda(cudaErrorStreamCaptureInvalidated, "kv workspace");
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        for (Captured* c : *g_captured)
+            if (c->stream == stream && c->capture == capture && (size_t)c->memory.numel() >= need) return c->memory;
+    }
+    auto* c = new Captured{new_workspace(need, dev), stream, capture};
+    at::Tensor memory = c->memory;
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        g_captured->push_back(c);
+    }
+    // a graph that cannot hold one leaves the memory with us, for good
+    cudaUserObject_t object = nullptr;
+    if (cudaUserObjectCreate(&object, c, graph_is_gone, 1, cudaUserObjectNoDestructorSync) != cudaSuccess ||
+        cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove) != cudaSuccess)
+        cudaGetLastError();
+    return memory;
+}
+
 // The workspace of a device and stream: kept and grown, as a user's program
-// would.  Not kept while the stream is being captured: that memory is the graph's.
+// would; of a stream that is being captured, the graph's.
 at::Tensor workspace_for(const mhc_kv_cache& c, int64_t q_heads, int64_t B, int64_t T, const at::Device& dev,
                          const c10::cuda::CUDAStream& stream) {
     const size_t need = mhc_kv_attend_workspace_bytes(&c, (int)q_heads, B, T);
     if (need == 0) return at::Tensor();
-    static std::mutex mutex;
-    static auto* kept = new std::map<std::pair<int, cudaStream_t>, at::Tensor>();   // never destroyed: outlives CUDA
-    std::lock_guard<std::mutex> lock(mutex);
-    at::Tensor& t = (*kept)[{dev.index(), stream.stream()}];
-    if (t.defined() && (size_t)t.numel() >= need) return t;
-    at::Tensor fresh = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(dev));
-    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream.stream(), &status) == cudaSuccess && status == cudaStreamCaptureStatusNone) t = fresh;
-    return fresh;
+    at::Tensor t = captured_workspace(need, dev, stream.stream());
+    if (t.defined()) return t;
+    const std::pair<int, cudaStream_t> key(dev.index(), stream.stream());
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        const at::Tensor& kept = (*g_kept)[key];
+        if (kept.defined() && (size_t)kept.numel() >= need) return kept;
+    }
+    t = new_workspace(need, dev);
+    at::Tensor old = t;                       // let go of after the lock
+    std::lock_guard<std::mutex> lock(g_mutex);
+    std::swap((*g_kept)[key], old);
+    return t;
 }
 
 void check_status(const char* fn, mhc_status st) {

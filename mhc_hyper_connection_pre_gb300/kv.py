@@ -110,7 +110,11 @@ def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, block_table: torch.
 def kv_workspace_for(cache: dict, q_heads: int, B: int, T: int, stream=None) -> torch.Tensor | None:
     """The device workspace that ``kv_attend`` uses when it is given none
     (None when it needs none): one buffer for each (device, stream), grown on
-    demand and allocated on that stream, as ``workspace_for``."""
+    demand and allocated on that stream, as ``workspace_for``.  A graph has
+    one of its own: while the stream is being captured this is the capture's,
+    which lives as long as the graph.  Passed on as ``workspace`` to calls on
+    another stream or in a graph, a buffer is shared with this stream's own
+    calls, and kept alive by whoever holds it."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return kv_workspace_for(cache, q_heads, B, T)

@@ -630,3 +630,126 @@ def test_offsets_out_of_range_leave_their_sequences_out(cu, good, Hq):
     check_attend({"out": out[at], "lse": lse[at]}, q_good, expect, [rows[b]], [lens[b]], [0, end - begin], D ** -0.5)
     rest = [i for i in range(T) if i not in whole]
     assert (out[rest] == 7).all() and (lse[rest] == 7).all()
+
+
+# ---------------------------------------------------- workspaces of graphs ---
+
+class _GraphCase:
+    """Decode attention of a few sequences, and a call that needs a larger workspace."""
+
+    def __init__(self):
+        D, P, H, self.Hq, lens = 128, 64, 2, 10, [2000, 64, 700]
+        rows, pages = _tables(lens, P, 41)
+        self.cache, self.table, self.lens = _random_cache(pages, H, P, D, 41), _i32(rows), _i32(lens)
+        g = torch.Generator(device="cuda").manual_seed(42)
+        self.q = torch.randn(3, self.Hq, D, generator=g, device="cuda").bfloat16()
+        self.out, self.lse = torch.empty_like(self.q), torch.empty(3, self.Hq, device="cuda")
+        self.many = torch.randn(600, self.Hq, D, generator=g, device="cuda").bfloat16()
+        self.cu = _i32([0, 500, 550, 600])
+        self.expect = mhc.kv_attend(self.q, self.cache, self.table, self.lens, return_lse=True)
+        torch.cuda.synchronize()
+
+    def call(self, stream=None):
+        mhc.kv_attend(self.q, self.cache, self.table, self.lens, out=self.out, lse=self.lse, stream=stream)
+
+    def larger(self, stream=None):
+        return mhc.kv_attend(self.many, self.cache, self.table, self.lens, self.cu, stream=stream)
+
+    def workspace(self, stream=None):
+        return mhc.kv_workspace_for(self.cache, self.Hq, 3, 3, stream)
+
+    def check(self):
+        torch.cuda.synchronize()
+        assert torch.equal(self.out, self.expect["out"]) and torch.equal(self.lse, self.expect["lse"])
+        self.out.zero_()
+        self.lse.zero_()
+
+
+def _blocks_of_others(nbytes, stream, n=6):
+    """What somebody else allocates on the stream, in the sizes that a workspace may have left free."""
+    with torch.cuda.stream(stream):
+        return [torch.full((nbytes,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(n)]
+
+
+def _capture(case, stream, kind):
+    if kind == "seam":
+        graph = SeamGraph(case.call, stream)
+        return graph, graph.replay
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        case.call()
+    return graph, graph.replay
+
+
+@pytest.mark.parametrize("kind", ["torch", "seam"])
+@pytest.mark.parametrize("warm", [True, False])
+def test_graph_keeps_its_workspace(kind, warm):
+    """Captured with the default workspace, after a call on the stream or as
+    the first one; then larger calls on it, and others' tensors in whatever
+    memory that set free: replays still give the outputs and touch nobody's."""
+    case, st = _GraphCase(), torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    if warm:
+        case.call(st)
+        case.check()
+    size = case.workspace(torch.cuda.current_stream()).numel()
+    graph, replay = _capture(case, st, kind)
+    others = _blocks_of_others(size, st)
+    case.larger(st)
+    others += _blocks_of_others(size, st)
+    for _ in range(3):
+        with torch.cuda.stream(st):
+            replay()
+        case.check()
+        case.larger(st)
+        others += _blocks_of_others(size, st, 2)
+    torch.cuda.synchronize()
+    assert all((o == 0x5A).all() for o in others)
+    del graph, replay
+
+
+def test_captures_have_workspaces_of_their_own():
+    """Two captures on one stream and the stream's own calls: three buffers; the calls of one capture share theirs."""
+    case, st = _GraphCase(), torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    case.call(st)
+    torch.cuda.synchronize()
+    own, seen, graphs = case.workspace(st).data_ptr(), [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            first = case.workspace()
+            case.call()
+            assert case.workspace().data_ptr() == first.data_ptr()
+        seen.append(first.data_ptr())
+        del first
+        graphs.append(graph)
+    assert len({own, *seen}) == 3 and case.workspace(st).data_ptr() == own
+    for graph in graphs:
+        graph.replay()
+        case.check()
+
+
+@pytest.mark.parametrize("kind", ["torch", "seam"])
+def test_workspace_ends_with_its_graph(kind):
+    """Graphs made and dropped do not add up; one that lives keeps its own."""
+    import gc
+    case, st = _GraphCase(), torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    case.call(st)
+    kept, replay = _capture(case, st, kind)
+    torch.cuda.synchronize()
+    case.call(st)
+    size, before = case.workspace(st).numel(), torch.cuda.memory_allocated()
+    for _ in range(12):
+        graph, again = _capture(case, st, kind)
+        again()
+        torch.cuda.synchronize()
+        del graph, again
+        gc.collect()
+    case.call(st)
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() <= before + 2 * size       # the last one may not be back yet
+    with torch.cuda.stream(st):
+        replay()
+    case.check()
