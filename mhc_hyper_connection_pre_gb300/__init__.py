@@ -135,25 +135,36 @@ def _device_index(device) -> int:
     return d.index if d.index is not None else torch.cuda.current_device()
 
 
+def _workspace(user: int, need: int, dev: int, s) -> torch.Tensor:
+    """The workspace of a user (1: the pre block, 2: ``seam_host``) on device
+    ``dev`` and stream ``s``; while the stream is being captured, the graph's:
+    it lives as long as the graph, whatever the stream's own calls need
+    meanwhile."""
+    from . import kv
+    buf = kv.captured_workspace(user, need, dev, s)
+    if buf is not None:
+        return buf
+    key = (user, dev, s.cuda_stream)
+    buf = _workspaces.get(key)
+    if buf is None or buf.numel() < need:
+        with torch.cuda.stream(s):
+            buf = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
+        _workspaces[key] = buf
+    return buf
+
+
 def workspace_for(T: int, n: int, C: int, device, stream=None) -> torch.Tensor | None:
     """A cached device workspace big enough for ``mhc_pre_delayed`` at this
     shape (None when the shape needs none).  One buffer per (device, stream),
     grown on demand and allocated on that stream, so calls on different
     streams never share one; ``stream`` defaults to the device's current
-    stream."""
+    stream.  A graph that is captured on the stream has one of its own."""
     dev = _device_index(device)
     with torch.cuda.device(dev):
         need = int(load_library().mhc_pre_workspace_bytes(T, n, C))
         if need == 0:
             return None
-        s = stream if stream is not None else torch.cuda.current_stream(dev)
-        key = (dev, s.cuda_stream)
-        buf = _workspaces.get(key)
-        if buf is None or buf.numel() < need:
-            with torch.cuda.stream(s):
-                buf = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
-            _workspaces[key] = buf
-    return buf
+        return _workspace(1, need, dev, stream if stream is not None else torch.cuda.current_stream(dev))
 
 
 def _stream_ptr(stream, device) -> int:
@@ -500,13 +511,7 @@ def seam_host(x: torch.Tensor, y: torch.Tensor, pre_in: torch.Tensor, fn: torch.
         di = _device_index(dev)
         with torch.cuda.device(di):
             need = int(lib.mhc_seam_host_workspace_bytes(T, n, C))
-            s = stream if stream is not None else torch.cuda.current_stream(di)
-            key = ("seam_host", di, s.cuda_stream)
-            workspace = _workspaces.get(key)
-            if workspace is None or workspace.numel() < need:
-                with torch.cuda.stream(s):
-                    workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=torch.device("cuda", di))
-                _workspaces[key] = workspace
+            workspace = _workspace(2, max(need, 1), di, stream if stream is not None else torch.cuda.current_stream(di))
     with torch.cuda.device(dev):
         st = lib.mhc_seam_host(
             _host_ptr(x, "x", torch.bfloat16), _host_ptr(y, "y", torch.bfloat16),

@@ -128,15 +128,18 @@ void check_cuda(cudaError_t e, const char* what) {
     if (e != cudaSuccess) throw Refused{PyExc_RuntimeError, std::string(what) + ": " + cudaGetErrorString(e)};
 }
 
-// The workspace of captured calls.  Replays write it at any time and on any
+// The workspace of captured calls (the seam's as well).  Replays write it at any time and on any
 // stream, so it is the graph's alone, for as long as the graph or an
 // instantiation of it lives: the graph holds a CUDA user object whose end hands
 // the memory back.  The calls of one capture on one stream follow one another
 // and share it.  (A buffer of the capturing allocator alone would not do: it is
 // free again once the call has returned, and outside of PyTorch's own captures
 // to anybody.)
+enum User { kAttend, kPre, kHost, kUsers };      // of the library's calls, each has its own
+
 struct Captured {
     at::Tensor memory;
+    User user;
     cudaStream_t stream;
     unsigned long long capture;
 };
@@ -158,7 +161,7 @@ at::Tensor new_workspace(size_t need, const at::Device& dev) {
 }
 
 // The workspace for a call on a stream that is being captured; undefined if it is not.
-at::Tensor captured_workspace(size_t need, const at::Device& dev, cudaStream_t stream) {
+at::Tensor captured_workspace(User user, size_t need, const at::Device& dev, cudaStream_t stream) {
     std::vector<Captured*> gone;
     {
         std::lock_guard<std::mutex> lock(g_mutex);
@@ -178,9 +181,10 @@ at::Tensor captured_workspace(size_t need, const at::Device& dev, cudaStream_t s
     {
         std::lock_guard<std::mutex> lock(g_mutex);
         for (Captured* c : *g_captured)
-            if (c->stream == stream && c->capture == capture && (size_t)c->memory.numel() >= need) return c->memory;
+            if (c->user == user && c->stream == stream && c->capture == capture && (size_t)c->memory.numel() >= need)
+                return c->memory;
     }
-    auto* c = new Captured{new_workspace(need, dev), stream, capture};
+    auto* c = new Captured{new_workspace(need, dev), user, stream, capture};
     at::Tensor memory = c->memory;
     {
         std::lock_guard<std::mutex> lock(g_mutex);
@@ -200,7 +204,7 @@ at::Tensor workspace_for(const mhc_kv_cache& c, int64_t q_heads, int64_t B, int6
                          const c10::cuda::CUDAStream& stream) {
     const size_t need = mhc_kv_attend_workspace_bytes(&c, (int)q_heads, B, T);
     if (need == 0) return at::Tensor();
-    at::Tensor t = captured_workspace(need, dev, stream.stream());
+    at::Tensor t = captured_workspace(kAttend, need, dev, stream.stream());
     if (t.defined()) return t;
     const std::pair<int, cudaStream_t> key(dev.index(), stream.stream());
     {
@@ -372,6 +376,23 @@ PyObject* workspace(PyObject*, PyObject* const* o, Py_ssize_t n) {
     });
 }
 
+// captured(user, bytes, device index, stream): the workspace of the capture that is under way on the stream, or None
+PyObject* captured(PyObject*, PyObject* const* o, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        count(n, 4);
+        const long long user = PyLong_AsLongLong(o[0]), need = PyLong_AsLongLong(o[1]), index = PyLong_AsLongLong(o[2]);
+        void* const stream = PyLong_AsVoidPtr(o[3]);
+        if (PyErr_Occurred()) throw Refused{nullptr, ""};
+        if (user < 0 || user >= kUsers || need < 1) value_error("no such workspace");
+        const at::Device dev(at::kCUDA, (c10::DeviceIndex)index);
+        const auto on = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), dev.index());
+        const c10::cuda::CUDAStreamGuard guard(on);              // memory is the stream's
+        at::Tensor t = captured_workspace((User)user, (size_t)need, dev, on.stream());
+        if (!t.defined()) Py_RETURN_NONE;
+        return THPVariable_Wrap(std::move(t));
+    });
+}
+
 // set_error(MhcError)
 PyObject* set_error(PyObject*, PyObject* type) {
     Py_INCREF(type);
@@ -384,6 +405,7 @@ PyMethodDef methods[] = {
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, "mhc_kv_append"},
     {"attend", (PyCFunction)(void (*)(void))attend, METH_FASTCALL, "mhc_kv_attend"},
     {"workspace", (PyCFunction)(void (*)(void))workspace, METH_FASTCALL, "a workspace for attend"},
+    {"captured", (PyCFunction)(void (*)(void))captured, METH_FASTCALL, "a workspace of a capture"},
     {"set_error", set_error, METH_O, "the exception for a status that is not MHC_OK"},
     {nullptr, nullptr, 0, nullptr},
 };

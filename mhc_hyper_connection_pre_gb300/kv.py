@@ -68,6 +68,11 @@ def _load():
         return _module
 
 
+def captured_workspace(user: int, need: int, device: int, stream) -> torch.Tensor | None:
+    """The workspace of the capture under way on ``stream``, which its graph keeps alive; None if there is none."""
+    return (_module or _load()).captured(user, need, device, stream.cuda_stream)
+
+
 def kv_cache(num_pages: int, heads: int, page_tokens: int = 64, head_dim: int = 128, *, device="cuda") -> dict:
     """An empty cache of one layer (every code and scale zero)."""
     shape = (num_pages, heads, page_tokens, head_dim)

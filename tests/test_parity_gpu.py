@@ -1004,3 +1004,47 @@ def test_packed_weights_are_bit_identical(T, C, fold):
     assert mhc.device_status() == 0
     for k in ("pre", "post", "comb", "layer_input", "logits"):
         assert torch.equal(got[k], ref[k]), k
+
+
+@pytest.mark.parametrize("call", ["pre_delayed", "seam_host"])
+@pytest.mark.parametrize("warm", [True, False])
+def test_graph_keeps_its_workspace(call, warm):
+    """Captured with the default workspace, after a call on the stream or as
+    the first one; then larger calls on it, and others' tensors in whatever
+    memory that set free: replays still give the outputs and touch nobody's."""
+    def inputs(T):
+        gd = seam_inputs(T, seed=2500, fold=True, with_y=True, device="cuda")
+        gd["hx"], gd["hy"], gd["hp"] = _pinned(gd["x"]), _pinned(gd["y"]), _pinned(gd["pre_in"])
+        return gd
+
+    def run(gd, out, st):
+        if call == "seam_host":
+            return mhc.seam_host(gd["hx"], gd["hy"], gd["hp"], gd["fn"], gd["bias"], gd["alpha"], gd["norm_w"], out=out,
+                                 stream=st)
+        return mhc.pre_delayed(gd["x"], gd["pre_in"], gd["fn"], gd["bias"], gd["alpha"], gd["norm_w"], out=out, stream=st)
+
+    small, large, st = inputs(300), inputs(1500), torch.cuda.Stream()
+    out = run(small, None, torch.cuda.current_stream())
+    large_out = run(large, None, torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    expect = {k: v.clone() for k, v in out.items()}
+    if warm:
+        run(small, out, st)
+    lib = mhc.load_library()
+    size = int((lib.mhc_seam_host_workspace_bytes if call == "seam_host" else lib.mhc_pre_workspace_bytes)(300, 4, 5120))
+    graph = SeamGraph(lambda s: run(small, out, s), st)
+    others = []
+    for _ in range(3):
+        with torch.cuda.stream(st):
+            others += [torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        run(large, large_out, st)
+        torch.cuda.synchronize()
+        for v in out.values():
+            v.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert mhc.device_status() == 0
+        assert all(torch.equal(out[k], expect[k]) for k in expect)
+    assert size > 0 and all((o == 0x5A).all() for o in others)
+    graph.close()
