@@ -325,16 +325,20 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     uint32_t pushed = 0, popped = 0;          // segments
     int key = 0, keys = 0, head = 0;          // of the next load: its first key, its segment's last key + 1 and head
     int b = 0;
+    bool over = false;                        // the plan has no more segments
     int blocks[2], ahead = 32;                // page and head of both halves of 32 loads, one in each lane (-1: no page);
                                               // the next load's lane
 
     // On to the next load; false: there is none, or none before a segment of the queue is done.
     auto settle = [&] {
         while (key >= keys) {
-            if (plan.w.left <= 0 || pushed - popped == kQueue) return false;
+            if (over || pushed - popped == kQueue) return false;
             Segment& s = sm.queue[warp][pushed % kQueue];
-            const bool found = lane == 0 && push_segment(a, plan, sm.shares[warp], s);
-            if (!__any_sync(0xffffffffu, found)) return false;        // the share ends in a tile's extra units
+            // none: the share is done, or what is left of it are a tile's extra units
+            if (!found_for_all(ThisWarp{lane}, [&] { return plan.w.left > 0 && push_segment(a, plan, sm.shares[warp], s); })) {
+                over = true;
+                return false;
+            }
             ++pushed;
             key = s.key0;
             keys = s.keys;

@@ -81,6 +81,14 @@ __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// The warp that runs it.
+struct ThisWarp {
+    int lane;
+    __device__ __forceinline__ bool first() const { return lane == 0; }
+    __device__ __forceinline__ bool any(bool x) const { return __any_sync(0xffffffffu, x); }
+    __device__ __forceinline__ void sync() const { __syncwarp(); }
+};
+
 // Finds sequence b for a plan.
 struct Lookup {
     const AttendArgs& a;

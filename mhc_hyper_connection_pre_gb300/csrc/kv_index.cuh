@@ -347,5 +347,16 @@ MHC_HD bool plan_next(Plan& p, const Look& look, const Cut& c, const Shares& sha
     return false;
 }
 
+// A segment that one lane of a warp finds, for all of its lanes: find() writes it
+// into the warp's queue and says whether there was one.  The vote brings the
+// lanes together but orders no memory, so a barrier follows before anybody reads
+// the segment.  The plan is the one lane's alone.
+template <class Warp, class Find>
+MHC_HD bool found_for_all(const Warp& warp, Find&& find) {
+    const bool found = warp.any(warp.first() && find());
+    warp.sync();
+    return found;
+}
+
 }  // namespace kv
 }  // namespace mhc

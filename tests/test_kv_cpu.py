@@ -345,3 +345,12 @@ def test_bad_offsets_leave_their_sequence_out(shim, cu, good):
         assert b in good and cu[b] <= t and see1 <= lens[b]
         rows[b, h] += n if k0 == 0 else 0
     assert all(n == (cu[b + 1] - cu[b]) * group for (b, _), n in rows.items())
+
+
+def test_a_warps_segments_are_handed_over_in_order(tmp_path):
+    """One lane plans, all lanes read: no data race where a vote orders no memory (a race ends the program with 66)."""
+    exe = str(tmp_path / "race")
+    subprocess.run(["g++", "-O1", "-g", "-std=c++17", "-fsanitize=thread", os.path.join(HERE, "kv_warp_race.cpp"), "-o", exe,
+                    "-pthread"], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
