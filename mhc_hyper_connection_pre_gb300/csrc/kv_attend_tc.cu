@@ -393,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     f = a.scale_log2 * __uint_as_float(0x7f000000u - __float_as_uint(power_up(my_top)));
-                    if (my_top == INFINITY) l = __int_as_float(0x7fc00000);   // e4m3 has no infinity: such a row is NaN
+                    // e4m3 has no infinity: such a row is NaN, if it sees a key
+                    if (my_top == INFINITY && lim > 0) l = __int_as_float(0x7fc00000);
                     fence_proxy_async_smem();
                     if (unread) {             // the last segment's reads of O come before this one's products
                         ok = __all_sync(0xffffffffu, wait_for(&sm.half_read, (halves - 1) & 1, &sm.abort));

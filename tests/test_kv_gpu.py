@@ -753,3 +753,16 @@ def test_workspace_ends_with_its_graph(kind):
     with torch.cuda.stream(st):
         replay()
     case.check()
+
+
+# ------------------------------------------------------ infinite queries ---
+
+@pytest.mark.parametrize("Hq", [2, 40])
+def test_attend_infinite_queries_without_keys(Hq):
+    """Rows that see no key are zero and minus infinity, whatever their queries hold, in each kernel."""
+    def fill(q, cache, rows):
+        q[0], q[1, :, 5], q[2, 0], q[2, 1, ::2] = math.inf, -math.inf, math.nan, math.inf
+    got, of = _attend((128, 16, 1, Hq, [6, 4], [3, 40]), 500, fill=fill)
+    assert (got["out"][:3] == 0).all() and (got["lse"][:3] == -math.inf).all()
+    got["out"][:3], of[0][:3] = 0, 0
+    check_attend(got, *of)
