@@ -112,7 +112,8 @@ mhc_status mhc_kv_append(const mhc_kv_cache *cache, const uint16_t *k, int64_t k
  *   lse    = log(sum_j exp(s_j))
  *   out    = bf16( sum_j exp(s_j - lse) v_j )
  * A token that sees no key gets out = 0 and lse = -infinity.  A key after p
- * never reaches the output, whatever its bytes stand for.
+ * never reaches the output, whatever its bytes stand for.  A query that holds
+ * an infinity or NaN gives NaN in out and lse if it sees a key.
  *
  *  q          bf16 as in mhc_kv_append (already rotated)
  *  q_heads    a multiple of cache->heads, at most 128 times as many

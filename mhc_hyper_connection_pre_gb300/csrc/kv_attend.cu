@@ -458,7 +458,8 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
                 const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) q[nb][i] = pack_f16x2(x[2 * i] * up, x[2 * i + 1] * up);
-                const float back = down * a.scale_log2;
+                // a row with an infinity is NaN where it sees a key, whatever its products are
+                const float back = top == INFINITY ? __int_as_float(0x7fc00000) : down * a.scale_log2;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int c = nb * 8 + 2 * t + i;

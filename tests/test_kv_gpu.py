@@ -766,3 +766,17 @@ def test_attend_infinite_queries_without_keys(Hq):
     assert (got["out"][:3] == 0).all() and (got["lse"][:3] == -math.inf).all()
     got["out"][:3], of[0][:3] = 0, 0
     check_attend(got, *of)
+
+
+@pytest.mark.parametrize("Hq", [2, 40])
+@pytest.mark.parametrize("n", [1, 70, 5000])
+def test_attend_infinite_query_is_nan(Hq, n):
+    """A query with an infinity that sees a key gives NaN in each kernel, also where every product is minus infinity."""
+    def fill(q, cache, rows):
+        cache["k"].view(torch.uint8)[:, :, :, 0] = 0x38        # one
+        q[0, 0] = 1.0
+        q[0, 0, 0] = -math.inf
+    got, of = _attend((64, 16, 1, Hq, None, [n]), 510, fill=fill)
+    assert got["out"][0, 0].isnan().all() and got["lse"][0, 0].isnan()
+    got["out"][0, 0], got["lse"][0, 0], of[0][0, 0] = 0, 0, 0
+    assert not got["out"].isnan().any() and not got["lse"].isnan().any()
