@@ -170,9 +170,10 @@ __device__ __forceinline__ void piece(bool full, uint32_t ks, uint32_t vs, const
     if (grow || most > acc.ref) {             // the same for the whole warp
         float shrink = 1.0f;
         if (most > acc.ref) {
-            acc.inv = __frcp_rn(most);
+            const float now = value_unit(most);
+            acc.inv = __frcp_rn(now);
             shrink = acc.ref * acc.inv;
-            acc.ref = most;
+            acc.ref = now;
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -509,7 +510,8 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
                 const float m = acc.m[nb][e];
                 const int r = nb * 8 + 2 * t + e;
                 if (r >= seg.rows) continue;
-                const float by = whole ? (l == 0.0f ? 0.0f : acc.ref * __frcp_rn(l)) : acc.ref;
+                // one after the other: their product may be too small for fp32
+                const float by = whole ? (l == 0.0f ? 0.0f : __frcp_rn(l)) : 1.0f, ref = acc.ref;
                 if (whole) {
                     const int64_t to = place_of(a, seg, r);
                     uint4* out = reinterpret_cast<uint4*>(a.out + to * D + g * (D / 8));
@@ -518,8 +520,8 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
                         float y[8];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            y[2 * i] = acc.o[j + i][nb][e] * by;
-                            y[2 * i + 1] = acc.o[j + i][nb][e + 2] * by;
+                            y[2 * i] = acc.o[j + i][nb][e] * by * ref;
+                            y[2 * i + 1] = acc.o[j + i][nb][e + 2] * by * ref;
                         }
                         out[j / 4] = pack8(y);
                     }
@@ -528,8 +530,8 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
                     float4* out = reinterpret_cast<float4*>(part + r * D + g * (D / 8));
 #pragma unroll
                     for (int j = 0; j < D / 16; j += 2)
-                        out[j / 2] = make_float4(acc.o[j][nb][e] * by, acc.o[j][nb][e + 2] * by,
-                                                 acc.o[j + 1][nb][e] * by, acc.o[j + 1][nb][e + 2] * by);
+                        out[j / 2] = make_float4(acc.o[j][nb][e] * ref, acc.o[j][nb][e + 2] * ref,
+                                                 acc.o[j + 1][nb][e] * ref, acc.o[j + 1][nb][e + 2] * ref);
                     if (g == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(m, l);
                 }
             }

@@ -16,6 +16,11 @@ constexpr float kLift = 10.0f;                // weights are 2^10 times the soft
 constexpr float kGrow = 5.0f;                   // the maximum follows when it has grown by more (in powers of two)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// The value scale that a tile's values are held relative to, from the largest
+// one: at least the smallest normal number, so that its reciprocal is finite.
+// Zero if all are.
+__device__ __forceinline__ float value_unit(float most) { return most > 0.0f ? fmaxf(most, 1.17549435e-38f) : 0.0f; }
+
 // A part of a tile that a share has left in the workspace.
 struct PartDesc {
     int parts, owner;                         // as the segment's; parts 0: nothing here

@@ -518,7 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float* part = part_of(a, blockIdx.x, slot, D);
                 const int kept = segs % kSegs;
                 const float unit = steps > 0 ? sm.ref[kept] * (1.0f / kVLift) : 0.0f;
-                const float by = whole ? (l == 0.0f ? 0.0f : unit * __frcp_rn(l)) : unit;
+                const float by = whole ? (l == 0.0f ? 0.0f : __frcp_rn(l)) : 1.0f;     // apart from the unit: their product
+                                                                                     // may be too small for fp32
                 const bool nans = steps > 0 && sm.has_nan[kept];
                 own *= by;
                 other *= by;
@@ -554,6 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 32; ++i)
                             o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), other, __uint_as_float(o[i])));
                     }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * unit);
                     if (nans) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -615,10 +618,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = id; i < D; i += 128) sm.nan_key[slot][i] = 0x7fffffff;
                 if (id == 0) sm.has_nan[slot] = 0;
                 named_bar_sync(1, 128);
-                most = fmaxf(fmaxf(sm.red[0], sm.red[1]), fmaxf(sm.red[2], sm.red[3]));
+                most = value_unit(fmaxf(fmaxf(sm.red[0], sm.red[1]), fmaxf(sm.red[2], sm.red[3])));
                 if (id == 0) sm.ref[slot] = most;
                 named_bar_sync(1, 128);
-                const float per = most > 0.0f ? kVLift * __frcp_rn(most) : 0.0f;
+                const float per = most > 0.0f ? __frcp_rn(most) : 0.0f;
                 const int all_see = keys_of_row(seg, a.cut, 0);
                 for (int key = key0; ok && key < keys; key += kTile) {
                     ok = __all_sync(0xffffffffu, wait_for(&sm.v_full[vr.stage], vr.phase, &sm.abort)) &&
@@ -627,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const Meta& meta = sm.v_meta[vr.stage];
                     const uint32_t src = smem_u32(sm.v[vr.stage]), dst = smem_u32(sm.v16[v16r.stage]);
                     const bool use = ((meta.valid >> (id / 16)) & 1) && key + id < keys;
-                    const float ratio = use ? meta.scale[id / 16] * per : 0.0f;
+                    const float ratio = use ? meta.scale[id / 16] * per * kVLift : 0.0f;
                     // 64 dims of a key are one 128-byte row, swizzled; the next 64 dims follow all keys
                     auto put = [&](int c, const uint32_t (&h)[8]) {
                         const uint32_t to_row = dst + (c / 4) * (kTile * 128) + id * 128;

@@ -7,7 +7,7 @@ import torch
 
 import mhc_hyper_connection_pre_gb300 as mhc
 from mhc_hyper_connection_pre_gb300.graphs import SeamGraph
-from kv_reference import check_append, check_attend, e4m3_round
+from kv_reference import attend, check_append, check_attend, e4m3_round
 
 pytestmark = pytest.mark.gpu
 
@@ -780,3 +780,37 @@ def test_attend_infinite_query_is_nan(Hq, n):
     assert got["out"][0, 0].isnan().all() and got["lse"][0, 0].isnan()
     got["out"][0, 0], got["lse"][0, 0], of[0][0, 0] = 0, 0, 0
     assert not got["out"].isnan().any() and not got["lse"].isnan().any()
+
+
+# ----------------------------------------------------------- value scales ---
+
+SCALES = {
+    "zero": [0.0], "one zero": [0.0, 1.0], "subnormal": [2.0 ** -140], "subnormal, then normal": [2.0 ** -149, 2.0 ** -3],
+    "reciprocal at the border": [2.0 ** -128, 2.0 ** -127, 2.0 ** -122], "smallest of append": [2.0 ** -116],
+    "far apart": [1.0, 2.0 ** -20], "far apart, no powers": [1.3 * 2.0 ** -20, 1.7],
+}
+
+
+@pytest.mark.parametrize("kind", SCALES)
+@pytest.mark.parametrize("case", [(128, 16, 2, 4, None, [70, 30]), (64, 16, 2, 32, None, [3000]), (128, 16, 1, 5, [30], [400]),
+                                  (64, 32, 1, 40, [3, 7], [3001, 100]), (128, 32, 1, 50, [3], [5000])])
+def test_attend_value_scales(kind, case):
+    """Any finite value scales that are not negative, page after page.
+
+    Beside the usual bounds: bf16's step in its subnormal range is 2^-133,
+    half of that for the output's rounding and the rest for fp32's subnormals
+    before it."""
+    D, P, H, Hq, counts, lens = case
+
+    def fill(q, cache, rows):
+        for r in rows:
+            for i, p in enumerate(r):
+                if p >= 0:
+                    cache["v_scale"][p] = SCALES[kind][i % len(SCALES[kind])]
+    got, of = _attend(case, 600, fill=fill)
+    out, lse, tol, tol_lse = attend(*of)
+    assert out.isfinite().all()
+    o, l = got["out"].double(), got["lse"].double()
+    bad = ~((o - out).abs() <= tol + 2.0 ** -133)
+    assert not bad.any(), (int(bad.sum()), o[bad][:4].tolist(), out[bad][:4].tolist())
+    assert ((l - lse).abs() <= tol_lse).all()
