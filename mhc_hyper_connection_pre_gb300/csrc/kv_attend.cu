@@ -511,28 +511,26 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
                 const int r = nb * 8 + 2 * t + e;
                 if (r >= seg.rows) continue;
                 // one after the other: their product may be too small for fp32
-                const float by = whole ? (l == 0.0f ? 0.0f : __frcp_rn(l)) : 1.0f, ref = acc.ref;
+                const float by = l == 0.0f ? 0.0f : __frcp_rn(l);
+                float y[D / 8];
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    y[2 * j] = acc.o[j][nb][e] * by * acc.ref;
+                    y[2 * j + 1] = acc.o[j][nb][e + 2] * by * acc.ref;
+                }
                 if (whole) {
                     const int64_t to = place_of(a, seg, r);
                     uint4* out = reinterpret_cast<uint4*>(a.out + to * D + g * (D / 8));
 #pragma unroll
-                    for (int j = 0; j < D / 16; j += 4) {
-                        float y[8];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            y[2 * i] = acc.o[j + i][nb][e] * by * ref;
-                            y[2 * i + 1] = acc.o[j + i][nb][e + 2] * by * ref;
-                        }
-                        out[j / 4] = pack8(y);
-                    }
+                    for (int j = 0; j < D / 64; ++j)
+                        out[j] = make_uint4(pack_bf16x2(y[8 * j], y[8 * j + 1]), pack_bf16x2(y[8 * j + 2], y[8 * j + 3]),
+                                            pack_bf16x2(y[8 * j + 4], y[8 * j + 5]), pack_bf16x2(y[8 * j + 6], y[8 * j + 7]));
                     if (g == 0 && a.lse) a.lse[to] = lse_of(m, l);
                 } else {
                     float4* out = reinterpret_cast<float4*>(part + r * D + g * (D / 8));
 #pragma unroll
-                    for (int j = 0; j < D / 16; j += 2)
-                        out[j / 2] = make_float4(acc.o[j][nb][e] * ref, acc.o[j][nb][e + 2] * ref,
-                                                 acc.o[j + 1][nb][e] * ref, acc.o[j + 1][nb][e + 2] * ref);
-                    if (g == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(m, l);
+                    for (int j = 0; j < D / 32; ++j) out[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                    if (g == 0) part[kRows * D + r] = weight_of(m, l);
                 }
             }
         }
@@ -549,7 +547,10 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     }
 }
 
-// Joins the tiles that borders between shares have cut.  A tile's parts are
+// Joins the tiles that borders between shares have cut.  A part holds its own
+// keys' mean of the values, not their sum, and its weight is held to add up to
+// one at most with the others', so that values up to fp32's largest stay in
+// range.  A tile's parts are
 // slot 1 of the share that began it (its owner) and slot 0 of the shares after
 // it.  Each share has a warp for either slot (or gridDim.y of them).  A tile's
 // warps divide its rows; from kMany parts on, a long sequence, the blocks whose
@@ -567,13 +568,13 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, share = blockIdx.x * 8 + warp;
     if (share >= a.shares) return;
-    const int64_t next = (int64_t)(2 * (D + 2)) << a.cut.tile_log2;      // from a share's part to the next share's
+    const int64_t next = (int64_t)(2 * (D + 1)) << a.cut.tile_log2;      // from a share's part to the next share's
     const PartDesc& d = a.desc[2 * share + blockIdx.z];
     const int parts = d.parts;
     if (parts == 0) return;
     const Segment seg = d.seg;
     const float* first = part_of(a, d.owner, 1, D);
-    const float* sums = (D << a.cut.tile_log2) + first;              // maxima and sums of the first part
+    const float* sums = (D << a.cut.tile_log2) + first;              // weights of the first part
     const int64_t to_rest = part_of(a, d.owner + 1, 0, D) - next - first;   // part k, k > 0, is k * next further
     if (parts < kSome) {                      // a warp takes a row; four parts at a time, all their loads at once
 #pragma unroll 1
@@ -581,17 +582,16 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
             float m = -INFINITY, l = 0.0f, o[kDims] = {};
 #pragma unroll 1
             for (int base = 0; base < parts; base += 4) {
-                float2 ml[4];
-                float y[4][kDims];
+                float w[4], y[4][kDims];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int k = base + i;
                     const int64_t off = k ? to_rest + k * next : 0;
-                    ml[i] = make_float2(-INFINITY, 0.0f);
+                    w[i] = -INFINITY;
 #pragma unroll
                     for (int c = 0; c < kDims; ++c) y[i][c] = 0.0f;
                     if (k < parts) {
-                        ml[i] = *reinterpret_cast<const float2*>(sums + off + 2 * r);
+                        w[i] = sums[off + r];
                         const float* src = first + off + r * D + lane * kDims;
                         if constexpr (D == 128) {
                             const float4 v = *reinterpret_cast<const float4*>(src);
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
                         }
                     }
                 }
-                const float now = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+                const float now = fmaxf(fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])), m);
                 const float zero = now == -INFINITY ? 0.0f : now, keep = ex2(m - zero);
                 m = now;
                 l *= keep;
@@ -610,8 +610,8 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
                 for (int c = 0; c < kDims; ++c) o[c] *= keep;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float x = ex2(ml[i].x - zero);
-                    l = fmaf(x, ml[i].y, l);
+                    const float x = ex2(w[i] - zero - kPartsLog2);
+                    l += x;
 #pragma unroll
                     for (int c = 0; c < kDims; ++c) o[c] = fmaf(x, y[i][c], o[c]);
                 }
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
                 *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o[0] * by, o[1] * by), pack_bf16x2(o[2] * by, o[3] * by));
             else
                 *out = pack_bf16x2(o[0] * by, o[1] * by);
-            if (lane == 0 && a.lse) a.lse[to] = lse_of(m, l);
+            if (lane == 0 && a.lse) a.lse[to] = lse_of(m + kPartsLog2, l);
         }
         return;
     }
@@ -645,9 +645,8 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
 #pragma unroll 1
         for (int base = k0; base < k1; base += kAhead) {             // the loads of kAhead parts at once
             float y[kAhead][kDims];
-            float2 ml = make_float2(-INFINITY, 0.0f);
-            if (lane < kAhead && base + lane < k1)
-                ml = *reinterpret_cast<const float2*>(sums + (base + lane ? to_rest + (base + lane) * next : 0) + 2 * r);
+            float w = -INFINITY;
+            if (lane < kAhead && base + lane < k1) w = sums[(base + lane ? to_rest + (base + lane) * next : 0) + r];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 const int k = base + i;
@@ -664,12 +663,13 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
                     }
                 }
             }
-            float now = ml.x;
+            float now = w;
 #pragma unroll
             for (int i = kAhead / 2; i; i >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, i));
             now = fmaxf(__shfl_sync(0xffffffffu, now, 0), m);
-            const float zero = now == -INFINITY ? 0.0f : now, keep = ex2(m - zero), w = ex2(ml.x - zero);
-            float all = w * ml.y;
+            const float zero = now == -INFINITY ? 0.0f : now, keep = ex2(m - zero);
+            w = ex2(w - zero - kPartsLog2);
+            float all = w;
 #pragma unroll
             for (int i = kAhead / 2; i; i >>= 1) all += __shfl_xor_sync(0xffffffffu, all, i);
             l = fmaf(l, keep, __shfl_sync(0xffffffffu, all, 0));
@@ -689,7 +689,7 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
             uint32_t* out = reinterpret_cast<uint32_t*>(a.out + to * D + lane * kDims);
             out[0] = pack_bf16x2(o[0] * by, o[1] * by);
             if constexpr (D == 128) out[1] = pack_bf16x2(o[2] * by, o[3] * by);
-            if (lane == 0 && a.lse) a.lse[to] = lse_of(m, l);
+            if (lane == 0 && a.lse) a.lse[to] = lse_of(m + kPartsLog2, l);
             continue;
         }
 #pragma unroll
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
             const int64_t to = place_of(a, seg, r);
             const float by = total == 0.0f ? 0.0f : __frcp_rn(total);
             reinterpret_cast<uint32_t*>(a.out + to * D)[threadIdx.x] = pack_bf16x2(x * by, y * by);
-            if (threadIdx.x == 0 && a.lse) a.lse[to] = lse_of(top, total);
+            if (threadIdx.x == 0 && a.lse) a.lse[to] = lse_of(top + kPartsLog2, total);
         }
         __syncthreads();
     }
@@ -732,14 +732,15 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
 // Of the tiles of 8 and 16: up to 8 rows 104, 105 | 65, 72 for 64 sequences of 4096.
 int tile_rows(int group, int64_t B, int64_t T) { return T * group > 32 * B ? 256 : (T * group > 8 * B ? 16 : 8); }
 
-// Shares of the work: warps, or the tensor-memory kernel's blocks.
+// Shares of the work: warps, or the tensor-memory kernel's blocks.  Fewer than
+// 2^kPartsLog2 up to 256 SMs.
 int shares_of(int rows, int D, int num_sms) {
     if (rows == 256) return num_sms;
     if (D == 64) return num_sms * (rows == 8 ? Shape<64, 1>::kWarps : Shape<64, 2>::kWarps);
     return num_sms * (rows == 8 ? Shape<128, 1>::kWarps : Shape<128, 2>::kWarps);
 }
 
-size_t part_bytes(int rows, int D, int shares) { return ((size_t)shares * 2 * rows * (D + 2) * 4 + 255) / 256 * 256; }
+size_t part_bytes(int rows, int D, int shares) { return ((size_t)shares * 2 * rows * (D + 1) * 4 + 255) / 256 * 256; }
 
 template <int D, int NB>
 cudaError_t launch(const CUtensorMap& k_map, const CUtensorMap& v_map, const AttendArgs& a, int blocks,

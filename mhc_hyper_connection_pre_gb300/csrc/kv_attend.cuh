@@ -14,6 +14,7 @@ namespace kv {
 
 constexpr float kLift = 10.0f;                // weights are 2^10 times the softmax's numerators
 constexpr float kGrow = 5.0f;                   // the maximum follows when it has grown by more (in powers of two)
+constexpr float kPartsLog2 = 12.0f;             // a tile has fewer than 2^12 parts; the join divides their weights by it
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // The value scale that a tile's values are held relative to, from the largest
@@ -38,13 +39,13 @@ struct AttendArgs {
     float scale_log2;                         // softmax_scale * log2(e)
     uint16_t* out;
     float* lse;
-    float* part;                              // [shares][2]: weighted values [rows][D], maximum and sum [rows][2]
+    float* part;                              // [shares][2]: mean of the values [rows][D], log2 of the weights' sum [rows]
     PartDesc* desc;                           // [shares][2]
 };
 
 // Part `slot` of a share: 1 of the tile that it began (it is the owner), 0 of one that it went on with.
 __device__ __forceinline__ float* part_of(const AttendArgs& a, int share, int slot, int D) {
-    return a.part + (((int64_t)share * 2 + slot) * (D + 2) << a.cut.tile_log2);
+    return a.part + (((int64_t)share * 2 + slot) * (D + 1) << a.cut.tile_log2);
 }
 
 constexpr int kSegments = 32;                 // that the tensor-memory kernel plans at a time
@@ -226,6 +227,9 @@ __device__ __forceinline__ int64_t place_of(const AttendArgs& a, const Segment& 
     row_of(s, a.cut, r, token, in_group);
     return (int64_t)token * (a.cut.heads * a.cut.group) + s.head * a.cut.group + in_group;
 }
+
+// What a part weighs, in powers of two.
+__device__ __forceinline__ float weight_of(float m, float l) { return l == 0.0f ? -INFINITY : m + __log2f(l); }
 
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -INFINITY : kLn2 * (m - kLift + __log2f(l));

@@ -518,8 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float* part = part_of(a, blockIdx.x, slot, D);
                 const int kept = segs % kSegs;
                 const float unit = steps > 0 ? sm.ref[kept] * (1.0f / kVLift) : 0.0f;
-                const float by = whole ? (l == 0.0f ? 0.0f : __frcp_rn(l)) : 1.0f;     // apart from the unit: their product
-                                                                                     // may be too small for fp32
+                const float by = l == 0.0f ? 0.0f : __frcp_rn(l);     // apart from the unit: their product may be too
+                                                                    // small for fp32
                 const bool nans = steps > 0 && sm.has_nan[kept];
                 own *= by;
                 other *= by;
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (mine < rows) {
                     to = whole ? reinterpret_cast<uint64_t>(a.out + at * D) : reinterpret_cast<uint64_t>(part + mine * D);
                     if (whole && a.lse) a.lse[at] = lse_of(m, l);
-                    if (!whole) *reinterpret_cast<float2*>(part + kPair * D + 2 * mine) = make_float2(m, l);
+                    if (!whole) part[kPair * D + mine] = weight_of(m, l);
                 }
                 auto staged = [&](int r, int c) {             // 16-byte chunk c of row r of the warp
                     const uint32_t row = D == 128 ? smem_u32(sm.q[x][0]) + (warp % 4) * 4096 + r * 128

@@ -814,3 +814,22 @@ def test_attend_value_scales(kind, case):
     bad = ~((o - out).abs() <= tol + 2.0 ** -133)
     assert not bad.any(), (int(bad.sum()), o[bad][:4].tolist(), out[bad][:4].tolist())
     assert ((l - lse).abs() <= tol_lse).all()
+
+
+@pytest.mark.parametrize("kind", [[2.0 ** 115], [2.0 ** 100, 2.0 ** 115], [2.0 ** -3, 2.0 ** 115], [1.7 * 2.0 ** 114]])
+@pytest.mark.parametrize("case", [(128, 16, 2, 4, None, [70, 30]), (64, 16, 2, 32, None, [3000]), (128, 16, 1, 5, [30], [400]),
+                                  (64, 32, 1, 40, [3, 7], [3001, 100]), (128, 32, 1, 50, [3], [5000]),
+                                  (64, 64, 1, 7, None, [40000])])
+def test_attend_largest_values(kind, case):
+    """Values near bf16's largest, whose sums are beyond fp32, from few and
+    from many shares of the work: the output is their mean and so finite."""
+    D, P, H, Hq, counts, lens = case
+
+    def fill(q, cache, rows):
+        for r in rows:
+            for i, p in enumerate(r):
+                if p >= 0:
+                    cache["v_scale"][p] = kind[i % len(kind)]
+    got, of = _attend(case, 610, fill=fill)
+    check_attend(got, *of)
+    assert got["out"].isfinite().all()
