@@ -82,9 +82,12 @@ def kv_cache(num_pages: int, heads: int, page_tokens: int = 64, head_dim: int = 
             "v_scale": torch.zeros(num_pages, heads, dtype=torch.float32, device=device)}
 
 
-def _on(stream, tensors):
-    """A context in which ``stream`` is the current stream, and so allocates
-    the outputs; the allocator learns that it uses the inputs."""
+def _on(stream, cache, tensors=()):
+    """A context in which ``stream``, of the cache's device, is the current
+    stream, and so allocates the outputs; the allocator learns that it uses
+    ``tensors``."""
+    if isinstance(cache["k"], torch.Tensor) and cache["k"].device != stream.device:
+        raise ValueError(f"stream must be on the cache's device {cache['k'].device} (got {stream.device})")
     for t in tensors:
         if isinstance(t, torch.Tensor) and t.is_cuda:
             t.record_stream(stream)
@@ -105,7 +108,7 @@ def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, block_table: torch.
     rotated queries (``q_out``, which may be q itself), or None without q.
     """
     if stream is not None:
-        with _on(stream, (*cache.values(), k, v, q, q_out, cos, sin, block_table, seq_lens, cu_q)):
+        with _on(stream, cache, (*cache.values(), k, v, q, q_out, cos, sin, block_table, seq_lens, cu_q)):
             return kv_append(cache, k, v, block_table, seq_lens, cu_q, q=q, cos=cos, sin=sin, interleaved=interleaved,
                              q_out=q_out)
     return (_module or _load()).append(cache["k"], cache["v"], cache["k_scale"], cache["v_scale"], k, v, block_table,
@@ -121,7 +124,7 @@ def kv_workspace_for(cache: dict, q_heads: int, B: int, T: int, stream=None) -> 
     another stream or in a graph, a buffer is shared with this stream's own
     calls, and kept alive by whoever holds it."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, cache):
             return kv_workspace_for(cache, q_heads, B, T)
     return (_module or _load()).workspace(cache["k"], cache["v"], cache["k_scale"], cache["v_scale"], q_heads, B, T)
 
@@ -138,7 +141,7 @@ def kv_attend(q: torch.Tensor, cache: dict, block_table: torch.Tensor, seq_lens:
     may supply them.
     """
     if stream is not None:
-        with _on(stream, (*cache.values(), q, out, lse, block_table, seq_lens, cu_q, workspace)):
+        with _on(stream, cache, (*cache.values(), q, out, lse, block_table, seq_lens, cu_q, workspace)):
             return kv_attend(q, cache, block_table, seq_lens, cu_q, softmax_scale=softmax_scale, out=out, lse=lse,
                              return_lse=return_lse, workspace=workspace)
     out, lse = (_module or _load()).attend(q, cache["k"], cache["v"], cache["k_scale"], cache["v_scale"], block_table,

@@ -354,3 +354,18 @@ def test_a_warps_segments_are_handed_over_in_order(tmp_path):
                     "-pthread"], check=True)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_a_stream_of_another_device_is_refused(lib):
+    """The calls run on the given stream or not at all: not on the current stream of the cache's device instead."""
+    class Other:
+        device, cuda_stream = torch.device("cuda", 1), 0
+    c = _cpu_cache()
+    x = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    table, lens = torch.zeros(1, 1, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="stream"):
+        mhc.kv_append(c, x, x, table, lens, stream=Other())
+    with pytest.raises(ValueError, match="stream"):
+        mhc.kv_attend(x, c, table, lens, stream=Other())
+    with pytest.raises(ValueError, match="stream"):
+        mhc.kv_workspace_for(c, 2, 1, 1, Other())
