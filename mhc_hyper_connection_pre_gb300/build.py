@@ -62,19 +62,34 @@ def _run(cmd: list, what: str) -> None:
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
+def _binding_made_for() -> str:
+    """What the kv binding's object code depends on beside its sources: the
+    interpreter, PyTorch and the toolkit whose headers it was compiled with."""
+    import torch
+    return "\n".join([sys.version, str(sysconfig.get_config_var("SOABI")), torch.__version__, str(torch.version.git_version),
+                      os.path.dirname(torch.__file__), _nvcc()]) + "\n"
+
+
 def _compile_binding() -> str:
     """The object of the kv binding, for the running interpreter and PyTorch."""
     import torch
     src, obj = os.path.join(CSRC, "kv_binding.cpp"), os.path.join(BUILD, "kv_binding.cpp.o")
+    made_for, stamp = _binding_made_for(), obj + ".made_for"
     if os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(src), _newest_dep_mtime()):
-        return obj
+        if os.path.exists(stamp) and open(stamp).read() == made_for:
+            return obj
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     dirs = [INCLUDE, inc, os.path.join(inc, "torch", "csrc", "api", "include"), cuda, sysconfig.get_paths()["include"]]
     abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
     _run(["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *[f"-I{d}" for d in dirs], "-c", src,
           "-o", obj + ".tmp"], "g++ for kv_binding.cpp")
+    for old in (stamp, BINDING):              # nothing of the old object stays beside the new one
+        if os.path.exists(old):
+            os.remove(old)
     os.replace(obj + ".tmp", obj)
+    with open(stamp, "w") as f:
+        f.write(made_for)
     return obj
 
 

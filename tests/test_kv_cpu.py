@@ -369,3 +369,25 @@ def test_a_stream_of_another_device_is_refused(lib):
         mhc.kv_attend(x, c, table, lens, stream=Other())
     with pytest.raises(ValueError, match="stream"):
         mhc.kv_workspace_for(c, 2, 1, 1, Other())
+
+
+def test_the_binding_is_built_anew_for_another_pytorch(tmp_path, monkeypatch):
+    """An object compiled for another PyTorch or interpreter is not linked, however new it is."""
+    ran = []
+
+    def run(cmd, what):
+        ran.append(what)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+    monkeypatch.setattr(mbuild, "BUILD", str(tmp_path))
+    monkeypatch.setattr(mbuild, "BINDING", str(tmp_path / "_mhc_kv.so"))
+    monkeypatch.setattr(mbuild, "_run", run)
+
+    def built():
+        ran.clear()
+        mbuild._link_binding(mbuild._compile_binding())
+        return len(ran)
+    assert built() == 2 and built() == 0
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert built() == 2 and built() == 0
+    monkeypatch.setattr(mbuild.sys, "version", "another interpreter")
+    assert built() == 2 and built() == 0
