@@ -26,8 +26,8 @@ extern "C" {
  * mantissa bits, no infinity, NaN = 0x7f / 0xff), dense
  * [num_pages][heads][page_tokens][head_dim]; a stored number stands for
  * code * scale[page][head].  k and v are 16-byte aligned, the scales 4-byte.
-Scales are finite and not negative; those of pages that mhc_kv_append goes on
-with are powers of two, as it writes them (mhc_kv_attend takes any).
+ * Scales are finite and not negative; those of pages that mhc_kv_append goes on
+ * with are powers of two, as it writes them (mhc_kv_attend takes any).
  * page_tokens is 16, 32, 64 or 128; head_dim 64 or 128; num_pages * heads
  * at most 2^31 - 1.
  */
@@ -114,6 +114,11 @@ mhc_status mhc_kv_append(const mhc_kv_cache *cache, const uint16_t *k, int64_t k
  * A token that sees no key gets out = 0 and lse = -infinity.  A key after p
  * never reaches the output, whatever its bytes stand for.  A query that holds
  * an infinity or NaN gives NaN in out and lse if it sees a key.
+ *
+ * Values are held relative to the largest value scale among the sequence's keys
+ * up to p, whatever those keys weigh: where other pages' scales are smaller by
+ * 2^20 or more, each key adds an error of up to 2^-26 times that largest scale
+ * to that of out's rounding.
  *
  *  q          bf16 as in mhc_kv_append (already rotated)
  *  q_heads    a multiple of cache->heads, at most 128 times as many

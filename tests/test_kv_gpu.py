@@ -833,3 +833,32 @@ def test_attend_largest_values(kind, case):
     got, of = _attend(case, 610, fill=fill)
     check_attend(got, *of)
     assert got["out"].isfinite().all()
+
+
+@pytest.mark.parametrize("case", [(128, 16, 2, 4, None, [70, 30]), (64, 16, 2, 32, None, [3000]), (128, 16, 1, 5, [30], [400]),
+                                  (64, 32, 1, 40, [3, 7], [3001, 100]), (128, 32, 1, 50, [3], [5000])])
+@pytest.mark.parametrize("apart", [12, 20, 28])
+def test_attend_small_values_beside_unseen_large_ones(apart, case):
+    """Pages whose values are smaller by 2^apart have all of the weight: each
+    key may add 2^-26 times the largest value scale to the usual bounds (a
+    weight below f16's normal numbers is off by 2^-35 of one, a code is at
+    most 448)."""
+    D, P, H, Hq, counts, lens = case
+
+    def fill(q, cache, rows):
+        q.fill_(1.0)
+        for r, n in zip(rows, lens):
+            for i, p in enumerate(r):
+                if p >= 0 and i % 3 == 1:
+                    cache["v_scale"][p], cache["k_scale"][p] = 1.0, 1.0
+                    cache["k"].view(torch.uint8)[p] = 0xC8             # -4: logits of -256 and less
+                elif p >= 0:
+                    cache["v_scale"][p], cache["k_scale"][p] = 2.0 ** -apart, 2.0 ** -8
+            if n % P:
+                for c in ("k", "v"):
+                    cache[c].view(torch.uint8)[r[n // P], :, n % P:] = 0x7F
+    got, of = _attend(case, 620, fill=fill)
+    out, lse, tol, tol_lse = attend(*of)
+    o, l = got["out"].double(), got["lse"].double()
+    assert ((o - out).abs() <= tol + max(lens) * 2.0 ** -26).all()
+    assert ((l - lse).abs() <= tol_lse).all()
