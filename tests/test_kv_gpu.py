@@ -862,3 +862,26 @@ def test_attend_small_values_beside_unseen_large_ones(apart, case):
     o, l = got["out"].double(), got["lse"].double()
     assert ((o - out).abs() <= tol + max(lens) * 2.0 ** -26).all()
     assert ((l - lse).abs() <= tol_lse).all()
+
+
+# ---------------------------------------------------------- mixed batches ---
+
+@pytest.mark.parametrize("D,P,H,Hq,prompt,tokens", [(128, 64, 2, 10, 300, 40), (64, 16, 1, 8, 700, 7), (128, 16, 2, 4, 90, 300),
+                                                    (64, 32, 2, 2, 257, 100)])
+def test_prompt_beside_tokens(D, P, H, Hq, prompt, tokens):
+    """A prompt's chunk and many single tokens in one call, some places empty:
+    appended and attended to as in calls of their own."""
+    counts = [1] * tokens
+    counts[tokens // 2] = prompt
+    lens = [max(n, (i * 37) % 150) for i, n in enumerate(counts)]
+    lens[tokens // 2] += 100
+    lens[0] = counts[0] = 0
+    rows, pages = _tables(lens, P, 15)
+    cu = _cu(counts)
+    q, k, v, cos, sin = _append_inputs(cu[-1], H, Hq, D, D, True, 15, max(lens))
+    cache = _random_cache(pages, H, P, D, 15)
+    before = _cpu({n: t.clone() for n, t in cache.items()})
+    q_out = mhc.kv_append(cache, k, v, _i32(rows), _i32(lens), _i32(cu), q=q, cos=cos, sin=sin)
+    check_append(before, _cpu(cache), k.cpu(), v.cpu(), rows, lens, cu, cos.cpu(), sin.cpu(), False, q.cpu(), q_out.cpu())
+    got = mhc.kv_attend(q_out, cache, _i32(rows), _i32(lens), _i32(cu), return_lse=True)
+    check_attend(got, q_out, cache, rows, lens, cu, D ** -0.5)
