@@ -115,10 +115,10 @@ mhc_status mhc_kv_append(const mhc_kv_cache *cache, const uint16_t *k, int64_t k
  * never reaches the output, whatever its bytes stand for.  A query that holds
  * an infinity or NaN gives NaN in out and lse if it sees a key.
  *
- * Values are held relative to the largest value scale among the sequence's keys
- * up to p, whatever those keys weigh: where other pages' scales are smaller by
- * 2^20 or more, each key adds an error of up to 2^-26 times that largest scale
- * to that of out's rounding.
+ * Accuracy.  With p_j = exp(s_j - lse), out is off by its own rounding, 2^-10
+ * of sum_j p_j |v_j| (as the weights are f16 numbers), and for each key 2^-26 of
+ * the largest value scale among the sequence's keys up to p, whatever that key
+ * weighs (f16's range); a logit by 2^-20 of sum_i |q_i k_i| softmax_scale.
  *
  *  q          bf16 as in mhc_kv_append (already rotated)
  *  q_heads    a multiple of cache->heads, at most 128 times as many

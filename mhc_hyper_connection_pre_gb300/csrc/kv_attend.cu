@@ -158,7 +158,7 @@ __device__ __forceinline__ void piece(bool full, uint32_t ks, uint32_t vs, const
                 x[3] = n1 > 24 ? x[3] : -INFINITY;
             }
             top[nb][e] = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-            grow = grow || top[nb][e] > acc.m[nb][e] + kGrow;
+            grow = grow || top[nb][e] - acc.m[nb][e] > kGrow;
             s[0][nb][e] = x[0]; s[0][nb][e + 2] = x[1]; s[1][nb][e] = x[2]; s[1][nb][e + 2] = x[3];
         }
     }
@@ -201,12 +201,12 @@ __device__ __forceinline__ void piece(bool full, uint32_t ks, uint32_t vs, const
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float m = acc.m[nb][e], zero = m == -INFINITY ? 0.0f : m - kLift;
+            const float zero = zero_of(acc.m[nb][e]);
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float& x = s[i / 2][nb][e + 2 * (i & 1)];
-                x = ex2(x - zero);
+                x = ex2(__fsub_rn(x, zero));      // of the rounded logit, as the maximum is
                 sum += x;
             }
             acc.l[nb][e] += sum;
@@ -525,12 +525,12 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
                     for (int j = 0; j < D / 64; ++j)
                         out[j] = make_uint4(pack_bf16x2(y[8 * j], y[8 * j + 1]), pack_bf16x2(y[8 * j + 2], y[8 * j + 3]),
                                             pack_bf16x2(y[8 * j + 4], y[8 * j + 5]), pack_bf16x2(y[8 * j + 6], y[8 * j + 7]));
-                    if (g == 0 && a.lse) a.lse[to] = lse_of(m, l);
+                    if (g == 0 && a.lse) a.lse[to] = lse_of(zero_of(m), l);
                 } else {
                     float4* out = reinterpret_cast<float4*>(part + r * D + g * (D / 8));
 #pragma unroll
                     for (int j = 0; j < D / 32; ++j) out[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-                    if (g == 0) part[kRows * D + r] = weight_of(m, l);
+                    if (g == 0) part[kRows * D + r] = weight_of(zero_of(m), l);
                 }
             }
         }

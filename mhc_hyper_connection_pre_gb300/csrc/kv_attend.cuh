@@ -228,12 +228,14 @@ __device__ __forceinline__ int64_t place_of(const AttendArgs& a, const Segment& 
     return (int64_t)token * (a.cut.heads * a.cut.group) + s.head * a.cut.group + in_group;
 }
 
-// What a part weighs, in powers of two.
-__device__ __forceinline__ float weight_of(float m, float l) { return l == 0.0f ? -INFINITY : m + __log2f(l); }
+// The logit (in powers of two) that has a weight of one: kLift below the maximum
+// m, or less where fp32's steps are larger, but never more, as weights have to
+// stay within f16.
+__device__ __forceinline__ float zero_of(float m) { return m == -INFINITY ? 0.0f : __fadd_ru(m, -kLift); }
 
-__device__ __forceinline__ float lse_of(float m, float l) {
-    return l == 0.0f ? -INFINITY : kLn2 * (m - kLift + __log2f(l));
-}
+// The logarithm, in powers of two, of the weights' sum l.
+__device__ __forceinline__ float weight_of(float zero, float l) { return l == 0.0f ? -INFINITY : zero + __log2f(l); }
+__device__ __forceinline__ float lse_of(float zero, float l) { return kLn2 * weight_of(zero, l); }
 
 using PFN_encodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                      const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,

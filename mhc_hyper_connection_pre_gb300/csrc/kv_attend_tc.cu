@@ -179,17 +179,6 @@ struct Ring {
     }
 };
 
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-
 // The bits of keys at .. at + 31 of a step that the row sees: those before the
 // n-th, in blocks of 16 that have a page.
 __device__ __forceinline__ uint32_t seen_bits(int at, int n, uint32_t valid) {
@@ -206,8 +195,28 @@ __device__ __forceinline__ float factor(const Meta& meta, int block, float f) {
     return fmaxf(f * meta.scale[block], 1e-37f);
 }
 
-// The largest of 32 logits: scales are not negative, so the largest product
-// times the factor.
+// 32 products of a row as logits in powers of two, each rounded, as the maximum
+// is: one operation for product and difference would leave an exponent's
+// argument above the maximum's by a rounding, and of sharp logits that may be
+// any size.
+__device__ __forceinline__ void logits(uint32_t (&s)[32], int at, const Meta& meta, float f) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float x = factor(meta, at / 16 + h, f);
+        const f32x2 xx = make_f32x2(x, x);
+#pragma unroll
+        for (int i = 16 * h; i < 16 * h + 16; i += 2) {
+            float a, b;
+            split_f32x2(mul_rn2(make_f32x2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), xx), a, b);
+            s[i] = __float_as_uint(a);
+            s[i + 1] = __float_as_uint(b);
+        }
+    }
+}
+
+// The largest of 32 logits, from the products: scales are not negative, and
+// rounding keeps the order.  (From the logits, after their products, it took the
+// chunk of the header from 918 to 943 us, as it then waits for them; this way 920.)
 __device__ __forceinline__ float row_max(const uint32_t (&s)[32], int at, const Meta& meta, float f) {
     float top = -INFINITY;
 #pragma unroll
@@ -215,28 +224,22 @@ __device__ __forceinline__ float row_max(const uint32_t (&s)[32], int at, const 
         float m = __uint_as_float(s[16 * h]);
 #pragma unroll
         for (int i = 1; i < 16; ++i) m = fmaxf(m, __uint_as_float(s[16 * h + i]));
-        top = fmaxf(top, m * factor(meta, at / 16 + h, f));
+        top = fmaxf(top, __fmul_rn(m, factor(meta, at / 16 + h, f)));
     }
     return top;
 }
 
 // 32 weights of a row, as 16 pairs of f16, added to the row's two sums.
-__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t (&p)[16], int at, const Meta& meta, float f,
-                                        float zero, f32x2& sum) {
+__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t (&p)[16], float zero, f32x2& sum) {
     const f32x2 z = make_f32x2(-zero, -zero);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const float x = factor(meta, at / 16 + h, f);
-        const f32x2 xx = make_f32x2(x, x);
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            float a, b;
-            split_f32x2(fma2(make_f32x2(__uint_as_float(s[16 * h + i]), __uint_as_float(s[16 * h + i + 1])), xx, z), a, b);
-            a = ex2(a);
-            b = ex2(b);
-            sum = add2(sum, make_f32x2(a, b));
-            p[8 * h + i / 2] = pack_f16x2(a, b);
-        }
+    for (int i = 0; i < 32; i += 2) {
+        float a, b;
+        split_f32x2(add_rn2(make_f32x2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), z), a, b);
+        a = ex2(a);
+        b = ex2(b);
+        sum = add_rn2(sum, make_f32x2(a, b));
+        p[i / 2] = pack_f16x2(a, b);
     }
 }
 
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int n = lim - key;  // keys of this step that the row sees
                     const uint32_t valid = meta.valid >> (half / 16);
                     const uint32_t from = lanes + col_s(x, buffer);
-                    // the row's 64 products: their largest, the weights and their sum
+                    // the row's 64 products: their largest, the logits, the weights and their sum
                     uint32_t s[2][32];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) tmem_ld32(from + c * 32, s[c]);
@@ -435,7 +438,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const float top = fmaxf(row_max(s[0], half, meta, f), row_max(s[1], half + 32, meta, f));
-                    const bool grow = top > m + kGrow;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) logits(s[c], half + c * 32, meta, f);
+                    const bool grow = top - m > kGrow;
                     if (__any_sync(0xffffffffu, grow)) {
                         const float keep = grow ? ex2(m - top) : 1.0f;
                         m = grow ? top : m;
@@ -458,12 +463,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    const float zero = m == -INFINITY ? 0.0f : m - kLift;
+                    const float zero = zero_of(m);
                     f32x2 sum = make_f32x2(0.0f, 0.0f);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t p[16];
-                        weights(s[c], p, half + c * 32, meta, f, zero, sum);
+                        weights(s[c], p, zero, sum);
                         tmem_st16(from + c * 16, p);
                     }
                     float sum0, sum1;
@@ -528,8 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint64_t to = 0;
                 if (mine < rows) {
                     to = whole ? reinterpret_cast<uint64_t>(a.out + at * D) : reinterpret_cast<uint64_t>(part + mine * D);
-                    if (whole && a.lse) a.lse[at] = lse_of(m, l);
-                    if (!whole) part[kPair * D + mine] = weight_of(m, l);
+                    if (whole && a.lse) a.lse[at] = lse_of(zero_of(m), l);
+                    if (!whole) part[kPair * D + mine] = weight_of(zero_of(m), l);
                 }
                 auto staged = [&](int r, int c) {             // 16-byte chunk c of row r of the warp
                     const uint32_t row = D == 128 ? smem_u32(sm.q[x][0]) + (warp % 4) * 4096 + r * 128

@@ -885,3 +885,38 @@ def test_prompt_beside_tokens(D, P, H, Hq, prompt, tokens):
     check_append(before, _cpu(cache), k.cpu(), v.cpu(), rows, lens, cu, cos.cpu(), sin.cpu(), False, q.cpu(), q_out.cpu())
     got = mhc.kv_attend(q_out, cache, _i32(rows), _i32(lens), _i32(cu), return_lse=True)
     check_attend(got, q_out, cache, rows, lens, cu, D ** -0.5)
+
+
+# ------------------------------------------------------------ sharp softmax ---
+
+@pytest.mark.parametrize("case", [(64, 16, 1, 3, None, [70, 900]), (128, 64, 2, 4, None, [5000]), (64, 32, 2, 32, None, [300, 64]),
+                                  (128, 16, 1, 16, None, [2000]), (64, 32, 1, 40, [3, 7], [3001, 100]),
+                                  (128, 32, 2, 10, [200, 9], [400, 30])])
+@pytest.mark.parametrize("scale,q_log2,k_log2", [(None, 0, 20), (1e7, 0, 0), (1e18, 0, 0), (None, 40, 0), (1e7, 20, -20), (3.0, 0, 60)])
+def test_attend_sharp_logits(case, scale, q_log2, k_log2):
+    """Logits of 2^23 to 2^70, where one step of fp32 is a logit's whole
+    difference: the key with the largest, or, within a few steps of fp32 of
+    it, a mean of such keys."""
+    D, P, H, Hq, counts, lens = case
+
+    def fill(q, cache, rows):
+        q *= 2.0 ** q_log2
+        cache["k_scale"].mul_(2.0 ** (k_log2 + 4))
+    got, (q, cache, rows, lens, cu, s) = _attend(case, 630, scale, fill=fill)
+    assert got["out"].isfinite().all()
+    check_attend(got, q, cache, rows, lens, cu, float(torch.tensor(s, dtype=torch.float32)))
+    T, G = q.shape[0], Hq // H
+    clear = 0
+    for b, (n, t0, t1) in enumerate(zip(lens, cu or range(T), cu[1:] if cu else range(1, T + 1))):
+        pages = torch.tensor(rows[b][:-(-n // P)], device="cuda")
+        for t in range(t0, t1):
+            for h in range(Hq):
+                k, v = (cache[c][pages, h // G].double().mul(cache[c + "_scale"][pages, h // G].double()[:, None, None])
+                        .reshape(-1, D)[:n - (t1 - 1 - t)] for c in ("k", "v"))
+                x = k @ q[t, h].double() * s
+                two = x.topk(min(2, len(x))).values
+                off = 2.0 ** -18 * (k.abs() @ q[t, h].double().abs() * s).max()
+                if len(two) == 1 or two[0] - two[1] > 2 * off + 40:             # beyond rounding: the one key's values
+                    clear += 1
+                    assert ((got["out"][t, h].double() - v[x.argmax()]).abs() <= 2.0 ** -8 * v[x.argmax()].abs()).all()
+    assert clear > 0
