@@ -152,7 +152,9 @@ const char* mhc_status_string(mhc_status s) {
     switch (s) {
         case MHC_OK: return "MHC_OK";
         case MHC_ERR_INVALID_ARGUMENT: return "MHC_ERR_INVALID_ARGUMENT: null, misaligned or overlapping pointer, or bad count";
-        case MHC_ERR_UNSUPPORTED: return "MHC_ERR_UNSUPPORTED: shape this library does not handle (n must be 4, C a multiple of 8 up to 6144)";
+        case MHC_ERR_UNSUPPORTED: return "MHC_ERR_UNSUPPORTED: shape this library does not handle (seam: n = 4, C a multiple of 8 "
+                                         "up to 6144; cache: head_dim 64 or 128, page_tokens 16, 32, 64 or 128, rotary_dim a "
+                                         "multiple of 16, up to 128 query heads to a key head)";
         case MHC_ERR_CUDA: return "MHC_ERR_CUDA: a CUDA runtime call or kernel launch failed";
         case MHC_ERR_TIMEOUT: return "MHC_ERR_TIMEOUT: a bounded device-side wait gave up";
         case MHC_ERR_INDEX: return "MHC_ERR_INDEX: a length, page number or token offset read on the device is out of range";

@@ -391,3 +391,9 @@ def test_the_binding_is_built_anew_for_another_pytorch(tmp_path, monkeypatch):
     assert built() == 2 and built() == 0
     monkeypatch.setattr(mbuild.sys, "version", "another interpreter")
     assert built() == 2 and built() == 0
+
+
+def test_status_string_of_an_unsupported_shape(lib):
+    """It names the cache's limits as well as the seam's."""
+    text = lib.mhc_status_string(2).decode()
+    assert all(w in text for w in ("C a multiple of 8", "head_dim", "page_tokens", "rotary_dim", "query heads"))
