@@ -525,12 +525,12 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
                     for (int j = 0; j < D / 64; ++j)
                         out[j] = make_uint4(pack_bf16x2(y[8 * j], y[8 * j + 1]), pack_bf16x2(y[8 * j + 2], y[8 * j + 3]),
                                             pack_bf16x2(y[8 * j + 4], y[8 * j + 5]), pack_bf16x2(y[8 * j + 6], y[8 * j + 7]));
-                    if (g == 0 && a.lse) a.lse[to] = lse_of(zero_of(m), l);
+                    if (g == 0 && a.lse) a.lse[to] = kLn2 * log_sum(m, l);
                 } else {
                     float4* out = reinterpret_cast<float4*>(part + r * D + g * (D / 8));
 #pragma unroll
                     for (int j = 0; j < D / 32; ++j) out[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-                    if (g == 0) part[kRows * D + r] = weight_of(zero_of(m), l);
+                    if (g == 0) part[kRows * D + r] = log_sum(m, l);
                 }
             }
         }
@@ -545,6 +545,11 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
         from = from + 1 == kStages ? 0 : from + 1;
         phase ^= from == 0;
     }
+}
+
+// Of the largest part's logarithm m and the sum l of 2^(part's - m - kPartsLog2).
+__device__ __forceinline__ float join_lse(float m, float l) {
+    return l == 0.0f ? -INFINITY : kLn2 * (m + __log2f(l * exp2f(kPartsLog2)));
 }
 
 // Joins the tiles that borders between shares have cut.  A part holds its own
@@ -623,7 +628,7 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
                 *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o[0] * by, o[1] * by), pack_bf16x2(o[2] * by, o[3] * by));
             else
                 *out = pack_bf16x2(o[0] * by, o[1] * by);
-            if (lane == 0 && a.lse) a.lse[to] = lse_of(m + kPartsLog2, l);
+            if (lane == 0 && a.lse) a.lse[to] = join_lse(m, l);
         }
         return;
     }
@@ -689,7 +694,7 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
             uint32_t* out = reinterpret_cast<uint32_t*>(a.out + to * D + lane * kDims);
             out[0] = pack_bf16x2(o[0] * by, o[1] * by);
             if constexpr (D == 128) out[1] = pack_bf16x2(o[2] * by, o[3] * by);
-            if (lane == 0 && a.lse) a.lse[to] = lse_of(m + kPartsLog2, l);
+            if (lane == 0 && a.lse) a.lse[to] = join_lse(m, l);
             continue;
         }
 #pragma unroll
@@ -712,7 +717,7 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
             const int64_t to = place_of(a, seg, r);
             const float by = total == 0.0f ? 0.0f : __frcp_rn(total);
             reinterpret_cast<uint32_t*>(a.out + to * D)[threadIdx.x] = pack_bf16x2(x * by, y * by);
-            if (threadIdx.x == 0 && a.lse) a.lse[to] = lse_of(top + kPartsLog2, total);
+            if (threadIdx.x == 0 && a.lse) a.lse[to] = join_lse(top, total);
         }
         __syncthreads();
     }

@@ -233,9 +233,12 @@ __device__ __forceinline__ int64_t place_of(const AttendArgs& a, const Segment& 
 // stay within f16.
 __device__ __forceinline__ float zero_of(float m) { return m == -INFINITY ? 0.0f : __fadd_ru(m, -kLift); }
 
-// The logarithm, in powers of two, of the weights' sum l.
-__device__ __forceinline__ float weight_of(float zero, float l) { return l == 0.0f ? -INFINITY : zero + __log2f(l); }
-__device__ __forceinline__ float lse_of(float zero, float l) { return kLn2 * weight_of(zero, l); }
+// The logarithm, in powers of two, of the numerators' sum: the maximum m and
+// the sum l of 2^(logit - zero_of(m)).  m comes in last, so that a small result
+// is not rounded in steps of the lift's size.
+__device__ __forceinline__ float log_sum(float m, float l) {
+    return l == 0.0f ? -INFINITY : m + (__log2f(l * exp2f(-kLift)) + (kLift - (m - zero_of(m))));
+}
 
 using PFN_encodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                      const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,

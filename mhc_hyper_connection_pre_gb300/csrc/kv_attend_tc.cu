@@ -533,8 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint64_t to = 0;
                 if (mine < rows) {
                     to = whole ? reinterpret_cast<uint64_t>(a.out + at * D) : reinterpret_cast<uint64_t>(part + mine * D);
-                    if (whole && a.lse) a.lse[at] = lse_of(zero_of(m), l);
-                    if (!whole) part[kPair * D + mine] = weight_of(zero_of(m), l);
+                    if (whole && a.lse) a.lse[at] = kLn2 * log_sum(m, l);
+                    if (!whole) part[kPair * D + mine] = log_sum(m, l);
                 }
                 auto staged = [&](int r, int c) {             // 16-byte chunk c of row r of the warp
                     const uint32_t row = D == 128 ? smem_u32(sm.q[x][0]) + (warp % 4) * 4096 + r * 128
