@@ -10,7 +10,10 @@
 // reads its numbers twice, the second time from the L1 cache: held in registers
 // between the passes they left half as many threads on an SM, and the loads of
 // a long prompt took 1.5 times as long.  16384 tokens of 40 query and 8 key
-// heads take 83 us: 445 MB at 5.4 TB/s (the queries alone 6.0 TB/s).
+// heads take 82 us: 445 MB at 5.4 TB/s (the queries alone 6.0 TB/s).  The forms
+// for many tokens that rotate spill 56 to 84 bytes a thread at the 64 registers
+// of four blocks an SM: cos, sin and both numbers of eight pairs are alive at once
+// beside the next step's loads.
 #include <cuda_runtime.h>
 
 #include "kv_common.cuh"
@@ -339,8 +342,13 @@ cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code,
     a.q_heads = q_heads;
     a.cos = cos; a.sin = sin;
     a.rope_rows = rope_rows; a.R = R;
-    // Few new tokens a sequence: a warp for each token that may start a run.
-    // Many: one to four warps for each window of as many tokens as a page has.
+    // Few new tokens a sequence on average: a warp for each token that may start a
+    // run.  Many: one to four warps for each window of as many tokens as a page
+    // has.  Like tile_rows for attend, this takes the sequences to be alike: a
+    // window of single tokens is as many runs one after the other.  A prompt of
+    // 2048 tokens beside 127 single ones takes 118 us (40 / 8 heads of 128; 14.5 and
+    // 3.7 in calls of their own), one of 1000 beside 255, a warp a page, 27.5
+    // (11.4 and 5.0).
     const bool few = seqs.T < 8 * (int64_t)seqs.B;
     a.window = few ? 1 : 1 << seqs.page_log2;
     a.windows = (seqs.T + a.window - 1) / a.window;

@@ -13,8 +13,10 @@
 // for the second product (2^-11 of each, well below the output's own bf16
 // rounding) after a factor of 2^10 that keeps small weights out of f16's
 // subnormal range.  The maximum follows only when a logit is more than 2^5 above
-// it, so weights reach 2^15.  A page's value scale multiplies the weights,
-// relative to the largest scale met so far, so that they get no larger.
+// it, so weights reach 2^15; logits are rounded before the maximum is taken off,
+// so that this holds for sharp ones too.  A page's value scale multiplies the
+// weights, relative to the largest scale met so far, so that they get no larger
+// (a weight in f16's subnormal range is off by 2^-35 of the row's largest).
 //
 // What bounds it: the cache is read once, 2 * head_dim bytes a key and head
 // for 4 * head_dim * group operations, far below the matrix rate for groups up
@@ -511,7 +513,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
                 const int r = nb * 8 + 2 * t + e;
                 if (r >= seg.rows) continue;
                 // one after the other: their product may be too small for fp32
-                const float by = l == 0.0f ? 0.0f : __frcp_rn(l);
+                const float by = l == 0.0f ? 0.0f : rcp(l);
                 float y[D / 8];
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
 
 // Of the largest part's logarithm m and the sum l of 2^(part's - m - kPartsLog2).
 __device__ __forceinline__ float join_lse(float m, float l) {
-    return l == 0.0f ? -INFINITY : kLn2 * (m + __log2f(l * exp2f(kPartsLog2)));
+    return l == 0.0f ? -INFINITY : kLn2 * (m + lg2(l * exp2f(kPartsLog2)));
 }
 
 // Joins the tiles that borders between shares have cut.  A part holds its own
@@ -622,7 +624,7 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
                 }
             }
             const int64_t to = place_of(a, seg, r);
-            const float by = l == 0.0f ? 0.0f : __frcp_rn(l);
+            const float by = l == 0.0f ? 0.0f : rcp(l);
             uint32_t* out = reinterpret_cast<uint32_t*>(a.out + to * D + lane * kDims);
             if constexpr (D == 128)
                 *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o[0] * by, o[1] * by), pack_bf16x2(o[2] * by, o[3] * by));
@@ -690,7 +692,7 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
         }
         if (parts < kMany) {
             const int64_t to = place_of(a, seg, r);
-            const float by = l == 0.0f ? 0.0f : __frcp_rn(l);
+            const float by = l == 0.0f ? 0.0f : rcp(l);
             uint32_t* out = reinterpret_cast<uint32_t*>(a.out + to * D + lane * kDims);
             out[0] = pack_bf16x2(o[0] * by, o[1] * by);
             if constexpr (D == 128) out[1] = pack_bf16x2(o[2] * by, o[3] * by);
@@ -715,7 +717,7 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
                 y = fmaf(by, v.y, y);
             }
             const int64_t to = place_of(a, seg, r);
-            const float by = total == 0.0f ? 0.0f : __frcp_rn(total);
+            const float by = total == 0.0f ? 0.0f : rcp(total);
             reinterpret_cast<uint32_t*>(a.out + to * D)[threadIdx.x] = pack_bf16x2(x * by, y * by);
             if (threadIdx.x == 0 && a.lse) a.lse[to] = join_lse(top, total);
         }
@@ -725,7 +727,13 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
 
 // Rows of a tile: 8 or 16 for the warps of this file, 256 for the
 // tensor-memory kernel, whose tiles cost more beside their keys.  On average B
-// sequences have T * group / B rows, and a tile reads all their keys.  Measured
+// sequences have T * group / B rows, and a tile reads all their keys.  The rule
+// takes the sequences to be alike.  Where they are not, one kernel runs for all of
+// them all the same: a prompt of 2048 tokens over 4096 keys beside 127 tokens over
+// 4000 keys takes 559 us (40 / 8 heads of 128; 137 and 177 in calls of their own),
+// a prompt of 2700 beside 512 tokens over 1000 keys, here in tiles of 16 rows, 740
+// (108 and 192), a prompt of 1000 in a batch of 256 places without other tokens 140
+// (40 in a batch of one).  Measured on batches of like sequences
 // (us; 8 key heads; 256 sequences of up to 300 keys | 64 of up to 2000 | 64 of
 // 4096 | 1 of 32768):
 //    rows   head_dim 128: 16, 256                           head_dim 64: 16, 256

@@ -56,6 +56,18 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// To within a step or two of fp32, for normal numbers.
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -237,7 +249,7 @@ __device__ __forceinline__ float zero_of(float m) { return m == -INFINITY ? 0.0f
 // the sum l of 2^(logit - zero_of(m)).  m comes in last, so that a small result
 // is not rounded in steps of the lift's size.
 __device__ __forceinline__ float log_sum(float m, float l) {
-    return l == 0.0f ? -INFINITY : m + (__log2f(l * exp2f(-kLift)) + (kLift - (m - zero_of(m))));
+    return l == 0.0f ? -INFINITY : m + (lg2(l * exp2f(-kLift)) + (kLift - (m - zero_of(m))));
 }
 
 using PFN_encodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

@@ -15,13 +15,16 @@
 //     largest.  (lo in e4m3 lost up to 2^-17 of it, from 2^-10 on.)  S = hi K +
 //     lo K costs as much tensor time as one f16 product and needs no conversion
 //     of K.
-//   * V becomes f16 on the way (exactly, times its page's scale over the
-//     largest scale of the segment, times 2^7), because the weights need
-//     more than e4m3's 4 bits: they are f16, 2^10 times the softmax's
-//     numerators, so that small weights stay out of f16's subnormals.
+//   * V becomes f16 on the way (times its page's scale over the largest scale of
+//     the segment, times 2^7: exactly for scales that are powers of two, down to
+//     f16's 2^-24, with one rounding for others), because the weights need more
+//     than e4m3's 4 bits: they are f16, 2^10 times the softmax's numerators, so
+//     that small weights stay out of f16's subnormals.
 //   * The running maximum follows only when it has grown by more than 2^5
 //     (weights then reach 2^15, within f16), so that O, in tensor memory, is
-//     rescaled rarely; sums are fp32 and of the unrounded weights.
+//     rescaled rarely; sums are fp32 and of the unrounded weights.  Logits are
+//     rounded before the maximum is taken off, so that this bound holds however
+//     large fp32's steps are at the logits' size.
 //
 // Up to 128 rows are one tile; both of a block's tiles then take it, each half
 // of every load's keys, and their results are joined as the rows go out: 48 rows
@@ -34,10 +37,14 @@
 // run during the softmax of this one; the two tiles share loads and conversion.
 // With one buffer (128 keys a step) each softmax waited for P V and Q K^T of its
 // own tile: 1272 us for a chunk of 4096 tokens over 16384 keys, 40 heads; now
-// 930.  A step of both tiles takes about 2000 cycles, of which the tensor cores
-// work 1280: their warps' instructions between the products (waits and
-// addresses, 10 cycles each among the softmax's) and the softmax's own chain
-// take the rest, about evenly.  A tile's queries, its first and last steps and
+// 920.  A step of both tiles takes about 1900 cycles at head_dim 128.  At the
+// tensor cores' rate its products are 1024, which is what their counter shows
+// (50% of the time).  S keeps them for longer than that: one product of 64 keys
+// by 32 dims is 32 cycles, but reads 4 KB of queries and 2 KB of keys from shared
+// memory, 48 cycles at 128 bytes a cycle, so that all products are 1280.  The
+// tensor warps' instructions between the products (waits and addresses, 10
+// cycles each among the softmax's) and the softmax's own chain take the rest,
+// about evenly.  A tile's queries, its first and last steps and
 // its rows' way out take 8000 (head_dim 64) to 14,000 cycles on top, which
 // bounds short prompts.
 //
@@ -523,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float* part = part_of(a, blockIdx.x, slot, D);
                 const int kept = segs % kSegs;
                 const float unit = steps > 0 ? sm.ref[kept] * (1.0f / kVLift) : 0.0f;
-                const float by = l == 0.0f ? 0.0f : __frcp_rn(l);     // apart from the unit: their product may be too
+                const float by = l == 0.0f ? 0.0f : rcp(l);     // apart from the unit: their product may be too
                                                                     // small for fp32
                 const bool nans = steps > 0 && sm.has_nan[kept];
                 own *= by;
