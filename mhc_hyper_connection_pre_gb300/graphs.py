@@ -5,7 +5,8 @@ pre block", section "Test Plan": graph mode, median of 5 x 200 calls).
 ``SeamGraph`` records whatever a callable launches on one stream into a
 graph, reports how many kernel nodes the graph holds (the launches per
 seam), and replays it.  All buffers the callable touches must be allocated
-before capture; nothing here allocates device memory during capture.
+before capture, but for the library's default workspaces: a capture has its
+own, which its graph keeps alive.
 
 Early launch.  A kernel launched with programmatic dependent launch is
 recorded with a programmatic edge from the kernel before it, taken from that
