@@ -106,6 +106,31 @@ mhc_status mhc_kv_append(const mhc_kv_cache *cache, const uint16_t *k, int64_t k
                          const int32_t *cu_q, int64_t B, int64_t T, void *stream);
 
 /*
+ * mhc_kv_append_norm -- mhc_kv_append with a norm of each head's query and key
+ * before the rotation, as decoders have it that norm queries and keys:
+ *   N x = x * r * w[h],  r = 1 / sqrt(sum_i x_i^2 / head_dim + norm_eps)
+ *   q_out[t][h] = bf16( R_p N q[t][h] ),   cache.k <- R_p N k[t][h]
+ * held in fp32 from the inputs to the one rounding at the end; values are
+ * written as they are.  Rows without a place in the cache are copied as they
+ * are.  A head that holds an infinity or NaN gives what the formula gives.
+ *
+ *  q_norm, k_norm  bf16 weights, head h's at h * stride (in elements: a
+ *                  multiple of 8, at least head_dim; 0: all heads have the
+ *                  same), 16-byte aligned.  NULL: no norm of these; q_norm
+ *                  without q is refused.
+ *  norm_eps        1e-20 or more, finite; read when there is a norm
+ */
+mhc_status mhc_kv_append_norm(const mhc_kv_cache *cache, const uint16_t *k, int64_t k_stride,
+                              const uint16_t *v, int64_t v_stride, const uint16_t *q, int64_t q_stride,
+                              int q_heads, uint16_t *q_out, int64_t q_out_stride,
+                              const uint16_t *q_norm, int64_t q_norm_stride, const uint16_t *k_norm,
+                              int64_t k_norm_stride, float norm_eps, const float *cos,
+                              const float *sin, int64_t rope_rows, int rotary_dim, int interleaved,
+                              const int32_t *block_table, int64_t table_width,
+                              const int32_t *seq_lens, const int32_t *cu_q, int64_t B, int64_t T,
+                              void *stream);
+
+/*
  * mhc_kv_attend -- for each new token t at position p and query head h, with
  * the key/value head h / (q_heads / heads):
  *   s_j    = softmax_scale * q[t][h] . k_j,   j = 0 .. p

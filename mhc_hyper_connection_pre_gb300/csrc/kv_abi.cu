@@ -14,8 +14,9 @@ namespace kv {
 cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code, float* k_scale, float* v_scale,
                              int heads, int head_dim, const uint16_t* k, int64_t k_stride, const uint16_t* v,
                              int64_t v_stride, const uint16_t* q, int64_t q_stride, int q_heads, uint16_t* q_out,
-                             int64_t q_out_stride, const float* cos, const float* sin, int rope_rows, int R,
-                             int interleaved, cudaStream_t stream);
+                             int64_t q_out_stride, const uint16_t* q_norm, int64_t q_norm_stride,
+                             const uint16_t* k_norm, int64_t k_norm_stride, float norm_eps, const float* cos,
+                             const float* sin, int rope_rows, int R, int interleaved, cudaStream_t stream);
 cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* v, const float* k_scale,
                              const float* v_scale, int heads, int head_dim, const uint16_t* q, int64_t q_stride,
                              int q_heads, float softmax_scale, uint16_t* out, float* lse, void* workspace,
@@ -83,6 +84,17 @@ bool rows_ok(const void* p, int64_t stride, int64_t width) {
     return p && aligned(p, 16) && stride >= width && stride % 8 == 0 && stride < ((int64_t)1 << 31);
 }
 
+// The least epsilon of a norm: squares that fp32 loses are far below it.
+constexpr float kLeastEps = 1e-20f;
+
+bool norm_ok(const uint16_t* w, int64_t stride, int head_dim) {
+    return aligned(w, 16) && (stride == 0 || (stride >= head_dim && stride % 8 == 0 && stride < ((int64_t)1 << 31)));
+}
+
+Rows norm_rows(const uint16_t* w, int64_t stride, int heads, int head_dim) {
+    return Rows{w, stride ? heads : 1, head_dim * 2, stride ? stride * 2 : head_dim * 2};
+}
+
 Seqs seqs_of(const mhc_kv_cache* c, const int32_t* block_table, int64_t table_width, const int32_t* seq_lens,
              const int32_t* cu_q, int64_t B, int64_t T) {
     int log2 = 4;                                        // page_tokens is a power of two from 16 on (check_common)
@@ -94,15 +106,19 @@ Seqs seqs_of(const mhc_kv_cache* c, const int32_t* block_table, int64_t table_wi
 
 extern "C" {
 
-mhc_status mhc_kv_append(const mhc_kv_cache* cache, const uint16_t* k, int64_t k_stride, const uint16_t* v,
-                         int64_t v_stride, const uint16_t* q, int64_t q_stride, int q_heads, uint16_t* q_out,
-                         int64_t q_out_stride, const float* cos, const float* sin, int64_t rope_rows, int rotary_dim,
-                         int interleaved, const int32_t* block_table, int64_t table_width, const int32_t* seq_lens,
-                         const int32_t* cu_q, int64_t B, int64_t T, void* stream) {
+mhc_status mhc_kv_append_norm(const mhc_kv_cache* cache, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                              int64_t v_stride, const uint16_t* q, int64_t q_stride, int q_heads, uint16_t* q_out,
+                              int64_t q_out_stride, const uint16_t* q_norm, int64_t q_norm_stride,
+                              const uint16_t* k_norm, int64_t k_norm_stride, float norm_eps, const float* cos,
+                              const float* sin, int64_t rope_rows, int rotary_dim, int interleaved,
+                              const int32_t* block_table, int64_t table_width, const int32_t* seq_lens,
+                              const int32_t* cu_q, int64_t B, int64_t T, void* stream) {
     mhc_status st = check_common(cache, table_width, B, T, cu_q);
     if (st != MHC_OK) return st;
     if (rotary_dim < 0 || (!cos) != (!sin) || rope_rows < 0 || (q && q_heads < 1) || (!q) != (!q_out))
         return MHC_ERR_INVALID_ARGUMENT;
+    if ((q_norm || k_norm) && !(norm_eps >= kLeastEps && norm_eps <= 3.0e38f)) return MHC_ERR_INVALID_ARGUMENT;
+    if (q_norm && !q) return MHC_ERR_INVALID_ARGUMENT;
     if (rotary_dim > cache->head_dim || rotary_dim % 16 != 0 || rope_rows > kMaxTokens) return MHC_ERR_UNSUPPORTED;
     if (T == 0) return MHC_OK;
     st = check_arrays(cache, block_table, seq_lens, cu_q);
@@ -111,18 +127,23 @@ mhc_status mhc_kv_append(const mhc_kv_cache* cache, const uint16_t* k, int64_t k
     if (!rows_ok(k, k_stride, row) || !rows_ok(v, v_stride, row)) return MHC_ERR_INVALID_ARGUMENT;
     const int64_t q_row = q ? (int64_t)q_heads * cache->head_dim : 0;
     if (q && (!rows_ok(q, q_stride, q_row) || !rows_ok(q_out, q_out_stride, q_row))) return MHC_ERR_INVALID_ARGUMENT;
+    if ((q_norm && !norm_ok(q_norm, q_norm_stride, cache->head_dim)) ||
+        (k_norm && !norm_ok(k_norm, k_norm_stride, cache->head_dim)))
+        return MHC_ERR_INVALID_ARGUMENT;
     const bool turn = cos && rotary_dim > 0;
     if (turn && (!aligned(cos, 16) || !aligned(sin, 16))) return MHC_ERR_INVALID_ARGUMENT;
     const int64_t codes = cache->num_pages * row * cache->page_tokens, scales = cache->num_pages * cache->heads * 4;
     const Rows outs[] = {dense(cache->k, codes), dense(cache->v, codes), dense(cache->k_scale, scales),
                          dense(cache->v_scale, scales), {q_out, T, q_row * 2, q_out_stride * 2}};
     const int64_t table = turn ? rope_rows * (rotary_dim / 2) * 4 : 0;
-    const Rows ins[] = {{k, T, row * 2, k_stride * 2}, {v, T, row * 2, v_stride * 2}, dense(cos, table),
-                        dense(sin, table), dense(block_table, B * table_width * 4), dense(seq_lens, B * 4),
-                        dense(cu_q, (B + 1) * 4), {q, T, q_row * 2, q_stride * 2}};
+    const Rows ins[] = {{q, T, q_row * 2, q_stride * 2}, {k, T, row * 2, k_stride * 2}, {v, T, row * 2, v_stride * 2},
+                        dense(cos, table), dense(sin, table), dense(block_table, B * table_width * 4),
+                        dense(seq_lens, B * 4), dense(cu_q, (B + 1) * 4),
+                        norm_rows(q_norm, q_norm_stride, q_heads, cache->head_dim),
+                        norm_rows(k_norm, k_norm_stride, cache->heads, cache->head_dim)};
     for (const Rows& o : outs) {
         for (const Rows& i : ins) {
-            const bool in_place = o.p == q_out && i.p == q && q == q_out && q_stride == q_out_stride;
+            const bool in_place = &o == outs + 4 && &i == ins && q == q_out && q_stride == q_out_stride;
             if (!in_place && meet(o, i)) return MHC_ERR_INVALID_ARGUMENT;
         }
         for (const Rows& o2 : outs)
@@ -132,9 +153,19 @@ mhc_status mhc_kv_append(const mhc_kv_cache* cache, const uint16_t* k, int64_t k
     const cudaError_t e = mhc::kv::launch_kv_append(
         seqs_of(cache, block_table, table_width, seq_lens, cu_q, B, T), cache->k, cache->v, cache->k_scale,
         cache->v_scale, cache->heads, cache->head_dim, k, k_stride, v, v_stride, q, q_stride, q ? q_heads : 0, q_out,
-        q_out_stride, cos, sin, (int)rope_rows, turn ? rotary_dim : 0, interleaved ? 1 : 0,
+        q_out_stride, q_norm, q_norm_stride, k_norm, k_norm_stride, norm_eps, cos, sin, (int)rope_rows, turn ? rotary_dim : 0, interleaved ? 1 : 0,
         static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MHC_OK : MHC_ERR_CUDA;
+}
+
+mhc_status mhc_kv_append(const mhc_kv_cache* cache, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                         int64_t v_stride, const uint16_t* q, int64_t q_stride, int q_heads, uint16_t* q_out,
+                         int64_t q_out_stride, const float* cos, const float* sin, int64_t rope_rows, int rotary_dim,
+                         int interleaved, const int32_t* block_table, int64_t table_width, const int32_t* seq_lens,
+                         const int32_t* cu_q, int64_t B, int64_t T, void* stream) {
+    return mhc_kv_append_norm(cache, k, k_stride, v, v_stride, q, q_stride, q_heads, q_out, q_out_stride, nullptr, 0,
+                              nullptr, 0, 0.f, cos, sin, rope_rows, rotary_dim, interleaved, block_table, table_width,
+                              seq_lens, cu_q, B, T, stream);
 }
 
 size_t mhc_kv_attend_workspace_bytes(const mhc_kv_cache* cache, int q_heads, int64_t B, int64_t T) {

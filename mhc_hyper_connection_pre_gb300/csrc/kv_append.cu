@@ -37,6 +37,9 @@ struct AppendArgs {
     const float* cos;
     const float* sin;
     int rope_rows, R;                 // R == 0: no rotation
+    const uint16_t* norm[2];          // weights of the queries' and the keys' norm; null: none
+    int64_t norm_stride[2];           // from a head's weights to the next head's; 0: the same for all
+    float norm_eps;
     int window;                       // tokens whose runs one group takes
     int windows;                      // ceil(T / window)
     int kv_blocks;                    // blocks [0, kv_blocks) append, the rest rotate q
@@ -97,6 +100,46 @@ __device__ __forceinline__ void rotate(const Turn& w, float (&x)[8], float (&y)[
     }
 }
 
+// The 16 numbers over their head's root mean square, times the head's weights:
+// x * (1 / sqrt(sum of squares / D + eps)) * w, sums and products in fp32.  Called
+// by whole warps; the D / 16 threads of a head add up their squares in a fixed
+// order.  Squares past fp32's range (numbers from 2^60 on) are summed once more from
+// numbers scaled by 2^-70.
+template <int D>
+__device__ __forceinline__ void norm16(const uint16_t* w, const Chunks& at, float eps, float (&x)[8], float (&y)[8]) {
+    constexpr int kLanes = D / 16;
+    constexpr float kSmaller = 8.4703295e-22f;                // 2^-70
+    auto squares = [&](float by) {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = fmaf(x[j] * by, x[j] * by, fmaf(y[j] * by, y[j] * by, s));
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return s;
+    };
+    float s = squares(1.0f);
+    if (__any_sync(0xffffffffu, s == INFINITY)) {
+        const float small = squares(kSmaller);
+        if (s == INFINITY) {
+            s = small;
+            eps = eps * kSmaller * kSmaller;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j] *= kSmaller;
+                y[j] *= kSmaller;
+            }
+        }
+    }
+    const float r = rsqrtf(fmaf(s, 1.0f / D, eps));
+    float u[8];
+    unpack8(__ldg(reinterpret_cast<const uint4*>(w + at.a)), u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = x[j] * r * u[j];
+    unpack8(__ldg(reinterpret_cast<const uint4*>(w + at.b)), u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = y[j] * r * u[j];
+}
+
 // The smallest power of two 2^e with a <= 448 * 2^e = 1.75 * 2^(8+e), e at
 // least -116 (so that the smallest step, 2^-9 * 2^e, is a normal fp32
 // number).  a is finite.
@@ -137,7 +180,7 @@ __device__ __forceinline__ float group_max(float v, int group, float* red) {
 
 // GT threads take one (window, head, k or v), the loads of kAhead steps under
 // way together.
-template <int D, int GT, int kMode, int kAhead>
+template <int D, int GT, int kMode, int kAhead, bool kNorm>
 __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
     constexpr int kBlock = 256, kGroups = kBlock / GT;
     constexpr int kLanes = D / 16, kRows = GT / kLanes;               // threads of a head; rows of one step
@@ -174,7 +217,22 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
         for (int base = first; base < end; base += kAhead * kHeads) {
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                if (turned) {
+                if constexpr (kNorm) {                // a row without a place stays as it is
+                    if (a.norm[0] && pos >= 0) {
+                        float x[8], y[8];
+                        unpack8(raw[i].a, x);
+                        unpack8(raw[i].b, y);
+                        norm16<D>(a.norm[0] + (h < end ? h : first) * a.norm_stride[0], at, a.norm_eps, x, y);
+                        if (turned) rotate<kMode>(turn, x, y);
+                        raw[i] = Raw{pack8(x), pack8(y)};
+                    } else if (turned) {
+                        float x[8], y[8];
+                        unpack8(raw[i].a, x);
+                        unpack8(raw[i].b, y);
+                        rotate<kMode>(turn, x, y);
+                        raw[i] = Raw{pack8(x), pack8(y)};
+                    }
+                } else if (turned) {
                     float x[8], y[8];
                     unpack8(raw[i].a, x);
                     unpack8(raw[i].b, y);
@@ -237,10 +295,18 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
                     const int r = base + i * kRows + r0;
-                    if (r >= n) break;
+                    if constexpr (kNorm) {            // the norm is whole warps' work
+                        if (r - lane / kLanes >= n) break;
+                    } else if (r >= n) {
+                        break;
+                    }
                     float x[8], y[8];
                     unpack8(raw[i].a, x);
                     unpack8(raw[i].b, y);
+                    if constexpr (kNorm) {
+                        if (kv == 0 && a.norm[1]) norm16<D>(a.norm[1] + head * a.norm_stride[1], at, a.norm_eps, x, y);
+                        if (r >= n) break;
+                    }
                     if (kMode != kPlain && kv == 0 && at.turned) {
                         Turn turn;
                         load_turn(a, run.pos + r, lane % kLanes, turn);
@@ -301,7 +367,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
     }
 }
 
-template <int D, int GT, int kMode, int kAhead>
+template <int D, int GT, int kMode, int kAhead, bool kNorm>
 static cudaError_t launch_mode(AppendArgs& a, cudaStream_t stream) {
     constexpr int kBlock = 256;
     const int64_t items = (int64_t)a.windows * a.heads * 2;
@@ -315,21 +381,29 @@ static cudaError_t launch_mode(AppendArgs& a, cudaStream_t stream) {
     }
     if (items > 0x7fffffff || kv_blocks + q_blocks > 0x7fffffff) return cudaErrorInvalidValue;
     a.kv_blocks = (int)kv_blocks;
-    kv_append_kernel<D, GT, kMode, kAhead><<<(unsigned)(kv_blocks + q_blocks), kBlock, 0, stream>>>(a);
+    kv_append_kernel<D, GT, kMode, kAhead, kNorm><<<(unsigned)(kv_blocks + q_blocks), kBlock, 0, stream>>>(a);
     return cudaGetLastError();
+}
+
+template <int D, int GT, int kAhead, bool kNorm>
+static cudaError_t launch_turned(AppendArgs& a, int interleaved, cudaStream_t stream) {
+    if (a.R == 0) return launch_mode<D, GT, kPlain, kAhead, kNorm>(a, stream);
+    return interleaved ? launch_mode<D, GT, kPairs, kAhead, kNorm>(a, stream)
+                       : launch_mode<D, GT, kHalves, kAhead, kNorm>(a, stream);
 }
 
 template <int D, int GT, int kAhead>
 static cudaError_t launch_append(AppendArgs& a, int interleaved, cudaStream_t stream) {
-    if (a.R == 0) return launch_mode<D, GT, kPlain, kAhead>(a, stream);
-    return interleaved ? launch_mode<D, GT, kPairs, kAhead>(a, stream) : launch_mode<D, GT, kHalves, kAhead>(a, stream);
+    return a.norm[0] || a.norm[1] ? launch_turned<D, GT, kAhead, true>(a, interleaved, stream)
+                                  : launch_turned<D, GT, kAhead, false>(a, interleaved, stream);
 }
 
 cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code, float* k_scale, float* v_scale,
                              int heads, int head_dim, const uint16_t* k, int64_t k_stride, const uint16_t* v,
                              int64_t v_stride, const uint16_t* q, int64_t q_stride, int q_heads, uint16_t* q_out,
-                             int64_t q_out_stride, const float* cos, const float* sin, int rope_rows, int R,
-                             int interleaved, cudaStream_t stream) {
+                             int64_t q_out_stride, const uint16_t* q_norm, int64_t q_norm_stride,
+                             const uint16_t* k_norm, int64_t k_norm_stride, float norm_eps, const float* cos,
+                             const float* sin, int rope_rows, int R, int interleaved, cudaStream_t stream) {
     AppendArgs a;
     a.seqs = seqs;
     a.code[0] = k_code; a.code[1] = v_code;
@@ -340,6 +414,9 @@ cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code,
     a.q = q; a.q_out = q_out;
     a.q_stride = q_stride; a.q_out_stride = q_out_stride;
     a.q_heads = q_heads;
+    a.norm[0] = q ? q_norm : nullptr; a.norm[1] = k_norm;
+    a.norm_stride[0] = q_norm_stride; a.norm_stride[1] = k_norm_stride;
+    a.norm_eps = norm_eps;
     a.cos = cos; a.sin = sin;
     a.rope_rows = rope_rows; a.R = R;
     // Few new tokens a sequence on average: a warp for each token that may start a

@@ -252,10 +252,33 @@ void count(Py_ssize_t n, Py_ssize_t want) {
     if (n != want) type_error("wrong number of arguments");
 }
 
-// append(k codes, v codes, k_scale, v_scale, k, v, block_table, seq_lens, cu_q, q, cos, sin, interleaved, q_out)
+// bf16 [head_dim] or [heads, head_dim], a head's weights contiguous.
+struct Weights {
+    const uint16_t* p = nullptr;
+    int64_t stride = 0;
+};
+
+Weights weights_of(PyObject* o, const char* name, int64_t heads, const mhc_kv_cache& c, const at::Device& dev) {
+    Weights w;
+    if (!given(o)) return w;
+    const at::Tensor& t = tensor(o, name);
+    const bool each = t.dim() == 2;
+    if (!(t.dim() == 1 || (each && t.size(0) == heads)) || t.size(-1) != c.head_dim)
+        value_error(std::string(name) + " must be [head_dim] or [heads, head_dim]");
+    if (t.device() != dev) value_error(std::string(name) + " must be on the cache's device (got " + t.device().str() + ")");
+    if (t.scalar_type() != at::kBFloat16)
+        type_error(std::string(name) + " must be BFloat16 (got " + c10::toString(t.scalar_type()) + ")");
+    if (t.stride(-1) != 1) value_error(std::string(name) + ": the weights of a head must be contiguous");
+    w.p = data<uint16_t>(t);
+    w.stride = each && heads > 1 ? t.stride(0) : 0;      // 0 as well where the heads are one expanded row
+    return w;
+}
+
+// append(k codes, v codes, k_scale, v_scale, k, v, block_table, seq_lens, cu_q, q, cos, sin, interleaved, q_out,
+// q_norm, k_norm, norm_eps)
 PyObject* append(PyObject*, PyObject* const* o, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        count(n, 14);
+        count(n, 17);
         at::Device dev(at::kCPU);
         const mhc_kv_cache c = cache_of(o, dev);
         const Rows k = rows_of(tensor(o[4], "k"), "k", c, dev), v = rows_of(tensor(o[5], "v"), "v", c, dev);
@@ -290,10 +313,21 @@ PyObject* append(PyObject*, PyObject* const* o, Py_ssize_t n) {
             dim = std::min<int64_t>(2 * ct.size(1), 1 << 20);
         }
         const bool inter = truth(o[12]);
-        check_status("mhc_kv_append",
-                     mhc_kv_append(&c, k.p, k.stride, v.p, v.stride, q.p, q.stride, (int)q.heads, out.p, out.stride, cos,
-                                   sin, rows, (int)dim, inter, s.table, s.width, s.lens, s.cu, s.B, k.tokens,
-                                   c10::cuda::getCurrentCUDAStream(dev.index()).stream()));
+        if (given(o[14]) && !given(o[9])) value_error("q_norm without q");
+        const Weights qn = weights_of(o[14], "q_norm", q.heads, c, dev), kn = weights_of(o[15], "k_norm", k.heads, c, dev);
+        const double eps = PyFloat_AsDouble(o[16]);
+        if (PyErr_Occurred()) throw Refused{nullptr, ""};
+        const auto stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+        if (qn.p || kn.p)
+            check_status("mhc_kv_append_norm",
+                         mhc_kv_append_norm(&c, k.p, k.stride, v.p, v.stride, q.p, q.stride, (int)q.heads, out.p,
+                                            out.stride, qn.p, qn.stride, kn.p, kn.stride, (float)eps, cos, sin, rows,
+                                            (int)dim, inter, s.table, s.width, s.lens, s.cu, s.B, k.tokens, stream));
+        else
+            check_status("mhc_kv_append",
+                         mhc_kv_append(&c, k.p, k.stride, v.p, v.stride, q.p, q.stride, (int)q.heads, out.p, out.stride,
+                                       cos, sin, rows, (int)dim, inter, s.table, s.width, s.lens, s.cu, s.B, k.tokens,
+                                       stream));
         if (!q_out.defined()) Py_RETURN_NONE;
         if (given(o[13])) {
             Py_INCREF(o[13]);

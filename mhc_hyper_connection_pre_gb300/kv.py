@@ -44,6 +44,9 @@ def declare(lib) -> None:
     C = ctypes.POINTER(_Cache)
     lib.mhc_kv_append.argtypes = [C, P, I64, P, I64, P, I64, I, P, I64, P, P, I64, I, I, P, I64, P, P, I64, I64, P]
     lib.mhc_kv_append.restype = I
+    lib.mhc_kv_append_norm.argtypes = [C, P, I64, P, I64, P, I64, I, P, I64, P, I64, P, I64, F, P, P, I64, I, I, P, I64, P,
+                                       P, I64, I64, P]
+    lib.mhc_kv_append_norm.restype = I
     lib.mhc_kv_attend.argtypes = [C, P, I64, I, P, I64, P, P, I64, I64, F, P, P, P, ctypes.c_size_t, P]
     lib.mhc_kv_attend.restype = I
     lib.mhc_kv_attend_workspace_bytes.argtypes = [C, I, I64, I64]
@@ -97,22 +100,25 @@ def _on(stream, cache, tensors=()):
 def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
               cu_q: torch.Tensor | None = None, *, q: torch.Tensor | None = None, cos: torch.Tensor | None = None,
               sin: torch.Tensor | None = None, interleaved: bool = False, q_out: torch.Tensor | None = None,
+              q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None, norm_eps: float = 1e-6,
               stream=None) -> torch.Tensor | None:
-    """Append the new tokens to the cache (``mhc_kv_append``).
+    """Append the new tokens to the cache (``mhc_kv_append``, ``mhc_kv_append_norm``).
 
     k, v bf16 [T, heads, head_dim]; q bf16 [T, q_heads, head_dim] or None;
     each may be a slice of a fused projection's rows.  cos, sin fp32
     [positions, rotary_dim / 2] or None (no rotation): keys and queries are
     rotated by their positions, in pairs (i, i + rotary_dim / 2) or,
-    ``interleaved``, (2i, 2i + 1).  The cache is written in place; returns the
-    rotated queries (``q_out``, which may be q itself), or None without q.
+    ``interleaved``, (2i, 2i + 1).  q_norm, k_norm bf16 [head_dim] or [heads,
+    head_dim]: queries or keys are divided by their head's root mean square
+    (``norm_eps`` is added to the mean) and multiplied by these weights before
+    the rotation.  The cache is written in place; returns the rotated queries (``q_out``, which may be q itself), or None without q.
     """
     if stream is not None:
-        with _on(stream, cache, (*cache.values(), k, v, q, q_out, cos, sin, block_table, seq_lens, cu_q)):
+        with _on(stream, cache, (*cache.values(), k, v, q, q_out, cos, sin, block_table, seq_lens, cu_q, q_norm, k_norm)):
             return kv_append(cache, k, v, block_table, seq_lens, cu_q, q=q, cos=cos, sin=sin, interleaved=interleaved,
-                             q_out=q_out)
+                             q_out=q_out, q_norm=q_norm, k_norm=k_norm, norm_eps=norm_eps)
     return (_module or _load()).append(cache["k"], cache["v"], cache["k_scale"], cache["v_scale"], k, v, block_table,
-                                       seq_lens, cu_q, q, cos, sin, interleaved, q_out)
+                                       seq_lens, cu_q, q, cos, sin, interleaved, q_out, q_norm, k_norm, norm_eps)
 
 
 def kv_workspace_for(cache: dict, q_heads: int, B: int, T: int, stream=None) -> torch.Tensor | None:
