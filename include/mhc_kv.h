@@ -160,6 +160,28 @@ mhc_status mhc_kv_attend(const mhc_kv_cache *cache, const uint16_t *q, int64_t q
                          uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
                          void *stream);
 
+/*
+ * mhc_kv_attend_window -- mhc_kv_attend with a sliding window and a few first
+ * keys that stay visible: token t at position p sees the keys j <= p with
+ *   j > p - window  or  j < sinks
+ * A page of which no new token of its sequence sees a key is not looked at:
+ * its place in the table may hold any number (-1, say, once the page has been
+ * given to somebody else), which is not a bad index.
+ *
+ * Accuracy as mhc_kv_attend, the value scales being those of the pages of
+ * which a token of the sequence sees a key.
+ *
+ *  window     1 or more
+ *  sinks      0 or more
+ *  workspace  as for mhc_kv_attend, of as many bytes
+ * Errors as mhc_kv_attend.
+ */
+mhc_status mhc_kv_attend_window(const mhc_kv_cache *cache, const uint16_t *q, int64_t q_stride,
+                                int q_heads, const int32_t *block_table, int64_t table_width,
+                                const int32_t *seq_lens, const int32_t *cu_q, int64_t B, int64_t T,
+                                float softmax_scale, int64_t window, int64_t sinks, uint16_t *out,
+                                float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Workspace bytes mhc_kv_attend needs on the current device (0: none). */
 size_t mhc_kv_attend_workspace_bytes(const mhc_kv_cache *cache, int q_heads, int64_t B, int64_t T);
 

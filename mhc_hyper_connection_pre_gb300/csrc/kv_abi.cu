@@ -19,8 +19,8 @@ cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code,
                              const float* sin, int rope_rows, int R, int interleaved, cudaStream_t stream);
 cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* v, const float* k_scale,
                              const float* v_scale, int heads, int head_dim, const uint16_t* q, int64_t q_stride,
-                             int q_heads, float softmax_scale, uint16_t* out, float* lse, void* workspace,
-                             int num_sms, cudaStream_t stream);
+                             int q_heads, float softmax_scale, int window, int sinks, uint16_t* out, float* lse,
+                             void* workspace, int num_sms, cudaStream_t stream);
 size_t kv_attend_workspace(int heads, int head_dim, int q_heads, int64_t B, int64_t T, int num_sms);
 }  // namespace kv
 }  // namespace mhc
@@ -102,6 +102,12 @@ Seqs seqs_of(const mhc_kv_cache* c, const int32_t* block_table, int64_t table_wi
     return Seqs{block_table, seq_lens, cu_q, (int)table_width, (int)B, (int)T, log2, (int)c->num_pages};
 }
 
+// Both attention calls; window 0: none.
+mhc_status attend(const mhc_kv_cache* cache, const uint16_t* q, int64_t q_stride, int q_heads,
+                  const int32_t* block_table, int64_t table_width, const int32_t* seq_lens, const int32_t* cu_q,
+                  int64_t B, int64_t T, float softmax_scale, int64_t window, int64_t sinks, uint16_t* out, float* lse,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
 }  // namespace
 
 extern "C" {
@@ -174,10 +180,32 @@ size_t mhc_kv_attend_workspace_bytes(const mhc_kv_cache* cache, int q_heads, int
     return sms > 0 ? mhc::kv::kv_attend_workspace(cache->heads, cache->head_dim, q_heads, B, T, sms) : 0;
 }
 
+mhc_status mhc_kv_attend_window(const mhc_kv_cache* cache, const uint16_t* q, int64_t q_stride, int q_heads,
+                                const int32_t* block_table, int64_t table_width, const int32_t* seq_lens,
+                                const int32_t* cu_q, int64_t B, int64_t T, float softmax_scale, int64_t window,
+                                int64_t sinks, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+    if (window < 1 || sinks < 0) return MHC_ERR_INVALID_ARGUMENT;
+    return attend(cache, q, q_stride, q_heads, block_table, table_width, seq_lens, cu_q, B, T, softmax_scale, window,
+                  sinks, out, lse, workspace, workspace_bytes, stream);
+}
+
 mhc_status mhc_kv_attend(const mhc_kv_cache* cache, const uint16_t* q, int64_t q_stride, int q_heads,
                          const int32_t* block_table, int64_t table_width, const int32_t* seq_lens,
                          const int32_t* cu_q, int64_t B, int64_t T, float softmax_scale, uint16_t* out, float* lse,
                          void* workspace, size_t workspace_bytes, void* stream) {
+    return attend(cache, q, q_stride, q_heads, block_table, table_width, seq_lens, cu_q, B, T, softmax_scale, 0, 0, out,
+                  lse, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+mhc_status attend(const mhc_kv_cache* cache, const uint16_t* q, int64_t q_stride, int q_heads,
+                  const int32_t* block_table, int64_t table_width, const int32_t* seq_lens, const int32_t* cu_q,
+                  int64_t B, int64_t T, float softmax_scale, int64_t window, int64_t sinks, uint16_t* out, float* lse,
+                  void* workspace, size_t workspace_bytes, void* stream) {
     mhc_status st = check_common(cache, table_width, B, T, cu_q);
     if (st != MHC_OK) return st;
     if (q_heads < 1 || q_heads % cache->heads != 0 || !(softmax_scale >= 0.f) || softmax_scale > 3.0e38f)
@@ -207,11 +235,14 @@ mhc_status mhc_kv_attend(const mhc_kv_cache* cache, const uint16_t* q, int64_t q
     if (sms <= 0) return MHC_ERR_CUDA;
     const size_t need = mhc::kv::kv_attend_workspace(cache->heads, cache->head_dim, q_heads, B, T, sms);
     if (workspace_bytes < need || (need && (!workspace || !aligned(workspace, 256)))) return MHC_ERR_INVALID_ARGUMENT;
+    // a window, or first tokens, of as many as the table can hold hide nothing
+    const int64_t most = table_width * cache->page_tokens;
+    const bool binds = window > 0 && window < most && sinks < most;
     const cudaError_t e = mhc::kv::launch_kv_attend(
         seqs_of(cache, block_table, table_width, seq_lens, cu_q, B, T), cache->k, cache->v, cache->k_scale,
-        cache->v_scale, cache->heads, cache->head_dim, q, q_stride, q_heads, softmax_scale, out, lse, workspace, sms,
-        static_cast<cudaStream_t>(stream));
+        cache->v_scale, cache->heads, cache->head_dim, q, q_stride, q_heads, softmax_scale, binds ? (int)window : 0,
+        binds ? (int)std::min(sinks, kMaxTokens) : 0, out, lse, workspace, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MHC_OK : MHC_ERR_CUDA;
 }
 
-}  // extern "C"
+}  // namespace

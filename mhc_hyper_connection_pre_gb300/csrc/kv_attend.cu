@@ -98,10 +98,10 @@ struct Acc {
 
 // `full`: every row sees all of them.  One copy of the code for both cases, as a
 // second one would fall out of the instruction cache between its rare uses.
-template <int D, int NB>
-__device__ __forceinline__ void piece(bool full, uint32_t ks, uint32_t vs, const Meta& meta, const uint32_t (&q)[NB][D / 8],
-                                      const float (&f)[NB][2], const int (&lim)[NB][2], int key0, int keys, int lane,
-                                      Acc<D, NB>& acc) {
+template <int D, int NB, class C>
+__device__ __forceinline__ void piece(const C& cut, bool full, uint32_t ks, uint32_t vs, const Meta& meta,
+                                      const uint32_t (&q)[NB][D / 8], const float (&f)[NB][2], const int (&lim)[NB][2],
+                                      int key0, int keys, int lane, Acc<D, NB>& acc) {
     const int g = lane / 4, t = lane % 4;
     float s[2][NB][4];
 #pragma unroll
@@ -158,6 +158,11 @@ __device__ __forceinline__ void piece(bool full, uint32_t ks, uint32_t vs, const
                 x[1] = n0 > 8 ? x[1] : -INFINITY;
                 x[2] = n1 > 16 ? x[2] : -INFINITY;
                 x[3] = n1 > 24 ? x[3] : -INFINITY;
+                if constexpr (C::kWindow) {
+                    const int out = n - cut.window, s = cut.sinks - key0 - g;   // those from `out` on, and those below s
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = 8 * i >= out || 8 * i < s ? x[i] : -INFINITY;
+                }
             }
             top[nb][e] = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
             grow = grow || top[nb][e] - acc.m[nb][e] > kGrow;
@@ -269,6 +274,10 @@ __device__ __forceinline__ void piece(bool full, uint32_t ks, uint32_t vs, const
                     mma_f16(acc.o[2 * x + y][nb], a[y][0], a[y][1], a[y][2], a[y][3], b[nb][0], b[nb][1]);
         }
     }
+    auto sees = [&](int key, int n) {
+        if constexpr (C::kWindow) return key_seen(key, n, cut);
+        else return key < n;
+    };
     if (!full && __any_sync(0xffffffffu, nans != 0)) {
 #pragma unroll 1
         for (int r = 0; r < kSub && key0 + r < keys; ++r) {
@@ -282,7 +291,7 @@ __device__ __forceinline__ void piece(bool full, uint32_t ks, uint32_t vs, const
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        if ((v[x / 4] >> (8 * (x % 4))) & 0x80u && key0 + r < lim[nb][e])
+                        if ((v[x / 4] >> (8 * (x % 4))) & 0x80u && sees(key0 + r, lim[nb][e]))
                             acc.o[x / 2][nb][2 * (x & 1) + e] = __int_as_float(0x7fc00000);
         }
     }
@@ -290,14 +299,15 @@ __device__ __forceinline__ void piece(bool full, uint32_t ks, uint32_t vs, const
 
 // The plan's segment into the queue.  A call of its own: it is rare, and its
 // code does not belong between the loads'.
-__device__ __noinline__ bool push_segment(const AttendArgs& a, Plan& plan, const Shares& shares, Segment& to) {
-    return plan_next(plan, Lookup{a}, a.cut, shares, to);
+template <class C>
+__device__ __noinline__ bool push_segment(const AttendArgs<C>& a, Plan& plan, const Shares& shares, Segment& to) {
+    return plan_next(plan, Lookup<C>{a}, a.cut, shares, to);
 }
 
-template <int D, int NB>
+template <int D, int NB, class C>
 __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     kv_attend_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                     const __grid_constant__ AttendArgs a) {
+                     const __grid_constant__ AttendArgs<C> a) {
     constexpr int kStages = Shape<D, NB>::kStages, kStage = Shape<D, NB>::kStage;
     constexpr int kRows = 8 * NB;
     extern __shared__ uint8_t raw[];
@@ -328,6 +338,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     uint32_t pushed = 0, popped = 0;          // segments
     int key = 0, keys = 0, head = 0;          // of the next load: its first key, its segment's last key + 1 and head
     int b = 0;
+    [[maybe_unused]] int skip_at = 0, skip = 0, first = 0;    // with a window: of its segment; the first place it looks at
     bool over = false;                        // the plan has no more segments
     int blocks[2], ahead = 32;                // page and head of both halves of 32 loads, one in each lane (-1: no page);
                                               // the next load's lane
@@ -347,6 +358,11 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
             keys = s.keys;
             head = s.head;
             b = s.b;
+            if constexpr (C::kWindow) {
+                skip_at = s.skip_at;
+                skip = s.skip;
+                first = first_seen(s, a.cut);
+            }
             ahead = 32;
         }
         if (ahead == 32) {
@@ -354,9 +370,15 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int k = key + kSub * lane + 16 * i;
-                const int page = k < keys ? __ldg(row + (k >> a.seqs.page_log2)) : -1;
+                int place = k;
+                bool look = k < keys;
+                if constexpr (C::kWindow) {
+                    place = k < skip_at ? k : k + skip;
+                    look = look && page_seen(place, first, a.cut.sinks, a.seqs.page_log2);
+                }
+                const int page = look ? __ldg(row + (place >> a.seqs.page_log2)) : -1;
                 const bool ok = page >= 0 && page < a.seqs.num_pages;
-                if (k < keys && !ok) atomicOr(&g_device_status, kIndexError);
+                if (look && !ok) atomicOr(&g_device_status, kIndexError);
                 blocks[i] = ok ? page * a.cut.heads + head : -1;
             }
             ahead = 0;
@@ -381,7 +403,9 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
             meta.block[0] = block0;
             meta.block[1] = block1;
             if (a.seqs.page_log2 >= 5) {      // both halves lie in one page
-                const int slot = key & ((1 << a.seqs.page_log2) - 1);
+                int place = key;
+                if constexpr (C::kWindow) place = key < skip_at ? key : key + skip;
+                const int slot = place & ((1 << a.seqs.page_log2) - 1);
                 mbar_arrive_expect_tx(bar, ok0 ? kStage : 0);
                 if (ok0) {
                     tma_load_3d(dst, &k_map, 0, slot, block0, bar);
@@ -410,6 +434,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     uint32_t q[NB][D / 8];
     float f[NB][2];
     int lim[NB][2], all_see = 0;
+    [[maybe_unused]] int last_sees = 0;       // with a window: keys up to which the last row sees them
     Acc<D, NB> acc;
     int at = 0, end = 0;                      // the next piece's first key, the segment's last + 1
     bool open = false;                        // a segment is under way
@@ -477,6 +502,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
                     for (int i = 0; i < 4; ++i) acc.o[j][nb][i] = 0.0f;
             }
             all_see = keys_of_row(seg, a.cut, 0);           // keys that every row sees
+            if constexpr (C::kWindow) last_sees = keys_of_row(seg, a.cut, seg.rows - 1);
         }
         if (at < end) {
             const int st = from;
@@ -487,8 +513,9 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
             phase ^= from == 0;
             const uint32_t base_addr = smem_u32(sm.ring[warp] + st * kStage);
             const Meta& meta = sm.meta[warp][st];
-            const bool full = at + kSub <= all_see && meta.block[0] >= 0 && meta.block[1] >= 0;
-            piece<D, NB>(full, base_addr, base_addr + kStage / 2, meta, q, f, lim, at, end, lane, acc);
+            bool full = at + kSub <= all_see && meta.block[0] >= 0 && meta.block[1] >= 0;
+            if constexpr (C::kWindow) full = full && keys_all_seen(at, kSub, all_see, last_sees, a.cut);
+            piece<D, NB>(a.cut, full, base_addr, base_addr + kStage / 2, meta, q, f, lim, at, end, lane, acc);
             __syncwarp();                     // every lane has read the stage
             at += kSub;
             continue;
@@ -568,7 +595,7 @@ __device__ __forceinline__ float join_lse(float m, float l) {
 // for the 228 parts of a whole GPU over eight heads.  Measured with blocks from
 // 16 parts on: one sequence of 1001 keys 14.3 us, 12.4 from 64 on.
 template <int D, int kAhead>
-__global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const AttendArgs<Cut> a) {
     constexpr int kSome = 16, kMany = 64, kDims = D / 32;
     __shared__ float sum_o[8][D];
     __shared__ float2 sum_ml[8];
@@ -755,18 +782,18 @@ int shares_of(int rows, int D, int num_sms) {
 
 size_t part_bytes(int rows, int D, int shares) { return ((size_t)shares * 2 * rows * (D + 1) * 4 + 255) / 256 * 256; }
 
-template <int D, int NB>
-cudaError_t launch(const CUtensorMap& k_map, const CUtensorMap& v_map, const AttendArgs& a, int blocks,
+template <int D, int NB, class C>
+cudaError_t launch(const CUtensorMap& k_map, const CUtensorMap& v_map, const AttendArgs<C>& a, int blocks,
                    cudaStream_t stream) {
     const int bytes = (int)sizeof(Smem<D, NB>) + 1024;
     // an attribute of the function on the current device: set on every call, which keeps no state here
-    const cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<D, NB, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kv_attend_kernel<D, NB><<<blocks, Shape<D, NB>::kThreads, bytes, stream>>>(k_map, v_map, a);
+    kv_attend_kernel<D, NB, C><<<blocks, Shape<D, NB>::kThreads, bytes, stream>>>(k_map, v_map, a);
     return cudaGetLastError();
 }
 
-cudaError_t launch_join(const AttendArgs& a, int head_dim, cudaStream_t stream) {
+cudaError_t launch_join(const AttendArgs<Cut>& a, int head_dim, cudaStream_t stream) {
     if (a.shares < 2) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -788,45 +815,43 @@ cudaError_t launch_join(const AttendArgs& a, int head_dim, cudaStream_t stream) 
 
 }  // namespace
 
-cudaError_t launch_kv_attend_tc(const AttendArgs& a, const uint8_t* k, const uint8_t* v, int head_dim, int blocks,
+cudaError_t launch_kv_attend_tc(const AttendArgs<Cut>& a, const uint8_t* k, const uint8_t* v, int head_dim, int blocks,
                                 cudaStream_t stream);
+cudaError_t launch_kv_attend_tc(const AttendArgs<WindowCut>& a, const uint8_t* k, const uint8_t* v, int head_dim,
+                                int blocks, cudaStream_t stream);
 
 size_t kv_attend_workspace(int heads, int head_dim, int q_heads, int64_t B, int64_t T, int num_sms) {
     const int rows = tile_rows(q_heads / heads, B, T), shares = shares_of(rows, head_dim, num_sms);
     return part_bytes(rows, head_dim, shares) + (size_t)shares * 2 * sizeof(PartDesc);
 }
 
-cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* v, const float* k_scale,
-                             const float* v_scale, int heads, int head_dim, const uint16_t* q, int64_t q_stride,
-                             int q_heads, float softmax_scale, uint16_t* out, float* lse, void* workspace,
-                             int num_sms, cudaStream_t stream) {
-    AttendArgs a;
-    const int group = q_heads / heads, rows = tile_rows(group, seqs.B, seqs.T);
-    a.seqs = seqs;
+namespace {
+
+// The kernel for the call's rows, then the join.  `a` lacks the cut's sizes of tiles and units, the shares and the
+// workspace's parts.
+template <class C>
+cudaError_t launch_rows(AttendArgs<C>& a, const uint8_t* k, int heads, int head_dim, int group, void* workspace,
+                        int num_sms, cudaStream_t stream) {
+    const Seqs& seqs = a.seqs;
+    const int rows = tile_rows(group, seqs.B, seqs.T);
     // What a tile costs beside its keys, in units.  Tensor-memory kernel: 2, 3, 4, 6, 8 took 660, 560, 515, 522, 532 us
     // for a prompt of 8192 tokens (4 heads of 128, 8 rows each), with heads of 64 458, 425, 430, 438, 446.  Warps: 0, 1, 2,
     // 3, 4, 6 took 39.5, 33.4, 31.6, 31.6, 31.7, 31.6 us for 256 sequences up to 300 keys, 700 short ones 47.5, 41.2,
     // 39.7, 39.6, 40.0, 41.7.
     const int extra = rows == 256 && head_dim == 128 ? 4 : 3;
-    a.cut = rows == 256 ? make_cut(heads, group, 8, 7, extra) : make_cut(heads, group, rows == 8 ? 3 : 4, kUnitLog2, extra);
+    static_cast<Cut&>(a.cut) =
+        rows == 256 ? make_cut(heads, group, 8, 7, extra) : make_cut(heads, group, rows == 8 ? 3 : 4, kUnitLog2, extra);
     a.shares = shares_of(rows, head_dim, num_sms);
-    a.k_scale = k_scale;
-    a.v_scale = v_scale;
-    a.q = q;
-    a.q_stride = q_stride;
-    a.scale_log2 = softmax_scale * kLog2e;
-    a.out = out;
-    a.lse = lse;
     a.part = static_cast<float*>(workspace);
     a.desc = reinterpret_cast<PartDesc*>(static_cast<uint8_t*>(workspace) + part_bytes(rows, head_dim, a.shares));
     cudaError_t e;
     if (rows == 256) {
-        e = launch_kv_attend_tc(a, k, v, head_dim, num_sms, stream);
+        e = launch_kv_attend_tc(a, k, a.v, head_dim, num_sms, stream);
     } else {
         CUtensorMap k_map, v_map;
         const int64_t pages = (int64_t)seqs.num_pages * heads;
         if (!encode_codes(&k_map, k, pages, 1 << seqs.page_log2, head_dim, kSub) ||
-            !encode_codes(&v_map, v, pages, 1 << seqs.page_log2, head_dim, kSub))
+            !encode_codes(&v_map, a.v, pages, 1 << seqs.page_log2, head_dim, kSub))
             return cudaErrorInvalidValue;
         if (rows == 8)
             e = head_dim == 64 ? launch<64, 1>(k_map, v_map, a, num_sms, stream)
@@ -835,7 +860,29 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
             e = head_dim == 64 ? launch<64, 2>(k_map, v_map, a, num_sms, stream)
                                : launch<128, 2>(k_map, v_map, a, num_sms, stream);
     }
-    return e == cudaSuccess ? launch_join(a, head_dim, stream) : e;
+    if (e != cudaSuccess) return e;
+    const AttendArgs<Cut> join{seqs, a.cut, a.shares, a.k_scale, a.v_scale, a.v, a.q, a.q_stride,
+                               a.scale_log2, a.out, a.lse, a.part, a.desc};
+    return launch_join(join, head_dim, stream);
+}
+
+}  // namespace
+
+// window 0: every token sees all keys up to its own.
+cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* v, const float* k_scale,
+                             const float* v_scale, int heads, int head_dim, const uint16_t* q, int64_t q_stride,
+                             int q_heads, float softmax_scale, int window, int sinks, uint16_t* out, float* lse,
+                             void* workspace, int num_sms, cudaStream_t stream) {
+    const int group = q_heads / heads;
+    const float scale_log2 = softmax_scale * kLog2e;
+    if (window == 0) {
+        AttendArgs<Cut> a{seqs, {}, 0, k_scale, v_scale, v, q, q_stride, scale_log2, out, lse, nullptr, nullptr};
+        return launch_rows(a, k, heads, head_dim, group, workspace, num_sms, stream);
+    }
+    AttendArgs<WindowCut> a{seqs, {}, 0, k_scale, v_scale, v, q, q_stride, scale_log2, out, lse, nullptr, nullptr};
+    a.cut.window = window;
+    a.cut.sinks = sinks;
+    return launch_rows(a, k, heads, head_dim, group, workspace, num_sms, stream);
 }
 
 cudaError_t read_attend_status(unsigned int* status) {

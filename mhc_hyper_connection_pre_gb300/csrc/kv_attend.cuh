@@ -28,12 +28,15 @@ struct PartDesc {
     Segment seg;
 };
 
+// C: Cut, or WindowCut for attention with a window.
+template <class C>
 struct AttendArgs {
     Seqs seqs;
-    Cut cut;
+    C cut;
     int shares;
     const float* k_scale;
     const float* v_scale;
+    const uint8_t* v;                         // value codes (with a window: to look once more for NaN)
     const uint16_t* q;
     int64_t q_stride;
     float scale_log2;                         // softmax_scale * log2(e)
@@ -44,7 +47,8 @@ struct AttendArgs {
 };
 
 // Part `slot` of a share: 1 of the tile that it began (it is the owner), 0 of one that it went on with.
-__device__ __forceinline__ float* part_of(const AttendArgs& a, int share, int slot, int D) {
+template <class C>
+__device__ __forceinline__ float* part_of(const AttendArgs<C>& a, int share, int slot, int D) {
     return a.part + (((int64_t)share * 2 + slot) * (D + 1) << a.cut.tile_log2);
 }
 
@@ -108,8 +112,9 @@ struct ThisWarp {
 };
 
 // Finds sequence b for a plan.
+template <class C>
 struct Lookup {
-    const AttendArgs& a;
+    const AttendArgs<C>& a;
     __device__ __forceinline__ int count() const { return a.seqs.B; }
     __device__ __forceinline__ SeqInfo operator()(int b) const { return info_of(span_of(a.seqs, b < a.seqs.B ? b : a.seqs.B - 1)); }
 };
@@ -124,7 +129,8 @@ __device__ __forceinline__ int64_t sum_upto(int64_t x, int lane) {
 }
 
 // With more than 32 sequences a 32nd of them is this many.
-__device__ __forceinline__ int each_of(const AttendArgs& a) { return a.seqs.B <= 32 ? 1 : (a.seqs.B + 31) / 32; }
+template <class C>
+__device__ __forceinline__ int each_of(const AttendArgs<C>& a) { return a.seqs.B <= 32 ? 1 : (a.seqs.B + 31) / 32; }
 
 // More sequences than this are counted by all warps of a block together.  In the
 // one-token kernel, 1 head, up to 100 keys: 200 sequences take 17.4 us, with each
@@ -132,8 +138,9 @@ __device__ __forceinline__ int each_of(const AttendArgs& a) { return a.seqs.B <=
 constexpr int kTogether = 256;
 
 // Units of the sequences of 32nd i, by one warp.
-__device__ inline void count_units(const AttendArgs& a, int i, int lane, int64_t& units) {
-    const Lookup look{a};
+template <class C>
+__device__ inline void count_units(const AttendArgs<C>& a, int i, int lane, int64_t& units) {
+    const Lookup<C> look{a};
     const int each = each_of(a), end = (i + 1) * each < a.seqs.B ? (i + 1) * each : a.seqs.B;
     int64_t n = 0;
 #pragma unroll 1
@@ -149,9 +156,10 @@ __device__ inline void count_units(const AttendArgs& a, int i, int lane, int64_t
 // then the ones of the 32nd in which the share begins.  No block-wide step, and
 // each length is loaded once or twice: what a decode step's latency consists of
 // is loads that wait for one another.
-__device__ inline void find_share(const AttendArgs& a, int share, Plan& p, Shares& shares, int lane,
+template <class C>
+__device__ inline void find_share(const AttendArgs<C>& a, int share, Plan& p, Shares& shares, int lane,
                                   const int64_t* counted = nullptr) {
-    const Lookup look{a};
+    const Lookup<C> look{a};
     const int each = each_of(a), first = lane * each;
     const int end = first + each < a.seqs.B ? first + each : a.seqs.B;
     SeqInfo info{0, 0, 0};
@@ -205,7 +213,8 @@ __device__ inline void find_share(const AttendArgs& a, int share, Plan& p, Share
 
 // Reports lengths and offsets that had to be cut to what the arrays hold: every
 // share's warp looks at some of them when it has nothing else to do.
-__device__ inline void check_sequences(const AttendArgs& a, int share, int lane) {
+template <class C>
+__device__ inline void check_sequences(const AttendArgs<C>& a, int share, int lane) {
     bool bad = share == 0 && lane == 0 && a.seqs.cu && (a.seqs.cu[0] != 0 || a.seqs.cu[a.seqs.B] != a.seqs.T);
 #pragma unroll 1
     for (int i = share * 32 + lane; i < a.seqs.B; i += a.shares * 32) bad = bad || span_of(a.seqs, i).bad;
@@ -234,7 +243,8 @@ __device__ __forceinline__ void report_abort(volatile int* abort) {
 __device__ __forceinline__ void block_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
 
 // Row r of a segment's tile: its place in out and lse.
-__device__ __forceinline__ int64_t place_of(const AttendArgs& a, const Segment& s, int r) {
+template <class C>
+__device__ __forceinline__ int64_t place_of(const AttendArgs<C>& a, const Segment& s, int r) {
     int token, in_group;
     row_of(s, a.cut, r, token, in_group);
     return (int64_t)token * (a.cut.heads * a.cut.group) + s.head * a.cut.group + in_group;

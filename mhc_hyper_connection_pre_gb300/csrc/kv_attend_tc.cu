@@ -188,11 +188,17 @@ struct Ring {
 
 // The bits of keys at .. at + 31 of a step that the row sees: those before the
 // n-th, in blocks of 16 that have a page.
+// (With a window: those from n - window on, or below `sinks` of the step.)
 __device__ __forceinline__ uint32_t seen_bits(int at, int n, uint32_t valid) {
     const int k = n - at;
     const uint32_t v = valid >> (at / 16);
     const uint32_t pages = ((v & 1) ? 0xffffu : 0u) | ((v & 2) ? 0xffff0000u : 0u);
     return k <= 0 ? 0u : (k >= 32 ? pages : pages & ((1u << k) - 1));
+}
+
+__device__ __forceinline__ uint32_t bits_below(int k) { return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1); }
+__device__ __forceinline__ uint32_t window_bits(int at, int n, int window, int sinks) {
+    return ~bits_below(n - window - at) | bits_below(sinks - at);
 }
 
 // The factor that makes a row's products with 16 keys logits in powers of two.
@@ -263,10 +269,45 @@ __device__ __forceinline__ int steps_of(bool split, int keys) {
     return split ? (keys + kTile - 1) / kTile : (keys + kStep - 1) / kStep;
 }
 
-template <int D>
+// NaN for 32 dims (from c * 32 on) of the row that sees the segment's keys up to the n-th, where a
+// value among those that not every row sees is NaN.  Rare, so the codes are read once more: which rows see which
+// keys differs at both ends of a window, and would need a set of keys for each dim.
+template <int D, class C>
+__device__ __noinline__ void nan_dims(const AttendArgs<C>& a, const Segment& s, int c, int n, uint32_t& mask) {
+    const int log2 = a.seqs.page_log2, first = first_seen(s, a.cut);
+    const int32_t* row = a.seqs.table + (int64_t)s.b * a.seqs.width;
+    mask = 0;
+#pragma unroll 1
+    for (int key = s.key0; key < s.keys; ++key) {
+        const int place = place_of_key(s, key);
+        if (!page_seen(place, first, a.cut.sinks, log2)) continue;
+        const int page = __ldg(row + (place >> log2));
+        if (page < 0 || page >= a.seqs.num_pages) continue;
+        const uint8_t* from =
+            a.v + ((((int64_t)page * a.cut.heads + s.head) << log2) + (place & ((1 << log2) - 1))) * D + c * 32;
+        uint32_t found = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t w = nan_bytes(__ldg(reinterpret_cast<const uint32_t*>(from) + i)) >> 7;
+            found |= ((w & 1) | (w >> 7 & 2) | (w >> 14 & 4) | (w >> 21 & 8)) << (4 * i);
+        }
+        if (key_seen(key, n, a.cut)) mask |= found;
+    }
+}
+
+template <int D, class C>
+__device__ __forceinline__ void put_nans(const AttendArgs<C>& a, const Segment& s, int c, int n, uint32_t (&o)[32]) {
+    uint32_t mask;
+    nan_dims<D>(a, s, c, n, mask);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if ((mask >> i) & 1) o[i] = 0x7fc00000u;
+}
+
+template <int D, class C>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_attend_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                        const AttendArgs a) {
+                        const AttendArgs<C> a) {
     extern __shared__ uint8_t raw[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -418,6 +459,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 
                 const int all_see = keys_of_row(seg, a.cut, split ? 0 : x * kTile);
+                [[maybe_unused]] int last_sees = 0;
+                if constexpr (C::kWindow)
+                    last_sees = keys_of_row(seg, a.cut, split || rows < (x + 1) * kTile ? rows - 1 : (x + 1) * kTile - 1);
                 for (int j = 0; j < steps; ++j) {
                     const int buffer = j & 1, half = kStep * (split ? x : buffer);   // of the load
                     ok = __all_sync(0xffffffffu, wait_for(&sm.s_full[x][buffer], (phases >> buffer) & 1, &sm.abort));
@@ -436,10 +480,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < 2; ++c) tmem_regs_ready(s[c]);
-                    if (key + kStep > all_see || (valid & 0xfu) != 0xfu) {
+                    bool part = key + kStep > all_see || (valid & 0xfu) != 0xfu;
+                    if constexpr (C::kWindow) part = part || !keys_all_seen(key, kStep, all_see, last_sees, a.cut);
+                    if (part) {
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const uint32_t bits = seen_bits(c * 32, n, valid);
+                            uint32_t bits = seen_bits(c * 32, n, valid);
+                            if constexpr (C::kWindow) bits &= window_bits(c * 32, n, a.cut.window, a.cut.sinks - key);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) s[c][i] = (bits >> i) & 1 ? s[c][i] : 0xff800000u;
                         }
@@ -569,7 +616,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * unit);
-                    if (nans) {
+                    if constexpr (C::kWindow) {
+                        if (nans) put_nans<D>(a, sm.segs[index], c, lim, o);
+                    } else if (nans) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (sm.nan_key[kept][c * 32 + i] < lim) o[i] = 0x7fc00000u;
@@ -620,7 +669,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int32_t* row = a.seqs.table + (int64_t)seg.b * a.seqs.width;
                 float most = 0.0f;
                 for (int i = (key0 >> log2) + id; i << log2 < keys; i += 128) {
-                    const int page = __ldg(row + i);
+                    int at = i;
+                    if constexpr (C::kWindow) {
+                        const int place = place_of_key(seg, i << log2);
+                        if (!page_seen(place, first_seen(seg, a.cut), a.cut.sinks, log2)) continue;
+                        at = place >> log2;
+                    }
+                    const int page = __ldg(row + at);
                     if (page >= 0 && page < a.seqs.num_pages)
                         most = fmaxf(most, __ldg(a.v_scale + (int64_t)page * a.cut.heads + seg.head));
                 }
@@ -635,6 +690,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 named_bar_sync(1, 128);
                 const float per = most > 0.0f ? __frcp_rn(most) : 0.0f;
                 const int all_see = keys_of_row(seg, a.cut, 0);
+                // whether every row sees `count` keys from `key` on
+                auto all = [&](int key, int count) {
+                    if constexpr (C::kWindow)
+                        return keys_all_seen(key, count, all_see, keys_of_row(seg, a.cut, seg.rows - 1), a.cut);
+                    else return key + count <= all_see;
+                };
                 for (int key = key0; ok && key < keys; key += kTile) {
                     ok = __all_sync(0xffffffffu, wait_for(&sm.v_full[vr.stage], vr.phase, &sm.abort)) &&
                          __all_sync(0xffffffffu, wait_for(&sm.v16_empty[v16r.stage], v16r.phase ^ 1, &sm.abort));
@@ -652,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
                     // a power of two, as mhc_kv_append writes them: exact, or one rounding in f16's subnormals
                     const bool exact = (__float_as_uint(ratio) & 0x7fffffu) == 0 && ratio >= 5.9604645e-8f;
-                    if (__all_sync(0xffffffffu, exact && key + kTile <= all_see)) {
+                    if (__all_sync(0xffffffffu, exact && all(key, kTile))) {
                         const uint32_t times = pack_f16x2(ratio, ratio);
 #pragma unroll 1
                         for (int c0 = 0; c0 < D / 16; c0 += 4) {
@@ -677,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint4 u = lds128(src + chunk_at<D>(id, c));
                             uint32_t w[4] = {u.x, u.y, u.z, u.w}, h[8];
                             if (!use) w[0] = w[1] = w[2] = w[3] = 0;
-                            if (key + id >= all_see) {
+                            if (!all(key + id, 1)) {
                                 // NaN must reach only the rows that see this key, but 0 * NaN is
                                 // NaN: it is taken out here and put back as the rows go out
                                 uint32_t any = 0;
@@ -689,10 +750,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                                 if (any) {
                                     sm.has_nan[slot] = 1;
+                                    if constexpr (!C::kWindow) {
 #pragma unroll 1
-                                    for (int b = 0; b < 16; ++b)
-                                        if ((sm.v[vr.stage][chunk_at<D>(id, c) + b] & 0x7f) == 0x7f)
-                                            atomicMin(&sm.nan_key[slot][16 * c + b], key + id);
+                                        for (int b = 0; b < 16; ++b)
+                                            if ((sm.v[vr.stage][chunk_at<D>(id, c) + b] & 0x7f) == 0x7f)
+                                                atomicMin(&sm.nan_key[slot][16 * c + b], key + id);
+                                    }
                                 }
                             }
 #pragma unroll
@@ -726,14 +789,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const Segment seg = sm.segs[index];
                     const int key0 = seg.key0, keys = seg.keys;
                     const int32_t* row = a.seqs.table + (int64_t)seg.b * a.seqs.width;
-                    auto page_at = [&](int key) {   // of this lane's 16 keys of a step
-                        return lane < 8 && key + 16 * lane < keys ? __ldg(row + ((key + 16 * lane) >> log2)) : -1;
+                    // this lane's 16 keys of a step: whether their page is looked at, and which it is
+                    auto looked = [&](int key) {
+                        bool look = lane < 8 && key + 16 * lane < keys;
+                        if constexpr (C::kWindow)
+                            look = look && page_seen(place_of_key(seg, key + 16 * lane), first_seen(seg, a.cut),
+                                                     a.cut.sinks, log2);
+                        return look;
+                    };
+                    auto page_at = [&](int key) {
+                        int place = key + 16 * lane;
+                        if constexpr (C::kWindow) place = place_of_key(seg, place);
+                        return looked(key) ? __ldg(row + (place >> log2)) : -1;
                     };
                     int page = page_at(key0);
                     for (int key = key0; key < keys; key += kTile) {
                         const int ahead = page_at(key + kTile);
                         const bool has = page >= 0 && page < a.seqs.num_pages;
-                        if (lane < 8 && key + 16 * lane < keys && !has) atomicOr(&g_device_status, kIndexError);
+                        if (looked(key) && !has) atomicOr(&g_device_status, kIndexError);
                         const uint32_t valid = __ballot_sync(0xffffffffu, lane < 8 && has);
                         const bool box = lane < 8 && has && (lane & (per_box - 1)) == 0;
                         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, box)) * D << log2;
@@ -847,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) {
                         int n = 0;
 #pragma unroll 1
-                        while (n < kSegments && plan_next(sm.plan, Lookup{a}, a.cut, sm.shares, sm.segs[n])) ++n;
+                        while (n < kSegments && plan_next(sm.plan, Lookup<C>{a}, a.cut, sm.shares, sm.segs[n])) ++n;
                         sm.count = n;
                     }
                 },
@@ -876,8 +949,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) report_abort(&sm.abort);
 }
 
-template <int D>
-cudaError_t launch(const AttendArgs& a, const uint8_t* k, const uint8_t* v, int blocks, cudaStream_t stream) {
+template <int D, class C>
+cudaError_t launch(const AttendArgs<C>& a, const uint8_t* k, const uint8_t* v, int blocks, cudaStream_t stream) {
     CUtensorMap k_map, v_map;
     const int64_t pages = (int64_t)a.seqs.num_pages * a.cut.heads;
     if (!encode_codes(&k_map, k, pages, 1 << a.seqs.page_log2, D, kTile) ||
@@ -885,16 +958,21 @@ cudaError_t launch(const AttendArgs& a, const uint8_t* k, const uint8_t* v, int 
         return cudaErrorInvalidValue;
     const int bytes = (int)sizeof(Smem<D>) + 1024;
     static_assert(sizeof(Smem<D>) + 1024 <= 227 * 1024, "shared memory of a block");
-    const cudaError_t e = cudaFuncSetAttribute(kv_attend_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = cudaFuncSetAttribute(kv_attend_tc_kernel<D, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kv_attend_tc_kernel<D><<<blocks, kThreads, bytes, stream>>>(k_map, v_map, a);
+    kv_attend_tc_kernel<D, C><<<blocks, kThreads, bytes, stream>>>(k_map, v_map, a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attend_tc(const AttendArgs& a, const uint8_t* k, const uint8_t* v, int head_dim, int blocks,
+cudaError_t launch_kv_attend_tc(const AttendArgs<Cut>& a, const uint8_t* k, const uint8_t* v, int head_dim, int blocks,
                                 cudaStream_t stream) {
+    return head_dim == 64 ? launch<64>(a, k, v, blocks, stream) : launch<128>(a, k, v, blocks, stream);
+}
+
+cudaError_t launch_kv_attend_tc(const AttendArgs<WindowCut>& a, const uint8_t* k, const uint8_t* v, int head_dim,
+                                int blocks, cudaStream_t stream) {
     return head_dim == 64 ? launch<64>(a, k, v, blocks, stream) : launch<128>(a, k, v, blocks, stream);
 }
 

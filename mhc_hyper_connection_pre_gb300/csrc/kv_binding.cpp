@@ -337,11 +337,17 @@ PyObject* append(PyObject*, PyObject* const* o, Py_ssize_t n) {
     });
 }
 
+int64_t integer(PyObject* o) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Refused{nullptr, ""};
+    return v;
+}
+
 // attend(q, k codes, v codes, k_scale, v_scale, block_table, seq_lens, cu_q, softmax_scale, out, lse, return_lse,
-// workspace) -> (out, lse)
+// workspace, window, sinks) -> (out, lse)
 PyObject* attend(PyObject*, PyObject* const* o, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        count(n, 13);
+        count(n, 15);
         at::Device dev(at::kCPU);
         const mhc_kv_cache c = cache_of(o + 1, dev);
         const Rows q = rows_of(tensor(o[0], "q"), "q", c, dev);
@@ -352,6 +358,8 @@ PyObject* attend(PyObject*, PyObject* const* o, Py_ssize_t n) {
             scale = PyFloat_AsDouble(o[8]);
             if (PyErr_Occurred()) throw Refused{nullptr, ""};
         }
+        const int64_t window = given(o[13]) ? integer(o[13]) : 0, sinks = integer(o[14]);
+        if (!given(o[13]) && sinks != 0) value_error("sinks go with a window");
         const c10::cuda::CUDAGuard guard(dev);
         const auto stream = c10::cuda::getCurrentCUDAStream(dev.index());
         at::Tensor out, lse, ws;
@@ -376,11 +384,18 @@ PyObject* attend(PyObject*, PyObject* const* o, Py_ssize_t n) {
         } else {
             ws = workspace_for(c, q.heads, s.B, q.tokens, dev, stream);
         }
-        check_status("mhc_kv_attend",
-                     mhc_kv_attend(&c, q.p, q.stride, (int)q.heads, s.table, s.width, s.lens, s.cu, s.B, q.tokens,
-                                   (float)scale, data<uint16_t>(out), lse.defined() ? data<float>(lse) : nullptr,
-                                   ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.numel() : 0,
-                                   stream.stream()));
+        float* const lse_at = lse.defined() ? data<float>(lse) : nullptr;
+        void* const ws_at = ws.defined() ? ws.data_ptr() : nullptr;
+        const size_t ws_bytes = ws.defined() ? (size_t)ws.numel() : 0;
+        if (given(o[13]))
+            check_status("mhc_kv_attend_window",
+                         mhc_kv_attend_window(&c, q.p, q.stride, (int)q.heads, s.table, s.width, s.lens, s.cu, s.B,
+                                              q.tokens, (float)scale, window, sinks, data<uint16_t>(out), lse_at, ws_at,
+                                              ws_bytes, stream.stream()));
+        else
+            check_status("mhc_kv_attend",
+                         mhc_kv_attend(&c, q.p, q.stride, (int)q.heads, s.table, s.width, s.lens, s.cu, s.B, q.tokens,
+                                       (float)scale, data<uint16_t>(out), lse_at, ws_at, ws_bytes, stream.stream()));
         PyObject* a = given(o[9]) ? o[9] : THPVariable_Wrap(std::move(out));
         if (given(o[9])) Py_INCREF(a);
         PyObject* b = given(o[10]) ? o[10] : (lse.defined() ? THPVariable_Wrap(std::move(lse)) : Py_None);

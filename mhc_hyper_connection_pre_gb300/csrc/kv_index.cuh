@@ -130,11 +130,23 @@ struct SeqInfo {
 
 // The cut's sizes; what would be divisions by the group is worked out once.
 struct Cut {
+    static constexpr bool kWindow = false;
     int heads, group;
     int tile_log2, unit_log2;
     int extra;              // units that a tile counts for beside those of its keys
     int group_inv;          // 65536 / group + 1: x / group is x * group_inv >> 16 for x up to 384
     int step_tokens, step_rem;  // rows of a tile / group and % group
+};
+
+// With a window: the token at position p sees the keys j <= p with j > p - window
+// or j < sinks.  A tile's keys that none of its rows sees, whole units of them between
+// the first ones and its first row's window, are left out of its units.  Keys are
+// then counted without them, from 0 on: of a tile those below skip_at are their own
+// places, the others lie `skip` further on.  A row's window and the first keys stay
+// what they are, as its last key moves by as much as its window does.
+struct WindowCut : Cut {
+    static constexpr bool kWindow = true;
+    int window, sinks;      // at most 2^30
 };
 
 MHC_HD Cut make_cut(int heads, int group, int tile_log2, int unit_log2, int extra) {
@@ -165,22 +177,34 @@ struct Tiles {
     int tile, units;
     int token, rem;         // of its row 0: new token of the sequence, query head of the group
     int rows, keys;         // keys: the most that any of its rows sees
+    int skip_at, skip;      // with a window
 };
 
-MHC_HD void tiles_measure(Tiles& t, const SeqInfo& s, const Cut& c) {
+template <class C>
+MHC_HD void tiles_measure(Tiles& t, const SeqInfo& s, const C& c) {
     const int left = s.tokens * c.group - (t.tile << c.tile_log2);
     t.rows = left < 1 << c.tile_log2 ? left : 1 << c.tile_log2;
     const int n = s.before + t.token + ((t.rem + t.rows - 1) * c.group_inv >> 16) + 1;    // its last row's
     t.keys = n < 0 ? 0 : n;
+    if constexpr (C::kWindow) {
+        const int first = s.before + t.token - c.window + 1;     // of its first row's window
+        const int early = ((c.sinks < t.keys ? c.sinks : t.keys) + (1 << c.unit_log2) - 1) >> c.unit_log2;
+        const int gap = (first < 0 ? 0 : first >> c.unit_log2) - early;
+        t.skip_at = early << c.unit_log2;
+        t.skip = gap > 0 ? gap << c.unit_log2 : 0;
+        t.keys -= t.skip;
+    }
     t.units = units_of(t.keys, c);
 }
 
-MHC_HD void tiles_start(Tiles& t, const SeqInfo& s, const Cut& c) {
+template <class C>
+MHC_HD void tiles_start(Tiles& t, const SeqInfo& s, const C& c) {
     t.tile = t.token = t.rem = 0;
     tiles_measure(t, s, c);
 }
 
-MHC_HD void tiles_next(Tiles& t, const SeqInfo& s, const Cut& c) {
+template <class C>
+MHC_HD void tiles_next(Tiles& t, const SeqInfo& s, const C& c) {
     ++t.tile;
     t.token += c.step_tokens;
     t.rem += c.step_rem;
@@ -192,7 +216,8 @@ MHC_HD void tiles_next(Tiles& t, const SeqInfo& s, const Cut& c) {
 }
 
 // Units of all tiles and heads of a sequence.
-MHC_HD int64_t units_of_seq(const SeqInfo& s, const Cut& c) {
+template <class C>
+MHC_HD int64_t units_of_seq(const SeqInfo& s, const C& c) {
     const int tiles = tiles_of(s, c);
     if (tiles == 0) return 0;
     int64_t n = 0;
@@ -238,9 +263,10 @@ struct Segment {
     int b, head;            // sequence, key/value head
     int token, rem;         // row 0 of the tile: new token, query head of the group
     int rows;               // of the tile
-    int see;                // keys before that token
+    int see;                // keys before that token (counted without those that a window leaves out)
     int key0, keys;         // the segment's keys [key0, keys); none where the tile sees none
     int parts, owner;       // shares that the tile's units lie in, the first of them
+    int skip_at, skip;      // with a window: of the tile
 };
 
 // Row r of a segment's tile.
@@ -254,6 +280,29 @@ MHC_HD void row_of(const Segment& s, const Cut& c, int r, int& token, int& in_gr
 MHC_HD int keys_of_row(const Segment& s, const Cut& c, int r) {
     const int n = s.see + ((s.rem + r) * c.group_inv >> 16) + 1;
     return n < 0 ? 0 : n;
+}
+
+// The place in the sequence of a segment's key.
+MHC_HD int place_of_key(const Segment& s, int key) { return key < s.skip_at ? key : key + s.skip; }
+
+// The first place of the windows of the tile's first row, the first of the tile's.
+MHC_HD int first_seen(const Segment& s, const WindowCut& c) {
+    const int n = s.see + s.skip + 1 - c.window;
+    return n < 0 ? 0 : n;
+}
+
+// Whether a row of the tile may see a key of the page that holds `place`: its
+// page is looked at then, and not otherwise.
+MHC_HD bool page_seen(int place, int first, int sinks, int page_log2) {
+    const int begin = place >> page_log2 << page_log2;
+    return begin < sinks || begin + (1 << page_log2) > first;
+}
+
+// Whether a row that sees the keys up to the n-th sees this one, and whether every row of a
+// tile does of which the first and the last row see them up to n0 and n1.
+MHC_HD bool key_seen(int key, int n, const WindowCut& c) { return key < n && (key < c.sinks || n - key <= c.window); }
+MHC_HD bool keys_all_seen(int key, int count, int n0, int n1, const WindowCut& c) {
+    return key + count <= n0 && (key + count <= c.sinks || n1 - key <= c.window);
 }
 
 // A walk over a share's segments.
@@ -270,7 +319,8 @@ MHC_HD void walk_cut(Walk& w) {
 
 // Enters a sequence (with new tokens) at unit r of its part of the line, with
 // `left` units of the share to go.
-MHC_HD void walk_enter(Walk& w, const SeqInfo& s, const Cut& c, int64_t r, int64_t left) {
+template <class C>
+MHC_HD void walk_enter(Walk& w, const SeqInfo& s, const C& c, int64_t r, int64_t left) {
     w.left = left;
     tiles_start(w.t, s, c);
     MHC_ROLLED
@@ -285,7 +335,8 @@ MHC_HD void walk_enter(Walk& w, const SeqInfo& s, const Cut& c, int64_t r, int64
 
 // The next segment; false where the sequence is done (then the caller enters
 // the next one with new tokens, if w.left > 0).
-MHC_HD bool walk_next(Walk& w, const SeqInfo& s, const Cut& c) {
+template <class C>
+MHC_HD bool walk_next(Walk& w, const SeqInfo& s, const C& c) {
     w.left -= w.count;
     if (w.left <= 0) return false;
     w.first = 0;
@@ -309,8 +360,8 @@ struct Plan {
 
 // The plan's next segment, if it has one: a part of a share that has only
 // extra units of a tile is none.  look(b) finds sequence b.
-template <class Look>
-MHC_HD bool plan_next(Plan& p, const Look& look, const Cut& c, const Shares& shares, Segment& s) {
+template <class Look, class C>
+MHC_HD bool plan_next(Plan& p, const Look& look, const C& c, const Shares& shares, Segment& s) {
     MHC_ROLLED
     while (p.w.left > 0) {
         const int end = p.w.first + p.w.count - c.extra;     // of the tile's key units
@@ -323,6 +374,11 @@ MHC_HD bool plan_next(Plan& p, const Look& look, const Cut& c, const Shares& sha
             s.rem = p.w.t.rem;
             s.rows = p.w.t.rows;
             s.see = p.info.before + p.w.t.token;
+            if constexpr (C::kWindow) {
+                s.skip_at = p.w.t.skip_at;
+                s.skip = p.w.t.skip;
+                s.see -= s.skip;
+            }
             s.key0 = first << c.unit_log2;
             s.keys = end << c.unit_log2 < p.w.t.keys ? end << c.unit_log2 : p.w.t.keys;
             if (first == 0 && end == p.w.t.units - c.extra) {

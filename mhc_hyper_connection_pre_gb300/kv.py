@@ -49,6 +49,8 @@ def declare(lib) -> None:
     lib.mhc_kv_append_norm.restype = I
     lib.mhc_kv_attend.argtypes = [C, P, I64, I, P, I64, P, P, I64, I64, F, P, P, P, ctypes.c_size_t, P]
     lib.mhc_kv_attend.restype = I
+    lib.mhc_kv_attend_window.argtypes = [C, P, I64, I, P, I64, P, P, I64, I64, F, I64, I64, P, P, P, ctypes.c_size_t, P]
+    lib.mhc_kv_attend_window.restype = I
     lib.mhc_kv_attend_workspace_bytes.argtypes = [C, I, I64, I64]
     lib.mhc_kv_attend_workspace_bytes.restype = ctypes.c_size_t
 
@@ -137,19 +139,23 @@ def kv_workspace_for(cache: dict, q_heads: int, B: int, T: int, stream=None) -> 
 
 def kv_attend(q: torch.Tensor, cache: dict, block_table: torch.Tensor, seq_lens: torch.Tensor,
               cu_q: torch.Tensor | None = None, *, softmax_scale: float | None = None,
-              out: torch.Tensor | None = None, lse: torch.Tensor | None = None, return_lse: bool = False,
-              workspace: torch.Tensor | None = None, stream=None) -> dict:
-    """Causal attention of the new tokens over the cache (``mhc_kv_attend``).
+              window: int | None = None, sinks: int = 0, out: torch.Tensor | None = None,
+              lse: torch.Tensor | None = None, return_lse: bool = False, workspace: torch.Tensor | None = None,
+              stream=None) -> dict:
+    """Causal attention of the new tokens over the cache (``mhc_kv_attend``, ``mhc_kv_attend_window``).
 
     q bf16 [T, q_heads, head_dim], rotated; q_heads a multiple of the cache's
-    heads.  softmax_scale defaults to head_dim ** -0.5.  Returns {"out": bf16
-    [T, q_heads, head_dim][, "lse": fp32 [T, q_heads]]}; ``out`` and ``lse``
-    may supply them.
+    heads.  softmax_scale defaults to head_dim ** -0.5.  With a ``window`` a
+    token sees the last ``window`` keys up to its own, and the sequence's first
+    ``sinks``; pages of which no new token sees a key need not be there (-1 in
+    the table).  Returns {"out": bf16 [T, q_heads, head_dim][, "lse": fp32 [T,
+    q_heads]]}; ``out`` and ``lse`` may supply them.
     """
     if stream is not None:
         with _on(stream, cache, (*cache.values(), q, out, lse, block_table, seq_lens, cu_q, workspace)):
-            return kv_attend(q, cache, block_table, seq_lens, cu_q, softmax_scale=softmax_scale, out=out, lse=lse,
-                             return_lse=return_lse, workspace=workspace)
+            return kv_attend(q, cache, block_table, seq_lens, cu_q, softmax_scale=softmax_scale, window=window,
+                             sinks=sinks, out=out, lse=lse, return_lse=return_lse, workspace=workspace)
     out, lse = (_module or _load()).attend(q, cache["k"], cache["v"], cache["k_scale"], cache["v_scale"], block_table,
-                                           seq_lens, cu_q, softmax_scale, out, lse, return_lse, workspace)
+                                           seq_lens, cu_q, softmax_scale, out, lse, return_lse, workspace, window,
+                                           sinks)
     return {"out": out} if lse is None else {"out": out, "lse": lse}
