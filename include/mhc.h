@@ -37,8 +37,9 @@ typedef enum mhc_status {
     MHC_ERR_UNSUPPORTED = 2,      /* valid but outside the shapes this library handles */
     MHC_ERR_CUDA = 3,             /* a CUDA runtime call or launch failed               */
     MHC_ERR_TIMEOUT = 4,          /* a bounded device-side wait gave up (see below)      */
-    MHC_ERR_INDEX = 5             /* bad length, page or offset in device data (mhc_kv.h);
+    MHC_ERR_INDEX = 5,            /* bad length, page or offset in device data (mhc_kv.h);
                                      returned by mhc_device_status only                 */
+    MHC_ERR_PAGES = 6             /* no free page was left (mhc_kv_fork); likewise       */
 } mhc_status;
 
 /*
@@ -351,8 +352,9 @@ const char *mhc_status_string(mhc_status status);
  * cluster peers push into it, then frees its tensor memory and returns.
  * Should one of those drain waits also give up, the kernel returns anyway
  * (a copy still in flight is then not waited for).  No test provokes a
- * timeout.  MHC_ERR_INDEX (no timeout, but mhc_kv_append or mhc_kv_attend met
- * an index that mhc_kv.h calls bad since the last call).  MHC_ERR_CUDA if the
+ * timeout.  MHC_ERR_INDEX (no timeout, but one of mhc_kv.h's calls met an
+ * index that mhc_kv.h calls bad since the last call).  MHC_ERR_PAGES (neither,
+ * but mhc_kv_fork had fewer free pages than it was to hand out).  MHC_ERR_CUDA if the
  * synchronisation or the read failed.
  */
 mhc_status mhc_device_status(void);

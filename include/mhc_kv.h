@@ -185,6 +185,84 @@ mhc_status mhc_kv_attend_window(const mhc_kv_cache *cache, const uint16_t *q, in
 /* Workspace bytes mhc_kv_attend needs on the current device (0: none). */
 size_t mhc_kv_attend_workspace_bytes(const mhc_kv_cache *cache, int q_heads, int64_t B, int64_t T);
 
+/*
+ * mhc_kv_fork -- the tables of the next step: place b of its batch goes on with
+ * the tokens of place parents[b] of this one, or, with -1, begins without any.
+ * Beams that follow their parents, several answers to one prompt, sequences
+ * that begin and end, and a plain step (parents NULL: b goes on with b, B ==
+ * B_in) are all of this form.  With n = the parent's length and P =
+ * page_tokens:
+ *   seq_lens_out[b] = n
+ *   Full pages, entries i < n / P, are shared: block_table_out[b][i] is the
+ *     parent's.  With a window (see mhc_kv_attend_window) only those of which a
+ *     token at position n can see a key: (i + 1) P > n - window + 1 or i P <
+ *     sinks; the others become -1.
+ *   A part-filled page (n % P > 0) is gone on with by the first place that has
+ *     it, unless it is held or is also somebody's full page; every other place
+ *     gets a copy: a free page whose slots below n % P, and scales, are the
+ *     original's, in every cache.  Its other slots keep their bytes.
+ *   room[b] further tokens (NULL: room_all for every place) get free pages in
+ *     the entries from ceil(n / P) to ceil((n + room) / P).
+ *   All other entries become -1.
+ * A page is free if block_table_out does not name it by the above and it is not
+ * held: what no place goes on with is free at once, and nothing is kept between
+ * calls.  Free pages are handed out from the lowest number on, in the order of
+ * the places and within a place of the entries.
+ *
+ * So a decoding loop is: mhc_kv_fork with room 1, lengths + 1, mhc_kv_append,
+ * mhc_kv_attend.  Pages for tokens that were not appended are free again in
+ * the next call, as they lie beyond the length.
+ *
+ *  caches     num_caches (1 to 512) caches that share their page numbers, the
+ *             layers of a model: num_pages and page_tokens alike; heads and
+ *             head_dim may differ.  Their arrays must not overlap.
+ *  block_table, seq_lens   [B_in][table_width], [B_in]: of this step
+ *  parents    [B], each -1 to B_in - 1, or NULL
+ *  room       [B], or NULL; not negative.  room_all not negative.
+ *  held       [num_pages] bytes, not zero for pages that others go on using
+ *             (a prefix cache, say), 4-byte aligned, or NULL
+ *  window     1 or more; 0: none, then sinks is 0 as well
+ *  block_table_out, seq_lens_out   [B][table_width], [B]; may be exactly
+ *             block_table and seq_lens if parents is NULL
+ *  workspace  as for mhc_pre_delayed, mhc_kv_fork_workspace_bytes bytes
+ * Bad indices are reported as for mhc_kv_append: a length is taken as the
+ * nearest one that the table can hold, as is a length with its room; a parent
+ * out of range as -1; an entry that is neither a page nor -1 as -1.  -1 is no
+ * page and nothing is reported.  Where free pages run out, entries that should
+ * have one stay -1, and mhc_device_status returns MHC_ERR_PAGES once.
+ * Two kernel launches, and one more for each 64 caches beyond the first.
+ * Errors as mhc_kv_append; MHC_ERR_UNSUPPORTED for num_pages above 2^30 or
+ * B * (table_width + 1) above 2^30 - 1.
+ */
+mhc_status mhc_kv_fork(const mhc_kv_cache *caches, int num_caches, const int32_t *block_table,
+                       int64_t table_width, const int32_t *seq_lens, int64_t B_in,
+                       const int32_t *parents, int64_t B, const int32_t *room, int64_t room_all,
+                       const uint8_t *held, int64_t window, int64_t sinks, int32_t *block_table_out,
+                       int32_t *seq_lens_out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * mhc_kv_compact -- moves the pages in use to the lowest numbers, so that the
+ * caches can be cut to their first *pages pages.  A page is in use if one of
+ * the first ceil(seq_lens[b] / page_tokens) entries of a row names it.  With U
+ * pages in use that are not held, these end up as the U lowest numbers that
+ * are not held: the k-th used one above them moves to the k-th free one among
+ * them, all of its slots and its scales, in every cache.
+ *   block_table_out  the same entries with the pages' new numbers; the others,
+ *                    and those that are no page, -1
+ *   pages            one number: 1 + the highest page in use or held, 0 if none
+ * held pages are not moved, whoever else uses them.  Pages that moved keep
+ * their bytes in their old place too.  block_table_out may be exactly
+ * block_table.  Arguments, bad indices and errors as mhc_kv_fork.
+ */
+mhc_status mhc_kv_compact(const mhc_kv_cache *caches, int num_caches, const int32_t *block_table,
+                          int64_t table_width, const int32_t *seq_lens, int64_t B,
+                          const uint8_t *held, int32_t *block_table_out, int32_t *pages,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of the two calls (0 for sizes that they refuse). */
+size_t mhc_kv_fork_workspace_bytes(int64_t num_pages, int64_t table_width, int64_t B);
+size_t mhc_kv_compact_workspace_bytes(int64_t num_pages);
+
 #ifdef __cplusplus
 }
 #endif

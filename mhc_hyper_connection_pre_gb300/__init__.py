@@ -16,6 +16,8 @@ and, for the attention sublayer between them, a paged 8-bit key/value cache
     kv_cache(num_pages, heads, page_tokens, head_dim) -> dict
     kv_append(cache, k, v, block_table, seq_lens, cu_q=None, ...) -> Tensor | None
     kv_attend(q, cache, block_table, seq_lens, cu_q=None, ...) -> dict
+    kv_fork(caches, block_table, seq_lens, parents=None, ...) -> dict
+    kv_compact(caches, block_table, seq_lens, ...) -> dict
 """
 from __future__ import annotations
 
@@ -27,13 +29,13 @@ import torch
 
 __all__ = ["pre_delayed", "pre_delayed_noalloc", "post", "pre_plan", "device_status", "workspace_for",
            "library_path", "load_library", "MhcError", "SINKHORN_ITERS", "kv_cache", "kv_append", "kv_attend",
-           "kv_workspace_for"]
+           "kv_fork", "kv_compact", "kv_workspace_for"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "_build", "libmhc.so")
 SINKHORN_ITERS = 20
 _STATUS = {0: "MHC_OK", 1: "MHC_ERR_INVALID_ARGUMENT", 2: "MHC_ERR_UNSUPPORTED",
-           3: "MHC_ERR_CUDA", 4: "MHC_ERR_TIMEOUT", 5: "MHC_ERR_INDEX"}
+           3: "MHC_ERR_CUDA", 4: "MHC_ERR_TIMEOUT", 5: "MHC_ERR_INDEX", 6: "MHC_ERR_PAGES"}
 
 _lock = threading.Lock()
 _lib = None
@@ -530,7 +532,8 @@ def seam_host(x: torch.Tensor, y: torch.Tensor, pre_in: torch.Tensor, fn: torch.
 def device_status() -> int:
     """Synchronise the current device and read-and-clear the library's device
     status word (``mhc_device_status``): 0 = OK, 4 = a bounded in-kernel wait
-    timed out since the last check, 5 = a kv call met a bad index."""
+    timed out since the last check, 5 = a kv call met a bad index, 6 =
+    ``kv_fork`` had too few free pages."""
     return load_library().mhc_device_status()
 
 
@@ -552,4 +555,4 @@ def pre_plan(T: int, n: int = 4, C: int = 5120) -> dict:
     return {"kernel": k.value, "grid": g.value, "cluster": c.value, "tokens_per_tile": tt.value}
 
 
-from .kv import kv_append, kv_attend, kv_cache, kv_workspace_for  # noqa: E402  (kv.py uses the helpers above)
+from .kv import kv_append, kv_attend, kv_cache, kv_compact, kv_fork, kv_workspace_for  # noqa: E402  (kv.py uses the helpers above)

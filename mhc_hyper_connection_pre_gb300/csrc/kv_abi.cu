@@ -7,6 +7,7 @@
 #include <algorithm>
 
 #include "kv_index.cuh"
+#include "kv_pages.cuh"
 
 namespace mhc {
 int kv_num_sms();                     // of the current device, 0 on error (mhc_abi.cu)
@@ -21,6 +22,12 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
                              const float* v_scale, int heads, int head_dim, const uint16_t* q, int64_t q_stride,
                              int q_heads, float softmax_scale, int window, int sinks, uint16_t* out, float* lse,
                              void* workspace, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_fork(const mhc_kv_cache* caches, int num_caches, const ForkIn& a, void* workspace, int num_sms,
+                           cudaStream_t stream);
+cudaError_t launch_kv_compact(const mhc_kv_cache* caches, int num_caches, const PagesIn& p, int32_t* top, void* workspace,
+                              int num_sms, cudaStream_t stream);
+size_t kv_fork_workspace(int64_t num_pages, int64_t width, int64_t B);
+size_t kv_compact_workspace(int64_t num_pages);
 size_t kv_attend_workspace(int heads, int head_dim, int q_heads, int64_t B, int64_t T, int num_sms);
 }  // namespace kv
 }  // namespace mhc
@@ -100,6 +107,85 @@ Seqs seqs_of(const mhc_kv_cache* c, const int32_t* block_table, int64_t table_wi
     int log2 = 4;                                        // page_tokens is a power of two from 16 on (check_common)
     while ((1 << log2) < c->page_tokens) ++log2;
     return Seqs{block_table, seq_lens, cu_q, (int)table_width, (int)B, (int)T, log2, (int)c->num_pages};
+}
+
+// The bytes of an array that a call writes (out) or reads.
+struct Extent {
+    uintptr_t begin, end;
+    bool out;
+};
+
+constexpr int kMaxCaches = 512;
+
+// Caches that share page numbers, and the calls' other arrays: n filled of all, which has 4 * kMaxCaches more places.
+// Whether an array that is written overlaps another one.
+bool overlap(const mhc_kv_cache* caches, int num_caches, Extent* all, int n) {
+    for (int i = 0; i < num_caches; ++i) {
+        const mhc_kv_cache& c = caches[i];
+        const int64_t scales = c.num_pages * c.heads * 4, codes = c.num_pages * c.heads * c.page_tokens * c.head_dim;
+        for (const void* p : {(const void*)c.k, (const void*)c.v}) {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+            all[n++] = Extent{at, at + (uintptr_t)codes, true};
+        }
+        for (const void* p : {(const void*)c.k_scale, (const void*)c.v_scale}) {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+            all[n++] = Extent{at, at + (uintptr_t)scales, true};
+        }
+    }
+    std::sort(all, all + n, [](const Extent& a, const Extent& b) { return a.begin < b.begin; });
+    uintptr_t written = 0, read = 0;                     // up to where arrays before this one reach
+    for (int i = 0; i < n; ++i) {
+        if (all[i].begin == all[i].end) continue;
+        if (all[i].begin < written || (all[i].out && all[i].begin < read)) return true;
+        (all[i].out ? written : read) = std::max(all[i].out ? written : read, all[i].end);
+    }
+    return false;
+}
+
+Extent extent(const void* p, int64_t bytes, bool out) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    return Extent{at, p ? at + (uintptr_t)bytes : at, out};
+}
+
+bool pages_sizes_ok(int64_t num_pages, int64_t width, int64_t B) {
+    return num_pages >= 1 && width >= 1 && B >= 0 && num_pages <= kMaxTokens && width <= kMaxTokens && B <= kMaxTokens &&
+           B * (width + 1) < kMaxTokens;
+}
+
+// What mhc_kv_fork and mhc_kv_compact share of their checks.
+mhc_status check_pages(const mhc_kv_cache* caches, int num_caches, const int32_t* block_table, int64_t table_width,
+                       const int32_t* seq_lens, int64_t B_in, int64_t B, const uint8_t* held, const int32_t* table_out) {
+    if (!caches || num_caches < 1 || B_in < 0 || B < 0) return MHC_ERR_INVALID_ARGUMENT;
+    if (num_caches > kMaxCaches) return MHC_ERR_UNSUPPORTED;
+    int64_t heads = 0;
+    for (int i = 0; i < num_caches; ++i) {
+        const mhc_status st = check_common(caches + i, table_width, 0, 0, nullptr);
+        if (st != MHC_OK) return st;
+        if (caches[i].num_pages != caches[0].num_pages || caches[i].page_tokens != caches[0].page_tokens)
+            return MHC_ERR_INVALID_ARGUMENT;
+        heads += caches[i].heads;
+    }
+    if (heads >= 1 << 28 || !pages_sizes_ok(caches[0].num_pages, table_width, B) || B_in > kMaxTokens)
+        return MHC_ERR_UNSUPPORTED;
+    if (B == 0) return MHC_OK;
+    for (int i = 0; i < num_caches; ++i) {
+        for (const void* p : {(const void*)caches[i].k, (const void*)caches[i].v})
+            if (!p || !aligned(p, 16)) return MHC_ERR_INVALID_ARGUMENT;
+        for (const void* p : {(const void*)caches[i].k_scale, (const void*)caches[i].v_scale})
+            if (!p || !aligned(p, 4)) return MHC_ERR_INVALID_ARGUMENT;
+    }
+    for (const void* p : {(const void*)block_table, (const void*)seq_lens})
+        if ((B_in > 0 && !p) || !aligned(p, 4)) return MHC_ERR_INVALID_ARGUMENT;
+    if (!aligned(held, 4) || !table_out || !aligned(table_out, 4)) return MHC_ERR_INVALID_ARGUMENT;
+    return MHC_OK;
+}
+
+mhc::kv::PagesIn pages_of(const mhc_kv_cache* c, const int32_t* block_table, int64_t table_width, const int32_t* seq_lens,
+                          int64_t B_in, int64_t B, const uint8_t* held, int32_t* table_out) {
+    int log2 = 4;
+    while ((1 << log2) < c->page_tokens) ++log2;
+    return mhc::kv::PagesIn{block_table, seq_lens, held, table_out, (int)table_width, (int)B_in, (int)B, log2,
+                            (int)c->num_pages};
 }
 
 // Both attention calls; window 0: none.
@@ -196,6 +282,80 @@ mhc_status mhc_kv_attend(const mhc_kv_cache* cache, const uint16_t* q, int64_t q
                          void* workspace, size_t workspace_bytes, void* stream) {
     return attend(cache, q, q_stride, q_heads, block_table, table_width, seq_lens, cu_q, B, T, softmax_scale, 0, 0, out,
                   lse, workspace, workspace_bytes, stream);
+}
+
+size_t mhc_kv_fork_workspace_bytes(int64_t num_pages, int64_t table_width, int64_t B) {
+    return pages_sizes_ok(num_pages, table_width, B) ? mhc::kv::kv_fork_workspace(num_pages, table_width, B) : 0;
+}
+
+size_t mhc_kv_compact_workspace_bytes(int64_t num_pages) {
+    return pages_sizes_ok(num_pages, 1, 0) ? mhc::kv::kv_compact_workspace(num_pages) : 0;
+}
+
+mhc_status mhc_kv_fork(const mhc_kv_cache* caches, int num_caches, const int32_t* block_table, int64_t table_width,
+                       const int32_t* seq_lens, int64_t B_in, const int32_t* parents, int64_t B, const int32_t* room,
+                       int64_t room_all, const uint8_t* held, int64_t window, int64_t sinks, int32_t* block_table_out,
+                       int32_t* seq_lens_out, void* workspace, size_t workspace_bytes, void* stream) {
+    mhc_status st = check_pages(caches, num_caches, block_table, table_width, seq_lens, B_in, B, held, block_table_out);
+    if (st != MHC_OK) return st;
+    if (room_all < 0 || window < 0 || sinks < 0 || (window == 0 && sinks != 0) || (!parents && B != B_in))
+        return MHC_ERR_INVALID_ARGUMENT;
+    if (B == 0) return MHC_OK;
+    if (!aligned(parents, 4) || !aligned(room, 4) || !seq_lens_out || !aligned(seq_lens_out, 4))
+        return MHC_ERR_INVALID_ARGUMENT;
+    const size_t need = mhc::kv::kv_fork_workspace(caches->num_pages, table_width, B);
+    if (workspace_bytes < need || !workspace || !aligned(workspace, 256)) return MHC_ERR_INVALID_ARGUMENT;
+    Extent all[9 + 4 * kMaxCaches];
+    int n = 0;
+    if (parents || block_table_out != block_table) all[n++] = extent(block_table, B_in * table_width * 4, false);
+    if (parents || seq_lens_out != seq_lens) all[n++] = extent(seq_lens, B_in * 4, false);
+    all[n++] = extent(parents, B * 4, false);
+    all[n++] = extent(room, B * 4, false);
+    all[n++] = extent(held, caches->num_pages, false);
+    all[n++] = extent(block_table_out, B * table_width * 4, true);
+    all[n++] = extent(seq_lens_out, B * 4, true);
+    all[n++] = extent(workspace, (int64_t)need, true);
+    if (overlap(caches, num_caches, all, n)) return MHC_ERR_INVALID_ARGUMENT;
+    const int sms = mhc::kv_num_sms();
+    if (sms <= 0) return MHC_ERR_CUDA;
+    mhc::kv::ForkIn a;
+    a.p = pages_of(caches, block_table, table_width, seq_lens, B_in, B, held, block_table_out);
+    a.parents = parents;
+    a.room = room;
+    a.room_all = (int)std::min(room_all, kMaxTokens);
+    a.window = (int)std::min(window, kMaxTokens);
+    a.sinks = (int)std::min(sinks, kMaxTokens);
+    a.lens_out = seq_lens_out;
+    return mhc::kv::launch_kv_fork(caches, num_caches, a, workspace, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MHC_OK
+               : MHC_ERR_CUDA;
+}
+
+mhc_status mhc_kv_compact(const mhc_kv_cache* caches, int num_caches, const int32_t* block_table, int64_t table_width,
+                          const int32_t* seq_lens, int64_t B, const uint8_t* held, int32_t* block_table_out,
+                          int32_t* pages, void* workspace, size_t workspace_bytes, void* stream) {
+    mhc_status st = check_pages(caches, num_caches, block_table, table_width, seq_lens, B, B > 0 ? B : 1,
+                                held, B ? block_table_out : pages);
+    if (st != MHC_OK) return st;
+    if (!pages || !aligned(pages, 4)) return MHC_ERR_INVALID_ARGUMENT;
+    const size_t need = mhc::kv::kv_compact_workspace(caches->num_pages);
+    if (workspace_bytes < need || !workspace || !aligned(workspace, 256)) return MHC_ERR_INVALID_ARGUMENT;
+    Extent all[9 + 4 * kMaxCaches];
+    int n = 0;
+    if (block_table_out != block_table) all[n++] = extent(block_table, B * table_width * 4, false);
+    all[n++] = extent(seq_lens, B * 4, false);
+    all[n++] = extent(held, caches->num_pages, false);
+    all[n++] = extent(block_table_out, B * table_width * 4, true);
+    all[n++] = extent(pages, 4, true);
+    all[n++] = extent(workspace, (int64_t)need, true);
+    if (overlap(caches, num_caches, all, n)) return MHC_ERR_INVALID_ARGUMENT;
+    const int sms = mhc::kv_num_sms();
+    if (sms <= 0) return MHC_ERR_CUDA;
+    const mhc::kv::PagesIn p = pages_of(caches, block_table, table_width, seq_lens, B, B, held, block_table_out);
+    return mhc::kv::launch_kv_compact(caches, num_caches, p, pages, workspace, sms, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? MHC_OK
+               : MHC_ERR_CUDA;
 }
 
 }  // extern "C"

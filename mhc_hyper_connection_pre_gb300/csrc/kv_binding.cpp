@@ -19,6 +19,7 @@
 #include <map>
 #include <mutex>
 #include <string>
+#include <tuple>
 #include <utility>
 #include <vector>
 
@@ -135,7 +136,7 @@ void check_cuda(cudaError_t e, const char* what) {
 // and share it.  (A buffer of the capturing allocator alone would not do: it is
 // free again once the call has returned, and outside of PyTorch's own captures
 // to anybody.)
-enum User { kAttend, kPre, kHost, kUsers };      // of the library's calls, each has its own
+enum User { kAttend, kPre, kHost, kPages, kUsers };      // of the library's calls, each has its own
 
 struct Captured {
     at::Tensor memory;
@@ -145,7 +146,7 @@ struct Captured {
 };
 
 std::mutex g_mutex;                                              // of what follows; never held during a CUDA call
-auto* const g_kept = new std::map<std::pair<int, cudaStream_t>, at::Tensor>();    // never destroyed: outlives CUDA
+auto* const g_kept = new std::map<std::tuple<User, int, cudaStream_t>, at::Tensor>();    // never destroyed: outlives CUDA
 auto* const g_captured = new std::vector<Captured*>();           // of graphs that live
 auto* const g_gone = new std::vector<Captured*>();               // of graphs that do not
 
@@ -200,13 +201,11 @@ at::Tensor captured_workspace(User user, size_t need, const at::Device& dev, cud
 
 // The workspace of a device and stream: kept and grown, as a user's program
 // would; of a stream that is being captured, the graph's.
-at::Tensor workspace_for(const mhc_kv_cache& c, int64_t q_heads, int64_t B, int64_t T, const at::Device& dev,
-                         const c10::cuda::CUDAStream& stream) {
-    const size_t need = mhc_kv_attend_workspace_bytes(&c, (int)q_heads, B, T);
+at::Tensor workspace_of(User user, size_t need, const at::Device& dev, const c10::cuda::CUDAStream& stream) {
     if (need == 0) return at::Tensor();
-    at::Tensor t = captured_workspace(kAttend, need, dev, stream.stream());
+    at::Tensor t = captured_workspace(user, need, dev, stream.stream());
     if (t.defined()) return t;
-    const std::pair<int, cudaStream_t> key(dev.index(), stream.stream());
+    const std::tuple<User, int, cudaStream_t> key(user, dev.index(), stream.stream());
     {
         std::lock_guard<std::mutex> lock(g_mutex);
         const at::Tensor& kept = (*g_kept)[key];
@@ -217,6 +216,11 @@ at::Tensor workspace_for(const mhc_kv_cache& c, int64_t q_heads, int64_t B, int6
     std::lock_guard<std::mutex> lock(g_mutex);
     std::swap((*g_kept)[key], old);
     return t;
+}
+
+at::Tensor workspace_for(const mhc_kv_cache& c, int64_t q_heads, int64_t B, int64_t T, const at::Device& dev,
+                         const c10::cuda::CUDAStream& stream) {
+    return workspace_of(kAttend, mhc_kv_attend_workspace_bytes(&c, (int)q_heads, B, T), dev, stream);
 }
 
 void check_status(const char* fn, mhc_status st) {
@@ -425,6 +429,140 @@ PyObject* workspace(PyObject*, PyObject* const* o, Py_ssize_t n) {
     });
 }
 
+// The caches of a sequence of dicts, on one device.
+std::vector<mhc_kv_cache> caches_of(PyObject* o, at::Device& dev) {
+    PyObject* const fast = PySequence_Fast(o, "caches must be a cache or a sequence of caches");
+    if (!fast) throw Refused{nullptr, ""};
+    struct Drop {
+        PyObject* o;
+        ~Drop() { Py_DECREF(o); }
+    } drop{fast};
+    static PyObject* const names[4] = {PyUnicode_InternFromString("k"), PyUnicode_InternFromString("v"),
+                                       PyUnicode_InternFromString("k_scale"), PyUnicode_InternFromString("v_scale")};
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(fast);
+    if (n < 1) value_error("caches must hold at least one cache");
+    std::vector<mhc_kv_cache> all;
+    all.reserve((size_t)n);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        PyObject* const d = PySequence_Fast_GET_ITEM(fast, i);
+        if (!PyDict_Check(d)) type_error("a cache must be a dict of tensors");
+        PyObject* parts[4];
+        for (int j = 0; j < 4; ++j) {
+            parts[j] = PyDict_GetItemWithError(d, names[j]);
+            if (!parts[j]) {
+                if (PyErr_Occurred()) throw Refused{nullptr, ""};
+                value_error("a cache must have 'k', 'v', 'k_scale' and 'v_scale'");
+            }
+        }
+        at::Device on(at::kCPU);
+        all.push_back(cache_of(parts, on));
+        if (i == 0) dev = on;
+        if (on != dev) value_error("the caches must be on one device");
+        if (all[(size_t)i].num_pages != all[0].num_pages || all[(size_t)i].page_tokens != all[0].page_tokens)
+            value_error("the caches must have the same num_pages and page_tokens");
+    }
+    if (n > 0x7fffffff) value_error("too many caches");
+    return all;
+}
+
+// An int32 array of those sizes.
+int32_t* ints_of(const at::Tensor& t, const char* name, std::initializer_list<int64_t> sizes, const at::Device& dev) {
+    check_dense(t, name, at::kInt, dev);
+    if (!t.sizes().equals(at::IntArrayRef(sizes.begin(), sizes.size()))) value_error(std::string(name) + " has the wrong shape");
+    return data<int32_t>(t);
+}
+
+// held: bool or uint8 [num_pages], or None
+const uint8_t* held_of(PyObject* o, const mhc_kv_cache& c, const at::Device& dev) {
+    if (!given(o)) return nullptr;
+    const at::Tensor& t = tensor(o, "held");
+    check_dense(t, "held", t.scalar_type() == at::kByte ? at::kByte : at::kBool, dev);
+    if (t.dim() != 1 || t.size(0) != c.num_pages) value_error("held must be [num_pages]");
+    return static_cast<const uint8_t*>(t.data_ptr());
+}
+
+at::Tensor pages_workspace(PyObject* o, size_t need, const at::Device& dev, const c10::cuda::CUDAStream& stream) {
+    if (!given(o)) return workspace_of(kPages, need, dev, stream);
+    const at::Tensor& t = tensor(o, "workspace");
+    check_dense(t, "workspace", at::kByte, dev);
+    return t;
+}
+
+// What is returned for an output: the tensor that was given, or the new one.
+PyObject* result(PyObject* o, at::Tensor&& t) {
+    if (!given(o)) return THPVariable_Wrap(std::move(t));
+    Py_INCREF(o);
+    return o;
+}
+
+PyObject* pair_of(PyObject* a, PyObject* b) {
+    PyObject* const r = a && b ? PyTuple_Pack(2, a, b) : nullptr;
+    Py_XDECREF(a);
+    Py_XDECREF(b);
+    return r;
+}
+
+// fork(caches, block_table, seq_lens, parents, room, window, sinks, held, out table, out lens, workspace) -> (table, lens)
+PyObject* fork_pages(PyObject*, PyObject* const* o, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        count(n, 11);
+        at::Device dev(at::kCPU);
+        const std::vector<mhc_kv_cache> caches = caches_of(o[0], dev);
+        const Seqs s = seqs_of(o[1], o[2], Py_None, tensor(o[2], "seq_lens").numel(), dev);
+        int64_t B = s.B, room_all = 0;
+        const int32_t *parents = nullptr, *room = nullptr;
+        if (given(o[3])) {
+            const at::Tensor& t = tensor(o[3], "parents");
+            if (t.dim() != 1) value_error("parents must be [B]");
+            B = t.size(0);
+            parents = ints_of(t, "parents", {B}, dev);
+        }
+        if (THPVariable_Check(o[4])) room = ints_of(THPVariable_Unpack(o[4]), "room", {B}, dev);
+        else room_all = integer(o[4]);
+        const int64_t window = given(o[5]) ? integer(o[5]) : 0, sinks = integer(o[6]);
+        if (given(o[5]) && window < 1) value_error("window must be at least 1");
+        if (!given(o[5]) && sinks != 0) value_error("sinks go with a window");
+        const uint8_t* held = held_of(o[7], caches[0], dev);
+        const c10::cuda::CUDAGuard guard(dev);
+        const auto stream = c10::cuda::getCurrentCUDAStream(dev.index());
+        const auto ints = at::TensorOptions().dtype(at::kInt).device(dev);
+        at::Tensor table = given(o[8]) ? tensor(o[8], "out['block_table']") : at::empty({B, s.width}, ints);
+        at::Tensor lens = given(o[9]) ? tensor(o[9], "out['seq_lens']") : at::empty({B}, ints);
+        int32_t* const table_at = ints_of(table, "out['block_table']", {B, s.width}, dev);
+        int32_t* const lens_at = ints_of(lens, "out['seq_lens']", {B}, dev);
+        const at::Tensor ws = pages_workspace(o[10], mhc_kv_fork_workspace_bytes(caches[0].num_pages, s.width, B), dev, stream);
+        check_status("mhc_kv_fork",
+                     mhc_kv_fork(caches.data(), (int)caches.size(), s.table, s.width, s.lens, s.B, parents, B, room,
+                                 room_all, held, window, sinks, table_at, lens_at, ws.defined() ? ws.data_ptr() : nullptr,
+                                 ws.defined() ? (size_t)ws.numel() : 0, stream.stream()));
+        return pair_of(result(o[8], std::move(table)), result(o[9], std::move(lens)));
+    });
+}
+
+// compact(caches, block_table, seq_lens, held, out table, out pages, workspace) -> (table, pages)
+PyObject* compact_pages(PyObject*, PyObject* const* o, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        count(n, 7);
+        at::Device dev(at::kCPU);
+        const std::vector<mhc_kv_cache> caches = caches_of(o[0], dev);
+        const Seqs s = seqs_of(o[1], o[2], Py_None, tensor(o[2], "seq_lens").numel(), dev);
+        const uint8_t* held = held_of(o[3], caches[0], dev);
+        const c10::cuda::CUDAGuard guard(dev);
+        const auto stream = c10::cuda::getCurrentCUDAStream(dev.index());
+        const auto ints = at::TensorOptions().dtype(at::kInt).device(dev);
+        at::Tensor table = given(o[4]) ? tensor(o[4], "out['block_table']") : at::empty({s.B, s.width}, ints);
+        at::Tensor pages = given(o[5]) ? tensor(o[5], "out['pages']") : at::empty({}, ints);
+        int32_t* const table_at = ints_of(table, "out['block_table']", {s.B, s.width}, dev);
+        int32_t* const pages_at = ints_of(pages, "out['pages']", {}, dev);
+        const at::Tensor ws = pages_workspace(o[6], mhc_kv_compact_workspace_bytes(caches[0].num_pages), dev, stream);
+        check_status("mhc_kv_compact",
+                     mhc_kv_compact(caches.data(), (int)caches.size(), s.table, s.width, s.lens, s.B, held, table_at,
+                                    pages_at, ws.defined() ? ws.data_ptr() : nullptr,
+                                    ws.defined() ? (size_t)ws.numel() : 0, stream.stream()));
+        return pair_of(result(o[4], std::move(table)), result(o[5], std::move(pages)));
+    });
+}
+
 // captured(user, bytes, device index, stream): the workspace of the capture that is under way on the stream, or None
 PyObject* captured(PyObject*, PyObject* const* o, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
@@ -453,6 +591,8 @@ PyObject* set_error(PyObject*, PyObject* type) {
 PyMethodDef methods[] = {
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, "mhc_kv_append"},
     {"attend", (PyCFunction)(void (*)(void))attend, METH_FASTCALL, "mhc_kv_attend"},
+    {"fork", (PyCFunction)(void (*)(void))fork_pages, METH_FASTCALL, "mhc_kv_fork"},
+    {"compact", (PyCFunction)(void (*)(void))compact_pages, METH_FASTCALL, "mhc_kv_compact"},
     {"workspace", (PyCFunction)(void (*)(void))workspace, METH_FASTCALL, "a workspace for attend"},
     {"captured", (PyCFunction)(void (*)(void))captured, METH_FASTCALL, "a workspace of a capture"},
     {"set_error", set_error, METH_O, "the exception for a status that is not MHC_OK"},

@@ -1,0 +1,357 @@
+// kv_pages.cuh -- which pages the next step's tables name (mhc_kv_fork), and
+// which pages move where when a cache is compacted (mhc_kv_compact): the
+// planning of both calls, written for a team of threads and free of device code,
+// so that it can be compiled and checked on the host, under a race detector too.
+//
+// A team T has `rank` of `size` threads (a power of two), sync(), a barrier after
+// which all see what each has written, scan(x, total), the sum of x over the ranks
+// below and over all (a collective that ends in a barrier), and load, set_bits,
+// lower and raise, which may meet one another on one word.
+//
+// Nothing is kept between calls: a page is in use if the tables name it or `held`
+// says so, and the pages that are handed out are the lowest others, in the order of
+// the places and their entries.  So the results do not depend on the team.
+#pragma once
+
+#include "kv_index.cuh"
+
+namespace mhc {
+namespace kv {
+
+constexpr unsigned int kPagesError = 4u;      // of a status word: no free page left
+constexpr unsigned int kBadIndex = 2u;        // kIndexError
+constexpr int kNobody = 0x7fffffff;
+
+// A page whose first `slots` slots are to be copied, and where to.
+struct PageCopy {
+    int32_t from, to, slots;
+};
+
+// What both calls are given.
+struct PagesIn {
+    const int32_t* table;                     // [B_in][width]
+    const int32_t* lens;                      // [B_in]
+    const uint8_t* held;                      // [num_pages] or null
+    int32_t* out;                             // [B][width]
+    int width, B_in, B;
+    int page_log2, num_pages;
+};
+
+struct ForkIn {
+    PagesIn p;
+    const int32_t* parents;                   // [B] or null: b goes on with b
+    const int32_t* room;                      // [B] or null: room_all
+    int room_all;
+    int window, sinks;                        // window 0: none
+    int32_t* lens_out;                        // [B]
+};
+
+// The planning's scratch.  bits: a bit for each page, in shared or global memory.
+struct ForkSpace {
+    uint32_t* bits;
+    int32_t *source, *len, *tail, *first;     // [B]: place that b goes on with (-1: none), tokens, page that is
+                                              // part-filled (-1: none), first of the pages that it is given
+    int32_t* keeper;                          // [num_pages], written where it is read
+    int32_t* given;                           // pages handed out, in order; as many as may be asked for
+    PageCopy* copies;                         // [B]
+    int32_t* count;                           // of copies
+};
+
+struct CompactSpace {
+    uint32_t* bits;
+    int32_t *mover, *hole, *moved;            // [num_pages]: used pages by rank; free places by rank; where a page is now
+    PageCopy* copies;                         // [num_pages]
+    int32_t* count;                           // of copies
+    int32_t* mark;                            // [2]: how many used pages stay, the first page that may have moved
+};
+
+MHC_HD int pages_for(int64_t tokens, int page_log2) { return (int)((tokens + ((int64_t)1 << page_log2) - 1) >> page_log2); }
+
+MHC_HD int words_of(int num_pages) { return (num_pages + 31) / 32; }
+
+// Bits of word w that are pages.
+MHC_HD uint32_t real_pages(int num_pages, int w) {
+    const int n = num_pages - 32 * w;
+    return n >= 32 ? 0xffffffffu : (1u << n) - 1;
+}
+
+MHC_HD uint32_t held_word(const uint8_t* held, int num_pages, int w) {
+    uint32_t bits = 0;
+    if (!held) return bits;
+    if (num_pages - 32 * w >= 32) {           // 4-byte aligned
+        const uint32_t* from = reinterpret_cast<const uint32_t*>(held) + 8 * (int64_t)w;
+#ifdef __CUDACC__
+#pragma unroll
+#endif
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t x = from[i];
+            const uint32_t y = ((x & 0xff) ? 1u : 0u) | ((x & 0xff00) ? 2u : 0u) | ((x & 0xff0000) ? 4u : 0u) |
+                               ((x & 0xff000000) ? 8u : 0u);
+            bits |= y << (4 * i);
+        }
+        return bits;
+    }
+    for (int i = 0; 32 * w + i < num_pages; ++i) bits |= held[32 * (int64_t)w + i] ? 1u << i : 0u;
+    return bits;
+}
+
+MHC_HD int ones(uint32_t x) {
+#ifdef __CUDA_ARCH__
+    return __popc(x);
+#else
+    return __builtin_popcount(x);
+#endif
+}
+MHC_HD int lowest(uint32_t x) {
+#ifdef __CUDA_ARCH__
+    return __ffs(x) - 1;
+#else
+    return __builtin_ctz(x);
+#endif
+}
+MHC_HD int highest(uint32_t x) {
+#ifdef __CUDA_ARCH__
+    return 31 - __clz(x);
+#else
+    return 31 - __builtin_clz(x);
+#endif
+}
+
+// load(b, i) and then use(b, i, value) for every entry of `rows` rows; four rows'
+// loads are under way at a time.  As many threads take a row as it has entries, or all.
+template <class Team, class Load, class Use>
+MHC_HD void each_entry(const Team& t, int rows, int width, Load&& load, Use&& use) {
+    int log2 = 0;
+    while ((2 << log2) <= t.size && (1 << log2) < width) ++log2;
+    const int lanes = 1 << log2, at_once = t.size >> log2, lane = t.rank & (lanes - 1);
+    MHC_ROLLED
+    for (int64_t b0 = t.rank >> log2; b0 < rows; b0 += 4 * (int64_t)at_once)
+        MHC_ROLLED
+        for (int64_t i = lane; i < width; i += lanes) {
+            int32_t v[4];
+#ifdef __CUDACC__
+#pragma unroll
+#endif
+            for (int j = 0; j < 4; ++j)
+                if (b0 + j * at_once < rows) v[j] = load((int)(b0 + j * at_once), (int)i);
+#ifdef __CUDACC__
+#pragma unroll
+#endif
+            for (int j = 0; j < 4; ++j)
+                if (b0 + j * at_once < rows) use((int)(b0 + j * at_once), (int)i, v[j]);
+        }
+}
+
+// A rank's part of n things in a row.
+template <class Team>
+MHC_HD void part_of_all(const Team& t, int64_t n, int64_t& begin, int64_t& end) {
+    const int64_t each = (n + t.size - 1) / t.size;
+    begin = each * t.rank < n ? each * t.rank : n;
+    end = begin + each < n ? begin + each : n;
+}
+
+// An entry as a page, or -1; anything but a page's number or -1 is reported.
+template <class Team>
+MHC_HD int checked_page(const Team& t, int p, int num_pages) {
+    if (p >= 0 && p < num_pages) return p;
+    if (p != -1) t.report(kBadIndex);
+    return -1;
+}
+
+// A length as the nearest one that a row of the table can hold.
+template <class Team>
+MHC_HD int checked_tokens(const Team& t, int64_t n, int cap) {
+    const int64_t m = n < 0 ? 0 : (n > cap ? cap : n);
+    if (m != n) t.report(kBadIndex);
+    return (int)m;
+}
+
+// Whether the next token after n, or a later one, may see a key of full page i.
+MHC_HD bool page_stays(int i, int n, int window, int sinks, int page_log2) {
+    if (window == 0) return true;
+    const int64_t begin = (int64_t)i << page_log2;
+    return begin < sinks || begin + (1 << page_log2) > (int64_t)n - window + 1;
+}
+
+template <class Team>
+MHC_HD void plan_fork(Team& t, const ForkIn& a, const ForkSpace& s) {
+    const PagesIn& p = a.p;
+    const int log2 = p.page_log2, P = 1 << log2, cap = p.width << log2, words = words_of(p.num_pages);
+
+    // every place: whom it goes on with, its tokens, its part-filled page
+    for (int b = t.rank; b < p.B; b += t.size) {
+        int from = a.parents ? a.parents[b] : b;
+        if (from < -1 || from >= p.B_in) {
+            t.report(kBadIndex);
+            from = -1;
+        }
+        const int n = from < 0 ? 0 : checked_tokens(t, p.lens[from], cap);
+        const int last = n & (P - 1) ? checked_page(t, p.table[(int64_t)from * p.width + (n >> log2)], p.num_pages) : -1;
+        s.source[b] = from;
+        s.len[b] = n;
+        s.tail[b] = last;
+        if (last >= 0) t.store(s.keeper + last, kNobody);
+    }
+    for (int w = t.rank; w < words; w += t.size) s.bits[w] = held_word(p.held, p.num_pages, w);
+    t.sync();
+
+    // full pages are shared
+    each_entry(
+        t, p.B, p.width,
+        [&](int b, int i) -> int32_t {
+            const int n = s.len[b];
+            const bool stays = i < n >> log2 && page_stays(i, n, a.window, a.sinks, log2);
+            return stays ? p.table[(int64_t)s.source[b] * p.width + i] : -1;
+        },
+        [&](int b, int i, int32_t x) {
+            const int page = checked_page(t, x, p.num_pages);
+            if (page >= 0) t.set_bits(s.bits + (page >> 5), 1u << (page & 31));
+            p.out[(int64_t)b * p.width + i] = page;
+        });
+    for (int b = t.rank; b < p.B; b += t.size)
+        if (s.tail[b] >= 0) t.lower(s.keeper + s.tail[b], b);
+    t.sync();
+
+    // A part-filled page stays with the first place that goes on with it, unless somebody else
+    // has it too: as a full page, or held.  What a place is given: a page for its copy, and those of
+    // its further tokens.
+    int64_t begin, end, mine = 0, total;
+    part_of_all(t, p.B, begin, end);
+    auto copied = [&](int b) {                // before any bit of a part-filled page is set, but for those that
+        const int last = s.tail[b];           // their keepers set: nobody else asks for these
+        if (last < 0) return false;
+        return t.load(s.keeper + last) != b || (t.load(s.bits + (last >> 5)) >> (last & 31) & 1);
+    };
+    for (int64_t b = begin; b < end; ++b) {
+        const int n = s.len[b];
+        const int64_t asked = a.room ? a.room[b] : a.room_all;
+        const int now = pages_for(n, log2);
+        const int then = pages_for(checked_tokens(t, n + (asked < 0 ? -1 - (int64_t)n : asked), cap), log2);
+        const bool copy = copied((int)b);
+        s.first[b] = copy ? 1 : 0;            // for now: whether it copies
+        mine += (then > now ? then - now : 0) + (copy ? ((int64_t)1 << 32) + 1 : 0);
+        if (!copy && s.tail[b] >= 0) {
+            t.set_bits(s.bits + (s.tail[b] >> 5), 1u << (s.tail[b] & 31));
+            p.out[b * p.width + (n >> log2)] = s.tail[b];
+        }
+    }
+    int64_t before = t.scan(mine, total);
+    const int64_t wanted = total & 0xffffffff;
+    if (t.rank == 0) *s.count = (int32_t)(total >> 32);
+    for (int64_t b = begin; b < end; ++b) {
+        const int n = s.len[b];
+        const int64_t asked = a.room ? a.room[b] : a.room_all;
+        const int64_t to = (int64_t)n + (asked < 0 ? 0 : asked);
+        const int now = pages_for(n, log2), then = pages_for(to < cap ? to : cap, log2);
+        const bool copy = s.first[b];
+        if (copy) s.copies[before >> 32] = PageCopy{s.tail[b], (int32_t)b, n & (P - 1)};    // `to` follows below
+        s.first[b] = (int32_t)(before & 0xffffffff) << 1 | (copy ? 1 : 0);
+        before += (then > now ? then - now : 0) + (copy ? ((int64_t)1 << 32) + 1 : 0);
+        a.lens_out[b] = n;
+    }
+
+    // the lowest free pages
+    part_of_all(t, words, begin, end);
+    mine = 0;
+    for (int64_t w = begin; w < end; ++w) mine += ones(~t.load(s.bits + w) & real_pages(p.num_pages, (int)w));
+    int64_t k = t.scan(mine, total);
+    for (int64_t w = begin; w < end && k < wanted; ++w) {
+        uint32_t left = ~s.bits[w] & real_pages(p.num_pages, (int)w);
+        for (; left && k < wanted; left &= left - 1) s.given[k++] = 32 * (int32_t)w + lowest(left);
+    }
+    if (t.rank == 0 && total < wanted) t.report(kPagesError);
+    t.sync();
+
+    // and the entries that get them
+    for (int i = t.rank; i < *s.count; i += t.size) {
+        const int b = s.copies[i].to, at = s.first[b] >> 1;
+        const int page = at < total ? s.given[at] : -1;
+        s.copies[i].to = page;
+        p.out[(int64_t)b * p.width + (s.len[b] >> log2)] = page;
+    }
+    const int lanes = t.size < 32 ? t.size : 32;
+    for (int b = t.rank / lanes; b < p.B; b += t.size / lanes) {
+        const int n = s.len[b];
+        const int64_t asked = a.room ? a.room[b] : a.room_all, to = (int64_t)n + (asked < 0 ? 0 : asked);
+        const int now = pages_for(n, log2), then = pages_for(to < cap ? to : cap, log2);
+        const int at = (s.first[b] >> 1) + (s.first[b] & 1) - now;
+        for (int i = now + t.rank % lanes; i < then; i += lanes)
+            p.out[(int64_t)b * p.width + i] = at + i < total ? s.given[at + i] : -1;
+    }
+}
+
+// What is in use and not held goes to the lowest numbers that are not held: the pages there that are
+// free ("holes") take the used ones above, in order.
+template <class Team>
+MHC_HD void plan_compact(Team& t, const PagesIn& p, int32_t* top, const CompactSpace& s) {
+    const int log2 = p.page_log2, cap = p.width << log2, words = words_of(p.num_pages);
+    for (int w = t.rank; w < words; w += t.size) s.bits[w] = 0;
+    if (t.rank == 0) t.store(top, 0);
+    t.sync();
+    auto entry = [&](int b, int i) -> int32_t {
+        const int n = p.lens[b], m = n < 0 ? 0 : (n > cap ? cap : n);
+        return i < pages_for(m, log2) ? p.table[(int64_t)b * p.width + i] : -1;
+    };
+    each_entry(t, p.B, p.width, entry, [&](int, int, int32_t x) {
+        const int page = checked_page(t, x, p.num_pages);
+        if (page >= 0) t.set_bits(s.bits + (page >> 5), 1u << (page & 31));
+    });
+    for (int b = t.rank; b < p.B; b += t.size) checked_tokens(t, p.lens[b], cap);
+    t.sync();
+
+    int64_t begin, end, mine = 0, total;      // in 32 bits each: used pages, and pages, that are not held
+    part_of_all(t, words, begin, end);
+    for (int64_t w = begin; w < end; ++w) {
+        const uint32_t loose = real_pages(p.num_pages, (int)w) & ~held_word(p.held, p.num_pages, (int)w);
+        mine += (int64_t)ones(s.bits[w] & loose) << 32 | ones(loose);
+    }
+    const int64_t before = t.scan(mine, total);
+    const int used = (int)(total >> 32);
+    int l = (int)(before >> 32), r = (int)(before & 0xffffffff), last = -1;
+    for (int64_t w = begin; w < end; ++w) {
+        const uint32_t held = held_word(p.held, p.num_pages, (int)w), loose = real_pages(p.num_pages, (int)w) & ~held;
+        const uint32_t in_use = s.bits[w] & loose;
+        const int count = ones(loose);
+        uint32_t goal = 0;                    // the word's pages among the lowest `used`
+        if (r + count <= used) {
+            goal = loose;
+        } else if (r < used) {
+            uint32_t rest = loose;
+            for (int i = r; i < used; ++i, rest &= rest - 1) goal |= rest & (0u - rest);
+        }
+        const uint32_t beyond = loose & ~goal;
+        if (beyond && r + ones(goal) == used) {       // the first page beyond them
+            s.mark[0] = l + ones(in_use & goal);
+            s.mark[1] = 32 * (int32_t)w + lowest(beyond);
+        }
+        int hole = r - l, rank = l + ones(in_use & goal);
+        for (uint32_t x = goal & ~in_use; x; x &= x - 1) s.hole[hole++] = 32 * (int32_t)w + lowest(x);
+        for (uint32_t x = in_use & ~goal; x; x &= x - 1) s.mover[rank++] = 32 * (int32_t)w + lowest(x);
+        if (goal | held) last = 32 * (int32_t)w + highest(goal | held);
+        l += ones(in_use);
+        r += count;
+    }
+    if (last >= 0) t.raise(top, last + 1);
+    if (t.rank == 0 && used == (int)(total & 0xffffffff)) {          // every page that is not held is used
+        s.mark[0] = used;
+        s.mark[1] = p.num_pages;
+    }
+    t.sync();
+
+    const int stay = s.mark[0], moves = used - stay, from = s.mark[1];
+    if (t.rank == 0) *s.count = moves;
+    for (int k = t.rank; k < moves; k += t.size) {
+        const int page = s.mover[stay + k];
+        s.moved[page] = s.hole[k];
+        s.copies[k] = PageCopy{page, s.hole[k], 1 << log2};
+    }
+    t.sync();
+    each_entry(t, p.B, p.width, entry, [&](int b, int i, int32_t x) {
+        if (x < 0 || x >= p.num_pages) x = -1;
+        if (x >= from && !(p.held && p.held[x])) x = s.moved[x];
+        p.out[(int64_t)b * p.width + i] = x;
+    });
+}
+
+}  // namespace kv
+}  // namespace mhc

@@ -43,7 +43,9 @@ namespace kv {
 cudaError_t read_append_status(unsigned int* status);
 cudaError_t read_attend_status(unsigned int* status);
 cudaError_t read_attend_tc_status(unsigned int* status);
+cudaError_t read_pages_status(unsigned int* status);
 constexpr unsigned int kIndexError = 2u;   // as in kv_common.cuh
+constexpr unsigned int kPagesError = 4u;   // as in kv_pages.cuh
 }  // namespace kv
 }  // namespace mhc
 
@@ -158,6 +160,7 @@ const char* mhc_status_string(mhc_status s) {
         case MHC_ERR_CUDA: return "MHC_ERR_CUDA: a CUDA runtime call or kernel launch failed";
         case MHC_ERR_TIMEOUT: return "MHC_ERR_TIMEOUT: a bounded device-side wait gave up";
         case MHC_ERR_INDEX: return "MHC_ERR_INDEX: a length, page number or token offset read on the device is out of range";
+        case MHC_ERR_PAGES: return "MHC_ERR_PAGES: no free page was left for a token";
     }
     return "unknown mhc_status";
 }
@@ -172,13 +175,15 @@ mhc_status mhc_device_status(void) {
     if (mhc::read_device_status(&v) != cudaSuccess) return MHC_ERR_CUDA;
     if (mhc::read_decode_status(&w) != cudaSuccess) return MHC_ERR_CUDA;
     if (mhc::read_collapse_status(&c) != cudaSuccess) return MHC_ERR_CUDA;
-    unsigned int ka = 0, kt = 0, kc = 0;
+    unsigned int ka = 0, kt = 0, kc = 0, kp = 0;
     if (mhc::kv::read_append_status(&ka) != cudaSuccess) return MHC_ERR_CUDA;
     if (mhc::kv::read_attend_status(&kt) != cudaSuccess) return MHC_ERR_CUDA;
     if (mhc::kv::read_attend_tc_status(&kc) != cudaSuccess) return MHC_ERR_CUDA;
+    if (mhc::kv::read_pages_status(&kp) != cudaSuccess) return MHC_ERR_CUDA;
     kt |= kc;
     if (v | w | c | ((ka | kt) & ~mhc::kv::kIndexError)) return MHC_ERR_TIMEOUT;
-    return (ka | kt) ? MHC_ERR_INDEX : MHC_OK;
+    if (ka | kt | (kp & mhc::kv::kIndexError)) return MHC_ERR_INDEX;
+    return kp & mhc::kv::kPagesError ? MHC_ERR_PAGES : MHC_OK;
 }
 
 mhc_status mhc_pre_delayed_plan(int64_t T, int n, int C, int* kernel, int* grid, int* cluster,

@@ -3,6 +3,8 @@
     kv_cache(num_pages, heads, page_tokens, head_dim) -> dict
     kv_append(cache, k, v, block_table, seq_lens, cu_q=None, q=None, cos=None, sin=None, ...) -> Tensor | None
     kv_attend(q, cache, block_table, seq_lens, cu_q=None, ...) -> dict
+    kv_fork(caches, block_table, seq_lens, parents=None, ...) -> dict
+    kv_compact(caches, block_table, seq_lens, ...) -> dict
 
 A cache is a dict of tensors: "k", "v" float8_e4m3fn [num_pages, heads,
 page_tokens, head_dim] and "k_scale", "v_scale" fp32 [num_pages, heads].
@@ -25,7 +27,7 @@ import torch
 
 from . import MhcError, library_path, load_library
 
-__all__ = ["kv_cache", "kv_append", "kv_attend", "kv_workspace_for"]
+__all__ = ["kv_cache", "kv_append", "kv_attend", "kv_fork", "kv_compact", "kv_workspace_for"]
 
 _lock = threading.Lock()
 _module = None
@@ -51,6 +53,14 @@ def declare(lib) -> None:
     lib.mhc_kv_attend.restype = I
     lib.mhc_kv_attend_window.argtypes = [C, P, I64, I, P, I64, P, P, I64, I64, F, I64, I64, P, P, P, ctypes.c_size_t, P]
     lib.mhc_kv_attend_window.restype = I
+    lib.mhc_kv_fork.argtypes = [C, I, P, I64, P, I64, P, I64, P, I64, P, I64, I64, P, P, P, ctypes.c_size_t, P]
+    lib.mhc_kv_fork.restype = I
+    lib.mhc_kv_compact.argtypes = [C, I, P, I64, P, I64, P, P, P, P, ctypes.c_size_t, P]
+    lib.mhc_kv_compact.restype = I
+    lib.mhc_kv_fork_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.mhc_kv_fork_workspace_bytes.restype = ctypes.c_size_t
+    lib.mhc_kv_compact_workspace_bytes.argtypes = [I64]
+    lib.mhc_kv_compact_workspace_bytes.restype = ctypes.c_size_t
     lib.mhc_kv_attend_workspace_bytes.argtypes = [C, I, I64, I64]
     lib.mhc_kv_attend_workspace_bytes.restype = ctypes.c_size_t
 
@@ -159,3 +169,58 @@ def kv_attend(q: torch.Tensor, cache: dict, block_table: torch.Tensor, seq_lens:
                                            seq_lens, cu_q, softmax_scale, out, lse, return_lse, workspace, window,
                                            sinks)
     return {"out": out} if lse is None else {"out": out, "lse": lse}
+
+
+def _layers(caches, out, tensors, stream):
+    """``_on`` for the calls that take all layers' caches."""
+    if not caches or not all(isinstance(c, dict) for c in caches):
+        raise ValueError("caches must be a cache or a sequence of caches")
+    every = [t for c in caches for t in c.values()] + list((out or {}).values())
+    return _on(stream, caches[0], (*every, *tensors))
+
+
+def kv_fork(caches, block_table: torch.Tensor, seq_lens: torch.Tensor, parents: torch.Tensor | None = None, *,
+            room=0, window: int | None = None, sinks: int = 0, held: torch.Tensor | None = None,
+            out: dict | None = None, workspace: torch.Tensor | None = None, stream=None) -> dict:
+    """The tables of the next step (``mhc_kv_fork``): place b goes on with place parents[b]'s tokens.
+
+    caches: a cache, or the caches of all layers, which share page numbers.
+    parents int32 [B], -1 for a place without tokens, or None (every place goes
+    on with itself).  Full pages are shared, a part-filled one is copied but
+    for the first place that goes on with it.  room: how many further tokens a
+    place gets pages for, a number or int32 [B].  With a ``window`` (and
+    ``sinks``) pages that no later token sees are let go.  held: bool
+    [num_pages], pages that others go on using.  Every other page is free, and
+    handed out from the lowest number on.  Returns {"block_table": int32 [B,
+    width], "seq_lens": int32 [B]}, the lengths without the room; ``out`` may
+    supply them (without parents they may be the call's own).
+    ``device_status()`` is 6 where free pages ran out; the entries are -1 then.
+    """
+    caches = (caches,) if isinstance(caches, dict) else tuple(caches)
+    if stream is not None:
+        with _layers(caches, out, (block_table, seq_lens, parents, room, held, workspace), stream):
+            return kv_fork(caches, block_table, seq_lens, parents, room=room, window=window, sinks=sinks, held=held,
+                           out=out, workspace=workspace)
+    o = out or {}
+    table, lens = (_module or _load()).fork(caches, block_table, seq_lens, parents, room, window, sinks, held,
+                                            o.get("block_table"), o.get("seq_lens"), workspace)
+    return {"block_table": table, "seq_lens": lens}
+
+
+def kv_compact(caches, block_table: torch.Tensor, seq_lens: torch.Tensor, *, held: torch.Tensor | None = None,
+               out: dict | None = None, workspace: torch.Tensor | None = None, stream=None) -> dict:
+    """Move the pages in use to the lowest numbers (``mhc_kv_compact``).
+
+    caches, held as in ``kv_fork``; held pages stay where they are.  Returns
+    {"block_table": int32 [B, width], the tables with the pages' new numbers,
+    "pages": int32 [], how many pages, from the first on, hold all that are in
+    use or held}; ``out`` may supply them (its table may be block_table itself).
+    """
+    caches = (caches,) if isinstance(caches, dict) else tuple(caches)
+    if stream is not None:
+        with _layers(caches, out, (block_table, seq_lens, held, workspace), stream):
+            return kv_compact(caches, block_table, seq_lens, held=held, out=out, workspace=workspace)
+    o = out or {}
+    table, pages = (_module or _load()).compact(caches, block_table, seq_lens, held, o.get("block_table"),
+                                                o.get("pages"), workspace)
+    return {"block_table": table, "pages": pages}

@@ -196,3 +196,272 @@ def test_largest_windows_and_positions(window_shim):
         window_shim.kv_window_walk(_ptr(lens), _ptr(cu), 1 << 23, 1, 1, 7, 1, 1, 8, 7, 4, window, sinks, 0, _ptr(one),
                                    _ptr(one), ctypes.byref(total), ctypes.byref(longest))
         assert total.value == (1 << 23) + 4
+
+
+# -------------------------------------------------------------------- pages ---
+
+def plan_fork(table, lens, pages, log2, parents, room, window, sinks, held):
+    """mhc_kv_fork's definition: (table, lens, copies, status), one place and entry after the other."""
+    P, width, cap = 1 << log2, len(table[0]) if table else 0, (len(table[0]) if table else 0) << log2
+    status = 0
+
+    def page(x):
+        nonlocal status
+        if 0 <= x < pages:
+            return x
+        status |= 2 if x != -1 else 0
+        return -1
+    B = len(lens) if parents is None else len(parents)
+    out, n, source = [[-1] * width for _ in range(B)], [], []
+    for b in range(B):
+        a = b if parents is None else parents[b]
+        if not -1 <= a < len(lens):
+            status, a = status | 2, -1
+        m = lens[a] if a >= 0 else 0
+        if not 0 <= m <= cap:
+            status, m = status | 2, min(max(m, 0), cap)
+        n.append(m)
+        source.append(a)
+    for b in range(B):
+        for i in range(n[b] >> log2):
+            if window == 0 or i * P < sinks or (i + 1) * P > n[b] - window + 1:
+                out[b][i] = page(table[source[b]][i])
+    shared = {x for row in out for x in row if x >= 0} | {x for x in range(pages) if held and held[x]}
+    keep, asks = set(), []
+    for b in range(B):
+        last = page(table[source[b]][n[b] >> log2]) if n[b] % P else -1
+        if last >= 0:
+            if last in shared or last in keep:
+                asks.append((b, n[b] >> log2, last))
+            else:
+                keep.add(last)
+                out[b][n[b] >> log2] = last
+        more = room[b] if isinstance(room, list) else room
+        if more < 0 or n[b] + more > cap:
+            status, more = status | 2, min(max(more, 0), cap - n[b])
+        asks += [(b, i, -1) for i in range(-(-n[b] // P), -(-(n[b] + more) // P))]
+    free = [x for x in range(pages) if x not in shared and x not in keep]
+    copies = []
+    for k, (b, i, last) in enumerate(asks):
+        out[b][i] = free[k] if k < len(free) else -1
+        if last >= 0:
+            copies.append((last, out[b][i], n[b] % P))
+    return out, n, copies, status | (4 if len(asks) > len(free) else 0)
+
+
+def plan_compact(table, lens, pages, log2, held):
+    """mhc_kv_compact's definition: (table, pages, copies, status)."""
+    width = len(table[0]) if table else 0
+    cap, status = width << log2, 0
+    out, used = [[-1] * width for _ in lens], set()
+    for b, m in enumerate(lens):
+        if not 0 <= m <= cap:
+            status, m = status | 2, min(max(m, 0), cap)
+        for i in range(-(-m >> log2) if m % (1 << log2) == 0 else (m >> log2) + 1):
+            x = table[b][i]
+            if 0 <= x < pages:
+                out[b][i] = x
+                used.add(x)
+            elif x != -1:
+                status |= 2
+    stay = {x for x in range(pages) if held and held[x]}
+    loose = sorted(used - stay)
+    goal = [x for x in range(pages) if x not in stay][:len(loose)]
+    moves = dict(zip([x for x in loose if x not in set(goal)], [x for x in goal if x not in used]))
+    out = [[moves.get(x, x) for x in row] for row in out]
+    return out, 1 + max([-1, *goal, *stay]), [(a, b, 1 << log2) for a, b in moves.items()], status
+
+
+@pytest.fixture(scope="module")
+def pages_exe(tmp_path_factory):
+    """The planning with the address and with the thread sanitizer."""
+    at = tmp_path_factory.mktemp("pages")
+    for kind in ("address,undefined", "thread"):
+        subprocess.run(["g++", "-O1", "-g", "-std=c++17", f"-fsanitize={kind}", "-fno-sanitize-recover=all",
+                        os.path.join(HERE, "kv_pages_shim.cpp"), "-o", str(at / kind[:6]), "-pthread"], check=True)
+    return at
+
+
+def _flat(x):
+    return [v for row in x for v in (row if isinstance(row, (list, tuple)) else [row])]
+
+
+def _planned(exe, cases):
+    """Runs cases (their numbers) through an executable; the lines of numbers that it writes."""
+    text = "\n".join(" ".join(str(int(v)) for v in c) for c in cases)
+    r = subprocess.run([str(exe)], input=text, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
+    lines = [[int(v) for v in line.split()] for line in r.stdout.splitlines()]
+    assert len(lines) == len(cases)
+    return lines
+
+
+def _tables(r, wild):
+    """A batch as a few steps leave it: pages shared from the front, part-filled ones too, some let go."""
+    log2, B, width = r.choice([4, 4, 5, 7]), r.choice([1, 1, 2, 5, 17, 40]), r.choice([1, 2, 5, 9, 40])
+    P, pages = 1 << log2, r.choice([1, 31, 32, 33, 64, 100, 500])
+    lens = [r.choice([0, r.randint(0, width * P), r.randint(0, width * P), width * P, P]) for _ in range(B)]
+    lens = [min(n, width * P) for n in lens]
+    table = [[r.randrange(pages) for _ in range(width)] for _ in range(B)]
+    for b in range(1, B):
+        if r.random() < 0.4:                                     # shares its front with another
+            a, k = r.randrange(b), r.randint(0, width)
+            table[b][:k] = table[a][:k]
+            if r.random() < 0.5:
+                lens[b] = lens[a]
+    for row in table:
+        for i in range(width):
+            if r.random() < 0.1:
+                row[i] = -1
+            if wild and r.random() < 0.1:
+                row[i] = r.choice([pages, -2, 2147483647, -2147483648])
+    if wild:
+        lens = [r.choice([n, n, n, -1, width * P + 1, 2147483647, -2147483648]) for n in lens]
+    held = [r.choice([0, 0, 0, 1, 255]) for _ in range(pages)] if r.random() < 0.5 else None
+    return log2, P, pages, width, lens, table, held
+
+
+def _fork_case(r, size, wild):
+    log2, P, pages, width, lens, table, held = _tables(r, wild)
+    B_in, parents = len(lens), None
+    if r.random() < 0.7:
+        parents = [r.randint(-1, B_in - 1) for _ in range(r.choice([1, B_in, 3 * B_in]))]
+        if wild:
+            parents = [r.choice([p, p, B_in, -2, 2147483647, -2147483648]) for p in parents]
+    B = B_in if parents is None else len(parents)
+    room = r.choice([0, 1, r.randint(0, 3 * P), None])
+    if room is None:
+        room = [r.choice([0, 1, r.randint(0, 2 * P)]) for _ in range(B)]
+        if wild:
+            room = [r.choice([x, -1, 2147483647, -2147483648]) for x in room]
+    window = r.choice([0, 0, 1, r.randint(1, width * P)])
+    sinks = r.choice([0, r.randint(0, 3 * P)]) if window else 0
+    in_place = parents is None and r.random() < 0.5
+    numbers = [0, size, width, B_in, B, log2, pages, in_place, held is not None, *_flat(table), *lens, *(held or []),
+               parents is not None, isinstance(room, list), *(parents or []), *(room if isinstance(room, list) else []),
+               0 if isinstance(room, list) else room, window, sinks]
+    out, n, copies, status = plan_fork(table, lens, pages, log2, parents, room, window, sinks, held)
+    return numbers, [*n, *_flat(out), status, len(copies), *_flat(copies)]
+
+
+def _compact_case(r, size, wild):
+    log2, P, pages, width, lens, table, held = _tables(r, wild)
+    B = len(lens)
+    numbers = [1, size, width, B, B, log2, pages, r.random() < 0.5, held is not None, *_flat(table), *lens, *(held or [])]
+    out, top, copies, status = plan_compact(table, lens, pages, log2, held)
+    return numbers, [top, *_flat(out), status, len(copies), *_flat(copies)]
+
+
+@pytest.mark.parametrize("make", [_fork_case, _compact_case])
+@pytest.mark.parametrize("wild", [False, True])
+def test_pages_are_planned_as_defined(pages_exe, make, wild):
+    """One to 64 threads: the definition's tables, lengths, copies and reports, whatever the arrays hold, inside
+    the arrays (a sanitizer ends the program otherwise)."""
+    r = random.Random(7 + wild)
+    cases = [make(r, r.choice([1, 2, 8, 64]), wild) for _ in range(250)]
+    got = _planned(pages_exe / "addres", [c for c, _ in cases])
+    for (_, want), line in zip(cases, got):
+        if line != want:
+            at = next(i for i, (x, y) in enumerate(zip(line, want)) if x != y)
+            raise AssertionError((at, line[at:at + 9], want[at:at + 9]))
+
+
+@pytest.mark.parametrize("make", [_fork_case, _compact_case])
+def test_pages_are_planned_without_races(pages_exe, make):
+    r = random.Random(11)
+    cases = [make(r, r.choice([2, 4, 16]), r.random() < 0.3) for _ in range(60)]
+    got = _planned(pages_exe / "thread", [c for c, _ in cases])
+    assert got == [want for _, want in cases]
+
+
+TABLE, LENS, OUT, OUT_LENS = (FAKE + (i << 32) for i in (20, 21, 22, 23))
+
+
+def _layers(n=2, **kw):
+    at = lambda i: {k: FAKE + ((30 + 4 * i + j) << 32) for j, k in enumerate(("k", "v", "k_scale", "v_scale"))}  # noqa: E731
+    return (kvmod._Cache * n)(*[_cache(**{**at(i), **(kw if i == n - 1 else {})}) for i in range(n)])
+
+
+def _fork(lib, caches=None, **kw):
+    a = dict(num=2, table=TABLE, width=10, lens=LENS, B_in=16, parents=FAKE + (24 << 32), B=20, room=FAKE + (25 << 32),
+             room_all=0, held=FAKE + (26 << 32), window=0, sinks=0, out=OUT, out_lens=OUT_LENS, ws=FAKE + (27 << 32),
+             ws_bytes=1 << 30, stream=None)
+    a.update(kw)
+    return lib.mhc_kv_fork(caches if caches is not None else _layers(), *a.values())
+
+
+def _compact(lib, caches=None, **kw):
+    a = dict(num=2, table=TABLE, width=10, lens=LENS, B=16, held=FAKE + (26 << 32), out=OUT, pages=OUT_LENS,
+             ws=FAKE + (27 << 32), ws_bytes=1 << 30, stream=None)
+    a.update(kw)
+    return lib.mhc_kv_compact(caches if caches is not None else _layers(), *a.values())
+
+
+PAGES = [
+    (dict(num=0), {}, INVALID), (dict(num=513), {}, UNSUPPORTED), (dict(width=0), {}, INVALID), (dict(B=-1), {}, INVALID),
+    (dict(table=None), {}, INVALID), (dict(lens=None), {}, INVALID), (dict(table=TABLE + 2), {}, INVALID),
+    (dict(lens=LENS + 1), {}, INVALID), (dict(held=FAKE + (26 << 32) + 1), {}, INVALID), (dict(out=None), {}, INVALID),
+    (dict(out=OUT + 2), {}, INVALID), (dict(ws=None), {}, INVALID), (dict(ws=FAKE + (27 << 32) + 128), {}, INVALID),
+    (dict(ws_bytes=256), {}, INVALID), (dict(width=1 << 26, B=16), {}, UNSUPPORTED),
+    ({}, dict(num_pages=101), INVALID), ({}, dict(page_tokens=32), INVALID), ({}, dict(page_tokens=8), UNSUPPORTED),
+    ({}, dict(head_dim=96), UNSUPPORTED), ({}, dict(heads=0), INVALID), ({}, dict(k=None), INVALID),
+    ({}, dict(v=FAKE + (40 << 32) + 8), INVALID), ({}, dict(v_scale=FAKE + (41 << 32) + 2), INVALID),
+    ({}, dict(k=FAKE + (31 << 32) + 16), INVALID),                 # in the first cache's values
+    ({}, dict(k_scale=FAKE + (32 << 32)), INVALID),                # the first cache's scales
+    (dict(out=TABLE + 4), {}, INVALID), (dict(out=LENS), {}, INVALID), (dict(out=FAKE + (30 << 32) + 64), {}, INVALID),
+    (dict(ws=OUT), {}, INVALID), (dict(held=OUT), {}, INVALID), (dict(lens=FAKE + (27 << 32)), {}, INVALID),
+    (dict(lens=FAKE + (32 << 32) + 100), {}, INVALID),
+]
+
+
+@pytest.mark.parametrize("call", [_fork, _compact])
+@pytest.mark.parametrize("case", range(len(PAGES)))
+def test_calls_on_pages_refuse(lib, call, case):
+    kw, c, status = PAGES[case]
+    assert call(lib, _layers(**c), **kw) == status
+
+
+def test_fork_and_compact_refuse(lib):
+    assert _fork(lib, parents=None) == INVALID                     # 16 places become 20 of their own
+    assert _fork(lib, room_all=-1) == INVALID
+    assert _fork(lib, window=-1) == INVALID
+    assert _fork(lib, sinks=-1, window=2) == INVALID
+    assert _fork(lib, sinks=1) == INVALID
+    assert _fork(lib, B_in=-1) == INVALID
+    assert _fork(lib, out_lens=None) == INVALID
+    assert _fork(lib, out_lens=OUT) == INVALID
+    assert _fork(lib, parents=FAKE + (24 << 32) + 2) == INVALID
+    assert _fork(lib, room=FAKE + (25 << 32) + 2) == INVALID
+    assert _fork(lib, out=TABLE) == INVALID                        # in place, with parents
+    assert _fork(lib, out_lens=LENS) == INVALID
+    assert _fork(lib, out_lens=FAKE + (24 << 32)) == INVALID
+    assert _compact(lib, pages=None) == INVALID
+    assert _compact(lib, pages=OUT_LENS + 2) == INVALID
+    assert _compact(lib, pages=OUT + 4) == INVALID
+    assert _compact(lib, pages=LENS + 4) == INVALID
+    assert lib.mhc_kv_fork(None, *[0] * 18) == INVALID and lib.mhc_kv_compact(None, *[0] * 11) == INVALID
+    assert _fork(lib, B_in=0, B=0, parents=None) == OK
+    for f, sizes in ((lib.mhc_kv_fork_workspace_bytes, [(0, 1, 1), (1, 0, 1), (1, 1, -1), ((1 << 30) + 1, 1, 1), (1, 1 << 29, 2)]),
+                     (lib.mhc_kv_compact_workspace_bytes, [(0,), (-1,), ((1 << 30) + 1,)])):
+        assert all(f(*s) == 0 for s in sizes)
+    assert lib.mhc_kv_fork_workspace_bytes(1000, 10, 20) > 4 * 1000 and lib.mhc_kv_compact_workspace_bytes(1000) > 24 * 1000
+
+
+@NO_DEVICE
+def test_calls_on_pages_pass_the_checks(lib):
+    assert _fork(lib) == CUDA_ERR
+    assert _fork(lib, window=100, sinks=4, held=None, room=None, room_all=1 << 40) == CUDA_ERR
+    assert _fork(lib, B_in=0, table=None, lens=None) == CUDA_ERR                   # a first batch
+    assert _fork(lib, parents=None, B=16, out=TABLE, out_lens=LENS) == CUDA_ERR    # in place
+    assert _fork(lib, _layers(1), num=1) == CUDA_ERR
+    assert _fork(lib, _layers(heads=2, head_dim=64)) == CUDA_ERR                   # layers of different heads
+    assert _compact(lib) == CUDA_ERR
+    assert _compact(lib, out=TABLE) == CUDA_ERR
+    assert _compact(lib, B=0, table=None, lens=None, out=None) == CUDA_ERR
+    assert _fork(lib, ws_bytes=lib.mhc_kv_fork_workspace_bytes(100, 10, 20)) == CUDA_ERR
+    assert _compact(lib, ws_bytes=lib.mhc_kv_compact_workspace_bytes(100)) == CUDA_ERR
+    assert _fork(lib, ws_bytes=lib.mhc_kv_fork_workspace_bytes(100, 10, 20) - 1) == INVALID
+
+
+def test_status_string_of_pages_that_ran_out(lib):
+    assert lib.mhc_status_string(6).decode().startswith("MHC_ERR_PAGES")
