@@ -232,7 +232,7 @@ size_t mhc_kv_attend_workspace_bytes(const mhc_kv_cache *cache, int q_heads, int
  * have one stay -1, and mhc_device_status returns MHC_ERR_PAGES once.
  * Two kernel launches, and one more for each 64 caches beyond the first.
  * Errors as mhc_kv_append; MHC_ERR_UNSUPPORTED for num_pages above 2^30 or
- * B * (table_width + 1) above 2^30 - 1.
+ * B * (table_width + 1) or B_in * (table_width + 1) above 2^30 - 1.
  */
 mhc_status mhc_kv_fork(const mhc_kv_cache *caches, int num_caches, const int32_t *block_table,
                        int64_t table_width, const int32_t *seq_lens, int64_t B_in,
@@ -261,7 +261,7 @@ mhc_status mhc_kv_compact(const mhc_kv_cache *caches, int num_caches, const int3
 
 /* Workspace bytes of the two calls (0 for sizes that they refuse). */
 size_t mhc_kv_fork_workspace_bytes(int64_t num_pages, int64_t table_width, int64_t B);
-size_t mhc_kv_compact_workspace_bytes(int64_t num_pages);
+size_t mhc_kv_compact_workspace_bytes(int64_t num_pages, int64_t B);
 
 #ifdef __cplusplus
 }

@@ -27,7 +27,7 @@ cudaError_t launch_kv_fork(const mhc_kv_cache* caches, int num_caches, const For
 cudaError_t launch_kv_compact(const mhc_kv_cache* caches, int num_caches, const PagesIn& p, int32_t* top, void* workspace,
                               int num_sms, cudaStream_t stream);
 size_t kv_fork_workspace(int64_t num_pages, int64_t width, int64_t B);
-size_t kv_compact_workspace(int64_t num_pages);
+size_t kv_compact_workspace(int64_t num_pages, int64_t B);
 size_t kv_attend_workspace(int heads, int head_dim, int q_heads, int64_t B, int64_t T, int num_sms);
 }  // namespace kv
 }  // namespace mhc
@@ -165,7 +165,8 @@ mhc_status check_pages(const mhc_kv_cache* caches, int num_caches, const int32_t
             return MHC_ERR_INVALID_ARGUMENT;
         heads += caches[i].heads;
     }
-    if (heads >= 1 << 28 || !pages_sizes_ok(caches[0].num_pages, table_width, B) || B_in > kMaxTokens)
+    if (heads >= 1 << 28 || !pages_sizes_ok(caches[0].num_pages, table_width, B) ||
+        !pages_sizes_ok(caches[0].num_pages, table_width, B_in))
         return MHC_ERR_UNSUPPORTED;
     if (B == 0) return MHC_OK;
     for (int i = 0; i < num_caches; ++i) {
@@ -288,8 +289,8 @@ size_t mhc_kv_fork_workspace_bytes(int64_t num_pages, int64_t table_width, int64
     return pages_sizes_ok(num_pages, table_width, B) ? mhc::kv::kv_fork_workspace(num_pages, table_width, B) : 0;
 }
 
-size_t mhc_kv_compact_workspace_bytes(int64_t num_pages) {
-    return pages_sizes_ok(num_pages, 1, 0) ? mhc::kv::kv_compact_workspace(num_pages) : 0;
+size_t mhc_kv_compact_workspace_bytes(int64_t num_pages, int64_t B) {
+    return pages_sizes_ok(num_pages, 1, B) ? mhc::kv::kv_compact_workspace(num_pages, B) : 0;
 }
 
 mhc_status mhc_kv_fork(const mhc_kv_cache* caches, int num_caches, const int32_t* block_table, int64_t table_width,
@@ -338,7 +339,7 @@ mhc_status mhc_kv_compact(const mhc_kv_cache* caches, int num_caches, const int3
                                 held, B ? block_table_out : pages);
     if (st != MHC_OK) return st;
     if (!pages || !aligned(pages, 4)) return MHC_ERR_INVALID_ARGUMENT;
-    const size_t need = mhc::kv::kv_compact_workspace(caches->num_pages);
+    const size_t need = mhc::kv::kv_compact_workspace(caches->num_pages, B);
     if (workspace_bytes < need || !workspace || !aligned(workspace, 256)) return MHC_ERR_INVALID_ARGUMENT;
     Extent all[9 + 4 * kMaxCaches];
     int n = 0;

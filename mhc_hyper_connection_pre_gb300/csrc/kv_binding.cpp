@@ -554,7 +554,7 @@ PyObject* compact_pages(PyObject*, PyObject* const* o, Py_ssize_t n) {
         at::Tensor pages = given(o[5]) ? tensor(o[5], "out['pages']") : at::empty({}, ints);
         int32_t* const table_at = ints_of(table, "out['block_table']", {s.B, s.width}, dev);
         int32_t* const pages_at = ints_of(pages, "out['pages']", {}, dev);
-        const at::Tensor ws = pages_workspace(o[6], mhc_kv_compact_workspace_bytes(caches[0].num_pages), dev, stream);
+        const at::Tensor ws = pages_workspace(o[6], mhc_kv_compact_workspace_bytes(caches[0].num_pages, s.B), dev, stream);
         check_status("mhc_kv_compact",
                      mhc_kv_compact(caches.data(), (int)caches.size(), s.table, s.width, s.lens, s.B, held, table_at,
                                     pages_at, ws.defined() ? ws.data_ptr() : nullptr,

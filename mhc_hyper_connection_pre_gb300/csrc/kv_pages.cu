@@ -102,7 +102,11 @@ struct GpuTeam {
         return *const_cast<const volatile T*>(p);
     }
     __device__ __forceinline__ void store(int32_t* p, int32_t x) const { *const_cast<volatile int32_t*>(p) = x; }
-    __device__ __forceinline__ void set_bits(uint32_t* p, uint32_t x) const { atomicOr(p, x); }
+    // Of the pages' bits, which one block has in shared memory.
+    __device__ __forceinline__ void set_bits(uint32_t* p, uint32_t x) const {
+        if constexpr (kOne) asm volatile("red.shared.or.b32 [%0], %1;" ::"r"(smem_u32(p)), "r"(x) : "memory");
+        else atomicOr(p, x);
+    }
     __device__ __forceinline__ void lower(int32_t* p, int32_t x) const { atomicMin(p, x); }
     __device__ __forceinline__ void raise(int32_t* p, int32_t x) const { atomicMax(p, x); }
     __device__ __forceinline__ void report(unsigned int x) const { atomicOr(&g_pages_status, x); }
@@ -114,22 +118,65 @@ __device__ __forceinline__ GpuTeam<kOne> this_team(TeamScratch* scratch, int64_t
     return GpuTeam<kOne>{block * kThreads + (int)threadIdx.x, blocks * kThreads, scratch, totals, 0};
 }
 
+// Shared memory of a block that plans alone, handed out as far as it goes; what
+// does not fit stays in the workspace.
+constexpr int kOwnBytes = 200 * 1024;
+struct Own {
+    uint8_t* at;
+    int left;
+    template <class T>
+    __host__ __device__ void take(T*& p, int64_t n) {
+        const int64_t bytes = (n * (int64_t)sizeof(T) + 15) / 16 * 16;
+        if (bytes > left) return;
+        if (at) {
+            p = reinterpret_cast<T*>(at);
+            at += bytes;
+        }
+        left -= (int)bytes;
+    }
+};
+__host__ __device__ void take_own(ForkSpace& s, const ForkIn& a, Own& own) {
+    own.take(s.bits, words_of(a.p.num_pages));
+    own.take(s.place, a.p.B);
+    own.take(s.first, a.p.B);
+    own.take(s.keeper, a.p.num_pages);
+}
+__host__ __device__ void take_own(CompactSpace& s, const PagesIn& p, Own& own) {
+    own.take(s.bits, words_of(p.num_pages));
+    own.take(s.entries, p.B);
+    own.take(s.moved, p.num_pages);
+    own.take(s.hole, p.num_pages);
+    own.take(s.mover, p.num_pages);
+}
+template <class Space, class In>
+int own_bytes(Space s, const In& in) {
+    Own own{nullptr, kOwnBytes};
+    take_own(s, in, own);
+    return kOwnBytes - own.left;
+}
+
 template <bool kOne>
 __global__ void __launch_bounds__(kThreads, 1) kv_fork_kernel(const ForkIn a, ForkSpace s, int64_t* totals) {
-    extern __shared__ uint32_t own_bits[];
+    extern __shared__ __align__(16) uint8_t own_memory[];
     __shared__ TeamScratch scratch;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the copies wait for this kernel's end
-    if constexpr (kOne) s.bits = own_bits;
+    if constexpr (kOne) {
+        Own own{own_memory, kOwnBytes};
+        take_own(s, a, own);
+    }
     GpuTeam<kOne> team = this_team<kOne>(&scratch, totals);
     plan_fork(team, a, s);
 }
 
 template <bool kOne>
 __global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const PagesIn p, int32_t* top, CompactSpace s, int64_t* totals) {
-    extern __shared__ uint32_t own_bits[];
+    extern __shared__ __align__(16) uint8_t own_memory[];
     __shared__ TeamScratch scratch;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if constexpr (kOne) s.bits = own_bits;
+    if constexpr (kOne) {
+        Own own{own_memory, kOwnBytes};
+        take_own(s, p, own);
+    }
     GpuTeam<kOne> team = this_team<kOne>(&scratch, totals);
     plan_compact(team, p, top, s);
 }
@@ -188,9 +235,7 @@ size_t lay_out(ForkSpace& s, int64_t*& totals, void* base, int64_t num_pages, in
     totals = m.take<int64_t>(2 * kCluster);
     s.count = m.take<int32_t>(1);
     s.bits = m.take<uint32_t>(words_of((int)num_pages));
-    s.source = m.take<int32_t>(B);
-    s.len = m.take<int32_t>(B);
-    s.tail = m.take<int32_t>(B);
+    s.place = m.take<Place>(B);
     s.first = m.take<int32_t>(B);
     s.keeper = m.take<int32_t>(num_pages);
     s.given = m.take<int32_t>(most < num_pages ? most : num_pages);
@@ -198,11 +243,12 @@ size_t lay_out(ForkSpace& s, int64_t*& totals, void* base, int64_t num_pages, in
     return m.used;
 }
 
-size_t lay_out(CompactSpace& s, int64_t*& totals, void* base, int64_t num_pages) {
+size_t lay_out(CompactSpace& s, int64_t*& totals, void* base, int64_t num_pages, int64_t B) {
     Arena m{static_cast<uint8_t*>(base)};
     totals = m.take<int64_t>(2 * kCluster);
     s.count = m.take<int32_t>(1);
     s.mark = m.take<int32_t>(2);
+    s.entries = m.take<int32_t>(B);
     s.bits = m.take<uint32_t>(words_of((int)num_pages));
     s.mover = m.take<int32_t>(num_pages);
     s.hole = m.take<int32_t>(num_pages);
@@ -215,8 +261,7 @@ size_t lay_out(CompactSpace& s, int64_t*& totals, void* base, int64_t num_pages)
 bool one_block(const PagesIn& p) { return (int64_t)p.B * p.width <= 65536 && p.num_pages <= 1 << 20; }
 
 template <class Kernel, class... Args>
-cudaError_t launch_plan(Kernel kernel, bool one, int num_pages, cudaStream_t stream, Args... args) {
-    const int bytes = one ? words_of(num_pages) * 4 : 0;
+cudaError_t launch_plan(Kernel kernel, bool one, int bytes, cudaStream_t stream, Args... args) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -274,10 +319,10 @@ size_t kv_fork_workspace(int64_t num_pages, int64_t width, int64_t B) {
     return lay_out(s, totals, nullptr, num_pages, width, B);
 }
 
-size_t kv_compact_workspace(int64_t num_pages) {
+size_t kv_compact_workspace(int64_t num_pages, int64_t B) {
     CompactSpace s;
     int64_t* totals;
-    return lay_out(s, totals, nullptr, num_pages);
+    return lay_out(s, totals, nullptr, num_pages, B);
 }
 
 cudaError_t launch_kv_fork(const mhc_kv_cache* caches, int num_caches, const ForkIn& a, void* workspace, int num_sms,
@@ -286,8 +331,8 @@ cudaError_t launch_kv_fork(const mhc_kv_cache* caches, int num_caches, const For
     int64_t* totals;
     lay_out(s, totals, workspace, a.p.num_pages, a.p.width, a.p.B);
     const bool one = one_block(a.p);
-    const cudaError_t e = one ? launch_plan(kv_fork_kernel<true>, one, a.p.num_pages, stream, a, s, totals)
-                              : launch_plan(kv_fork_kernel<false>, one, a.p.num_pages, stream, a, s, totals);
+    const cudaError_t e = one ? launch_plan(kv_fork_kernel<true>, one, own_bytes(s, a), stream, a, s, totals)
+                              : launch_plan(kv_fork_kernel<false>, one, 0, stream, a, s, totals);
     return e == cudaSuccess ? launch_copies(caches, num_caches, s.copies, s.count, a.p.B, a.p.page_log2, num_sms, stream) : e;
 }
 
@@ -295,10 +340,10 @@ cudaError_t launch_kv_compact(const mhc_kv_cache* caches, int num_caches, const 
                               int num_sms, cudaStream_t stream) {
     CompactSpace s;
     int64_t* totals;
-    lay_out(s, totals, workspace, p.num_pages);
+    lay_out(s, totals, workspace, p.num_pages, p.B);
     const bool one = one_block(p);
-    const cudaError_t e = one ? launch_plan(kv_compact_kernel<true>, one, p.num_pages, stream, p, top, s, totals)
-                              : launch_plan(kv_compact_kernel<false>, one, p.num_pages, stream, p, top, s, totals);
+    const cudaError_t e = one ? launch_plan(kv_compact_kernel<true>, one, own_bytes(s, p), stream, p, top, s, totals)
+                              : launch_plan(kv_compact_kernel<false>, one, 0, stream, p, top, s, totals);
     // half of the pages at most move
     const int64_t most = p.num_pages / 2 + 1;
     return e == cudaSuccess ? launch_copies(caches, num_caches, s.copies, s.count, most, p.page_log2, num_sms, stream) : e;

@@ -15,6 +15,12 @@
 
 #include "kv_index.cuh"
 
+#ifdef __CUDACC__
+#define MHC_UNROLLED _Pragma("unroll")
+#else
+#define MHC_UNROLLED
+#endif
+
 namespace mhc {
 namespace kv {
 
@@ -37,6 +43,13 @@ struct PagesIn {
     int page_log2, num_pages;
 };
 
+// A place of the batch: where the row begins that it goes on with, its tokens, the
+// first of its full pages that stay (after those of the first tokens), the page that
+// is part-filled (-1: none).
+struct alignas(16) Place {
+    int32_t row, len, low, tail;
+};
+
 struct ForkIn {
     PagesIn p;
     const int32_t* parents;                   // [B] or null: b goes on with b
@@ -46,11 +59,11 @@ struct ForkIn {
     int32_t* lens_out;                        // [B]
 };
 
-// The planning's scratch.  bits: a bit for each page, in shared or global memory.
+// The planning's scratch, in shared or global memory.  bits: a bit for each page.
 struct ForkSpace {
     uint32_t* bits;
-    int32_t *source, *len, *tail, *first;     // [B]: place that b goes on with (-1: none), tokens, page that is
-                                              // part-filled (-1: none), first of the pages that it is given
+    Place* place;                             // [B]
+    int32_t* first;                           // [B]: first of the pages that a place is given, times 2, and whether it copies
     int32_t* keeper;                          // [num_pages], written where it is read
     int32_t* given;                           // pages handed out, in order; as many as may be asked for
     PageCopy* copies;                         // [B]
@@ -59,6 +72,7 @@ struct ForkSpace {
 
 struct CompactSpace {
     uint32_t* bits;
+    int32_t* entries;                         // [B]: of each row, those that name its pages
     int32_t *mover, *hole, *moved;            // [num_pages]: used pages by rank; free places by rank; where a page is now
     PageCopy* copies;                         // [num_pages]
     int32_t* count;                           // of copies
@@ -80,9 +94,7 @@ MHC_HD uint32_t held_word(const uint8_t* held, int num_pages, int w) {
     if (!held) return bits;
     if (num_pages - 32 * w >= 32) {           // 4-byte aligned
         const uint32_t* from = reinterpret_cast<const uint32_t*>(held) + 8 * (int64_t)w;
-#ifdef __CUDACC__
-#pragma unroll
-#endif
+        MHC_UNROLLED
         for (int i = 0; i < 8; ++i) {
             const uint32_t x = from[i];
             const uint32_t y = ((x & 0xff) ? 1u : 0u) | ((x & 0xff00) ? 2u : 0u) | ((x & 0xff0000) ? 4u : 0u) |
@@ -117,28 +129,30 @@ MHC_HD int highest(uint32_t x) {
 #endif
 }
 
-// load(b, i) and then use(b, i, value) for every entry of `rows` rows; four rows'
-// loads are under way at a time.  As many threads take a row as it has entries, or all.
-template <class Team, class Load, class Use>
-MHC_HD void each_entry(const Team& t, int rows, int width, Load&& load, Use&& use) {
+// use(b, i, value) for every entry of `rows` rows, with the entry of `from` that at(b, i) says, -1
+// where that is negative.  As many threads take a row as it has entries, or all, and
+// eight rows' loads are under way at a time.  One block's instructions are what
+// takes its time here, so offsets are 32 bits (checked on the host), and what is a row's
+// is worked out once.
+template <class Team, class At, class Use>
+MHC_HD void each_entry(const Team& t, int rows, int width, const int32_t* from, At&& at, Use&& use) {
+    constexpr int kAhead = 8;
     int log2 = 0;
     while ((2 << log2) <= t.size && (1 << log2) < width) ++log2;
     const int lanes = 1 << log2, at_once = t.size >> log2, lane = t.rank & (lanes - 1);
     MHC_ROLLED
-    for (int64_t b0 = t.rank >> log2; b0 < rows; b0 += 4 * (int64_t)at_once)
+    for (int b0 = t.rank >> log2; b0 < rows; b0 += kAhead * at_once)
         MHC_ROLLED
-        for (int64_t i = lane; i < width; i += lanes) {
-            int32_t v[4];
-#ifdef __CUDACC__
-#pragma unroll
-#endif
-            for (int j = 0; j < 4; ++j)
-                if (b0 + j * at_once < rows) v[j] = load((int)(b0 + j * at_once), (int)i);
-#ifdef __CUDACC__
-#pragma unroll
-#endif
-            for (int j = 0; j < 4; ++j)
-                if (b0 + j * at_once < rows) use((int)(b0 + j * at_once), (int)i, v[j]);
+        for (int i = lane; i < width; i += lanes) {
+            int32_t v[kAhead];
+            MHC_UNROLLED
+            for (int j = 0; j < kAhead; ++j) {
+                const int where = b0 + j * at_once < rows ? at(b0 + j * at_once, i) : -1;
+                v[j] = where >= 0 ? from[where] : -1;
+            }
+            MHC_UNROLLED
+            for (int j = 0; j < kAhead; ++j)
+                if (b0 + j * at_once < rows) use(b0 + j * at_once, i, v[j]);
         }
 }
 
@@ -166,11 +180,10 @@ MHC_HD int checked_tokens(const Team& t, int64_t n, int cap) {
     return (int)m;
 }
 
-// Whether the next token after n, or a later one, may see a key of full page i.
-MHC_HD bool page_stays(int i, int n, int window, int sinks, int page_log2) {
-    if (window == 0) return true;
-    const int64_t begin = (int64_t)i << page_log2;
-    return begin < sinks || begin + (1 << page_log2) > (int64_t)n - window + 1;
+// The first page of the window of the next token after n: with no window the first of all.
+MHC_HD int first_page(int n, int window, int page_log2) {
+    const int first = n - window + 1;
+    return window == 0 || first < 0 ? 0 : first >> page_log2;
 }
 
 template <class Team>
@@ -187,29 +200,27 @@ MHC_HD void plan_fork(Team& t, const ForkIn& a, const ForkSpace& s) {
         }
         const int n = from < 0 ? 0 : checked_tokens(t, p.lens[from], cap);
         const int last = n & (P - 1) ? checked_page(t, p.table[(int64_t)from * p.width + (n >> log2)], p.num_pages) : -1;
-        s.source[b] = from;
-        s.len[b] = n;
-        s.tail[b] = last;
+        s.place[b] = Place{from * p.width, n, first_page(n, a.window, log2), last};
         if (last >= 0) t.store(s.keeper + last, kNobody);
     }
     for (int w = t.rank; w < words; w += t.size) s.bits[w] = held_word(p.held, p.num_pages, w);
     t.sync();
 
-    // full pages are shared
+    // full pages are shared, those of the first tokens and of the window
+    const int early = pages_for(a.sinks, log2);
     each_entry(
-        t, p.B, p.width,
-        [&](int b, int i) -> int32_t {
-            const int n = s.len[b];
-            const bool stays = i < n >> log2 && page_stays(i, n, a.window, a.sinks, log2);
-            return stays ? p.table[(int64_t)s.source[b] * p.width + i] : -1;
+        t, p.B, p.width, p.table,
+        [&](int b, int i) {
+            const Place x = s.place[b];
+            return i < x.len >> log2 && (i >= x.low || i < early) ? x.row + i : -1;
         },
         [&](int b, int i, int32_t x) {
             const int page = checked_page(t, x, p.num_pages);
             if (page >= 0) t.set_bits(s.bits + (page >> 5), 1u << (page & 31));
-            p.out[(int64_t)b * p.width + i] = page;
+            p.out[b * p.width + i] = page;
         });
     for (int b = t.rank; b < p.B; b += t.size)
-        if (s.tail[b] >= 0) t.lower(s.keeper + s.tail[b], b);
+        if (s.place[b].tail >= 0) t.lower(s.keeper + s.place[b].tail, b);
     t.sync();
 
     // A part-filled page stays with the first place that goes on with it, unless somebody else
@@ -218,33 +229,33 @@ MHC_HD void plan_fork(Team& t, const ForkIn& a, const ForkSpace& s) {
     int64_t begin, end, mine = 0, total;
     part_of_all(t, p.B, begin, end);
     auto copied = [&](int b) {                // before any bit of a part-filled page is set, but for those that
-        const int last = s.tail[b];           // their keepers set: nobody else asks for these
+        const int last = s.place[b].tail;     // their keepers set: nobody else asks for these
         if (last < 0) return false;
         return t.load(s.keeper + last) != b || (t.load(s.bits + (last >> 5)) >> (last & 31) & 1);
     };
     for (int64_t b = begin; b < end; ++b) {
-        const int n = s.len[b];
+        const int n = s.place[b].len, last = s.place[b].tail;
         const int64_t asked = a.room ? a.room[b] : a.room_all;
         const int now = pages_for(n, log2);
         const int then = pages_for(checked_tokens(t, n + (asked < 0 ? -1 - (int64_t)n : asked), cap), log2);
         const bool copy = copied((int)b);
         s.first[b] = copy ? 1 : 0;            // for now: whether it copies
         mine += (then > now ? then - now : 0) + (copy ? ((int64_t)1 << 32) + 1 : 0);
-        if (!copy && s.tail[b] >= 0) {
-            t.set_bits(s.bits + (s.tail[b] >> 5), 1u << (s.tail[b] & 31));
-            p.out[b * p.width + (n >> log2)] = s.tail[b];
+        if (!copy && last >= 0) {
+            t.set_bits(s.bits + (last >> 5), 1u << (last & 31));
+            p.out[b * p.width + (n >> log2)] = last;
         }
     }
     int64_t before = t.scan(mine, total);
     const int64_t wanted = total & 0xffffffff;
     if (t.rank == 0) *s.count = (int32_t)(total >> 32);
     for (int64_t b = begin; b < end; ++b) {
-        const int n = s.len[b];
+        const int n = s.place[b].len;
         const int64_t asked = a.room ? a.room[b] : a.room_all;
         const int64_t to = (int64_t)n + (asked < 0 ? 0 : asked);
         const int now = pages_for(n, log2), then = pages_for(to < cap ? to : cap, log2);
         const bool copy = s.first[b];
-        if (copy) s.copies[before >> 32] = PageCopy{s.tail[b], (int32_t)b, n & (P - 1)};    // `to` follows below
+        if (copy) s.copies[before >> 32] = PageCopy{s.place[b].tail, (int32_t)b, n & (P - 1)};    // `to` follows below
         s.first[b] = (int32_t)(before & 0xffffffff) << 1 | (copy ? 1 : 0);
         before += (then > now ? then - now : 0) + (copy ? ((int64_t)1 << 32) + 1 : 0);
         a.lens_out[b] = n;
@@ -267,16 +278,17 @@ MHC_HD void plan_fork(Team& t, const ForkIn& a, const ForkSpace& s) {
         const int b = s.copies[i].to, at = s.first[b] >> 1;
         const int page = at < total ? s.given[at] : -1;
         s.copies[i].to = page;
-        p.out[(int64_t)b * p.width + (s.len[b] >> log2)] = page;
+        p.out[b * p.width + (s.place[b].len >> log2)] = page;
     }
-    const int lanes = t.size < 32 ? t.size : 32;
+    // a thread a place where each gets a few pages at most, as far as the call tells
+    const int lanes = t.size < 32 || (!a.room && a.room_all <= 4 * P) ? 1 : 32;
     for (int b = t.rank / lanes; b < p.B; b += t.size / lanes) {
-        const int n = s.len[b];
+        const int n = s.place[b].len;
         const int64_t asked = a.room ? a.room[b] : a.room_all, to = (int64_t)n + (asked < 0 ? 0 : asked);
         const int now = pages_for(n, log2), then = pages_for(to < cap ? to : cap, log2);
         const int at = (s.first[b] >> 1) + (s.first[b] & 1) - now;
         for (int i = now + t.rank % lanes; i < then; i += lanes)
-            p.out[(int64_t)b * p.width + i] = at + i < total ? s.given[at + i] : -1;
+            p.out[b * p.width + i] = at + i < total ? s.given[at + i] : -1;
     }
 }
 
@@ -286,17 +298,14 @@ template <class Team>
 MHC_HD void plan_compact(Team& t, const PagesIn& p, int32_t* top, const CompactSpace& s) {
     const int log2 = p.page_log2, cap = p.width << log2, words = words_of(p.num_pages);
     for (int w = t.rank; w < words; w += t.size) s.bits[w] = 0;
+    for (int b = t.rank; b < p.B; b += t.size) s.entries[b] = pages_for(checked_tokens(t, p.lens[b], cap), log2);
     if (t.rank == 0) t.store(top, 0);
     t.sync();
-    auto entry = [&](int b, int i) -> int32_t {
-        const int n = p.lens[b], m = n < 0 ? 0 : (n > cap ? cap : n);
-        return i < pages_for(m, log2) ? p.table[(int64_t)b * p.width + i] : -1;
-    };
-    each_entry(t, p.B, p.width, entry, [&](int, int, int32_t x) {
+    auto entry = [&](int b, int i) { return i < s.entries[b] ? b * p.width + i : -1; };
+    each_entry(t, p.B, p.width, p.table, entry, [&](int, int, int32_t x) {
         const int page = checked_page(t, x, p.num_pages);
         if (page >= 0) t.set_bits(s.bits + (page >> 5), 1u << (page & 31));
     });
-    for (int b = t.rank; b < p.B; b += t.size) checked_tokens(t, p.lens[b], cap);
     t.sync();
 
     int64_t begin, end, mine = 0, total;      // in 32 bits each: used pages, and pages, that are not held
@@ -346,10 +355,10 @@ MHC_HD void plan_compact(Team& t, const PagesIn& p, int32_t* top, const CompactS
         s.copies[k] = PageCopy{page, s.hole[k], 1 << log2};
     }
     t.sync();
-    each_entry(t, p.B, p.width, entry, [&](int b, int i, int32_t x) {
+    each_entry(t, p.B, p.width, p.table, entry, [&](int b, int i, int32_t x) {
         if (x < 0 || x >= p.num_pages) x = -1;
         if (x >= from && !(p.held && p.held[x])) x = s.moved[x];
-        p.out[(int64_t)b * p.width + i] = x;
+        p.out[b * p.width + i] = x;
     });
 }
 

@@ -59,7 +59,7 @@ def declare(lib) -> None:
     lib.mhc_kv_compact.restype = I
     lib.mhc_kv_fork_workspace_bytes.argtypes = [I64, I64, I64]
     lib.mhc_kv_fork_workspace_bytes.restype = ctypes.c_size_t
-    lib.mhc_kv_compact_workspace_bytes.argtypes = [I64]
+    lib.mhc_kv_compact_workspace_bytes.argtypes = [I64, I64]
     lib.mhc_kv_compact_workspace_bytes.restype = ctypes.c_size_t
     lib.mhc_kv_attend_workspace_bytes.argtypes = [C, I, I64, I64]
     lib.mhc_kv_attend_workspace_bytes.restype = ctypes.c_size_t

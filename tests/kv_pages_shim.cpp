@@ -124,20 +124,20 @@ int main() {
             const std::vector<int32_t> parents = numbers<int32_t>(has_parents ? B : 0), room = numbers<int32_t>(has_room ? B : 0);
             const int room_all = (int)number(), window = (int)number(), sinks = (int)number();
             const int64_t most = (int64_t)B * (width + 1);
-            std::vector<int32_t> source = scratch<int32_t>(B), len = scratch<int32_t>(B), tail = scratch<int32_t>(B),
-                                 first = scratch<int32_t>(B), keeper = scratch<int32_t>(pages),
+            std::vector<Place> place = scratch<Place>(B);
+            std::vector<int32_t> first = scratch<int32_t>(B), keeper = scratch<int32_t>(pages),
                                  out = scratch<int32_t>(most < pages ? most : pages);
             copies = scratch<PageCopy>(B);
             const ForkIn a{p, given(parents), given(room), room_all, window, sinks, in_place ? lens.data() : lens_out.data()};
-            const ForkSpace s{bits.data(), source.data(), len.data(), tail.data(), first.data(), keeper.data(), out.data(),
+            const ForkSpace s{bits.data(), place.data(), first.data(), keeper.data(), out.data(),
                               copies.data(), &count};
             status = run(size, [&](HostTeam& t) { plan_fork(t, a, s); });
             print(in_place ? lens.data() : lens_out.data(), B);
         } else {
             std::vector<int32_t> mover = scratch<int32_t>(pages), hole = scratch<int32_t>(pages), moved = scratch<int32_t>(pages),
-                                 mark = scratch<int32_t>(2);
+                                 mark = scratch<int32_t>(2), entries = scratch<int32_t>(B);
             copies = scratch<PageCopy>(pages);
-            const CompactSpace s{bits.data(), mover.data(), hole.data(), moved.data(), copies.data(), &count, mark.data()};
+            const CompactSpace s{bits.data(), entries.data(), mover.data(), hole.data(), moved.data(), copies.data(), &count, mark.data()};
             status = run(size, [&](HostTeam& t) { plan_compact(t, p, &top, s); });
             std::printf("%d ", top);
         }

@@ -442,9 +442,9 @@ def test_fork_and_compact_refuse(lib):
     assert lib.mhc_kv_fork(None, *[0] * 18) == INVALID and lib.mhc_kv_compact(None, *[0] * 11) == INVALID
     assert _fork(lib, B_in=0, B=0, parents=None) == OK
     for f, sizes in ((lib.mhc_kv_fork_workspace_bytes, [(0, 1, 1), (1, 0, 1), (1, 1, -1), ((1 << 30) + 1, 1, 1), (1, 1 << 29, 2)]),
-                     (lib.mhc_kv_compact_workspace_bytes, [(0,), (-1,), ((1 << 30) + 1,)])):
+                     (lib.mhc_kv_compact_workspace_bytes, [(0, 1), (-1, 1), ((1 << 30) + 1, 1), (1, -1)])):
         assert all(f(*s) == 0 for s in sizes)
-    assert lib.mhc_kv_fork_workspace_bytes(1000, 10, 20) > 4 * 1000 and lib.mhc_kv_compact_workspace_bytes(1000) > 24 * 1000
+    assert lib.mhc_kv_fork_workspace_bytes(1000, 10, 20) > 4 * 1000 and lib.mhc_kv_compact_workspace_bytes(1000, 9) > 24 * 1000
 
 
 @NO_DEVICE
@@ -459,7 +459,7 @@ def test_calls_on_pages_pass_the_checks(lib):
     assert _compact(lib, out=TABLE) == CUDA_ERR
     assert _compact(lib, B=0, table=None, lens=None, out=None) == CUDA_ERR
     assert _fork(lib, ws_bytes=lib.mhc_kv_fork_workspace_bytes(100, 10, 20)) == CUDA_ERR
-    assert _compact(lib, ws_bytes=lib.mhc_kv_compact_workspace_bytes(100)) == CUDA_ERR
+    assert _compact(lib, ws_bytes=lib.mhc_kv_compact_workspace_bytes(100, 16)) == CUDA_ERR
     assert _fork(lib, ws_bytes=lib.mhc_kv_fork_workspace_bytes(100, 10, 20) - 1) == INVALID
 
 
