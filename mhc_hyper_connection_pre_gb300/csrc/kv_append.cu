@@ -100,44 +100,83 @@ __device__ __forceinline__ void rotate(const Turn& w, float (&x)[8], float (&y)[
     }
 }
 
+// Norms.  16 numbers as pairs, for the packed instructions: a number took 12
+// instructions one by one.
+struct Pairs {
+    f32x2 p[8];                               // chunk a, then chunk b
+};
+
+__device__ __forceinline__ f32x2 swapped(f32x2 v) {
+    float lo, hi;
+    split_f32x2(v, lo, hi);
+    return make_f32x2(hi, lo);
+}
+__device__ __forceinline__ f32x2 both(float x) { return make_f32x2(x, x); }
+
+__device__ __forceinline__ Pairs pairs_of(const Raw& raw) {
+    const uint32_t w[8] = {raw.a.x, raw.a.y, raw.a.z, raw.a.w, raw.b.x, raw.b.y, raw.b.z, raw.b.w};
+    Pairs v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.p[i] = bf16x2_to_f32x2(w[i]);
+    return v;
+}
+__device__ __forceinline__ Raw raw_of(const Pairs& v) {
+    return Raw{make_uint4(f32x2_to_bf16x2(v.p[0]), f32x2_to_bf16x2(v.p[1]), f32x2_to_bf16x2(v.p[2]), f32x2_to_bf16x2(v.p[3])),
+               make_uint4(f32x2_to_bf16x2(v.p[4]), f32x2_to_bf16x2(v.p[5]), f32x2_to_bf16x2(v.p[6]), f32x2_to_bf16x2(v.p[7]))};
+}
+
 // The 16 numbers over their head's root mean square, times the head's weights:
 // x * (1 / sqrt(sum of squares / D + eps)) * w, sums and products in fp32.  Called
 // by whole warps; the D / 16 threads of a head add up their squares in a fixed
 // order.  Squares past fp32's range (numbers from 2^60 on) are summed once more from
 // numbers scaled by 2^-70.
 template <int D>
-__device__ __forceinline__ void norm16(const uint16_t* w, const Chunks& at, float eps, float (&x)[8], float (&y)[8]) {
-    constexpr int kLanes = D / 16;
+__device__ __forceinline__ void norm16(const uint16_t* weights, const Chunks& at, float eps, Pairs& v) {
     constexpr float kSmaller = 8.4703295e-22f;                // 2^-70
-    auto squares = [&](float by) {
-        float s = 0.0f;
+    const Pairs w = pairs_of(Raw{__ldg(reinterpret_cast<const uint4*>(weights + at.a)),
+                                 __ldg(reinterpret_cast<const uint4*>(weights + at.b))});
+    auto squares = [&] {
+        f32x2 a = mul_rn2(v.p[0], v.p[0]), b = mul_rn2(v.p[1], v.p[1]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s = fmaf(x[j] * by, x[j] * by, fmaf(y[j] * by, y[j] * by, s));
+        for (int i = 2; i < 8; i += 2) {
+            a = fma_rn2(v.p[i], v.p[i], a);
+            b = fma_rn2(v.p[i + 1], v.p[i + 1], b);
+        }
+        float lo, hi;
+        split_f32x2(add_rn2(a, b), lo, hi);
+        float s = lo + hi;
 #pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        for (int o = D / 32; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         return s;
     };
-    float s = squares(1.0f);
+    float s = squares();
     if (__any_sync(0xffffffffu, s == INFINITY)) {
-        const float small = squares(kSmaller);
-        if (s == INFINITY) {
-            s = small;
-            eps = eps * kSmaller * kSmaller;
+        const bool large = s == INFINITY;
+        const f32x2 by = both(large ? kSmaller : 1.0f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[j] *= kSmaller;
-                y[j] *= kSmaller;
-            }
+        for (int i = 0; i < 8; ++i) v.p[i] = mul_rn2(v.p[i], by);
+        s = squares();
+        if (large) eps = eps * kSmaller * kSmaller;
+    }
+    const f32x2 r = both(rsqrtf(fmaf(s, 1.0f / D, eps)));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.p[i] = mul_rn2(mul_rn2(v.p[i], r), w.p[i]);
+}
+
+// The rotation of normed numbers; sums take the exact second product.
+template <int kMode>
+__device__ __forceinline__ void rotate(const Turn& t, Pairs& v) {
+    const Pairs x = v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (kMode == kHalves) {
+            const int j = 2 * (i & 3);
+            const f32x2 s = i < 4 ? make_f32x2(-t.s[j], -t.s[j + 1]) : make_f32x2(t.s[j], t.s[j + 1]);
+            v.p[i] = fma_rn2(x.p[i], make_f32x2(t.c[j], t.c[j + 1]), mul_rn2(x.p[i ^ 4], s));
+        } else {
+            v.p[i] = fma_rn2(x.p[i], both(t.c[i]), mul_rn2(swapped(x.p[i]), make_f32x2(-t.s[i], t.s[i])));
         }
     }
-    const float r = rsqrtf(fmaf(s, 1.0f / D, eps));
-    float u[8];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(w + at.a)), u);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = x[j] * r * u[j];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(w + at.b)), u);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = y[j] * r * u[j];
 }
 
 // The smallest power of two 2^e with a <= 448 * 2^e = 1.75 * 2^(8+e), e at
@@ -181,7 +220,7 @@ __device__ __forceinline__ float group_max(float v, int group, float* red) {
 // GT threads take one (window, head, k or v), the loads of kAhead steps under
 // way together.
 template <int D, int GT, int kMode, int kAhead, bool kNorm>
-__global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(256, kNorm && kAhead > 1 ? 3 : 4) kv_append_kernel(const AppendArgs a) {
     constexpr int kBlock = 256, kGroups = kBlock / GT;
     constexpr int kLanes = D / 16, kRows = GT / kLanes;               // threads of a head; rows of one step
     __shared__ float red[kBlock / 32];
@@ -211,27 +250,18 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
         const int b = seq_of(a.seqs, t, lane);
         const int pos = pos_of(span_of(a.seqs, b), t);
         const bool turned = at.turned && pos >= 0 && pos < a.rope_rows;       // beyond: reported by the append part
+        const bool normed = kNorm && a.norm[0] && pos >= 0 && (kMode == kPlain || pos < a.rope_rows);    // others stay as they are
         Turn turn;
         if (turned) load_turn(a, pos, lane % kLanes, turn);
 #pragma unroll 1
         for (int base = first; base < end; base += kAhead * kHeads) {
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                if constexpr (kNorm) {                // a row without a place stays as it is
-                    if (a.norm[0] && pos >= 0) {
-                        float x[8], y[8];
-                        unpack8(raw[i].a, x);
-                        unpack8(raw[i].b, y);
-                        norm16<D>(a.norm[0] + (h < end ? h : first) * a.norm_stride[0], at, a.norm_eps, x, y);
-                        if (turned) rotate<kMode>(turn, x, y);
-                        raw[i] = Raw{pack8(x), pack8(y)};
-                    } else if (turned) {
-                        float x[8], y[8];
-                        unpack8(raw[i].a, x);
-                        unpack8(raw[i].b, y);
-                        rotate<kMode>(turn, x, y);
-                        raw[i] = Raw{pack8(x), pack8(y)};
-                    }
+                if (kNorm && normed) {
+                    Pairs v = pairs_of(raw[i]);
+                    norm16<D>(a.norm[0] + (h < end ? h : first) * a.norm_stride[0], at, a.norm_eps, v);
+                    if (turned) rotate<kMode>(turn, v);
+                    raw[i] = raw_of(v);
                 } else if (turned) {
                     float x[8], y[8];
                     unpack8(raw[i].a, x);
@@ -301,12 +331,26 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendArgs a) {
                         break;
                     }
                     float x[8], y[8];
+                    if (kNorm && kv == 0 && a.norm[1]) {
+                        Pairs v = pairs_of(raw[i]);
+                        norm16<D>(a.norm[1] + head * a.norm_stride[1], at, a.norm_eps, v);
+                        if (r >= n) break;
+                        if (kMode != kPlain && at.turned) {
+                            Turn turn;
+                            load_turn(a, run.pos + r, lane % kLanes, turn);
+                            rotate<kMode>(turn, v);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            split_f32x2(v.p[j], x[2 * j], x[2 * j + 1]);
+                            split_f32x2(v.p[4 + j], y[2 * j], y[2 * j + 1]);
+                        }
+                        f(r, x, y);
+                        continue;
+                    }
+                    if (kNorm && r >= n) break;
                     unpack8(raw[i].a, x);
                     unpack8(raw[i].b, y);
-                    if constexpr (kNorm) {
-                        if (kv == 0 && a.norm[1]) norm16<D>(a.norm[1] + head * a.norm_stride[1], at, a.norm_eps, x, y);
-                        if (r >= n) break;
-                    }
                     if (kMode != kPlain && kv == 0 && at.turned) {
                         Turn turn;
                         load_turn(a, run.pos + r, lane % kLanes, turn);
