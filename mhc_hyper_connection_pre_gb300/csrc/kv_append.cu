@@ -231,11 +231,15 @@ __global__ void __launch_bounds__(256, kNorm && kAhead > 1 ? 3 : 4) kv_append_ke
     };
     const uint4 none = make_uint4(0, 0, 0, 0);
 
-    if ((int)blockIdx.x >= a.kv_blocks) {             // queries: a warp takes one token and some of its heads
+    // blocks of both kinds in turn, then those of which there are more
+    const int kvs = a.kv_blocks, qs = (int)gridDim.x - kvs, paired = 2 * (kvs < qs ? kvs : qs), i = blockIdx.x;
+    const bool is_q = i < paired ? i & 1 : kvs < qs;
+    const uint32_t block = i < paired ? i / 2 : i - paired / 2;
+    if (is_q) {                                       // queries: a warp takes one token and some of its heads
         constexpr int kHeads = 32 / kLanes;           // heads of one step
         const int steps = (a.q_heads + kHeads - 1) / kHeads;
         const uint32_t parts = (steps + a.q_steps - 1) / a.q_steps;
-        const uint32_t w = (blockIdx.x - a.kv_blocks) * (kBlock / 32) + threadIdx.x / 32;
+        const uint32_t w = block * (kBlock / 32) + threadIdx.x / 32;
         const int t = (int)(w / parts), part = (int)(w % parts);
         if (t >= a.seqs.T) return;
         const int first = part * a.q_steps * kHeads;
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(256, kNorm && kAhead > 1 ? 3 : 4) kv_append_ke
     }
 
     const int group = threadIdx.x / GT, id = threadIdx.x % GT;
-    const uint32_t item = blockIdx.x * kGroups + group, pair = item / a.heads;
+    const uint32_t item = block * kGroups + group, pair = item / a.heads;
     const int head = (int)(item % a.heads), kv = (int)(pair & 1), win = (int)(pair >> 1);
     if (win >= a.windows) return;
     const int64_t next = (int64_t)(win + 1) * a.window;
