@@ -189,7 +189,14 @@ __device__ __forceinline__ float scale_for(float a) {
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+// Infinities as NaN, which is what they are stored as.
+__device__ __forceinline__ void drop_infinities(float (&x)[8], float (&y)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        x[j] = fabsf(x[j]) == INFINITY ? __int_as_float(0x7fc00000) : x[j];
+        y[j] = fabsf(y[j]) == INFINITY ? __int_as_float(0x7fc00000) : y[j];
+    }
+}
 
 template <int GT>
 __device__ __forceinline__ void group_sync(int group) {
@@ -373,23 +380,31 @@ __global__ void __launch_bounds__(256, kNorm && kAhead > 1 ? 3 : 4) kv_append_ke
         uint8_t* code = a.code[kv] + (((int64_t)page * a.heads + head) * D << a.seqs.page_log2);
         const float old = run.slot ? *scale_at : 0.0f;
         float top = 0.0f;
-        each([&](int, const float(&x)[8], const float(&y)[8]) {
+        // the largest magnitude, NaN left out; infinities, which are rare, only in a further round
+        bool infinite = false;
+#pragma unroll 1
+        for (;;) {
+            each([&](int, float(&x)[8], float(&y)[8]) {
+                if (infinite) drop_infinities(x, y);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                top = finite(x[j]) ? fmaxf(top, fabsf(x[j])) : top;
-                top = finite(y[j]) ? fmaxf(top, fabsf(y[j])) : top;
-            }
-        });
-        top = group_max<GT>(top, group, red);
+                for (int j = 0; j < 8; ++j) top = fmaxf(top, fmaxf(fabsf(x[j]), fabsf(y[j])));
+            });
+            top = group_max<GT>(top, group, red);
+            if (top != INFINITY) break;               // the same for the whole group
+            infinite = true;
+            top = 0.0f;
+            fetch_all(r0);
+        }
         const float need = scale_for(top), scale = run.slot ? fmaxf(old, need) : need;
         const float per = 1.0f / scale;               // scales are powers of two: x * per is x / scale
         if (id == 0) *scale_at = scale;               // every thread has read it: group_max was a barrier
         if (n > kAhead * kRows) fetch_all(r0);
         each([&](int r, float(&x)[8], float(&y)[8]) {
+            if (infinite) drop_infinities(x, y);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                x[j] = finite(x[j]) ? x[j] * per : __int_as_float(0x7fc00000);
-                y[j] = finite(y[j]) ? y[j] * per : __int_as_float(0x7fc00000);
+                x[j] *= per;
+                y[j] *= per;
             }
             uint8_t* to = code + (run.slot + r) * D;
             *reinterpret_cast<uint2*>(to + at.a) = make_uint2(e4m3x4(x, 0), e4m3x4(x, 4));
