@@ -1,15 +1,18 @@
 // kv_pages.cu -- the pages of the next step (mhc_kv_fork) and moving the pages in
-// use to the lowest numbers (mhc_kv_compact): one launch that plans, by the
-// threads of one block or of one cluster (kv_pages.cuh), and one that copies.
+// use to the lowest numbers (mhc_kv_compact): one block plans (kv_pages.cuh), a further
+// launch copies; the rows of large tables are all SMs' work before that.
 //
 // What bounds it: planning reads and writes the tables once, a few hundred KB at
-// most; its time is a chain of dependent loads (parent, length, entry) and of
-// barriers, whose number is fixed.  Copying is memory: every byte of the copied
-// slots is read and written once, 16 bytes a lane, by warps that take one page,
-// head and tensor of one layer at a time.
+// most; its time is a chain of dependent loads (parent, length, entry), of barriers,
+// and one block's instructions.  A cluster of eight blocks that met in global memory was slower
+// at every size: 256 rows of 47 entries 22.5 us, one block 15.4; 2048 rows of 128 169 and 90.
+// Copying is memory: every byte of the copied slots is read and written once, 16 bytes a lane,
+// by warps that take one page, head and tensor of one layer at a time.
 #include "../../include/mhc_kv.h"
 
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "kv_common.cuh"
 #include "kv_pages.cuh"
@@ -22,8 +25,8 @@ static __device__ unsigned int g_pages_status = 0;
 
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kCluster = 8;                   // blocks of the large team
+constexpr int kThreads = 1024, kWarps = kThreads / 32;    // of the block that plans
+constexpr int kRowThreads = 256;              // of a block that takes rows of large tables
 
 // Caches that one launch copies: the layers that share page numbers.
 constexpr int kMaxSet = 64;
@@ -40,24 +43,14 @@ struct TeamScratch {
     int64_t all;
 };
 
-// One block, or (kOne false) the blocks of one cluster, which meet in global memory.
-template <bool kOne>
-struct GpuTeam {
+// The threads of the one block that plans.
+struct BlockTeam {
     int rank, size;
     TeamScratch* scratch;
-    int64_t* totals;                          // [2][kCluster] in the workspace
-    int scans;
+    bool own_bits;                            // the pages' bits are in shared memory
 
-    __device__ __forceinline__ void sync() const {
-        __syncwarp();
-        if constexpr (kOne) {
-            __syncthreads();
-        } else {
-            cluster_arrive_release();
-            cluster_wait_acquire();
-        }
-    }
-    __device__ __forceinline__ int64_t scan(int64_t x, int64_t& total) {
+    __device__ __forceinline__ void sync() const { __syncthreads(); }
+    __device__ __forceinline__ int64_t scan(int64_t x, int64_t& total) const {
         const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
         int64_t upto = x;
 #pragma unroll
@@ -79,22 +72,9 @@ struct GpuTeam {
             if (lane == 31) scratch->all = y;
         }
         __syncthreads();
-        int64_t before = scratch->sums[warp] + upto - x;
+        const int64_t before = scratch->sums[warp] + upto - x;
         total = scratch->all;
-        if constexpr (kOne) {
-            __syncthreads();
-        } else {
-            int64_t* of_blocks = totals + (scans++ & 1) * kCluster;
-            const int block = (int)cluster_ctarank(), blocks = (int)ncluster_x();
-            if (threadIdx.x == 0) of_blocks[block] = total;
-            sync();
-            total = 0;
-            for (int i = 0; i < blocks; ++i) {
-                const int64_t n = load(of_blocks + i);
-                before += i < block ? n : 0;
-                total += n;
-            }
-        }
+        __syncthreads();
         return before;
     }
     template <class T>
@@ -102,20 +82,30 @@ struct GpuTeam {
         return *const_cast<const volatile T*>(p);
     }
     __device__ __forceinline__ void store(int32_t* p, int32_t x) const { *const_cast<volatile int32_t*>(p) = x; }
-    // Of the pages' bits, which one block has in shared memory.
-    __device__ __forceinline__ void set_bits(uint32_t* p, uint32_t x) const {
-        if constexpr (kOne) asm volatile("red.shared.or.b32 [%0], %1;" ::"r"(smem_u32(p)), "r"(x) : "memory");
-        else atomicOr(p, x);
+    __device__ __forceinline__ void set_bit(uint32_t* bits, int page) const {
+        if (own_bits)
+            asm volatile("{ .reg .pred p; setp.ge.s32 p, %2, 0; @p red.shared.or.b32 [%0], %1; }" ::"r"(
+                             smem_u32(bits) + (page >> 5) * 4),
+                         "r"(1u << (page & 31)), "r"(page)
+                         : "memory");
+        else if (page >= 0) atomicOr(bits + (page >> 5), 1u << (page & 31));
     }
     __device__ __forceinline__ void lower(int32_t* p, int32_t x) const { atomicMin(p, x); }
     __device__ __forceinline__ void raise(int32_t* p, int32_t x) const { atomicMax(p, x); }
     __device__ __forceinline__ void report(unsigned int x) const { atomicOr(&g_pages_status, x); }
 };
 
-template <bool kOne>
-__device__ __forceinline__ GpuTeam<kOne> this_team(TeamScratch* scratch, int64_t* totals) {
-    const int block = kOne ? 0 : (int)cluster_ctarank(), blocks = kOne ? 1 : (int)ncluster_x();
-    return GpuTeam<kOne>{block * kThreads + (int)threadIdx.x, blocks * kThreads, scratch, totals, 0};
+// All threads of a grid, which meet nowhere.
+struct GridTeam {
+    int rank, size;
+    __device__ __forceinline__ void store(int32_t* p, int32_t x) const { *const_cast<volatile int32_t*>(p) = x; }
+    __device__ __forceinline__ void set_bit(uint32_t* bits, int page) const {
+        if (page >= 0) atomicOr(bits + (page >> 5), 1u << (page & 31));
+    }
+    __device__ __forceinline__ void report(unsigned int x) const { atomicOr(&g_pages_status, x); }
+};
+__device__ __forceinline__ GridTeam this_grid() {
+    return GridTeam{(int)(blockIdx.x * kRowThreads + threadIdx.x), (int)(gridDim.x * kRowThreads)};
 }
 
 // Shared memory of a block that plans alone, handed out as far as it goes; what
@@ -135,50 +125,69 @@ struct Own {
         left -= (int)bytes;
     }
 };
-__host__ __device__ void take_own(ForkSpace& s, const ForkIn& a, Own& own) {
+// `rows`: what the rows' own kernel does not fill.
+__host__ __device__ void take_own(ForkSpace& s, const ForkIn& a, Own& own, bool rows) {
     own.take(s.bits, words_of(a.p.num_pages));
+    if (!rows) return;
     own.take(s.place, a.p.B);
     own.take(s.first, a.p.B);
     own.take(s.keeper, a.p.num_pages);
 }
-__host__ __device__ void take_own(CompactSpace& s, const PagesIn& p, Own& own) {
+__host__ __device__ void take_own(CompactSpace& s, const PagesIn& p, Own& own, bool rows) {
     own.take(s.bits, words_of(p.num_pages));
+    if (!rows) return;
     own.take(s.entries, p.B);
     own.take(s.moved, p.num_pages);
     own.take(s.hole, p.num_pages);
     own.take(s.mover, p.num_pages);
 }
 template <class Space, class In>
-int own_bytes(Space s, const In& in) {
+int own_bytes(Space s, const In& in, bool rows) {
     Own own{nullptr, kOwnBytes};
-    take_own(s, in, own);
+    take_own(s, in, own, rows);
     return kOwnBytes - own.left;
 }
 
-template <bool kOne>
-__global__ void __launch_bounds__(kThreads, 1) kv_fork_kernel(const ForkIn a, ForkSpace s, int64_t* totals) {
+// kRows: the block takes the rows as well.  Else the bits of their pages are in s.bits.
+template <bool kRows>
+__global__ void __launch_bounds__(kThreads, 1) kv_fork_kernel(const ForkIn a, ForkSpace s) {
     extern __shared__ __align__(16) uint8_t own_memory[];
     __shared__ TeamScratch scratch;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the copies wait for this kernel's end
-    if constexpr (kOne) {
-        Own own{own_memory, kOwnBytes};
-        take_own(s, a, own);
-    }
-    GpuTeam<kOne> team = this_team<kOne>(&scratch, totals);
-    plan_fork(team, a, s);
+    const uint32_t* const marked = s.bits;
+    Own own{own_memory, kOwnBytes};
+    take_own(s, a, own, kRows);
+    BlockTeam team{(int)threadIdx.x, kThreads, &scratch, s.bits != marked};
+    if constexpr (kRows) plan_fork(team, a, s);
+    else fork_rest(team, a, s, marked);
 }
 
-template <bool kOne>
-__global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const PagesIn p, int32_t* top, CompactSpace s, int64_t* totals) {
+template <bool kRows>
+__global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const PagesIn p, int32_t* top, CompactSpace s) {
     extern __shared__ __align__(16) uint8_t own_memory[];
     __shared__ TeamScratch scratch;
+    if constexpr (kRows) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t* const marked = s.bits;
+    Own own{own_memory, kOwnBytes};
+    take_own(s, p, own, kRows);
+    BlockTeam team{(int)threadIdx.x, kThreads, &scratch, s.bits != marked};
+    if constexpr (kRows) plan_compact(team, p, top, s);
+    else compact_moves(team, p, top, s, marked);
+}
+
+__global__ void __launch_bounds__(kRowThreads) kv_fork_rows_kernel(const ForkIn a, const ForkSpace s) {
+    fork_rows(this_grid(), a, s);
+}
+__global__ void __launch_bounds__(kRowThreads) kv_compact_rows_kernel(const PagesIn p, const CompactSpace s) {
+    compact_rows(this_grid(), p, s);
+}
+__global__ void __launch_bounds__(kRowThreads) kv_compact_rename_kernel(const PagesIn p, const CompactSpace s) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if constexpr (kOne) {
-        Own own{own_memory, kOwnBytes};
-        take_own(s, p, own);
-    }
-    GpuTeam<kOne> team = this_team<kOne>(&scratch, totals);
-    plan_compact(team, p, top, s);
+    const GridTeam team = this_grid();
+    compact_rename(team, p, s, [&](int b) {
+        const int64_t n = p.lens[b], cap = (int64_t)p.width << p.page_log2;      // bad ones are reported already
+        return pages_for(n < 0 ? 0 : (n > cap ? cap : n), p.page_log2);
+    });
 }
 
 __global__ void __launch_bounds__(256) kv_copy_kernel(const __grid_constant__ CacheSet set, const PageCopy* copies,
@@ -229,10 +238,9 @@ struct Arena {
     }
 };
 
-size_t lay_out(ForkSpace& s, int64_t*& totals, void* base, int64_t num_pages, int64_t width, int64_t B) {
+size_t lay_out(ForkSpace& s, void* base, int64_t num_pages, int64_t width, int64_t B) {
     Arena m{static_cast<uint8_t*>(base)};
     const int64_t most = B * (width + 1);
-    totals = m.take<int64_t>(2 * kCluster);
     s.count = m.take<int32_t>(1);
     s.bits = m.take<uint32_t>(words_of((int)num_pages));
     s.place = m.take<Place>(B);
@@ -243,9 +251,8 @@ size_t lay_out(ForkSpace& s, int64_t*& totals, void* base, int64_t num_pages, in
     return m.used;
 }
 
-size_t lay_out(CompactSpace& s, int64_t*& totals, void* base, int64_t num_pages, int64_t B) {
+size_t lay_out(CompactSpace& s, void* base, int64_t num_pages, int64_t B) {
     Arena m{static_cast<uint8_t*>(base)};
-    totals = m.take<int64_t>(2 * kCluster);
     s.count = m.take<int32_t>(1);
     s.mark = m.take<int32_t>(2);
     s.entries = m.take<int32_t>(B);
@@ -257,25 +264,24 @@ size_t lay_out(CompactSpace& s, int64_t*& totals, void* base, int64_t num_pages,
     return m.used;
 }
 
-// Whether one block plans: its barriers are short, but it has one SM's loads.
-bool one_block(const PagesIn& p) { return (int64_t)p.B * p.width <= 65536 && p.num_pages <= 1 << 20; }
+// Whether one block takes the rows too: fewer launches to wait for, but one SM's instructions.  fork | compact, one
+// block and apart, us, pages of 16 tokens, 64 dims: 64 rows of 32 entries 12.9, 18.0 | 15.0, 24.7; 256 of 64 17.4, 19.6 | 28.1,
+// 38.8; 512 of 64 23.6, 23.2 | 47.4, 48.5; 1024 of 64 34.9, 25.8 | 90.1, 68.8; 4096 of 128 185, 49.6 | 635, 319.
+bool few_rows(const PagesIn& p) { return (int64_t)p.B * p.width <= 32768 && p.num_pages <= 1 << 20; }
 
 template <class Kernel, class... Args>
-cudaError_t launch_plan(Kernel kernel, bool one, int bytes, cudaStream_t stream, Args... args) {
+cudaError_t launch_plan(Kernel kernel, int bytes, cudaStream_t stream, Args... args) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = one ? 1 : kCluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.gridDim = dim3(one ? 1 : kCluster, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = stream;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    kernel<<<1, kThreads, bytes, stream>>>(args...);
+    return cudaGetLastError();
+}
+
+template <class Kernel, class... Args>
+cudaError_t launch_rows(Kernel kernel, const PagesIn& p, int num_sms, cudaStream_t stream, Args... args) {
+    const int64_t blocks = ((int64_t)p.B * p.width + 16 * kRowThreads - 1) / (16 * kRowThreads);    // 16 entries a thread
+    kernel<<<(unsigned)std::min<int64_t>(blocks, 4 * num_sms), kRowThreads, 0, stream>>>(args...);
+    return cudaGetLastError();
 }
 
 // `most`: copies that there may be.
@@ -315,35 +321,42 @@ cudaError_t launch_copies(const mhc_kv_cache* caches, int n, const PageCopy* cop
 
 size_t kv_fork_workspace(int64_t num_pages, int64_t width, int64_t B) {
     ForkSpace s;
-    int64_t* totals;
-    return lay_out(s, totals, nullptr, num_pages, width, B);
+    return lay_out(s, nullptr, num_pages, width, B);
 }
 
 size_t kv_compact_workspace(int64_t num_pages, int64_t B) {
     CompactSpace s;
-    int64_t* totals;
-    return lay_out(s, totals, nullptr, num_pages, B);
+    return lay_out(s, nullptr, num_pages, B);
 }
 
 cudaError_t launch_kv_fork(const mhc_kv_cache* caches, int num_caches, const ForkIn& a, void* workspace, int num_sms,
                            cudaStream_t stream) {
     ForkSpace s;
-    int64_t* totals;
-    lay_out(s, totals, workspace, a.p.num_pages, a.p.width, a.p.B);
-    const bool one = one_block(a.p);
-    const cudaError_t e = one ? launch_plan(kv_fork_kernel<true>, one, own_bytes(s, a), stream, a, s, totals)
-                              : launch_plan(kv_fork_kernel<false>, one, 0, stream, a, s, totals);
+    lay_out(s, workspace, a.p.num_pages, a.p.width, a.p.B);
+    cudaError_t e;
+    if (few_rows(a.p)) {
+        e = launch_plan(kv_fork_kernel<true>, own_bytes(s, a, true), stream, a, s);
+    } else {
+        e = cudaMemsetAsync(s.bits, 0, (size_t)words_of(a.p.num_pages) * 4, stream);
+        if (e == cudaSuccess) e = launch_rows(kv_fork_rows_kernel, a.p, num_sms, stream, a, s);
+        if (e == cudaSuccess) e = launch_plan(kv_fork_kernel<false>, own_bytes(s, a, false), stream, a, s);
+    }
     return e == cudaSuccess ? launch_copies(caches, num_caches, s.copies, s.count, a.p.B, a.p.page_log2, num_sms, stream) : e;
 }
 
 cudaError_t launch_kv_compact(const mhc_kv_cache* caches, int num_caches, const PagesIn& p, int32_t* top, void* workspace,
                               int num_sms, cudaStream_t stream) {
     CompactSpace s;
-    int64_t* totals;
-    lay_out(s, totals, workspace, p.num_pages, p.B);
-    const bool one = one_block(p);
-    const cudaError_t e = one ? launch_plan(kv_compact_kernel<true>, one, own_bytes(s, p), stream, p, top, s, totals)
-                              : launch_plan(kv_compact_kernel<false>, one, 0, stream, p, top, s, totals);
+    lay_out(s, workspace, p.num_pages, p.B);
+    cudaError_t e;
+    if (few_rows(p)) {
+        e = launch_plan(kv_compact_kernel<true>, own_bytes(s, p, true), stream, p, top, s);
+    } else {
+        e = cudaMemsetAsync(s.bits, 0, (size_t)words_of(p.num_pages) * 4, stream);
+        if (e == cudaSuccess) e = launch_rows(kv_compact_rows_kernel, p, num_sms, stream, p, s);
+        if (e == cudaSuccess) e = launch_plan(kv_compact_kernel<false>, own_bytes(s, p, false), stream, p, top, s);
+        if (e == cudaSuccess) e = launch_rows(kv_compact_rename_kernel, p, num_sms, stream, p, s);
+    }
     // half of the pages at most move
     const int64_t most = p.num_pages / 2 + 1;
     return e == cudaSuccess ? launch_copies(caches, num_caches, s.copies, s.count, most, p.page_log2, num_sms, stream) : e;

@@ -5,10 +5,12 @@
 //
 // A team T has `rank` of `size` threads (a power of two), sync(), a barrier after
 // which all see what each has written, scan(x, total), the sum of x over the ranks
-// below and over all (a collective that ends in a barrier), and load, set_bits,
-// lower and raise, which may meet one another on one word.
+// below and over all (a collective that ends in a barrier), load, set_bit (of a page, none
+// for -1), lower and raise, which may meet one another on one word, and report.
 //
-// Nothing is kept between calls: a page is in use if the tables name it or `held`
+// The rows of large tables are the work of all SMs (the _rows functions, by any
+// number of threads that meet nowhere, between a call's other parts); of small ones, one block does
+// all.  Nothing is kept between calls: a page is in use if the tables name it or `held`
 // says so, and the pages that are handed out are the lowest others, in the order of
 // the places and their entries.  So the results do not depend on the team.
 #pragma once
@@ -129,31 +131,53 @@ MHC_HD int highest(uint32_t x) {
 #endif
 }
 
-// use(b, i, value) for every entry of `rows` rows, with the entry of `from` that at(b, i) says, -1
-// where that is negative.  As many threads take a row as it has entries, or all, and
-// eight rows' loads are under way at a time.  One block's instructions are what
-// takes its time here, so offsets are 32 bits (checked on the host), and what is a row's
-// is worked out once.
-template <class Team, class At, class Use>
-MHC_HD void each_entry(const Team& t, int rows, int width, const int32_t* from, At&& at, Use&& use) {
-    constexpr int kAhead = 8;
+// The entries of a row that are pages of its own: those below `early` and from `low` on, up to `end`; `base`
+// is where the row begins.  Entry `skip` is left alone (-1: none).
+struct RowPages {
+    int32_t base, end, low, early, skip;
+};
+
+// use(b, i, page) for every entry of `rows` rows: the page that `from` has there, -1 for an entry that is not of
+// the row's own (pages(b) says which are) or no page's number; numbers that are neither a page nor
+// -1 are reported.  A thread takes four entries side by side of four rows, whose
+// loads are under way together.  Half of the time is one block's instructions, so what
+// is a row's is worked out once, and offsets are 32 bits (checked on the host).
+template <class Team, class Pages, class Use>
+MHC_HD void each_entry(const Team& t, int rows, int width, const int32_t* from, int num_pages, Pages&& pages, Use&& use) {
+    constexpr int kRows = 4, kWide = 4;
     int log2 = 0;
-    while ((2 << log2) <= t.size && (1 << log2) < width) ++log2;
+    while ((2 << log2) <= t.size && (kWide << log2) < width) ++log2;
     const int lanes = 1 << log2, at_once = t.size >> log2, lane = t.rank & (lanes - 1);
+    bool bad = false;
     MHC_ROLLED
-    for (int b0 = t.rank >> log2; b0 < rows; b0 += kAhead * at_once)
+    for (int b0 = t.rank >> log2; b0 < rows; b0 += kRows * at_once)
         MHC_ROLLED
-        for (int i = lane; i < width; i += lanes) {
-            int32_t v[kAhead];
+        for (int i0 = kWide * lane; i0 < width; i0 += kWide * lanes) {
+            int32_t v[kRows][kWide], skip[kRows];
             MHC_UNROLLED
-            for (int j = 0; j < kAhead; ++j) {
-                const int where = b0 + j * at_once < rows ? at(b0 + j * at_once, i) : -1;
-                v[j] = where >= 0 ? from[where] : -1;
+            for (int j = 0; j < kRows; ++j) {
+                const int b = b0 + j * at_once;
+                const RowPages r = b < rows ? pages(b) : RowPages{0, 0, 0, 0, -1};
+                skip[j] = r.skip;
+                MHC_UNROLLED
+                for (int k = 0; k < kWide; ++k) {
+                    const int i = i0 + k;
+                    v[j][k] = i < r.end && (i >= r.low || i < r.early) ? from[r.base + i] : -1;
+                }
             }
             MHC_UNROLLED
-            for (int j = 0; j < kAhead; ++j)
-                if (b0 + j * at_once < rows) use(b0 + j * at_once, i, v[j]);
+            for (int j = 0; j < kRows; ++j) {
+                const int b = b0 + j * at_once;
+                if (b >= rows) continue;
+                MHC_UNROLLED
+                for (int k = 0; k < kWide; ++k) {
+                    const bool ok = (uint32_t)v[j][k] < (uint32_t)num_pages;
+                    bad = bad || (!ok && v[j][k] != -1);
+                    if (i0 + k < width && i0 + k != skip[j]) use(b, i0 + k, ok ? v[j][k] : -1);
+                }
+            }
         }
+    if (bad) t.report(kBadIndex);
 }
 
 // A rank's part of n things in a row.
@@ -186,39 +210,64 @@ MHC_HD int first_page(int n, int window, int page_log2) {
     return window == 0 || first < 0 ? 0 : first >> page_log2;
 }
 
+// Place b of the batch, without its part-filled page.
 template <class Team>
-MHC_HD void plan_fork(Team& t, const ForkIn& a, const ForkSpace& s) {
-    const PagesIn& p = a.p;
-    const int log2 = p.page_log2, P = 1 << log2, cap = p.width << log2, words = words_of(p.num_pages);
-
-    // every place: whom it goes on with, its tokens, its part-filled page
-    for (int b = t.rank; b < p.B; b += t.size) {
-        int from = a.parents ? a.parents[b] : b;
-        if (from < -1 || from >= p.B_in) {
-            t.report(kBadIndex);
-            from = -1;
-        }
-        const int n = from < 0 ? 0 : checked_tokens(t, p.lens[from], cap);
-        const int last = n & (P - 1) ? checked_page(t, p.table[(int64_t)from * p.width + (n >> log2)], p.num_pages) : -1;
-        s.place[b] = Place{from * p.width, n, first_page(n, a.window, log2), last};
-        if (last >= 0) t.store(s.keeper + last, kNobody);
+MHC_HD Place place_of(const Team& t, const ForkIn& a, int b) {
+    int from = a.parents ? a.parents[b] : b;
+    if (from < -1 || from >= a.p.B_in) {
+        t.report(kBadIndex);
+        from = -1;
     }
-    for (int w = t.rank; w < words; w += t.size) s.bits[w] = held_word(p.held, p.num_pages, w);
-    t.sync();
+    const int n = from < 0 ? 0 : checked_tokens(t, a.p.lens[from], a.p.width << a.p.page_log2);
+    return Place{from * a.p.width, n, first_page(n, a.window, a.p.page_log2), -1};
+}
 
-    // full pages are shared, those of the first tokens and of the window
-    const int early = pages_for(a.sinks, log2);
+// Every place: whom it goes on with, its tokens, its part-filled page.
+template <class Team>
+MHC_HD void fork_places(const Team& t, const ForkIn& a, const ForkSpace& s) {
+    const int log2 = a.p.page_log2;
+    for (int b = t.rank; b < a.p.B; b += t.size) {
+        Place x = place_of(t, a, b);
+        if (x.len & ((1 << log2) - 1)) x.tail = checked_page(t, a.p.table[x.row + (x.len >> log2)], a.p.num_pages);
+        s.place[b] = x;
+        if (x.tail >= 0) t.store(s.keeper + x.tail, kNobody);
+    }
+}
+
+// Full pages are shared, those of the first tokens and of the window.  place(b): whom place b goes on with.
+// The entry after the full pages is fork_rest's to write: others may still read it, where tables are written in place.
+template <class Team, class PlaceOf>
+MHC_HD void fork_entries(const Team& t, const ForkIn& a, const ForkSpace& s, PlaceOf&& place) {
+    const PagesIn& p = a.p;
+    const int early = pages_for(a.sinks, p.page_log2);
     each_entry(
-        t, p.B, p.width, p.table,
-        [&](int b, int i) {
-            const Place x = s.place[b];
-            return i < x.len >> log2 && (i >= x.low || i < early) ? x.row + i : -1;
+        t, p.B, p.width, p.table, p.num_pages,
+        [&](int b) {
+            const Place x = place(b);
+            const int full = x.len >> p.page_log2;
+            return RowPages{x.row, full, x.low, early, full};
         },
-        [&](int b, int i, int32_t x) {
-            const int page = checked_page(t, x, p.num_pages);
-            if (page >= 0) t.set_bits(s.bits + (page >> 5), 1u << (page & 31));
+        [&](int b, int i, int32_t page) {
+            t.set_bit(s.bits, page);
             p.out[b * p.width + i] = page;
         });
+}
+
+// The rows of large tables; no bit is set before.
+template <class Team>
+MHC_HD void fork_rows(const Team& t, const ForkIn& a, const ForkSpace& s) {
+    fork_places(t, a, s);
+    fork_entries(t, a, s, [&](int b) { return place_of(t, a, b); });
+}
+
+// The rest, once the rows' full pages are marked.  `marked`: those and the pages that are held, where they are not
+// in s.bits yet.
+template <class Team>
+MHC_HD void fork_rest(Team& t, const ForkIn& a, const ForkSpace& s, const uint32_t* marked = nullptr) {
+    const PagesIn& p = a.p;
+    const int log2 = p.page_log2, P = 1 << log2, cap = p.width << log2, words = words_of(p.num_pages);
+    if (marked)
+        for (int w = t.rank; w < words; w += t.size) s.bits[w] = marked[w] | held_word(p.held, p.num_pages, w);
     for (int b = t.rank; b < p.B; b += t.size)
         if (s.place[b].tail >= 0) t.lower(s.keeper + s.place[b].tail, b);
     t.sync();
@@ -241,9 +290,9 @@ MHC_HD void plan_fork(Team& t, const ForkIn& a, const ForkSpace& s) {
         const bool copy = copied((int)b);
         s.first[b] = copy ? 1 : 0;            // for now: whether it copies
         mine += (then > now ? then - now : 0) + (copy ? ((int64_t)1 << 32) + 1 : 0);
-        if (!copy && last >= 0) {
-            t.set_bits(s.bits + (last >> 5), 1u << (last & 31));
-            p.out[b * p.width + (n >> log2)] = last;
+        if (!copy) {
+            t.set_bit(s.bits, last);
+            if (n < cap) p.out[b * p.width + (n >> log2)] = last;
         }
     }
     int64_t before = t.scan(mine, total);
@@ -292,22 +341,48 @@ MHC_HD void plan_fork(Team& t, const ForkIn& a, const ForkSpace& s) {
     }
 }
 
+template <class Team>
+MHC_HD void plan_fork(Team& t, const ForkIn& a, const ForkSpace& s) {
+    fork_places(t, a, s);
+    for (int w = t.rank; w < words_of(a.p.num_pages); w += t.size) s.bits[w] = held_word(a.p.held, a.p.num_pages, w);
+    t.sync();
+    fork_entries(t, a, s, [&](int b) { return s.place[b]; });
+    fork_rest(t, a, s);
+}
+
 // What is in use and not held goes to the lowest numbers that are not held: the pages there that are
 // free ("holes") take the used ones above, in order.
+template <class Team, class Entries, class Use>
+MHC_HD void compact_entries(const Team& t, const PagesIn& p, Entries&& entries, Use&& use) {
+    each_entry(t, p.B, p.width, p.table, p.num_pages, [&](int b) { return RowPages{b * p.width, entries(b), 0, 0, -1}; }, use);
+}
+
+// Marks the pages that the rows name; no bit is set before.
 template <class Team>
-MHC_HD void plan_compact(Team& t, const PagesIn& p, int32_t* top, const CompactSpace& s) {
-    const int log2 = p.page_log2, cap = p.width << log2, words = words_of(p.num_pages);
-    for (int w = t.rank; w < words; w += t.size) s.bits[w] = 0;
-    for (int b = t.rank; b < p.B; b += t.size) s.entries[b] = pages_for(checked_tokens(t, p.lens[b], cap), log2);
+MHC_HD void compact_rows(const Team& t, const PagesIn& p, const CompactSpace& s) {
+    compact_entries(
+        t, p, [&](int b) { return pages_for(checked_tokens(t, p.lens[b], p.width << p.page_log2), p.page_log2); },
+        [&](int, int, int32_t page) { t.set_bit(s.bits, page); });
+}
+
+// The new rows, with the pages that moved in their new places.
+template <class Team, class Entries>
+MHC_HD void compact_rename(const Team& t, const PagesIn& p, const CompactSpace& s, Entries&& entries) {
+    const int from = s.mark[1];
+    compact_entries(t, p, entries, [&](int b, int i, int32_t x) {
+        if (x >= from && !(p.held && p.held[x])) x = s.moved[x];
+        p.out[b * p.width + i] = x;
+    });
+}
+
+// Which pages move where, once those in use are marked (in `marked`, or in s.bits).
+template <class Team>
+MHC_HD void compact_moves(Team& t, const PagesIn& p, int32_t* top, const CompactSpace& s, const uint32_t* marked = nullptr) {
+    const int log2 = p.page_log2, words = words_of(p.num_pages);
+    if (marked)
+        for (int w = t.rank; w < words; w += t.size) s.bits[w] = marked[w];
     if (t.rank == 0) t.store(top, 0);
     t.sync();
-    auto entry = [&](int b, int i) { return i < s.entries[b] ? b * p.width + i : -1; };
-    each_entry(t, p.B, p.width, p.table, entry, [&](int, int, int32_t x) {
-        const int page = checked_page(t, x, p.num_pages);
-        if (page >= 0) t.set_bits(s.bits + (page >> 5), 1u << (page & 31));
-    });
-    t.sync();
-
     int64_t begin, end, mine = 0, total;      // in 32 bits each: used pages, and pages, that are not held
     part_of_all(t, words, begin, end);
     for (int64_t w = begin; w < end; ++w) {
@@ -354,12 +429,18 @@ MHC_HD void plan_compact(Team& t, const PagesIn& p, int32_t* top, const CompactS
         s.moved[page] = s.hole[k];
         s.copies[k] = PageCopy{page, s.hole[k], 1 << log2};
     }
+}
+
+template <class Team>
+MHC_HD void plan_compact(Team& t, const PagesIn& p, int32_t* top, const CompactSpace& s) {
+    for (int w = t.rank; w < words_of(p.num_pages); w += t.size) s.bits[w] = 0;
+    for (int b = t.rank; b < p.B; b += t.size)
+        s.entries[b] = pages_for(checked_tokens(t, p.lens[b], p.width << p.page_log2), p.page_log2);
     t.sync();
-    each_entry(t, p.B, p.width, p.table, entry, [&](int b, int i, int32_t x) {
-        if (x < 0 || x >= p.num_pages) x = -1;
-        if (x >= from && !(p.held && p.held[x])) x = s.moved[x];
-        p.out[b * p.width + i] = x;
-    });
+    compact_entries(t, p, [&](int b) { return s.entries[b]; }, [&](int, int, int32_t page) { t.set_bit(s.bits, page); });
+    compact_moves(t, p, top, s);
+    t.sync();
+    compact_rename(t, p, s, [&](int b) { return s.entries[b]; });
 }
 
 }  // namespace kv

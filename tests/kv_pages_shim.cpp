@@ -52,7 +52,9 @@ struct HostTeam {
     template <class T>
     T load(const T* p) const { return __atomic_load_n(p, __ATOMIC_RELAXED); }
     void store(int32_t* p, int32_t x) const { __atomic_store_n(p, x, __ATOMIC_RELAXED); }
-    void set_bits(uint32_t* p, uint32_t x) const { __atomic_fetch_or(p, x, __ATOMIC_RELAXED); }
+    void set_bit(uint32_t* bits, int page) const {
+        if (page >= 0) __atomic_fetch_or(bits + page / 32, 1u << page % 32, __ATOMIC_RELAXED);
+    }
     void lower(int32_t* p, int32_t x) const {
         for (int32_t v = load(p); x < v && !__atomic_compare_exchange_n(p, &v, x, true, __ATOMIC_RELAXED, __ATOMIC_RELAXED);) {}
     }
@@ -109,7 +111,7 @@ int main() {
         const bool fork = number() == 0;
         const int size = (int)number(), width = (int)number(), B_in = (int)number(), B = (int)number();
         const int log2 = (int)number(), pages = (int)number();
-        const bool in_place = number(), has_held = number();
+        const bool in_place = number(), has_held = number(), rows_apart = number();
         std::vector<int32_t> table = numbers<int32_t>((int64_t)B_in * width), lens = numbers<int32_t>(B_in);
         const std::vector<uint8_t> held = numbers<uint8_t>(has_held ? pages : 0);
         std::vector<int32_t> table_out = scratch<int32_t>((int64_t)B * width), lens_out = scratch<int32_t>(B);
@@ -131,14 +133,38 @@ int main() {
             const ForkIn a{p, given(parents), given(room), room_all, window, sinks, in_place ? lens.data() : lens_out.data()};
             const ForkSpace s{bits.data(), place.data(), first.data(), keeper.data(), out.data(),
                               copies.data(), &count};
-            status = run(size, [&](HostTeam& t) { plan_fork(t, a, s); });
+            if (rows_apart) {
+                std::vector<uint32_t> own = scratch<uint32_t>(words_of(pages));
+                for (uint32_t& w : bits) w = 0;
+                ForkSpace rest = s;
+                rest.bits = own.data();
+                status = run(size, [&](HostTeam& t) { fork_rows(t, a, s); });
+                status |= run(size, [&](HostTeam& t) { fork_rest(t, a, rest, s.bits); });
+            } else {
+                status = run(size, [&](HostTeam& t) { plan_fork(t, a, s); });
+            }
             print(in_place ? lens.data() : lens_out.data(), B);
         } else {
             std::vector<int32_t> mover = scratch<int32_t>(pages), hole = scratch<int32_t>(pages), moved = scratch<int32_t>(pages),
                                  mark = scratch<int32_t>(2), entries = scratch<int32_t>(B);
             copies = scratch<PageCopy>(pages);
             const CompactSpace s{bits.data(), entries.data(), mover.data(), hole.data(), moved.data(), copies.data(), &count, mark.data()};
-            status = run(size, [&](HostTeam& t) { plan_compact(t, p, &top, s); });
+            if (rows_apart) {
+                std::vector<uint32_t> own = scratch<uint32_t>(words_of(pages));
+                for (uint32_t& w : bits) w = 0;
+                CompactSpace moves = s;
+                moves.bits = own.data();
+                status = run(size, [&](HostTeam& t) { compact_rows(t, p, s); });
+                status |= run(size, [&](HostTeam& t) { compact_moves(t, p, &top, moves, s.bits); });
+                status |= run(size, [&](HostTeam& t) {
+                    compact_rename(t, p, s, [&](int b) {
+                        const int64_t n = lens[b], cap = (int64_t)width << log2;
+                        return pages_for(n < 0 ? 0 : (n > cap ? cap : n), log2);
+                    });
+                });
+            } else {
+                status = run(size, [&](HostTeam& t) { plan_compact(t, p, &top, s); });
+            }
             std::printf("%d ", top);
         }
         print(in_place ? table.data() : table_out.data(), (int64_t)B * width);

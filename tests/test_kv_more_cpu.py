@@ -337,7 +337,7 @@ def _fork_case(r, size, wild):
     window = r.choice([0, 0, 1, r.randint(1, width * P)])
     sinks = r.choice([0, r.randint(0, 3 * P)]) if window else 0
     in_place = parents is None and r.random() < 0.5
-    numbers = [0, size, width, B_in, B, log2, pages, in_place, held is not None, *_flat(table), *lens, *(held or []),
+    numbers = [0, size, width, B_in, B, log2, pages, in_place, held is not None, r.random() < 0.5, *_flat(table), *lens, *(held or []),
                parents is not None, isinstance(room, list), *(parents or []), *(room if isinstance(room, list) else []),
                0 if isinstance(room, list) else room, window, sinks]
     out, n, copies, status = plan_fork(table, lens, pages, log2, parents, room, window, sinks, held)
@@ -347,7 +347,8 @@ def _fork_case(r, size, wild):
 def _compact_case(r, size, wild):
     log2, P, pages, width, lens, table, held = _tables(r, wild)
     B = len(lens)
-    numbers = [1, size, width, B, B, log2, pages, r.random() < 0.5, held is not None, *_flat(table), *lens, *(held or [])]
+    numbers = [1, size, width, B, B, log2, pages, r.random() < 0.5, held is not None, r.random() < 0.5,
+               *_flat(table), *lens, *(held or [])]
     out, top, copies, status = plan_compact(table, lens, pages, log2, held)
     return numbers, [top, *_flat(out), status, len(copies), *_flat(copies)]
 
@@ -355,7 +356,7 @@ def _compact_case(r, size, wild):
 @pytest.mark.parametrize("make", [_fork_case, _compact_case])
 @pytest.mark.parametrize("wild", [False, True])
 def test_pages_are_planned_as_defined(pages_exe, make, wild):
-    """One to 64 threads: the definition's tables, lengths, copies and reports, whatever the arrays hold, inside
+    """One to 64 threads, the rows with the rest or apart: the definition's tables, lengths, copies and reports, whatever the arrays hold, inside
     the arrays (a sanitizer ends the program otherwise)."""
     r = random.Random(7 + wild)
     cases = [make(r, r.choice([1, 2, 8, 64]), wild) for _ in range(250)]

@@ -168,6 +168,23 @@ def test_one_cache_alone_and_outputs_given():
     assert torch.equal(t, a["block_table"]) and torch.equal(pages, a["pages"])
 
 
+def test_large_tables_in_place():
+    """Tables whose rows have kernels of their own, written over themselves: as into new ones."""
+    r = random.Random(15)
+    lens, table = batch(r, 300, 130, 30000, 16, shared=0.3)
+    lens = [min(n, 129 * 16) for n in lens]
+    a, b = caches_of([(1, 64)], 30000, 16, 15), caches_of([(1, 64)], 30000, 16, 15)
+    expect = mhc.kv_fork(a, _i32(table), _i32(lens), room=9, window=700, sinks=20)
+    t, n = _i32(table), _i32(lens)
+    mhc.kv_fork(b, t, n, room=9, window=700, sinks=20, out={"block_table": t, "seq_lens": n})
+    assert torch.equal(t, expect["block_table"]) and torch.equal(n, expect["seq_lens"])
+    moved = mhc.kv_compact(a, expect["block_table"], n)
+    got = mhc.kv_compact(b, t, n, out={"block_table": t})
+    assert torch.equal(t, moved["block_table"]) and torch.equal(got["pages"], moved["pages"])
+    for x, y in zip(bytes_of(a), bytes_of(b)):
+        assert all(torch.equal(x[k], y[k]) for k in x)
+
+
 def test_running_out_of_pages_is_reported():
     (c,) = caches_of([(1, 64)], 4, 16, 6)
     table, lens = _i32([[0, 1, 2, -1, -1], [3, -1, -1, -1, -1]]), _i32([48, 16])
