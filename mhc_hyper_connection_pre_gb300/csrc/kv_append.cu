@@ -238,10 +238,13 @@ __global__ void __launch_bounds__(256, kNorm && kAhead > 1 ? 3 : 4) kv_append_ke
     };
     const uint4 none = make_uint4(0, 0, 0, 0);
 
-    // blocks of both kinds in turn, then those of which there are more
-    const int kvs = a.kv_blocks, qs = (int)gridDim.x - kvs, paired = 2 * (kvs < qs ? kvs : qs), i = blockIdx.x;
-    const bool is_q = i < paired ? i & 1 : kvs < qs;
-    const uint32_t block = i < paired ? i / 2 : i - paired / 2;
+    // With norms and many tokens, blocks of both kinds in turn, then those of which there are more (a prompt of 16384
+    // tokens 91.5 us, first those that append 92.4); else first those that append (256 single tokens 8.5 us, in
+    // turn 8.8).
+    constexpr bool kInTurn = kNorm && kAhead > 1;
+    const int kvs = a.kv_blocks, qs = (int)gridDim.x - kvs, paired = kInTurn ? 2 * (kvs < qs ? kvs : qs) : 0, i = blockIdx.x;
+    const bool is_q = i < paired ? i & 1 : kInTurn ? kvs < qs : i >= kvs;
+    const uint32_t block = i < paired ? i / 2 : kInTurn ? i - paired / 2 : is_q ? i - kvs : i;
     if (is_q) {                                       // queries: a warp takes one token and some of its heads
         constexpr int kHeads = 32 / kLanes;           // heads of one step
         const int steps = (a.q_heads + kHeads - 1) / kHeads;

@@ -52,12 +52,12 @@ struct __align__(16) Meta {                   // of one load
     int pad[2];
 };
 
-template <int D, int NB>
+template <int D, int NB, class Seg>
 struct __align__(1024) Smem {
     static constexpr int kWarps = Shape<D, NB>::kWarps, kStages = Shape<D, NB>::kStages;
     uint8_t ring[kWarps][kStages * Shape<D, NB>::kStage];
     Meta meta[kWarps][kStages];
-    Segment queue[kWarps][kQueue];
+    Seg queue[kWarps][kQueue];
     Plan plan[kWarps];
     Shares shares[kWarps];
     int64_t counted[32];
@@ -299,8 +299,8 @@ __device__ __forceinline__ void piece(const C& cut, bool full, uint32_t ks, uint
 
 // The plan's segment into the queue.  A call of its own: it is rare, and its
 // code does not belong between the loads'.
-template <class C>
-__device__ __noinline__ bool push_segment(const AttendArgs<C>& a, Plan& plan, const Shares& shares, Segment& to) {
+template <class C, class Seg>
+__device__ __noinline__ bool push_segment(const AttendArgs<C>& a, Plan& plan, const Shares& shares, Seg& to) {
     return plan_next(plan, Lookup<C>{a}, a.cut, shares, to);
 }
 
@@ -311,7 +311,9 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     constexpr int kStages = Shape<D, NB>::kStages, kStage = Shape<D, NB>::kStage;
     constexpr int kRows = 8 * NB;
     extern __shared__ uint8_t raw[];
-    Smem<D, NB>& sm = *reinterpret_cast<Smem<D, NB>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    using Seg = typename SegmentOf<C::kWindow>::type;
+    using Shared = Smem<D, NB, Seg>;
+    Shared& sm = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, t = lane % 4;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel waits for this one's end
     if (tid == 0) sm.abort = 0;
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
     auto settle = [&] {
         while (key >= keys) {
             if (over || pushed - popped == kQueue) return false;
-            Segment& s = sm.queue[warp][pushed % kQueue];
+            Seg& s = sm.queue[warp][pushed % kQueue];
             // none: the share is done, or what is left of it are a tile's extra units
             if (!found_for_all(ThisWarp{lane}, [&] { return plan.w.left > 0 && push_segment(a, plan, sm.shares[warp], s); })) {
                 over = true;
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
         }
         if (!open) {
             if (popped == pushed) break;
-            const Segment& seg = sm.queue[warp][popped % kQueue];
+            const Seg& seg = sm.queue[warp][popped % kQueue];
             at = seg.key0;
             end = seg.keys;
             open = true;
@@ -523,7 +525,7 @@ __global__ void __launch_bounds__(Shape<D, NB>::kThreads, 1)
         open = false;
 
         // the rows go out, or to the workspace: thread (g, t) has D/8 dims of rows 2t and 2t + 1
-        const Segment& seg = sm.queue[warp][popped % kQueue];
+        const Seg& seg = sm.queue[warp][popped % kQueue];
         const bool whole = seg.parts == 1;
         const int slot = seg.owner == share ? 1 : 0;
         float* part = part_of(a, share, slot, D);
@@ -785,7 +787,7 @@ size_t part_bytes(int rows, int D, int shares) { return ((size_t)shares * 2 * ro
 template <int D, int NB, class C>
 cudaError_t launch(const CUtensorMap& k_map, const CUtensorMap& v_map, const AttendArgs<C>& a, int blocks,
                    cudaStream_t stream) {
-    const int bytes = (int)sizeof(Smem<D, NB>) + 1024;
+    const int bytes = (int)sizeof(Smem<D, NB, typename SegmentOf<C::kWindow>::type>) + 1024;
     // an attribute of the function on the current device: set on every call, which keeps no state here
     const cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<D, NB, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
@@ -817,7 +819,7 @@ cudaError_t launch_join(const AttendArgs<Cut>& a, int head_dim, cudaStream_t str
 
 cudaError_t launch_kv_attend_tc(const AttendArgs<Cut>& a, const uint8_t* k, const uint8_t* v, int head_dim, int blocks,
                                 cudaStream_t stream);
-cudaError_t launch_kv_attend_tc(const AttendArgs<WindowCut>& a, const uint8_t* k, const uint8_t* v, int head_dim,
+cudaError_t launch_kv_attend_tc(const AttendArgs<WindowWork>& a, const uint8_t* k, const uint8_t* v, int head_dim,
                                 int blocks, cudaStream_t stream);
 
 size_t kv_attend_workspace(int heads, int head_dim, int q_heads, int64_t B, int64_t T, int num_sms) {
@@ -830,7 +832,7 @@ namespace {
 // The kernel for the call's rows, then the join.  `a` lacks the cut's sizes of tiles and units, the shares and the
 // workspace's parts.
 template <class C>
-cudaError_t launch_rows(AttendArgs<C>& a, const uint8_t* k, int heads, int head_dim, int group, void* workspace,
+cudaError_t launch_rows(AttendArgs<C>& a, const uint8_t* k, const uint8_t* v, int heads, int head_dim, int group, void* workspace,
                         int num_sms, cudaStream_t stream) {
     const Seqs& seqs = a.seqs;
     const int rows = tile_rows(group, seqs.B, seqs.T);
@@ -846,12 +848,12 @@ cudaError_t launch_rows(AttendArgs<C>& a, const uint8_t* k, int heads, int head_
     a.desc = reinterpret_cast<PartDesc*>(static_cast<uint8_t*>(workspace) + part_bytes(rows, head_dim, a.shares));
     cudaError_t e;
     if (rows == 256) {
-        e = launch_kv_attend_tc(a, k, a.v, head_dim, num_sms, stream);
+        e = launch_kv_attend_tc(a, k, v, head_dim, num_sms, stream);
     } else {
         CUtensorMap k_map, v_map;
         const int64_t pages = (int64_t)seqs.num_pages * heads;
         if (!encode_codes(&k_map, k, pages, 1 << seqs.page_log2, head_dim, kSub) ||
-            !encode_codes(&v_map, a.v, pages, 1 << seqs.page_log2, head_dim, kSub))
+            !encode_codes(&v_map, v, pages, 1 << seqs.page_log2, head_dim, kSub))
             return cudaErrorInvalidValue;
         if (rows == 8)
             e = head_dim == 64 ? launch<64, 1>(k_map, v_map, a, num_sms, stream)
@@ -861,8 +863,7 @@ cudaError_t launch_rows(AttendArgs<C>& a, const uint8_t* k, int heads, int head_
                                : launch<128, 2>(k_map, v_map, a, num_sms, stream);
     }
     if (e != cudaSuccess) return e;
-    const AttendArgs<Cut> join{seqs, a.cut, a.shares, a.k_scale, a.v_scale, a.v, a.q, a.q_stride,
-                               a.scale_log2, a.out, a.lse, a.part, a.desc};
+    const AttendArgs<Cut> join{seqs, a.cut, a.shares, a.k_scale, a.v_scale, a.q, a.q_stride, a.scale_log2, a.out, a.lse, a.part, a.desc};
     return launch_join(join, head_dim, stream);
 }
 
@@ -876,13 +877,14 @@ cudaError_t launch_kv_attend(const Seqs& seqs, const uint8_t* k, const uint8_t* 
     const int group = q_heads / heads;
     const float scale_log2 = softmax_scale * kLog2e;
     if (window == 0) {
-        AttendArgs<Cut> a{seqs, {}, 0, k_scale, v_scale, v, q, q_stride, scale_log2, out, lse, nullptr, nullptr};
-        return launch_rows(a, k, heads, head_dim, group, workspace, num_sms, stream);
+        AttendArgs<Cut> a{seqs, {}, 0, k_scale, v_scale, q, q_stride, scale_log2, out, lse, nullptr, nullptr};
+        return launch_rows(a, k, v, heads, head_dim, group, workspace, num_sms, stream);
     }
-    AttendArgs<WindowCut> a{seqs, {}, 0, k_scale, v_scale, v, q, q_stride, scale_log2, out, lse, nullptr, nullptr};
+    AttendArgs<WindowWork> a{seqs, {}, 0, k_scale, v_scale, q, q_stride, scale_log2, out, lse, nullptr, nullptr};
     a.cut.window = window;
     a.cut.sinks = sinks;
-    return launch_rows(a, k, heads, head_dim, group, workspace, num_sms, stream);
+    a.cut.v = v;
+    return launch_rows(a, k, v, heads, head_dim, group, workspace, num_sms, stream);
 }
 
 cudaError_t read_attend_status(unsigned int* status) {

@@ -28,7 +28,12 @@ struct PartDesc {
     Segment seg;
 };
 
-// C: Cut, or WindowCut for attention with a window.
+// The cut of attention with a window; the value codes, to look once more for NaN.
+struct WindowWork : WindowCut {
+    const uint8_t* v;
+};
+
+// C: Cut, or WindowWork.
 template <class C>
 struct AttendArgs {
     Seqs seqs;
@@ -36,7 +41,6 @@ struct AttendArgs {
     int shares;
     const float* k_scale;
     const float* v_scale;
-    const uint8_t* v;                         // value codes (with a window: to look once more for NaN)
     const uint16_t* q;
     int64_t q_stride;
     float scale_log2;                         // softmax_scale * log2(e)

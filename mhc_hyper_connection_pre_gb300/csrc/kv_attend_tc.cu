@@ -74,13 +74,13 @@ struct __align__(16) Meta {                   // of one load: the scales of each
     int pad[3];
 };
 
-template <int D>
+template <int D, class Seg>
 struct __align__(1024) Smem {
     uint8_t q[2][2][kTile * D];               // tile, hi / lo (e4m3, e5m2)
     uint8_t k[kKStages][kTile * D];
     uint8_t v[kVStages][kTile * D];           // as stored
     uint8_t v16[2][kTile * D * 2];            // f16: 64 dims of every key, then the next 64
-    Segment segs[kSegments];
+    Seg segs[kSegments];
     Plan plan;
     Shares shares;
     int64_t counted[32];
@@ -273,7 +273,7 @@ __device__ __forceinline__ int steps_of(bool split, int keys) {
 // value among those that not every row sees is NaN.  Rare, so the codes are read once more: which rows see which
 // keys differs at both ends of a window, and would need a set of keys for each dim.
 template <int D, class C>
-__device__ __noinline__ void nan_dims(const AttendArgs<C>& a, const Segment& s, int c, int n, uint32_t& mask) {
+__device__ __noinline__ void nan_dims(const AttendArgs<C>& a, const WindowSegment& s, int c, int n, uint32_t& mask) {
     const int log2 = a.seqs.page_log2, first = first_seen(s, a.cut);
     const int32_t* row = a.seqs.table + (int64_t)s.b * a.seqs.width;
     mask = 0;
@@ -284,7 +284,7 @@ __device__ __noinline__ void nan_dims(const AttendArgs<C>& a, const Segment& s, 
         const int page = __ldg(row + (place >> log2));
         if (page < 0 || page >= a.seqs.num_pages) continue;
         const uint8_t* from =
-            a.v + ((((int64_t)page * a.cut.heads + s.head) << log2) + (place & ((1 << log2) - 1))) * D + c * 32;
+            a.cut.v + ((((int64_t)page * a.cut.heads + s.head) << log2) + (place & ((1 << log2) - 1))) * D + c * 32;
         uint32_t found = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -296,7 +296,7 @@ __device__ __noinline__ void nan_dims(const AttendArgs<C>& a, const Segment& s, 
 }
 
 template <int D, class C>
-__device__ __forceinline__ void put_nans(const AttendArgs<C>& a, const Segment& s, int c, int n, uint32_t (&o)[32]) {
+__device__ __forceinline__ void put_nans(const AttendArgs<C>& a, const WindowSegment& s, int c, int n, uint32_t (&o)[32]) {
     uint32_t mask;
     nan_dims<D>(a, s, c, n, mask);
 #pragma unroll
@@ -309,7 +309,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     kv_attend_tc_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                         const AttendArgs<C> a) {
     extern __shared__ uint8_t raw[];
-    Smem<D>& sm = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    using Seg = typename SegmentOf<C::kWindow>::type;
+    using Shared = Smem<D, Seg>;
+    Shared& sm = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kStep >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
     constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t lanes = tmem + ((uint32_t)(warp % 4) << 21);
             bool ok = true;
             for (int index = 0; ok && index < sm.count; ++index) {
-                const Segment seg = sm.segs[index];
+                const Seg seg = sm.segs[index];
                 const int rows = seg.rows;
                 const bool split = rows <= kTile;
                 const int mine = split ? in_tile : x * kTile + in_tile;              // of the block's rows
@@ -662,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int id = tid - 256;         // this thread's key of a step
             bool ok = true;                   // after a wait that gave up all go on to the barriers, without work
             for (int index = 0; index < sm.count; ++index) {
-                const Segment seg = sm.segs[index];
+                const Seg seg = sm.segs[index];
                 const int key0 = seg.key0, keys = seg.keys;
                 if (keys <= key0) continue;
                 const int slot = segs++ % kSegs, log2 = a.seqs.page_log2;
@@ -786,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int log2 = a.seqs.page_log2, per_box = 1 << (log2 - 4);
                 bool ok = true;
                 for (int index = 0; ok && index < sm.count; ++index) {
-                    const Segment seg = sm.segs[index];
+                    const Seg seg = sm.segs[index];
                     const int key0 = seg.key0, keys = seg.keys;
                     const int32_t* row = a.seqs.table + (int64_t)seg.b * a.seqs.width;
                     // this lane's 16 keys of a step: whether their page is looked at, and which it is
@@ -956,8 +958,9 @@ cudaError_t launch(const AttendArgs<C>& a, const uint8_t* k, const uint8_t* v, i
     if (!encode_codes(&k_map, k, pages, 1 << a.seqs.page_log2, D, kTile) ||
         !encode_codes(&v_map, v, pages, 1 << a.seqs.page_log2, D, kTile))
         return cudaErrorInvalidValue;
-    const int bytes = (int)sizeof(Smem<D>) + 1024;
-    static_assert(sizeof(Smem<D>) + 1024 <= 227 * 1024, "shared memory of a block");
+    using Shared = Smem<D, typename SegmentOf<C::kWindow>::type>;
+    const int bytes = (int)sizeof(Shared) + 1024;
+    static_assert(sizeof(Shared) + 1024 <= 227 * 1024, "shared memory of a block");
     const cudaError_t e = cudaFuncSetAttribute(kv_attend_tc_kernel<D, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     kv_attend_tc_kernel<D, C><<<blocks, kThreads, bytes, stream>>>(k_map, v_map, a);
@@ -971,7 +974,7 @@ cudaError_t launch_kv_attend_tc(const AttendArgs<Cut>& a, const uint8_t* k, cons
     return head_dim == 64 ? launch<64>(a, k, v, blocks, stream) : launch<128>(a, k, v, blocks, stream);
 }
 
-cudaError_t launch_kv_attend_tc(const AttendArgs<WindowCut>& a, const uint8_t* k, const uint8_t* v, int head_dim,
+cudaError_t launch_kv_attend_tc(const AttendArgs<WindowWork>& a, const uint8_t* k, const uint8_t* v, int head_dim,
                                 int blocks, cudaStream_t stream) {
     return head_dim == 64 ? launch<64>(a, k, v, blocks, stream) : launch<128>(a, k, v, blocks, stream);
 }

@@ -266,7 +266,11 @@ struct Segment {
     int see;                // keys before that token (counted without those that a window leaves out)
     int key0, keys;         // the segment's keys [key0, keys); none where the tile sees none
     int parts, owner;       // shares that the tile's units lie in, the first of them
-    int skip_at, skip;      // with a window: of the tile
+};
+
+// With a window: those of the tile as well.
+struct WindowSegment : Segment {
+    int skip_at, skip;
 };
 
 // Row r of a segment's tile.
@@ -282,11 +286,21 @@ MHC_HD int keys_of_row(const Segment& s, const Cut& c, int r) {
     return n < 0 ? 0 : n;
 }
 
+// Those of a cut.
+template <bool kWindow>
+struct SegmentOf {
+    using type = Segment;
+};
+template <>
+struct SegmentOf<true> {
+    using type = WindowSegment;
+};
+
 // The place in the sequence of a segment's key.
-MHC_HD int place_of_key(const Segment& s, int key) { return key < s.skip_at ? key : key + s.skip; }
+MHC_HD int place_of_key(const WindowSegment& s, int key) { return key < s.skip_at ? key : key + s.skip; }
 
 // The first place of the windows of the tile's first row, the first of the tile's.
-MHC_HD int first_seen(const Segment& s, const WindowCut& c) {
+MHC_HD int first_seen(const WindowSegment& s, const WindowCut& c) {
     const int n = s.see + s.skip + 1 - c.window;
     return n < 0 ? 0 : n;
 }
@@ -360,8 +374,8 @@ struct Plan {
 
 // The plan's next segment, if it has one: a part of a share that has only
 // extra units of a tile is none.  look(b) finds sequence b.
-template <class Look, class C>
-MHC_HD bool plan_next(Plan& p, const Look& look, const C& c, const Shares& shares, Segment& s) {
+template <class Look, class C, class Seg>
+MHC_HD bool plan_next(Plan& p, const Look& look, const C& c, const Shares& shares, Seg& s) {
     MHC_ROLLED
     while (p.w.left > 0) {
         const int end = p.w.first + p.w.count - c.extra;     // of the tile's key units

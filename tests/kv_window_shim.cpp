@@ -43,7 +43,7 @@ int64_t kv_window_walk(const int32_t* lens, const int32_t* cu, int width, int B,
         }
         p.at = from;
         walk_enter(p.w, p.info, c, from - before, left);
-        Segment g;
+        WindowSegment g;
         while (plan_next(p, Look{s}, c, shares, g)) {
             const int first = first_seen(g, c), n0 = keys_of_row(g, c, 0), n1 = keys_of_row(g, c, g.rows - 1);
             wrong += g.key0 % unit != 0 || g.skip % unit != 0 || g.skip_at % unit != 0 || g.skip < 0 || g.keys > n1;
