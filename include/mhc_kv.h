@@ -111,8 +111,8 @@ mhc_status mhc_kv_append(const mhc_kv_cache *cache, const uint16_t *k, int64_t k
  *   N x = x * r * w[h],  r = 1 / sqrt(sum_i x_i^2 / head_dim + norm_eps)
  *   q_out[t][h] = bf16( R_p N q[t][h] ),   cache.k <- R_p N k[t][h]
  * held in fp32 from the inputs to the one rounding at the end; values are
- * written as they are.  Rows without a place in the cache are copied as they
- * are.  A head that holds an infinity or NaN gives what the formula gives.
+ * written as they are.  Rows without a place in the cache, or with a position
+ * that the rotation's tables lack, are copied as they are.  A head that holds an infinity or NaN gives what the formula gives.
  *
  *  q_norm, k_norm  bf16 weights, head h's at h * stride (in elements: a
  *                  multiple of 8, at least head_dim; 0: all heads have the

@@ -280,7 +280,7 @@ cudaError_t launch_plan(Kernel kernel, int bytes, cudaStream_t stream, Args... a
 template <class Kernel, class... Args>
 cudaError_t launch_rows(Kernel kernel, const PagesIn& p, int num_sms, cudaStream_t stream, Args... args) {
     const int64_t blocks = ((int64_t)p.B * p.width + 16 * kRowThreads - 1) / (16 * kRowThreads);    // 16 entries a thread
-    kernel<<<(unsigned)std::min<int64_t>(blocks, 4 * num_sms), kRowThreads, 0, stream>>>(args...);
+    kernel<<<(unsigned)std::min<int64_t>(std::max<int64_t>(blocks, 1), 4 * num_sms), kRowThreads, 0, stream>>>(args...);
     return cudaGetLastError();
 }
 

@@ -271,6 +271,23 @@ def test_bad_indices_leave_rows_and_pages_alone():
             assert all(torch.equal(after[n][p], before[n][p]) for n in after)
 
 
+@pytest.mark.parametrize("counts,lens", [(None, [5, 40, 17]), ([30, 20], [50, 25])])
+def test_positions_beyond_the_rotation_are_left_alone(counts, lens):
+    """Their tokens are not written, and their queries neither normed nor rotated."""
+    m = _make((64, 16, 2, 4, counts, lens, 64, False, "qk", False), 99)
+    before = _bytes(m["cache"])
+    rows = 18                                                  # positions that the tables have
+    out = _run(m, cos=m["cos"][:rows].contiguous(), sin=m["sin"][:rows].contiguous())
+    assert mhc.device_status() == INDEX_ERROR
+    after = _bytes(m["cache"])
+    for b, t0, t1, first in spans(lens, m["cu"], m["k"].shape[0]):
+        for t in range(t0, t1):
+            p = first + t - t0
+            assert torch.equal(out[t], m["q"][t]) == (p >= rows)
+            page, slot = m["rows"][b][p // 16], p % 16
+            assert torch.equal(after["v"][page, :, slot], before["v"][page, :, slot]) == (p >= rows)
+
+
 def test_refusals():
     m = _make((64, 16, 2, 4, None, [3, 4], 64, False, "qk", True), 98)
     before = _bytes(m["cache"])

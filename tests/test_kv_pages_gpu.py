@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import mhc_hyper_connection_pre_gb300 as mhc
+from mhc_hyper_connection_pre_gb300.graphs import SeamGraph
 from test_kv_more_cpu import plan_compact, plan_fork
 
 pytestmark = pytest.mark.gpu
@@ -263,6 +264,39 @@ def test_far_pages():
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("pages", [1_100_000, 1_700_000])
+def test_many_pages(pages):
+    """More pages than one block takes beside the rows, and than its shared memory has bits for."""
+    r = random.Random(pages)
+    B, width = 20, 12
+    lens = [r.randint(0, width * 16 - 20) for _ in range(B)]
+    pick = r.sample(range(pages), B * width)
+    table = [[pick[b * width + i] if i * 16 < n else -1 for i in range(width)] for b, n in enumerate(lens)]
+    parents = [r.randint(-1, B - 1) for _ in range(2 * B)]
+    hold = set(range(300)) | set(range(pages - 70, pages - 10)) | set(r.sample(pick, 9))
+    held = torch.zeros(pages, dtype=torch.bool, device="cuda")
+    held[list(hold)] = True
+    flags = held.tolist()
+    c = mhc.kv_cache(pages, 1, 16, 64)
+    for n in ("k", "v"):
+        c[n].view(torch.uint8)[pick] = torch.randint(0, 256, (len(pick), 1, 16, 64), device="cuda", dtype=torch.uint8)
+    got = mhc.kv_fork(c, _i32(table), _i32(lens), _i32(parents), room=20, held=held)
+    out, n, copies, status = plan_fork(table, lens, pages, 4, parents, 20, 0, 0, flags)
+    assert status == 0 and copies
+    assert got["block_table"].tolist() == out and got["seq_lens"].tolist() == n
+    for a, b, slots in copies:
+        assert torch.equal(c["k"].view(torch.uint8)[b, 0, :slots], c["k"].view(torch.uint8)[a, 0, :slots])
+    got = mhc.kv_compact(c, _i32(table), _i32(lens), held=held)
+    out, top, copies, _ = plan_compact(table, lens, pages, 4, flags)
+    assert got["block_table"].tolist() == out and got["pages"].item() == top and copies
+    for a, b, _ in copies:
+        assert torch.equal(c["v"].view(torch.uint8)[b], c["v"].view(torch.uint8)[a])
+    none, no_rows = _i32([]), torch.empty(0, 3, dtype=torch.int32, device="cuda")
+    assert mhc.kv_compact(c, no_rows, none, held=held)["pages"].item() == pages - 10
+    del c
+    torch.cuda.empty_cache()
+
+
 def test_stream_graph_and_workspace():
     """On another stream, with a workspace of any contents, and captured and replayed: the same."""
     r = random.Random(12)
@@ -291,12 +325,14 @@ def test_stream_graph_and_workspace():
         assert all(torch.equal(moved[k], again[k]) for k in again)
     out = {"block_table": torch.zeros_like(expect["block_table"]), "seq_lens": torch.zeros_like(expect["seq_lens"])}
     fin = {"block_table": torch.zeros_like(out["block_table"]), "pages": torch.zeros((), dtype=torch.int32, device="cuda")}
-    graphs = []
+    def calls(stream=None):
+        mhc.kv_fork(b, t, n, parents, room=1, out=out, stream=stream)
+        mhc.kv_compact(b, out["block_table"], out["seq_lens"], out=fin, stream=stream)
+    graphs = [SeamGraph(calls, st), SeamGraph(calls, st, early_launch=True)]
     for _ in range(2):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=st):
-            mhc.kv_fork(b, t, n, parents, room=1, out=out)
-            mhc.kv_compact(b, out["block_table"], out["seq_lens"], out=fin)
+            calls()
         graphs.append(graph)
     for graph in graphs + graphs:
         for x in (*out.values(), *fin.values()):
