@@ -2,12 +2,15 @@
 
 One decoder layer's attention: ``mhc.pre_delayed`` collapses the streams into
 the layer's input, a projection forms queries, keys and values in one product,
-``mhc.kv_append`` rotates them and writes the cache, ``mhc.kv_attend`` reads
-it, and ``mhc.post`` mixes the projected result back into the streams.
+``mhc.kv_append`` norms and rotates them and writes the cache, ``mhc.kv_attend``
+reads it, with a sliding window if the layer has one, and ``mhc.post`` mixes the
+projected result back into the streams.  ``mhc.kv_fork`` hands out the cache's
+pages as sequences grow, and lets go of those that left the window.
 
 ``run()`` feeds three prompts of different lengths in one ragged call and then
-decodes one token a sequence, a CUDA graph replayed for each step.  It repeats
-the whole as single ragged calls over all tokens, and returns both results.
+decodes one token a sequence, a CUDA graph replayed for each step, pages
+included.  It repeats the whole as single ragged calls over all tokens, and
+returns both results.
 
     python examples/attention_decode.py
 """
@@ -27,10 +30,11 @@ from workloads import seam_inputs
 class AttentionSublayer:
     """Random weights, and one layer's cache, for up to ``max_tokens`` tokens a sequence."""
 
-    def __init__(self, sequences, max_tokens, *, C=5120, q_heads=40, heads=8, head_dim=128, page_tokens=64, seed=0):
+    def __init__(self, sequences, max_tokens, *, C=5120, q_heads=40, heads=8, head_dim=128, page_tokens=64, window=None,
+                 sinks=0, seed=0):
         p = seam_inputs(1, C=C, seed=seed, fold=True)
         self.fn, self.bias, self.alpha, self.norm_w = (p[k].cuda() for k in ("fn", "bias", "alpha", "norm_w"))
-        self.q_heads, self.heads, self.head_dim = q_heads, heads, head_dim
+        self.q_heads, self.heads, self.head_dim, self.window, self.sinks = q_heads, heads, head_dim, window, sinks
         g = torch.Generator(device="cuda").manual_seed(seed)
 
         def weight(rows, cols):
@@ -38,21 +42,27 @@ class AttentionSublayer:
 
         self.w_qkv = weight((q_heads + 2 * heads) * head_dim, C)
         self.w_out = weight(C, q_heads * head_dim)
+        self.q_norm, self.k_norm = (1 + 0.1 * torch.randn(2, head_dim, generator=g, device="cuda")).bfloat16()
         turns = torch.outer(torch.arange(max_tokens, device="cuda"),
                             10000.0 ** (-torch.arange(0, head_dim, 2, device="cuda") / head_dim))
         self.cos, self.sin = turns.cos(), turns.sin()
         pages = -(-max_tokens // page_tokens)
         self.cache = mhc.kv_cache(sequences * pages, heads, page_tokens, head_dim)
-        # a real server hands out pages as sequences grow; here each sequence owns some, in no order
-        self.block_table = torch.randperm(sequences * pages, generator=g, device="cuda").int().view(sequences, pages)
+        self.block_table = torch.full((sequences, pages), -1, dtype=torch.int32, device="cuda")
+
+    def room(self, seq_lens, more):
+        """Pages for ``more`` tokens (a number, or one for each sequence) after seq_lens."""
+        mhc.kv_fork(self.cache, self.block_table, seq_lens, room=more, window=self.window, sinks=self.sinks,
+                    out={"block_table": self.block_table, "seq_lens": seq_lens})
 
     def __call__(self, x, pre_in, seq_lens, cu_q=None):
         """x [T, n, C], the new tokens of all sequences; seq_lens with them.  Returns (next x, next pre_in)."""
         seam = mhc.pre_delayed(x, pre_in, self.fn, self.bias, self.alpha, self.norm_w)
         qkv = (seam["layer_input"] @ self.w_qkv.T).view(-1, self.q_heads + 2 * self.heads, self.head_dim)
         q, k, v = qkv.split([self.q_heads, self.heads, self.heads], dim=1)      # slices, not copies
-        q = mhc.kv_append(self.cache, k, v, self.block_table, seq_lens, cu_q, q=q, cos=self.cos, sin=self.sin)
-        o = mhc.kv_attend(q, self.cache, self.block_table, seq_lens, cu_q)["out"]
+        q = mhc.kv_append(self.cache, k, v, self.block_table, seq_lens, cu_q, q=q, cos=self.cos, sin=self.sin,
+                          q_norm=self.q_norm, k_norm=self.k_norm)
+        o = mhc.kv_attend(q, self.cache, self.block_table, seq_lens, cu_q, window=self.window, sinks=self.sinks)["out"]
         y = o.flatten(1) @ self.w_out.T
         return mhc.post(x, y, seam["comb"], seam["post"]), seam["pre"]
 
@@ -63,7 +73,7 @@ def ragged(lengths):
     return lens, torch.cat([lens.new_zeros(1), lens.cumsum(0, dtype=torch.int32)])
 
 
-def run(prompts=(130, 5, 77), steps=4):
+def run(prompts=(130, 5, 77), steps=4, window=None, sinks=0):
     """(stepped, at_once): x of the decoded tokens [sequences, steps, n, C], prompt first and then token by
     token, and all tokens in one call."""
     B, lengths = len(prompts), [n + steps for n in prompts]
@@ -73,17 +83,20 @@ def run(prompts=(130, 5, 77), steps=4):
     def tokens(key, begin, end):
         return torch.cat([t[b:e] for t, b, e in zip(every[key], begin, end)])
 
-    layer = AttentionSublayer(B, max(lengths))
+    layer = AttentionSublayer(B, max(lengths), window=window, sinks=sinks)
     lens, cu_q = ragged(lengths)
+    layer.room(torch.zeros_like(lens), lens)
     x, _ = layer(tokens("x", [0] * B, lengths), tokens("pre_in", [0] * B, lengths), lens, cu_q)
     at_once = torch.stack([t[-steps:] for t in x.split(lengths)])
 
-    layer = AttentionSublayer(B, max(lengths))
+    layer = AttentionSublayer(B, max(lengths), window=window, sinks=sinks)
     lens, cu_q = ragged(prompts)
+    layer.room(torch.zeros_like(lens), lens)
     layer(tokens("x", [0] * B, prompts), tokens("pre_in", [0] * B, prompts), lens, cu_q)
     x_in, pre_in = torch.empty_like(at_once[:, 0]), torch.empty_like(tokens("pre_in", [0] * B, [1] * B))
 
     def step():
+        layer.room(lens, 1)
         lens.add_(1)
         return layer(x_in, pre_in, lens)[0]
 

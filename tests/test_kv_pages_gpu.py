@@ -393,6 +393,22 @@ def test_refusals():
 
 # --------------------------------------------------------------- together ---
 
+def test_example_with_a_window():
+    """examples/attention_decode.py with a window shorter than the prompts: token by token from a replayed graph, with
+    pages handed out and let go in it, and at once; the same keys, with scales that grew differently (e4m3's half
+    step, 2^-4, on either side)."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "attention_decode.py")
+    spec = importlib.util.spec_from_file_location("attention_decode", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    stepped, at_once = (t.double() for t in m.run(window=40, sinks=3))
+    whole = m.run()[1].double()
+    assert (stepped - at_once).norm() <= 2 * 2.0 ** -4 * at_once.norm()
+    assert not torch.equal(whole, at_once)                     # the window hides something
+
+
 @pytest.mark.parametrize("D,P,H,Hq,window,sinks,seed", [(128, 16, 2, 10, None, 0, 0), (64, 16, 1, 4, 40, 5, 1),
                                                         (128, 32, 2, 8, 20, 0, 2), (64, 64, 3, 3, 100, 70, 3)])
 def test_decoding_over_shared_pages(D, P, H, Hq, window, sinks, seed):
