@@ -501,8 +501,10 @@ cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code,
     if (few)
         return head_dim == 64 ? launch_append<64, 32, 1>(a, interleaved, stream)
                               : launch_append<128, 32, 1>(a, interleaved, stream);
-    switch ((head_dim << seqs.page_log2) / 128) {     // a page is 8 steps of its group, or fewer
-        case 128: return launch_append<128, 128, 2>(a, interleaved, stream);
+    switch ((head_dim << seqs.page_log2) / 64) {      // a page is 4 steps of its group, or fewer
+        case 256: return launch_append<128, 256, 2>(a, interleaved, stream);
+        case 128: return head_dim == 64 ? launch_append<64, 128, 2>(a, interleaved, stream)
+                                        : launch_append<128, 128, 2>(a, interleaved, stream);
         case 64: return head_dim == 64 ? launch_append<64, 64, 2>(a, interleaved, stream)
                                        : launch_append<128, 64, 2>(a, interleaved, stream);
         default: return head_dim == 64 ? launch_append<64, 32, 2>(a, interleaved, stream)
