@@ -136,6 +136,7 @@ __host__ __device__ void take_own(ForkSpace& s, const ForkIn& a, Own& own, bool 
 __host__ __device__ void take_own(CompactSpace& s, const PagesIn& p, Own& own, bool rows) {
     own.take(s.bits, words_of(p.num_pages));
     if (!rows) return;
+    own.take(s.held, words_of(p.num_pages));
     own.take(s.entries, p.B);
     own.take(s.moved, p.num_pages);
     own.take(s.hole, p.num_pages);
@@ -257,6 +258,7 @@ size_t lay_out(CompactSpace& s, void* base, int64_t num_pages, int64_t B) {
     s.mark = m.take<int32_t>(2);
     s.entries = m.take<int32_t>(B);
     s.bits = m.take<uint32_t>(words_of((int)num_pages));
+    s.held = m.take<uint32_t>(words_of((int)num_pages));
     s.mover = m.take<int32_t>(num_pages);
     s.hole = m.take<int32_t>(num_pages);
     s.moved = m.take<int32_t>(num_pages);

@@ -73,7 +73,7 @@ struct ForkSpace {
 };
 
 struct CompactSpace {
-    uint32_t* bits;
+    uint32_t *bits, *held;                    // a bit for each page, in use and held
     int32_t* entries;                         // [B]: of each row, those that name its pages
     int32_t *mover, *hole, *moved;            // [num_pages]: used pages by rank; free places by rank; where a page is now
     PageCopy* copies;                         // [num_pages]
@@ -85,10 +85,21 @@ MHC_HD int pages_for(int64_t tokens, int page_log2) { return (int)((tokens + ((i
 
 MHC_HD int words_of(int num_pages) { return (num_pages + 31) / 32; }
 
-// Bits of word w that are pages.
-MHC_HD uint32_t real_pages(int num_pages, int w) {
-    const int n = num_pages - 32 * w;
-    return n >= 32 ? 0xffffffffu : (1u << n) - 1;
+// The pages in pieces that the threads divide: 8 of them where each thread gets few, so that none goes over
+// 32 bits one by one while the others wait, else whole words.
+struct Pieces {
+    int log2, count, num_pages;
+    MHC_HD int first(int64_t c) const { return (int)(c << log2); }
+    MHC_HD uint32_t real(int64_t c) const {
+        const int n = num_pages - first(c);
+        return n >= 32 ? (log2 == 5 ? 0xffffffffu : 0xffu) : ((1u << n) - 1) & (log2 == 5 ? 0xffffffffu : 0xffu);
+    }
+    MHC_HD uint32_t bits(uint32_t word, int64_t c) const { return word >> (first(c) & 31); }   // `real` of it count
+    MHC_HD int word(int64_t c) const { return first(c) >> 5; }
+};
+MHC_HD Pieces pieces_of(int num_pages, int threads) {
+    const int log2 = num_pages <= 64 * (int64_t)threads ? 3 : 5;
+    return Pieces{log2, (int)(((int64_t)num_pages + (1 << log2) - 1) >> log2), num_pages};
 }
 
 MHC_HD uint32_t held_word(const uint8_t* held, int num_pages, int w) {
@@ -311,14 +322,14 @@ MHC_HD void fork_rest(Team& t, const ForkIn& a, const ForkSpace& s, const uint32
     }
 
     // the lowest free pages
-    part_of_all(t, words, begin, end);
+    const Pieces pieces = pieces_of(p.num_pages, t.size);
+    auto free_in = [&](int64_t c) { return ~pieces.bits(t.load(s.bits + pieces.word(c)), c) & pieces.real(c); };
+    part_of_all(t, pieces.count, begin, end);
     mine = 0;
-    for (int64_t w = begin; w < end; ++w) mine += ones(~t.load(s.bits + w) & real_pages(p.num_pages, (int)w));
+    for (int64_t c = begin; c < end; ++c) mine += ones(free_in(c));
     int64_t k = t.scan(mine, total);
-    for (int64_t w = begin; w < end && k < wanted; ++w) {
-        uint32_t left = ~s.bits[w] & real_pages(p.num_pages, (int)w);
-        for (; left && k < wanted; left &= left - 1) s.given[k++] = 32 * (int32_t)w + lowest(left);
-    }
+    for (int64_t c = begin; c < end && k < wanted; ++c)
+        for (uint32_t left = free_in(c); left && k < wanted; left &= left - 1) s.given[k++] = pieces.first(c) + lowest(left);
     if (t.rank == 0 && total < wanted) t.report(kPagesError);
     t.sync();
 
@@ -380,23 +391,28 @@ template <class Team>
 MHC_HD void compact_moves(Team& t, const PagesIn& p, int32_t* top, const CompactSpace& s, const uint32_t* marked = nullptr) {
     const int log2 = p.page_log2, words = words_of(p.num_pages);
     if (marked)
-        for (int w = t.rank; w < words; w += t.size) s.bits[w] = marked[w];
+        for (int w = t.rank; w < words; w += t.size) {
+            s.bits[w] = marked[w];
+            s.held[w] = held_word(p.held, p.num_pages, w);
+        }
     if (t.rank == 0) t.store(top, 0);
     t.sync();
+    const Pieces pieces = pieces_of(p.num_pages, t.size);
+    auto held_in = [&](int64_t c) { return pieces.bits(s.held[pieces.word(c)], c) & pieces.real(c); };
+    auto used_in = [&](int64_t c) { return pieces.bits(s.bits[pieces.word(c)], c) & pieces.real(c); };
     int64_t begin, end, mine = 0, total;      // in 32 bits each: used pages, and pages, that are not held
-    part_of_all(t, words, begin, end);
-    for (int64_t w = begin; w < end; ++w) {
-        const uint32_t loose = real_pages(p.num_pages, (int)w) & ~held_word(p.held, p.num_pages, (int)w);
-        mine += (int64_t)ones(s.bits[w] & loose) << 32 | ones(loose);
+    part_of_all(t, pieces.count, begin, end);
+    for (int64_t c = begin; c < end; ++c) {
+        const uint32_t loose = pieces.real(c) & ~held_in(c);
+        mine += (int64_t)ones(used_in(c) & loose) << 32 | ones(loose);
     }
     const int64_t before = t.scan(mine, total);
     const int used = (int)(total >> 32);
     int l = (int)(before >> 32), r = (int)(before & 0xffffffff), last = -1;
-    for (int64_t w = begin; w < end; ++w) {
-        const uint32_t held = held_word(p.held, p.num_pages, (int)w), loose = real_pages(p.num_pages, (int)w) & ~held;
-        const uint32_t in_use = s.bits[w] & loose;
-        const int count = ones(loose);
-        uint32_t goal = 0;                    // the word's pages among the lowest `used`
+    for (int64_t c = begin; c < end; ++c) {
+        const uint32_t held = held_in(c), loose = pieces.real(c) & ~held, in_use = used_in(c) & loose;
+        const int count = ones(loose), first = pieces.first(c);
+        uint32_t goal = 0;                    // the piece's pages among the lowest `used`
         if (r + count <= used) {
             goal = loose;
         } else if (r < used) {
@@ -406,12 +422,12 @@ MHC_HD void compact_moves(Team& t, const PagesIn& p, int32_t* top, const Compact
         const uint32_t beyond = loose & ~goal;
         if (beyond && r + ones(goal) == used) {       // the first page beyond them
             s.mark[0] = l + ones(in_use & goal);
-            s.mark[1] = 32 * (int32_t)w + lowest(beyond);
+            s.mark[1] = first + lowest(beyond);
         }
         int hole = r - l, rank = l + ones(in_use & goal);
-        for (uint32_t x = goal & ~in_use; x; x &= x - 1) s.hole[hole++] = 32 * (int32_t)w + lowest(x);
-        for (uint32_t x = in_use & ~goal; x; x &= x - 1) s.mover[rank++] = 32 * (int32_t)w + lowest(x);
-        if (goal | held) last = 32 * (int32_t)w + highest(goal | held);
+        for (uint32_t x = goal & ~in_use; x; x &= x - 1) s.hole[hole++] = first + lowest(x);
+        for (uint32_t x = in_use & ~goal; x; x &= x - 1) s.mover[rank++] = first + lowest(x);
+        if (goal | held) last = first + highest(goal | held);
         l += ones(in_use);
         r += count;
     }
@@ -433,7 +449,10 @@ MHC_HD void compact_moves(Team& t, const PagesIn& p, int32_t* top, const Compact
 
 template <class Team>
 MHC_HD void plan_compact(Team& t, const PagesIn& p, int32_t* top, const CompactSpace& s) {
-    for (int w = t.rank; w < words_of(p.num_pages); w += t.size) s.bits[w] = 0;
+    for (int w = t.rank; w < words_of(p.num_pages); w += t.size) {
+        s.bits[w] = 0;
+        s.held[w] = held_word(p.held, p.num_pages, w);
+    }
     for (int b = t.rank; b < p.B; b += t.size)
         s.entries[b] = pages_for(checked_tokens(t, p.lens[b], p.width << p.page_log2), p.page_log2);
     t.sync();

@@ -148,7 +148,8 @@ int main() {
             std::vector<int32_t> mover = scratch<int32_t>(pages), hole = scratch<int32_t>(pages), moved = scratch<int32_t>(pages),
                                  mark = scratch<int32_t>(2), entries = scratch<int32_t>(B);
             copies = scratch<PageCopy>(pages);
-            const CompactSpace s{bits.data(), entries.data(), mover.data(), hole.data(), moved.data(), copies.data(), &count, mark.data()};
+            std::vector<uint32_t> held_bits = scratch<uint32_t>(words_of(pages));
+            const CompactSpace s{bits.data(), held_bits.data(), entries.data(), mover.data(), hole.data(), moved.data(), copies.data(), &count, mark.data()};
             if (rows_apart) {
                 std::vector<uint32_t> own = scratch<uint32_t>(words_of(pages));
                 for (uint32_t& w : bits) w = 0;
