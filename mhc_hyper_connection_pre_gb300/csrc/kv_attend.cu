@@ -774,6 +774,18 @@ __global__ void __launch_bounds__(256, kAhead == 4 ? 4 : 2) kv_join_kernel(const
 // Of the tiles of 8 and 16: up to 8 rows 104, 105 | 65, 72 for 64 sequences of 4096.
 int tile_rows(int group, int64_t B, int64_t T) { return T * group > 32 * B ? 256 : (T * group > 8 * B ? 16 : 8); }
 
+// The same with a window, which bounds a tile's keys: few keys do not pay for the tensor-memory kernel's
+// tiles (us, 16 rows and 256; 8 key heads of 128 | of 64; 64 sequences):
+//    rows   window of 8        of 64              of 256             of 1024
+//      40   22, 38 | 16, 30    40, 44 | 28, 36    55, 58 | 39, 48    108, 90 | 71, 67
+//      60   22, 39 | 20, 30    44, 45 | 32, 36    67, 59 | 45, 48    137, 91 | 87, 67
+// From 256 rows on (16 sequences) 33, 34 | 27, 28 for a window of 8, 44, 38 | 32, 32 for 64, 67, 43 | 46, 36 for 256.
+int tile_rows(int group, int64_t B, int64_t T, int window, int sinks) {
+    const int rows = tile_rows(group, B, T);
+    const int64_t keys = (int64_t)window + sinks + 128;      // and as much as 128 keys for what a tile costs besides
+    return window && rows == 256 && T * group <= 16384 / keys * B ? 16 : rows;
+}
+
 // Shares of the work: warps, or the tensor-memory kernel's blocks.  Fewer than
 // 2^kPartsLog2 up to 256 SMs.
 int shares_of(int rows, int D, int num_sms) {
@@ -822,6 +834,7 @@ cudaError_t launch_kv_attend_tc(const AttendArgs<Cut>& a, const uint8_t* k, cons
 cudaError_t launch_kv_attend_tc(const AttendArgs<WindowWork>& a, const uint8_t* k, const uint8_t* v, int head_dim,
                                 int blocks, cudaStream_t stream);
 
+// For any window: 256 rows a tile need more than 16 would.
 size_t kv_attend_workspace(int heads, int head_dim, int q_heads, int64_t B, int64_t T, int num_sms) {
     const int rows = tile_rows(q_heads / heads, B, T), shares = shares_of(rows, head_dim, num_sms);
     return part_bytes(rows, head_dim, shares) + (size_t)shares * 2 * sizeof(PartDesc);
@@ -835,7 +848,12 @@ template <class C>
 cudaError_t launch_rows(AttendArgs<C>& a, const uint8_t* k, const uint8_t* v, int heads, int head_dim, int group, void* workspace,
                         int num_sms, cudaStream_t stream) {
     const Seqs& seqs = a.seqs;
-    const int rows = tile_rows(group, seqs.B, seqs.T);
+    int window = 0, sinks = 0;
+    if constexpr (C::kWindow) {
+        window = a.cut.window;
+        sinks = a.cut.sinks;
+    }
+    const int rows = tile_rows(group, seqs.B, seqs.T, window, sinks);
     // What a tile costs beside its keys, in units.  Tensor-memory kernel: 2, 3, 4, 6, 8 took 660, 560, 515, 522, 532 us
     // for a prompt of 8192 tokens (4 heads of 128, 8 rows each), with heads of 64 458, 425, 430, 438, 446.  Warps: 0, 1, 2,
     // 3, 4, 6 took 39.5, 33.4, 31.6, 31.6, 31.7, 31.6 us for 256 sequences up to 300 keys, 700 short ones 47.5, 41.2,

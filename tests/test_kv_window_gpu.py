@@ -166,6 +166,10 @@ CASES = [
     (64, 64, 1, 43, [3, 3], [3001, 64], 1024, 0),
     (64, 16, 1, 2, [600], [1000], 450, 17),
     (128, 64, 2, 10, [700], [5000], 1024, 4),
+    (128, 64, 2, 80, None, [700, 33, 1, 0], 8, 2),                     # many rows, few keys: the one-token kernel
+    (64, 16, 1, 60, None, [300, 64, 41], 40, 5),
+    (128, 32, 1, 22, [4, 2, 0], [300, 2, 77], 60, 0),
+    (128, 64, 2, 80, None, [1700, 33, 1, 0], 300, 2),                  # and many keys: the other
 ]
 
 
@@ -290,10 +294,10 @@ def test_long_contexts(case):
     check(attend(made), *of(made))
 
 
-@pytest.mark.parametrize("Hq", [2, 16, 48])
+@pytest.mark.parametrize("Hq,window", [(2, 40), (16, 40), (48, 40), (48, 500)])
 @pytest.mark.parametrize("B", [33, 300])
-def test_many_sequences(B, Hq):
-    made = make((64, 16, 1, Hq, None, [(i * 29) % 200 for i in range(B)], 40, 5), 450)
+def test_many_sequences(B, Hq, window):
+    made = make((64, 16, 1, Hq, None, [(i * 29) % (5 * window) for i in range(B)], window, 5), 450)
     check(attend(made), *of(made))
 
 
