@@ -834,6 +834,18 @@ cudaError_t launch_kv_attend_tc(const AttendArgs<Cut>& a, const uint8_t* k, cons
 cudaError_t launch_kv_attend_tc(const AttendArgs<WindowWork>& a, const uint8_t* k, const uint8_t* v, int head_dim,
                                 int blocks, cudaStream_t stream);
 
+// With a window, whether tiles of 256 rows stay whole: a second piece of a tile costs what
+// the first did beside its keys, and its join another six units' time.  Few tiles of few keys are sooner
+// done without.  Takes the sequences to be alike, as tile_rows does.  us, cut and whole (8 key heads of 128 | of 64): 16
+// sequences of 256 rows, window 64 38.4, 26.1 | 31.6, 23.4; window 1024 54.9, 42.1 | 45.6, 36.0; 4096 tokens of 5 rows,
+// window 64 96, 86 | 77, 71; 4 sequences of 1025 rows (160 tiles on 152 SMs), window 256 40.4, 40.4 | 33.2, 36.2.
+static bool whole_tiles(const Seqs& seqs, int heads, int group, int extra, int window, int sinks, int num_sms) {
+    const int64_t rows = (int64_t)seqs.T * group, each = (rows + 256 * (int64_t)seqs.B - 1) / (256 * (int64_t)seqs.B);
+    const int64_t tiles = (int64_t)seqs.B * heads * each, keys = (int64_t)window + sinks + 256 / group + 128;
+    const int64_t units = keys / 128 + extra, rounds = (tiles + num_sms - 1) / num_sms;
+    return rounds * units * num_sms <= tiles * units + 6 * num_sms;
+}
+
 // For any window: 256 rows a tile need more than 16 would.
 size_t kv_attend_workspace(int heads, int head_dim, int q_heads, int64_t B, int64_t T, int num_sms) {
     const int rows = tile_rows(q_heads / heads, B, T), shares = shares_of(rows, head_dim, num_sms);
@@ -861,6 +873,13 @@ cudaError_t launch_rows(AttendArgs<C>& a, const uint8_t* k, const uint8_t* v, in
     const int extra = rows == 256 && head_dim == 128 ? 4 : 3;
     static_cast<Cut&>(a.cut) =
         rows == 256 ? make_cut(heads, group, 8, 7, extra) : make_cut(heads, group, rows == 8 ? 3 : 4, kUnitLog2, extra);
+    if constexpr (C::kWindow) {
+        a.cut.load_log2 = a.cut.unit_log2;
+        if (rows == 256 && whole_tiles(seqs, heads, group, extra, window, sinks, num_sms)) {
+            a.cut.unit_log2 = 30;             // a tile is one unit, whatever its keys
+            a.cut.extra = 0;
+        }
+    }
     a.shares = shares_of(rows, head_dim, num_sms);
     a.part = static_cast<float*>(workspace);
     a.desc = reinterpret_cast<PartDesc*>(static_cast<uint8_t*>(workspace) + part_bytes(rows, head_dim, a.shares));

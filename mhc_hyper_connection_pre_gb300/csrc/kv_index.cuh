@@ -139,7 +139,7 @@ struct Cut {
 };
 
 // With a window: the token at position p sees the keys j <= p with j > p - window
-// or j < sinks.  A tile's keys that none of its rows sees, whole units of them between
+// or j < sinks.  A tile's keys that none of its rows sees, whole loads of them between
 // the first ones and its first row's window, are left out of its units.  Keys are
 // then counted without them, from 0 on: of a tile those below skip_at are their own
 // places, the others lie `skip` further on.  A row's window and the first keys stay
@@ -147,6 +147,7 @@ struct Cut {
 struct WindowCut : Cut {
     static constexpr bool kWindow = true;
     int window, sinks;      // at most 2^30
+    int load_log2;          // keys of a load: 2^load_log2, no more than a unit has
 };
 
 MHC_HD Cut make_cut(int heads, int group, int tile_log2, int unit_log2, int extra) {
@@ -188,10 +189,10 @@ MHC_HD void tiles_measure(Tiles& t, const SeqInfo& s, const C& c) {
     t.keys = n < 0 ? 0 : n;
     if constexpr (C::kWindow) {
         const int first = s.before + t.token - c.window + 1;     // of its first row's window
-        const int early = ((c.sinks < t.keys ? c.sinks : t.keys) + (1 << c.unit_log2) - 1) >> c.unit_log2;
-        const int gap = (first < 0 ? 0 : first >> c.unit_log2) - early;
-        t.skip_at = early << c.unit_log2;
-        t.skip = gap > 0 ? gap << c.unit_log2 : 0;
+        const int early = ((c.sinks < t.keys ? c.sinks : t.keys) + (1 << c.load_log2) - 1) >> c.load_log2;
+        const int gap = (first < 0 ? 0 : first >> c.load_log2) - early;
+        t.skip_at = early << c.load_log2;
+        t.skip = gap > 0 ? gap << c.load_log2 : 0;
         t.keys -= t.skip;
     }
     t.units = units_of(t.keys, c);

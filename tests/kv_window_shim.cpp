@@ -23,7 +23,8 @@ int64_t kv_window_walk(const int32_t* lens, const int32_t* cu, int width, int B,
     static_cast<Cut&>(c) = make_cut(heads, group, tile_log2, unit_log2, extra);
     c.window = window;
     c.sinks = sinks;
-    const int cap = width << log2, unit = 1 << unit_log2;
+    c.load_log2 = unit_log2 > 7 ? 7 : unit_log2;
+    const int cap = width << log2, unit = 1 << c.load_log2;
     *total = 0;
     for (int b = 0; b < B; ++b) *total += units_of_seq(info_of(span_of(s, b)), c);
     if (n == 0) return 0;                                       // the units alone

@@ -157,14 +157,14 @@ def test_every_row_meets_the_keys_that_it_sees_once(window_shim, seed):
     r = random.Random(seed)
     log2, B = r.choice([4, 5, 6, 7]), r.randint(1, 5)
     heads, group = r.choice([1, 2]), r.choice([1, 1, 2, 3, 5])
-    tile_log2, unit_log2 = r.choice([(3, 5), (4, 5), (8, 7)])
+    tile_log2, unit_log2 = r.choice([(3, 5), (4, 5), (8, 7), (8, 30)])
     counts = [r.choice([0, 1, 1, r.randint(0, 20), r.randint(0, 300 // group)]) for _ in range(B)]
     lens = [r.choice([0, n, max(0, n - 2), n + r.randint(0, 900)]) for n in counts]
     if not any(counts):
         counts[0] = 1
     window, sinks = r.choice([1, 2, 17, 64, 128, r.randint(1, 700)]), r.choice([0, 0, 1, 4, 31, 32, 33, 130, r.randint(0, 500)])
     wrong, seen, looked, total, cu = _walk(window_shim, lens, counts, log2, heads, group, tile_log2, unit_log2,
-                                           r.choice([0, 3, 4]), window, sinks, r.choice([1, 7, 152, 500]))
+                                           0 if unit_log2 == 30 else r.choice([0, 3, 4]), window, sinks, r.choice([1, 7, 152, 500]))
     assert wrong == 0
     for b, n in enumerate(counts):
         pages = set()
