@@ -27,6 +27,9 @@
 // end cost 10 us a tile and more in barriers and idle warps.  Tiles that a
 // border between shares cuts are left as partial sums in the workspace and
 // joined by a second kernel.
+#include <algorithm>
+#include <cmath>
+
 #include "kv_attend.cuh"
 
 namespace mhc {
@@ -834,16 +837,25 @@ cudaError_t launch_kv_attend_tc(const AttendArgs<Cut>& a, const uint8_t* k, cons
 cudaError_t launch_kv_attend_tc(const AttendArgs<WindowWork>& a, const uint8_t* k, const uint8_t* v, int head_dim,
                                 int blocks, cudaStream_t stream);
 
-// With a window, whether tiles of 256 rows stay whole: a second piece of a tile costs what
-// the first did beside its keys, and its join another six units' time.  Few tiles of few keys are sooner
-// done without.  Takes the sequences to be alike, as tile_rows does.  us, cut and whole (8 key heads of 128 | of 64): 16
-// sequences of 256 rows, window 64 38.4, 26.1 | 31.6, 23.4; window 1024 54.9, 42.1 | 45.6, 36.0; 4096 tokens of 5 rows,
-// window 64 96, 86 | 77, 71; 4 sequences of 1025 rows (160 tiles on 152 SMs), window 256 40.4, 40.4 | 33.2, 36.2.
-static bool whole_tiles(const Seqs& seqs, int heads, int group, int extra, int window, int sinks, int num_sms) {
-    const int64_t rows = (int64_t)seqs.T * group, each = (rows + 256 * (int64_t)seqs.B - 1) / (256 * (int64_t)seqs.B);
-    const int64_t tiles = (int64_t)seqs.B * heads * each, keys = (int64_t)window + sinks + 256 / group + 128;
-    const int64_t units = keys / 128 + extra, rounds = (tiles + num_sms - 1) / num_sms;
-    return rounds * units * num_sms <= tiles * units + 6 * num_sms;
+// With a window, which bounds a tile's keys, whether tiles stay whole: few tiles of few keys are sooner done without
+// the second piece's cost beside its keys and without the join.  Takes the sequences to be alike, as tile_rows does.
+// All in units.  256 rows: cut pieces cost `extra` again, and their join six.  us, cut and whole (8 key heads of
+// 128 | of 64): 16 sequences of 256 rows, window 64 38.4, 26.1 | 31.6, 23.4; window 1024 54.9, 42.1 | 45.6, 36.0; 4096 tokens
+// of 5 rows, window 64 96, 86 | 77, 71; 4 sequences of 1025 rows (160 tiles on 152 SMs), window 256 40.4, 40.4 | 33.2, 36.2.
+// 8 and 16 rows: the join costs one and a half and one more for each 1500 rows, or 3000 where there are more tiles than
+// shares, as fewer are cut then.  128 single tokens (40 / 8 heads),
+// window 8 20.1, 16.0 | 17.6, 15.3; 64 24.2, 20.0 | 20.6, 17.8; 1024 65.7, 63.2 | 43.0, 52.6; 8 tokens, window 64 13.6,
+// 16.7 | 13.5, 15.7; 256 tokens of 16 rows (2 key heads), window 64 28.2, 21.5 | 24.1, 19.4; 1024 53.5, 65.0 | 37.6, 54.5.
+static bool whole_tiles(const Seqs& seqs, int heads, int group, int rows, int extra, int window, int sinks, int shares) {
+    const double of_seq = (double)seqs.T * group / seqs.B, each = std::ceil(of_seq / rows), tiles = seqs.B * heads * each;
+    const double tokens = (double)rows / group, rounds = std::ceil(tiles / shares);
+    if (rows == 256) {
+        const double units = std::floor((window + sinks + tokens + 128) / 128) + extra;
+        return rounds * units <= tiles * units / shares + 6;
+    }
+    const double keys = (window + sinks + std::min(tokens, of_seq / group) + 47) / 32;
+    const double join = std::min<double>(tiles, shares) * std::min<double>(rows, of_seq) / (rounds > 1 ? 3000 : 1500) + 1.5;
+    return rounds * keys <= tiles * (keys + extra) / shares + join;
 }
 
 // For any window: 256 rows a tile need more than 16 would.
@@ -873,14 +885,14 @@ cudaError_t launch_rows(AttendArgs<C>& a, const uint8_t* k, const uint8_t* v, in
     const int extra = rows == 256 && head_dim == 128 ? 4 : 3;
     static_cast<Cut&>(a.cut) =
         rows == 256 ? make_cut(heads, group, 8, 7, extra) : make_cut(heads, group, rows == 8 ? 3 : 4, kUnitLog2, extra);
+    a.shares = shares_of(rows, head_dim, num_sms);
     if constexpr (C::kWindow) {
         a.cut.load_log2 = a.cut.unit_log2;
-        if (rows == 256 && whole_tiles(seqs, heads, group, extra, window, sinks, num_sms)) {
+        if (whole_tiles(seqs, heads, group, rows, extra, window, sinks, a.shares)) {
             a.cut.unit_log2 = 30;             // a tile is one unit, whatever its keys
             a.cut.extra = 0;
         }
     }
-    a.shares = shares_of(rows, head_dim, num_sms);
     a.part = static_cast<float*>(workspace);
     a.desc = reinterpret_cast<PartDesc*>(static_cast<uint8_t*>(workspace) + part_bytes(rows, head_dim, a.shares));
     cudaError_t e;
