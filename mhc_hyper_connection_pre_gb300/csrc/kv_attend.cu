@@ -839,23 +839,27 @@ cudaError_t launch_kv_attend_tc(const AttendArgs<WindowWork>& a, const uint8_t* 
 
 // With a window, which bounds a tile's keys, whether tiles stay whole: few tiles of few keys are sooner done without
 // the second piece's cost beside its keys and without the join.  Takes the sequences to be alike, as tile_rows does.
-// All in units.  256 rows: cut pieces cost `extra` again, and their join six.  us, cut and whole (8 key heads of
-// 128 | of 64): 16 sequences of 256 rows, window 64 38.4, 26.1 | 31.6, 23.4; window 1024 54.9, 42.1 | 45.6, 36.0; 4096 tokens
-// of 5 rows, window 64 96, 86 | 77, 71; 4 sequences of 1025 rows (160 tiles on 152 SMs), window 256 40.4, 40.4 | 33.2, 36.2.
-// 8 and 16 rows: the join costs one and a half and one more for each 1500 rows, or 3000 where there are more tiles than
-// shares, as fewer are cut then.  128 single tokens (40 / 8 heads),
-// window 8 20.1, 16.0 | 17.6, 15.3; 64 24.2, 20.0 | 20.6, 17.8; 1024 65.7, 63.2 | 43.0, 52.6; 8 tokens, window 64 13.6,
-// 16.7 | 13.5, 15.7; 256 tokens of 16 rows (2 key heads), window 64 28.2, 21.5 | 24.1, 19.4; 1024 53.5, 65.0 | 37.6, 54.5.
-static bool whole_tiles(const Seqs& seqs, int heads, int group, int rows, int extra, int window, int sinks, int shares) {
+// In units of a share's time: 256 rows, 128 keys; cut pieces cost `extra` again, and the join with its launch eight.
+//   8 and 16 rows, 32 keys; `memory` is what a unit takes in every warp of an SM at HBM's rate (a unit by itself takes
+// 1.15 us); the join and its launch cost three and one more for each 1500 rows, or 3000 where there are more tiles
+// than shares, as fewer are cut then.
+//   us, cut and whole, heads of 128 | of 64.  16 sequences of 256 rows (8 key heads), window 64: 38.4, 22.7 | 31.6, 20.0;
+// 1024 54.9, 39.5 | 45.6, 33.5; 4096 97.3, 85.6 | 82.8, 77.  4096 tokens of 5 rows, window 64 96, 86 | 77, 71.  Single
+// tokens, 40 / 8 heads: 8 of them, window 8 15.2, 11.5 | 13.7, 11.4; 64 13.6, 15.2 | 13.5, 13.4; 256 15.4, 21.4 | 14.0, 19.4;
+// 128 of them, window 64 24.2, 17.9 | 20.6, 15.7; 1024 65.7, 61.4 | 43.0, 50.6; 256 of them, window 256 49.2, 53.2 | 34.8, 28.8.
+static bool whole_tiles(const Seqs& seqs, int heads, int head_dim, int group, int rows, int extra, int window, int sinks,
+                        int shares, int num_sms) {
     const double of_seq = (double)seqs.T * group / seqs.B, each = std::ceil(of_seq / rows), tiles = seqs.B * heads * each;
     const double tokens = (double)rows / group, rounds = std::ceil(tiles / shares);
     if (rows == 256) {
         const double units = std::floor((window + sinks + tokens + 128) / 128) + extra;
-        return rounds * units <= tiles * units / shares + 6;
+        return rounds * units <= tiles * units / shares + 8;
     }
     const double keys = (window + sinks + std::min(tokens, of_seq / group) + 47) / 32;
-    const double join = std::min<double>(tiles, shares) * std::min<double>(rows, of_seq) / (rounds > 1 ? 3000 : 1500) + 1.5;
-    return rounds * keys <= tiles * (keys + extra) / shares + join;
+    const double memory = (head_dim == 128 ? 0.16 : 0.08) * shares / num_sms, last = tiles - (rounds - 1) * shares;
+    const double join = std::min<double>(tiles, shares) * std::min<double>(rows, of_seq) / (rounds > 1 ? 3000 : 1500) + 3;
+    const double whole = keys * ((rounds - 1) * std::max(1.0, memory) + std::max(1.0, memory * last / shares));
+    return whole <= std::max(tiles * (keys + extra), tiles * keys * memory) / shares + join;
 }
 
 // For any window: 256 rows a tile need more than 16 would.
@@ -886,11 +890,13 @@ cudaError_t launch_rows(AttendArgs<C>& a, const uint8_t* k, const uint8_t* v, in
     static_cast<Cut&>(a.cut) =
         rows == 256 ? make_cut(heads, group, 8, 7, extra) : make_cut(heads, group, rows == 8 ? 3 : 4, kUnitLog2, extra);
     a.shares = shares_of(rows, head_dim, num_sms);
+    bool whole = false;
     if constexpr (C::kWindow) {
         a.cut.load_log2 = a.cut.unit_log2;
-        if (whole_tiles(seqs, heads, group, rows, extra, window, sinks, a.shares)) {
-            a.cut.unit_log2 = 30;             // a tile is one unit, whatever its keys
+        if (whole_tiles(seqs, heads, head_dim, group, rows, extra, window, sinks, a.shares, num_sms)) {
+            a.cut.unit_log2 = 30;             // a tile is one unit, whatever its keys, and nothing is joined
             a.cut.extra = 0;
+            whole = true;
         }
     }
     a.part = static_cast<float*>(workspace);
@@ -911,7 +917,7 @@ cudaError_t launch_rows(AttendArgs<C>& a, const uint8_t* k, const uint8_t* v, in
             e = head_dim == 64 ? launch<64, 2>(k_map, v_map, a, num_sms, stream)
                                : launch<128, 2>(k_map, v_map, a, num_sms, stream);
     }
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || whole) return e;
     const AttendArgs<Cut> join{seqs, a.cut, a.shares, a.k_scale, a.v_scale, a.q, a.q_stride, a.scale_log2, a.out, a.lse, a.part, a.desc};
     return launch_join(join, head_dim, stream);
 }
