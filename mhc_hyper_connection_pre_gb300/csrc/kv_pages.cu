@@ -34,7 +34,7 @@ struct CacheSet {
     uint8_t* code[kMaxSet][2];                // k, v
     float* scale[kMaxSet][2];
     int heads[kMaxSet], dim[kMaxSet];
-    int first[kMaxSet + 1];                   // of a page's pieces (one head of k or v): those of cache i begin here
+    int first[kMaxSet + 1];                   // of a page's pieces those of cache i begin here, k's and then as many of v
     int count;
 };
 
@@ -191,6 +191,11 @@ __global__ void __launch_bounds__(kRowThreads) kv_compact_rename_kernel(const Pa
     });
 }
 
+// One warp takes a piece at a time: of a part-filled page one head of k or v, whose filled slots lie
+// together; of a whole page (kWhole) up to kChunk bytes of k or v, all heads lying together.
+constexpr int kChunk = 16384;
+
+template <bool kWhole>
 __global__ void __launch_bounds__(256) kv_copy_kernel(const __grid_constant__ CacheSet set, const PageCopy* copies,
                                                       const int32_t* count, int page_log2) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -208,12 +213,25 @@ __global__ void __launch_bounds__(256) kv_copy_kernel(const __grid_constant__ Ca
             if (set.first[mid] <= piece) lo = mid;
             else hi = mid;
         }
-        const int heads = set.heads[lo], in_cache = piece - set.first[lo], kv = in_cache >= heads, head = in_cache - (kv ? heads : 0);
-        const int64_t from = (int64_t)c.from * heads + head, to = (int64_t)c.to * heads + head;
-        const int dim = set.dim[lo], n = c.slots * dim / 16;
-        const uint4* src = reinterpret_cast<const uint4*>(set.code[lo][kv] + ((from * dim) << page_log2));
-        uint4* dst = reinterpret_cast<uint4*>(set.code[lo][kv] + ((to * dim) << page_log2));
-        if (lane == 0) set.scale[lo][kv][to] = set.scale[lo][kv][from];
+        const int heads = set.heads[lo], dim = set.dim[lo], in_cache = piece - set.first[lo];
+        const int of_kv = (set.first[lo + 1] - set.first[lo]) / 2, kv = in_cache >= of_kv, at = in_cache - (kv ? of_kv : 0);
+        float* const scale = set.scale[lo][kv];
+        const int64_t from = (int64_t)c.from * heads, to = (int64_t)c.to * heads;     // first heads of the pages
+        int64_t off;                                  // of the piece in its page, bytes
+        int n;                                        // 16 bytes each
+        if constexpr (kWhole) {
+            off = (int64_t)at * kChunk;
+            const int64_t left = ((int64_t)heads * dim << page_log2) - off;
+            n = (int)(left < kChunk ? left : kChunk) / 16;
+            if (at == 0)
+                for (int h = lane; h < heads; h += 32) scale[to + h] = scale[from + h];
+        } else {
+            off = (int64_t)at * dim << page_log2;
+            n = c.slots * dim / 16;
+            if (lane == 0) scale[to + at] = scale[from + at];
+        }
+        const uint4* src = reinterpret_cast<const uint4*>(set.code[lo][kv] + ((from * dim) << page_log2) + off);
+        uint4* dst = reinterpret_cast<uint4*>(set.code[lo][kv] + ((to * dim) << page_log2) + off);
 #pragma unroll 1
         for (int i = lane; i < n; i += 128) {
             uint4 v[4];
@@ -287,6 +305,7 @@ cudaError_t launch_rows(Kernel kernel, const PagesIn& p, int num_sms, cudaStream
 }
 
 // `most`: copies that there may be.
+template <bool kWhole>
 cudaError_t launch_copies(const mhc_kv_cache* caches, int n, const PageCopy* copies, const int32_t* count, int64_t most,
                           int page_log2, int num_sms, cudaStream_t stream) {
     for (int begin = 0; begin < n; begin += kMaxSet) {
@@ -300,7 +319,8 @@ cudaError_t launch_copies(const mhc_kv_cache* caches, int n, const PageCopy* cop
             set.heads[i] = c.heads;
             set.dim[i] = c.head_dim;
             set.first[i] = pieces;
-            pieces += 2 * c.heads;
+            const int64_t page = (int64_t)c.heads * c.head_dim << page_log2;
+            pieces += 2 * (kWhole ? (int)((page + kChunk - 1) / kChunk) : c.heads);
         }
         set.first[set.count] = pieces;
         cudaLaunchConfig_t cfg = {};
@@ -313,7 +333,7 @@ cudaError_t launch_copies(const mhc_kv_cache* caches, int n, const PageCopy* cop
         cfg.gridDim = dim3((unsigned)(blocks < 8 * num_sms ? blocks : 8 * num_sms), 1, 1);
         cfg.blockDim = dim3(256, 1, 1);
         cfg.stream = stream;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_copy_kernel, set, copies, count, page_log2);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_copy_kernel<kWhole>, set, copies, count, page_log2);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -343,7 +363,7 @@ cudaError_t launch_kv_fork(const mhc_kv_cache* caches, int num_caches, const For
         if (e == cudaSuccess) e = launch_rows(kv_fork_rows_kernel, a.p, num_sms, stream, a, s);
         if (e == cudaSuccess) e = launch_plan(kv_fork_kernel<false>, own_bytes(s, a, false), stream, a, s);
     }
-    return e == cudaSuccess ? launch_copies(caches, num_caches, s.copies, s.count, a.p.B, a.p.page_log2, num_sms, stream) : e;
+    return e == cudaSuccess ? launch_copies<false>(caches, num_caches, s.copies, s.count, a.p.B, a.p.page_log2, num_sms, stream) : e;
 }
 
 cudaError_t launch_kv_compact(const mhc_kv_cache* caches, int num_caches, const PagesIn& p, int32_t* top, void* workspace,
@@ -361,7 +381,7 @@ cudaError_t launch_kv_compact(const mhc_kv_cache* caches, int num_caches, const 
     }
     // half of the pages at most move
     const int64_t most = p.num_pages / 2 + 1;
-    return e == cudaSuccess ? launch_copies(caches, num_caches, s.copies, s.count, most, p.page_log2, num_sms, stream) : e;
+    return e == cudaSuccess ? launch_copies<true>(caches, num_caches, s.copies, s.count, most, p.page_log2, num_sms, stream) : e;
 }
 
 cudaError_t read_pages_status(unsigned int* status) {
