@@ -43,11 +43,12 @@ struct TeamScratch {
     int64_t all;
 };
 
-// The threads of the one block that plans.
+// The threads of the one block that plans.  kOwn: the pages' bits are in shared memory for certain.
+template <bool kOwn>
 struct BlockTeam {
     int rank, size;
     TeamScratch* scratch;
-    bool own_bits;                            // the pages' bits are in shared memory
+    bool own_bits;                            // they are
 
     __device__ __forceinline__ void sync() const { __syncthreads(); }
     __device__ __forceinline__ int64_t scan(int64_t x, int64_t& total) const {
@@ -83,7 +84,7 @@ struct BlockTeam {
     }
     __device__ __forceinline__ void store(int32_t* p, int32_t x) const { *const_cast<volatile int32_t*>(p) = x; }
     __device__ __forceinline__ void set_bit(uint32_t* bits, int page) const {
-        if (own_bits)
+        if (kOwn || own_bits)
             asm volatile("{ .reg .pred p; setp.ge.s32 p, %2, 0; @p red.shared.or.b32 [%0], %1; }" ::"r"(
                              smem_u32(bits) + (page >> 5) * 4),
                          "r"(1u << (page & 31)), "r"(page)
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_fork_kernel(const ForkIn a, Fo
     const uint32_t* const marked = s.bits;
     Own own{own_memory, kOwnBytes};
     take_own(s, a, own, kRows);
-    BlockTeam team{(int)threadIdx.x, kThreads, &scratch, s.bits != marked};
+    BlockTeam<kRows> team{(int)threadIdx.x, kThreads, &scratch, s.bits != marked};
     if constexpr (kRows) plan_fork(team, a, s);
     else fork_rest(team, a, s, marked);
 }
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const PagesIn p
     const uint32_t* const marked = s.bits;
     Own own{own_memory, kOwnBytes};
     take_own(s, p, own, kRows);
-    BlockTeam team{(int)threadIdx.x, kThreads, &scratch, s.bits != marked};
+    BlockTeam<kRows> team{(int)threadIdx.x, kThreads, &scratch, s.bits != marked};
     if constexpr (kRows) plan_compact(team, p, top, s);
     else compact_moves(team, p, top, s, marked);
 }
