@@ -1,5 +1,6 @@
 // kv_append.cu -- rotation of the new tokens' queries and keys, and the write
-// of keys and values into the paged e4m3 cache (mhc_kv_append).
+// of keys and values into the paged e4m3 cache (mhc_kv_append); with norms of
+// queries and keys before the rotation (mhc_kv_append_norm).
 //
 // What bounds it: each input number is read once and each output written
 // once, a few operations a number, so memory for long prompts and the launch
@@ -11,9 +12,10 @@
 // between the passes they left half as many threads on an SM, and the loads of
 // a long prompt took 1.5 times as long.  16384 tokens of 40 query and 8 key
 // heads take 82 us: 445 MB at 5.4 TB/s (the queries alone 6.0 TB/s).  The forms
-// for many tokens that rotate spill 56 to 84 bytes a thread at the 64 registers
+// for many tokens that rotate spill 36 to 76 bytes a thread at the 64 registers
 // of four blocks an SM: cos, sin and both numbers of eight pairs are alive at once
-// beside the next step's loads.
+// beside the next step's loads.  With norms, three blocks an SM and 80 registers: 90 us, 4.9 TB/s,
+// as their instructions fill 59% of the issue slots (queries alone 5.4 TB/s).
 #include <cuda_runtime.h>
 
 #include "kv_common.cuh"
@@ -486,11 +488,11 @@ cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code,
     a.cos = cos; a.sin = sin;
     a.rope_rows = rope_rows; a.R = R;
     // Few new tokens a sequence on average: a warp for each token that may start a
-    // run.  Many: one to four warps for each window of as many tokens as a page
+    // run.  Many: one to eight warps for each window of as many tokens as a page
     // has.  Like tile_rows for attend, this takes the sequences to be alike: a
     // window of single tokens is as many runs one after the other.  A prompt of
-    // 2048 tokens beside 127 single ones takes 118 us (40 / 8 heads of 128; 14.5 and
-    // 3.7 in calls of their own), one of 1000 beside 255, a warp a page, 27.5
+    // 2048 tokens beside 127 single ones takes 116 us (40 / 8 heads of 128; 14.5 and
+    // 3.7 in calls of their own), one of 1000 beside 255, a warp a page, 27.9
     // (11.4 and 5.0).
     const bool few = seqs.T < 8 * (int64_t)seqs.B;
     a.window = few ? 1 : 1 << seqs.page_log2;

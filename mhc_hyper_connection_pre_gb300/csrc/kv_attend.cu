@@ -27,6 +27,10 @@
 // end cost 10 us a tile and more in barriers and idle warps.  Tiles that a
 // border between shares cuts are left as partial sums in the workspace and
 // joined by a second kernel.
+//
+// With a window (mhc_kv_attend_window) a tile's units are those of the keys that its rows
+// see, and a warp's masks have two ends (kv_index.cuh).  128 sequences of up to 8192 keys,
+// window 1024: 59 us, 265 MB at 4.5 TB/s; below 20 us it is launches and dependent loads.
 #include <algorithm>
 #include <cmath>
 
