@@ -490,11 +490,15 @@ cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code,
     // Few new tokens a sequence on average: a warp for each token that may start a
     // run.  Many: one to eight warps for each window of as many tokens as a page
     // has.  Like tile_rows for attend, this takes the sequences to be alike: a
-    // window of single tokens is as many runs one after the other.  A prompt of
-    // 2048 tokens beside 127 single ones takes 116 us (40 / 8 heads of 128; 14.5 and
-    // 3.7 in calls of their own), one of 1000 beside 255, a warp a page, 27.9
-    // (11.4 and 5.0).
-    const bool few = seqs.T < 8 * (int64_t)seqs.B;
+    // window of single tokens is as many runs one after the other, one a page in the
+    // worst case, and a prompt's page a single warp's.  A prompt of 2048 tokens beside 127
+    // single ones takes 32 us (40 / 8 heads of 128; 14.5 and 3.7 in calls of their own), one of 1000
+    // beside 255 27.7 (11.4 and 5.0).  From 8 to 20 tokens a sequence it is few as long as they
+    // have less than half a page.  us, many and few, 40 / 8 heads of 128, pages of 64: 32 sequences of
+    // 10 tokens 14.0, 6.8; of 17 11.6, 9.8; 128 of 10 17.6, 13.2; one of 40 5.8, 9.7; pages of 16, 32 of 17 9.1, 8.8, 96 of 8 (56
+    // query heads) 8.6, 9.8.
+    const int64_t T = seqs.T, B = seqs.B;
+    const bool few = T < 8 * B || (T <= 20 * B && 2 * T < B << seqs.page_log2);
     a.window = few ? 1 : 1 << seqs.page_log2;
     a.windows = (seqs.T + a.window - 1) / a.window;
     // With few tokens a warp takes one step of a token's heads, else all of
