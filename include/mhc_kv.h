@@ -3,13 +3,15 @@
  * attention sublayer's cache that a decoder keeps next to the mHC seam
  * (mhc.h).  Between mhc_pre_delayed, which forms the sublayer's input, and
  * mhc_post, which takes its output, an attention sublayer projects queries,
- * keys and values; mhc_kv_append rotates them and stores keys and values, and
- * mhc_kv_attend is the causal attention of the new tokens over the cache.
+ * keys and values; mhc_kv_append rotates them (mhc_kv_append_norm norms them
+ * first) and stores keys and values, and mhc_kv_attend is the causal attention
+ * of the new tokens over the cache (mhc_kv_attend_window with a sliding
+ * window).  mhc_kv_fork and mhc_kv_compact say which pages are whose.
  *
  * The conventions of mhc.h hold: caller-owned device pointers of the current
  * device, bf16 as uint16_t, asynchronous calls on the given stream, host-side
  * checks before any launch, no allocation and no synchronisation inside a
- * call; both calls can be captured in a CUDA graph.  What only the device
+ * call; every call can be captured in a CUDA graph.  What only the device
  * knows (lengths, page numbers) is checked there: see "Bad indices" below.
  */
 #ifndef MHC_KV_H
@@ -112,7 +114,8 @@ mhc_status mhc_kv_append(const mhc_kv_cache *cache, const uint16_t *k, int64_t k
  *   q_out[t][h] = bf16( R_p N q[t][h] ),   cache.k <- R_p N k[t][h]
  * held in fp32 from the inputs to the one rounding at the end; values are
  * written as they are.  Rows without a place in the cache, or with a position
- * that the rotation's tables lack, are copied as they are.  A head that holds an infinity or NaN gives what the formula gives.
+ * that the rotation's tables lack, are copied as they are.  A head that holds
+ * an infinity or NaN gives what the formula gives.
  *
  *  q_norm, k_norm  bf16 weights, head h's at h * stride (in elements: a
  *                  multiple of 8, at least head_dim; 0: all heads have the

@@ -344,6 +344,30 @@ def test_stream_graph_and_workspace():
         assert all(torch.equal(expect[k], out[k]) for k in out) and all(torch.equal(moved[k], fin[k]) for k in fin)
 
 
+def test_two_streams_at_once():
+    """Calls on two streams, each with tables and caches of its own, small and large: as one after the other."""
+    r = random.Random(16)
+    sets = []
+    for B, width, pages in ((40, 9, 500), (400, 90, 40000)):
+        lens, table = batch(r, B, width, pages, 16)
+        lens = [min(n, width * 16 - 1) for n in lens]
+        parents = _i32([r.randint(-1, B - 1) for _ in range(B)])
+        c = caches_of([(2, 64)], pages, 16, 16)
+        expect = mhc.kv_fork(c, _i32(table), _i32(lens), parents, room=1)
+        moved = mhc.kv_compact(c, expect["block_table"], expect["seq_lens"])
+        sets.append((c, _i32(table), _i32(lens), parents, expect, moved, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for c, t, n, parents, _, _, st in sets:
+            f = mhc.kv_fork(c, t, n, parents, room=1, stream=st)
+            got.append((f, mhc.kv_compact(c, f["block_table"], f["seq_lens"], stream=st)))
+    torch.cuda.synchronize()
+    for i, (f, m) in enumerate(got):
+        expect, moved = sets[i % 2][4:6]
+        assert all(torch.equal(f[k], expect[k]) for k in f) and all(torch.equal(m[k], moved[k]) for k in m)
+
+
 def test_refusals():
     r = random.Random(13)
     lens, table = batch(r, 4, 3, 30, 16)
