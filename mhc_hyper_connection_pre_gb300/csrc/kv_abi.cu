@@ -246,8 +246,8 @@ mhc_status mhc_kv_append_norm(const mhc_kv_cache* cache, const uint16_t* k, int6
     const cudaError_t e = mhc::kv::launch_kv_append(
         seqs_of(cache, block_table, table_width, seq_lens, cu_q, B, T), cache->k, cache->v, cache->k_scale,
         cache->v_scale, cache->heads, cache->head_dim, k, k_stride, v, v_stride, q, q_stride, q ? q_heads : 0, q_out,
-        q_out_stride, q_norm, q_norm_stride, k_norm, k_norm_stride, norm_eps, cos, sin, (int)rope_rows, turn ? rotary_dim : 0, interleaved ? 1 : 0,
-        static_cast<cudaStream_t>(stream));
+        q_out_stride, q_norm, q_norm_stride, k_norm, k_norm_stride, norm_eps, cos, sin, (int)rope_rows,
+        turn ? rotary_dim : 0, interleaved ? 1 : 0, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MHC_OK : MHC_ERR_CUDA;
 }
 

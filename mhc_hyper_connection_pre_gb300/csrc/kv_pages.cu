@@ -290,9 +290,10 @@ size_t lay_out(CompactSpace& s, void* base, int64_t num_pages, int64_t B) {
 // 38.8; 512 of 64 23.6, 23.2 | 47.4, 48.5; 1024 of 64 34.9, 25.8 | 90.1, 68.8; 4096 of 128 185, 49.6 | 635, 319.
 bool few_rows(const PagesIn& p) { return (int64_t)p.B * p.width <= 32768 && p.num_pages <= 1 << 20; }
 
+// The function's attribute is the most that any call uses: a call on another thread may set it in between.
 template <class Kernel, class... Args>
 cudaError_t launch_plan(Kernel kernel, int bytes, cudaStream_t stream, Args... args) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwnBytes);
     if (e != cudaSuccess) return e;
     kernel<<<1, kThreads, bytes, stream>>>(args...);
     return cudaGetLastError();

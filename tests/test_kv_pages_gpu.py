@@ -1,6 +1,7 @@
 """GPU checks of mhc_kv_fork and mhc_kv_compact against their definitions, and
 of a decoding loop over shared pages."""
 import random
+import threading
 
 import pytest
 import torch
@@ -366,6 +367,46 @@ def test_two_streams_at_once():
     for i, (f, m) in enumerate(got):
         expect, moved = sets[i % 2][4:6]
         assert all(torch.equal(f[k], expect[k]) for k in f) and all(torch.equal(m[k], moved[k]) for k in m)
+
+
+def test_two_threads_at_once():
+    """C calls of two host threads, each of its own sizes: none refuses the other's shared memory."""
+    lib = mhc.load_library()
+    failed = []
+
+    def calls(B, width, pages):
+        c = caches_of([(1, 64)], pages, 16, B)[0]
+        cache = mhc.kv._Cache(*(c[k].data_ptr() for k in ("k", "v", "k_scale", "v_scale")), pages, 1, 16, 64)
+        table, lens = _i32([[b * width + i for i in range(width)] for b in range(B)]), _i32([width * 16 - 1] * B)
+        top = torch.zeros(1, dtype=torch.int32, device="cuda")
+        need = max(lib.mhc_kv_fork_workspace_bytes(pages, width, B), lib.mhc_kv_compact_workspace_bytes(pages, B))
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        st = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        t, n = table.data_ptr(), lens.data_ptr()
+
+        def run():
+            for _ in range(1000):
+                got = [lib.mhc_kv_fork(cache, 1, t, width, n, B, None, B, None, 1, None, 0, 0, t, n, ws.data_ptr(), need,
+                                       st.cuda_stream),
+                       lib.mhc_kv_compact(cache, 1, t, width, n, B, None, t, top.data_ptr(), ws.data_ptr(), need,
+                                          st.cuda_stream)]
+                if any(got):
+                    failed.append(got)
+            st.synchronize()
+        return run, lambda: (table.tolist(), lens.tolist(), top.item())
+
+    sides = [calls(4, 3, 12), calls(60, 50, 20000)]
+    expect = [state() for _, state in sides]
+    threads = [threading.Thread(target=run) for run, _ in sides]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed[:3]
+    for (_, state), (table, lens, _), top in zip(sides, expect, (12, 3000)):
+        assert state() == (table, lens, top)
 
 
 def test_refusals():
