@@ -220,7 +220,8 @@ size_t mhc_kv_attend_workspace_bytes(const mhc_kv_cache *cache, int q_heads, int
  *             layers of a model: num_pages and page_tokens alike; heads and
  *             head_dim may differ.  Their arrays must not overlap.
  *  block_table, seq_lens   [B_in][table_width], [B_in]: of this step
- *  parents    [B], each -1 to B_in - 1, or NULL
+ *  parents    [B], each -1 to B_in - 1, or NULL; with B 0 (a batch that has
+ *             ended) nothing is done, and parents may be NULL for any B_in
  *  room       [B], or NULL; not negative.  room_all not negative.
  *  held       [num_pages] bytes, not zero for pages that others go on using
  *             (a prefix cache, say), 4-byte aligned, or NULL

@@ -299,10 +299,9 @@ mhc_status mhc_kv_fork(const mhc_kv_cache* caches, int num_caches, const int32_t
                        int32_t* seq_lens_out, void* workspace, size_t workspace_bytes, void* stream) {
     mhc_status st = check_pages(caches, num_caches, block_table, table_width, seq_lens, B_in, B, held, block_table_out);
     if (st != MHC_OK) return st;
-    if (room_all < 0 || window < 0 || sinks < 0 || (window == 0 && sinks != 0) || (!parents && B != B_in))
-        return MHC_ERR_INVALID_ARGUMENT;
-    if (B == 0) return MHC_OK;
-    if (!aligned(parents, 4) || !aligned(room, 4) || !seq_lens_out || !aligned(seq_lens_out, 4))
+    if (room_all < 0 || window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return MHC_ERR_INVALID_ARGUMENT;
+    if (B == 0) return MHC_OK;                           // an array of no parents may be a null pointer, too
+    if ((!parents && B != B_in) || !aligned(parents, 4) || !aligned(room, 4) || !seq_lens_out || !aligned(seq_lens_out, 4))
         return MHC_ERR_INVALID_ARGUMENT;
     const size_t need = mhc::kv::kv_fork_workspace(caches->num_pages, table_width, B);
     if (workspace_bytes < need || !workspace || !aligned(workspace, 256)) return MHC_ERR_INVALID_ARGUMENT;
