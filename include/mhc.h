@@ -354,8 +354,9 @@ const char *mhc_status_string(mhc_status status);
  * (a copy still in flight is then not waited for).  No test provokes a
  * timeout.  MHC_ERR_INDEX (no timeout, but one of mhc_kv.h's calls met an
  * index that mhc_kv.h calls bad since the last call).  MHC_ERR_PAGES (neither,
- * but mhc_kv_fork had fewer free pages than it was to hand out).  MHC_ERR_CUDA if the
- * synchronisation or the read failed.
+ * but mhc_kv_fork had fewer free pages than it was to hand out; where there is
+ * either, a later call returns this).  MHC_ERR_CUDA if the synchronisation or
+ * the read failed.
  */
 mhc_status mhc_device_status(void);
 

@@ -233,7 +233,8 @@ size_t mhc_kv_attend_workspace_bytes(const mhc_kv_cache *cache, int q_heads, int
  * nearest one that the table can hold, as is a length with its room; a parent
  * out of range as -1; an entry that is neither a page nor -1 as -1.  -1 is no
  * page and nothing is reported.  Where free pages run out, entries that should
- * have one stay -1, and mhc_device_status returns MHC_ERR_PAGES once.
+ * have one stay -1, and mhc_device_status returns MHC_ERR_PAGES once (after
+ * MHC_ERR_INDEX if there was a bad index as well).
  * Two kernel launches, three and a memset for large tables, and one more for
  * each 64 caches beyond the first.
  * Errors as mhc_kv_append; MHC_ERR_UNSUPPORTED for num_pages above 2^30 or

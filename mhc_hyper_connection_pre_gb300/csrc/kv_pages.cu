@@ -386,10 +386,12 @@ cudaError_t launch_kv_compact(const mhc_kv_cache* caches, int num_caches, const 
     return e == cudaSuccess ? launch_copies<true>(caches, num_caches, s.copies, s.count, most, p.page_log2, num_sms, stream) : e;
 }
 
-cudaError_t read_pages_status(unsigned int* status) {
-    unsigned int v = 0, zero = 0;
+// One query reports one thing: that pages ran out stays where a bad index, or what `other` says, comes first.
+cudaError_t read_pages_status(unsigned int* status, bool other) {
+    unsigned int v = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_pages_status, sizeof v);
-    if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_pages_status, &zero, sizeof zero);
+    const unsigned int keep = other || (v & kBadIndex) ? v & kPagesError : 0;
+    if (e == cudaSuccess && v != keep) e = cudaMemcpyToSymbol(g_pages_status, &keep, sizeof keep);
     *status = v;
     return e;
 }

@@ -43,7 +43,7 @@ namespace kv {
 cudaError_t read_append_status(unsigned int* status);
 cudaError_t read_attend_status(unsigned int* status);
 cudaError_t read_attend_tc_status(unsigned int* status);
-cudaError_t read_pages_status(unsigned int* status);
+cudaError_t read_pages_status(unsigned int* status, bool other);
 constexpr unsigned int kIndexError = 2u;   // as in kv_common.cuh
 constexpr unsigned int kPagesError = 4u;   // as in kv_pages.cuh
 }  // namespace kv
@@ -179,8 +179,8 @@ mhc_status mhc_device_status(void) {
     if (mhc::kv::read_append_status(&ka) != cudaSuccess) return MHC_ERR_CUDA;
     if (mhc::kv::read_attend_status(&kt) != cudaSuccess) return MHC_ERR_CUDA;
     if (mhc::kv::read_attend_tc_status(&kc) != cudaSuccess) return MHC_ERR_CUDA;
-    if (mhc::kv::read_pages_status(&kp) != cudaSuccess) return MHC_ERR_CUDA;
     kt |= kc;
+    if (mhc::kv::read_pages_status(&kp, v | w | c | ka | kt) != cudaSuccess) return MHC_ERR_CUDA;
     if (v | w | c | ((ka | kt) & ~mhc::kv::kIndexError)) return MHC_ERR_TIMEOUT;
     if (ka | kt | (kp & mhc::kv::kIndexError)) return MHC_ERR_INDEX;
     return kp & mhc::kv::kPagesError ? MHC_ERR_PAGES : MHC_OK;

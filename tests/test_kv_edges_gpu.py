@@ -30,3 +30,15 @@ def test_fork_of_a_batch_that_has_ended():
     got = mhc.kv_fork(cache, got["block_table"], got["seq_lens"], _i32([-1]), room=17)
     assert got["block_table"].tolist() == [[0, 1]] and got["seq_lens"].tolist() == [0]
     assert not cache["k"].view(torch.uint8).any()
+
+
+@pytest.mark.parametrize("where", ["nowhere", "fork", "attend"])
+def test_pages_that_ran_out_are_reported_after_a_bad_index(where):
+    """Both between two queries: the first tells of the index, the next of the pages, the third of nothing."""
+    cache = mhc.kv_cache(2, 1, 16, 64)
+    bad = where == "fork"                              # a full page that is none, and no place for a further token
+    got = mhc.kv_fork(cache, _i32([[0, -1], [1, 77 if bad else -1]]), _i32([16, 32 if bad else 16]), _i32([0, 0, 1]), room=1)
+    assert got["block_table"].tolist() == [[0, -1], [0, -1], [1, -1]]
+    if where == "attend":
+        mhc.kv_attend(torch.zeros(1, 1, 64, device="cuda").bfloat16(), cache, _i32([[5]]), _i32([3]))
+    assert [mhc.device_status() for _ in range(3)] == ([6, 0, 0] if where == "nowhere" else [5, 6, 0])
