@@ -211,9 +211,9 @@ mhc_status mhc_kv_append_norm(const mhc_kv_cache* cache, const uint16_t* k, int6
     if (rotary_dim < 0 || (!cos) != (!sin) || rope_rows < 0 || (q && q_heads < 1) || (!q) != (!q_out))
         return MHC_ERR_INVALID_ARGUMENT;
     if ((q_norm || k_norm) && !(norm_eps >= kLeastEps && norm_eps <= 3.0e38f)) return MHC_ERR_INVALID_ARGUMENT;
-    if (q_norm && !q) return MHC_ERR_INVALID_ARGUMENT;
     if (rotary_dim > cache->head_dim || rotary_dim % 16 != 0 || rope_rows > kMaxTokens) return MHC_ERR_UNSUPPORTED;
-    if (T == 0) return MHC_OK;
+    if (T == 0) return MHC_OK;                           // an array of no queries may be a null pointer
+    if (q_norm && !q) return MHC_ERR_INVALID_ARGUMENT;
     st = check_arrays(cache, block_table, seq_lens, cu_q);
     if (st != MHC_OK) return st;
     const int64_t row = (int64_t)cache->heads * cache->head_dim;

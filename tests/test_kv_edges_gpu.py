@@ -42,3 +42,17 @@ def test_pages_that_ran_out_are_reported_after_a_bad_index(where):
     if where == "attend":
         mhc.kv_attend(torch.zeros(1, 1, 64, device="cuda").bfloat16(), cache, _i32([[5]]), _i32([3]))
     assert [mhc.device_status() for _ in range(3)] == ([6, 0, 0] if where == "nowhere" else [5, 6, 0])
+
+
+def test_a_step_without_new_tokens():
+    """Three sequences of which none has a new token: empty queries back, the cache as it was."""
+    cache = mhc.kv_cache(3, 2, 16, 64)
+    w = torch.ones(64, device="cuda").bfloat16()
+    x = torch.zeros(0, 8, 64, device="cuda").bfloat16()
+    table, lens, cu = _i32([[0], [1], [2]]), _i32([3, 0, 16]), _i32([0, 0, 0, 0])
+    for norms in ({}, {"k_norm": w}, {"q_norm": w}, {"q_norm": w.expand(4, 64), "k_norm": w.expand(2, 64)}):
+        q = mhc.kv_append(cache, x[:, 4:6], x[:, 6:], table, lens, cu, q=x[:, :4], **norms)
+        assert q.shape == (0, 4, 64)
+        got = mhc.kv_attend(q, cache, table, lens, cu, window=4, return_lse=True)
+        assert got["out"].shape == (0, 4, 64) and got["lse"].shape == (0, 4)
+    assert not cache["k"].view(torch.uint8).any() and not cache["v_scale"].any()
