@@ -3,7 +3,7 @@
 // planning of both calls, written for a team of threads and free of device code,
 // so that it can be compiled and checked on the host, under a race detector too.
 //
-// A team T has `rank` of `size` threads (a power of two), sync(), a barrier after
+// A team T has `rank` of `size` threads (a power of two for what needs barriers), sync(), a barrier after
 // which all see what each has written, scan(x, total), the sum of x over the ranks
 // below and over all (a collective that ends in a barrier), load, set_bit (of a page, none
 // for -1), lower and raise, which may meet one another on one word, and report.
@@ -159,6 +159,7 @@ MHC_HD void each_entry(const Team& t, int rows, int width, const int32_t* from, 
     int log2 = 0;
     while ((2 << log2) <= t.size && (kWide << log2) < width) ++log2;
     const int lanes = 1 << log2, at_once = t.size >> log2, lane = t.rank & (lanes - 1);
+    if (t.rank >> log2 >= at_once) return;    // threads left over, where a row's do not divide a grid's: an entry is one thread's alone
     bool bad = false;
     MHC_ROLLED
     for (int b0 = t.rank >> log2; b0 < rows; b0 += kRows * at_once)

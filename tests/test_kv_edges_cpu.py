@@ -1,5 +1,12 @@
 """Host-only checks of calls of the paged cache at their edges."""
-from test_kv_more_cpu import CUDA_ERR, FAKE, INVALID, NO_DEVICE, OK, _append_norm, _fork, lib  # noqa: F401  (lib is a fixture)
+import os
+import random
+import subprocess
+
+import pytest
+
+from test_kv_more_cpu import (CUDA_ERR, FAKE, HERE, INVALID, NO_DEVICE, OK, _append_norm, _flat, _fork, _planned, lib,  # noqa: F401
+                              plan_compact, plan_fork)             # (lib is a fixture)
 
 
 def test_a_batch_that_has_ended(lib):
@@ -23,3 +30,36 @@ def test_norms_of_no_tokens(lib):
         assert _append_norm(lib, T=0, B=0, k=None, v=None, q=None, q_out=None, q_norm=q_norm) == OK
         assert _append_norm(lib, T=0, B=3, cu=FAKE, k=None, v=None, q=None, q_out=None, q_norm=q_norm) == OK
     assert _append_norm(lib, q=None, q_out=None) == INVALID        # keys alone have no queries to norm
+
+
+@pytest.fixture(scope="module")
+def rows_exe(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("rows") / "rows")
+    subprocess.run(["g++", "-O1", "-g", "-std=c++17", "-fsanitize=thread", "-fno-sanitize-recover=all",
+                    os.path.join(HERE, "kv_rows_shim.cpp"), "-o", exe, "-pthread"], check=True)
+    return exe
+
+
+@pytest.mark.parametrize("make", ["fork", "compact"])
+def test_rows_in_place_by_any_number_of_threads(rows_exe, make):
+    """As many threads as a grid has, which is no power of two and no multiple of a wide row's threads: each
+    entry is one thread's alone (the thread sanitizer ends the program otherwise), and the definition's."""
+    r, cases = random.Random(17), []
+    for size in (3, 5, 6, 11, 12, 20, 24, 44):
+        for width in (1, 9, 40, 150):
+            log2, B = 4, r.choice([1, 2, 5, 9, 13])
+            pages = B * width + 7
+            order = r.sample(range(pages), B * width)
+            table = [[x if r.random() < 0.9 else -1 for x in order[b * width:(b + 1) * width]] for b in range(B)]
+            lens = [r.choice([0, width << log2, r.randint(0, width << log2)]) for _ in range(B)]
+            head = [0 if make == "fork" else 1, size, width, B, log2, pages, *_flat(table), *lens]
+            if make == "fork":
+                room, window = r.choice([0, 1, 30]), r.choice([0, 1, 100])
+                sinks = r.choice([0, 20]) if window else 0
+                out, n, copies, status = plan_fork(table, lens, pages, log2, None, room, window, sinks, None)
+                cases.append((head + [room, window, sinks], [*n, *_flat(out), status, len(copies), *_flat(copies)]))
+            else:
+                out, top, copies, status = plan_compact(table, lens, pages, log2, None)
+                cases.append((head, [top, *_flat(out), status, len(copies), *_flat(copies)]))
+    got = _planned(rows_exe, [c for c, _ in cases])
+    assert got == [want for _, want in cases]

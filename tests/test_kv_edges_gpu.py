@@ -1,8 +1,11 @@
 """GPU checks of calls of the paged cache at their edges."""
+import random
+
 import pytest
 import torch
 
 import mhc_hyper_connection_pre_gb300 as mhc
+from test_kv_more_cpu import plan_compact, plan_fork
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +59,22 @@ def test_a_step_without_new_tokens():
         got = mhc.kv_attend(q, cache, table, lens, cu, window=4, return_lse=True)
         assert got["out"].shape == (0, 4, 64) and got["lse"].shape == (0, 4)
     assert not cache["k"].view(torch.uint8).any() and not cache["v_scale"].any()
+
+
+@pytest.mark.parametrize("B,width", [(5, 8192), (9, 5000), (11, 3001)])
+def test_wide_tables_in_place(B, width):
+    """Rows whose threads do not divide the grid's, written in place: the definition's tables."""
+    P, pages = 16, B * width + 50
+    r = random.Random(width)
+    order = r.sample(range(pages), B * width)
+    lens = [r.randint(0, width * P - 20) if b else width * P - 20 for b in range(B)]
+    table = [[order[b * width + i] if i * P < lens[b] and r.random() < 0.95 else -1 for i in range(width)] for b in range(B)]
+    cache = mhc.kv_cache(pages, 1, P, 64)
+    at, n = _i32(table), _i32(lens)
+    out, want, _, _ = plan_fork(table, lens, pages, 4, None, 17, 3000, 40, None)
+    mhc.kv_fork(cache, at, n, room=17, window=3000, sinks=40, out={"block_table": at, "seq_lens": n})
+    assert at.tolist() == out and n.tolist() == want
+    at, n = _i32(table), _i32(lens)
+    out, top, _, _ = plan_compact(table, lens, pages, 4, None)
+    got = mhc.kv_compact(cache, at, n, out={"block_table": at, "pages": _i32(0)})
+    assert got["block_table"].tolist() == out and got["pages"].item() == top
