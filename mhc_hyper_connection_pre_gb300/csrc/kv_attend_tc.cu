@@ -70,6 +70,7 @@ constexpr int kPair = 2 * kTile;              // rows of a block's work
 constexpr int kKStages = 3, kVStages = 2;
 constexpr int kMetas = 2 * kKStages;          // the softmax reads a load's key scales after its stage is free
 constexpr float kVLift = 128.0f;              // V in f16 is 2^7 times code * scale / largest scale
+constexpr int kHighEnd = 1024;                // a stretch of kv_index.cuh's Ends is no longer: 256 tokens and two loads
 constexpr int kSegs = 4;                      // segments whose value scale and NaNs are kept: the converter runs two ahead
 
 struct __align__(16) Meta {                   // of one load: the scales of each 16 keys, which of them have a page
@@ -91,7 +92,8 @@ struct __align__(1024) Smem {
     int count;                                // of segs
     Meta k_meta[kMetas];
     Meta v_meta[kVStages];
-    int nan_key[kSegs][D];                    // first key with NaN in each dim, among those that not every row sees
+    int nan_key[kSegs][D];                    // of the keys that not every row sees: the first with NaN in each dim; with a
+                                              // window a bit for each that has NaN, from kHighEnd on those at the windows' ends
     int has_nan[kSegs];
     float ref[kSegs];                         // largest value scale of the segment
     float red[4];
@@ -274,35 +276,42 @@ __device__ __forceinline__ int steps_of(bool split, int keys) {
 }
 
 // NaN for 32 dims (from c * 32 on) of the row that sees the segment's keys up to the n-th, where a
-// value among those that not every row sees is NaN.  Rare, so the codes are read once more: which rows see which
-// keys differs at both ends of a window, and would need a set of keys for each dim.
+// value among those that not every row sees is NaN.  Rare, so the codes of the keys that have NaN are read once
+// more: which rows see which keys differs at both ends of a window, and would need a set of keys for each dim.
+// 512 tokens of 40 / 8 heads of 128 over 5000 keys, window 4096: 69 us without NaN, 88 with one value at the windows'
+// beginning; 5381 with all of the segment's codes read again.
 template <int D, class C>
-__device__ __noinline__ void nan_dims(const AttendArgs<C>& a, const WindowSegment& s, int c, int n, uint32_t& mask) {
-    const int log2 = a.seqs.page_log2, first = first_seen(s, a.cut);
+__device__ __noinline__ void nan_dims(const AttendArgs<C>& a, const WindowSegment& s, const int* marks, int c, int n,
+                                      uint32_t& mask) {
+    const int log2 = a.seqs.page_log2;
     const int32_t* row = a.seqs.table + (int64_t)s.b * a.seqs.width;
+    const Ends ends = ends_of(s, a.cut);
     mask = 0;
 #pragma unroll 1
-    for (int key = s.key0; key < s.keys; ++key) {
-        const int place = place_of_key(s, key);
-        if (!page_seen(place, first, a.cut.sinks, log2)) continue;
-        const int page = __ldg(row + (place >> log2));
-        if (page < 0 || page >= a.seqs.num_pages) continue;
-        const uint8_t* from =
-            a.cut.v + ((((int64_t)page * a.cut.heads + s.head) << log2) + (place & ((1 << log2) - 1))) * D + c * 32;
-        uint32_t found = 0;
+    for (int w = 0; w < 2 * kHighEnd / 32; ++w)
+#pragma unroll 1
+        for (uint32_t left = marks[w]; left; left &= left - 1) {
+            const int bit = 32 * w + __ffs(left) - 1, key = bit < kHighEnd ? ends.low + bit : ends.high + bit - kHighEnd;
+            const int place = place_of_key(s, key), page = __ldg(row + (place >> log2));
+            if (page < 0 || page >= a.seqs.num_pages) continue;
+            const uint8_t* from =
+                a.cut.v + ((((int64_t)page * a.cut.heads + s.head) << log2) + (place & ((1 << log2) - 1))) * D + c * 32;
+            uint32_t found = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t w = nan_bytes(__ldg(reinterpret_cast<const uint32_t*>(from) + i)) >> 7;
-            found |= ((w & 1) | (w >> 7 & 2) | (w >> 14 & 4) | (w >> 21 & 8)) << (4 * i);
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t x = nan_bytes(__ldg(reinterpret_cast<const uint32_t*>(from) + i)) >> 7;
+                found |= ((x & 1) | (x >> 7 & 2) | (x >> 14 & 4) | (x >> 21 & 8)) << (4 * i);
+            }
+            if (key_seen(key, n, a.cut)) mask |= found;
         }
-        if (key_seen(key, n, a.cut)) mask |= found;
-    }
 }
 
 template <int D, class C>
-__device__ __forceinline__ void put_nans(const AttendArgs<C>& a, const WindowSegment& s, int c, int n, uint32_t (&o)[32]) {
+__device__ __forceinline__ void put_nans(const AttendArgs<C>& a, const WindowSegment& s, const int* marks, int c, int n,
+                                         uint32_t (&o)[32]) {
+    static_assert(2 * kHighEnd <= 32 * D, "a bit for each key of both ends");
     uint32_t mask;
-    nan_dims<D>(a, s, c, n, mask);
+    nan_dims<D>(a, s, marks, c, n, mask);
 #pragma unroll
     for (int i = 0; i < 32; ++i)
         if ((mask >> i) & 1) o[i] = 0x7fc00000u;
@@ -623,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * unit);
                     if constexpr (C::kWindow) {
-                        if (nans) put_nans<D>(a, sm.segs[index], c, lim, o);
+                        if (nans) put_nans<D>(a, sm.segs[index], sm.nan_key[kept], c, lim, o);
                     } else if (nans) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -688,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
                 if (lane == 0) sm.red[warp - 8] = most;
-                for (int i = id; i < D; i += 128) sm.nan_key[slot][i] = 0x7fffffff;
+                for (int i = id; i < D; i += 128) sm.nan_key[slot][i] = C::kWindow ? 0 : 0x7fffffff;
                 if (id == 0) sm.has_nan[slot] = 0;
                 named_bar_sync(1, 128);
                 most = value_unit(fmaxf(fmaxf(sm.red[0], sm.red[1]), fmaxf(sm.red[2], sm.red[3])));
@@ -756,7 +765,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                                 if (any) {
                                     sm.has_nan[slot] = 1;
-                                    if constexpr (!C::kWindow) {
+                                    if constexpr (C::kWindow) {
+                                        const Ends ends = ends_of(seg, a.cut);
+                                        const int k = key + id, bit = k < ends.low_end && k >= ends.low ? k - ends.low
+                                                                                                        : kHighEnd + k - ends.high;
+                                        atomicOr(&sm.nan_key[slot][bit >> 5], 1 << (bit & 31));
+                                    } else {
 #pragma unroll 1
                                         for (int b = 0; b < 16; ++b)
                                             if ((sm.v[vr.stage][chunk_at<D>(id, c) + b] & 0x7f) == 0x7f)

@@ -320,6 +320,24 @@ MHC_HD bool keys_all_seen(int key, int count, int n0, int n1, const WindowCut& c
     return key + count <= n0 && (key + count <= c.sinks || n1 - key <= c.window);
 }
 
+// A segment's keys that not every row of the tile sees, in two stretches: where the rows' windows begin, and where
+// they end.  Each row's token comes at most one after the row's before it, and the keys between the first ones and the first
+// row's window are whole loads but for less than one at either end; so neither stretch is longer
+// than the tile's tokens and two loads, whatever the window.
+struct Ends {
+    int low, low_end, high, high_end;         // none where the end is not beyond the beginning
+};
+MHC_HD Ends ends_of(const WindowSegment& s, const WindowCut& c) {
+    const int n0 = keys_of_row(s, c, 0), begin = keys_of_row(s, c, s.rows - 1) - c.window;
+    Ends e;
+    e.high = n0 > s.key0 ? n0 : s.key0;
+    e.high_end = s.keys;
+    e.low = c.sinks > s.key0 ? c.sinks : s.key0;
+    e.low_end = begin < e.high ? begin : e.high;
+    if (e.low_end > s.keys) e.low_end = s.keys;
+    return e;
+}
+
 // A walk over a share's segments.
 struct Walk {
     Tiles t;

@@ -1,11 +1,13 @@
 """Host-only checks of calls of the paged cache at their edges."""
+import ctypes
 import os
 import random
 import subprocess
 
+import numpy as np
 import pytest
 
-from test_kv_more_cpu import (CUDA_ERR, FAKE, HERE, INVALID, NO_DEVICE, OK, _append_norm, _flat, _fork, _planned, lib,  # noqa: F401
+from test_kv_more_cpu import (CUDA_ERR, FAKE, HERE, INVALID, NO_DEVICE, OK, _append_norm, _flat, _fork, _planned, _ptr, lib,  # noqa: F401
                               plan_compact, plan_fork)             # (lib is a fixture)
 
 
@@ -63,3 +65,31 @@ def test_rows_in_place_by_any_number_of_threads(rows_exe, make):
                 cases.append((head, [top, *_flat(out), status, len(copies), *_flat(copies)]))
     got = _planned(rows_exe, [c for c, _ in cases])
     assert got == [want for _, want in cases]
+
+
+@pytest.fixture(scope="module")
+def ends_shim(tmp_path_factory):
+    so = str(tmp_path_factory.mktemp("ends") / "libkvends.so")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover=undefined", "-shared",
+                    "-fPIC", "-x", "c++", os.path.join(HERE, "kv_ends_shim.cpp"), "-o", so], check=True)
+    lib = ctypes.CDLL(so)
+    lib.kv_window_ends.restype = ctypes.c_int64
+    return lib
+
+
+@pytest.mark.parametrize("seed", range(80))
+def test_ends_of_windows_are_short(ends_shim, seed):
+    """The keys that not every row of a tile sees lie in two stretches, neither longer than its tokens and two loads of
+    128, whatever the window: what is done again for a value that is NaN does not grow with it."""
+    r = random.Random(seed)
+    log2, B, group = r.choice([4, 5, 6, 7]), r.randint(1, 3), r.choice([1, 1, 2, 3, 5, 40])
+    counts = [r.choice([1, r.randint(1, 20), r.randint(1, 700 // group)]) for _ in range(B)]
+    lens = [r.choice([0, n, max(0, n - 2), n + r.randint(0, 9000)]) for n in counts]
+    window, sinks = r.choice([1, 17, 128, 300, r.randint(1, 7000)]), r.choice([0, 1, 4, 127, 128, 129, r.randint(0, 5000)])
+    width, cu = max(1, (max(lens) + (1 << log2) - 1) >> log2), np.cumsum([0] + counts).astype(np.int32)
+    longest, segments = ctypes.c_int32(0), ctypes.c_int32(0)
+    unit, extra, shares = r.choice([(7, 4, 152), (7, 3, 7), (30, 0, 152), (30, 0, 1)])
+    wrong = ends_shim.kv_window_ends(_ptr(np.array(lens, np.int32)), _ptr(cu), width, B, int(cu[-1]), log2, r.choice([1, 2]), group,
+                                     unit, extra, window, sinks, shares, ctypes.byref(longest), ctypes.byref(segments))
+    assert wrong == 0 and segments.value > 0
+    assert longest.value <= -(-256 // group) + 1 + 256

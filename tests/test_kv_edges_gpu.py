@@ -6,6 +6,7 @@ import torch
 
 import mhc_hyper_connection_pre_gb300 as mhc
 from test_kv_more_cpu import plan_compact, plan_fork
+from test_kv_window_gpu import attend, check, make, of
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +79,71 @@ def test_wide_tables_in_place(B, width):
     out, top, _, _ = plan_compact(table, lens, pages, 4, None)
     got = mhc.kv_compact(cache, at, n, out={"block_table": at, "pages": _i32(0)})
     assert got["block_table"].tolist() == out and got["pages"].item() == top
+
+
+WIDE = [
+    # D, P, H, Hq, new tokens, lengths, window, sinks
+    (128, 64, 2, 10, [300], [5000], 4096, 40), (64, 16, 1, 1, [600], [5000], 3000, 0), (64, 128, 2, 16, [20, 90], [4100, 6000], 4096, 500),
+    (128, 32, 1, 40, [30], [9000], 8000, 129),
+]
+
+
+@pytest.mark.parametrize("case", WIDE)
+def test_nan_values_in_wide_windows(case):
+    """NaN at both ends of windows of thousands of keys, in the middle and among the first: NaN in those dims of the rows that
+    see them, no other number changes; and a call with one takes about as long as one without."""
+    D, P, H, Hq, counts, lens, window, sinks = case
+    made, clean = make(case, 500), make(case, 500)
+    q, cache, rows, _, cu, _, _ = made
+    put = []
+    for b, (m, n) in enumerate(zip(counts, lens)):
+        for j in {0, sinks, n - m - window, n - m - window + 1, n - m - window + 2, n - window - m // 2, n - window, n - 1500, n - m,
+                  n - m // 2, n - 2, n - 1}:
+            if 0 <= j < n and rows[b][j // P] >= 0:
+                d = (7 * j + 3) % D
+                for k, c in enumerate((cache, clean[1])):
+                    c["v"].view(torch.uint8)[rows[b][j // P], j % H, j % P, d] = 0x38 if k else (0x7F if j % 2 else 0xFF)
+                put.append((b, j, j % H, d))
+    got, expect = attend(made), attend(clean)
+    check(expect, *of(clean))
+    nan, G = torch.zeros_like(got["out"], dtype=torch.bool), Hq // H
+    for b, j, h, d in put:
+        for t in range(cu[b], cu[b + 1]):
+            p = lens[b] - (cu[b + 1] - t)
+            if j <= p and (j > p - window or j < sinks):
+                nan[t, h * G:(h + 1) * G, d] = True
+    assert nan.any() and not nan.all(-1).any()
+    assert torch.equal(got["out"].isnan(), nan)
+    assert torch.equal(got["out"][~nan], expect["out"][~nan]) and torch.equal(got["lse"], expect["lse"])
+
+    def us(made):                                                  # the least of a few calls
+        q, cache, rows, lens, cu, window, sinks = made
+        args, best = (q, cache, _i32(rows), _i32(lens), _i32(cu)), 1e9
+        for _ in range(10):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            mhc.kv_attend(*args, window=window, sinks=sinks)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, 1e3 * a.elapsed_time(b))
+        return best
+    with_nan, without = us(made), us(clean)
+    assert with_nan < 3 * without + 100, (with_nan, without)
+
+
+def test_ends_full_of_nan():
+    """Every value a window's ends hold is NaN: NaN in every row that sees one of them, whose number is the definition's."""
+    case = (64, 32, 1, 5, [200], [3000], 700, 10)
+    D, P, H, Hq, counts, lens, window, sinks = case
+    made, clean = make(case, 510), make(case, 510)
+    q, cache, rows, _, cu, _, _ = made
+    m, n = counts[0], lens[0]
+    where = [*range(n - m - window, n - m - window + 120), *range(n - 60, n)]
+    for j in where:
+        for k, c in enumerate((cache, clean[1])):
+            c["v"].view(torch.uint8)[rows[0][j // P], :, j % P] = 0x38 if k else 0x7F
+    got, expect = attend(made), attend(clean)
+    see = torch.tensor([any(j <= p and j > p - window for j in where) for p in range(n - m, n)], device="cuda")
+    assert see.any() and not see.all()
+    assert got["out"][see].isnan().all() and torch.equal(got["out"][~see], expect["out"][~see])
+    assert torch.equal(got["lse"], expect["lse"])
