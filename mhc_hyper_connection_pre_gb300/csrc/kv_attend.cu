@@ -851,19 +851,24 @@ cudaError_t launch_kv_attend_tc(const AttendArgs<WindowWork>& a, const uint8_t* 
 // 1024 54.9, 39.5 | 45.6, 33.5; 4096 97.3, 85.6 | 82.8, 77.  4096 tokens of 5 rows, window 64 96, 86 | 77, 71.  Single
 // tokens, 40 / 8 heads: 8 of them, window 8 15.2, 11.5 | 13.7, 11.4; 64 13.6, 15.2 | 13.5, 13.4; 256 15.4, 21.4 | 14.0, 19.4;
 // 128 of them, window 64 24.2, 17.9 | 20.6, 15.7; 1024 65.7, 61.4 | 43.0, 50.6; 256 of them, window 256 49.2, 53.2 | 34.8, 28.8.
+//   A whole tile is one warp's, or block's, walk, of which a batch of one long sequence and short ones consists, and which
+// grows with the window: so only up to some 41 us of it, 36 units of 32 keys or 22 of 128.  One token of 32768 beside 127 of
+// 500, heads of 128, cut and whole: window 1024 48.8, 60.0; 2048 47.7, 92.8; 4096 49.8, 164; 32768 61.1, 1152 (without a window 60).
+// 51 tokens of 32768 beside 15 sequences of 500: 2048 43.7, 51.8; 4096 43.7, 78.5 (without 66).  What that leaves to alike
+// batches: 128 single tokens 126.6, 113.3 for a window of 2048 and 229, 197 for 4096; 16 x 255 rows 96.9, 82.6 for 4096.
 static bool whole_tiles(const Seqs& seqs, int heads, int head_dim, int group, int rows, int extra, int window, int sinks,
                         int shares, int num_sms) {
     const double of_seq = (double)seqs.T * group / seqs.B, each = std::ceil(of_seq / rows), tiles = seqs.B * heads * each;
     const double tokens = (double)rows / group, rounds = std::ceil(tiles / shares);
     if (rows == 256) {
         const double units = std::floor((window + sinks + tokens + 128) / 128) + extra;
-        return rounds * units <= tiles * units / shares + 8;
+        return units <= 22 && rounds * units <= tiles * units / shares + 8;
     }
     const double keys = (window + sinks + std::min(tokens, of_seq / group) + 47) / 32;
     const double memory = (head_dim == 128 ? 0.16 : 0.08) * shares / num_sms, last = tiles - (rounds - 1) * shares;
     const double join = std::min<double>(tiles, shares) * std::min<double>(rows, of_seq) / (rounds > 1 ? 3000 : 1500) + 3;
     const double whole = keys * ((rounds - 1) * std::max(1.0, memory) + std::max(1.0, memory * last / shares));
-    return whole <= std::max(tiles * (keys + extra), tiles * keys * memory) / shares + join;
+    return keys <= 36 && whole <= std::max(tiles * (keys + extra), tiles * keys * memory) / shares + join;
 }
 
 // For any window: 256 rows a tile need more than 16 would.

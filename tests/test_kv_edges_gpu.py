@@ -81,6 +81,20 @@ def test_wide_tables_in_place(B, width):
     assert got["block_table"].tolist() == out and got["pages"].item() == top
 
 
+def us(made, windowed=True):
+    """The least time of a few calls."""
+    q, cache, rows, lens, cu, window, sinks = made
+    args, best = (q, cache, _i32(rows), _i32(lens), None if cu is None else _i32(cu)), 1e9
+    for _ in range(10):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        mhc.kv_attend(*args, **({"window": window, "sinks": sinks} if windowed else {}))
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, 1e3 * a.elapsed_time(b))
+    return best
+
+
 WIDE = [
     # D, P, H, Hq, new tokens, lengths, window, sinks
     (128, 64, 2, 10, [300], [5000], 4096, 40), (64, 16, 1, 1, [600], [5000], 3000, 0), (64, 128, 2, 16, [20, 90], [4100, 6000], 4096, 500),
@@ -115,18 +129,6 @@ def test_nan_values_in_wide_windows(case):
     assert nan.any() and not nan.all(-1).any()
     assert torch.equal(got["out"].isnan(), nan)
     assert torch.equal(got["out"][~nan], expect["out"][~nan]) and torch.equal(got["lse"], expect["lse"])
-
-    def us(made):                                                  # the least of a few calls
-        q, cache, rows, lens, cu, window, sinks = made
-        args, best = (q, cache, _i32(rows), _i32(lens), _i32(cu)), 1e9
-        for _ in range(10):
-            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-            a.record()
-            mhc.kv_attend(*args, window=window, sinks=sinks)
-            b.record()
-            torch.cuda.synchronize()
-            best = min(best, 1e3 * a.elapsed_time(b))
-        return best
     with_nan, without = us(made), us(clean)
     assert with_nan < 3 * without + 100, (with_nan, without)
 
@@ -147,3 +149,22 @@ def test_ends_full_of_nan():
     assert see.any() and not see.all()
     assert got["out"][see].isnan().all() and torch.equal(got["out"][~see], expect["out"][~see])
     assert torch.equal(got["lse"], expect["lse"])
+
+
+@pytest.mark.parametrize("tokens,short,window", [(1, 127, 2048), (1, 127, 16384), (1, 99, 8192), (51, 15, 4096)])
+def test_one_long_sequence_in_a_wide_window(tokens, short, window):
+    """One long sequence beside short ones: a window saves work, so the call takes no longer than without one (to a
+    fifth and 10 us); and the long sequence's rows are the definition's."""
+    counts, lens = None if tokens == 1 else [tokens] * (short + 1), [20000] + [500] * short
+    made = make((128, 64, 2, 10, counts, lens, window, 4), 520)
+    q, cache, rows, _, cu, _, _ = made
+    rows = [r + [-1] * 100 for r in rows]                              # a table that has room for longer ones
+    every = [[max(x, 0) for x in r] for r in rows]
+    got = attend((q, cache, rows, lens, cu, window, 4))
+    n = 1 if cu is None else tokens
+    check({k: t[:n] for k, t in got.items()}, q[:n], cache, rows[:1], lens[:1], None if cu is None else cu[:2], 128 ** -0.5, window, 4)
+    # heads as a model has them, for the time
+    wide = mhc.kv_cache(cache["k"].shape[0], 8, 64, 128)
+    x = torch.randn(q.shape[0], 40, 128, device="cuda").bfloat16()
+    with_window, without = us((x, wide, rows, lens, cu, window, 4)), us((x, wide, every, lens, cu, None, 0), False)
+    assert with_window < 1.2 * without + 10, (with_window, without)
