@@ -491,15 +491,17 @@ cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code,
     // run.  Many: one to eight warps for each window of as many tokens as a page
     // has.  Like tile_rows for attend, this takes the sequences to be alike: a
     // window of single tokens is as many runs one after the other, one a page in the
-    // worst case, and a prompt's page a single warp's.  A prompt of 2048 tokens beside 127
-    // single ones takes 32 us (40 / 8 heads of 128; 14.5 and 3.7 in calls of their own), one of 1000
-    // beside 255 27.7 (11.4 and 5.0).  From 8 to 20 tokens a sequence it is few as long as they
-    // have less than half a page.  us, many and few, 40 / 8 heads of 128, pages of 64: 32 sequences of
-    // 10 tokens 14.0, 6.8; of 17 11.6, 9.8; 128 of 10 17.6, 13.2; one of 40 5.8, 9.7; pages of 16, 32 of 17 9.1, 8.8, 96 of 8 (56
-    // query heads) 8.6, 9.8.
+    // worst case.  One prompt of 1000 tokens beside 255 single ones takes 27.7 us (11.4 and 5.0 in calls of their own).
+    //   From 8 to 20 tokens a sequence, of less than half a page: windows of four tokens, by half of the page's warps, as
+    // a run is short; then neither single tokens beside a prompt wait long for one another, nor a prompt's page for a
+    // single warp.  us, windows of a page, a warp for each token, and these; 40 / 8 heads of 128, pages of 128 | heads of
+    // 64, pages of 64: one of 16 8.8, 12.9, 8.9 | 8.8, 10.9, 8.9; 32 of 10 39.6, 13.0, 13.0 | 29.3, 12.9, 12.9; 128 of 10 43.0,
+    // 21.1, 23.2 | 31.4, 17.0, 15.0; one of 150 and 7 of 1 21.1, 55.9, 17.2 | 23.2, 19.1, 17.1; one of 1500 and 127 of 1 201, 68.2,
+    // 29.3 | 152, 27.3, 23.1.  Windows of 8, heads of 64: 15 single tokens beside one of 200 23.2 instead of 17.1.
+    // With norms, heads of 128, pages of 128, a warp for each token and these: 128 of 10 22.5, 30.1; one of 150 and 7 of 1 53.8, 19.8.
     const int64_t T = seqs.T, B = seqs.B;
-    const bool few = T < 8 * B || (T <= 20 * B && 2 * T < B << seqs.page_log2);
-    a.window = few ? 1 : 1 << seqs.page_log2;
+    const bool few = T < 8 * B, some = T <= 20 * B && 2 * T < B << seqs.page_log2;
+    a.window = few ? 1 : some ? 4 : 1 << seqs.page_log2;
     a.windows = (seqs.T + a.window - 1) / a.window;
     // With few tokens a warp takes one step of a token's heads, else all of
     // them, so that the position is found and its row of cos and sin read once.
@@ -507,7 +509,7 @@ cudaError_t launch_kv_append(const Seqs& seqs, uint8_t* k_code, uint8_t* v_code,
     if (few)
         return head_dim == 64 ? launch_append<64, 32, 1>(a, interleaved, stream)
                               : launch_append<128, 32, 1>(a, interleaved, stream);
-    switch ((head_dim << seqs.page_log2) / 64) {      // a page is 4 steps of its group, or fewer
+    switch ((head_dim << seqs.page_log2) / (some ? 128 : 64)) {      // a page is 4 steps of its group, or fewer
         case 256: return launch_append<128, 256, 2>(a, interleaved, stream);
         case 128: return head_dim == 64 ? launch_append<64, 128, 2>(a, interleaved, stream)
                                         : launch_append<128, 128, 2>(a, interleaved, stream);

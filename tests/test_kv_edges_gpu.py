@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import mhc_hyper_connection_pre_gb300 as mhc
+from kv_reference import check_append
 from test_kv_more_cpu import plan_compact, plan_fork
 from test_kv_window_gpu import attend, check, make, of
 
@@ -168,3 +169,44 @@ def test_one_long_sequence_in_a_wide_window(tokens, short, window):
     x = torch.randn(q.shape[0], 40, 128, device="cuda").bfloat16()
     with_window, without = us((x, wide, rows, lens, cu, window, 4)), us((x, wide, every, lens, cu, None, 0), False)
     assert with_window < 1.2 * without + 10, (with_window, without)
+
+
+def append_us(counts, D, P, normed):
+    """An append of 40 query and 8 key/value heads, held to its definition without norms; the least time of a few calls."""
+    B, T, H, Hq = len(counts), sum(counts), 8, 40
+    width = -(-(max(counts) + 40) // P)
+    cache = mhc.kv_cache(B * width, H, P, D)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rows = torch.randperm(B * width, generator=g, device="cuda").view(B, width).tolist()
+    lens, cu = [n + 7 * i % 40 for i, n in enumerate(counts)], [0]
+    for n in counts:
+        cu.append(cu[-1] + n)
+    x = torch.randn(T, Hq + 2 * H, D, generator=g, device="cuda").bfloat16()
+    q, k, v = x.split([Hq, H, H], dim=1)
+    angles = torch.rand(width * P, D // 2, generator=g, device="cuda") * 6
+    w = torch.ones(D, device="cuda").bfloat16()
+    norms = {"q_norm": w, "k_norm": w} if normed else {}
+    args, out = (cache, k, v, _i32(rows), _i32(lens), _i32(cu)), torch.empty(T, Hq, D, device="cuda").bfloat16()
+    before, best, cos, sin = {n: t.cpu() for n, t in cache.items()}, 1e9, angles.cos(), angles.sin()
+    for i in range(12):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        mhc.kv_append(*args, q=q, cos=cos, sin=sin, q_out=out, **norms)
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, 1e3 * a.elapsed_time(b))
+        if i == 0 and not normed:
+            check_append(before, {n: t.cpu() for n, t in cache.items()}, k.cpu(), v.cpu(), rows, lens, cu, cos.cpu(),
+                         sin.cpu(), q=q.cpu(), q_out=out.cpu())
+    return best
+
+
+@pytest.mark.parametrize("normed", [False, True])
+@pytest.mark.parametrize("D,P", [(128, 128), (128, 64), (64, 128), (64, 32)])
+def test_appends_of_8_to_20_tokens_a_sequence(D, P, normed):
+    """A prompt beside single tokens, and a few tokens of one sequence, 8 to 20 a sequence on average: as long as the
+    prompt and the single tokens would take in calls of their own, or as some more tokens, to half as much and 5 us."""
+    n = 150 if P > 64 else 70
+    apart = append_us([n], D, P, normed) + append_us([1] * 7, D, P, normed)
+    assert append_us([n] + [1] * 7, D, P, normed) < 1.5 * apart + 5
+    assert append_us([min(16, P // 2 - 1)], D, P, normed) < 1.5 * append_us([40], D, P, normed) + 5
