@@ -120,7 +120,7 @@ mhc_status mhc_kv_append(const mhc_kv_cache *cache, const uint16_t *k, int64_t k
  *  q_norm, k_norm  bf16 weights, head h's at h * stride (in elements: a
  *                  multiple of 8, at least head_dim; 0: all heads have the
  *                  same), 16-byte aligned.  NULL: no norm of these; q_norm
- *                  without q is refused.
+ *                  without q is refused where there are tokens.
  *  norm_eps        1e-20 or more, finite; read when there is a norm
  */
 mhc_status mhc_kv_append_norm(const mhc_kv_cache *cache, const uint16_t *k, int64_t k_stride,
@@ -258,7 +258,9 @@ mhc_status mhc_kv_fork(const mhc_kv_cache *caches, int num_caches, const int32_t
  *   pages            one number: 1 + the highest page in use or held, 0 if none
  * held pages are not moved, whoever else uses them.  Pages that moved keep
  * their bytes in their old place too.  block_table_out may be exactly
- * block_table.  Arguments, bad indices and errors as mhc_kv_fork.
+ * block_table.  Two kernel launches, four and a memset for large tables, and
+ * one more for each 64 caches beyond the first.  Arguments, bad indices and
+ * errors as mhc_kv_fork.
  */
 mhc_status mhc_kv_compact(const mhc_kv_cache *caches, int num_caches, const int32_t *block_table,
                           int64_t table_width, const int32_t *seq_lens, int64_t B,

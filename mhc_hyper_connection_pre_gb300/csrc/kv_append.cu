@@ -14,8 +14,8 @@
 // heads take 82 us: 445 MB at 5.4 TB/s (the queries alone 6.0 TB/s).  The forms
 // for many tokens that rotate spill 36 to 76 bytes a thread at the 64 registers
 // of four blocks an SM: cos, sin and both numbers of eight pairs are alive at once
-// beside the next step's loads.  With norms, three blocks an SM and 80 registers: 90 us, 4.9 TB/s,
-// as their instructions fill 59% of the issue slots (queries alone 5.4 TB/s).
+// beside the next step's loads.  With norms, three blocks an SM and 80 registers: 90 us, 4.9 TB/s
+// (queries alone 5.4), with 59% of the issue slots in use and fewer warps that wait for loads.
 #include <cuda_runtime.h>
 
 #include "kv_common.cuh"

@@ -5,7 +5,7 @@
 // What bounds it: planning reads and writes the tables once, a few hundred KB at
 // most; its time is a chain of dependent loads (parent, length, entry), of barriers,
 // and one block's instructions.  A cluster of eight blocks that met in global memory was slower
-// at every size: 256 rows of 47 entries 22.5 us, one block 15.4; 2048 rows of 128 169 and 90.
+// at every size: 256 rows of 47 entries 22.5 us when one block took 15.4 (12.3 since); 2048 rows of 128 169 and 90.
 // Copying is memory: every byte of the copied slots is read and written once, 16 bytes a lane,
 // by warps that take one page, head and tensor of one layer at a time.
 #include "../../include/mhc_kv.h"
